@@ -435,6 +435,90 @@ attn_status paged_decode_attn_append_q8(const attn_tensor *q, const attn_tensor 
                                         const int32_t *pos, float scale, const attn_tensor *out, float *lse,
                                         void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * Rotary positions.  A token at position p turns pair i of each of its query
+ * and key rows by the angle theta = p * f_i (i < n = rotary_dim / 2):
+ *     (a, b) -> m * (a cos theta - b sin theta, a sin theta + b cos theta)
+ * where the pair is dims (2i, 2i + 1) with interleaved = 1 and dims (i, i + n)
+ * with interleaved = 0; dims from rotary_dim on are copied.  m is `magnitude`
+ * (1 unless the scaling below asks for another).
+ *
+ * The frequencies are given as 64-bit fractions of a turn a token,
+ * freqs[i] = round(f_i / (2 pi) * 2^64), so that the angle of any int32 position
+ * is exact modulo a turn.
+ */
+typedef enum attn_rope_scaling {
+    ATTN_ROPE_PLAIN = 0,   /* f_i = base^(-2i / rotary_dim)                                         */
+    ATTN_ROPE_LINEAR = 1,  /* f_i / factor: positions interpolated                                  */
+    ATTN_ROPE_BASE = 2,    /* base * factor^(d / (d - 2)) for base, d = rotary_dim > 2              */
+    ATTN_ROPE_BANDED = 3,  /* f_i w + f_i / factor (1 - w), w = clamp((r - low) / (high - low), 0, 1),
+                              r = original_len f_i / (2 pi): the turns of pair i in the original
+                              context; slow pairs are interpolated, fast ones kept                  */
+    ATTN_ROPE_RAMP = 4     /* the same blend with w falling linearly over the pair index, from 1 at
+                              floor(j(high)) to 0 at ceil(j(low)), j(r) = d ln(original_len / (2 pi r))
+                              / (2 ln base), clamped to [0, d - 1]; *magnitude = 0.1 ln(factor) + 1 for
+                              factor > 1                                                            */
+} attn_rope_scaling;
+
+/* attn_rope_frequencies -- fill turns[rotary_dim / 2] (HOST memory) with the
+ * frequencies above and *magnitude with m; the caller copies turns to the
+ * device.  rotary_dim even and > 0 (> 2 for ATTN_ROPE_BASE); base > 1 and
+ * factor >= 1 finite; BANDED and RAMP: original_len > 0, 0 < low < high. */
+attn_status attn_rope_frequencies(int32_t rotary_dim, double base, int32_t scaling, double factor,
+                                  int64_t original_len, double low, double high,
+                                  uint64_t *turns, float *magnitude);
+
+/*
+ * rope_apply -- rotate x by its tokens' positions.
+ *   x, out     [B, H, T, D] bf16 or f32, the same dtype (strided views of any
+ *              alignment; 16-byte aligned rows are faster); out may be x itself
+ *              (same data pointer and strides), else they must not overlap.
+ *              D <= 512.
+ *   positions  int32, token t of row b at positions[b * pos_stride_b + t]
+ *              (pos_stride_b = 0: one row for all); any value, negative too
+ *   freqs      [rotary_dim / 2] on the device; rotary_dim even, 2 .. D
+ *   inverse    1: the transposed rotation m R(-theta), which carries the
+ *              gradient of out to the gradient of x (and, with m = 1, undoes
+ *              the rotation)
+ * Sines, cosines and products are float32; one rounding at the end.
+ */
+attn_status rope_apply(const attn_tensor *x, const int32_t *positions, int64_t pos_stride_b,
+                       const uint64_t *freqs, int32_t rotary_dim, int32_t interleaved, int32_t inverse,
+                       float magnitude, const attn_tensor *out, cudaStream_t stream);
+
+/*
+ * rope_kv_append -- rope_apply to q and k_new, and kv_append of the rotated
+ * keys and of v_new, for T tokens a sequence, in one launch.
+ *   q, q_out      [B, Hq, T, head_dim] bf16; q_out may be q itself
+ *   k_new, v_new  [B, Hkv, T, head_dim] bf16
+ *   positions     rotary positions (as rope_apply)
+ *   start_pos     int32 [B]: token i goes to slot start_pos[b] + i of sequence
+ *                 b's cache (the slot and the position differ once tokens have
+ *                 been evicted).  start_pos[b] < 0: an idle sequence, nothing
+ *                 is cached.  start_pos[b] + T past the table, or a bad block id,
+ *                 sets ATTN_ERR_DEVICE_BOUNDS and is not written.  q_out is
+ *                 written for every sequence.
+ *   workspace     >= kv_append_workspace_size() bytes (the status word)
+ * The cached keys are bit for bit those of rope_apply followed by kv_append.
+ */
+attn_status rope_kv_append(const attn_tensor *q, const attn_tensor *k_new, const attn_tensor *v_new,
+                           const int32_t *positions, int64_t pos_stride_b, const uint64_t *freqs,
+                           int32_t rotary_dim, int32_t interleaved, float magnitude, const attn_tensor *q_out,
+                           const attn_kv_cache *cache, const int32_t *block_table, int64_t bt_stride,
+                           int32_t max_blocks, const int32_t *start_pos,
+                           void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* rope_kv_append_q8 -- rope_kv_append into an INT8 cache: the rotated keys are
+ * rounded to bf16 and then quantised as kv_append_q8 does, bit for bit.  Rows of
+ * q, q_out, k_new and v_new 16-byte aligned; without interleaved, rotary_dim a
+ * multiple of 16 (else ATTN_ERR_UNSUPPORTED). */
+attn_status rope_kv_append_q8(const attn_tensor *q, const attn_tensor *k_new, const attn_tensor *v_new,
+                              const int32_t *positions, int64_t pos_stride_b, const uint64_t *freqs,
+                              int32_t rotary_dim, int32_t interleaved, float magnitude, const attn_tensor *q_out,
+                              const attn_kv_cache_q8 *cache, const int32_t *block_table, int64_t bt_stride,
+                              int32_t max_blocks, const int32_t *start_pos,
+                              void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Test/debug export: gather the paged cache of every (sequence, KV head) into
  * contiguous dst [batch, num_kv_heads, max_len, head_dim] (bf16), tokens
  * t < lens[b]; rows t >= lens[b] are left untouched.  Bit-exact.

@@ -25,6 +25,7 @@ __all__ = [
     "load", "LibAttnError", "Workspace",
     "attn_fwd", "attn_lse_merge", "kv_append", "paged_decode_attn", "paged_kv_gather",
     "attn_fwd_workspace_size", "paged_decode_workspace_size", "check_device_status",
+    "rope_frequencies", "rope_apply", "rope_kv_append", "rope_kv_append_q8",
 ]
 
 ATTN_F32, ATTN_BF16 = 0, 1
@@ -81,6 +82,11 @@ def _signatures() -> dict:
         "paged_decode_attn_append_q8": (I32, [T, T, T, CQ, P, I64, I32, P, F, T, P, P, SZ, P]),
         "paged_kv_gather": (I32, [C, I32, P, I64, I32, P, I32, I64, P, P, SZ, P]),
         "paged_decode_attn_noalloc": (I32, [T, C, P, I64, I32, P, F, T, P, P, P]),
+        "attn_rope_frequencies": (I32, [I32, ctypes.c_double, I32, ctypes.c_double, I64, ctypes.c_double,
+                                        ctypes.c_double, P, ctypes.POINTER(F)]),
+        "rope_apply": (I32, [T, P, I64, P, I32, I32, I32, F, T, P]),
+        "rope_kv_append": (I32, [T, T, T, P, I64, P, I32, I32, F, T, C, P, I64, I32, P, P, SZ, P]),
+        "rope_kv_append_q8": (I32, [T, T, T, P, I64, P, I32, I32, F, T, CQ, P, I64, I32, P, P, SZ, P]),
         "attn_check_device_status": (I32, [P, ctypes.POINTER(ctypes.c_uint32), P]),
         "attn_reset_device_status": (I32, [P, P]),
         "attn_selftest_wait_timeout": (I32, [P, SZ, ctypes.c_uint32, P]),
@@ -123,7 +129,8 @@ def exported_symbols() -> list[str]:
             "attn_check_device_status", "attn_reset_device_status", "attn_status_string", "attn_version",
             "paged_decode_attn_noalloc", "attn_selftest_wait_timeout", "attn_fwd_varlen",
             "attn_key_padding_to_additive", "paged_decode_attn_append", "paged_prefill_attn",
-            "attn_fwd_workspace_size_for", "kv_append_q8", "paged_decode_attn_q8", "paged_decode_attn_append_q8"]
+            "attn_fwd_workspace_size_for", "kv_append_q8", "paged_decode_attn_q8", "paged_decode_attn_append_q8",
+            "attn_rope_frequencies", "rope_apply", "rope_kv_append", "rope_kv_append_q8"]
 
 
 # --------------------------------------------------------------------------
@@ -666,3 +673,128 @@ def paged_decode_attn_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
                                        _stream(stream))
     _check("paged_decode_attn_noalloc", st)
     return out
+
+
+# --------------------------------------------------------------------------
+# rotary positions
+# --------------------------------------------------------------------------
+_ROPE_SCALING = {"plain": 0, "linear": 1, "base": 2, "banded": 3, "ramp": 4}
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                     original_len: int = 0, low: float = 1.0, high: float = 4.0, device=None):
+    """Frequencies for the rope calls: (freqs, magnitude) with freqs int64
+    [rotary_dim / 2] on the device, each pair's turns a token as a 64-bit
+    fraction.  scaling: "plain", "linear" (positions / factor), "base" (a larger
+    base), "banded" or "ramp" (slow pairs interpolated, fast ones kept; low and
+    high in turns over original_len tokens)."""
+    _require(scaling in _ROPE_SCALING, f"scaling must be one of {sorted(_ROPE_SCALING)}, got {scaling!r}")
+    turns = torch.empty(max(0, int(rotary_dim) // 2), dtype=torch.int64)
+    magnitude = ctypes.c_float(1.0)
+    st = load().attn_rope_frequencies(int(rotary_dim), float(base), _ROPE_SCALING[scaling], float(factor),
+                                      int(original_len), float(low), float(high), turns.data_ptr() or None,
+                                      ctypes.byref(magnitude))
+    _check("attn_rope_frequencies", st)
+    return turns.to(device or "cuda"), float(magnitude.value)
+
+
+def _check_devices(name: str, *tensors: Optional[torch.Tensor]):
+    """The kernels run on the current device: a tensor of another one is refused."""
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            _require(t.device.index == torch.cuda.current_device(),
+                     f"{name} runs on the current device cuda:{torch.cuda.current_device()}, got a tensor on {t.device}")
+
+
+def _check_rope(positions: torch.Tensor, freqs: torch.Tensor, B: int, T: int, D: int):
+    _require(isinstance(positions, torch.Tensor) and positions.dtype == torch.int32, "positions must be int32")
+    _require(positions.dim() == 2 and tuple(positions.shape) == (B, T) and (positions.stride(1) == 1 or T <= 1),
+             f"positions must be [{B}, {T}] with contiguous rows, got {tuple(positions.shape)}")
+    _require(isinstance(freqs, torch.Tensor) and freqs.dtype == torch.int64 and freqs.dim() == 1
+             and freqs.is_contiguous(), "freqs must be contiguous int64 [rotary_dim / 2]")
+    _require(1 <= freqs.shape[0] <= D // 2, f"freqs must hold 1 to {D // 2} pairs, got {freqs.shape[0]}")
+
+
+def _one_token(*tensors: torch.Tensor):
+    """[B, H, D] rows as [B, H, 1, D] views."""
+    _require(all(t.dim() == 3 for t in tensors), "rows without a token dimension must all be [B, H, D]")
+    return tuple(t.unsqueeze(2) for t in tensors)
+
+
+def rope_apply(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, interleaved: bool = False,
+               inverse: bool = False, magnitude: float = 1.0, out: Optional[torch.Tensor] = None, stream=None):
+    """Rotate x [B, H, T, D] (bf16 or f32, any strides with a contiguous last
+    dim) by its tokens' positions (int32 [B, T]), the first 2 * len(freqs) dims
+    of each row in neighbouring pairs (interleaved) or pairs half the rotated
+    dims apart.  x [B, H, D] with positions [B] is one token a row.  inverse:
+    the transposed rotation, which is its gradient.  out may be x."""
+    lib = load()
+    if out is None:
+        out = torch.empty_like(x)
+    _require(out.dtype == x.dtype and out.shape == x.shape, f"out must be {x.dtype} {tuple(x.shape)}")
+    full = out
+    if x.dim() == 3:
+        x, full = _one_token(x, out)
+        positions = positions.unsqueeze(-1)
+    _require(x.dim() == 4, f"x must be [B, H, T, D] or [B, H, D], got {tuple(x.shape)}")
+    B, H, T, D = x.shape
+    _check_rope(positions, freqs, B, T, D)
+    _check_devices("rope_apply", x, positions, freqs, out)
+    dx, do = _desc(x), _desc(full)
+    st = lib.rope_apply(ctypes.byref(dx), _ptr(positions, "positions"), positions.stride(0), _ptr(freqs, "freqs"),
+                        2 * freqs.shape[0], int(bool(interleaved)), int(bool(inverse)), float(magnitude),
+                        ctypes.byref(do), _stream(stream))
+    _check("rope_apply", st)
+    return out
+
+
+def _rope_append(name, cache, device, q, k_new, v_new, positions, freqs, block_table, start_pos, interleaved, magnitude,
+                 q_out, workspace, stream):
+    lib = load()
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    _require(q_out.dtype == q.dtype and q_out.shape == q.shape, f"q_out must be {q.dtype} {tuple(q.shape)}")
+    full = q_out
+    if q.dim() == 3:
+        q, k_new, v_new, full = _one_token(q, k_new, v_new, q_out)
+        positions = positions.unsqueeze(-1)
+    _require(q.dim() == 4, f"q must be [B, Hq, T, D] or [B, Hq, D], got {tuple(q.shape)}")
+    B, Hq, T, D = q.shape
+    _check_rope(positions, freqs, B, T, D)
+    _check_block_table(block_table, B)
+    _check_int32_vec(start_pos, B, "start_pos")
+    _check_devices(name, q, k_new, v_new, positions, freqs, block_table, start_pos, q_out)
+    ws = workspace or _small_ws(device)
+    _require(k_new.dim() == 4 and v_new.dim() == 4, "k_new and v_new must have q's number of dimensions")
+    dq, dk, dv, do = _desc(q), _desc(k_new), _desc(v_new), _desc(full)
+    st = getattr(lib, name)(ctypes.byref(dq), ctypes.byref(dk), ctypes.byref(dv), _ptr(positions, "positions"),
+                            positions.stride(0), _ptr(freqs, "freqs"), 2 * freqs.shape[0], int(bool(interleaved)),
+                            float(magnitude), ctypes.byref(do), ctypes.byref(cache), _ptr(block_table, "block_table"),
+                            block_table.stride(0), block_table.shape[1], _ptr(start_pos, "start_pos"), ws.ptr,
+                            ws.nbytes, _stream(stream))
+    _check(name, st)
+    return q_out
+
+
+def rope_kv_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, positions: torch.Tensor,
+                   freqs: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                   start_pos: torch.Tensor, interleaved: bool = False, magnitude: float = 1.0,
+                   q_out: Optional[torch.Tensor] = None, workspace: Optional[Workspace] = None, stream=None):
+    """Rotate q [B, Hq, T, D] and k_new [B, Hkv, T, D] by positions (int32
+    [B, T]), and write the rotated keys and v_new to cache slots start_pos[b] +
+    i.  Without the T dimension (and positions [B]): one token a sequence.
+    Returns the rotated q (q_out may be q)."""
+    return _rope_append("rope_kv_append", _cache(k_cache, v_cache), k_cache.device, q, k_new, v_new, positions, freqs,
+                        block_table, start_pos, interleaved, magnitude, q_out, workspace, stream)
+
+
+def rope_kv_append_q8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, positions: torch.Tensor,
+                      freqs: torch.Tensor, kq_cache: torch.Tensor, vq_cache: torch.Tensor, k_scale: torch.Tensor,
+                      v_scale: torch.Tensor, block_table: torch.Tensor, start_pos: torch.Tensor,
+                      interleaved: bool = False, magnitude: float = 1.0, q_out: Optional[torch.Tensor] = None,
+                      workspace: Optional[Workspace] = None, stream=None):
+    """rope_kv_append into an INT8 cache (codes int8 [N, Hkv, 16, D], scales
+    float32 [N, Hkv, 16])."""
+    return _rope_append("rope_kv_append_q8", _cache_q8(kq_cache, vq_cache, k_scale, v_scale), kq_cache.device, q,
+                        k_new, v_new, positions, freqs, block_table, start_pos, interleaved, magnitude, q_out,
+                        workspace, stream)

@@ -533,6 +533,146 @@ attn_status paged_prefill_attn(const attn_tensor* q, const attn_tensor* k_new, c
   return from_cuda(launch_paged_prefill_tc(a, stream));
 }
 
+attn_status attn_rope_frequencies(int32_t rotary_dim, double base, int32_t scaling, double factor,
+                                  int64_t original_len, double low, double high, uint64_t* turns, float* magnitude) {
+  if (rotary_dim <= 0 || rotary_dim % 2 != 0 || turns == nullptr || magnitude == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (!isfinite(base) || !(base > 1.0) || !isfinite(factor) || !(factor >= 1.0)) return ATTN_ERR_INVALID_ARG;
+  if (scaling < ATTN_ROPE_PLAIN || scaling > ATTN_ROPE_RAMP) return ATTN_ERR_INVALID_ARG;
+  const bool blend = scaling == ATTN_ROPE_BANDED || scaling == ATTN_ROPE_RAMP;
+  if (blend && (original_len <= 0 || !isfinite(high) || !(low > 0.0) || !(low < high))) return ATTN_ERR_INVALID_ARG;
+  if (scaling == ATTN_ROPE_BASE && rotary_dim <= 2) return ATTN_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925;
+  const double d = rotary_dim, len = static_cast<double>(original_len);
+  if (scaling == ATTN_ROPE_BASE) base *= pow(factor, d / (d - 2.0));
+  if (!isfinite(base)) return ATTN_ERR_INVALID_ARG;
+  double ramp0 = 0.0, ramp1 = 0.0;  // RAMP: the pair indices where w leaves 1 and reaches 0
+  if (scaling == ATTN_ROPE_RAMP) {
+    ramp0 = fmax(floor(d * log(len / (two_pi * high)) / (2.0 * log(base))), 0.0);
+    ramp1 = fmin(ceil(d * log(len / (two_pi * low)) / (2.0 * log(base))), d - 1.0);
+    if (!(ramp1 > ramp0)) ramp1 = ramp0 + 1e-3;
+  }
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double f = pow(base, -2.0 * i / d);
+    if (scaling == ATTN_ROPE_LINEAR) f /= factor;
+    if (blend) {
+      const double w = scaling == ATTN_ROPE_BANDED ? (len * f / two_pi - low) / (high - low)
+                                                   : 1.0 - (i - ramp0) / (ramp1 - ramp0);
+      const double wc = fmin(fmax(w, 0.0), 1.0);
+      f = f * wc + f / factor * (1.0 - wc);
+    }
+    turns[i] = static_cast<uint64_t>(nearbyint(ldexp(f / two_pi, 64)));  // f <= 1: below 2^62
+  }
+  *magnitude = scaling == ATTN_ROPE_RAMP && factor > 1.0 ? static_cast<float>(0.1 * log(factor) + 1.0) : 1.0f;
+  return ATTN_OK;
+}
+
+// Checks shared by the rotary calls; fills the rotation's part of the arguments.
+static attn_status rope_args(RopeArgs& a, const attn_tensor* x, const int32_t* positions, int64_t pos_stride_b,
+                             const uint64_t* freqs, int32_t rotary_dim, int32_t interleaved, int32_t inverse,
+                             float magnitude, const attn_tensor* out) {
+  attn_status st;
+  if ((st = check_tensor(x, 4)) != ATTN_OK) return st;
+  if ((st = check_tensor(out, 4)) != ATTN_OK) return st;
+  if (x->dtype != out->dtype) return ATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)
+    if (x->shape[i] != out->shape[i]) return ATTN_ERR_INVALID_ARG;
+  const int64_t B = x->shape[0], H = x->shape[1], T = x->shape[2], D = x->shape[3];
+  if (rotary_dim <= 0 || rotary_dim % 2 != 0 || rotary_dim > D) return ATTN_ERR_INVALID_ARG;
+  if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1)) return ATTN_ERR_INVALID_ARG;
+  if (!isfinite(magnitude)) return ATTN_ERR_INVALID_ARG;
+  if (D > 512 || H > 65535 || B > 0x7fffffff || T > 0x7fffffff || B * T > 0x7fffffff) return ATTN_ERR_UNSUPPORTED;
+  if (B == 0 || H == 0 || T == 0) return ATTN_OK;
+  if (positions == nullptr || freqs == nullptr || !aligned(positions, 4) || !aligned(freqs, 8))
+    return ATTN_ERR_INVALID_ARG;
+  if (pos_stride_b != 0 && pos_stride_b < T && B > 1) return ATTN_ERR_INVALID_ARG;
+  if (pos_stride_b < 0) return ATTN_ERR_INVALID_ARG;
+  const int eb = elem_bytes(x->dtype);
+  if (!aligned(x->data, eb) || !aligned(out->data, eb)) return ATTN_ERR_INVALID_ARG;
+  a.x = view(x);
+  a.out = view(out);
+  a.positions = positions;
+  a.pos_stride = pos_stride_b;
+  a.freqs = freqs;
+  a.rotary_dim = rotary_dim;
+  a.interleaved = interleaved;
+  a.inverse = inverse;
+  a.magnitude = magnitude;
+  return ATTN_OK;
+}
+
+attn_status rope_apply(const attn_tensor* x, const int32_t* positions, int64_t pos_stride_b, const uint64_t* freqs,
+                       int32_t rotary_dim, int32_t interleaved, int32_t inverse, float magnitude,
+                       const attn_tensor* out, cudaStream_t stream) {
+  RopeArgs a = {};
+  attn_status st = rope_args(a, x, positions, pos_stride_b, freqs, rotary_dim, interleaved, inverse, magnitude, out);
+  if (st != ATTN_OK) return st;
+  if (x->shape[0] == 0 || x->shape[1] == 0 || x->shape[2] == 0) return ATTN_OK;
+  return from_cuda(launch_rope(a, stream));
+}
+
+static attn_status rope_append_core(const attn_tensor* q, const attn_tensor* k_new, const attn_tensor* v_new,
+                                    const int32_t* positions, int64_t pos_stride_b, const uint64_t* freqs,
+                                    int32_t rotary_dim, int32_t interleaved, float magnitude,
+                                    const attn_tensor* q_out, const PagedCache& pc, const int32_t* block_table,
+                                    int64_t bt_stride, int32_t max_blocks, const int32_t* start_pos, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream) {
+  RopeArgs a = {};
+  attn_status st = rope_args(a, q, positions, pos_stride_b, freqs, rotary_dim, interleaved, 0, magnitude, q_out);
+  if (st != ATTN_OK) return st;
+  if ((st = check_tensor(k_new, 4)) != ATTN_OK) return st;
+  if ((st = check_tensor(v_new, 4)) != ATTN_OK) return st;
+  const int64_t B = q->shape[0], Hq = q->shape[1], T = q->shape[2];
+  if (q->dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
+  if (k_new->dtype != ATTN_BF16 || v_new->dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+  if (q->shape[3] != pc.D || Hq <= 0 || Hq % pc.Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  const int64_t want[4] = {B, pc.Hkv, T, pc.D};
+  for (int i = 0; i < 4; ++i)
+    if (k_new->shape[i] != want[i] || v_new->shape[i] != want[i]) return ATTN_ERR_INVALID_ARG;
+  if (pc.Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
+  if ((st = check_workspace(workspace, workspace_bytes, kv_append_workspace_size())) != ATTN_OK) return st;
+  if (B == 0 || T == 0) return ATTN_OK;
+  if (block_table == nullptr || start_pos == nullptr || max_blocks <= 0 || max_blocks > (1 << 24))
+    return ATTN_ERR_INVALID_ARG;
+  if (B > 1 && bt_stride < max_blocks) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(k_new->data, 2) || !aligned(v_new->data, 2)) return ATTN_ERR_INVALID_ARG;
+  a.k_new = view(k_new);
+  a.v_new = view(v_new);
+  a.cache = pc;
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.max_blocks = max_blocks;
+  a.start_pos = start_pos;
+  a.status = static_cast<uint32_t*>(workspace);
+  if (pc.k_scale != nullptr && !rope_rows_in_vectors(a)) return ATTN_ERR_UNSUPPORTED;
+  return from_cuda(launch_rope(a, stream));
+}
+
+attn_status rope_kv_append(const attn_tensor* q, const attn_tensor* k_new, const attn_tensor* v_new,
+                           const int32_t* positions, int64_t pos_stride_b, const uint64_t* freqs, int32_t rotary_dim,
+                           int32_t interleaved, float magnitude, const attn_tensor* q_out,
+                           const attn_kv_cache* cache, const int32_t* block_table, int64_t bt_stride,
+                           int32_t max_blocks, const int32_t* start_pos, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream) {
+  attn_status st;
+  if ((st = check_cache(cache)) != ATTN_OK) return st;
+  return rope_append_core(q, k_new, v_new, positions, pos_stride_b, freqs, rotary_dim, interleaved, magnitude, q_out,
+                          paged(cache), block_table, bt_stride, max_blocks, start_pos, workspace, workspace_bytes,
+                          stream);
+}
+
+attn_status rope_kv_append_q8(const attn_tensor* q, const attn_tensor* k_new, const attn_tensor* v_new,
+                              const int32_t* positions, int64_t pos_stride_b, const uint64_t* freqs,
+                              int32_t rotary_dim, int32_t interleaved, float magnitude, const attn_tensor* q_out,
+                              const attn_kv_cache_q8* cache, const int32_t* block_table, int64_t bt_stride,
+                              int32_t max_blocks, const int32_t* start_pos, void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream) {
+  attn_status st;
+  if ((st = check_cache_q8(cache)) != ATTN_OK) return st;
+  return rope_append_core(q, k_new, v_new, positions, pos_stride_b, freqs, rotary_dim, interleaved, magnitude, q_out,
+                          paged_q8(cache), block_table, bt_stride, max_blocks, start_pos, workspace, workspace_bytes,
+                          stream);
+}
+
 attn_status attn_selftest_wait_timeout(void* workspace, size_t workspace_bytes, uint32_t timeout_us,
                                        cudaStream_t stream) {
   attn_status st;

@@ -168,6 +168,27 @@ cudaError_t launch_kv_append_chunk(const PrefillArgs& a, cudaStream_t stream);
 // the chunk's queries over the paged cache (tcgen05 kernel, paged instance)
 cudaError_t launch_paged_prefill_tc(const PrefillArgs& a, cudaStream_t stream);
 
+// Rotary positions; with k_new set, also the rotated append to the cache.
+struct RopeArgs {
+  View4 x, out;        // [B, H, T, D] bf16 or f32 (bf16 with a cache)
+  View4 k_new, v_new;  // [B, Hkv, T, D]; data null without a cache
+  const int32_t* positions;  // row b at positions + b * pos_stride
+  int64_t pos_stride;
+  const uint64_t* freqs;  // [rotary_dim / 2] turns per token, 64-bit fractions
+  int rotary_dim;
+  int interleaved, inverse;
+  float magnitude;
+  PagedCache cache;  // bf16, or INT8 when k_scale is set
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int max_blocks;
+  const int32_t* start_pos;  // [B] slot of the chunk's first token
+  uint32_t* status;
+};
+// rows are moved in 16-byte vectors (the INT8 append needs it)
+bool rope_rows_in_vectors(const RopeArgs& a);
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
+
 // boolean key-padding mask (non-zero = padded) -> additive 0 / -inf
 cudaError_t launch_padding_mask_to_additive(const uint8_t* kpm, int64_t kpm_stride, int64_t B, int64_t Pk,
                                             float* out, int64_t out_stride, cudaStream_t stream);
