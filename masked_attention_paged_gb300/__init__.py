@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 from typing import Optional, Sequence
 
@@ -136,25 +137,33 @@ def exported_symbols() -> list[str]:
 # --------------------------------------------------------------------------
 # marshalling helpers
 # --------------------------------------------------------------------------
+_DTYPE_CODES = {torch.bfloat16: ATTN_BF16, torch.float32: ATTN_F32}
+
+
 def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.bfloat16:
-        return ATTN_BF16
-    if t.dtype == torch.float32:
-        return ATTN_F32
-    raise TypeError(f"libattn takes bfloat16 or float32 tensors, got {t.dtype}")
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"libattn takes bfloat16 or float32 tensors, got {t.dtype}")
+    return code
+
+
+# An AttnTensor's bytes in one step: a call of a few microseconds on the GPU is
+# bound by the host, and setting the structure's fields one by one costs about
+# as much as the launch.
+_pack_tensor = struct.Struct("@Pii8q").pack
+_pack_cache = struct.Struct("@PPiiqii").pack  # an AttnKVCache
+_NO_DIMS = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())  # by number of dimensions used
 
 
 def _desc(t: torch.Tensor) -> AttnTensor:
     if not _on_device(t):
         raise ValueError("libattn tensors must be on a CUDA device")
-    d = AttnTensor()
-    d.data = t.data_ptr()
-    d.dtype = _dtype_code(t)
-    d.ndim = t.dim()
-    for i in range(t.dim()):
-        d.shape[i] = t.shape[i]
-        d.stride[i] = t.stride(i)
-    return d
+    n = t.dim()
+    if n > 4:
+        raise ValueError(f"libattn tensors have up to 4 dimensions, got {n}")
+    rest = _NO_DIMS[n]
+    return AttnTensor.from_buffer_copy(_pack_tensor(t.data_ptr(), _dtype_code(t), n, *t.shape, *rest, *t.stride(),
+                                                    *rest))
 
 
 def _stream(stream) -> int:
@@ -194,8 +203,12 @@ def _ptr(t: Optional[torch.Tensor], name: str = "tensor"):
     return t.data_ptr()
 
 
+# The checks of every call test their conditions first and word the refusal
+# after: the wording costs more than the check.
 def _check_f32_buffer(t: torch.Tensor, numel: int, name: str):
     """float32, contiguous, exactly `numel` elements."""
+    if isinstance(t, torch.Tensor) and t.dtype == torch.float32 and t.is_contiguous() and t.numel() == numel:
+        return
     _require(isinstance(t, torch.Tensor), f"{name} must be a torch tensor")
     _require(t.dtype == torch.float32, f"{name} must be float32, got {t.dtype}")
     _require(t.is_contiguous(), f"{name} must be contiguous")
@@ -204,6 +217,8 @@ def _check_f32_buffer(t: torch.Tensor, numel: int, name: str):
 
 def _check_int32_vec(t: torch.Tensor, n: int, name: str):
     """int32 [n], contiguous."""
+    if isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.shape == (n,) and t.is_contiguous():
+        return
     _require(isinstance(t, torch.Tensor), f"{name} must be a torch tensor")
     _require(t.dtype == torch.int32, f"{name} must be int32, got {t.dtype}")
     _require(t.dim() == 1 and t.shape[0] == n and t.is_contiguous(), f"{name} must be contiguous [{n}], got "
@@ -212,6 +227,9 @@ def _check_int32_vec(t: torch.Tensor, n: int, name: str):
 
 def _check_block_table(t: torch.Tensor, batch: int):
     """int32 [>= batch, max_blocks] with unit stride along a row."""
+    if (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.dim() == 2 and t.shape[0] >= batch
+            and t.stride(1) == 1 and t.stride(0) >= t.shape[1]):
+        return
     _require(isinstance(t, torch.Tensor), "block_table must be a torch tensor")
     _require(t.dtype == torch.int32, f"block_table must be int32, got {t.dtype}")
     _require(t.dim() == 2 and t.shape[0] >= batch and t.stride(1) == 1 and t.stride(0) >= t.shape[1],
@@ -387,19 +405,15 @@ def attn_lse_merge(outs: Sequence[torch.Tensor], lses: Sequence[torch.Tensor], o
 
 
 def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor) -> AttnKVCache:
-    _require(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype,
-             "K and V caches must be [num_blocks, Hkv, block_size, D] of one dtype")
-    _require(k_cache.is_contiguous() and v_cache.is_contiguous(), "K and V caches must be contiguous")
-    _require(_on_device(k_cache) and _on_device(v_cache), "K and V caches must be on a CUDA device")
-    c = AttnKVCache()
-    c.k = k_cache.data_ptr()
-    c.v = v_cache.data_ptr()
-    c.dtype = _dtype_code(k_cache)
-    c.num_blocks = k_cache.shape[0]
-    c.num_kv_heads = k_cache.shape[1]
-    c.block_size = k_cache.shape[2]
-    c.head_dim = k_cache.shape[3]
-    return c
+    if not (k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype):
+        raise ValueError("K and V caches must be [num_blocks, Hkv, block_size, D] of one dtype")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("K and V caches must be contiguous")
+    if not (_on_device(k_cache) and _on_device(v_cache)):
+        raise ValueError("K and V caches must be on a CUDA device")
+    nb, heads, bs, D = k_cache.shape
+    return AttnKVCache.from_buffer_copy(_pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), _dtype_code(k_cache), bs,
+                                                    nb, heads, D))
 
 
 def kv_append(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, pos: torch.Tensor,
@@ -700,19 +714,25 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "pla
 
 def _check_devices(name: str, *tensors: Optional[torch.Tensor]):
     """The kernels run on the current device: a tensor of another one is refused."""
+    current = -1
     for t in tensors:
         if t is not None and t.is_cuda:
-            _require(t.device.index == torch.cuda.current_device(),
-                     f"{name} runs on the current device cuda:{torch.cuda.current_device()}, got a tensor on {t.device}")
+            if current < 0:
+                current = torch.cuda.current_device()
+            if t.get_device() != current:
+                raise ValueError(f"{name} runs on the current device cuda:{current}, got a tensor on {t.device}")
 
 
 def _check_rope(positions: torch.Tensor, freqs: torch.Tensor, B: int, T: int, D: int):
-    _require(isinstance(positions, torch.Tensor) and positions.dtype == torch.int32, "positions must be int32")
-    _require(positions.dim() == 2 and tuple(positions.shape) == (B, T) and (positions.stride(1) == 1 or T <= 1),
-             f"positions must be [{B}, {T}] with contiguous rows, got {tuple(positions.shape)}")
-    _require(isinstance(freqs, torch.Tensor) and freqs.dtype == torch.int64 and freqs.dim() == 1
-             and freqs.is_contiguous(), "freqs must be contiguous int64 [rotary_dim / 2]")
-    _require(1 <= freqs.shape[0] <= D // 2, f"freqs must hold 1 to {D // 2} pairs, got {freqs.shape[0]}")
+    if not (isinstance(positions, torch.Tensor) and positions.dtype == torch.int32):
+        raise ValueError("positions must be int32")
+    if positions.shape != (B, T) or not (T <= 1 or positions.stride(1) == 1):
+        raise ValueError(f"positions must be [{B}, {T}] with contiguous rows, got {tuple(positions.shape)}")
+    if not (isinstance(freqs, torch.Tensor) and freqs.dtype == torch.int64 and freqs.dim() == 1
+            and freqs.is_contiguous()):
+        raise ValueError("freqs must be contiguous int64 [rotary_dim / 2]")
+    if not 1 <= freqs.shape[0] <= D // 2:
+        raise ValueError(f"freqs must hold 1 to {D // 2} pairs, got {freqs.shape[0]}")
 
 
 def _one_token(*tensors: torch.Tensor):
@@ -731,12 +751,14 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, in
     lib = load()
     if out is None:
         out = torch.empty_like(x)
-    _require(out.dtype == x.dtype and out.shape == x.shape, f"out must be {x.dtype} {tuple(x.shape)}")
+    elif not (out.dtype == x.dtype and out.shape == x.shape):
+        raise ValueError(f"out must be {x.dtype} {tuple(x.shape)}")
     full = out
     if x.dim() == 3:
         x, full = _one_token(x, out)
         positions = positions.unsqueeze(-1)
-    _require(x.dim() == 4, f"x must be [B, H, T, D] or [B, H, D], got {tuple(x.shape)}")
+    if x.dim() != 4:
+        raise ValueError(f"x must be [B, H, T, D] or [B, H, D], got {tuple(x.shape)}")
     B, H, T, D = x.shape
     _check_rope(positions, freqs, B, T, D)
     _check_devices("rope_apply", x, positions, freqs, out)
@@ -753,12 +775,14 @@ def _rope_append(name, cache, device, q, k_new, v_new, positions, freqs, block_t
     lib = load()
     if q_out is None:
         q_out = torch.empty_like(q)
-    _require(q_out.dtype == q.dtype and q_out.shape == q.shape, f"q_out must be {q.dtype} {tuple(q.shape)}")
+    elif not (q_out.dtype == q.dtype and q_out.shape == q.shape):
+        raise ValueError(f"q_out must be {q.dtype} {tuple(q.shape)}")
     full = q_out
     if q.dim() == 3:
         q, k_new, v_new, full = _one_token(q, k_new, v_new, q_out)
         positions = positions.unsqueeze(-1)
-    _require(q.dim() == 4, f"q must be [B, Hq, T, D] or [B, Hq, D], got {tuple(q.shape)}")
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, Hq, T, D] or [B, Hq, D], got {tuple(q.shape)}")
     B, Hq, T, D = q.shape
     _check_rope(positions, freqs, B, T, D)
     _check_block_table(block_table, B)
