@@ -519,6 +519,72 @@ attn_status rope_kv_append_q8(const attn_tensor *q, const attn_tensor *k_new, co
                               int32_t max_blocks, const int32_t *start_pos,
                               void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * paged_tree_attn -- attention of a tree of drafted tokens over a paged cache:
+ * the drafts' K/V are appended and every draft attends, in one launch.
+ *
+ * Sequence b holds ctx_lens[b] tokens and T drafts; parents[b][t] says which
+ * token draft t follows:
+ *     -1           the context's last token
+ *     0 .. t - 1   that draft
+ *     below -1     none: an absent draft (a shorter tree in the batch).  It and
+ *                  the drafts that follow it are not cached, nobody attends to
+ *                  them, and their rows are out = 0, lse = -inf.
+ * A parent at or past its own index sets ATTN_ERR_DEVICE_BOUNDS and counts as
+ * absent.  Draft t attends to the ctx_lens[b] cached tokens, to itself and to
+ * its ancestors: with s_j = scale * <q[b,h,t,:], K[j]> over those,
+ *     out[b,h,t,:] = sum_j softmax(s)_j V[j],  lse[b,h,t] = log sum_j exp(s_j).
+ * What keys and values that a draft does not attend to hold (infinities and NaN
+ * too) does not reach its row.  A chain of parents -1, 0, 1, ... is a causal
+ * chunk.
+ *
+ *   q, out        [batch, Hq, T, head_dim]; q bf16, out bf16 or f32 (strided
+ *                 views, 16-byte aligned rows); Hq a multiple of Hkv
+ *   k_new, v_new  [batch, Hkv, T, head_dim] bf16: draft t's rows, written to slot
+ *                 ctx_lens[b] + t.  Both NULL: they are in the cache already.
+ *   parents       int32, row b at parents + b * par_stride_b (0: one tree for all)
+ *   ctx_lens      int32 [batch].  < 0: an idle sequence (nothing cached, out = 0,
+ *                 lse = -inf).  ctx_lens[b] + T past the table sets
+ *                 ATTN_ERR_DEVICE_BOUNDS and counts as idle; a bad block id sets
+ *                 the same flag and that sequence's result must be discarded.
+ *   lse           float32 [batch, Hq, T] contiguous, or NULL
+ *   workspace     >= paged_tree_workspace_size(...) bytes on the current device:
+ *                 partial rows of the items that are cut between SMs, and their
+ *                 counts.  It needs no clearing between calls (only the status
+ *                 word must start at zero).  Calls that share a workspace must
+ *                 not overlap on the GPU.
+ * T <= 256.  Blocks that hold drafts must not be shared between sequences.
+ * Products run on the tensor cores with fp32 accumulation; the softmax weights
+ * are rounded to bf16 before P.V, as in attn_fwd.  Results do not depend on
+ * timing.
+ */
+size_t paged_tree_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t num_drafts,
+                                 int32_t max_blocks, int32_t block_size, int32_t head_dim);
+attn_status paged_tree_attn(const attn_tensor *q, const attn_tensor *k_new, const attn_tensor *v_new,
+                            const attn_kv_cache *cache, const int32_t *block_table, int64_t bt_stride,
+                            int32_t max_blocks, const int32_t *ctx_lens,
+                            const int32_t *parents, int64_t par_stride_b, float scale,
+                            const attn_tensor *out, float *lse,
+                            void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * kv_tree_accept -- keep an accepted path of the drafts: the cache rows of the
+ * drafts path[b][0 .. n_accept[b]) move to the slots right behind the context,
+ *     slot ctx_lens[b] + i  <-  slot ctx_lens[b] + path[b][i],
+ * after which the sequence holds ctx_lens[b] + n_accept[b] tokens.  Bit-exact.
+ *   path      int32, row b at path + b * path_stride_b, max_path entries: draft
+ *             indices, strictly increasing (parents come before children)
+ *   n_accept  int32 [batch]; <= 0 (or ctx_lens[b] < 0) leaves the sequence alone
+ * A path that is not strictly increasing, runs past the table or is longer than
+ * max_path sets ATTN_ERR_DEVICE_BOUNDS and leaves the sequence alone; a bad block
+ * id sets it and leaves that row alone.
+ *   workspace >= kv_append_workspace_size() bytes (the status word)
+ */
+attn_status kv_tree_accept(const attn_kv_cache *cache, const int32_t *block_table, int64_t bt_stride,
+                           int32_t max_blocks, const int32_t *ctx_lens, const int32_t *path, int64_t path_stride_b,
+                           int32_t max_path, const int32_t *n_accept, int32_t batch,
+                           void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Test/debug export: gather the paged cache of every (sequence, KV head) into
  * contiguous dst [batch, num_kv_heads, max_len, head_dim] (bf16), tokens
  * t < lens[b]; rows t >= lens[b] are left untouched.  Bit-exact.

@@ -27,6 +27,7 @@ __all__ = [
     "attn_fwd", "attn_lse_merge", "kv_append", "paged_decode_attn", "paged_kv_gather",
     "attn_fwd_workspace_size", "paged_decode_workspace_size", "check_device_status",
     "rope_frequencies", "rope_apply", "rope_kv_append", "rope_kv_append_q8",
+    "paged_tree_workspace_size", "paged_tree_attn", "kv_tree_accept",
 ]
 
 ATTN_F32, ATTN_BF16 = 0, 1
@@ -88,6 +89,9 @@ def _signatures() -> dict:
         "rope_apply": (I32, [T, P, I64, P, I32, I32, I32, F, T, P]),
         "rope_kv_append": (I32, [T, T, T, P, I64, P, I32, I32, F, T, C, P, I64, I32, P, P, SZ, P]),
         "rope_kv_append_q8": (I32, [T, T, T, P, I64, P, I32, I32, F, T, CQ, P, I64, I32, P, P, SZ, P]),
+        "paged_tree_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32, I32]),
+        "paged_tree_attn": (I32, [T, T, T, C, P, I64, I32, P, P, I64, F, T, P, P, SZ, P]),
+        "kv_tree_accept": (I32, [C, P, I64, I32, P, P, I64, I32, P, I32, P, SZ, P]),
         "attn_check_device_status": (I32, [P, ctypes.POINTER(ctypes.c_uint32), P]),
         "attn_reset_device_status": (I32, [P, P]),
         "attn_selftest_wait_timeout": (I32, [P, SZ, ctypes.c_uint32, P]),
@@ -131,7 +135,8 @@ def exported_symbols() -> list[str]:
             "paged_decode_attn_noalloc", "attn_selftest_wait_timeout", "attn_fwd_varlen",
             "attn_key_padding_to_additive", "paged_decode_attn_append", "paged_prefill_attn",
             "attn_fwd_workspace_size_for", "kv_append_q8", "paged_decode_attn_q8", "paged_decode_attn_append_q8",
-            "attn_rope_frequencies", "rope_apply", "rope_kv_append", "rope_kv_append_q8"]
+            "attn_rope_frequencies", "rope_apply", "rope_kv_append", "rope_kv_append_q8",
+            "paged_tree_workspace_size", "paged_tree_attn", "kv_tree_accept"]
 
 
 # --------------------------------------------------------------------------
@@ -822,3 +827,83 @@ def rope_kv_append_q8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
     return _rope_append("rope_kv_append_q8", _cache_q8(kq_cache, vq_cache, k_scale, v_scale), kq_cache.device, q,
                         k_new, v_new, positions, freqs, block_table, start_pos, interleaved, magnitude, q_out,
                         workspace, stream)
+
+
+# --------------------------------------------------------------------------
+# trees of drafted tokens
+# --------------------------------------------------------------------------
+def _check_int32_rows(t: torch.Tensor, batch: int, name: str):
+    """int32 [batch, n] with contiguous rows."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32):
+        raise ValueError(f"{name} must be int32")
+    if not (t.dim() == 2 and t.shape[0] == batch and (t.shape[1] <= 1 or t.stride(1) == 1)):
+        raise ValueError(f"{name} must be [{batch}, n] with contiguous rows, got {tuple(t.shape)}")
+
+
+def paged_tree_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, num_drafts: int, max_blocks: int,
+                              block_size: int = 16, head_dim: int = 128) -> int:
+    return int(load().paged_tree_workspace_size(batch, num_q_heads, num_kv_heads, num_drafts, max_blocks, block_size,
+                                                head_dim))
+
+
+def paged_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                    ctx_lens: torch.Tensor, parents: torch.Tensor, k_new: Optional[torch.Tensor] = None,
+                    v_new: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, return_lse: bool = False,
+                    workspace: Optional[Workspace] = None, stream=None):
+    """A tree of T drafted tokens per sequence over its paged cache: q [B, Hq,
+    T, D]; parents int32 [B, T] (-1: follows the context, below: no token);
+    ctx_lens int32 [B] counts the tokens before the drafts.  With k_new / v_new
+    ([B, Hkv, T, D]) draft t's K/V go to slot ctx_lens[b] + t; each draft
+    attends to the context, itself and its ancestors."""
+    lib = load()
+    B, Hq, T, D = q.shape
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    _check_block_table(block_table, B)
+    _check_int32_vec(ctx_lens, B, "ctx_lens")
+    _check_int32_rows(parents, B, "parents")
+    if parents.shape[1] != T:
+        raise ValueError(f"parents must be [{B}, {T}], got {tuple(parents.shape)}")
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device).transpose(1, 2)
+    if lse is None and return_lse:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _check_f32_buffer(lse, B * Hq * T, "lse")
+    _check_devices("paged_tree_attn", q, k_cache, v_cache, block_table, ctx_lens, parents, k_new, v_new, out, lse)
+    c = _cache(k_cache, v_cache)
+    max_blocks = block_table.shape[1]
+    ws = workspace
+    if ws is None:
+        ws = Workspace(paged_tree_workspace_size(B, Hq, k_cache.shape[1], T, max_blocks, k_cache.shape[2], D),
+                       device=q.device)
+    dq, do = _desc(q), _desc(out)
+    dk = ctypes.byref(_desc(k_new)) if k_new is not None else None
+    dv = ctypes.byref(_desc(v_new)) if v_new is not None else None
+    st = lib.paged_tree_attn(ctypes.byref(dq), dk, dv, ctypes.byref(c), _ptr(block_table, "block_table"),
+                             block_table.stride(0), max_blocks, _ptr(ctx_lens, "ctx_lens"), _ptr(parents, "parents"),
+                             parents.stride(0), float(scale), ctypes.byref(do), _ptr(lse, "lse"), ws.ptr, ws.nbytes,
+                             _stream(stream))
+    _check("paged_tree_attn", st)
+    return (out, lse) if return_lse else out
+
+
+def kv_tree_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, ctx_lens: torch.Tensor,
+                   path: torch.Tensor, n_accept: torch.Tensor, workspace: Optional[Workspace] = None, stream=None):
+    """Move the cache rows of the accepted drafts path[b, :n_accept[b]] (int32
+    [B, n], strictly increasing draft indices) to the slots behind the context,
+    ctx_lens[b] + i."""
+    lib = load()
+    B = ctx_lens.shape[0]
+    _check_block_table(block_table, B)
+    _check_int32_vec(ctx_lens, B, "ctx_lens")
+    _check_int32_rows(path, B, "path")
+    _check_int32_vec(n_accept, B, "n_accept")
+    _check_devices("kv_tree_accept", k_cache, v_cache, block_table, ctx_lens, path, n_accept)
+    ws = workspace or _small_ws(k_cache.device)
+    c = _cache(k_cache, v_cache)
+    st = lib.kv_tree_accept(ctypes.byref(c), _ptr(block_table, "block_table"), block_table.stride(0),
+                            block_table.shape[1], _ptr(ctx_lens, "ctx_lens"), _ptr(path, "path"), path.stride(0),
+                            path.shape[1], _ptr(n_accept, "n_accept"), B, ws.ptr, ws.nbytes, _stream(stream))
+    _check("kv_tree_accept", st)

@@ -673,6 +673,104 @@ attn_status rope_kv_append_q8(const attn_tensor* q, const attn_tensor* k_new, co
                           stream);
 }
 
+size_t paged_tree_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t num_drafts,
+                                 int32_t max_blocks, int32_t block_size, int32_t head_dim) {
+  if (batch < 0 || num_q_heads < 0 || num_kv_heads <= 0 || num_drafts < 0 || max_blocks < 0 || block_size <= 0 ||
+      head_dim <= 0 || num_q_heads % num_kv_heads != 0)
+    return 0;
+  const int64_t rows = static_cast<int64_t>(num_drafts) * (num_q_heads / num_kv_heads);
+  return kStatusBytes + tree_partial_bytes(batch, num_kv_heads, rows, head_dim, device_sm_count());
+}
+
+attn_status paged_tree_attn(const attn_tensor* q, const attn_tensor* k_new, const attn_tensor* v_new,
+                            const attn_kv_cache* cache, const int32_t* block_table, int64_t bt_stride,
+                            int32_t max_blocks, const int32_t* ctx_lens, const int32_t* parents, int64_t par_stride_b,
+                            float scale, const attn_tensor* out, float* lse, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  attn_status st;
+  if ((st = check_cache(cache)) != ATTN_OK) return st;
+  if ((st = check_tensor(q, 4)) != ATTN_OK) return st;
+  if ((st = check_tensor(out, 4)) != ATTN_OK) return st;
+  const int64_t B = q->shape[0], Hq = q->shape[1], T = q->shape[2], D = q->shape[3];
+  for (int i = 0; i < 4; ++i)
+    if (out->shape[i] != q->shape[i]) return ATTN_ERR_INVALID_ARG;
+  if (q->dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
+  if (D != cache->head_dim) return ATTN_ERR_INVALID_ARG;
+  if (Hq <= 0 || Hq % cache->num_kv_heads != 0) return ATTN_ERR_INVALID_ARG;
+  if (!isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (max_blocks <= 0 || max_blocks > (1 << 24)) return ATTN_ERR_INVALID_ARG;
+  if ((k_new == nullptr) != (v_new == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (k_new != nullptr) {
+    if ((st = check_tensor(k_new, 4)) != ATTN_OK) return st;
+    if ((st = check_tensor(v_new, 4)) != ATTN_OK) return st;
+    if (k_new->dtype != ATTN_BF16 || v_new->dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+    const int64_t want[4] = {B, cache->num_kv_heads, T, D};
+    for (int i = 0; i < 4; ++i)
+      if (k_new->shape[i] != want[i] || v_new->shape[i] != want[i]) return ATTN_ERR_INVALID_ARG;
+  }
+  if (T > kTreeMaxDrafts || B > 65535 || Hq > 65535 || cache->num_blocks > 0x7fffffff) return ATTN_ERR_UNSUPPORTED;
+  const size_t need = paged_tree_workspace_size(static_cast<int32_t>(B), static_cast<int32_t>(Hq),
+                                                cache->num_kv_heads, static_cast<int32_t>(T), max_blocks,
+                                                cache->block_size, cache->head_dim);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != ATTN_OK) return st;
+  if (B == 0 || T == 0) return ATTN_OK;
+  if (block_table == nullptr || ctx_lens == nullptr || parents == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (B > 1 && (bt_stride < max_blocks || (par_stride_b != 0 && par_stride_b < T))) return ATTN_ERR_INVALID_ARG;
+  if (!vec16_ok(q) || !vec16_ok(out)) return ATTN_ERR_INVALID_ARG;
+  if (k_new != nullptr && (!vec16_ok(k_new) || !vec16_ok(v_new))) return ATTN_ERR_INVALID_ARG;
+  TreeArgs a;
+  a.cache = paged(cache);
+  a.q = view(q);
+  a.out = view(out);
+  a.k_new = k_new != nullptr ? view(k_new) : View4{};
+  a.v_new = v_new != nullptr ? view(v_new) : View4{};
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.max_blocks = max_blocks;
+  a.ctx_lens = ctx_lens;
+  a.parents = parents;
+  a.par_stride = par_stride_b;
+  a.B = B;
+  a.Hq = Hq;
+  a.T = T;
+  a.scale = scale;
+  a.lse = lse;
+  a.partials = static_cast<uint8_t*>(workspace) + kStatusBytes;
+  a.n_cta = device_sm_count();
+  a.gen = next_decode_gen();
+  a.status = static_cast<uint32_t*>(workspace);
+  if (a.n_cta <= 0) return ATTN_ERR_CUDA;
+  return from_cuda(launch_paged_tree(a, stream));
+}
+
+attn_status kv_tree_accept(const attn_kv_cache* cache, const int32_t* block_table, int64_t bt_stride,
+                           int32_t max_blocks, const int32_t* ctx_lens, const int32_t* path, int64_t path_stride_b,
+                           int32_t max_path, const int32_t* n_accept, int32_t batch, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream) {
+  attn_status st;
+  if ((st = check_cache(cache)) != ATTN_OK) return st;
+  if (batch < 0 || max_path < 0 || max_blocks <= 0 || max_blocks > (1 << 24)) return ATTN_ERR_INVALID_ARG;
+  if (batch > 65535 || max_path > (1 << 24)) return ATTN_ERR_UNSUPPORTED;
+  if ((st = check_workspace(workspace, workspace_bytes, kv_append_workspace_size())) != ATTN_OK) return st;
+  if (batch == 0 || max_path == 0) return ATTN_OK;
+  if (block_table == nullptr || ctx_lens == nullptr || path == nullptr || n_accept == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  if (batch > 1 && (bt_stride < max_blocks || path_stride_b < max_path)) return ATTN_ERR_INVALID_ARG;
+  AcceptArgs a;
+  a.cache = paged(cache);
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.max_blocks = max_blocks;
+  a.ctx_lens = ctx_lens;
+  a.path = path;
+  a.path_stride = path_stride_b;
+  a.max_path = max_path;
+  a.n_accept = n_accept;
+  a.B = batch;
+  a.status = static_cast<uint32_t*>(workspace);
+  return from_cuda(launch_tree_accept(a, stream));
+}
+
 attn_status attn_selftest_wait_timeout(void* workspace, size_t workspace_bytes, uint32_t timeout_us,
                                        cudaStream_t stream) {
   attn_status st;

@@ -1103,6 +1103,10 @@ bool make_bf16_cache_map(CUtensorMap* map, void* base, int64_t num_blocks, int H
   return make_cache_map(map, base, num_blocks, Hkv, 128);
 }
 
+bool make_paged_map(CUtensorMap* map, void* base, int64_t num_blocks, int Hkv, int D) {
+  return make_cache_map(map, base, num_blocks, Hkv, D);
+}
+
 bool make_code_cache_map(CUtensorMap* map, void* base, int64_t num_blocks, int Hkv) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return false;

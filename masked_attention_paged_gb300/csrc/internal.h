@@ -168,6 +168,48 @@ cudaError_t launch_kv_append_chunk(const PrefillArgs& a, cudaStream_t stream);
 // the chunk's queries over the paged cache (tcgen05 kernel, paged instance)
 cudaError_t launch_paged_prefill_tc(const PrefillArgs& a, cudaStream_t stream);
 
+// the same for head dim 64 or 128
+bool make_paged_map(CUtensorMap* map, void* base, int64_t num_blocks, int Hkv, int D);
+
+constexpr int kTreeMaxDrafts = 256;  // drafts per sequence of the tree attention
+struct TreeArgs {
+  PagedCache cache;
+  View4 q, out;        // [B, Hq, T, D]
+  View4 k_new, v_new;  // [B, Hkv, T, D]; data null when the drafts are cached already
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int max_blocks;
+  const int32_t* ctx_lens;  // [B] tokens before the drafts
+  const int32_t* parents;   // row b at parents + b * par_stride
+  int64_t par_stride;
+  int64_t B, Hq, T;
+  float scale;
+  float* lse;      // [B, Hq, T] or null
+  void* partials;  // workspace after the status block
+  int n_cta;       // CTAs of the launch (one per SM)
+  uint32_t gen;    // this call's generation, tags the piece counts (never 0)
+  uint32_t* status;
+};
+// workspace past the status block for R = T * Hq / Hkv rows per KV head
+size_t tree_partial_bytes(int64_t B, int64_t Hkv, int64_t R, int D, int n_cta);
+cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream);
+
+struct AcceptArgs {
+  PagedCache cache;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int max_blocks;
+  const int32_t* ctx_lens;
+  const int32_t* path;  // row b at path + b * path_stride, max_path entries
+  int64_t path_stride;
+  int max_path;
+  const int32_t* n_accept;
+  int64_t B;
+  uint32_t* status;
+};
+// cache slots ctx + path[i] -> ctx + i, i < n_accept
+cudaError_t launch_tree_accept(const AcceptArgs& a, cudaStream_t stream);
+
 // Rotary positions; with k_new set, also the rotated append to the cache.
 struct RopeArgs {
   View4 x, out;        // [B, H, T, D] bf16 or f32 (bf16 with a cache)

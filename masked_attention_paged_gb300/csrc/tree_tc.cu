@@ -1,0 +1,1016 @@
+// tree_tc.cu -- attention of a tree of drafted tokens over a paged KV cache
+// (tcgen05 + TMEM + TMA), with the drafts' append in the same launch.
+//
+// Sequence b holds ctx tokens in its cache and T drafts; draft t attends to the
+// whole context and, among the drafts, to itself and its ancestors:
+//   s_j = scale q.k_j,  out = sum_j softmax(s)_j v_j,  lse = log sum_j e^{s_j}.
+//
+// Few query rows read a long cache, so K and V are read once for all T drafts
+// and all G query heads of a KV head: row r of a (sequence, KV head) is draft
+// r / G, head r % G, and NT tiles of 128 rows share every K/V tile (NT = 1 for
+// up to 128 rows, else 2).  What bounds it is HBM (a 128-key tile of K and V at
+// D = 128 is 64 KB, 1.4 us of an SM's share, against 0.6 us of softmax), until
+// rows pass 256 a KV head and the tensor cores and exponentials do.
+//
+// Every SM takes an equal run of the call's K/V tiles: an item (sequence, KV
+// head, row pair) is its draft tiles followed by its context tiles, the items
+// are laid end to end, and CTA c of n takes tiles [total c / n, total (c+1) / n).
+// An item inside one run is written at once; one that is cut leaves partials
+// (normalised rows and log2 LSE; at most two per CTA), merged in order by
+// whichever piece finishes last, so results do not depend on the timing.
+//
+// Warps: 0 streams context tiles (TMA through the block table), 1 issues the
+// MMAs, 2-3 load the draft tiles from k_new / v_new (or the cache), append them
+// and build the ancestor masks, 4.. one warpgroup of softmax per row tile
+// (thread r owns row r: TMEM lane r).  With NT = 1 two score buffers let the
+// next S run under the current softmax.  P goes over its S as bf16 (relative
+// rounding 2^-9; row sums are taken in fp32 before it).
+//
+// V rows past the context's end and rows of absent drafts are zeroed: P is 0
+// there, but 0 x NaN is not.  A draft's own V may hold infinities or NaN that
+// only its descendants may see: such elements enter the tile as zeros, and the
+// epilogue adds p x v for the rows that do attend to them.
+#include <cuda.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace attn {
+namespace {
+
+constexpr int kBM = 128;
+constexpr int kBN = 128;
+constexpr int kBS = 16;
+constexpr int kBoxBytes = kBM * 128;
+constexpr float kRescaleMargin = 8.0f;
+constexpr int kBarBytes = 512;
+constexpr uint32_t kAbsent = 0x7fc0a5a5u;  // a partial's LSE for the row of an absent draft (a NaN of its own)
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int kThreads = 128 + 128 * NT;
+  static constexpr int kSoft = 128 * NT;      // softmax threads
+  static constexpr int kMaxT = NT == 1 ? 128 : kTreeMaxDrafts;
+  static constexpr int kWords = kMaxT / 32;
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTileBytes = kBM * D * 2;
+  // D = 128: K runs a tile further ahead than V (its S is issued earlier), and
+  // 227 KB hold Q and five tiles (NT = 1) or four
+  static constexpr int KS = D == 64 ? 4 : (NT == 1 ? 3 : 2);
+  static constexpr int VS = D == 64 ? 4 : 2;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + NT * kTileBytes;
+  static constexpr int kOffV = kOffK + KS * kTileBytes;
+  static constexpr int kOffAnc = kOffV + VS * kTileBytes;  // [kMaxT][kWords] ancestor bits
+  static constexpr int kOffPar = kOffAnc + kMaxT * kWords * 4;  // [kMaxT] parents
+  static constexpr int kOffBar = kOffPar + kMaxT * 4;
+  static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
+  static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+  static constexpr uint32_t kColO = 256;  // O_t at kColO + t * D; scores below
+  // NT = 2: 384 threads launched with 168 registers, split as in attn_tc.cu
+  static constexpr int kRegsCtl = 88, kRegsSoft = 208;
+};
+
+struct Bars {
+  uint64_t q_full[2];
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[2], p_full[2];  // [row tile] (NT = 2) or [score buffer] (NT = 1)
+  uint64_t o_done[2];  // [row tile] (NT = 2) or, alternating, [tile parity] (NT = 1)
+  uint64_t draft_go[4];  // the producer hands K stage (and the tile's V stage) to the draft loader
+  uint64_t mask_full, mask_empty;
+  uint64_t piece_full, piece_go;  // an item's piece is written; whether it was the last
+  uint64_t drained;
+  int64_t lo, hi, total, bstart;  // this CTA's run of tiles; the first item's sequence starts at bstart
+  int b0;
+  int n_cta;
+  uint32_t bad[8];  // drafts whose V holds a non-finite element
+  uint32_t tmem_base;
+  int abort;
+  int last;
+};
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block outgrew its shared-memory slot");
+
+struct TreeParams {
+  int B, T, Hq, Hkv, G, R;  // R = T * G rows per KV head
+  int MP;                   // row pairs per KV head
+  float scale_log2;
+  int scale_positive;
+  const uint16_t* q;
+  int64_t q_stride[3];
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  int64_t kn_stride[3], vn_stride[3];
+  uint16_t* kc;
+  uint16_t* vc;
+  int num_blocks;
+  const int32_t* bt;
+  int64_t bt_stride;
+  int max_blocks;
+  const int32_t* ctx_lens;
+  const int32_t* parents;
+  int64_t par_stride;
+  void* out;
+  int out_bf16;
+  int64_t out_stride[3];
+  float* lse;
+  float* part_o;    // [2 n][slot_rows][D]
+  float* part_lse;  // [2 n][slot_rows]
+  int slot_rows;
+  unsigned long long* count;  // [B * Hkv * MP] (generation << 32) | pieces done
+  uint32_t gen;
+  uint32_t* status;
+};
+
+// A sequence that does not fit its table, or is idle, has no context and no drafts.
+__device__ __forceinline__ int seq_ctx(const TreeParams& p, int b, bool& ok) {
+  const int c = p.ctx_lens[b];
+  ok = c >= 0 && static_cast<int64_t>(c) + p.T <= static_cast<int64_t>(p.max_blocks) * kBS;
+  return ok ? c : 0;
+}
+__device__ __forceinline__ int draft_tiles(const TreeParams& p) { return (p.T + kBN - 1) / kBN; }
+__device__ __forceinline__ int seq_tiles(const TreeParams& p, int b, int& ctx, bool& ok) {
+  ctx = seq_ctx(p, b, ok);
+  return draft_tiles(p) + (ctx + kBN - 1) / kBN;
+}
+
+// A run of one item's tiles [t0, t1) of `tiles`.
+struct Seg {
+  int b, g, m, t0, t1, tiles, ctx;
+  bool ok;        // the sequence is present
+  int64_t item0;  // the item's first tile in the call's order
+};
+
+struct Cursor {
+  const TreeParams& p;
+  int64_t pos, hi, bstart;
+  int b, tiles, ctx;
+  bool ok;
+  __device__ Cursor(const TreeParams& prm, const Bars* bars)
+      : p(prm), pos(bars->lo), hi(bars->hi), bstart(bars->bstart), b(bars->b0) {
+    if (pos < hi) tiles = seq_tiles(p, b, ctx, ok);
+  }
+  __device__ bool next(Seg& s) {
+    if (pos >= hi) return false;
+    const int items = p.Hkv * p.MP;
+    while (pos >= bstart + static_cast<int64_t>(tiles) * items) {
+      bstart += static_cast<int64_t>(tiles) * items;
+      ++b;
+      tiles = seq_tiles(p, b, ctx, ok);
+    }
+    const int64_t local = pos - bstart;
+    const int item = static_cast<int>(local / tiles);
+    s.t0 = static_cast<int>(local - static_cast<int64_t>(item) * tiles);
+    s.t1 = static_cast<int>(min(static_cast<int64_t>(tiles), s.t0 + (hi - pos)));
+    s.b = b;
+    s.g = item / p.MP;
+    s.m = item % p.MP;
+    s.tiles = tiles;
+    s.ctx = ctx;
+    s.ok = ok;
+    s.item0 = bstart + static_cast<int64_t>(item) * tiles;
+    pos += s.t1 - s.t0;
+    return true;
+  }
+};
+
+// byte offset of 16-byte chunk ch of row r in a tile (128-byte swizzle, 64-column boxes)
+__device__ __forceinline__ uint32_t tile_off(int r, int ch) {
+  return static_cast<uint32_t>((ch >> 3) * kBoxBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+}
+
+// bf16 pair with its non-finite elements cleared; `any` reports them
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w, bool& any) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u, any = true;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu, any = true;
+  return w;
+}
+
+// the cache row of slot `slot` of (b, g), or -1 for a bad block id (reported)
+__device__ __forceinline__ int64_t cache_row(const TreeParams& p, int b, int g, int slot) {
+  const int blk = p.bt[static_cast<int64_t>(b) * p.bt_stride + slot / kBS];
+  if (blk < 0 || blk >= p.num_blocks) {
+    report(p.status, kStatusBounds);
+    return -1;
+  }
+  return (static_cast<int64_t>(blk) * p.Hkv + g) * kBS + slot % kBS;
+}
+
+template <int D>
+__device__ __forceinline__ const uint16_t* draft_row(const TreeParams& p, bool is_v, int b, int g, int j, int ctx) {
+  if (p.k_new != nullptr)
+    return is_v ? p.v_new + b * p.vn_stride[0] + g * p.vn_stride[1] + j * p.vn_stride[2]
+                : p.k_new + b * p.kn_stride[0] + g * p.kn_stride[1] + j * p.kn_stride[2];
+  const int64_t row = cache_row(p, b, g, ctx + j);
+  return row < 0 ? nullptr : (is_v ? p.vc : p.kc) + row * D;
+}
+
+// The partial slot of an item's piece in CTA c: a CTA's first segment uses
+// slot 2c, a later one (only its last can be cut) slot 2c + 1.
+__device__ __forceinline__ int64_t run_lo(int64_t total, int n, int c) { return total * c / n; }
+__device__ __forceinline__ int run_of(int64_t total, int n, int64_t tile) {
+  return static_cast<int>(((tile + 1) * n - 1) / total);
+}
+
+// Merge an item's pieces (CTAs c0 .. c0 + np - 1): out = sum_c 2^(lse_c - M)
+// out_c / sum_c 2^(lse_c - M), four dims a thread and step.
+template <int D>
+__device__ __forceinline__ void merge_item(const TreeParams& p, const Seg& s, int row0, int rows, int c0, int np,
+                                           bool first_is_head, int tid, int nthr) {
+  constexpr int V4 = D / 4;
+  for (int x = tid; x < rows * V4; x += nthr) {
+    const int r = x / V4, d = (x % V4) * 4;
+    auto slot_row = [&](int c) {
+      const int slot = 2 * (c0 + c) + ((c == 0 && !first_is_head) ? 1 : 0);
+      return static_cast<int64_t>(slot) * p.slot_rows + r;
+    };
+    const float l0 = __ldcg(p.part_lse + slot_row(0));
+    const bool absent = __float_as_uint(l0) == kAbsent;
+    float M = l0;
+    bool any = l0 != -INFINITY;  // a NaN counts: it has to reach the row
+    for (int c = 1; c < np; ++c) {
+      const float l = __ldcg(p.part_lse + slot_row(c));
+      M = fmaxf(M, l);
+      any |= l != -INFINITY;
+    }
+    float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f, ws = 0.f;
+    const bool empty = absent || !any;
+    if (!empty) {
+#pragma unroll 4
+      for (int c = 0; c < np; ++c) {
+        const float l = __ldcg(p.part_lse + slot_row(c));
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot_row(c) * D + d));
+        if (l == -INFINITY) continue;
+        const float w = fast_exp2(l - M);
+        ws += w;
+        a0 = fmaf(w, o.x, a0), a1 = fmaf(w, o.y, a1), a2 = fmaf(w, o.z, a2), a3 = fmaf(w, o.w, a3);
+      }
+    }
+    const float inv = empty ? 0.f : 1.f / ws;
+    const int rr = row0 + r, t = rr / p.G, h = s.g * p.G + rr % p.G;
+    const int64_t ob = s.b * p.out_stride[0] + h * p.out_stride[1] + t * p.out_stride[2] + d;
+    if (p.out_bf16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ob) =
+          make_uint2(pack_bf16x2(a0 * inv, a1 * inv), pack_bf16x2(a2 * inv, a3 * inv));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + ob) = make_float4(a0 * inv, a1 * inv, a2 * inv, a3 * inv);
+    if (d == 0 && p.lse != nullptr)
+      p.lse[(static_cast<int64_t>(s.b) * p.Hq + h) * p.T + t] =
+          empty ? -INFINITY : (M + __log2f(ws)) * 0.6931471805599453f;
+  }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+    paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ TreeParams p) {
+  using C = Cfg<D, NT>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBar);
+  uint32_t* anc = reinterpret_cast<uint32_t*>(smem + C::kOffAnc);
+  int32_t* par = reinterpret_cast<int32_t*>(smem + C::kOffPar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ntd = draft_tiles(p);
+  volatile int* abort = &bars->abort;
+
+  if (threadIdx.x == 32) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->q_full[t], 4);
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_full[t], 4);
+      mbar_init(&bars->o_done[t], 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->k_empty[s], 1);
+      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->v_empty[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) mbar_init(&bars->draft_go[s], 1);
+    mbar_init(&bars->piece_full, 4 * NT);
+    mbar_init(&bars->piece_go, 1);
+    mbar_init(&bars->drained, 1);
+    mbar_init(&bars->mask_full, 1);
+    mbar_init(&bars->mask_empty, 4 * NT);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    // the call's tiles, this CTA's run of them, and the sequence it starts in
+    const int64_t items = static_cast<int64_t>(p.Hkv) * p.MP;
+    int64_t total = 0;
+    for (int b = lane; b < p.B; b += 32) {
+      int ctx;
+      bool ok;
+      total += seq_tiles(p, b, ctx, ok) * items;
+      if (blockIdx.x == 0 && !ok && p.ctx_lens[b] >= 0) report(p.status, kStatusBounds);
+    }
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
+    const int n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    const int c = static_cast<int>(blockIdx.x);
+    const int64_t lo = c < n ? run_lo(total, n, c) : 0, hi = c < n ? run_lo(total, n, c + 1) : 0;
+    int64_t run = 0;
+    int b0 = 0;
+    for (int base = 0; base < p.B && lo < hi; base += 32) {
+      int64_t mine = 0;
+      if (base + lane < p.B) {
+        int ctx;
+        bool ok;
+        mine = seq_tiles(p, base + lane, ctx, ok) * items;
+      }
+      int64_t incl = mine;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, incl, m);
+        if (lane >= m) incl += up;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, run + incl > lo);
+      if (past != 0) {
+        const int l = __ffs(past) - 1;
+        b0 = base + l;
+        run += __shfl_sync(0xffffffffu, incl - mine, l);
+        break;
+      }
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      bars->lo = lo;
+      bars->hi = hi;
+      bars->total = total;
+      bars->bstart = run;
+      bars->b0 = b0;
+      bars->n_cta = n;
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if constexpr (NT == 2) {
+    if (warp < 4) regs_dec<C::kRegsCtl>();
+  }
+  if (warp == 0) {
+    // ------------------------------------------------------------ context tiles
+    // lane i < 8 owns block i of the tile: its 64-column boxes of K and of V
+    Cursor cur(p, bars);
+    Seg s;
+    int j = 0, k_issued = 0, v_issued = 0;
+    bool ok = true;
+    while (ok && cur.next(s)) {
+      const int32_t* bt_row = p.bt + static_cast<int64_t>(s.b) * p.bt_stride;
+      auto block_id = [&](int tile) {
+        const int kt = tile - ntd;
+        if (kt < 0 || tile >= s.t1) return -1;
+        const int nb = min(kBN / kBS, (s.ctx - kt * kBN + kBS - 1) / kBS);
+        return lane < nb ? bt_row[kt * (kBN / kBS) + lane] : -1;
+      };
+      int id_next = block_id(max(s.t0, ntd));
+      for (int tile = s.t0; tile < s.t1; ++tile, ++j) {
+        const int ks = j % C::KS, vs = j % C::VS;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->k_empty[ks], ((j / C::KS) & 1) ^ 1, abort, p.status))) {
+          ok = false;
+          break;
+        }
+        if (tile < ntd) {
+          // the draft loader fills these stages; every ring wait stays here, so
+          // that no waiter ever skips or lags a phase
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_empty[vs], ((j / C::VS) & 1) ^ 1, abort, p.status))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive(&bars->draft_go[ks]);
+          continue;
+        }
+        int id = id_next;
+        id_next = block_id(tile + 1);
+        if (id != -1 && (id < 0 || id >= p.num_blocks)) {
+          report(p.status, kStatusBounds);
+          id = -1;
+        }
+        const int bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * (kBS * D * 2);
+        if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[ks], bytes);
+        __syncwarp();
+        if (id >= 0)
+#pragma unroll
+          for (int x = 0; x < C::kBoxes; ++x)
+            tma_load_4d(smem + C::kOffK + ks * C::kTileBytes + x * kBoxBytes + lane * 2048, &tm_k, &bars->k_full[ks],
+                        x * 64, 0, s.g, id);
+        k_issued = j + 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_empty[vs], ((j / C::VS) & 1) ^ 1, abort, p.status))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&bars->v_full[vs], bytes);
+        __syncwarp();
+        if (id >= 0)
+#pragma unroll
+          for (int x = 0; x < C::kBoxes; ++x)
+            tma_load_4d(smem + C::kOffV + vs * C::kTileBytes + x * kBoxBytes + lane * 2048, &tm_v, &bars->v_full[vs],
+                        x * 64, 0, s.g, id);
+        v_issued = j + 1;
+      }
+    }
+    if (lane == 0 && *abort) {
+      // let every copy in flight land before the CTA exits (a draft tile's stage
+      // holds no copy: the wait on it runs out or passes)
+      for (int x = max(0, k_issued - C::KS); x < k_issued; ++x) drain_wait(&bars->k_full[x % C::KS], (x / C::KS) & 1);
+      for (int x = max(0, v_issued - C::VS); x < v_issued; ++x) drain_wait(&bars->v_full[x % C::VS], (x / C::VS) & 1);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBN, false, false);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(kBM, D, false, true);
+      auto s_col = [&](int t, int j) { return NT == 1 ? static_cast<uint32_t>((j & 1) * 128) : t * 128u; };
+      auto issue_s = [&](int t, int j) {  // S = Q_t K_j^T
+        const uint32_t qa = smem_u32(smem + C::kOffQ) + t * C::kTileBytes;
+        const uint32_t ka = smem_u32(smem + C::kOffK + (j % C::KS) * C::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
+          umma_bf16_ss(tmem + s_col(t, j), sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), idesc_s,
+                       kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&bars->s_full[NT == 1 ? (j & 1) : t]);
+      };
+      auto issue_pv = [&](int t, int j, bool first) {  // O_t (+)= P V_j
+        const uint32_t va = smem_u32(smem + C::kOffV + (j % C::VS) * C::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk)
+          umma_bf16_ts(tmem + C::kColO + t * D, tmem + s_col(t, j) + kk * 8,
+                       sdesc_sw128(va + kk * 2048, kBoxBytes, 1024), idesc_o, (!first || kk > 0) ? 1u : 0u);
+        umma_commit(&bars->o_done[NT == 1 ? (j & 1) : t]);
+      };
+      auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, abort, p.status); };
+      auto wait_k = [&](int j) { return wait(&bars->k_full[j % C::KS], j / C::KS); };
+      auto wait_v = [&](int j) { return wait(&bars->v_full[j % C::VS], j / C::VS); };
+      Cursor cur(p, bars);
+      Seg s;
+      int j = 0, seg = 0;
+      bool ok = true;
+      for (; ok && cur.next(s); ++seg) {
+        const int n = s.t1 - s.t0;
+        for (int t = 0; t < NT; ++t) ok = ok && wait(&bars->q_full[t], seg);
+        if constexpr (NT == 1) {
+          // S runs two tiles ahead of PV
+          for (int x = 0; ok && x < min(2, n); ++x) {
+            ok = wait_k(j + x);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(0, j + x);
+            umma_commit(&bars->k_empty[(j + x) % C::KS]);
+          }
+          for (int x = 0; ok && x < n; ++x, ++j) {
+            ok = wait(&bars->p_full[j & 1], j >> 1) && wait_v(j);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(0, j, x == 0);
+            umma_commit(&bars->v_empty[j % C::VS]);
+            if (x + 2 < n) {
+              ok = wait_k(j + 2);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(0, j + 2);
+              umma_commit(&bars->k_empty[(j + 2) % C::KS]);
+            }
+          }
+        } else {
+          // PV_A, S_A', PV_B, S_B': each tile's softmax runs under the other's MMAs
+          ok = ok && wait_k(j);
+          if (ok) {
+            tc_fence_after();
+            issue_s(0, j);
+            issue_s(1, j);
+            umma_commit(&bars->k_empty[j % C::KS]);
+          }
+          for (int x = 0; ok && x < n; ++x, ++j) {
+            ok = wait(&bars->p_full[0], j) && wait_v(j);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(0, j, x == 0);
+            if (x + 1 < n) {
+              ok = wait_k(j + 1);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(0, j + 1);
+            }
+            ok = wait(&bars->p_full[1], j);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(1, j, x == 0);
+            umma_commit(&bars->v_empty[j % C::VS]);
+            if (x + 1 < n) {
+              issue_s(1, j + 1);
+              umma_commit(&bars->k_empty[(j + 1) % C::KS]);
+            }
+          }
+        }
+      }
+      // no MMA may be in flight when the TMEM is freed
+      umma_commit(&bars->drained);
+      drain_wait(&bars->drained, 0);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ draft tiles
+    constexpr int CH = D / 8;  // 16-byte chunks per row
+    constexpr int NL = 64;
+    const int lt = threadIdx.x - 64;
+    Cursor cur(p, bars);
+    Seg s;
+    int j0 = 0, round = 0;
+    uint32_t go = 0u;  // bit ks: parity of the next hand-over of K stage ks
+    bool ok = true;
+    while (ok && cur.next(s)) {
+      if (s.t0 < ntd) {
+        // the masks of the segment before may still be in use
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->mask_empty, (round & 1) ^ 1, abort, p.status));
+        ok = !named_bar_or(1, NL, !ok);
+        if (!ok) break;
+        for (int t = lt; t < p.T; t += NL) par[t] = s.ok ? p.parents[s.b * p.par_stride + t] : -2;
+        if (lt < 8) bars->bad[lt] = 0u;
+        named_bar_sync(1, NL);
+        // node t's ancestors, itself included: parents come before children, so
+        // a walk up ends within t steps; absent (no bits) unless it ends at -1
+        for (int t = lt; t < p.T; t += NL) {
+          uint32_t w[C::kWords];
+#pragma unroll
+          for (int x = 0; x < C::kWords; ++x) w[x] = 0u;
+          int a = t;
+          bool there = true;
+          for (;;) {
+            const int up = par[a];
+            if (up >= a) report(p.status, kStatusBounds);
+            if (up >= a || up < -1) {
+              there = false;
+              break;
+            }
+#pragma unroll
+            for (int x = 0; x < C::kWords; ++x)
+              if (x == (a >> 5)) w[x] |= 1u << (a & 31);
+            if (up < 0) break;
+            a = up;
+          }
+#pragma unroll
+          for (int x = 0; x < C::kWords; ++x) anc[t * C::kWords + x] = there ? w[x] : 0u;
+        }
+        named_bar_sync(1, NL);
+        for (int tile = s.t0; ok && tile < min(s.t1, ntd); ++tile) {
+          const int j = j0 + tile - s.t0;
+          const int ks = j % C::KS, vs = j % C::VS;
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->draft_go[ks], (go >> ks) & 1u, abort, p.status));
+          go ^= 1u << ks;
+          ok = !named_bar_or(1, NL, !ok);
+          if (!ok) break;
+          uint8_t* kt = smem + C::kOffK + ks * C::kTileBytes;
+          uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
+          const int n = min(kBN, p.T - tile * kBN);
+#pragma unroll 4
+          for (int x = lt; x < kBN * CH; x += NL) {
+            const int r = x / CH, ch = x % CH, node = tile * kBN + r;
+            uint4 kw = make_uint4(0u, 0u, 0u, 0u), vw = kw;
+            // present: its own bit is set
+            if (r < n && ((anc[node * C::kWords + (node >> 5)] >> (node & 31)) & 1u)) {
+              const uint16_t* kr = draft_row<D>(p, false, s.b, s.g, node, s.ctx);
+              const uint16_t* vr = draft_row<D>(p, true, s.b, s.g, node, s.ctx);
+              if (kr != nullptr) kw = *reinterpret_cast<const uint4*>(kr + ch * 8);
+              if (vr != nullptr) vw = *reinterpret_cast<const uint4*>(vr + ch * 8);
+              if (p.k_new != nullptr && s.m == 0) {
+                const int64_t row = cache_row(p, s.b, s.g, s.ctx + node);
+                if (row >= 0) {
+                  *reinterpret_cast<uint4*>(p.kc + row * D + ch * 8) = kw;
+                  *reinterpret_cast<uint4*>(p.vc + row * D + ch * 8) = vw;
+                }
+              }
+              bool bad = false;
+              vw.x = finite_pair(vw.x, bad), vw.y = finite_pair(vw.y, bad);
+              vw.z = finite_pair(vw.z, bad), vw.w = finite_pair(vw.w, bad);
+              if (bad) atomicOr(&bars->bad[node >> 5], 1u << (node & 31));
+            }
+            *reinterpret_cast<uint4*>(kt + tile_off(r, ch)) = kw;
+            *reinterpret_cast<uint4*>(vt + tile_off(r, ch)) = vw;
+          }
+          fence_proxy_async_smem();
+          named_bar_sync(1, NL);
+          if (lt == 0) {
+            mbar_arrive(&bars->k_full[ks]);
+            mbar_arrive(&bars->v_full[vs]);
+          }
+        }
+        if (ok && lt == 0) mbar_arrive(&bars->mask_full);
+        ++round;
+      }
+      j0 += s.t1 - s.t0;
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    if constexpr (NT == 2) regs_inc<C::kRegsSoft>();
+    const int t = (warp >> 2) - 1;  // row tile
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const int tid = threadIdx.x - 128;
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t o_col = C::kColO + t * D;
+    constexpr int CH = D / 8;
+
+    auto load_q = [&](const Seg& s) {
+      // this warpgroup's 128 rows; rows past R are zeros
+      uint8_t* qt = smem + C::kOffQ + t * C::kTileBytes;
+      const int r0 = (s.m * NT + t) * kBM;
+      const int wt = tid & 127;
+#pragma unroll 8
+      for (int x = wt; x < kBM * CH; x += 128) {
+        const int r = x / CH, ch = x % CH, rr = r0 + r;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (rr < p.R)
+          w = *reinterpret_cast<const uint4*>(p.q + s.b * p.q_stride[0] + (s.g * p.G + rr % p.G) * p.q_stride[1] +
+                                              (rr / p.G) * p.q_stride[2] + ch * 8);
+        *reinterpret_cast<uint4*>(qt + tile_off(r, ch)) = w;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->q_full[t]);
+    };
+
+    // PV of tile x is done.  Asked about the latest tile or the one before it;
+    // S(x + 1 or x + 2), seen by then, follows the PV that completed the phase
+    // before, so the parity is never read a phase early, and the phase after
+    // needs this warp's next P, so never a phase late.
+    auto o_wait = [&](int x) {
+      return NT == 1 ? mbar_wait(&bars->o_done[x & 1], (x >> 1) & 1, abort, p.status)
+                     : mbar_wait(&bars->o_done[t], x & 1, abort, p.status);
+    };
+
+    Cursor cur(p, bars);
+    Seg s, s_next;
+    bool ok = true;
+    bool more = cur.next(s);
+    if (more) load_q(s);
+    int j = 0, round = 0, pieces = 0;
+    while (ok && more) {
+      const int rr = (s.m * NT + t) * kBM + row;                // row of the KV head
+      const bool warp_on = rr - lane < p.R;                     // any row of this warp exists
+      const int node = rr < p.R ? rr / p.G : 0;
+      const bool has_draft = s.t0 < ntd;
+      float m_run = -INFINITY, l_run = 0.0f;
+      for (int tile = s.t0; tile < s.t1; ++tile, ++j) {
+        const int sb = NT == 1 ? (j & 1) : t;
+        const int sph = NT == 1 ? (j >> 1) & 1 : j & 1;
+        const uint32_t s_col = NT == 1 ? static_cast<uint32_t>((j & 1) * 128) : t * 128u;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[sb], sph, abort, p.status))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (tile == s.t0 && has_draft) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars->mask_full, round & 1, abort, p.status))) {
+            ok = false;
+            break;
+          }
+        }
+        // keys this row may see, a bit each
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+        bool masked = !p.scale_positive;
+        if (tile < ntd) {
+          masked = true;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            see[x] = (tile * 4 + x < C::kWords && rr < p.R) ? anc[node * C::kWords + tile * 4 + x] : 0u;
+        } else {
+          const int lim = s.ctx - (tile - ntd) * kBN;
+          if (lim < kBN) {
+            masked = true;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int left = lim - x * 32;
+              see[x] = left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u);
+            }
+            // V rows past the context: whatever the slots hold, or nothing loaded
+            const int vs = j % C::VS;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs], (j / C::VS) & 1, abort, p.status))) {
+              ok = false;
+              break;
+            }
+            uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
+            for (int x = tid & 127; x < (kBN - lim) * CH; x += 128)
+              *reinterpret_cast<uint4*>(vt + tile_off(lim + x / CH, x % CH)) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+          }
+        }
+        if (warp_on) {
+          uint32_t sr[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_addr + s_col + c * 32, sr[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_wait_ld(sr[c]);
+          float mx[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+          if (!masked) {
+#pragma unroll
+            for (int c = 0; c < kBN; c += 2)
+              mx[(c >> 1) & 7] = fmax3(mx[(c >> 1) & 7], __uint_as_float(sr[c >> 5][c & 31]),
+                                       __uint_as_float(sr[c >> 5][(c & 31) + 1]));
+          } else {
+#pragma unroll
+            for (int c = 0; c < kBN; ++c) {
+              const float x = ((see[c >> 5] >> (c & 31)) & 1u) ? __uint_as_float(sr[c >> 5][c & 31]) * p.scale_log2
+                                                               : -INFINITY;
+              sr[c >> 5][c & 31] = __float_as_uint(x);
+              mx[c & 7] = fmaxf(mx[c & 7], x);
+            }
+          }
+          float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+          if (!masked) mt *= p.scale_log2;
+          // the reference max moves only when the tile exceeds it by the margin
+          float alpha = 1.0f;
+          if (mt > m_run + kRescaleMargin || (m_run == -INFINITY && mt != -INFINITY)) {
+            alpha = fast_exp2(m_run - mt);
+            m_run = mt;
+          }
+          const float neg = m_run == -INFINITY ? 0.0f : -m_run;
+          const float mul = masked ? 1.0f : p.scale_log2;
+          const uint64_t mul2 = f2_pack(mul, mul), neg2 = f2_pack(neg, neg);
+          uint64_t sum[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pw[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float x0, x1;
+              f2_unpack(ffma2(f2_pack(__uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1])), mul2, neg2), x0, x1);
+              const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+              pw[i >> 1] = pack_bf16x2(p0, p1);
+              sum[(i >> 1) & 3] = fadd2(sum[(i >> 1) & 3], f2_pack(p0, p1));
+            }
+            tmem_st16(tmem + lane_addr + s_col + c * 16, pw);
+          }
+          float a0, a1;
+          f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
+          l_run = l_run * alpha + (a0 + a1);
+          if (tile > s.t0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+            if (!__all_sync(0xffffffffu, o_wait(j - 1))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tmem + lane_addr + o_col + c * 32, o);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(tmem + lane_addr + o_col + c * 32, o);
+            }
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[sb]);
+      }
+      if (!ok) break;
+      // the next segment's queries while the last PV runs (every S of this one is done)
+      const bool more_next = cur.next(s_next);
+      if (more_next) load_q(s_next);
+
+      // ---------------------------------------------------------- epilogue
+      if (!__all_sync(0xffffffffu, o_wait(j - 1))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+      // drafts this row sees whose V is not finite, and whether the row's own draft is absent
+      bool absent = false;
+      uint32_t fix_any = 0u;
+      if (has_draft && rr < p.R) {
+        uint32_t own = 0u;
+#pragma unroll
+        for (int x = 0; x < C::kWords; ++x) {
+          own |= anc[node * C::kWords + x];
+          fix_any |= anc[node * C::kWords + x] & bars->bad[x];
+        }
+        absent = own == 0u;
+      }
+      const bool empty = absent || l_run == 0.0f;
+      const float inv = empty ? 0.0f : 1.0f / l_run;
+      const float lse2 = empty ? -INFINITY : m_run + __log2f(l_run);
+      const int head = s.g * p.G + (rr < p.R ? rr % p.G : 0);
+      const int slot = 2 * static_cast<int>(blockIdx.x) + (s.item0 + s.t0 == bars->lo ? 0 : 1);
+      const int64_t prow = static_cast<int64_t>(slot) * p.slot_rows + t * kBM + row;
+      const int64_t obase = s.b * p.out_stride[0] + head * p.out_stride[1] + node * p.out_stride[2];
+      if (warp_on) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lane_addr + o_col + c * 32, o);
+          tmem_wait_ld(o);
+          if (rr < p.R) {
+            if (fix_any != 0u) {
+              for (int a = s.t0 * kBN; a < min(p.T, s.t1 * kBN); ++a) {
+                if (!((anc[node * C::kWords + (a >> 5)] & bars->bad[a >> 5]) >> (a & 31) & 1u)) continue;
+                const uint16_t* kr = draft_row<D>(p, false, s.b, s.g, a, s.ctx);
+                const uint16_t* vr = draft_row<D>(p, true, s.b, s.g, a, s.ctx);
+                const uint16_t* qr = p.q + s.b * p.q_stride[0] + head * p.q_stride[1] + node * p.q_stride[2];
+                if (kr == nullptr || vr == nullptr) continue;
+                float dot = 0.f;
+                for (int d = 0; d < D; ++d)
+                  dot = fmaf(__uint_as_float(static_cast<uint32_t>(qr[d]) << 16),
+                             __uint_as_float(static_cast<uint32_t>(kr[d]) << 16), dot);
+                const float w = fast_exp2(dot * p.scale_log2 - m_run);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float v = __uint_as_float(static_cast<uint32_t>(vr[c * 32 + i]) << 16);
+                  if (!isfinite(v)) o[i] = __float_as_uint(fmaf(w, v, __uint_as_float(o[i])));
+                }
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = empty ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+            if (!whole) {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                     __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+            } else if (p.out_bf16) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + obase + c * 32);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                dst[i] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
+                                    pack_bf16x2(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
+                                    pack_bf16x2(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
+                                    pack_bf16x2(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])));
+            } else {
+              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + obase + c * 32);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                     __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+            }
+          }
+          __syncwarp();
+        }
+        if (rr < p.R) {
+          if (!whole)
+            p.part_lse[prow] = absent ? __uint_as_float(kAbsent) : lse2;
+          else if (p.lse != nullptr)
+            p.lse[(static_cast<int64_t>(s.b) * p.Hq + head) * p.T + node] = lse2 * 0.6931471805599453f;
+        }
+      }
+      tc_fence_before();  // O is read: the next segment's PV may overwrite it after p_full
+      if (has_draft) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->mask_empty);
+        ++round;
+      }
+      if (!whole) {
+        // Count this piece in; the piece that completes the item takes the count
+        // back to zero and merges.  A word of another generation (another call,
+        // or whatever the workspace held) reads as zero; a captured graph replays
+        // its own generation with other lengths, hence the way back to zero.
+        const int c0 = run_of(bars->total, bars->n_cta, s.item0);
+        const int np = run_of(bars->total, bars->n_cta, s.item0 + s.tiles - 1) - c0 + 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->piece_full);
+        if (tid < 32 && !__all_sync(0xffffffffu, mbar_wait(&bars->piece_full, pieces & 1, abort, p.status))) {
+          ok = false;
+          break;
+        }
+        if (tid == 0) {
+          __threadfence();
+          unsigned long long* w = p.count + (static_cast<int64_t>(s.b) * p.Hkv + s.g) * p.MP + s.m;
+          const unsigned long long tag = static_cast<unsigned long long>(p.gen) << 32;
+          unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(w), now;
+          for (;;) {
+            now = (old >> 32) == p.gen ? old + 1 : tag + 1;
+            const unsigned long long seen = atomicCAS(w, old, now);
+            if (seen == old) break;
+            old = seen;
+          }
+          const bool last = (now & 0xffffffffull) == static_cast<unsigned long long>(np);
+          if (last) *w = tag;
+          bars->last = last;
+          mbar_arrive(&bars->piece_go);
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->piece_go, pieces & 1, abort, p.status))) {
+          ok = false;
+          break;
+        }
+        ++pieces;
+        if (bars->last) {
+          __threadfence();
+          const int row0 = s.m * NT * kBM;
+          merge_item<D>(p, s, row0, min(p.R - row0, NT * kBM), c0, np,
+                        run_lo(bars->total, bars->n_cta, c0) == s.item0, tid, C::kSoft);
+        }
+      }
+      s = s_next;
+      more = more_next;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+int tree_nt(int64_t R) { return R <= kBM ? 1 : 2; }
+
+template <int D, int NT>
+cudaError_t launch(const TreeArgs& a, TreeParams& p, cudaStream_t stream) {
+  using C = Cfg<D, NT>;
+  CUtensorMap mk, mv;
+  if (!make_paged_map(&mk, a.cache.k, a.cache.num_blocks, a.cache.Hkv, D) ||
+      !make_paged_map(&mv, a.cache.v, a.cache.num_blocks, a.cache.Hkv, D))
+    return cudaErrorInvalidValue;
+  auto kern = paged_tree_tc_kernel<D, NT>;
+  if constexpr (NT == 2) {
+    // the setmaxnreg split must fit in what the launch gives (a larger one waits forever)
+    static const bool fits = [&] {
+      cudaFuncAttributes fa;
+      return cudaFuncGetAttributes(&fa, kern) == cudaSuccess &&
+             128 * C::kRegsCtl + 256 * C::kRegsSoft <= fa.numRegs * C::kThreads;
+    }();
+    if (!fits) return cudaErrorInvalidConfiguration;
+  }
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(a.n_cta), C::kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Partials of two cut items per CTA, then one 8-byte count per item.
+size_t tree_partial_bytes(int64_t B, int64_t Hkv, int64_t R, int D, int n_cta) {
+  const int nt = tree_nt(R);
+  const size_t rows = static_cast<size_t>(2) * n_cta * (R < nt * kBM ? R : nt * kBM);
+  const size_t parts = (rows * (D + 1) * sizeof(float) + 255) & ~size_t(255);
+  const size_t items = static_cast<size_t>(B) * Hkv * ((R + nt * kBM - 1) / (nt * kBM));
+  return parts + ((items * sizeof(unsigned long long) + 255) & ~size_t(255));
+}
+
+cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream) {
+  TreeParams p = {};
+  p.B = static_cast<int>(a.B);
+  p.T = static_cast<int>(a.T);
+  p.Hq = static_cast<int>(a.Hq);
+  p.Hkv = a.cache.Hkv;
+  p.G = p.Hq / p.Hkv;
+  p.R = p.T * p.G;
+  const int nt = tree_nt(p.R);
+  p.MP = (p.R + nt * kBM - 1) / (nt * kBM);
+  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  p.scale_positive = p.scale_log2 > 0.0f;
+  p.q = static_cast<const uint16_t*>(a.q.data);
+  p.k_new = static_cast<const uint16_t*>(a.k_new.data);
+  p.v_new = static_cast<const uint16_t*>(a.v_new.data);
+  for (int i = 0; i < 3; ++i) {
+    p.q_stride[i] = a.q.stride[i];
+    p.kn_stride[i] = a.k_new.stride[i];
+    p.vn_stride[i] = a.v_new.stride[i];
+    p.out_stride[i] = a.out.stride[i];
+  }
+  p.kc = static_cast<uint16_t*>(a.cache.k);
+  p.vc = static_cast<uint16_t*>(a.cache.v);
+  p.num_blocks = static_cast<int>(a.cache.num_blocks);
+  p.bt = a.block_table;
+  p.bt_stride = a.bt_stride;
+  p.max_blocks = a.max_blocks;
+  p.ctx_lens = a.ctx_lens;
+  p.parents = a.parents;
+  p.par_stride = a.par_stride;
+  p.out = a.out.data;
+  p.out_bf16 = a.out.dtype == ATTN_BF16;
+  p.lse = a.lse;
+  p.slot_rows = p.R < nt * kBM ? p.R : nt * kBM;
+  const size_t rows = static_cast<size_t>(2) * a.n_cta * p.slot_rows;
+  p.part_o = static_cast<float*>(a.partials);
+  p.part_lse = p.part_o + rows * a.cache.D;
+  const size_t parts = (rows * (a.cache.D + 1) * sizeof(float) + 255) & ~size_t(255);
+  p.count = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(a.partials) + parts);
+  p.gen = a.gen;
+  p.status = a.status;
+  if (a.cache.D == 64) return nt == 1 ? launch<64, 1>(a, p, stream) : launch<64, 2>(a, p, stream);
+  if (a.cache.D == 128) return nt == 1 ? launch<128, 1>(a, p, stream) : launch<128, 2>(a, p, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace attn
