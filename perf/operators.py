@@ -246,6 +246,8 @@ def _run_own(s):
         nbytes = 256
         if op == "tree":
             nbytes = lib.paged_tree_workspace_size(s["B"], s["Hq"], s["Hkv"], s["T"], s["bt"].shape[1], BS, s["D"])
+        elif op == "weights":
+            nbytes = lib.paged_attn_weights_workspace_size(s["B"], s["Hkv"], s["bt"].shape[1], BS)
         s["ws"] = lib.Workspace(nbytes)
     if op == "rope_append":
         q = lib.rope_kv_append(s["q"], s["k_new"], s["v_new"], s["positions"], s["freqs"], s["k_cache"], s["v_cache"],
