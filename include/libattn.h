@@ -585,6 +585,79 @@ attn_status kv_tree_accept(const attn_kv_cache *cache, const int32_t *block_tabl
                            int32_t max_path, const int32_t *n_accept, int32_t batch,
                            void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * paged_attn_weights -- the attention weight that every cached token received
+ * from a chunk of queries, added to a running sum per (token, KV head): what
+ * kv_evict ranks tokens by.
+ *
+ * Sequence b's chunk has n = q_lens[b] queries (T without q_lens) at positions
+ * start_pos[b] + i, whose keys are in the cache and whose softmax LSE an
+ * attention call over the same keys returned.  With g = h / (Hq / Hkv):
+ *     w[g, t] = sum over query heads h of g and rows i that see token t of
+ *               exp(scale * <q[b,h,i,:], K[t]> - lse[b,h,i])
+ *     t <  start_pos[b]:                      acc[t] += w[t]
+ *     start_pos[b] <= t < start_pos[b] + n:   acc[t]  = w[t]
+ * so a chunk's own tokens begin their sums, whatever the slot held before.  Row
+ * i sees tokens t <= start_pos[b] + i (causal = 1) or t < start_pos[b] + n (0).
+ * A row whose lse is -inf (it saw nothing) adds nothing.
+ *
+ *   q        [batch, Hq, T, head_dim] bf16 (strided view, 16-byte aligned rows)
+ *   lse      float32 [batch, Hq, T] contiguous
+ *   cache    K is read (V is not)
+ *   acc      float32 [num_blocks, num_kv_heads, block_size], the sums of the
+ *            cache's slots.  Blocks must not be shared between sequences of a call.
+ *   q_lens   int32 [batch] (clamped to [0, T]) or NULL
+ *   start_pos  int32 [batch].  < 0: an idle sequence.  start_pos[b] + n past the
+ *            table sets ATTN_ERR_DEVICE_BOUNDS and counts as idle; tokens of a bad
+ *            block id are left out (the flag is set).
+ *   workspace >= paged_attn_weights_workspace_size(...) bytes on the current
+ *            device: partial sums of the tiles that are cut between SMs, and
+ *            their counts; no clearing between calls.  Calls that share a
+ *            workspace must not overlap on the GPU.
+ * Scores on the tensor cores, fp32 accumulation and sums; the result does not
+ * depend on timing.
+ */
+size_t paged_attn_weights_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t max_blocks,
+                                         int32_t block_size);
+attn_status paged_attn_weights(const attn_tensor *q, const float *lse, const attn_kv_cache *cache,
+                               const int32_t *block_table, int64_t bt_stride, int32_t max_blocks,
+                               const int32_t *start_pos, const int32_t *q_lens, int32_t causal, float scale,
+                               float *acc, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * kv_evict -- cut every sequence's cache to at most `keep` tokens a KV head, by
+ * accumulated attention weight.
+ *
+ * For sequence b with L = ctx_lens[b] > keep tokens, each KV head keeps, on its
+ * own: the first `sink` slots, the last `recent` slots, and of the others those
+ * with the largest acc, `keep` in all (ties go to the lowest slot; a NaN ranks
+ * below every number).  With L <= keep everything is kept.  The kept tokens' K,
+ * V and acc are copied bit for bit, in slot order, to slots 0, 1, ... of the
+ * blocks of dst_table; the source blocks are only read (they may be shared) and
+ * are the caller's to free.  Heads keep different tokens, so afterwards a slot
+ * stands for a different position in each head: keys must have been rotated
+ * before they were cached (rope_kv_append), and later tokens' positions go on
+ * from the sequence's true length while their slots go on from new_lens[b].
+ *
+ *   acc        float32 [num_blocks, num_kv_heads, block_size]
+ *   dst_table  int32 [batch, >= dst_blocks] (row stride dst_stride): blocks that
+ *              no block_table row of the call names, each at most once.
+ *              A kept token past its dst_blocks * 16 slots, or a bad block id in
+ *              either table, sets ATTN_ERR_DEVICE_BOUNDS and is not copied.
+ *   ctx_lens   int32 [batch]; < 0 marks an idle sequence; more than the table
+ *              holds sets ATTN_ERR_DEVICE_BOUNDS and is cut to it
+ *   keep       >= 1; sink, recent >= 0, sink + recent <= keep
+ *   new_lens   int32 [batch], written: min(L, keep) (idle: ctx_lens[b])
+ *   kept       int32 [batch, num_kv_heads, keep], written: the source slots in
+ *              order, -1 past them
+ *   workspace  >= kv_append_workspace_size() bytes (the status word)
+ */
+attn_status kv_evict(const attn_kv_cache *cache, float *acc, const int32_t *block_table, int64_t bt_stride,
+                     int32_t max_blocks, const int32_t *ctx_lens, const int32_t *dst_table, int64_t dst_stride,
+                     int32_t dst_blocks, int32_t batch, int32_t keep, int32_t sink, int32_t recent,
+                     int32_t *new_lens, int32_t *kept,
+                     void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Test/debug export: gather the paged cache of every (sequence, KV head) into
  * contiguous dst [batch, num_kv_heads, max_len, head_dim] (bf16), tokens
  * t < lens[b]; rows t >= lens[b] are left untouched.  Bit-exact.

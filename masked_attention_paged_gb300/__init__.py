@@ -28,6 +28,7 @@ __all__ = [
     "attn_fwd_workspace_size", "paged_decode_workspace_size", "check_device_status",
     "rope_frequencies", "rope_apply", "rope_kv_append", "rope_kv_append_q8",
     "paged_tree_workspace_size", "paged_tree_attn", "kv_tree_accept",
+    "paged_attn_weights_workspace_size", "paged_attn_weights", "kv_evict",
 ]
 
 ATTN_F32, ATTN_BF16 = 0, 1
@@ -92,6 +93,9 @@ def _signatures() -> dict:
         "paged_tree_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32, I32]),
         "paged_tree_attn": (I32, [T, T, T, C, P, I64, I32, P, P, I64, F, T, P, P, SZ, P]),
         "kv_tree_accept": (I32, [C, P, I64, I32, P, P, I64, I32, P, I32, P, SZ, P]),
+        "paged_attn_weights_workspace_size": (SZ, [I32, I32, I32, I32]),
+        "paged_attn_weights": (I32, [T, P, C, P, I64, I32, P, P, I32, F, P, P, SZ, P]),
+        "kv_evict": (I32, [C, P, P, I64, I32, P, P, I64, I32, I32, I32, I32, I32, P, P, P, SZ, P]),
         "attn_check_device_status": (I32, [P, ctypes.POINTER(ctypes.c_uint32), P]),
         "attn_reset_device_status": (I32, [P, P]),
         "attn_selftest_wait_timeout": (I32, [P, SZ, ctypes.c_uint32, P]),
@@ -136,7 +140,8 @@ def exported_symbols() -> list[str]:
             "attn_key_padding_to_additive", "paged_decode_attn_append", "paged_prefill_attn",
             "attn_fwd_workspace_size_for", "kv_append_q8", "paged_decode_attn_q8", "paged_decode_attn_append_q8",
             "attn_rope_frequencies", "rope_apply", "rope_kv_append", "rope_kv_append_q8",
-            "paged_tree_workspace_size", "paged_tree_attn", "kv_tree_accept"]
+            "paged_tree_workspace_size", "paged_tree_attn", "kv_tree_accept",
+            "paged_attn_weights_workspace_size", "paged_attn_weights", "kv_evict"]
 
 
 # --------------------------------------------------------------------------
@@ -907,3 +912,89 @@ def kv_tree_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: to
                             block_table.shape[1], _ptr(ctx_lens, "ctx_lens"), _ptr(path, "path"), path.stride(0),
                             path.shape[1], _ptr(n_accept, "n_accept"), B, ws.ptr, ws.nbytes, _stream(stream))
     _check("kv_tree_accept", st)
+
+
+# --------------------------------------------------------------------------
+# eviction by accumulated attention weight
+# --------------------------------------------------------------------------
+def _check_acc(acc: torch.Tensor, cache: torch.Tensor):
+    if not (isinstance(acc, torch.Tensor) and acc.dtype == torch.float32 and acc.is_contiguous()
+            and acc.shape == cache.shape[:3]):
+        raise ValueError(f"acc must be contiguous float32 {tuple(cache.shape[:3])}")
+
+
+def paged_attn_weights_workspace_size(batch: int, num_kv_heads: int, max_blocks: int, block_size: int = 16) -> int:
+    return int(load().paged_attn_weights_workspace_size(batch, num_kv_heads, max_blocks, block_size))
+
+
+def paged_attn_weights(q: torch.Tensor, lse: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor,
+                       start_pos: torch.Tensor, acc: torch.Tensor, q_lens: Optional[torch.Tensor] = None,
+                       causal: bool = True, scale: Optional[float] = None, workspace: Optional[Workspace] = None,
+                       stream=None) -> torch.Tensor:
+    """Add the attention weight each cached token received from a chunk of
+    queries to acc (float32 [num_blocks, Hkv, 16], in place; the chunk's own
+    tokens start from zero).  q [B, Hq, T, D] at positions start_pos[b] + i with
+    lse float32 [B, Hq, T] as an attention call returned it; [B, Hq, D] and [B,
+    Hq] for one token a sequence.  q_lens int32 [B]: queries of each sequence."""
+    lib = load()
+    if q.dim() == 3:
+        q, lse = q.unsqueeze(2), lse.unsqueeze(2)
+    B, Hq, T, D = q.shape
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    _check_f32_buffer(lse, B * Hq * T, "lse")
+    _check_block_table(block_table, B)
+    _check_int32_vec(start_pos, B, "start_pos")
+    if q_lens is not None:
+        _check_int32_vec(q_lens, B, "q_lens")
+    c = _cache(k_cache, k_cache)
+    _check_acc(acc, k_cache)
+    _check_devices("paged_attn_weights", q, lse, k_cache, block_table, start_pos, acc, q_lens)
+    max_blocks = block_table.shape[1]
+    ws = workspace
+    if ws is None:
+        ws = Workspace(paged_attn_weights_workspace_size(B, k_cache.shape[1], max_blocks, k_cache.shape[2]),
+                       device=q.device)
+    dq = _desc(q)
+    st = lib.paged_attn_weights(ctypes.byref(dq), _ptr(lse, "lse"), ctypes.byref(c), _ptr(block_table, "block_table"),
+                                block_table.stride(0), max_blocks, _ptr(start_pos, "start_pos"),
+                                _ptr(q_lens, "q_lens"), int(bool(causal)), float(scale), _ptr(acc, "acc"), ws.ptr,
+                                ws.nbytes, _stream(stream))
+    _check("paged_attn_weights", st)
+    return acc
+
+
+def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, block_table: torch.Tensor,
+             ctx_lens: torch.Tensor, dst_block_table: torch.Tensor, keep: int, sink: int = 0, recent: int = 0,
+             new_lens: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None,
+             workspace: Optional[Workspace] = None, stream=None):
+    """Keep `keep` tokens of each sequence and KV head (the first `sink`, the
+    last `recent`, and the largest acc of the others) and copy their K, V and
+    acc, in order, to the blocks of dst_block_table.  Returns (new_lens int32
+    [B], kept int32 [B, Hkv, keep]: the source slots, -1 past them)."""
+    lib = load()
+    B, Hkv = ctx_lens.shape[0], k_cache.shape[1]
+    _check_block_table(block_table, B)
+    _check_int32_vec(ctx_lens, B, "ctx_lens")
+    if not (isinstance(dst_block_table, torch.Tensor) and dst_block_table.dtype == torch.int32
+            and dst_block_table.dim() == 2 and dst_block_table.shape[0] >= B and dst_block_table.stride(1) == 1
+            and dst_block_table.stride(0) >= dst_block_table.shape[1]):
+        raise ValueError(f"dst_block_table must be int32 [>= {B}, blocks] with contiguous rows")
+    c = _cache(k_cache, v_cache)
+    _check_acc(acc, k_cache)
+    keep = int(keep)
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=k_cache.device)
+    if kept is None:
+        kept = torch.empty((B, Hkv, max(keep, 0)), dtype=torch.int32, device=k_cache.device)
+    _check_int32_vec(new_lens, B, "new_lens")
+    if not (kept.dtype == torch.int32 and kept.is_contiguous() and kept.shape == (B, Hkv, keep)):
+        raise ValueError(f"kept must be contiguous int32 {(B, Hkv, keep)}, got {tuple(kept.shape)}")
+    _check_devices("kv_evict", k_cache, v_cache, acc, block_table, ctx_lens, dst_block_table, new_lens, kept)
+    ws = workspace or _small_ws(k_cache.device)
+    st = lib.kv_evict(ctypes.byref(c), _ptr(acc, "acc"), _ptr(block_table, "block_table"), block_table.stride(0),
+                      block_table.shape[1], _ptr(ctx_lens, "ctx_lens"), _ptr(dst_block_table, "dst_block_table"),
+                      dst_block_table.stride(0), dst_block_table.shape[1], B, keep, int(sink), int(recent),
+                      _ptr(new_lens, "new_lens"), _ptr(kept, "kept"), ws.ptr, ws.nbytes, _stream(stream))
+    _check("kv_evict", st)
+    return new_lens, kept

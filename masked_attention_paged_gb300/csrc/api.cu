@@ -771,6 +771,97 @@ attn_status kv_tree_accept(const attn_kv_cache* cache, const int32_t* block_tabl
   return from_cuda(launch_tree_accept(a, stream));
 }
 
+size_t paged_attn_weights_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t max_blocks,
+                                         int32_t block_size) {
+  if (batch < 0 || num_kv_heads < 0 || max_blocks < 0 || block_size != 16) return 0;
+  return kStatusBytes + weights_partial_bytes(batch, num_kv_heads, max_blocks, device_sm_count());
+}
+
+attn_status paged_attn_weights(const attn_tensor* q, const float* lse, const attn_kv_cache* cache,
+                               const int32_t* block_table, int64_t bt_stride, int32_t max_blocks,
+                               const int32_t* start_pos, const int32_t* q_lens, int32_t causal, float scale,
+                               float* acc, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  attn_status st;
+  if ((st = check_cache(cache)) != ATTN_OK) return st;
+  if ((st = check_tensor(q, 4)) != ATTN_OK) return st;
+  const int64_t B = q->shape[0], Hq = q->shape[1], T = q->shape[2], D = q->shape[3];
+  if (q->dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
+  if (D != cache->head_dim) return ATTN_ERR_INVALID_ARG;
+  if (Hq <= 0 || Hq % cache->num_kv_heads != 0) return ATTN_ERR_INVALID_ARG;
+  if (!isfinite(scale) || (causal != 0 && causal != 1)) return ATTN_ERR_INVALID_ARG;
+  if (max_blocks <= 0 || max_blocks > (1 << 24)) return ATTN_ERR_INVALID_ARG;
+  if (B > 65535 || Hq > 65535 || T > (1 << 24) || T * (Hq / cache->num_kv_heads) > (int64_t(1) << 30) ||
+      cache->num_blocks > 0x7fffffff)
+    return ATTN_ERR_UNSUPPORTED;
+  const size_t need = paged_attn_weights_workspace_size(static_cast<int32_t>(B), cache->num_kv_heads, max_blocks,
+                                                        cache->block_size);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != ATTN_OK) return st;
+  if (B == 0 || T == 0) return ATTN_OK;
+  if (block_table == nullptr || start_pos == nullptr || lse == nullptr || acc == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(acc, 4)) return ATTN_ERR_INVALID_ARG;
+  if (B > 1 && bt_stride < max_blocks) return ATTN_ERR_INVALID_ARG;
+  if (!vec16_ok(q)) return ATTN_ERR_INVALID_ARG;
+  WeightArgs a;
+  a.cache = paged(cache);
+  a.q = view(q);
+  a.lse = lse;
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.max_blocks = max_blocks;
+  a.start_pos = start_pos;
+  a.q_lens = q_lens;
+  a.causal = causal;
+  a.B = B;
+  a.Hq = Hq;
+  a.T = T;
+  a.scale = scale;
+  a.acc = acc;
+  a.partials = static_cast<uint8_t*>(workspace) + kStatusBytes;
+  a.n_cta = device_sm_count();
+  a.gen = next_decode_gen();
+  a.status = static_cast<uint32_t*>(workspace);
+  if (a.n_cta <= 0) return ATTN_ERR_CUDA;
+  return from_cuda(launch_attn_weights(a, stream));
+}
+
+attn_status kv_evict(const attn_kv_cache* cache, float* acc, const int32_t* block_table, int64_t bt_stride,
+                     int32_t max_blocks, const int32_t* ctx_lens, const int32_t* dst_table, int64_t dst_stride,
+                     int32_t dst_blocks, int32_t batch, int32_t keep, int32_t sink, int32_t recent, int32_t* new_lens,
+                     int32_t* kept, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  attn_status st;
+  if ((st = check_cache(cache)) != ATTN_OK) return st;
+  if (batch < 0 || keep < 1 || sink < 0 || recent < 0 || static_cast<int64_t>(sink) + recent > keep)
+    return ATTN_ERR_INVALID_ARG;
+  if (max_blocks <= 0 || max_blocks > (1 << 24) || dst_blocks <= 0 || dst_blocks > (1 << 24))
+    return ATTN_ERR_INVALID_ARG;
+  if (batch > 65535 || cache->num_kv_heads > 65535 || keep > (1 << 28)) return ATTN_ERR_UNSUPPORTED;
+  if ((st = check_workspace(workspace, workspace_bytes, kv_append_workspace_size())) != ATTN_OK) return st;
+  if (batch == 0) return ATTN_OK;
+  if (acc == nullptr || block_table == nullptr || ctx_lens == nullptr || dst_table == nullptr ||
+      new_lens == nullptr || kept == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(acc, 4)) return ATTN_ERR_INVALID_ARG;
+  if (batch > 1 && (bt_stride < max_blocks || dst_stride < dst_blocks)) return ATTN_ERR_INVALID_ARG;
+  EvictArgs a;
+  a.cache = paged(cache);
+  a.acc = acc;
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.max_blocks = max_blocks;
+  a.dst_table = dst_table;
+  a.dst_stride = dst_stride;
+  a.dst_blocks = dst_blocks;
+  a.ctx_lens = ctx_lens;
+  a.B = batch;
+  a.keep = keep;
+  a.sink = sink;
+  a.recent = recent;
+  a.new_lens = new_lens;
+  a.kept = kept;
+  a.status = static_cast<uint32_t*>(workspace);
+  return from_cuda(launch_kv_evict(a, stream));
+}
+
 attn_status attn_selftest_wait_timeout(void* workspace, size_t workspace_bytes, uint32_t timeout_us,
                                        cudaStream_t stream) {
   attn_status st;

@@ -210,6 +210,45 @@ struct AcceptArgs {
 // cache slots ctx + path[i] -> ctx + i, i < n_accept
 cudaError_t launch_tree_accept(const AcceptArgs& a, cudaStream_t stream);
 
+struct WeightArgs {
+  PagedCache cache;  // K only
+  View4 q;           // [B, Hq, T, D]
+  const float* lse;  // [B, Hq, T]
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int max_blocks;
+  const int32_t* start_pos;  // [B] position of the chunk's first query
+  const int32_t* q_lens;     // [B] queries of each sequence, or null (T)
+  int causal;
+  int64_t B, Hq, T;
+  float scale;
+  float* acc;      // [num_blocks, Hkv, 16]
+  void* partials;  // workspace after the status block
+  int n_cta;       // CTAs of the launch (one per SM)
+  uint32_t gen;    // this call's generation (never 0)
+  uint32_t* status;
+};
+size_t weights_partial_bytes(int64_t B, int64_t Hkv, int max_blocks, int n_cta);
+cudaError_t launch_attn_weights(const WeightArgs& a, cudaStream_t stream);
+
+struct EvictArgs {
+  PagedCache cache;
+  float* acc;  // [num_blocks, Hkv, 16]
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int max_blocks;
+  const int32_t* dst_table;
+  int64_t dst_stride;
+  int dst_blocks;
+  const int32_t* ctx_lens;
+  int64_t B;
+  int keep, sink, recent;
+  int32_t* new_lens;  // [B]
+  int32_t* kept;      // [B, Hkv, keep]
+  uint32_t* status;
+};
+cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t stream);
+
 // Rotary positions; with k_new set, also the rotated append to the cache.
 struct RopeArgs {
   View4 x, out;        // [B, H, T, D] bf16 or f32 (bf16 with a cache)

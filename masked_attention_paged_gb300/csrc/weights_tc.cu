@@ -1,0 +1,591 @@
+// weights_tc.cu -- attention weight received by every cached token (tcgen05 +
+// TMEM + TMA): the sums that an eviction policy ranks tokens by.
+//
+// For a chunk of queries whose softmax LSE is known,
+//   acc[key] (+)= sum over the KV head's query heads and the chunk's rows that
+//                 see the key of 2^(scale_log2 q.k - lse_log2).
+// Scores are computed transposed, S^T = K Q^T: keys are the MMA's rows (TMEM
+// lanes) and queries its columns, so a thread owns a key and its sum stays in one
+// register, with no exchange between threads.  K is read once per query chunk
+// list (a pair of 128-key tiles stays in shared memory while all queries pass),
+// V not at all.  Bound: HBM for single tokens (64 KB of K per pair, 1.4 us of an
+// SM's share); the exponentials for long chunks (one per query row and key).
+//
+// Row r of a (sequence, KV head) is query r / G, head r % G; a key at position x
+// is seen by rows r >= (x - start) G, so a causal tile is one comparison per
+// column, and chunks of 128 rows before the pair's first key are left out.  An
+// item is a (sequence, KV head, key pair), its steps are its chunks; every SM
+// takes an equal run of all steps (as in tree_tc.cu), and an item cut between
+// SMs leaves partial sums that its last piece adds up in order: the result does
+// not depend on the timing.
+//
+// Warps: 0 streams K pairs, 1 issues the MMAs, 2-3 gather query chunks with
+// cp.async (any strides), 4-7 and 8-11 own the two key tiles.
+#include <cuda.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace attn {
+namespace {
+
+constexpr int kBM = 128;       // keys per tile
+constexpr int kPair = 2 * kBM;
+constexpr int kBN = 128;       // query rows per chunk
+constexpr int kBS = 16;
+constexpr int kBoxBytes = kBM * 128;
+constexpr int kThreads = 384;
+constexpr int kLoaders = 64;
+constexpr int kLseRing = 8;
+
+template <int D>
+struct Cfg {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTileBytes = kBM * D * 2;
+  static constexpr int KS = 2;                // K pair stages
+  static constexpr int QS = D == 64 ? 4 : 2;  // query chunk stages
+  static constexpr int kOffK = 0;
+  static constexpr int kOffQ = kOffK + KS * 2 * kTileBytes;
+  static constexpr int kOffLse = kOffQ + QS * kTileBytes;  // [kLseRing][kBN] log2 LSEs, +inf: no weight
+  static constexpr int kOffBar = kOffLse + kLseRing * kBN * 4;
+  static constexpr int kSmemBytes = kOffBar + 512 + 1024;
+  static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+};
+
+struct Bars {
+  uint64_t k_full[2], k_empty[2];
+  uint64_t q_full[4], q_empty[4];
+  uint64_t s_full[2], s_free[2];  // [score buffer], both key tiles
+  uint64_t piece_full, piece_go, drained;
+  int64_t lo, hi, total, bstart;
+  int b0, n_cta;
+  uint32_t tmem_base;
+  int abort, last;
+  int odd[kLseRing];  // the chunk has columns without weight (padding, or rows that see nothing)
+};
+static_assert(sizeof(Bars) <= 512, "barrier block outgrew its shared-memory slot");
+
+struct WeightParams {
+  int B, T, Hq, Hkv, G;
+  int causal;
+  float scale_log2;
+  const uint16_t* q;
+  int64_t q_stride[3];
+  const float* lse;  // [B, Hq, T]
+  int num_blocks;
+  const int32_t* bt;
+  int64_t bt_stride;
+  int max_blocks;
+  const int32_t* start_pos;
+  const int32_t* q_lens;  // or null: T each
+  float* acc;             // [num_blocks, Hkv, 16]
+  float* part;            // [2 n][kPair]
+  unsigned long long* count;  // [B, Hkv, pairs] (generation << 32) | pieces done
+  int pairs_max;
+  uint32_t gen;
+  uint32_t* status;
+};
+
+// One sequence's work: `pairs` key pairs, the first `full` of which all chunks
+// see; pair p >= full starts at chunk first(p).
+struct SeqWork {
+  int start, rows, keys, pairs, chunks, full, G;
+  int64_t steps;  // per KV head
+  __device__ int first(int p) const {
+    if (p < full) return 0;
+    return min(static_cast<int>((static_cast<int64_t>(p) * kPair - start) * G / kBN), chunks - 1);
+  }
+};
+
+__device__ __forceinline__ SeqWork seq_work(const WeightParams& p, int b, bool report_bad) {
+  SeqWork w = {};
+  w.G = p.G;
+  w.start = p.start_pos[b];
+  int n = p.q_lens != nullptr ? p.q_lens[b] : p.T;
+  n = max(0, min(n, p.T));
+  if (w.start < 0 || n == 0) return w;
+  if (static_cast<int64_t>(w.start) + n > static_cast<int64_t>(p.max_blocks) * kBS) {
+    if (report_bad) report(p.status, kStatusBounds);
+    return w;
+  }
+  w.rows = n * p.G;
+  w.keys = w.start + n;
+  w.pairs = (w.keys + kPair - 1) / kPair;
+  w.chunks = (w.rows + kBN - 1) / kBN;
+  w.full = p.causal ? min(w.pairs, w.start / kPair + 1) : w.pairs;
+  w.steps = static_cast<int64_t>(w.full) * w.chunks;
+  for (int x = w.full; x < w.pairs; ++x) w.steps += w.chunks - w.first(x);
+  return w;
+}
+
+struct Seg {
+  int b, g, pair;
+  int c0, c1;        // chunks [c0, c1)
+  bool whole;
+  int64_t item0, item1;  // the item's steps in the call's order
+  int64_t step0;
+};
+
+struct Cursor {
+  const WeightParams& p;
+  int64_t pos, hi, item0;
+  int b, g, pair, c;  // the next step: chunk c of this item
+  SeqWork w;
+  __device__ Cursor(const WeightParams& prm, const Bars* bars)
+      : p(prm), pos(bars->lo), hi(bars->hi), item0(0), b(bars->b0), g(0), pair(0), c(0) {
+    if (pos >= hi) return;
+    w = seq_work(p, b, false);
+    const int64_t local = pos - bars->bstart;
+    g = static_cast<int>(local / w.steps);
+    const int64_t rem = local - g * w.steps;  // step within the (sequence, KV head)
+    int64_t base;
+    if (rem < static_cast<int64_t>(w.full) * w.chunks) {
+      pair = static_cast<int>(rem / w.chunks);
+      base = static_cast<int64_t>(pair) * w.chunks;
+    } else {
+      pair = w.full;
+      base = static_cast<int64_t>(w.full) * w.chunks;
+      while (rem >= base + w.chunks - w.first(pair)) base += w.chunks - w.first(pair), ++pair;
+    }
+    c = w.first(pair) + static_cast<int>(rem - base);
+    item0 = pos - (rem - base);
+  }
+  __device__ bool next(Seg& s) {
+    if (pos >= hi) return false;
+    if (c == w.chunks) {  // the item is done: the next pair, KV head or sequence
+      item0 = pos;
+      if (++pair == w.pairs) {
+        pair = 0;
+        if (++g == p.Hkv) {
+          g = 0;
+          do w = seq_work(p, ++b, false);
+          while (w.steps == 0);
+        }
+      }
+      c = w.first(pair);
+    }
+    const int f = w.first(pair);
+    s.b = b;
+    s.g = g;
+    s.pair = pair;
+    s.c0 = c;
+    s.c1 = static_cast<int>(min(static_cast<int64_t>(w.chunks), c + (hi - pos)));
+    s.item0 = item0;
+    s.item1 = item0 + w.chunks - f;
+    s.step0 = pos;
+    s.whole = s.c0 == f && s.c1 == w.chunks;
+    pos += s.c1 - s.c0;
+    c = s.c1;
+    return true;
+  }
+};
+
+__device__ __forceinline__ int64_t run_lo(int64_t total, int n, int c) { return total * c / n; }
+__device__ __forceinline__ int run_of(int64_t total, int n, int64_t step) {
+  return static_cast<int>(((step + 1) * n - 1) / total);
+}
+
+__device__ __forceinline__ uint32_t tile_off(int r, int ch) {
+  return static_cast<uint32_t>((ch >> 3) * kBoxBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool there) {
+  const int n = there ? 16 : 0;  // 0: zero fill
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ WeightParams p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBar);
+  float* lse_ring = reinterpret_cast<float*>(smem + C::kOffLse);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort = &bars->abort;
+
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->k_empty[s], 1);
+      mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->s_free[s], 8);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&bars->q_full[s], 1);
+      mbar_init(&bars->q_empty[s], 1);
+    }
+    mbar_init(&bars->piece_full, 8);
+    mbar_init(&bars->piece_go, 1);
+    mbar_init(&bars->drained, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    int64_t total = 0;
+    for (int b = lane; b < p.B; b += 32) total += seq_work(p, b, blockIdx.x == 0).steps * p.Hkv;
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
+    const int n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    const int c = static_cast<int>(blockIdx.x);
+    const int64_t lo = c < n ? run_lo(total, n, c) : 0, hi = c < n ? run_lo(total, n, c + 1) : 0;
+    int64_t run = 0;
+    int b0 = 0;
+    for (int base = 0; base < p.B && lo < hi; base += 32) {
+      const int64_t mine = base + lane < p.B ? seq_work(p, base + lane, false).steps * p.Hkv : 0;
+      int64_t incl = mine;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, incl, m);
+        if (lane >= m) incl += up;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, run + incl > lo);
+      if (past != 0) {
+        const int l = __ffs(past) - 1;
+        b0 = base + l;
+        run += __shfl_sync(0xffffffffu, incl - mine, l);
+        break;
+      }
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      bars->lo = lo, bars->hi = hi, bars->total = total, bars->bstart = run;
+      bars->b0 = b0, bars->n_cta = n;
+      tma_prefetch_desc(&tm_k);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  // scores of tile t, buffer j & 1, at column (2 t + (j & 1)) * 128
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ K pairs
+    // lane i < 16 owns block i of the pair
+    Cursor cur(p, bars);
+    Seg s;
+    int n = 0;
+    while (cur.next(s)) {
+      const int st = n % C::KS;
+      const int blocks = (cur.w.keys + kBS - 1) / kBS - s.pair * (kPair / kBS);
+      int id = lane < min(blocks, kPair / kBS)
+                   ? p.bt[static_cast<int64_t>(s.b) * p.bt_stride + s.pair * (kPair / kBS) + lane]
+                   : -1;
+      if (id != -1 && (id < 0 || id >= p.num_blocks)) {
+        report(p.status, kStatusBounds);
+        id = -1;
+      }
+      const int bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * (kBS * D * 2);
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->k_empty[st], ((n / C::KS) & 1) ^ 1, abort, p.status))) break;
+      if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], bytes);
+      __syncwarp();
+      if (id >= 0)
+#pragma unroll
+        for (int x = 0; x < C::kBoxes; ++x)
+          tma_load_4d(smem + C::kOffK + (st * 2 + (lane >> 3)) * C::kTileBytes + x * kBoxBytes + (lane & 7) * 2048,
+                      &tm_k, &bars->k_full[st], x * 64, 0, s.g, id);
+      ++n;
+    }
+    if (lane == 0 && *abort)
+      for (int x = max(0, n - C::KS); x < n; ++x) drain_wait(&bars->k_full[x % C::KS], (x / C::KS) & 1);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, abort, p.status); };
+      Cursor cur(p, bars);
+      Seg s;
+      int n = 0, j = 0;
+      bool ok = true;
+      while (ok && cur.next(s)) {
+        const int st = n % C::KS;
+        ok = wait(&bars->k_full[st], n / C::KS);
+        for (int c = s.c0; ok && c < s.c1; ++c, ++j) {
+          const int qs = j % C::QS;
+          ok = wait(&bars->q_full[qs], j / C::QS) && wait(&bars->s_free[j & 1], (j >> 1) ^ 1);
+          if (!ok) break;
+          tc_fence_after();
+          const int cols = min(kBN, cur.w.rows - c * kBN);
+          const uint32_t idesc = idesc_bf16_f32(kBM, (cols + 15) / 16 * 16, false, false);
+          const uint32_t qa = smem_u32(smem + C::kOffQ + qs * C::kTileBytes);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const uint32_t ka = smem_u32(smem + C::kOffK + (st * 2 + t) * C::kTileBytes);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
+              umma_bf16_ss(tmem + (2 * t + (j & 1)) * 128, sdesc_sw128(ka + off, 16, 1024),
+                           sdesc_sw128(qa + off, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+            }
+          }
+          umma_commit(&bars->s_full[j & 1]);
+          umma_commit(&bars->q_empty[qs]);
+        }
+        if (ok) umma_commit(&bars->k_empty[st]);
+        ++n;
+      }
+      umma_commit(&bars->drained);
+      drain_wait(&bars->drained, 0);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ query chunks
+    // One chunk ahead: chunk j's copies are waited for after chunk j + 1's are
+    // issued.  A chunk's last LSE use is before the s_free that lets S(j + 2)
+    // run, so a ring of kLseRing >= QS + 3 LSE rows is never overtaken.
+    static_assert(kLseRing >= C::QS + 3, "LSE ring");
+    constexpr int CH = D / 8;
+    const int lt = threadIdx.x - 64;
+    Cursor cur(p, bars);
+    Seg s;
+    int j = 0;
+    bool ok = true;
+    float lse_next[2] = {0.f, 0.f};
+    auto publish = [&](int jj, const float (&l)[2]) {  // chunk jj has landed (this thread's copies are waited for)
+      float* row = lse_ring + (jj % kLseRing) * kBN;
+      bool odd = false;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float v = l[x] == -INFINITY ? INFINITY : l[x] * 1.4426950408889634f;
+        odd |= v == INFINITY;
+        row[lt + x * kLoaders] = v;
+      }
+      fence_proxy_async_smem();
+      odd = named_bar_or(1, kLoaders, odd);
+      if (lt == 0) {
+        bars->odd[jj % kLseRing] = odd;
+        mbar_arrive(&bars->q_full[jj % C::QS]);
+      }
+    };
+    while (ok && cur.next(s)) {
+      for (int c = s.c0; c < s.c1; ++c, ++j) {
+        const int qs = j % C::QS;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty[qs], ((j / C::QS) & 1) ^ 1, abort, p.status));
+        ok = !named_bar_or(2, kLoaders, !ok);
+        if (!ok) break;
+        uint8_t* qt = smem + C::kOffQ + qs * C::kTileBytes;
+        const int r0 = c * kBN;
+        const int n16 = (min(kBN, cur.w.rows - r0) + 15) / 16 * 16;
+        const uint16_t* qb = p.q + s.b * p.q_stride[0] + static_cast<int64_t>(s.g) * p.G * p.q_stride[1];
+        for (int x = lt; x < n16 * CH; x += kLoaders) {
+          const int r = x / CH, ch = x % CH, rr = r0 + r;
+          const bool there = rr < cur.w.rows;
+          const int t = there ? rr / p.G : 0, hh = there ? rr - t * p.G : 0;
+          cp_async16(qt + tile_off(r, ch), qb + hh * p.q_stride[1] + t * p.q_stride[2] + ch * 8, there);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        float l[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int rr = r0 + lt + x * kLoaders;
+          l[x] = -INFINITY;
+          if (rr < cur.w.rows)
+            l[x] = p.lse[(static_cast<int64_t>(s.b) * p.Hq + s.g * p.G + rr % p.G) * p.T + rr / p.G];
+        }
+        if (j > 0) {
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          publish(j - 1, lse_next);
+        }
+        lse_next[0] = l[0], lse_next[1] = l[1];
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (ok && j > 0) publish(j - 1, lse_next);
+  } else {
+    // ------------------------------------------------------------ sums
+    const int t = (warp >> 2) - 1;
+    const int row = (warp & 3) * 32 + lane;
+    const int tid = threadIdx.x - 128;
+    const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    Cursor cur(p, bars);
+    Seg s;
+    int j = 0, pieces = 0;
+    bool ok = true;
+    while (ok && cur.next(s)) {
+      const int key = s.pair * kPair + t * kBM + row;
+      const bool there = key < cur.w.keys;
+      const int blk = there ? p.bt[static_cast<int64_t>(s.b) * p.bt_stride + key / kBS] : -1;
+      // The key's sum belongs to this thread alone, so an add without a return
+      // value has no order to depend on, and no read to wait for.  A token of
+      // the chunk itself starts from nothing.
+      auto put = [&](float got) {
+        if (blk < 0 || blk >= p.num_blocks) return;
+        float* at = p.acc + (static_cast<int64_t>(blk) * p.Hkv + s.g) * kBS + key % kBS;
+        if (key < cur.w.start)
+          asm volatile("red.global.add.f32 [%0], %1;" ::"l"(at), "f"(got) : "memory");
+        else
+          *at = got;
+      };
+      // rows that see the key: r >= rmin
+      const int64_t rmin =
+          p.causal ? max(static_cast<int64_t>(0), static_cast<int64_t>(key - cur.w.start) * p.G) : 0;
+      const int64_t tile_rmin = __shfl_sync(0xffffffffu, rmin, 31);  // the warp's last key is seen by the fewest
+      uint64_t sum[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sum[x] = f2_pack(0.f, 0.f);
+      const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), m1 = f2_pack(-1.f, -1.f);
+      for (int c = s.c0; c < s.c1; ++c, ++j) {
+        const int buf = j & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[buf], (j >> 1) & 1, abort, p.status))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int r0 = c * kBN;
+        const int cols = min(kBN, cur.w.rows - r0);
+        const float* lse2 = lse_ring + (j % kLseRing) * kBN;
+        const bool masked = bars->odd[j % kLseRing] != 0 || tile_rmin > r0;
+        const int rel = static_cast<int>(min(rmin - r0, static_cast<int64_t>(kBN)));  // columns >= rel see the key
+        for (int cc = 0; cc < cols; cc += 32) {
+          uint32_t sr[32];
+          tmem_ld32(tmem + lane_addr + (2 * t + buf) * 128 + cc, sr);
+          tmem_wait_ld(sr);
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(lse2 + cc + i);
+            float x0, x1, x2, x3;
+            const uint64_t a = ffma2(f2_pack(l4.x, l4.y), m1, f2_pack(0.f, 0.f));
+            const uint64_t b = ffma2(f2_pack(l4.z, l4.w), m1, f2_pack(0.f, 0.f));
+            f2_unpack(ffma2(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), sc2, a), x0, x1);
+            f2_unpack(ffma2(f2_pack(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])), sc2, b), x2, x3);
+            float w0 = fast_exp2(x0), w1 = fast_exp2(x1), w2 = fast_exp2(x2), w3 = fast_exp2(x3);
+            if (masked) {
+              // selected, not multiplied: whatever a column without weight holds stays out
+              w0 = (cc + i >= rel && l4.x != INFINITY) ? w0 : 0.f;
+              w1 = (cc + i + 1 >= rel && l4.y != INFINITY) ? w1 : 0.f;
+              w2 = (cc + i + 2 >= rel && l4.z != INFINITY) ? w2 : 0.f;
+              w3 = (cc + i + 3 >= rel && l4.w != INFINITY) ? w3 : 0.f;
+            }
+            sum[(i >> 1) & 3] = fadd2(sum[(i >> 1) & 3], f2_pack(w0, w1));
+            sum[((i >> 1) + 1) & 3] = fadd2(sum[((i >> 1) + 1) & 3], f2_pack(w2, w3));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->s_free[buf]);
+      }
+      if (!ok) break;
+      float a0, a1;
+      f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
+      const float got = a0 + a1;
+      if (s.whole) {
+        put(got);
+        continue;
+      }
+      // a cut item: leave the piece; the last one adds them in order
+      const int slot = 2 * static_cast<int>(blockIdx.x) + (s.step0 == bars->lo ? 0 : 1);
+      p.part[static_cast<int64_t>(slot) * kPair + tid] = got;
+      const int p0 = run_of(bars->total, bars->n_cta, s.item0);
+      const int np = run_of(bars->total, bars->n_cta, s.item1 - 1) - p0 + 1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->piece_full);
+      if (tid < 32 && !__all_sync(0xffffffffu, mbar_wait(&bars->piece_full, pieces & 1, abort, p.status))) {
+        ok = false;
+        break;
+      }
+      if (tid == 0) {
+        __threadfence();
+        // the count returns to zero with the last piece; a word of another
+        // generation (another call, or anything else) reads as zero
+        unsigned long long* w =
+            p.count + (static_cast<int64_t>(s.b) * p.Hkv + s.g) * p.pairs_max + s.pair;
+        const unsigned long long tag = static_cast<unsigned long long>(p.gen) << 32;
+        unsigned long long before = *reinterpret_cast<volatile unsigned long long*>(w), now;
+        for (;;) {
+          now = (before >> 32) == p.gen ? before + 1 : tag + 1;
+          const unsigned long long seen = atomicCAS(w, before, now);
+          if (seen == before) break;
+          before = seen;
+        }
+        const bool last = (now & 0xffffffffull) == static_cast<unsigned long long>(np);
+        if (last) *w = tag;
+        bars->last = last;
+        mbar_arrive(&bars->piece_go);
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->piece_go, pieces & 1, abort, p.status))) {
+        ok = false;
+        break;
+      }
+      ++pieces;
+      if (bars->last) {
+        __threadfence();
+        const bool head = run_lo(bars->total, bars->n_cta, p0) == s.item0;
+        float all = 0.f;
+        for (int x = 0; x < np; ++x) {
+          const int sl = 2 * (p0 + x) + ((x == 0 && !head) ? 1 : 0);
+          all += __ldcg(p.part + static_cast<int64_t>(sl) * kPair + tid);
+        }
+        put(all);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch(const WeightArgs& a, const WeightParams& p, cudaStream_t stream) {
+  CUtensorMap mk;
+  if (!make_paged_map(&mk, a.cache.k, a.cache.num_blocks, a.cache.Hkv, D)) return cudaErrorInvalidValue;
+  auto kern = attn_weights_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(a.n_cta), kThreads, Cfg<D>::kSmemBytes, stream>>>(mk, p);
+  return cudaGetLastError();
+}
+
+size_t part_bytes(int n_cta) { return static_cast<size_t>(2) * n_cta * kPair * sizeof(float); }
+int pairs_of(int max_blocks) {
+  return static_cast<int>((static_cast<int64_t>(max_blocks) * kBS + kPair - 1) / kPair);
+}
+
+}  // namespace
+
+// Partial sums of two cut items per CTA, then one 8-byte count per item.
+size_t weights_partial_bytes(int64_t B, int64_t Hkv, int max_blocks, int n_cta) {
+  const size_t counts = static_cast<size_t>(B) * Hkv * pairs_of(max_blocks) * sizeof(unsigned long long);
+  return ((part_bytes(n_cta) + 255) & ~size_t(255)) + ((counts + 255) & ~size_t(255));
+}
+
+cudaError_t launch_attn_weights(const WeightArgs& a, cudaStream_t stream) {
+  WeightParams p = {};
+  p.B = static_cast<int>(a.B);
+  p.T = static_cast<int>(a.T);
+  p.Hq = static_cast<int>(a.Hq);
+  p.Hkv = a.cache.Hkv;
+  p.G = p.Hq / p.Hkv;
+  p.causal = a.causal;
+  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  p.q = static_cast<const uint16_t*>(a.q.data);
+  for (int i = 0; i < 3; ++i) p.q_stride[i] = a.q.stride[i];
+  p.lse = a.lse;
+  p.num_blocks = static_cast<int>(a.cache.num_blocks);
+  p.bt = a.block_table;
+  p.bt_stride = a.bt_stride;
+  p.max_blocks = a.max_blocks;
+  p.start_pos = a.start_pos;
+  p.q_lens = a.q_lens;
+  p.acc = a.acc;
+  p.part = static_cast<float*>(a.partials);
+  p.count = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(a.partials) +
+                                                  ((part_bytes(a.n_cta) + 255) & ~size_t(255)));
+  p.pairs_max = pairs_of(a.max_blocks);
+  p.gen = a.gen;
+  p.status = a.status;
+  if (a.cache.D == 64) return launch<64>(a, p, stream);
+  if (a.cache.D == 128) return launch<128>(a, p, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace attn
