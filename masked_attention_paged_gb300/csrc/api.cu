@@ -678,8 +678,8 @@ size_t paged_tree_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num
   if (batch < 0 || num_q_heads < 0 || num_kv_heads <= 0 || num_drafts < 0 || max_blocks < 0 || block_size <= 0 ||
       head_dim <= 0 || num_q_heads % num_kv_heads != 0)
     return 0;
-  const int64_t rows = static_cast<int64_t>(num_drafts) * (num_q_heads / num_kv_heads);
-  return kStatusBytes + tree_partial_bytes(batch, num_kv_heads, rows, head_dim, device_sm_count());
+  return kStatusBytes + tree_partial_bytes(batch, num_kv_heads, num_drafts, num_q_heads / num_kv_heads, head_dim,
+                                           device_sm_count());
 }
 
 attn_status paged_tree_attn(const attn_tensor* q, const attn_tensor* k_new, const attn_tensor* v_new,
@@ -708,7 +708,9 @@ attn_status paged_tree_attn(const attn_tensor* q, const attn_tensor* k_new, cons
     for (int i = 0; i < 4; ++i)
       if (k_new->shape[i] != want[i] || v_new->shape[i] != want[i]) return ATTN_ERR_INVALID_ARG;
   }
-  if (T > kTreeMaxDrafts || B > 65535 || Hq > 65535 || cache->num_blocks > 0x7fffffff) return ATTN_ERR_UNSUPPORTED;
+  if (T > kTreeMaxDrafts || B > 65535 || Hq > 65535 || Hq / cache->num_kv_heads > 128 ||
+      cache->num_blocks > 0x7fffffff)
+    return ATTN_ERR_UNSUPPORTED;
   const size_t need = paged_tree_workspace_size(static_cast<int32_t>(B), static_cast<int32_t>(Hq),
                                                 cache->num_kv_heads, static_cast<int32_t>(T), max_blocks,
                                                 cache->block_size, cache->head_dim);
@@ -790,8 +792,7 @@ attn_status paged_attn_weights(const attn_tensor* q, const float* lse, const att
   if (Hq <= 0 || Hq % cache->num_kv_heads != 0) return ATTN_ERR_INVALID_ARG;
   if (!isfinite(scale) || (causal != 0 && causal != 1)) return ATTN_ERR_INVALID_ARG;
   if (max_blocks <= 0 || max_blocks > (1 << 24)) return ATTN_ERR_INVALID_ARG;
-  if (B > 65535 || Hq > 65535 || T > (1 << 24) || T * (Hq / cache->num_kv_heads) > (int64_t(1) << 30) ||
-      cache->num_blocks > 0x7fffffff)
+  if (B > 65535 || Hq > 65535 || Hq / cache->num_kv_heads > 128 || T > (1 << 24) || cache->num_blocks > 0x7fffffff)
     return ATTN_ERR_UNSUPPORTED;
   const size_t need = paged_attn_weights_workspace_size(static_cast<int32_t>(B), cache->num_kv_heads, max_blocks,
                                                         cache->block_size);

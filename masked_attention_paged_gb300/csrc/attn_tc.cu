@@ -1107,6 +1107,26 @@ bool make_paged_map(CUtensorMap* map, void* base, int64_t num_blocks, int Hkv, i
   return make_cache_map(map, base, num_blocks, Hkv, D);
 }
 
+bool make_rows_map(CUtensorMap* map, const View4& t, int64_t Hkv, int tokens) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  const int64_t G = t.shape[1] / Hkv;
+  const int64_t size[4] = {G, t.shape[2], Hkv, t.shape[0]};
+  const int64_t stride[4] = {t.stride[1], t.stride[2], G * t.stride[1], t.stride[0]};
+  cuuint64_t dims[5] = {static_cast<cuuint64_t>(t.shape[3])};
+  cuuint64_t strides[4];
+  for (int i = 0; i < 4; ++i) {
+    dims[i + 1] = static_cast<cuuint64_t>(size[i]);
+    strides[i] = size[i] > 1 ? static_cast<cuuint64_t>(stride[i]) * 2 : cuuint64_t(1) << 30;  // extent 1: any
+  }
+  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tokens), 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, t.data, dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool make_code_cache_map(CUtensorMap* map, void* base, int64_t num_blocks, int Hkv) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return false;

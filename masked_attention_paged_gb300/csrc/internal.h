@@ -171,6 +171,11 @@ cudaError_t launch_paged_prefill_tc(const PrefillArgs& a, cudaStream_t stream);
 // the same for head dim 64 or 128
 bool make_paged_map(CUtensorMap* map, void* base, int64_t num_blocks, int Hkv, int D);
 
+// 5-D bf16 tensor map over a [B, H, T, D] view as (dim, head of the group, token,
+// KV head, batch): box 64 columns x the G = H / Hkv heads of `tokens` tokens, 128-byte
+// swizzle, so row r of a box is token r / G, head r % G; zero fill past T
+bool make_rows_map(CUtensorMap* map, const View4& t, int64_t Hkv, int tokens);
+
 constexpr int kTreeMaxDrafts = 256;  // drafts per sequence of the tree attention
 struct TreeArgs {
   PagedCache cache;
@@ -190,8 +195,8 @@ struct TreeArgs {
   uint32_t gen;    // this call's generation, tags the piece counts (never 0)
   uint32_t* status;
 };
-// workspace past the status block for R = T * Hq / Hkv rows per KV head
-size_t tree_partial_bytes(int64_t B, int64_t Hkv, int64_t R, int D, int n_cta);
+// workspace past the status block, G = Hq / Hkv
+size_t tree_partial_bytes(int64_t B, int64_t Hkv, int64_t T, int64_t G, int D, int n_cta);
 cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream);
 
 struct AcceptArgs {

@@ -6,11 +6,12 @@
 //   s_j = scale q.k_j,  out = sum_j softmax(s)_j v_j,  lse = log sum_j e^{s_j}.
 //
 // Few query rows read a long cache, so K and V are read once for all T drafts
-// and all G query heads of a KV head: row r of a (sequence, KV head) is draft
-// r / G, head r % G, and NT tiles of 128 rows share every K/V tile (NT = 1 for
-// up to 128 rows, else 2).  What bounds it is HBM (a 128-key tile of K and V at
-// D = 128 is 64 KB, 1.4 us of an SM's share, against 0.6 us of softmax), until
-// rows pass 256 a KV head and the tensor cores and exponentials do.
+// and all G query heads of a KV head.  A row tile is the G heads of tb = min(T,
+// 128 / G) drafts (row r: draft r / G, head r % G), one 5-D TMA box of q whatever
+// its strides; NT row tiles share every K/V tile (NT = 1 if one holds all drafts,
+// else 2).  What bounds it is HBM (a 128-key tile of K and V at D = 128 is 64 KB,
+// 1.4 us of an SM's share, against 0.6 us of softmax), until rows pass 256 a KV
+// head and the tensor cores and exponentials do.
 //
 // Every SM takes an equal run of the call's K/V tiles: an item (sequence, KV
 // head, row pair) is its draft tiles followed by its context tiles, the items
@@ -19,12 +20,14 @@
 // (normalised rows and log2 LSE; at most two per CTA), merged in order by
 // whichever piece finishes last, so results do not depend on the timing.
 //
-// Warps: 0 streams context tiles (TMA through the block table), 1 issues the
-// MMAs, 2-3 load the draft tiles from k_new / v_new (or the cache), append them
-// and build the ancestor masks, 4.. one warpgroup of softmax per row tile
-// (thread r owns row r: TMEM lane r).  With NT = 1 two score buffers let the
-// next S run under the current softmax.  P goes over its S as bf16 (relative
-// rounding 2^-9; row sums are taken in fp32 before it).
+// Warps: 0 streams all tiles (TMA: context tiles through the block table, draft
+// tiles from k_new / v_new, or from the cache's blocks when they are there
+// already, shifted by the context's last partial block), 1 issues the MMAs, 2-3
+// build the ancestor masks, clean the drafts' V and append K and V from shared
+// memory, 4.. one warpgroup of softmax per row tile (thread r owns row r: TMEM
+// lane r).  With NT = 1 two score buffers let the next S run under the current
+// softmax.  P goes over its S as bf16 (relative rounding 2^-9; row sums are taken
+// in fp32 before it).
 //
 // V rows past the context's end and rows of absent drafts are zeroed: P is 0
 // there, but 0 x NaN is not.  A draft's own V may hold infinities or NaN that
@@ -32,6 +35,8 @@
 // epilogue adds p x v for the rows that do attend to them.
 #include <cuda.h>
 #include <math.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 #include "internal.h"
@@ -62,8 +67,8 @@ struct Cfg {
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + NT * kTileBytes;
   static constexpr int kOffV = kOffK + KS * kTileBytes;
-  static constexpr int kOffAnc = kOffV + VS * kTileBytes;  // [kMaxT][kWords] ancestor bits
-  static constexpr int kOffPar = kOffAnc + kMaxT * kWords * 4;  // [kMaxT] parents
+  static constexpr int kOffAnc = kOffV + VS * kTileBytes;  // [2][kMaxT][kWords] ancestor bits
+  static constexpr int kOffPar = kOffAnc + 2 * kMaxT * kWords * 4;  // [kMaxT] parents
   static constexpr int kOffBar = kOffPar + kMaxT * 4;
   static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
@@ -77,14 +82,14 @@ struct Bars {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2], p_full[2];  // [row tile] (NT = 2) or [score buffer] (NT = 1)
   uint64_t o_done[2];  // [row tile] (NT = 2) or, alternating, [tile parity] (NT = 1)
-  uint64_t draft_go[4];  // the producer hands K stage (and the tile's V stage) to the draft loader
-  uint64_t mask_full, mask_empty;
+  uint64_t draft_in[4];  // a draft tile's K and V have landed in K stage ks (and the tile's V stage)
+  uint64_t mask_full[2], mask_empty[2];
   uint64_t piece_full, piece_go;  // an item's piece is written; whether it was the last
   uint64_t drained;
   int64_t lo, hi, total, bstart;  // this CTA's run of tiles; the first item's sequence starts at bstart
   int b0;
   int n_cta;
-  uint32_t bad[8];  // drafts whose V holds a non-finite element
+  uint32_t bad[2][8];  // drafts whose V holds a non-finite element
   uint32_t tmem_base;
   int abort;
   int last;
@@ -92,13 +97,16 @@ struct Bars {
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block outgrew its shared-memory slot");
 
 struct TreeParams {
-  int B, T, Hq, Hkv, G, R;  // R = T * G rows per KV head
-  int MP;                   // row pairs per KV head
+  int B, T, Hq, Hkv, G;
+  int tb, RT;  // drafts and rows (tb * G) of a row tile
+  int MP;      // groups of NT row tiles per KV head
+  int ntd;     // draft tiles
+  int new_box; // rows of a k_new / v_new box: T up to a multiple of 16, or 128
   float scale_log2;
   int scale_positive;
   const uint16_t* q;
   int64_t q_stride[3];
-  const uint16_t* k_new;
+  const uint16_t* k_new;  // null: the drafts are in the cache
   const uint16_t* v_new;
   int64_t kn_stride[3], vn_stride[3];
   uint16_t* kc;
@@ -128,10 +136,17 @@ __device__ __forceinline__ int seq_ctx(const TreeParams& p, int b, bool& ok) {
   ok = c >= 0 && static_cast<int64_t>(c) + p.T <= static_cast<int64_t>(p.max_blocks) * kBS;
   return ok ? c : 0;
 }
-__device__ __forceinline__ int draft_tiles(const TreeParams& p) { return (p.T + kBN - 1) / kBN; }
 __device__ __forceinline__ int seq_tiles(const TreeParams& p, int b, int& ctx, bool& ok) {
   ctx = seq_ctx(p, b, ok);
-  return draft_tiles(p) + (ctx + kBN - 1) / kBN;
+  return p.ntd + (ctx + kBN - 1) / kBN;
+}
+
+// The drafts' first key in their tiles: a block's start when they come from the cache.
+__device__ __forceinline__ int draft_off(const TreeParams& p, int ctx) { return p.k_new != nullptr ? 0 : ctx % kBS; }
+// Keys of a tile that its MMAs cover: a multiple of 16, at least 16.
+__device__ __forceinline__ int tile_keys(const TreeParams& p, int tile, int ctx) {
+  const int left = tile < p.ntd ? p.T + draft_off(p, ctx) - tile * kBN : ctx - (tile - p.ntd) * kBN;
+  return min(kBN, max(16, (left + 15) / 16 * 16));
 }
 
 // A run of one item's tiles [t0, t1) of `tiles`.
@@ -215,7 +230,7 @@ __device__ __forceinline__ int run_of(int64_t total, int n, int64_t tile) {
 // Merge an item's pieces (CTAs c0 .. c0 + np - 1): out = sum_c 2^(lse_c - M)
 // out_c / sum_c 2^(lse_c - M), four dims a thread and step.
 template <int D>
-__device__ __forceinline__ void merge_item(const TreeParams& p, const Seg& s, int row0, int rows, int c0, int np,
+__device__ __forceinline__ void merge_item(const TreeParams& p, const Seg& s, int node0, int rows, int c0, int np,
                                            bool first_is_head, int tid, int nthr) {
   constexpr int V4 = D / 4;
   for (int x = tid; x < rows * V4; x += nthr) {
@@ -247,7 +262,7 @@ __device__ __forceinline__ void merge_item(const TreeParams& p, const Seg& s, in
       }
     }
     const float inv = empty ? 0.f : 1.f / ws;
-    const int rr = row0 + r, t = rr / p.G, h = s.g * p.G + rr % p.G;
+    const int t = node0 + r / p.G, h = s.g * p.G + r % p.G;
     const int64_t ob = s.b * p.out_stride[0] + h * p.out_stride[1] + t * p.out_stride[2] + d;
     if (p.out_bf16)
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ob) =
@@ -262,8 +277,9 @@ __device__ __forceinline__ void merge_item(const TreeParams& p, const Seg& s, in
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
-    paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                         const __grid_constant__ TreeParams p) {
+    paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kn,
+                         const __grid_constant__ CUtensorMap tm_vn, const __grid_constant__ TreeParams p) {
   using C = Cfg<D, NT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -271,12 +287,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   uint32_t* anc = reinterpret_cast<uint32_t*>(smem + C::kOffAnc);
   int32_t* par = reinterpret_cast<int32_t*>(smem + C::kOffPar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ntd = draft_tiles(p);
+  const int ntd = p.ntd;
   volatile int* abort = &bars->abort;
 
   if (threadIdx.x == 32) {
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bars->q_full[t], 4);
+      mbar_init(&bars->q_full[t], 1);
       mbar_init(&bars->s_full[t], 1);
       mbar_init(&bars->p_full[t], 4);
       mbar_init(&bars->o_done[t], 1);
@@ -287,12 +303,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       mbar_init(&bars->v_full[s], 1);
       mbar_init(&bars->v_empty[s], 1);
     }
-    for (int s = 0; s < 4; ++s) mbar_init(&bars->draft_go[s], 1);
+    for (int s = 0; s < 4; ++s) mbar_init(&bars->draft_in[s], 1);
     mbar_init(&bars->piece_full, 4 * NT);
     mbar_init(&bars->piece_go, 1);
     mbar_init(&bars->drained, 1);
-    mbar_init(&bars->mask_full, 1);
-    mbar_init(&bars->mask_empty, 4 * NT);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->mask_full[s], 1);
+      mbar_init(&bars->mask_empty[s], 4 * NT);
+    }
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -350,6 +368,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
   }
+  // query rows past a row tile's box: zeros, once
+  for (int x = threadIdx.x; x < NT * C::kBoxes * (kBM - p.RT) * 8; x += C::kThreads) {
+    const int box = x / ((kBM - p.RT) * 8), y = x % ((kBM - p.RT) * 8);
+    *reinterpret_cast<uint4*>(smem + C::kOffQ + box * kBoxBytes + p.RT * 128 + y * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -359,79 +383,100 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     if (warp < 4) regs_dec<C::kRegsCtl>();
   }
   if (warp == 0) {
-    // ------------------------------------------------------------ context tiles
-    // lane i < 8 owns block i of the tile: its 64-column boxes of K and of V
+    // ------------------------------------------------------------ K/V tiles
+    // lane i < 8 owns block i of a context tile: its 64-column boxes of K and of
+    // V.  A draft tile's data go to the drafts' warps first (draft_in), which
+    // hand the stages on.
     Cursor cur(p, bars);
     Seg s;
-    int j = 0, k_issued = 0, v_issued = 0;
+    int j = 0, issued = 0;
     bool ok = true;
     while (ok && cur.next(s)) {
       const int32_t* bt_row = p.bt + static_cast<int64_t>(s.b) * p.bt_stride;
+      const int off = draft_off(p, s.ctx);
       auto block_id = [&](int tile) {
-        const int kt = tile - ntd;
-        if (kt < 0 || tile >= s.t1) return -1;
-        const int nb = min(kBN / kBS, (s.ctx - kt * kBN + kBS - 1) / kBS);
-        return lane < nb ? bt_row[kt * (kBN / kBS) + lane] : -1;
-      };
-      int id_next = block_id(max(s.t0, ntd));
-      for (int tile = s.t0; tile < s.t1; ++tile, ++j) {
-        const int ks = j % C::KS, vs = j % C::VS;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->k_empty[ks], ((j / C::KS) & 1) ^ 1, abort, p.status))) {
-          ok = false;
-          break;
-        }
+        if (tile >= s.t1) return -1;
+        int first, blocks;  // the tile's blocks
         if (tile < ntd) {
-          // the draft loader fills these stages; every ring wait stays here, so
-          // that no waiter ever skips or lags a phase
-          if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_empty[vs], ((j / C::VS) & 1) ^ 1, abort, p.status))) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive(&bars->draft_go[ks]);
-          continue;
+          if (p.k_new != nullptr || !s.ok) return -1;
+          first = s.ctx / kBS + tile * (kBN / kBS);
+          blocks = (p.T + off + kBS - 1) / kBS - tile * (kBN / kBS);
+        } else {
+          first = (tile - ntd) * (kBN / kBS);
+          blocks = (s.ctx + kBS - 1) / kBS - first;
         }
+        return lane < min(kBN / kBS, blocks) ? bt_row[first + lane] : -1;
+      };
+      int id_next = block_id(s.t0);
+      for (int tile = s.t0; tile < s.t1; ++tile, ++j) {
         int id = id_next;
         id_next = block_id(tile + 1);
         if (id != -1 && (id < 0 || id >= p.num_blocks)) {
           report(p.status, kStatusBounds);
           id = -1;
         }
-        const int bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * (kBS * D * 2);
-        if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[ks], bytes);
-        __syncwarp();
-        if (id >= 0)
-#pragma unroll
-          for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_4d(smem + C::kOffK + ks * C::kTileBytes + x * kBoxBytes + lane * 2048, &tm_k, &bars->k_full[ks],
-                        x * 64, 0, s.g, id);
-        k_issued = j + 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_empty[vs], ((j / C::VS) & 1) ^ 1, abort, p.status))) {
+        const int ks = j % C::KS, vs = j % C::VS;
+        uint8_t* kt = smem + C::kOffK + ks * C::kTileBytes;
+        uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * (kBS * D * 2);
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->k_empty[ks], ((j / C::KS) & 1) ^ 1, abort, p.status))) {
           ok = false;
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(&bars->v_full[vs], bytes);
+        const bool draft = tile < ntd;
+        const bool fresh = draft && p.k_new != nullptr;  // one box of k_new and one of v_new per 64 columns
+        if (draft && !__all_sync(0xffffffffu,
+                                 mbar_wait(&bars->v_empty[vs], ((j / C::VS) & 1) ^ 1, abort, p.status))) {
+          ok = false;
+          break;
+        }
+        uint64_t* k_bar = draft ? &bars->draft_in[ks] : &bars->k_full[ks];
+        uint64_t* v_bar = draft ? &bars->draft_in[ks] : &bars->v_full[vs];
+        if (lane == 0)
+          mbar_arrive_expect_tx(k_bar, fresh ? 2u * static_cast<uint32_t>(p.new_box) * D * 2 : (draft ? 2u : 1u) * bytes);
         __syncwarp();
+        if (fresh && lane == 0) {
+#pragma unroll
+          for (int x = 0; x < C::kBoxes; ++x) {
+            tma_load_5d(kt + x * kBoxBytes, &tm_kn, k_bar, x * 64, 0, tile * kBN, s.g, s.b);
+            tma_load_5d(vt + x * kBoxBytes, &tm_vn, k_bar, x * 64, 0, tile * kBN, s.g, s.b);
+          }
+        }
         if (id >= 0)
 #pragma unroll
           for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_4d(smem + C::kOffV + vs * C::kTileBytes + x * kBoxBytes + lane * 2048, &tm_v, &bars->v_full[vs],
-                        x * 64, 0, s.g, id);
-        v_issued = j + 1;
+            tma_load_4d(kt + x * kBoxBytes + lane * 2048, &tm_k, k_bar, x * 64, 0, s.g, id);
+        if (!draft) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_empty[vs], ((j / C::VS) & 1) ^ 1, abort, p.status))) {
+            // this tile's K is in flight: let it land
+            if (lane == 0) drain_wait(k_bar, (j / C::KS) & 1);
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(v_bar, bytes);
+          __syncwarp();
+        }
+        if (id >= 0)
+#pragma unroll
+          for (int x = 0; x < C::kBoxes; ++x)
+            tma_load_4d(vt + x * kBoxBytes + lane * 2048, &tm_v, v_bar, x * 64, 0, s.g, id);
+        issued = j + 1;
       }
     }
     if (lane == 0 && *abort) {
-      // let every copy in flight land before the CTA exits (a draft tile's stage
-      // holds no copy: the wait on it runs out or passes)
-      for (int x = max(0, k_issued - C::KS); x < k_issued; ++x) drain_wait(&bars->k_full[x % C::KS], (x / C::KS) & 1);
-      for (int x = max(0, v_issued - C::VS); x < v_issued; ++x) drain_wait(&bars->v_full[x % C::VS], (x / C::VS) & 1);
+      // let every copy in flight land before the CTA exits: those of the last
+      // tiles, and of a draft tile that nobody took over (a wait on a barrier
+      // without copies runs out or passes)
+      for (int x = max(0, issued - C::KS); x < issued; ++x) drain_wait(&bars->k_full[x % C::KS], (x / C::KS) & 1);
+      for (int x = max(0, issued - C::VS); x < issued; ++x) drain_wait(&bars->v_full[x % C::VS], (x / C::VS) & 1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBN, false, false);
       constexpr uint32_t idesc_o = idesc_bf16_f32(kBM, D, false, true);
       auto s_col = [&](int t, int j) { return NT == 1 ? static_cast<uint32_t>((j & 1) * 128) : t * 128u; };
-      auto issue_s = [&](int t, int j) {  // S = Q_t K_j^T
+      auto issue_s = [&](int t, int j, int keys) {  // S = Q_t K_j^T
+        const uint32_t idesc_s = idesc_bf16_f32(kBM, keys, false, false);
         const uint32_t qa = smem_u32(smem + C::kOffQ) + t * C::kTileBytes;
         const uint32_t ka = smem_u32(smem + C::kOffK + (j % C::KS) * C::kTileBytes);
 #pragma unroll
@@ -442,12 +487,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         umma_commit(&bars->s_full[NT == 1 ? (j & 1) : t]);
       };
-      auto issue_pv = [&](int t, int j, bool first) {  // O_t (+)= P V_j
+      auto issue_pv = [&](int t, int j, int keys, bool first) {  // O_t (+)= P V_j
         const uint32_t va = smem_u32(smem + C::kOffV + (j % C::VS) * C::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
-          umma_bf16_ts(tmem + C::kColO + t * D, tmem + s_col(t, j) + kk * 8,
-                       sdesc_sw128(va + kk * 2048, kBoxBytes, 1024), idesc_o, (!first || kk > 0) ? 1u : 0u);
+          if (kk * 16 < keys)
+            umma_bf16_ts(tmem + C::kColO + t * D, tmem + s_col(t, j) + kk * 8,
+                         sdesc_sw128(va + kk * 2048, kBoxBytes, 1024), idesc_o, (!first || kk > 0) ? 1u : 0u);
         umma_commit(&bars->o_done[NT == 1 ? (j & 1) : t]);
       };
       auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, abort, p.status); };
@@ -459,6 +505,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       bool ok = true;
       for (; ok && cur.next(s); ++seg) {
         const int n = s.t1 - s.t0;
+        auto keys = [&](int x) { return tile_keys(p, s.t0 + x, s.ctx); };
         for (int t = 0; t < NT; ++t) ok = ok && wait(&bars->q_full[t], seg);
         if constexpr (NT == 1) {
           // S runs two tiles ahead of PV
@@ -466,20 +513,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             ok = wait_k(j + x);
             if (!ok) break;
             tc_fence_after();
-            issue_s(0, j + x);
+            issue_s(0, j + x, keys(x));
             umma_commit(&bars->k_empty[(j + x) % C::KS]);
           }
           for (int x = 0; ok && x < n; ++x, ++j) {
             ok = wait(&bars->p_full[j & 1], j >> 1) && wait_v(j);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(0, j, x == 0);
+            issue_pv(0, j, keys(x), x == 0);
             umma_commit(&bars->v_empty[j % C::VS]);
             if (x + 2 < n) {
               ok = wait_k(j + 2);
               if (!ok) break;
               tc_fence_after();
-              issue_s(0, j + 2);
+              issue_s(0, j + 2, keys(x + 2));
               umma_commit(&bars->k_empty[(j + 2) % C::KS]);
             }
           }
@@ -488,28 +535,28 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           ok = ok && wait_k(j);
           if (ok) {
             tc_fence_after();
-            issue_s(0, j);
-            issue_s(1, j);
+            issue_s(0, j, keys(0));
+            issue_s(1, j, keys(0));
             umma_commit(&bars->k_empty[j % C::KS]);
           }
           for (int x = 0; ok && x < n; ++x, ++j) {
             ok = wait(&bars->p_full[0], j) && wait_v(j);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(0, j, x == 0);
+            issue_pv(0, j, keys(x), x == 0);
             if (x + 1 < n) {
               ok = wait_k(j + 1);
               if (!ok) break;
               tc_fence_after();
-              issue_s(0, j + 1);
+              issue_s(0, j + 1, keys(x + 1));
             }
             ok = wait(&bars->p_full[1], j);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(1, j, x == 0);
+            issue_pv(1, j, keys(x), x == 0);
             umma_commit(&bars->v_empty[j % C::VS]);
             if (x + 1 < n) {
-              issue_s(1, j + 1);
+              issue_s(1, j + 1, keys(x + 1));
               umma_commit(&bars->k_empty[(j + 1) % C::KS]);
             }
           }
@@ -520,23 +567,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       drain_wait(&bars->drained, 0);
     }
   } else if (warp < 4) {
-    // ------------------------------------------------------------ draft tiles
+    // ------------------------------------------------------------ drafts
     constexpr int CH = D / 8;  // 16-byte chunks per row
     constexpr int NL = 64;
     const int lt = threadIdx.x - 64;
     Cursor cur(p, bars);
     Seg s;
     int j0 = 0, round = 0;
-    uint32_t go = 0u;  // bit ks: parity of the next hand-over of K stage ks
+    uint32_t in = 0u;  // bit ks: parity of the next draft tile in K stage ks
     bool ok = true;
     while (ok && cur.next(s)) {
       if (s.t0 < ntd) {
-        // the masks of the segment before may still be in use
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->mask_empty, (round & 1) ^ 1, abort, p.status));
+        const int mb = round & 1;
+        uint32_t* am = anc + mb * C::kMaxT * C::kWords;
+        // the masks of two segments before may still be in use
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->mask_empty[mb], ((round >> 1) & 1) ^ 1, abort, p.status));
         ok = !named_bar_or(1, NL, !ok);
         if (!ok) break;
         for (int t = lt; t < p.T; t += NL) par[t] = s.ok ? p.parents[s.b * p.par_stride + t] : -2;
-        if (lt < 8) bars->bad[lt] = 0u;
+        if (lt < 8) bars->bad[mb][lt] = 0u;
         named_bar_sync(1, NL);
         // node t's ancestors, itself included: parents come before children, so
         // a walk up ends within t steps; absent (no bits) unless it ends at -1
@@ -560,43 +609,46 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             a = up;
           }
 #pragma unroll
-          for (int x = 0; x < C::kWords; ++x) anc[t * C::kWords + x] = there ? w[x] : 0u;
+          for (int x = 0; x < C::kWords; ++x) am[t * C::kWords + x] = there ? w[x] : 0u;
         }
         named_bar_sync(1, NL);
+        const int off = draft_off(p, s.ctx);
         for (int tile = s.t0; ok && tile < min(s.t1, ntd); ++tile) {
           const int j = j0 + tile - s.t0;
           const int ks = j % C::KS, vs = j % C::VS;
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->draft_go[ks], (go >> ks) & 1u, abort, p.status));
-          go ^= 1u << ks;
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->draft_in[ks], (in >> ks) & 1u, abort, p.status));
+          in ^= 1u << ks;
           ok = !named_bar_or(1, NL, !ok);
           if (!ok) break;
-          uint8_t* kt = smem + C::kOffK + ks * C::kTileBytes;
+          const uint8_t* kt = smem + C::kOffK + ks * C::kTileBytes;
           uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
-          const int n = min(kBN, p.T - tile * kBN);
-#pragma unroll 4
-          for (int x = lt; x < kBN * CH; x += NL) {
-            const int r = x / CH, ch = x % CH, node = tile * kBN + r;
-            uint4 kw = make_uint4(0u, 0u, 0u, 0u), vw = kw;
+          const int rows = tile_keys(p, tile, s.ctx);
+          const bool append = p.k_new != nullptr && s.m == 0;
+#pragma unroll 2
+          for (int x = lt; x < rows * CH; x += NL) {
+            const int r = x / CH, ch = x % CH, node = tile * kBN + r - off;
+            uint4* vp = reinterpret_cast<uint4*>(vt + tile_off(r, ch));
             // present: its own bit is set
-            if (r < n && ((anc[node * C::kWords + (node >> 5)] >> (node & 31)) & 1u)) {
-              const uint16_t* kr = draft_row<D>(p, false, s.b, s.g, node, s.ctx);
-              const uint16_t* vr = draft_row<D>(p, true, s.b, s.g, node, s.ctx);
-              if (kr != nullptr) kw = *reinterpret_cast<const uint4*>(kr + ch * 8);
-              if (vr != nullptr) vw = *reinterpret_cast<const uint4*>(vr + ch * 8);
-              if (p.k_new != nullptr && s.m == 0) {
-                const int64_t row = cache_row(p, s.b, s.g, s.ctx + node);
-                if (row >= 0) {
-                  *reinterpret_cast<uint4*>(p.kc + row * D + ch * 8) = kw;
-                  *reinterpret_cast<uint4*>(p.vc + row * D + ch * 8) = vw;
-                }
-              }
-              bool bad = false;
-              vw.x = finite_pair(vw.x, bad), vw.y = finite_pair(vw.y, bad);
-              vw.z = finite_pair(vw.z, bad), vw.w = finite_pair(vw.w, bad);
-              if (bad) atomicOr(&bars->bad[node >> 5], 1u << (node & 31));
+            if (node < 0 || node >= p.T || !((am[node * C::kWords + (node >> 5)] >> (node & 31)) & 1u)) {
+              *vp = make_uint4(0u, 0u, 0u, 0u);
+              continue;
             }
-            *reinterpret_cast<uint4*>(kt + tile_off(r, ch)) = kw;
-            *reinterpret_cast<uint4*>(vt + tile_off(r, ch)) = vw;
+            uint4 vw = *vp;
+            if (append) {
+              const int64_t row = cache_row(p, s.b, s.g, s.ctx + node);
+              if (row >= 0) {
+                *reinterpret_cast<uint4*>(p.kc + row * D + ch * 8) =
+                    *reinterpret_cast<const uint4*>(kt + tile_off(r, ch));
+                *reinterpret_cast<uint4*>(p.vc + row * D + ch * 8) = vw;
+              }
+            }
+            bool bad = false;
+            vw.x = finite_pair(vw.x, bad), vw.y = finite_pair(vw.y, bad);
+            vw.z = finite_pair(vw.z, bad), vw.w = finite_pair(vw.w, bad);
+            if (bad) {
+              *vp = vw;
+              atomicOr(&bars->bad[mb][node >> 5], 1u << (node & 31));
+            }
           }
           fence_proxy_async_smem();
           named_bar_sync(1, NL);
@@ -605,7 +657,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             mbar_arrive(&bars->v_full[vs]);
           }
         }
-        if (ok && lt == 0) mbar_arrive(&bars->mask_full);
+        if (ok && lt == 0) mbar_arrive(&bars->mask_full[mb]);
         ++round;
       }
       j0 += s.t1 - s.t0;
@@ -621,23 +673,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     const uint32_t o_col = C::kColO + t * D;
     constexpr int CH = D / 8;
 
+    // this row tile's queries: every S of the segment before is done by then
     auto load_q = [&](const Seg& s) {
-      // this warpgroup's 128 rows; rows past R are zeros
-      uint8_t* qt = smem + C::kOffQ + t * C::kTileBytes;
-      const int r0 = (s.m * NT + t) * kBM;
-      const int wt = tid & 127;
-#pragma unroll 8
-      for (int x = wt; x < kBM * CH; x += 128) {
-        const int r = x / CH, ch = x % CH, rr = r0 + r;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (rr < p.R)
-          w = *reinterpret_cast<const uint4*>(p.q + s.b * p.q_stride[0] + (s.g * p.G + rr % p.G) * p.q_stride[1] +
-                                              (rr / p.G) * p.q_stride[2] + ch * 8);
-        *reinterpret_cast<uint4*>(qt + tile_off(r, ch)) = w;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->q_full[t]);
+      if (quarter != 0 || lane != 0) return;
+      mbar_arrive_expect_tx(&bars->q_full[t], static_cast<uint32_t>(p.RT) * D * 2);
+#pragma unroll
+      for (int x = 0; x < C::kBoxes; ++x)
+        tma_load_5d(smem + C::kOffQ + t * C::kTileBytes + x * kBoxBytes, &tm_q, &bars->q_full[t], x * 64, 0,
+                    (s.m * NT + t) * p.tb, s.g, s.b);
     };
 
     // PV of tile x is done.  Asked about the latest tile or the one before it;
@@ -656,10 +699,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     if (more) load_q(s);
     int j = 0, round = 0, pieces = 0;
     while (ok && more) {
-      const int rr = (s.m * NT + t) * kBM + row;                // row of the KV head
-      const bool warp_on = rr - lane < p.R;                     // any row of this warp exists
-      const int node = rr < p.R ? rr / p.G : 0;
+      const int node = (s.m * NT + t) * p.tb + row / p.G;
+      const bool mine = row < p.RT && node < p.T;               // the row exists
+      const bool warp_on = __any_sync(0xffffffffu, mine);
+      const int head = s.g * p.G + row % p.G;
       const bool has_draft = s.t0 < ntd;
+      const int mb = round & 1;
+      const uint32_t* am = anc + mb * C::kMaxT * C::kWords + (mine ? node : 0) * C::kWords;
+      const int off = draft_off(p, s.ctx);
+      bool more_next = false;
       float m_run = -INFINITY, l_run = 0.0f;
       for (int tile = s.t0; tile < s.t1; ++tile, ++j) {
         const int sb = NT == 1 ? (j & 1) : t;
@@ -670,8 +718,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           break;
         }
         tc_fence_after();
+        if (tile == s.t1 - 1) {
+          more_next = cur.next(s_next);
+          if (more_next) load_q(s_next);
+        }
         if (tile == s.t0 && has_draft) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&bars->mask_full, round & 1, abort, p.status))) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars->mask_full[mb], (round >> 1) & 1, abort, p.status))) {
             ok = false;
             break;
           }
@@ -682,8 +734,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         if (tile < ntd) {
           masked = true;
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            see[x] = (tile * 4 + x < C::kWords && rr < p.R) ? anc[node * C::kWords + tile * 4 + x] : 0u;
+          for (int x = 0; x < 4; ++x) {
+            // bits [32 x - off, +32) of the tile's drafts
+            const int w = tile * 4 + x - (off > 0 ? 1 : 0);
+            const uint32_t lo = w >= 0 && w < C::kWords ? am[w] : 0u;
+            const uint32_t hi = w + 1 >= 0 && w + 1 < C::kWords ? am[w + 1] : 0u;
+            see[x] = mine ? (off > 0 ? __funnelshift_r(lo, hi, 32 - off) : lo) : 0u;
+          }
         } else {
           const int lim = s.ctx - (tile - ntd) * kBN;
           if (lim < kBN) {
@@ -700,7 +757,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
               break;
             }
             uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
-            for (int x = tid & 127; x < (kBN - lim) * CH; x += 128)
+            for (int x = tid & 127; x < (tile_keys(p, tile, s.ctx) - lim) * CH; x += 128)
               *reinterpret_cast<uint4*>(vt + tile_off(lim + x / CH, x % CH)) = make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
           }
@@ -711,53 +768,66 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_addr + s_col + c * 32, sr[c]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_wait_ld(sr[c]);
-          float mx[8];
+          float alpha = 1.0f, rs = 0.0f;
+          // weights 2^(mul s + neg) of the row, P to TMEM and their sum
+          auto weigh = [&](float mul, float neg) {
+            const uint64_t mul2 = f2_pack(mul, mul), neg2 = f2_pack(neg, neg);
+            uint64_t sum[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
-          if (!masked) {
+            for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
 #pragma unroll
-            for (int c = 0; c < kBN; c += 2)
-              mx[(c >> 1) & 7] = fmax3(mx[(c >> 1) & 7], __uint_as_float(sr[c >> 5][c & 31]),
-                                       __uint_as_float(sr[c >> 5][(c & 31) + 1]));
-          } else {
+            for (int c = 0; c < 4; ++c) {
+              uint32_t pw[16];
 #pragma unroll
-            for (int c = 0; c < kBN; ++c) {
-              const float x = ((see[c >> 5] >> (c & 31)) & 1u) ? __uint_as_float(sr[c >> 5][c & 31]) * p.scale_log2
-                                                               : -INFINITY;
-              sr[c >> 5][c & 31] = __float_as_uint(x);
-              mx[c & 7] = fmaxf(mx[c & 7], x);
+              for (int i = 0; i < 32; i += 2) {
+                float x0, x1;
+                f2_unpack(ffma2(f2_pack(__uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1])), mul2, neg2), x0, x1);
+                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                pw[i >> 1] = pack_bf16x2(p0, p1);
+                sum[(i >> 1) & 3] = fadd2(sum[(i >> 1) & 3], f2_pack(p0, p1));
+              }
+              tmem_st16(tmem + lane_addr + s_col + c * 16, pw);
             }
+            float a0, a1;
+            f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
+            rs = a0 + a1;
+          };
+          // Against the reference max at hand, without a max pass; if some row's
+          // sum says its scores outgrew it (2^64; or NaN), from the registers again.
+          bool done = false;
+          if (!masked && __all_sync(0xffffffffu, m_run != -INFINITY)) {
+            weigh(p.scale_log2, -m_run);
+            done = __all_sync(0xffffffffu, rs <= 18446744073709551616.0f);
+            if (!done) tmem_wait_st();
           }
-          float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-          if (!masked) mt *= p.scale_log2;
-          // the reference max moves only when the tile exceeds it by the margin
-          float alpha = 1.0f;
-          if (mt > m_run + kRescaleMargin || (m_run == -INFINITY && mt != -INFINITY)) {
-            alpha = fast_exp2(m_run - mt);
-            m_run = mt;
-          }
-          const float neg = m_run == -INFINITY ? 0.0f : -m_run;
-          const float mul = masked ? 1.0f : p.scale_log2;
-          const uint64_t mul2 = f2_pack(mul, mul), neg2 = f2_pack(neg, neg);
-          uint64_t sum[4];
+          if (!done) {
+            float mx[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
+            for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+            if (!masked) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pw[16];
+              for (int c = 0; c < kBN; c += 2)
+                mx[(c >> 1) & 7] = fmax3(mx[(c >> 1) & 7], __uint_as_float(sr[c >> 5][c & 31]),
+                                         __uint_as_float(sr[c >> 5][(c & 31) + 1]));
+            } else {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float x0, x1;
-              f2_unpack(ffma2(f2_pack(__uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1])), mul2, neg2), x0, x1);
-              const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-              pw[i >> 1] = pack_bf16x2(p0, p1);
-              sum[(i >> 1) & 3] = fadd2(sum[(i >> 1) & 3], f2_pack(p0, p1));
+              for (int c = 0; c < kBN; ++c) {
+                const float x = ((see[c >> 5] >> (c & 31)) & 1u) ? __uint_as_float(sr[c >> 5][c & 31]) * p.scale_log2
+                                                                 : -INFINITY;
+                sr[c >> 5][c & 31] = __float_as_uint(x);
+                mx[c & 7] = fmaxf(mx[c & 7], x);
+              }
             }
-            tmem_st16(tmem + lane_addr + s_col + c * 16, pw);
+            float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+            if (!masked) mt *= p.scale_log2;
+            // the reference max moves only when the tile exceeds it by the margin
+            if (mt > m_run + kRescaleMargin || (m_run == -INFINITY && mt != -INFINITY)) {
+              alpha = fast_exp2(m_run - mt);
+              m_run = mt;
+            }
+            weigh(masked ? 1.0f : p.scale_log2, m_run == -INFINITY ? 0.0f : -m_run);
           }
-          float a0, a1;
-          f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
-          l_run = l_run * alpha + (a0 + a1);
+          l_run = l_run * alpha + rs;
           if (tile > s.t0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
             if (!__all_sync(0xffffffffu, o_wait(j - 1))) {
               ok = false;
@@ -781,9 +851,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         if (lane == 0) mbar_arrive(&bars->p_full[sb]);
       }
       if (!ok) break;
-      // the next segment's queries while the last PV runs (every S of this one is done)
-      const bool more_next = cur.next(s_next);
-      if (more_next) load_q(s_next);
 
       // ---------------------------------------------------------- epilogue
       if (!__all_sync(0xffffffffu, o_wait(j - 1))) {
@@ -795,21 +862,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       // drafts this row sees whose V is not finite, and whether the row's own draft is absent
       bool absent = false;
       uint32_t fix_any = 0u;
-      if (has_draft && rr < p.R) {
+      if (has_draft && mine) {
         uint32_t own = 0u;
 #pragma unroll
         for (int x = 0; x < C::kWords; ++x) {
-          own |= anc[node * C::kWords + x];
-          fix_any |= anc[node * C::kWords + x] & bars->bad[x];
+          own |= am[x];
+          fix_any |= am[x] & bars->bad[mb][x];
         }
         absent = own == 0u;
       }
       const bool empty = absent || l_run == 0.0f;
       const float inv = empty ? 0.0f : 1.0f / l_run;
       const float lse2 = empty ? -INFINITY : m_run + __log2f(l_run);
-      const int head = s.g * p.G + (rr < p.R ? rr % p.G : 0);
       const int slot = 2 * static_cast<int>(blockIdx.x) + (s.item0 + s.t0 == bars->lo ? 0 : 1);
-      const int64_t prow = static_cast<int64_t>(slot) * p.slot_rows + t * kBM + row;
+      const int64_t prow = static_cast<int64_t>(slot) * p.slot_rows + t * p.RT + row;
       const int64_t obase = s.b * p.out_stride[0] + head * p.out_stride[1] + node * p.out_stride[2];
       if (warp_on) {
 #pragma unroll
@@ -817,10 +883,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           uint32_t o[32];
           tmem_ld32(tmem + lane_addr + o_col + c * 32, o);
           tmem_wait_ld(o);
-          if (rr < p.R) {
+          if (mine) {
             if (fix_any != 0u) {
-              for (int a = s.t0 * kBN; a < min(p.T, s.t1 * kBN); ++a) {
-                if (!((anc[node * C::kWords + (a >> 5)] & bars->bad[a >> 5]) >> (a & 31) & 1u)) continue;
+              for (int a = max(0, s.t0 * kBN - off); a < min(p.T, s.t1 * kBN - off); ++a) {
+                if (!((am[a >> 5] & bars->bad[mb][a >> 5]) >> (a & 31) & 1u)) continue;
                 const uint16_t* kr = draft_row<D>(p, false, s.b, s.g, a, s.ctx);
                 const uint16_t* vr = draft_row<D>(p, true, s.b, s.g, a, s.ctx);
                 const uint16_t* qr = p.q + s.b * p.q_stride[0] + head * p.q_stride[1] + node * p.q_stride[2];
@@ -863,7 +929,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           }
           __syncwarp();
         }
-        if (rr < p.R) {
+        if (mine) {
           if (!whole)
             p.part_lse[prow] = absent ? __uint_as_float(kAbsent) : lse2;
           else if (p.lse != nullptr)
@@ -873,7 +939,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       tc_fence_before();  // O is read: the next segment's PV may overwrite it after p_full
       if (has_draft) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->mask_empty);
+        if (lane == 0) mbar_arrive(&bars->mask_empty[mb]);
         ++round;
       }
       if (!whole) {
@@ -912,8 +978,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         ++pieces;
         if (bars->last) {
           __threadfence();
-          const int row0 = s.m * NT * kBM;
-          merge_item<D>(p, s, row0, min(p.R - row0, NT * kBM), c0, np,
+          const int node0 = s.m * NT * p.tb;
+          merge_item<D>(p, s, node0, min(p.T - node0, NT * p.tb) * p.G, c0, np,
                         run_lo(bars->total, bars->n_cta, c0) == s.item0, tid, C::kSoft);
         }
       }
@@ -931,14 +997,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   }
 }
 
-int tree_nt(int64_t R) { return R <= kBM ? 1 : 2; }
+// Row tiles: tb drafts each, one or two to a CTA
+int tile_drafts(int64_t T, int64_t G) { return static_cast<int>(std::min(T, kBM / G)); }
+int tree_nt(int64_t T, int64_t G) { return T <= kBM / G ? 1 : 2; }
 
 template <int D, int NT>
 cudaError_t launch(const TreeArgs& a, TreeParams& p, cudaStream_t stream) {
   using C = Cfg<D, NT>;
-  CUtensorMap mk, mv;
-  if (!make_paged_map(&mk, a.cache.k, a.cache.num_blocks, a.cache.Hkv, D) ||
+  CUtensorMap mq, mk, mv, mkn, mvn;
+  if (!make_rows_map(&mq, a.q, a.cache.Hkv, p.tb) || !make_paged_map(&mk, a.cache.k, a.cache.num_blocks, a.cache.Hkv, D) ||
       !make_paged_map(&mv, a.cache.v, a.cache.num_blocks, a.cache.Hkv, D))
+    return cudaErrorInvalidValue;
+  mkn = mk, mvn = mv;  // not read without k_new
+  if (p.k_new != nullptr && (!make_rows_map(&mkn, a.k_new, a.cache.Hkv, p.new_box) ||
+                             !make_rows_map(&mvn, a.v_new, a.cache.Hkv, p.new_box)))
     return cudaErrorInvalidValue;
   auto kern = paged_tree_tc_kernel<D, NT>;
   if constexpr (NT == 2) {
@@ -952,18 +1024,19 @@ cudaError_t launch(const TreeArgs& a, TreeParams& p, cudaStream_t stream) {
   }
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(a.n_cta), C::kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
+  kern<<<static_cast<unsigned>(a.n_cta), C::kThreads, C::kSmemBytes, stream>>>(mq, mk, mv, mkn, mvn, p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-// Partials of two cut items per CTA, then one 8-byte count per item.
-size_t tree_partial_bytes(int64_t B, int64_t Hkv, int64_t R, int D, int n_cta) {
-  const int nt = tree_nt(R);
-  const size_t rows = static_cast<size_t>(2) * n_cta * (R < nt * kBM ? R : nt * kBM);
+// Partials of two cut items per CTA (their rows), then one 8-byte count per item.
+size_t tree_partial_bytes(int64_t B, int64_t Hkv, int64_t T, int64_t G, int D, int n_cta) {
+  if (T == 0 || G == 0 || G > kBM) return 0;
+  const int64_t group = static_cast<int64_t>(tree_nt(T, G)) * tile_drafts(T, G);  // drafts per item
+  const size_t rows = static_cast<size_t>(2) * n_cta * group * G;
   const size_t parts = (rows * (D + 1) * sizeof(float) + 255) & ~size_t(255);
-  const size_t items = static_cast<size_t>(B) * Hkv * ((R + nt * kBM - 1) / (nt * kBM));
+  const size_t items = static_cast<size_t>(B) * Hkv * ((T + group - 1) / group);
   return parts + ((items * sizeof(unsigned long long) + 255) & ~size_t(255));
 }
 
@@ -974,9 +1047,12 @@ cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream) {
   p.Hq = static_cast<int>(a.Hq);
   p.Hkv = a.cache.Hkv;
   p.G = p.Hq / p.Hkv;
-  p.R = p.T * p.G;
-  const int nt = tree_nt(p.R);
-  p.MP = (p.R + nt * kBM - 1) / (nt * kBM);
+  const int nt = tree_nt(p.T, p.G);
+  p.tb = tile_drafts(p.T, p.G);
+  p.RT = p.tb * p.G;
+  p.MP = (p.T + nt * p.tb - 1) / (nt * p.tb);
+  p.new_box = std::min(kBN, (p.T + 15) / 16 * 16);
+  p.ntd = a.k_new.data != nullptr ? (p.T + kBN - 1) / kBN : (p.T + kBS - 1 + kBN - 1) / kBN;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.scale_positive = p.scale_log2 > 0.0f;
   p.q = static_cast<const uint16_t*>(a.q.data);
@@ -1000,7 +1076,7 @@ cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream) {
   p.out = a.out.data;
   p.out_bf16 = a.out.dtype == ATTN_BF16;
   p.lse = a.lse;
-  p.slot_rows = p.R < nt * kBM ? p.R : nt * kBM;
+  p.slot_rows = nt * p.RT;
   const size_t rows = static_cast<size_t>(2) * a.n_cta * p.slot_rows;
   p.part_o = static_cast<float*>(a.partials);
   p.part_lse = p.part_o + rows * a.cache.D;

@@ -11,18 +11,20 @@
 // V not at all.  Bound: HBM for single tokens (64 KB of K per pair, 1.4 us of an
 // SM's share); the exponentials for long chunks (one per query row and key).
 //
-// Row r of a (sequence, KV head) is query r / G, head r % G; a key at position x
-// is seen by rows r >= (x - start) G, so a causal tile is one comparison per
-// column, and chunks of 128 rows before the pair's first key are left out.  An
-// item is a (sequence, KV head, key pair), its steps are its chunks; every SM
-// takes an equal run of all steps (as in tree_tc.cu), and an item cut between
-// SMs leaves partial sums that its last piece adds up in order: the result does
-// not depend on the timing.
+// A chunk is the G heads of up to 128 / G tokens, one 5-D TMA box of q whatever
+// its strides: column r is token r / G, head r % G.  A key at position x is seen
+// by tokens t >= x - start, so a causal tile is one comparison per column, and
+// chunks before the pair's first key are left out.  An item is a (sequence, KV
+// head, key pair), its steps are its chunks; every SM takes an equal run of all
+// steps (as in tree_tc.cu), and an item cut between SMs leaves partial sums that
+// its last piece adds up in order: the result does not depend on the timing.
 //
-// Warps: 0 streams K pairs, 1 issues the MMAs, 2-3 gather query chunks with
-// cp.async (any strides), 4-7 and 8-11 own the two key tiles.
+// Warps: 0 streams K pairs, 1 issues the MMAs, 2 streams query chunks, 3 their
+// LSEs, 4-7 and 8-11 own the two key tiles.
 #include <cuda.h>
 #include <math.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 #include "internal.h"
@@ -32,12 +34,11 @@ namespace {
 
 constexpr int kBM = 128;       // keys per tile
 constexpr int kPair = 2 * kBM;
-constexpr int kBN = 128;       // query rows per chunk
+constexpr int kBN = 128;       // query rows per chunk, at most
 constexpr int kBS = 16;
 constexpr int kBoxBytes = kBM * 128;
 constexpr int kThreads = 384;
-constexpr int kLoaders = 64;
-constexpr int kLseRing = 8;
+constexpr int kLseRing = 4;
 
 template <int D>
 struct Cfg {
@@ -47,7 +48,7 @@ struct Cfg {
   static constexpr int QS = D == 64 ? 4 : 2;  // query chunk stages
   static constexpr int kOffK = 0;
   static constexpr int kOffQ = kOffK + KS * 2 * kTileBytes;
-  static constexpr int kOffLse = kOffQ + QS * kTileBytes;  // [kLseRing][kBN] log2 LSEs, +inf: no weight
+  static constexpr int kOffLse = kOffQ + QS * kTileBytes;  // [kLseRing][kBN] negated log2 LSEs, -inf: no weight
   static constexpr int kOffBar = kOffLse + kLseRing * kBN * 4;
   static constexpr int kSmemBytes = kOffBar + 512 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
@@ -57,6 +58,7 @@ struct Bars {
   uint64_t k_full[2], k_empty[2];
   uint64_t q_full[4], q_empty[4];
   uint64_t s_full[2], s_free[2];  // [score buffer], both key tiles
+  uint64_t l_full[kLseRing], l_empty[kLseRing];
   uint64_t piece_full, piece_go, drained;
   int64_t lo, hi, total, bstart;
   int b0, n_cta;
@@ -68,10 +70,9 @@ static_assert(sizeof(Bars) <= 512, "barrier block outgrew its shared-memory slot
 
 struct WeightParams {
   int B, T, Hq, Hkv, G;
+  int ct, cr;  // tokens and rows (ct * G) of a chunk
   int causal;
   float scale_log2;
-  const uint16_t* q;
-  int64_t q_stride[3];
   const float* lse;  // [B, Hq, T]
   int num_blocks;
   const int32_t* bt;
@@ -90,17 +91,17 @@ struct WeightParams {
 // One sequence's work: `pairs` key pairs, the first `full` of which all chunks
 // see; pair p >= full starts at chunk first(p).
 struct SeqWork {
-  int start, rows, keys, pairs, chunks, full, G;
+  int start, n, keys, pairs, chunks, full, ct;
   int64_t steps;  // per KV head
   __device__ int first(int p) const {
     if (p < full) return 0;
-    return min(static_cast<int>((static_cast<int64_t>(p) * kPair - start) * G / kBN), chunks - 1);
+    return min((p * kPair - start) / ct, chunks - 1);
   }
 };
 
 __device__ __forceinline__ SeqWork seq_work(const WeightParams& p, int b, bool report_bad) {
   SeqWork w = {};
-  w.G = p.G;
+  w.ct = p.ct;
   w.start = p.start_pos[b];
   int n = p.q_lens != nullptr ? p.q_lens[b] : p.T;
   n = max(0, min(n, p.T));
@@ -109,10 +110,10 @@ __device__ __forceinline__ SeqWork seq_work(const WeightParams& p, int b, bool r
     if (report_bad) report(p.status, kStatusBounds);
     return w;
   }
-  w.rows = n * p.G;
+  w.n = n;
   w.keys = w.start + n;
   w.pairs = (w.keys + kPair - 1) / kPair;
-  w.chunks = (w.rows + kBN - 1) / kBN;
+  w.chunks = (n + p.ct - 1) / p.ct;
   w.full = p.causal ? min(w.pairs, w.start / kPair + 1) : w.pairs;
   w.steps = static_cast<int64_t>(w.full) * w.chunks;
   for (int x = w.full; x < w.pairs; ++x) w.steps += w.chunks - w.first(x);
@@ -186,18 +187,10 @@ __device__ __forceinline__ int run_of(int64_t total, int n, int64_t step) {
   return static_cast<int>(((step + 1) * n - 1) / total);
 }
 
-__device__ __forceinline__ uint32_t tile_off(int r, int ch) {
-  return static_cast<uint32_t>((ch >> 3) * kBoxBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-}
-
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool there) {
-  const int n = there ? 16 : 0;  // 0: zero fill
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ WeightParams p) {
+    attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
+                        const __grid_constant__ WeightParams p) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -216,6 +209,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 4; ++s) {
       mbar_init(&bars->q_full[s], 1);
       mbar_init(&bars->q_empty[s], 1);
+    }
+    for (int s = 0; s < kLseRing; ++s) {
+      mbar_init(&bars->l_full[s], 1);
+      mbar_init(&bars->l_empty[s], 8);
     }
     mbar_init(&bars->piece_full, 8);
     mbar_init(&bars->piece_go, 1);
@@ -254,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bars->lo = lo, bars->hi = hi, bars->total = total, bars->bstart = run;
       bars->b0 = b0, bars->n_cta = n;
       tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_q);
     }
   }
   if (warp == 1) {
@@ -311,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(&bars->q_full[qs], j / C::QS) && wait(&bars->s_free[j & 1], (j >> 1) ^ 1);
           if (!ok) break;
           tc_fence_after();
-          const int cols = min(kBN, cur.w.rows - c * kBN);
+          const int cols = min(p.ct, cur.w.n - c * p.ct) * p.G;
           const uint32_t idesc = idesc_bf16_f32(kBM, (cols + 15) / 16 * 16, false, false);
           const uint32_t qa = smem_u32(smem + C::kOffQ + qs * C::kTileBytes);
 #pragma unroll
@@ -333,69 +331,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit(&bars->drained);
       drain_wait(&bars->drained, 0);
     }
-  } else if (warp < 4) {
+  } else if (warp == 2) {
     // ------------------------------------------------------------ query chunks
-    // One chunk ahead: chunk j's copies are waited for after chunk j + 1's are
-    // issued.  A chunk's last LSE use is before the s_free that lets S(j + 2)
-    // run, so a ring of kLseRing >= QS + 3 LSE rows is never overtaken.
-    static_assert(kLseRing >= C::QS + 3, "LSE ring");
-    constexpr int CH = D / 8;
-    const int lt = threadIdx.x - 64;
+    if (lane == 0) {
+      Cursor cur(p, bars);
+      Seg s;
+      int j = 0;
+      bool ok = true;
+      const uint32_t bytes = static_cast<uint32_t>(p.cr) * D * 2;  // tokens past T arrive as zeros
+      while (ok && cur.next(s)) {
+        for (int c = s.c0; c < s.c1; ++c, ++j) {
+          const int qs = j % C::QS;
+          ok = mbar_wait(&bars->q_empty[qs], ((j / C::QS) & 1) ^ 1, abort, p.status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bars->q_full[qs], bytes);
+#pragma unroll
+          for (int x = 0; x < C::kBoxes; ++x)
+            tma_load_5d(smem + C::kOffQ + qs * C::kTileBytes + x * kBoxBytes, &tm_q, &bars->q_full[qs], x * 64, 0,
+                        c * p.ct, s.g, s.b);
+        }
+      }
+      if (*abort)
+        for (int x = max(0, j - C::QS); x < j; ++x) drain_wait(&bars->q_full[x % C::QS], (x / C::QS) & 1);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ their LSEs
+    // negated, in log2 units; -inf where a column has no weight (past the
+    // chunk, or a row that saw nothing).  Loaded a chunk ahead of the store.
     Cursor cur(p, bars);
     Seg s;
     int j = 0;
     bool ok = true;
-    float lse_next[2] = {0.f, 0.f};
-    auto publish = [&](int jj, const float (&l)[2]) {  // chunk jj has landed (this thread's copies are waited for)
-      float* row = lse_ring + (jj % kLseRing) * kBN;
+    float v[4];
+    int dt[4], dh[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) dt[x] = (lane + 32 * x) / p.G, dh[x] = (lane + 32 * x) % p.G;
+    auto publish = [&](int jj) {
+      const int sl = jj % kLseRing;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->l_empty[sl], ((jj / kLseRing) & 1) ^ 1, abort, p.status)))
+        return false;
       bool odd = false;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float v = l[x] == -INFINITY ? INFINITY : l[x] * 1.4426950408889634f;
-        odd |= v == INFINITY;
-        row[lt + x * kLoaders] = v;
+      for (int x = 0; x < 4; ++x) {
+        const float l = v[x] == -INFINITY ? -INFINITY : v[x] * -1.4426950408889634f;
+        odd |= l == -INFINITY;
+        lse_ring[sl * kBN + lane + 32 * x] = l;
       }
-      fence_proxy_async_smem();
-      odd = named_bar_or(1, kLoaders, odd);
-      if (lt == 0) {
-        bars->odd[jj % kLseRing] = odd;
-        mbar_arrive(&bars->q_full[jj % C::QS]);
-      }
+      odd = __any_sync(0xffffffffu, odd);
+      if (lane == 0) bars->odd[sl] = odd;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->l_full[sl]);
+      return true;
     };
     while (ok && cur.next(s)) {
-      for (int c = s.c0; c < s.c1; ++c, ++j) {
-        const int qs = j % C::QS;
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty[qs], ((j / C::QS) & 1) ^ 1, abort, p.status));
-        ok = !named_bar_or(2, kLoaders, !ok);
-        if (!ok) break;
-        uint8_t* qt = smem + C::kOffQ + qs * C::kTileBytes;
-        const int r0 = c * kBN;
-        const int n16 = (min(kBN, cur.w.rows - r0) + 15) / 16 * 16;
-        const uint16_t* qb = p.q + s.b * p.q_stride[0] + static_cast<int64_t>(s.g) * p.G * p.q_stride[1];
-        for (int x = lt; x < n16 * CH; x += kLoaders) {
-          const int r = x / CH, ch = x % CH, rr = r0 + r;
-          const bool there = rr < cur.w.rows;
-          const int t = there ? rr / p.G : 0, hh = there ? rr - t * p.G : 0;
-          cp_async16(qt + tile_off(r, ch), qb + hh * p.q_stride[1] + t * p.q_stride[2] + ch * 8, there);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        float l[2];
+      const float* row = p.lse + (static_cast<int64_t>(s.b) * p.Hq + static_cast<int64_t>(s.g) * p.G) * p.T;
+      for (int c = s.c0; ok && c < s.c1; ++c, ++j) {
+        float next[4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int rr = r0 + lt + x * kLoaders;
-          l[x] = -INFINITY;
-          if (rr < cur.w.rows)
-            l[x] = p.lse[(static_cast<int64_t>(s.b) * p.Hq + s.g * p.G + rr % p.G) * p.T + rr / p.G];
+        for (int x = 0; x < 4; ++x) {
+          const int t = c * p.ct + dt[x];
+          next[x] = dt[x] < p.ct && t < cur.w.n ? row[static_cast<int64_t>(dh[x]) * p.T + t] : -INFINITY;
         }
-        if (j > 0) {
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-          publish(j - 1, lse_next);
-        }
-        lse_next[0] = l[0], lse_next[1] = l[1];
+        if (j > 0) ok = publish(j - 1);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[x] = next[x];
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (ok && j > 0) publish(j - 1, lse_next);
+    if (ok && j > 0) publish(j - 1);
   } else {
     // ------------------------------------------------------------ sums
     const int t = (warp >> 2) - 1;
@@ -421,45 +423,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           *at = got;
       };
-      // rows that see the key: r >= rmin
-      const int64_t rmin =
-          p.causal ? max(static_cast<int64_t>(0), static_cast<int64_t>(key - cur.w.start) * p.G) : 0;
-      const int64_t tile_rmin = __shfl_sync(0xffffffffu, rmin, 31);  // the warp's last key is seen by the fewest
+      // tokens that see the key: t >= tmin; the warp's last key is seen by the fewest
+      const int tmin = p.causal ? key - cur.w.start : 0;
+      const int warp_tmin = __shfl_sync(0xffffffffu, tmin, 31);
       uint64_t sum[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) sum[x] = f2_pack(0.f, 0.f);
-      const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), m1 = f2_pack(-1.f, -1.f);
+      const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
       for (int c = s.c0; c < s.c1; ++c, ++j) {
-        const int buf = j & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[buf], (j >> 1) & 1, abort, p.status))) {
+        const int buf = j & 1, sl = j % kLseRing;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->l_full[sl], (j / kLseRing) & 1, abort, p.status) &&
+                                         mbar_wait(&bars->s_full[buf], (j >> 1) & 1, abort, p.status))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int r0 = c * kBN;
-        const int cols = min(kBN, cur.w.rows - r0);
-        const float* lse2 = lse_ring + (j % kLseRing) * kBN;
-        const bool masked = bars->odd[j % kLseRing] != 0 || tile_rmin > r0;
-        const int rel = static_cast<int>(min(rmin - r0, static_cast<int64_t>(kBN)));  // columns >= rel see the key
+        const int t0 = c * p.ct;
+        const int cols = min(p.ct, cur.w.n - t0) * p.G;
+        const float* nl = lse_ring + sl * kBN;
+        const bool masked = bars->odd[sl] != 0 || warp_tmin > t0;
+        const int rel = max(0, min(tmin - t0, p.ct)) * p.G;  // columns >= rel see the key
         for (int cc = 0; cc < cols; cc += 32) {
           uint32_t sr[32];
           tmem_ld32(tmem + lane_addr + (2 * t + buf) * 128 + cc, sr);
           tmem_wait_ld(sr);
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(lse2 + cc + i);
+            const float4 l4 = *reinterpret_cast<const float4*>(nl + cc + i);
             float x0, x1, x2, x3;
-            const uint64_t a = ffma2(f2_pack(l4.x, l4.y), m1, f2_pack(0.f, 0.f));
-            const uint64_t b = ffma2(f2_pack(l4.z, l4.w), m1, f2_pack(0.f, 0.f));
-            f2_unpack(ffma2(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), sc2, a), x0, x1);
-            f2_unpack(ffma2(f2_pack(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])), sc2, b), x2, x3);
+            f2_unpack(ffma2(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), sc2, f2_pack(l4.x, l4.y)), x0,
+                      x1);
+            f2_unpack(ffma2(f2_pack(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])), sc2, f2_pack(l4.z, l4.w)),
+                      x2, x3);
             float w0 = fast_exp2(x0), w1 = fast_exp2(x1), w2 = fast_exp2(x2), w3 = fast_exp2(x3);
             if (masked) {
               // selected, not multiplied: whatever a column without weight holds stays out
-              w0 = (cc + i >= rel && l4.x != INFINITY) ? w0 : 0.f;
-              w1 = (cc + i + 1 >= rel && l4.y != INFINITY) ? w1 : 0.f;
-              w2 = (cc + i + 2 >= rel && l4.z != INFINITY) ? w2 : 0.f;
-              w3 = (cc + i + 3 >= rel && l4.w != INFINITY) ? w3 : 0.f;
+              w0 = (cc + i >= rel && l4.x != -INFINITY) ? w0 : 0.f;
+              w1 = (cc + i + 1 >= rel && l4.y != -INFINITY) ? w1 : 0.f;
+              w2 = (cc + i + 2 >= rel && l4.z != -INFINITY) ? w2 : 0.f;
+              w3 = (cc + i + 3 >= rel && l4.w != -INFINITY) ? w3 : 0.f;
             }
             sum[(i >> 1) & 3] = fadd2(sum[(i >> 1) & 3], f2_pack(w0, w1));
             sum[((i >> 1) + 1) & 3] = fadd2(sum[((i >> 1) + 1) & 3], f2_pack(w2, w3));
@@ -467,7 +469,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->s_free[buf]);
+        if (lane == 0) {
+          mbar_arrive(&bars->s_free[buf]);
+          mbar_arrive(&bars->l_empty[sl]);
+        }
       }
       if (!ok) break;
       float a0, a1;
@@ -536,12 +541,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D>
 cudaError_t launch(const WeightArgs& a, const WeightParams& p, cudaStream_t stream) {
-  CUtensorMap mk;
-  if (!make_paged_map(&mk, a.cache.k, a.cache.num_blocks, a.cache.Hkv, D)) return cudaErrorInvalidValue;
+  CUtensorMap mk, mq;
+  if (!make_paged_map(&mk, a.cache.k, a.cache.num_blocks, a.cache.Hkv, D) ||
+      !make_rows_map(&mq, a.q, a.cache.Hkv, p.ct))
+    return cudaErrorInvalidValue;
   auto kern = attn_weights_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(a.n_cta), kThreads, Cfg<D>::kSmemBytes, stream>>>(mk, p);
+  kern<<<static_cast<unsigned>(a.n_cta), kThreads, Cfg<D>::kSmemBytes, stream>>>(mk, mq, p);
   return cudaGetLastError();
 }
 
@@ -567,8 +574,8 @@ cudaError_t launch_attn_weights(const WeightArgs& a, cudaStream_t stream) {
   p.G = p.Hq / p.Hkv;
   p.causal = a.causal;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
-  p.q = static_cast<const uint16_t*>(a.q.data);
-  for (int i = 0; i < 3; ++i) p.q_stride[i] = a.q.stride[i];
+  p.ct = std::min(p.T, kBN / p.G);
+  p.cr = p.ct * p.G;
   p.lse = a.lse;
   p.num_blocks = static_cast<int>(a.cache.num_blocks);
   p.bt = a.block_table;
