@@ -550,8 +550,8 @@ attn_status rope_kv_append_q8(const attn_tensor *q, const attn_tensor *k_new, co
  *                 the same flag and that sequence's result must be discarded.
  *   lse           float32 [batch, Hq, T] contiguous, or NULL
  *   workspace     >= paged_tree_workspace_size(...) bytes on the current device:
- *                 partial rows of the items that are cut between SMs, and their
- *                 counts.  It needs no clearing between calls (only the status
+ *                 partial rows of the (sequence, KV head)s that are cut between
+ *                 SMs.  It needs no clearing between calls (only the status
  *                 word must start at zero).  Calls that share a workspace must
  *                 not overlap on the GPU.
  * T <= 256.  Blocks that hold drafts must not be shared between sequences.

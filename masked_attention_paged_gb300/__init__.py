@@ -87,15 +87,15 @@ def _signatures() -> dict:
         "paged_decode_attn_noalloc": (I32, [T, C, P, I64, I32, P, F, T, P, P, P]),
         "attn_rope_frequencies": (I32, [I32, ctypes.c_double, I32, ctypes.c_double, I64, ctypes.c_double,
                                         ctypes.c_double, P, ctypes.POINTER(F)]),
-        "rope_apply": (I32, [T, P, I64, P, I32, I32, I32, F, T, P]),
-        "rope_kv_append": (I32, [T, T, T, P, I64, P, I32, I32, F, T, C, P, I64, I32, P, P, SZ, P]),
-        "rope_kv_append_q8": (I32, [T, T, T, P, I64, P, I32, I32, F, T, CQ, P, I64, I32, P, P, SZ, P]),
+        "rope_apply": (I32, [P, P, I64, P, I32, I32, I32, F, P, P]),
+        "rope_kv_append": (I32, [P, P, P, P, I64, P, I32, I32, F, P, P, P, I64, I32, P, P, SZ, P]),
+        "rope_kv_append_q8": (I32, [P, P, P, P, I64, P, I32, I32, F, P, P, P, I64, I32, P, P, SZ, P]),
         "paged_tree_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32, I32]),
-        "paged_tree_attn": (I32, [T, T, T, C, P, I64, I32, P, P, I64, F, T, P, P, SZ, P]),
-        "kv_tree_accept": (I32, [C, P, I64, I32, P, P, I64, I32, P, I32, P, SZ, P]),
+        "paged_tree_attn": (I32, [P, P, P, P, P, I64, I32, P, P, I64, F, P, P, P, SZ, P]),
+        "kv_tree_accept": (I32, [P, P, I64, I32, P, P, I64, I32, P, I32, P, SZ, P]),
         "paged_attn_weights_workspace_size": (SZ, [I32, I32, I32, I32]),
-        "paged_attn_weights": (I32, [T, P, C, P, I64, I32, P, P, I32, F, P, P, SZ, P]),
-        "kv_evict": (I32, [C, P, P, I64, I32, P, P, I64, I32, I32, I32, I32, I32, P, P, P, SZ, P]),
+        "paged_attn_weights": (I32, [P, P, P, P, I64, I32, P, P, I32, F, P, P, SZ, P]),
+        "kv_evict": (I32, [P, P, P, I64, I32, P, P, I64, I32, I32, I32, I32, I32, P, P, P, SZ, P]),
         "attn_check_device_status": (I32, [P, ctypes.POINTER(ctypes.c_uint32), P]),
         "attn_reset_device_status": (I32, [P, P]),
         "attn_selftest_wait_timeout": (I32, [P, SZ, ctypes.c_uint32, P]),
@@ -161,6 +161,7 @@ def _dtype_code(t: torch.Tensor) -> int:
 # bound by the host, and setting the structure's fields one by one costs about
 # as much as the launch.
 _pack_tensor = struct.Struct("@Pii8q").pack
+_pack_by_dim = tuple(struct.Struct(f"@Pii{n}q{32 - 8 * n}x{n}q{32 - 8 * n}x").pack for n in range(5))
 _pack_cache = struct.Struct("@PPiiqii").pack  # an AttnKVCache
 _NO_DIMS = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())  # by number of dimensions used
 
@@ -176,8 +177,37 @@ def _desc(t: torch.Tensor) -> AttnTensor:
                                                     *rest))
 
 
+# The current stream's handle without a Stream object around it (which costs ten
+# times as much), where torch has the call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _tensor_bytes(t: torch.Tensor) -> bytes:
+    """An AttnTensor as bytes, for entry points declared with a plain pointer."""
+    if not _on_device(t):
+        raise ValueError("libattn tensors must be on a CUDA device")
+    n = t.dim()
+    if n > 4:
+        raise ValueError(f"libattn tensors have up to 4 dimensions, got {n}")
+    return _pack_by_dim[n](t.data_ptr(), _dtype_code(t), n, *t.shape, *t.stride())
+
+
+def _cache_bytes(k_cache: torch.Tensor, v_cache: torch.Tensor) -> bytes:
+    """The AttnKVCache of two cache tensors, as bytes."""
+    if not (k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype):
+        raise ValueError("K and V caches must be [num_blocks, Hkv, block_size, D] of one dtype")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("K and V caches must be contiguous")
+    if not (_on_device(k_cache) and _on_device(v_cache)):
+        raise ValueError("K and V caches must be on a CUDA device")
+    nb, heads, bs, D = k_cache.shape
+    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), _dtype_code(k_cache), bs, nb, heads, D)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -415,15 +445,7 @@ def attn_lse_merge(outs: Sequence[torch.Tensor], lses: Sequence[torch.Tensor], o
 
 
 def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor) -> AttnKVCache:
-    if not (k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype):
-        raise ValueError("K and V caches must be [num_blocks, Hkv, block_size, D] of one dtype")
-    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
-        raise ValueError("K and V caches must be contiguous")
-    if not (_on_device(k_cache) and _on_device(v_cache)):
-        raise ValueError("K and V caches must be on a CUDA device")
-    nb, heads, bs, D = k_cache.shape
-    return AttnKVCache.from_buffer_copy(_pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), _dtype_code(k_cache), bs,
-                                                    nb, heads, D))
+    return AttnKVCache.from_buffer_copy(_cache_bytes(k_cache, v_cache))
 
 
 def kv_append(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, pos: torch.Tensor,
@@ -772,10 +794,9 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, in
     B, H, T, D = x.shape
     _check_rope(positions, freqs, B, T, D)
     _check_devices("rope_apply", x, positions, freqs, out)
-    dx, do = _desc(x), _desc(full)
-    st = lib.rope_apply(ctypes.byref(dx), _ptr(positions, "positions"), positions.stride(0), _ptr(freqs, "freqs"),
+    st = lib.rope_apply(_tensor_bytes(x), _ptr(positions, "positions"), positions.stride(0), _ptr(freqs, "freqs"),
                         2 * freqs.shape[0], int(bool(interleaved)), int(bool(inverse)), float(magnitude),
-                        ctypes.byref(do), _stream(stream))
+                        _tensor_bytes(full), _stream(stream))
     _check("rope_apply", st)
     return out
 
@@ -800,10 +821,9 @@ def _rope_append(name, cache, device, q, k_new, v_new, positions, freqs, block_t
     _check_devices(name, q, k_new, v_new, positions, freqs, block_table, start_pos, q_out)
     ws = workspace or _small_ws(device)
     _require(k_new.dim() == 4 and v_new.dim() == 4, "k_new and v_new must have q's number of dimensions")
-    dq, dk, dv, do = _desc(q), _desc(k_new), _desc(v_new), _desc(full)
-    st = getattr(lib, name)(ctypes.byref(dq), ctypes.byref(dk), ctypes.byref(dv), _ptr(positions, "positions"),
+    st = getattr(lib, name)(_tensor_bytes(q), _tensor_bytes(k_new), _tensor_bytes(v_new), _ptr(positions, "positions"),
                             positions.stride(0), _ptr(freqs, "freqs"), 2 * freqs.shape[0], int(bool(interleaved)),
-                            float(magnitude), ctypes.byref(do), ctypes.byref(cache), _ptr(block_table, "block_table"),
+                            float(magnitude), _tensor_bytes(full), cache, _ptr(block_table, "block_table"),
                             block_table.stride(0), block_table.shape[1], _ptr(start_pos, "start_pos"), ws.ptr,
                             ws.nbytes, _stream(stream))
     _check(name, st)
@@ -818,7 +838,7 @@ def rope_kv_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, po
     [B, T]), and write the rotated keys and v_new to cache slots start_pos[b] +
     i.  Without the T dimension (and positions [B]): one token a sequence.
     Returns the rotated q (q_out may be q)."""
-    return _rope_append("rope_kv_append", _cache(k_cache, v_cache), k_cache.device, q, k_new, v_new, positions, freqs,
+    return _rope_append("rope_kv_append", _cache_bytes(k_cache, v_cache), k_cache.device, q, k_new, v_new, positions, freqs,
                         block_table, start_pos, interleaved, magnitude, q_out, workspace, stream)
 
 
@@ -829,7 +849,7 @@ def rope_kv_append_q8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
                       workspace: Optional[Workspace] = None, stream=None):
     """rope_kv_append into an INT8 cache (codes int8 [N, Hkv, 16, D], scales
     float32 [N, Hkv, 16])."""
-    return _rope_append("rope_kv_append_q8", _cache_q8(kq_cache, vq_cache, k_scale, v_scale), kq_cache.device, q,
+    return _rope_append("rope_kv_append_q8", bytes(_cache_q8(kq_cache, vq_cache, k_scale, v_scale)), kq_cache.device, q,
                         k_new, v_new, positions, freqs, block_table, start_pos, interleaved, magnitude, q_out,
                         workspace, stream)
 
@@ -877,18 +897,17 @@ def paged_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if lse is not None:
         _check_f32_buffer(lse, B * Hq * T, "lse")
     _check_devices("paged_tree_attn", q, k_cache, v_cache, block_table, ctx_lens, parents, k_new, v_new, out, lse)
-    c = _cache(k_cache, v_cache)
+    c = _cache_bytes(k_cache, v_cache)
     max_blocks = block_table.shape[1]
     ws = workspace
     if ws is None:
         ws = Workspace(paged_tree_workspace_size(B, Hq, k_cache.shape[1], T, max_blocks, k_cache.shape[2], D),
                        device=q.device)
-    dq, do = _desc(q), _desc(out)
-    dk = ctypes.byref(_desc(k_new)) if k_new is not None else None
-    dv = ctypes.byref(_desc(v_new)) if v_new is not None else None
-    st = lib.paged_tree_attn(ctypes.byref(dq), dk, dv, ctypes.byref(c), _ptr(block_table, "block_table"),
+    dk = _tensor_bytes(k_new) if k_new is not None else None
+    dv = _tensor_bytes(v_new) if v_new is not None else None
+    st = lib.paged_tree_attn(_tensor_bytes(q), dk, dv, c, _ptr(block_table, "block_table"),
                              block_table.stride(0), max_blocks, _ptr(ctx_lens, "ctx_lens"), _ptr(parents, "parents"),
-                             parents.stride(0), float(scale), ctypes.byref(do), _ptr(lse, "lse"), ws.ptr, ws.nbytes,
+                             parents.stride(0), float(scale), _tensor_bytes(out), _ptr(lse, "lse"), ws.ptr, ws.nbytes,
                              _stream(stream))
     _check("paged_tree_attn", st)
     return (out, lse) if return_lse else out
@@ -907,8 +926,8 @@ def kv_tree_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: to
     _check_int32_vec(n_accept, B, "n_accept")
     _check_devices("kv_tree_accept", k_cache, v_cache, block_table, ctx_lens, path, n_accept)
     ws = workspace or _small_ws(k_cache.device)
-    c = _cache(k_cache, v_cache)
-    st = lib.kv_tree_accept(ctypes.byref(c), _ptr(block_table, "block_table"), block_table.stride(0),
+    c = _cache_bytes(k_cache, v_cache)
+    st = lib.kv_tree_accept(c, _ptr(block_table, "block_table"), block_table.stride(0),
                             block_table.shape[1], _ptr(ctx_lens, "ctx_lens"), _ptr(path, "path"), path.stride(0),
                             path.shape[1], _ptr(n_accept, "n_accept"), B, ws.ptr, ws.nbytes, _stream(stream))
     _check("kv_tree_accept", st)
@@ -947,7 +966,7 @@ def paged_attn_weights(q: torch.Tensor, lse: torch.Tensor, k_cache: torch.Tensor
     _check_int32_vec(start_pos, B, "start_pos")
     if q_lens is not None:
         _check_int32_vec(q_lens, B, "q_lens")
-    c = _cache(k_cache, k_cache)
+    c = _cache_bytes(k_cache, k_cache)
     _check_acc(acc, k_cache)
     _check_devices("paged_attn_weights", q, lse, k_cache, block_table, start_pos, acc, q_lens)
     max_blocks = block_table.shape[1]
@@ -955,8 +974,7 @@ def paged_attn_weights(q: torch.Tensor, lse: torch.Tensor, k_cache: torch.Tensor
     if ws is None:
         ws = Workspace(paged_attn_weights_workspace_size(B, k_cache.shape[1], max_blocks, k_cache.shape[2]),
                        device=q.device)
-    dq = _desc(q)
-    st = lib.paged_attn_weights(ctypes.byref(dq), _ptr(lse, "lse"), ctypes.byref(c), _ptr(block_table, "block_table"),
+    st = lib.paged_attn_weights(_tensor_bytes(q), _ptr(lse, "lse"), c, _ptr(block_table, "block_table"),
                                 block_table.stride(0), max_blocks, _ptr(start_pos, "start_pos"),
                                 _ptr(q_lens, "q_lens"), int(bool(causal)), float(scale), _ptr(acc, "acc"), ws.ptr,
                                 ws.nbytes, _stream(stream))
@@ -980,7 +998,7 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
             and dst_block_table.dim() == 2 and dst_block_table.shape[0] >= B and dst_block_table.stride(1) == 1
             and dst_block_table.stride(0) >= dst_block_table.shape[1]):
         raise ValueError(f"dst_block_table must be int32 [>= {B}, blocks] with contiguous rows")
-    c = _cache(k_cache, v_cache)
+    c = _cache_bytes(k_cache, v_cache)
     _check_acc(acc, k_cache)
     keep = int(keep)
     if new_lens is None:
@@ -992,7 +1010,7 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
         raise ValueError(f"kept must be contiguous int32 {(B, Hkv, keep)}, got {tuple(kept.shape)}")
     _check_devices("kv_evict", k_cache, v_cache, acc, block_table, ctx_lens, dst_block_table, new_lens, kept)
     ws = workspace or _small_ws(k_cache.device)
-    st = lib.kv_evict(ctypes.byref(c), _ptr(acc, "acc"), _ptr(block_table, "block_table"), block_table.stride(0),
+    st = lib.kv_evict(c, _ptr(acc, "acc"), _ptr(block_table, "block_table"), block_table.stride(0),
                       block_table.shape[1], _ptr(ctx_lens, "ctx_lens"), _ptr(dst_block_table, "dst_block_table"),
                       dst_block_table.stride(0), dst_block_table.shape[1], B, keep, int(sink), int(recent),
                       _ptr(new_lens, "new_lens"), _ptr(kept, "kept"), ws.ptr, ws.nbytes, _stream(stream))

@@ -678,8 +678,7 @@ size_t paged_tree_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num
   if (batch < 0 || num_q_heads < 0 || num_kv_heads <= 0 || num_drafts < 0 || max_blocks < 0 || block_size <= 0 ||
       head_dim <= 0 || num_q_heads % num_kv_heads != 0)
     return 0;
-  return kStatusBytes + tree_partial_bytes(batch, num_kv_heads, num_drafts, num_q_heads / num_kv_heads, head_dim,
-                                           device_sm_count());
+  return kStatusBytes + tree_partial_bytes(num_drafts, num_q_heads / num_kv_heads, head_dim, device_sm_count());
 }
 
 attn_status paged_tree_attn(const attn_tensor* q, const attn_tensor* k_new, const attn_tensor* v_new,
@@ -739,7 +738,6 @@ attn_status paged_tree_attn(const attn_tensor* q, const attn_tensor* k_new, cons
   a.lse = lse;
   a.partials = static_cast<uint8_t*>(workspace) + kStatusBytes;
   a.n_cta = device_sm_count();
-  a.gen = next_decode_gen();
   a.status = static_cast<uint32_t*>(workspace);
   if (a.n_cta <= 0) return ATTN_ERR_CUDA;
   return from_cuda(launch_paged_tree(a, stream));

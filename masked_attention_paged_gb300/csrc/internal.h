@@ -192,11 +192,10 @@ struct TreeArgs {
   float* lse;      // [B, Hq, T] or null
   void* partials;  // workspace after the status block
   int n_cta;       // CTAs of the launch (one per SM)
-  uint32_t gen;    // this call's generation, tags the piece counts (never 0)
   uint32_t* status;
 };
 // workspace past the status block, G = Hq / Hkv
-size_t tree_partial_bytes(int64_t B, int64_t Hkv, int64_t T, int64_t G, int D, int n_cta);
+size_t tree_partial_bytes(int64_t T, int64_t G, int D, int n_cta);
 cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream);
 
 struct AcceptArgs {

@@ -115,7 +115,7 @@ struct EvictParams {
 };
 
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
-constexpr int kKeys = 32;  // keys a thread holds
+constexpr int kKeys = 16;  // keys a thread holds
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ uint32_t rank_key(float x) {
@@ -132,20 +132,21 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// the word at the same shared-memory place in CTA `rank` of the cluster
-__device__ __forceinline__ int peer_read(const int* p, uint32_t rank) {
+// store to the word at the same shared-memory place in CTA `rank` of the cluster
+__device__ __forceinline__ void peer_store(int* p, uint32_t rank, int v) {
   uint32_t addr;
-  int v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // grid (cluster size, Hkv, B), clusters along x
 __global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const EvictParams p, const int nc) {
   __shared__ int warp_cnt[kSelWarps][3];
-  __shared__ int cta_cnt[2][3];  // this CTA's counts, alternating between rounds
+  // every CTA's counts, pushed by their owners, alternating between rounds (a
+  // cluster barrier separates a buffer's readers from its next writers)
+  __shared__ int cta_cnt[2][kMaxCluster][3];
   __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int g = blockIdx.y, b = blockIdx.z;
   const int rank = static_cast<int>(cluster_rank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -179,10 +180,20 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const E
   const bool held = per <= 32 * kKeys;  // the same for the whole cluster
   uint32_t key[kKeys];
   if (held) {
+    // all block ids, then all sums: two round trips to memory
 #pragma unroll
     for (int e = 0; e < kKeys; ++e) {
       const int i = w0 + 32 * e + lane;
-      key[e] = i < w1 ? key_of(i) : 0u;
+      key[e] = i < w1 ? static_cast<uint32_t>(bt[i / kBS]) : 0u;
+    }
+#pragma unroll
+    for (int e = 0; e < kKeys; ++e) {
+      const int i = w0 + 32 * e + lane;
+      const bool there = i < w1 && key[e] < static_cast<uint64_t>(p.num_blocks);
+      if (i < w1 && !there) report(p.status, kStatusBounds);
+      const float x = there ? p.acc[(static_cast<int64_t>(key[e]) * p.Hkv + g) * kBS + i % kBS] : 0.f;
+      key[e] = there ? rank_key(x) : 0u;
+      if (i < w1 && (i < p.sink || i >= L - p.recent)) key[e] = 0xffffffffu;
     }
   }
   // largest threshold that at least `keep` keys reach (a filler key 0 is only
@@ -211,23 +222,19 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const E
     c3 = __reduce_add_sync(0xffffffffu, c3);
     if (lane == 0) warp_cnt[warp][0] = c1, warp_cnt[warp][1] = c2, warp_cnt[warp][2] = c3;
     __syncthreads();
-    if (threadIdx.x < 3) {
+    if (threadIdx.x < 3 * nc) {
+      const int c = threadIdx.x % 3;
       int s = 0;
 #pragma unroll
-      for (int w = 0; w < kSelWarps; ++w) s += warp_cnt[w][threadIdx.x];
-      cta_cnt[round & 1][threadIdx.x] = s;
+      for (int w = 0; w < kSelWarps; ++w) s += warp_cnt[w][c];
+      peer_store(&cta_cnt[round & 1][rank][c], threadIdx.x / 3, s);
     }
-    if (nc > 1) {
-      cluster_sync();
-    } else {
-      __syncthreads();
-    }
+    cluster_sync();
     c1 = c2 = c3 = 0;
     for (int r = 0; r < nc; ++r) {
-      const int* c = cta_cnt[round & 1];
-      c1 += nc > 1 ? peer_read(c, r) : c[0];
-      c2 += nc > 1 ? peer_read(c + 1, r) : c[1];
-      c3 += nc > 1 ? peer_read(c + 2, r) : c[2];
+      c1 += cta_cnt[round & 1][r][0];
+      c2 += cta_cnt[round & 1][r][1];
+      c3 += cta_cnt[round & 1][r][2];
     }
     if (c3 >= p.keep)
       thr = t3;
@@ -262,15 +269,18 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const E
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) warp_gt[warp] = gt, warp_eq[warp] = eq;
-  if (nc > 1) {
-    cluster_sync();
-  } else {
-    __syncthreads();
+  __syncthreads();
+  if (threadIdx.x < 2 * nc) {
+    const int c = threadIdx.x & 1;
+    int s = 0;
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) s += c ? warp_eq[w] : warp_gt[w];
+    peer_store(&cta_cnt[0][rank][c], threadIdx.x >> 1, s);  // round 15 used buffer 1
   }
+  cluster_sync();
   int gt0 = 0, eq0 = 0;  // before this warp's range
-  for (int r = 0; r < rank; ++r)
-    for (int w = lane; w < kSelWarps; w += 32) gt0 += peer_read(&warp_gt[w], r), eq0 += peer_read(&warp_eq[w], r);
-  if (lane < warp) gt0 += warp_gt[lane], eq0 += warp_eq[lane];
+  if (lane < warp) gt0 = warp_gt[lane], eq0 = warp_eq[lane];
+  if (lane < rank) gt0 += cta_cnt[0][lane][0], eq0 += cta_cnt[0][lane][1];
   gt0 = __reduce_add_sync(0xffffffffu, gt0);
   eq0 = __reduce_add_sync(0xffffffffu, eq0);
   const uint32_t below = (1u << lane) - 1u;
@@ -292,20 +302,21 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const E
   } else {
     for (int e = 0; e < ne; ++e) place(e, key_at(e));
   }
-  if (nc > 1) cluster_sync();  // a peer may still read this CTA's counts
 }
 
 // kv_evict, second launch: the kept rows and their weights to the other table's
-// blocks.  grid (row groups, Hkv, B).
-constexpr int kCopyThreads = 256, kCopyVecs = 4;
-__global__ void __launch_bounds__(kCopyThreads) kv_evict_copy_kernel(const EvictParams p, const int rows_per_cta) {
+// blocks.  grid (row groups, Hkv, B).  The rows' places come first, one thread a
+// row (kept slot -> block -> row: three dependent loads, once), then the rows
+// stream through registers, kCopyVecs 16-byte vectors a thread in flight.
+constexpr int kCopyThreads = 256, kCopyVecs = 8, kCopyRows = 128;
+template <int CH>  // 16-byte chunks per row
+__global__ void __launch_bounds__(kCopyThreads) kv_evict_copy_kernel(const EvictParams p) {
+  __shared__ int64_t from[kCopyRows], to[kCopyRows];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int g = blockIdx.y, b = blockIdx.z;
-  const int r0 = blockIdx.x * rows_per_cta;
-  const int n = min(p.keep, r0 + rows_per_cta) - r0;
+  const int r0 = blockIdx.x * kCopyRows;
   const int32_t* kept = p.kept + (static_cast<int64_t>(b) * p.Hkv + g) * p.keep + r0;
-  const int32_t* bt = p.bt + b * p.bt_stride;
-  const int32_t* dt = p.dst + b * p.dst_stride;
-  // row i of the group: its place in the cache (in rows), or -1
+  // the cache row of a slot, or -1
   auto place = [&](const int32_t* table, int blocks, int slot) -> int64_t {
     const int blk = slot / kBS < blocks ? table[slot / kBS] : -1;
     if (blk < 0 || blk >= p.num_blocks) {
@@ -314,28 +325,41 @@ __global__ void __launch_bounds__(kCopyThreads) kv_evict_copy_kernel(const Evict
     }
     return (static_cast<int64_t>(blk) * p.Hkv + g) * kBS + slot % kBS;
   };
-  const int vecs = n * 2 * p.ch;
-  for (int x0 = threadIdx.x; x0 < vecs; x0 += kCopyThreads * kCopyVecs) {
-    uint4 w[kCopyVecs];
-    int64_t to[kCopyVecs];
-#pragma unroll
-    for (int u = 0; u < kCopyVecs; ++u) {
-      const int x = x0 + u * kCopyThreads;
-      to[u] = -1;
-      if (x >= vecs) continue;
-      const int i = x / (2 * p.ch), c = x % (2 * p.ch);
-      const int from_slot = kept[i];
-      if (from_slot < 0) continue;
-      const int64_t from = place(bt, p.max_blocks, from_slot), dst = place(dt, p.dst_blocks, r0 + i);
-      if (from < 0 || dst < 0) continue;
-      w[u] = (c < p.ch ? p.kc : p.vc)[from * p.ch + c % p.ch];
-      to[u] = dst * p.ch + c % p.ch;
-      if (c == 0) p.acc[dst] = p.acc[from];
+  if (threadIdx.x < kCopyRows) {
+    const int i = threadIdx.x;
+    int64_t f = -1, d = -1;
+    const int slot = r0 + i < p.keep ? kept[i] : -1;
+    if (slot >= 0) {
+      f = place(p.bt + b * p.bt_stride, p.max_blocks, slot);
+      d = place(p.dst + b * p.dst_stride, p.dst_blocks, r0 + i);
     }
+    if (f >= 0 && d >= 0)
+      p.acc[d] = p.acc[f];
+    else
+      f = -1;
+    from[i] = f;
+    to[i] = d;
+  }
+  __syncthreads();
+  constexpr int kRowsPerStep = kCopyThreads / CH;
+  const int c = threadIdx.x % CH, i0 = threadIdx.x / CH;
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+    const uint4* src = half ? p.vc : p.kc;
+    uint4* dst = half ? p.vd : p.kd;
+#pragma unroll 1
+    for (int i = i0; i < kCopyRows; i += kRowsPerStep * kCopyVecs) {
+      uint4 w[kCopyVecs];
 #pragma unroll
-    for (int u = 0; u < kCopyVecs; ++u) {
-      const int x = x0 + u * kCopyThreads;
-      if (to[u] >= 0) (x % (2 * p.ch) < p.ch ? p.kd : p.vd)[to[u]] = w[u];
+      for (int u = 0; u < kCopyVecs; ++u) {
+        const int r = i + u * kRowsPerStep;
+        if (r < kCopyRows && from[r] >= 0) w[u] = src[from[r] * CH + c];
+      }
+#pragma unroll
+      for (int u = 0; u < kCopyVecs; ++u) {
+        const int r = i + u * kRowsPerStep;
+        if (r < kCopyRows && from[r] >= 0) dst[to[r] * CH + c] = w[u];
+      }
     }
   }
 }
@@ -382,11 +406,13 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t stream) {
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kv_evict_select_kernel, p, nc);
   if (e != cudaSuccess) return e;
-  const int rows = kCopyThreads * kCopyVecs * 4 / (2 * p.ch);
-  dim3 grid(static_cast<unsigned>((a.keep + rows - 1) / rows), static_cast<unsigned>(a.cache.Hkv),
-            static_cast<unsigned>(a.B));
-  kv_evict_copy_kernel<<<grid, kCopyThreads, 0, stream>>>(p, rows);
-  return cudaGetLastError();
+  cfg.gridDim = dim3(static_cast<unsigned>((a.keep + kCopyRows - 1) / kCopyRows),
+                     static_cast<unsigned>(a.cache.Hkv), static_cast<unsigned>(a.B));
+  cfg.blockDim = dim3(kCopyThreads);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  return p.ch == 16 ? cudaLaunchKernelEx(&cfg, kv_evict_copy_kernel<16>, p)
+                    : cudaLaunchKernelEx(&cfg, kv_evict_copy_kernel<8>, p);
 }
 
 cudaError_t launch_tree_accept(const AcceptArgs& a, cudaStream_t stream) {

@@ -17,8 +17,10 @@
 // head, row pair) is its draft tiles followed by its context tiles, the items
 // are laid end to end, and CTA c of n takes tiles [total c / n, total (c+1) / n).
 // An item inside one run is written at once; one that is cut leaves partials
-// (normalised rows and log2 LSE; at most two per CTA), merged in order by
-// whichever piece finishes last, so results do not depend on the timing.
+// (normalised rows and log2 LSE; at most two per CTA), which a second launch
+// merges in order, so results do not depend on the timing.  That launch spreads
+// the rows over the whole GPU: left to the piece that finished last, the merge of
+// 108 rows took as long as the attention (16 x 27 drafts, 118 us against ~60).
 //
 // Warps: 0 streams all tiles (TMA: context tiles through the block table, draft
 // tiles from k_new / v_new, or from the cache's blocks when they are there
@@ -84,7 +86,6 @@ struct Bars {
   uint64_t o_done[2];  // [row tile] (NT = 2) or, alternating, [tile parity] (NT = 1)
   uint64_t draft_in[4];  // a draft tile's K and V have landed in K stage ks (and the tile's V stage)
   uint64_t mask_full[2], mask_empty[2];
-  uint64_t piece_full, piece_go;  // an item's piece is written; whether it was the last
   uint64_t drained;
   int64_t lo, hi, total, bstart;  // this CTA's run of tiles; the first item's sequence starts at bstart
   int b0;
@@ -92,7 +93,6 @@ struct Bars {
   uint32_t bad[2][8];  // drafts whose V holds a non-finite element
   uint32_t tmem_base;
   int abort;
-  int last;
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block outgrew its shared-memory slot");
 
@@ -125,9 +125,15 @@ struct TreeParams {
   float* part_o;    // [2 n][slot_rows][D]
   float* part_lse;  // [2 n][slot_rows]
   int slot_rows;
-  unsigned long long* count;  // [B * Hkv * MP] (generation << 32) | pieces done
-  uint32_t gen;
+  struct CutItem* cuts;  // [n] the item that starts in CTA c's run and goes on past it
   uint32_t* status;
+};
+
+// pieces == 0: no item of the kind
+struct CutItem {
+  int b, g, node0, rows;
+  int pieces;         // in CTAs c, c + 1, ...
+  int first_is_head;  // CTA c's run begins with it
 };
 
 // A sequence that does not fit its table, or is idle, has no context and no drafts.
@@ -220,57 +226,67 @@ __device__ __forceinline__ const uint16_t* draft_row(const TreeParams& p, bool i
   return row < 0 ? nullptr : (is_v ? p.vc : p.kc) + row * D;
 }
 
-// The partial slot of an item's piece in CTA c: a CTA's first segment uses
+// The runs.  The partial slot of an item's piece in CTA c: a CTA's first segment uses
 // slot 2c, a later one (only its last can be cut) slot 2c + 1.
 __device__ __forceinline__ int64_t run_lo(int64_t total, int n, int c) { return total * c / n; }
 __device__ __forceinline__ int run_of(int64_t total, int n, int64_t tile) {
   return static_cast<int>(((tile + 1) * n - 1) / total);
 }
 
-// Merge an item's pieces (CTAs c0 .. c0 + np - 1): out = sum_c 2^(lse_c - M)
-// out_c / sum_c 2^(lse_c - M), four dims a thread and step.
+// The merge: out = sum_c 2^(lse_c - M) out_c / sum_c 2^(lse_c - M) over a cut
+// item's pieces.  grid (CTAs of the main launch, groups of kMergeRows rows);
+// a warp per row (D = 128: four dims a lane) or per two rows (D = 64).  Waits for
+// the main launch to finish, then takes ~2 us.
+constexpr int kMergeThreads = 128, kMergeRows = 16;
 template <int D>
-__device__ __forceinline__ void merge_item(const TreeParams& p, const Seg& s, int node0, int rows, int c0, int np,
-                                           bool first_is_head, int tid, int nthr) {
-  constexpr int V4 = D / 4;
-  for (int x = tid; x < rows * V4; x += nthr) {
-    const int r = x / V4, d = (x % V4) * 4;
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kLanes = D / 4;  // lanes per row
+  constexpr int kPer = kMergeThreads / kLanes;
+  const int c0 = blockIdx.x;
+  const CutItem it = p.cuts[c0];
+  const int lane = threadIdx.x % kLanes;
+  for (int r = blockIdx.y * kMergeRows + threadIdx.x / kLanes; r < min(it.rows, (static_cast<int>(blockIdx.y) + 1) * kMergeRows);
+       r += kPer) {
+    if (it.pieces == 0) return;
     auto slot_row = [&](int c) {
-      const int slot = 2 * (c0 + c) + ((c == 0 && !first_is_head) ? 1 : 0);
+      const int slot = 2 * (c0 + c) + ((c == 0 && !it.first_is_head) ? 1 : 0);
       return static_cast<int64_t>(slot) * p.slot_rows + r;
     };
-    const float l0 = __ldcg(p.part_lse + slot_row(0));
+    const float l0 = p.part_lse[slot_row(0)];
     const bool absent = __float_as_uint(l0) == kAbsent;
     float M = l0;
     bool any = l0 != -INFINITY;  // a NaN counts: it has to reach the row
-    for (int c = 1; c < np; ++c) {
-      const float l = __ldcg(p.part_lse + slot_row(c));
+#pragma unroll 8
+    for (int c = 1; c < it.pieces; ++c) {
+      const float l = p.part_lse[slot_row(c)];
       M = fmaxf(M, l);
       any |= l != -INFINITY;
     }
     float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f, ws = 0.f;
     const bool empty = absent || !any;
     if (!empty) {
-#pragma unroll 4
-      for (int c = 0; c < np; ++c) {
-        const float l = __ldcg(p.part_lse + slot_row(c));
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot_row(c) * D + d));
-        if (l == -INFINITY) continue;
-        const float w = fast_exp2(l - M);
+#pragma unroll 8
+      for (int c = 0; c < it.pieces; ++c) {
+        const float l = p.part_lse[slot_row(c)];
+        const float4 o = *reinterpret_cast<const float4*>(p.part_o + slot_row(c) * D + lane * 4);
+        const float w = l == -INFINITY ? 0.f : fast_exp2(l - M);
+        const bool use = l != -INFINITY;  // a piece that saw nothing holds zeros
         ws += w;
-        a0 = fmaf(w, o.x, a0), a1 = fmaf(w, o.y, a1), a2 = fmaf(w, o.z, a2), a3 = fmaf(w, o.w, a3);
+        a0 = fmaf(w, use ? o.x : 0.f, a0), a1 = fmaf(w, use ? o.y : 0.f, a1);
+        a2 = fmaf(w, use ? o.z : 0.f, a2), a3 = fmaf(w, use ? o.w : 0.f, a3);
       }
     }
     const float inv = empty ? 0.f : 1.f / ws;
-    const int t = node0 + r / p.G, h = s.g * p.G + r % p.G;
-    const int64_t ob = s.b * p.out_stride[0] + h * p.out_stride[1] + t * p.out_stride[2] + d;
+    const int t = it.node0 + r / p.G, h = it.g * p.G + r % p.G;
+    const int64_t ob = it.b * p.out_stride[0] + h * p.out_stride[1] + t * p.out_stride[2] + lane * 4;
     if (p.out_bf16)
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ob) =
           make_uint2(pack_bf16x2(a0 * inv, a1 * inv), pack_bf16x2(a2 * inv, a3 * inv));
     else
       *reinterpret_cast<float4*>(static_cast<float*>(p.out) + ob) = make_float4(a0 * inv, a1 * inv, a2 * inv, a3 * inv);
-    if (d == 0 && p.lse != nullptr)
-      p.lse[(static_cast<int64_t>(s.b) * p.Hq + h) * p.T + t] =
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[(static_cast<int64_t>(it.b) * p.Hq + h) * p.T + t] =
           empty ? -INFINITY : (M + __log2f(ws)) * 0.6931471805599453f;
   }
 }
@@ -304,8 +320,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       mbar_init(&bars->v_empty[s], 1);
     }
     for (int s = 0; s < 4; ++s) mbar_init(&bars->draft_in[s], 1);
-    mbar_init(&bars->piece_full, 4 * NT);
-    mbar_init(&bars->piece_go, 1);
     mbar_init(&bars->drained, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->mask_full[s], 1);
@@ -314,6 +328,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     bars->abort = 0;
     fence_mbar_init();
   }
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 0) {
     // the call's tiles, this CTA's run of them, and the sequence it starts in
     const int64_t items = static_cast<int64_t>(p.Hkv) * p.MP;
@@ -360,6 +375,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       bars->bstart = run;
       bars->b0 = b0;
       bars->n_cta = n;
+      p.cuts[c].pieces = 0;  // unless the softmax below finds one
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
@@ -697,7 +713,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     bool ok = true;
     bool more = cur.next(s);
     if (more) load_q(s);
-    int j = 0, round = 0, pieces = 0;
+    int j = 0, round = 0;
     while (ok && more) {
       const int node = (s.m * NT + t) * p.tb + row / p.G;
       const bool mine = row < p.RT && node < p.T;               // the row exists
@@ -942,46 +958,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         if (lane == 0) mbar_arrive(&bars->mask_empty[mb]);
         ++round;
       }
-      if (!whole) {
-        // Count this piece in; the piece that completes the item takes the count
-        // back to zero and merges.  A word of another generation (another call,
-        // or whatever the workspace held) reads as zero; a captured graph replays
-        // its own generation with other lengths, hence the way back to zero.
-        const int c0 = run_of(bars->total, bars->n_cta, s.item0);
-        const int np = run_of(bars->total, bars->n_cta, s.item0 + s.tiles - 1) - c0 + 1;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->piece_full);
-        if (tid < 32 && !__all_sync(0xffffffffu, mbar_wait(&bars->piece_full, pieces & 1, abort, p.status))) {
-          ok = false;
-          break;
-        }
-        if (tid == 0) {
-          __threadfence();
-          unsigned long long* w = p.count + (static_cast<int64_t>(s.b) * p.Hkv + s.g) * p.MP + s.m;
-          const unsigned long long tag = static_cast<unsigned long long>(p.gen) << 32;
-          unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(w), now;
-          for (;;) {
-            now = (old >> 32) == p.gen ? old + 1 : tag + 1;
-            const unsigned long long seen = atomicCAS(w, old, now);
-            if (seen == old) break;
-            old = seen;
-          }
-          const bool last = (now & 0xffffffffull) == static_cast<unsigned long long>(np);
-          if (last) *w = tag;
-          bars->last = last;
-          mbar_arrive(&bars->piece_go);
-        }
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->piece_go, pieces & 1, abort, p.status))) {
-          ok = false;
-          break;
-        }
-        ++pieces;
-        if (bars->last) {
-          __threadfence();
-          const int node0 = s.m * NT * p.tb;
-          merge_item<D>(p, s, node0, min(p.T - node0, NT * p.tb) * p.G, c0, np,
-                        run_lo(bars->total, bars->n_cta, c0) == s.item0, tid, C::kSoft);
-        }
+      if (!whole && s.t0 == 0 && tid == 0) {  // cut, and it starts here
+        const int node0 = s.m * NT * p.tb;
+        CutItem it;
+        it.b = s.b, it.g = s.g, it.node0 = node0;
+        it.rows = min(p.T - node0, NT * p.tb) * p.G;
+        it.pieces = run_of(bars->total, bars->n_cta, s.item0 + s.tiles - 1) - static_cast<int>(blockIdx.x) + 1;
+        it.first_is_head = s.item0 == bars->lo;
+        p.cuts[blockIdx.x] = it;
       }
       s = s_next;
       more = more_next;
@@ -1025,19 +1009,30 @@ cudaError_t launch(const TreeArgs& a, TreeParams& p, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   kern<<<static_cast<unsigned>(a.n_cta), C::kThreads, C::kSmemBytes, stream>>>(mq, mk, mv, mkn, mvn, p);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // in place on the SMs as the main launch's CTAs leave
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.n_cta), static_cast<unsigned>((p.slot_rows + kMergeRows - 1) / kMergeRows));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, p);
 }
 
 }  // namespace
 
-// Partials of two cut items per CTA (their rows), then one 8-byte count per item.
-size_t tree_partial_bytes(int64_t B, int64_t Hkv, int64_t T, int64_t G, int D, int n_cta) {
+// Partials of two cut items per CTA (their rows), and a CutItem per CTA.
+size_t tree_partial_bytes(int64_t T, int64_t G, int D, int n_cta) {
   if (T == 0 || G == 0 || G > kBM) return 0;
   const int64_t group = static_cast<int64_t>(tree_nt(T, G)) * tile_drafts(T, G);  // drafts per item
   const size_t rows = static_cast<size_t>(2) * n_cta * group * G;
   const size_t parts = (rows * (D + 1) * sizeof(float) + 255) & ~size_t(255);
-  const size_t items = static_cast<size_t>(B) * Hkv * ((T + group - 1) / group);
-  return parts + ((items * sizeof(unsigned long long) + 255) & ~size_t(255));
+  return parts + ((n_cta * sizeof(CutItem) + 255) & ~size_t(255));
 }
 
 cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream) {
@@ -1081,8 +1076,7 @@ cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream) {
   p.part_o = static_cast<float*>(a.partials);
   p.part_lse = p.part_o + rows * a.cache.D;
   const size_t parts = (rows * (a.cache.D + 1) * sizeof(float) + 255) & ~size_t(255);
-  p.count = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(a.partials) + parts);
-  p.gen = a.gen;
+  p.cuts = reinterpret_cast<CutItem*>(static_cast<uint8_t*>(a.partials) + parts);
   p.status = a.status;
   if (a.cache.D == 64) return nt == 1 ? launch<64, 1>(a, p, stream) : launch<64, 2>(a, p, stream);
   if (a.cache.D == 128) return nt == 1 ? launch<128, 1>(a, p, stream) : launch<128, 2>(a, p, stream);

@@ -25,6 +25,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -38,14 +39,14 @@ constexpr int kBN = 128;       // query rows per chunk, at most
 constexpr int kBS = 16;
 constexpr int kBoxBytes = kBM * 128;
 constexpr int kThreads = 384;
-constexpr int kLseRing = 4;
+constexpr int kLseRing = 2;
 
 template <int D>
 struct Cfg {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = kBM * D * 2;
   static constexpr int KS = 2;                // K pair stages
-  static constexpr int QS = D == 64 ? 4 : 2;  // query chunk stages
+  static constexpr int QS = D == 64 ? 4 : 3;  // query chunk stages
   static constexpr int kOffK = 0;
   static constexpr int kOffQ = kOffK + KS * 2 * kTileBytes;
   static constexpr int kOffLse = kOffQ + QS * kTileBytes;  // [kLseRing][kBN] negated log2 LSEs, -inf: no weight
@@ -443,10 +444,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* nl = lse_ring + sl * kBN;
         const bool masked = bars->odd[sl] != 0 || warp_tmin > t0;
         const int rel = max(0, min(tmin - t0, p.ct)) * p.G;  // columns >= rel see the key
-        for (int cc = 0; cc < cols; cc += 32) {
-          uint32_t sr[32];
-          tmem_ld32(tmem + lane_addr + (2 * t + buf) * 128 + cc, sr);
-          tmem_wait_ld(sr);
+        const uint32_t col = tmem + lane_addr + (2 * t + buf) * 128;
+        auto add32 = [&](const uint32_t (&sr)[32], int cc, auto masked_c) {
+          constexpr bool MASKED = decltype(masked_c)::value;
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             const float4 l4 = *reinterpret_cast<const float4*>(nl + cc + i);
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             f2_unpack(ffma2(f2_pack(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])), sc2, f2_pack(l4.z, l4.w)),
                       x2, x3);
             float w0 = fast_exp2(x0), w1 = fast_exp2(x1), w2 = fast_exp2(x2), w3 = fast_exp2(x3);
-            if (masked) {
+            if constexpr (MASKED) {
               // selected, not multiplied: whatever a column without weight holds stays out
               w0 = (cc + i >= rel && l4.x != -INFINITY) ? w0 : 0.f;
               w1 = (cc + i + 1 >= rel && l4.y != -INFINITY) ? w1 : 0.f;
@@ -465,6 +465,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             sum[(i >> 1) & 3] = fadd2(sum[(i >> 1) & 3], f2_pack(w0, w1));
             sum[((i >> 1) + 1) & 3] = fadd2(sum[((i >> 1) + 1) & 3], f2_pack(w2, w3));
+          }
+        };
+        if (!masked) {
+          // a whole chunk: the next 32 columns load while these are added (cr may
+          // be below 128 only with a column of padding, which is masked)
+          uint32_t sa[32], sb[32];
+          tmem_ld32(col, sa);
+          tmem_wait_ld(sa);
+          tmem_ld32(col + 32, sb);
+          add32(sa, 0, std::false_type());
+          tmem_wait_ld(sb);
+          tmem_ld32(col + 64, sa);
+          add32(sb, 32, std::false_type());
+          tmem_wait_ld(sa);
+          tmem_ld32(col + 96, sb);
+          add32(sa, 64, std::false_type());
+          tmem_wait_ld(sb);
+          add32(sb, 96, std::false_type());
+        } else {
+          for (int cc = 0; cc < cols; cc += 32) {
+            uint32_t sr[32];
+            tmem_ld32(col + cc, sr);
+            tmem_wait_ld(sr);
+            add32(sr, cc, std::true_type());
           }
         }
         tc_fence_before();

@@ -14,7 +14,7 @@ BIG = 1 << 30
 def test_workspace_size(L):
     size = lambda *a: L.paged_tree_workspace_size(*a, 64, 16, 128)  # noqa: E731  (batch, Hq, Hkv, T)
     assert size(4, 32, 8, 0) >= 256 and size(4, 32, 8, 8) % 256 == 0
-    assert size(64, 32, 8, 25) >= size(4, 32, 8, 25) >= size(4, 32, 8, 8)
+    assert size(64, 32, 8, 25) == size(4, 32, 8, 25) >= size(4, 32, 8, 8)
     assert size(4, 30, 8, 8) == 0 and size(-1, 32, 8, 8) == 0 and size(4, 32, 0, 8) == 0
     # the context's length does not matter: what is cut is bounded by the SMs
     a = L.paged_tree_workspace_size(4, 32, 8, 8, 100, 16, 128)
@@ -55,7 +55,7 @@ def test_paged_tree_rejects(L):
     assert call(c=_cache(H=4, D=96)) == UNSUPPORTED
     assert call(ws=None) == WORKSPACE
     assert call(ws=FAKE + 16) == WORKSPACE
-    assert call(ws_bytes=256) == WORKSPACE
+    assert call(ws_bytes=128) == WORKSPACE  # without a GPU there are no SMs to size partials for
     assert call(q=_t([2, 12, 0, 128]), out=_t([2, 12, 0, 128])) == OK  # no drafts: nothing launched
 
 
