@@ -708,7 +708,7 @@ attn_status paged_tree_attn(const attn_tensor* q, const attn_tensor* k_new, cons
       if (k_new->shape[i] != want[i] || v_new->shape[i] != want[i]) return ATTN_ERR_INVALID_ARG;
   }
   if (T > kTreeMaxDrafts || B > 65535 || Hq > 65535 || Hq / cache->num_kv_heads > 128 ||
-      cache->num_blocks > 0x7fffffff)
+      cache->num_blocks * cache->num_kv_heads > 0x7fffffff)
     return ATTN_ERR_UNSUPPORTED;
   const size_t need = paged_tree_workspace_size(static_cast<int32_t>(B), static_cast<int32_t>(Hq),
                                                 cache->num_kv_heads, static_cast<int32_t>(T), max_blocks,
@@ -790,7 +790,8 @@ attn_status paged_attn_weights(const attn_tensor* q, const float* lse, const att
   if (Hq <= 0 || Hq % cache->num_kv_heads != 0) return ATTN_ERR_INVALID_ARG;
   if (!isfinite(scale) || (causal != 0 && causal != 1)) return ATTN_ERR_INVALID_ARG;
   if (max_blocks <= 0 || max_blocks > (1 << 24)) return ATTN_ERR_INVALID_ARG;
-  if (B > 65535 || Hq > 65535 || Hq / cache->num_kv_heads > 128 || T > (1 << 24) || cache->num_blocks > 0x7fffffff)
+  if (B > 65535 || Hq > 65535 || Hq / cache->num_kv_heads > 128 || T > (1 << 24) ||
+      cache->num_blocks * cache->num_kv_heads > 0x7fffffff)
     return ATTN_ERR_UNSUPPORTED;
   const size_t need = paged_attn_weights_workspace_size(static_cast<int32_t>(B), cache->num_kv_heads, max_blocks,
                                                         cache->block_size);

@@ -1104,7 +1104,18 @@ bool make_bf16_cache_map(CUtensorMap* map, void* base, int64_t num_blocks, int H
 }
 
 bool make_paged_map(CUtensorMap* map, void* base, int64_t num_blocks, int Hkv, int D) {
-  return make_cache_map(map, base, num_blocks, Hkv, D);
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;  // bytes
+  const cuuint32_t halves = static_cast<cuuint32_t>(D / 64);
+  const cuuint64_t dims[5] = {64, 8, halves, 2, static_cast<cuuint64_t>(num_blocks) * Hkv};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, 16 * row};
+  const cuuint32_t box[5] = {64, 8, halves, 2, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
 }
 
 bool make_rows_map(CUtensorMap* map, const View4& t, int64_t Hkv, int tokens) {

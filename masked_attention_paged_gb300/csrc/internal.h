@@ -168,7 +168,9 @@ cudaError_t launch_kv_append_chunk(const PrefillArgs& a, cudaStream_t stream);
 // the chunk's queries over the paged cache (tcgen05 kernel, paged instance)
 cudaError_t launch_paged_prefill_tc(const PrefillArgs& a, cudaStream_t stream);
 
-// the same for head dim 64 or 128
+// 5-D bf16 tensor map over one paged cache tensor [num_blocks, Hkv, 16, D] as (64
+// columns, 8 rows, half, row group, block * Hkv + head), D 64 or 128, contiguous:
+// a box is all 16 rows of one (block, head), laid out as paged_tile.cuh says
 bool make_paged_map(CUtensorMap* map, void* base, int64_t num_blocks, int Hkv, int D);
 
 // 5-D bf16 tensor map over a [B, H, T, D] view as (dim, head of the group, token,

@@ -10,8 +10,8 @@
 // 128 / G) drafts (row r: draft r / G, head r % G), one 5-D TMA box of q whatever
 // its strides; NT row tiles share every K/V tile (NT = 1 if one holds all drafts,
 // else 2).  What bounds it is HBM (a 128-key tile of K and V at D = 128 is 64 KB,
-// 1.4 us of an SM's share, against 0.6 us of softmax), until rows pass 256 a KV
-// head and the tensor cores and exponentials do.
+// 1.4 us of an SM's share), until rows pass 256 a KV head and the tensor cores and
+// exponentials do.
 //
 // Every SM takes an equal run of the call's K/V tiles: an item (sequence, KV
 // head, row pair) is its draft tiles followed by its context tiles, the items
@@ -22,14 +22,16 @@
 // the rows over the whole GPU: left to the piece that finished last, the merge of
 // 108 rows took as long as the attention (16 x 27 drafts, 118 us against ~60).
 //
-// Warps: 0 streams all tiles (TMA: context tiles through the block table, draft
+// Warps: 0-1 stream K and 2-3 V (TMA: context tiles through the block table, draft
 // tiles from k_new / v_new, or from the cache's blocks when they are there
-// already, shifted by the context's last partial block), 1 issues the MMAs, 2-3
+// already, shifted by the context's last partial block), 4 issues the MMAs, 6-7
 // build the ancestor masks, clean the drafts' V and append K and V from shared
-// memory, 4.. one warpgroup of softmax per row tile (thread r owns row r: TMEM
-// lane r).  With NT = 1 two score buffers let the next S run under the current
-// softmax.  P goes over its S as bf16 (relative rounding 2^-9; row sums are taken
-// in fp32 before it).
+// memory, 8-11 and 12-15 the softmax (thread r owns row r: TMEM lane r).  With NT =
+// 2 each warpgroup has a row tile.  With NT = 1 both have the same rows and take
+// the K/V tiles in turn, each with a score buffer, an output accumulator and a
+// running max and sum of its own, joined by the LSE rule when an item ends: one
+// warpgroup alone took 2.1 us a tile, more than the tile's bytes.  P goes over its
+// S as bf16 (relative rounding 2^-9; row sums are taken in fp32 before it).
 //
 // V rows past the context's end and rows of absent drafts are zeroed: P is 0
 // there, but 0 x NaN is not.  A draft's own V may hold infinities or NaN that
@@ -42,6 +44,8 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "paged_tile.cuh"
+#include "runs.cuh"
 
 namespace attn {
 namespace {
@@ -56,8 +60,7 @@ constexpr uint32_t kAbsent = 0x7fc0a5a5u;  // a partial's LSE for the row of an 
 
 template <int D, int NT>
 struct Cfg {
-  static constexpr int kThreads = 128 + 128 * NT;
-  static constexpr int kSoft = 128 * NT;      // softmax threads
+  static constexpr int kThreads = 512;
   static constexpr int kMaxT = NT == 1 ? 128 : kTreeMaxDrafts;
   static constexpr int kWords = kMaxT / 32;
   static constexpr int kBoxes = D / 64;
@@ -71,25 +74,27 @@ struct Cfg {
   static constexpr int kOffV = kOffK + KS * kTileBytes;
   static constexpr int kOffAnc = kOffV + VS * kTileBytes;  // [2][kMaxT][kWords] ancestor bits
   static constexpr int kOffPar = kOffAnc + 2 * kMaxT * kWords * 4;  // [kMaxT] parents
-  static constexpr int kOffBar = kOffPar + kMaxT * 4;
+  static constexpr int kOffXch = kOffPar + kMaxT * 4;  // NT = 1: [2][kBM] running max and sum
+  static constexpr int kOffBar = kOffXch + (NT == 1 ? 2 * kBM * 8 : 0);
   static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-  static constexpr uint32_t kColO = 256;  // O_t at kColO + t * D; scores below
-  // NT = 2: 384 threads launched with 168 registers, split as in attn_tc.cu
-  static constexpr int kRegsCtl = 88, kRegsSoft = 208;
+  static constexpr uint32_t kColO = 256;  // O of warpgroup w at kColO + w * D; its scores at w * 128
+  // 512 threads launched with 128 registers; 256 x 72 + 256 x 184 = 65536
+  static constexpr int kRegsCtl = 72, kRegsSoft = 184;
 };
 
 struct Bars {
   uint64_t q_full[2];
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_full[2];  // [row tile] (NT = 2) or [score buffer] (NT = 1)
-  uint64_t o_done[2];  // [row tile] (NT = 2) or, alternating, [tile parity] (NT = 1)
+  uint64_t s_full[2], p_full[2], o_done[2];  // [warpgroup]
+  uint64_t xch_full[2];  // NT = 1: a warpgroup's running max and sum are in smem
+  uint64_t o_free;       // NT = 1: both warpgroups have read both accumulators
   uint64_t draft_in[4];  // a draft tile's K and V have landed in K stage ks (and the tile's V stage)
   uint64_t mask_full[2], mask_empty[2];
   uint64_t drained;
-  int64_t lo, hi, total, bstart;  // this CTA's run of tiles; the first item's sequence starts at bstart
-  int b0;
-  int n_cta;
+  Runs runs;
+  int64_t lo, hi;        // this CTA's run of tiles, and the place of its first:
+  int b0, item0, tile0;  // sequence, item (KV head, row group) in it, tile in that
   uint32_t bad[2][8];  // drafts whose V holds a non-finite element
   uint32_t tmem_base;
   int abort;
@@ -129,7 +134,8 @@ struct TreeParams {
   uint32_t* status;
 };
 
-// pieces == 0: no item of the kind
+// pieces == 0: no item of the kind.  A CTA's first segment uses partial slot 2c, a
+// later one (only its last can be cut) slot 2c + 1.
 struct CutItem {
   int b, g, node0, rows;
   int pieces;         // in CTAs c, c + 1, ...
@@ -164,40 +170,46 @@ struct Seg {
 
 struct Cursor {
   const TreeParams& p;
-  int64_t pos, hi, bstart;
-  int b, tiles, ctx;
+  int64_t pos, hi;
+  int b, item, t, tiles, ctx;
   bool ok;
   __device__ Cursor(const TreeParams& prm, const Bars* bars)
-      : p(prm), pos(bars->lo), hi(bars->hi), bstart(bars->bstart), b(bars->b0) {
+      : p(prm), pos(bars->lo), hi(bars->hi), b(bars->b0), item(bars->item0), t(bars->tile0) {
     if (pos < hi) tiles = seq_tiles(p, b, ctx, ok);
   }
   __device__ bool next(Seg& s) {
     if (pos >= hi) return false;
-    const int items = p.Hkv * p.MP;
-    while (pos >= bstart + static_cast<int64_t>(tiles) * items) {
-      bstart += static_cast<int64_t>(tiles) * items;
-      ++b;
-      tiles = seq_tiles(p, b, ctx, ok);
+    if (t == tiles) {  // the item is done: the next one, or the next sequence
+      t = 0;
+      if (++item == p.Hkv * p.MP) {
+        item = 0;
+        tiles = seq_tiles(p, ++b, ctx, ok);
+      }
     }
-    const int64_t local = pos - bstart;
-    const int item = static_cast<int>(local / tiles);
-    s.t0 = static_cast<int>(local - static_cast<int64_t>(item) * tiles);
-    s.t1 = static_cast<int>(min(static_cast<int64_t>(tiles), s.t0 + (hi - pos)));
     s.b = b;
     s.g = item / p.MP;
     s.m = item % p.MP;
+    s.t0 = t;
+    s.t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t + (hi - pos)));
     s.tiles = tiles;
     s.ctx = ctx;
     s.ok = ok;
-    s.item0 = bstart + static_cast<int64_t>(item) * tiles;
-    pos += s.t1 - s.t0;
+    s.item0 = pos - t;
+    pos += s.t1 - t;
+    t = s.t1;
     return true;
   }
 };
 
-// byte offset of 16-byte chunk ch of row r in a tile (128-byte swizzle, 64-column boxes)
-__device__ __forceinline__ uint32_t tile_off(int r, int ch) {
-  return static_cast<uint32_t>((ch >> 3) * kBoxBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+// Layout of tile `tile`: fresh drafts arrive as 64-column boxes of rows, cached
+// rows block by block.
+struct Layout {
+  uint32_t half, group;  // bytes to the next 64 columns, to the next 8 rows
+};
+template <int D>
+__device__ __forceinline__ Layout tile_layout(const TreeParams& p, int tile) {
+  if (tile < p.ntd && p.k_new != nullptr) return {static_cast<uint32_t>(kBoxBytes), 1024u};
+  return {PagedTile<D>::kHalf, PagedTile<D>::kGroup};
 }
 
 // bf16 pair with its non-finite elements cleared; `any` reports them
@@ -224,13 +236,6 @@ __device__ __forceinline__ const uint16_t* draft_row(const TreeParams& p, bool i
                 : p.k_new + b * p.kn_stride[0] + g * p.kn_stride[1] + j * p.kn_stride[2];
   const int64_t row = cache_row(p, b, g, ctx + j);
   return row < 0 ? nullptr : (is_v ? p.vc : p.kc) + row * D;
-}
-
-// The runs.  The partial slot of an item's piece in CTA c: a CTA's first segment uses
-// slot 2c, a later one (only its last can be cut) slot 2c + 1.
-__device__ __forceinline__ int64_t run_lo(int64_t total, int n, int c) { return total * c / n; }
-__device__ __forceinline__ int run_of(int64_t total, int n, int64_t tile) {
-  return static_cast<int>(((tile + 1) * n - 1) / total);
 }
 
 // The merge: out = sum_c 2^(lse_c - M) out_c / sum_c 2^(lse_c - M) over a cut
@@ -312,19 +317,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       mbar_init(&bars->s_full[t], 1);
       mbar_init(&bars->p_full[t], 4);
       mbar_init(&bars->o_done[t], 1);
+      mbar_init(&bars->xch_full[t], 4);
+      mbar_init(&bars->mask_full[t], 1);
+      mbar_init(&bars->mask_empty[t], 8);
     }
     for (int s = 0; s < 4; ++s) {
-      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->k_full[s], 2);  // two producer warps each
       mbar_init(&bars->k_empty[s], 1);
-      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->v_full[s], 2);
       mbar_init(&bars->v_empty[s], 1);
+      mbar_init(&bars->draft_in[s], 4);
     }
-    for (int s = 0; s < 4; ++s) mbar_init(&bars->draft_in[s], 1);
+    mbar_init(&bars->o_free, 8);
     mbar_init(&bars->drained, 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars->mask_full[s], 1);
-      mbar_init(&bars->mask_empty[s], 4 * NT);
-    }
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -332,23 +337,27 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   if (warp == 0) {
     // the call's tiles, this CTA's run of them, and the sequence it starts in
     const int64_t items = static_cast<int64_t>(p.Hkv) * p.MP;
-    int64_t total = 0;
-    for (int b = lane; b < p.B; b += 32) {
-      int ctx;
-      bool ok;
-      total += seq_tiles(p, b, ctx, ok) * items;
-      if (blockIdx.x == 0 && !ok && p.ctx_lens[b] >= 0) report(p.status, kStatusBounds);
+    int64_t total = 0, mine0 = 0;
+    for (int base = 0; base < p.B; base += 32) {
+      int64_t mine = 0;
+      if (base + lane < p.B) {
+        int ctx;
+        bool ok;
+        mine = seq_tiles(p, base + lane, ctx, ok) * items;
+        if (blockIdx.x == 0 && !ok && p.ctx_lens[base + lane] >= 0) report(p.status, kStatusBounds);
+      }
+      if (base == 0) mine0 = mine;
+      total += mine;
     }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
-    const int n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    const Runs runs = Runs::make(total, gridDim.x);
     const int c = static_cast<int>(blockIdx.x);
-    const int64_t lo = c < n ? run_lo(total, n, c) : 0, hi = c < n ? run_lo(total, n, c + 1) : 0;
+    const int64_t lo = c < runs.n ? runs.lo(c) : 0, hi = c < runs.n ? runs.lo(c + 1) : 0;
     int64_t run = 0;
-    int b0 = 0;
     for (int base = 0; base < p.B && lo < hi; base += 32) {
-      int64_t mine = 0;
-      if (base + lane < p.B) {
+      int64_t mine = base == 0 ? mine0 : 0;
+      if (base > 0 && base + lane < p.B) {
         int ctx;
         bool ok;
         mine = seq_tiles(p, base + lane, ctx, ok) * items;
@@ -361,26 +370,27 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       }
       const uint32_t past = __ballot_sync(0xffffffffu, run + incl > lo);
       if (past != 0) {
-        const int l = __ffs(past) - 1;
-        b0 = base + l;
-        run += __shfl_sync(0xffffffffu, incl - mine, l);
+        if (lane == __ffs(past) - 1) {
+          const int64_t local = lo - run - (incl - mine), tiles = div_pos(mine, items);
+          bars->b0 = base + lane;
+          bars->item0 = static_cast<int>(div_pos(local, tiles));
+          bars->tile0 = static_cast<int>(local - bars->item0 * tiles);
+        }
         break;
       }
       run += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) {
+      bars->runs = runs;
       bars->lo = lo;
       bars->hi = hi;
-      bars->total = total;
-      bars->bstart = run;
-      bars->b0 = b0;
-      bars->n_cta = n;
       p.cuts[c].pieces = 0;  // unless the softmax below finds one
+      tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
   }
-  if (warp == 1) {
+  if (warp == 4) {
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
   }
@@ -395,33 +405,39 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  if constexpr (NT == 2) {
-    if (warp < 4) regs_dec<C::kRegsCtl>();
-  }
-  if (warp == 0) {
+  if (warp < 8) regs_dec<C::kRegsCtl>();
+  if (warp < 4) {
     // ------------------------------------------------------------ K/V tiles
-    // lane i < 8 owns block i of a context tile: its 64-column boxes of K and of
-    // V.  A draft tile's data go to the drafts' warps first (draft_in), which
-    // hand the stages on.
+    // warps 0, 1 the halves of K, 2, 3 of V; lane i < 4 owns block 4 (warp & 1) + i
+    // of a tile, its id read a tile ahead.  A draft tile's data go to the drafts'
+    // warps first (draft_in, all four producers' arrivals), which hand the stages on.
+    const bool is_v = warp >= 2;
+    const int S = is_v ? C::VS : C::KS;  // this operand's stages
+    const void* map = is_v ? static_cast<const void*>(&tm_v) : &tm_k;
+    const void* map_new = is_v ? static_cast<const void*>(&tm_vn) : &tm_kn;
+    uint64_t* full = is_v ? bars->v_full : bars->k_full;
+    uint64_t* empty = is_v ? bars->v_empty : bars->k_empty;
+    uint8_t* base = smem + (is_v ? C::kOffV : C::kOffK);
+    const int place = (warp & 1) * kWarpBlocks + lane;
     Cursor cur(p, bars);
     Seg s;
-    int j = 0, issued = 0;
+    int j = 0, issued = 0, st = 0, ks = 0;  // st, ks: tile j's stage, and its K stage
+    uint32_t ph = 1u;                       // parity of the stage's last release
     bool ok = true;
     while (ok && cur.next(s)) {
       const int32_t* bt_row = p.bt + static_cast<int64_t>(s.b) * p.bt_stride;
-      const int off = draft_off(p, s.ctx);
       auto block_id = [&](int tile) {
-        if (tile >= s.t1) return -1;
-        int first, blocks;  // the tile's blocks
+        if (tile >= s.t1 || lane >= kWarpBlocks) return -1;
+        int blk, end;  // the block, and where the tile's kind of blocks ends
         if (tile < ntd) {
           if (p.k_new != nullptr || !s.ok) return -1;
-          first = s.ctx / kBS + tile * (kBN / kBS);
-          blocks = (p.T + off + kBS - 1) / kBS - tile * (kBN / kBS);
+          blk = s.ctx / kBS + tile * kTileBlocks + place;
+          end = (s.ctx + p.T + kBS - 1) / kBS;
         } else {
-          first = (tile - ntd) * (kBN / kBS);
-          blocks = (s.ctx + kBS - 1) / kBS - first;
+          blk = (tile - ntd) * kTileBlocks + place;
+          end = (s.ctx + kBS - 1) / kBS;
         }
-        return lane < min(kBN / kBS, blocks) ? bt_row[first + lane] : -1;
+        return blk < end ? bt_row[blk] : -1;
       };
       int id_next = block_id(s.t0);
       for (int tile = s.t0; tile < s.t1; ++tile, ++j) {
@@ -431,86 +447,59 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           report(p.status, kStatusBounds);
           id = -1;
         }
-        const int ks = j % C::KS, vs = j % C::VS;
-        uint8_t* kt = smem + C::kOffK + ks * C::kTileBytes;
-        uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * (kBS * D * 2);
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->k_empty[ks], ((j / C::KS) & 1) ^ 1, abort, p.status))) {
+        uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * (kBS * D * 2);
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ph, abort, p.status))) {
           ok = false;
           break;
         }
         const bool draft = tile < ntd;
-        const bool fresh = draft && p.k_new != nullptr;  // one box of k_new and one of v_new per 64 columns
-        if (draft && !__all_sync(0xffffffffu,
-                                 mbar_wait(&bars->v_empty[vs], ((j / C::VS) & 1) ^ 1, abort, p.status))) {
-          ok = false;
-          break;
-        }
-        uint64_t* k_bar = draft ? &bars->draft_in[ks] : &bars->k_full[ks];
-        uint64_t* v_bar = draft ? &bars->draft_in[ks] : &bars->v_full[vs];
-        if (lane == 0)
-          mbar_arrive_expect_tx(k_bar, fresh ? 2u * static_cast<uint32_t>(p.new_box) * D * 2 : (draft ? 2u : 1u) * bytes);
+        // one box of k_new (v_new) per 64 columns, by the operand's first warp
+        const bool fresh = draft && p.k_new != nullptr && (warp & 1) == 0;
+        if (fresh) bytes = static_cast<uint32_t>(p.new_box) * D * 2;
+        uint64_t* bar = draft ? &bars->draft_in[ks] : &full[st];
+        uint8_t* dst = base + st * C::kTileBytes;
+        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
         __syncwarp();
-        if (fresh && lane == 0) {
-#pragma unroll
-          for (int x = 0; x < C::kBoxes; ++x) {
-            tma_load_5d(kt + x * kBoxBytes, &tm_kn, k_bar, x * 64, 0, tile * kBN, s.g, s.b);
-            tma_load_5d(vt + x * kBoxBytes, &tm_vn, k_bar, x * 64, 0, tile * kBN, s.g, s.b);
-          }
+        if (fresh) {
+          if (lane < C::kBoxes) tma_load_5d(dst + lane * kBoxBytes, map_new, bar, lane * 64, 0, tile * kBN, s.g, s.b);
+        } else {
+          load_block<D>(dst, place, map, bar, id, p.Hkv, s.g);
         }
-        if (id >= 0)
-#pragma unroll
-          for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_4d(kt + x * kBoxBytes + lane * 2048, &tm_k, k_bar, x * 64, 0, s.g, id);
-        if (!draft) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_empty[vs], ((j / C::VS) & 1) ^ 1, abort, p.status))) {
-            // this tile's K is in flight: let it land
-            if (lane == 0) drain_wait(k_bar, (j / C::KS) & 1);
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(v_bar, bytes);
-          __syncwarp();
-        }
-        if (id >= 0)
-#pragma unroll
-          for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_4d(vt + x * kBoxBytes + lane * 2048, &tm_v, v_bar, x * 64, 0, s.g, id);
         issued = j + 1;
+        if (++st == S) st = 0, ph ^= 1u;
+        if (++ks == C::KS) ks = 0;
       }
     }
     if (lane == 0 && *abort) {
-      // let every copy in flight land before the CTA exits: those of the last
-      // tiles, and of a draft tile that nobody took over (a wait on a barrier
-      // without copies runs out or passes)
-      for (int x = max(0, issued - C::KS); x < issued; ++x) drain_wait(&bars->k_full[x % C::KS], (x / C::KS) & 1);
-      for (int x = max(0, issued - C::VS); x < issued; ++x) drain_wait(&bars->v_full[x % C::VS], (x / C::VS) & 1);
+      // let every copy in flight land before the CTA exits (a wait on a barrier
+      // without copies, as a draft tile's that nobody took over, runs out or passes)
+      for (int x = max(0, issued - S); x < issued; ++x) drain_wait(&full[x % S], (x / S) & 1);
     }
-  } else if (warp == 1) {
+  } else if (warp == 4) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc_o = idesc_bf16_f32(kBM, D, false, true);
-      auto s_col = [&](int t, int j) { return NT == 1 ? static_cast<uint32_t>((j & 1) * 128) : t * 128u; };
-      auto issue_s = [&](int t, int j, int keys) {  // S = Q_t K_j^T
+      // w: the warpgroup whose scores and accumulator these are
+      auto issue_s = [&](int w, int j, int keys, Layout l) {  // S_w = Q K_j^T
         const uint32_t idesc_s = idesc_bf16_f32(kBM, keys, false, false);
-        const uint32_t qa = smem_u32(smem + C::kOffQ) + t * C::kTileBytes;
+        const uint32_t qa = smem_u32(smem + C::kOffQ) + (NT == 2 ? w * C::kTileBytes : 0);
         const uint32_t ka = smem_u32(smem + C::kOffK + (j % C::KS) * C::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
-          umma_bf16_ss(tmem + s_col(t, j), sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), idesc_s,
-                       kk > 0 ? 1u : 0u);
+          // 16 dims = 32 bytes of a 128-byte row
+          umma_bf16_ss(tmem + w * 128, sdesc_sw128(qa + (kk >> 2) * kBoxBytes + (kk & 3) * 32, 16, 1024),
+                       sdesc_sw128(ka + (kk >> 2) * l.half + (kk & 3) * 32, 16, l.group), idesc_s, kk > 0 ? 1u : 0u);
         }
-        umma_commit(&bars->s_full[NT == 1 ? (j & 1) : t]);
+        umma_commit(&bars->s_full[w]);
       };
-      auto issue_pv = [&](int t, int j, int keys, bool first) {  // O_t (+)= P V_j
+      auto issue_pv = [&](int w, int j, int keys, Layout l, bool first) {  // O_w (+)= P_w V_j
         const uint32_t va = smem_u32(smem + C::kOffV + (j % C::VS) * C::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
           if (kk * 16 < keys)
-            umma_bf16_ts(tmem + C::kColO + t * D, tmem + s_col(t, j) + kk * 8,
-                         sdesc_sw128(va + kk * 2048, kBoxBytes, 1024), idesc_o, (!first || kk > 0) ? 1u : 0u);
-        umma_commit(&bars->o_done[NT == 1 ? (j & 1) : t]);
+            umma_bf16_ts(tmem + C::kColO + w * D, tmem + w * 128 + kk * 8, sdesc_sw128(va + kk * 2 * l.group, l.half, l.group),
+                         idesc_o, (!first || kk > 0) ? 1u : 0u);
+        umma_commit(&bars->o_done[w]);
       };
       auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, abort, p.status); };
       auto wait_k = [&](int j) { return wait(&bars->k_full[j % C::KS], j / C::KS); };
@@ -522,27 +511,30 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       for (; ok && cur.next(s); ++seg) {
         const int n = s.t1 - s.t0;
         auto keys = [&](int x) { return tile_keys(p, s.t0 + x, s.ctx); };
+        auto lay = [&](int x) { return tile_layout<D>(p, s.t0 + x); };
         for (int t = 0; t < NT; ++t) ok = ok && wait(&bars->q_full[t], seg);
         if constexpr (NT == 1) {
-          // S runs two tiles ahead of PV
+          // tile j is warpgroup j & 1's; S runs two tiles ahead of PV
           for (int x = 0; ok && x < min(2, n); ++x) {
             ok = wait_k(j + x);
             if (!ok) break;
             tc_fence_after();
-            issue_s(0, j + x, keys(x));
+            issue_s((j + x) & 1, j + x, keys(x), lay(x));
             umma_commit(&bars->k_empty[(j + x) % C::KS]);
           }
+          // the accumulators of the segment before have been read
+          if (seg > 0) ok = ok && wait(&bars->o_free, seg - 1);
           for (int x = 0; ok && x < n; ++x, ++j) {
             ok = wait(&bars->p_full[j & 1], j >> 1) && wait_v(j);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(0, j, keys(x), x == 0);
+            issue_pv(j & 1, j, keys(x), lay(x), x < 2);
             umma_commit(&bars->v_empty[j % C::VS]);
             if (x + 2 < n) {
               ok = wait_k(j + 2);
               if (!ok) break;
               tc_fence_after();
-              issue_s(0, j + 2, keys(x + 2));
+              issue_s(j & 1, j + 2, keys(x + 2), lay(x + 2));
               umma_commit(&bars->k_empty[(j + 2) % C::KS]);
             }
           }
@@ -551,28 +543,28 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           ok = ok && wait_k(j);
           if (ok) {
             tc_fence_after();
-            issue_s(0, j, keys(0));
-            issue_s(1, j, keys(0));
+            issue_s(0, j, keys(0), lay(0));
+            issue_s(1, j, keys(0), lay(0));
             umma_commit(&bars->k_empty[j % C::KS]);
           }
           for (int x = 0; ok && x < n; ++x, ++j) {
             ok = wait(&bars->p_full[0], j) && wait_v(j);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(0, j, keys(x), x == 0);
+            issue_pv(0, j, keys(x), lay(x), x == 0);
             if (x + 1 < n) {
               ok = wait_k(j + 1);
               if (!ok) break;
               tc_fence_after();
-              issue_s(0, j + 1, keys(x + 1));
+              issue_s(0, j + 1, keys(x + 1), lay(x + 1));
             }
             ok = wait(&bars->p_full[1], j);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(1, j, keys(x), x == 0);
+            issue_pv(1, j, keys(x), lay(x), x == 0);
             umma_commit(&bars->v_empty[j % C::VS]);
             if (x + 1 < n) {
-              issue_s(1, j + 1, keys(x + 1));
+              issue_s(1, j + 1, keys(x + 1), lay(x + 1));
               umma_commit(&bars->k_empty[(j + 1) % C::KS]);
             }
           }
@@ -582,11 +574,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       umma_commit(&bars->drained);
       drain_wait(&bars->drained, 0);
     }
-  } else if (warp < 4) {
+  } else if (warp == 6 || warp == 7) {
     // ------------------------------------------------------------ drafts
     constexpr int CH = D / 8;  // 16-byte chunks per row
     constexpr int NL = 64;
-    const int lt = threadIdx.x - 64;
+    const int lt = threadIdx.x - 192;
     Cursor cur(p, bars);
     Seg s;
     int j0 = 0, round = 0;
@@ -639,11 +631,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           const uint8_t* kt = smem + C::kOffK + ks * C::kTileBytes;
           uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
           const int rows = tile_keys(p, tile, s.ctx);
+          const Layout lay = tile_layout<D>(p, tile);
           const bool append = p.k_new != nullptr && s.m == 0;
 #pragma unroll 2
           for (int x = lt; x < rows * CH; x += NL) {
             const int r = x / CH, ch = x % CH, node = tile * kBN + r - off;
-            uint4* vp = reinterpret_cast<uint4*>(vt + tile_off(r, ch));
+            uint4* vp = reinterpret_cast<uint4*>(vt + swizzled_off(r, ch, lay.half, lay.group));
             // present: its own bit is set
             if (node < 0 || node >= p.T || !((am[node * C::kWords + (node >> 5)] >> (node & 31)) & 1u)) {
               *vp = make_uint4(0u, 0u, 0u, 0u);
@@ -654,7 +647,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
               const int64_t row = cache_row(p, s.b, s.g, s.ctx + node);
               if (row >= 0) {
                 *reinterpret_cast<uint4*>(p.kc + row * D + ch * 8) =
-                    *reinterpret_cast<const uint4*>(kt + tile_off(r, ch));
+                    *reinterpret_cast<const uint4*>(kt + swizzled_off(r, ch, lay.half, lay.group));
                 *reinterpret_cast<uint4*>(p.vc + row * D + ch * 8) = vw;
               }
             }
@@ -669,8 +662,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           fence_proxy_async_smem();
           named_bar_sync(1, NL);
           if (lt == 0) {
-            mbar_arrive(&bars->k_full[ks]);
-            mbar_arrive(&bars->v_full[vs]);
+            for (int x = 0; x < 2; ++x) {  // for both producers of each
+              mbar_arrive(&bars->k_full[ks]);
+              mbar_arrive(&bars->v_full[vs]);
+            }
           }
         }
         if (ok && lt == 0) mbar_arrive(&bars->mask_full[mb]);
@@ -678,20 +673,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       }
       j0 += s.t1 - s.t0;
     }
-  } else {
+  } else if (warp >= 8) {
     // ------------------------------------------------------------ softmax
-    if constexpr (NT == 2) regs_inc<C::kRegsSoft>();
-    const int t = (warp >> 2) - 1;  // row tile
+    regs_inc<C::kRegsSoft>();
+    const int wg = (warp >> 2) - 2;
+    const int t = NT == 2 ? wg : 0;  // row tile
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const int tid = threadIdx.x - 128;
+    const int tid = threadIdx.x - 256;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t o_col = C::kColO + t * D;
+    const uint32_t s_col = wg * 128, o_col = C::kColO + wg * D;
     constexpr int CH = D / 8;
 
     // this row tile's queries: every S of the segment before is done by then
     auto load_q = [&](const Seg& s) {
-      if (quarter != 0 || lane != 0) return;
+      if (quarter != 0 || lane != 0) return;  // NT = 1: called by one warpgroup only
       mbar_arrive_expect_tx(&bars->q_full[t], static_cast<uint32_t>(p.RT) * D * 2);
 #pragma unroll
       for (int x = 0; x < C::kBoxes; ++x)
@@ -699,22 +695,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     (s.m * NT + t) * p.tb, s.g, s.b);
     };
 
-    // PV of tile x is done.  Asked about the latest tile or the one before it;
-    // S(x + 1 or x + 2), seen by then, follows the PV that completed the phase
-    // before, so the parity is never read a phase early, and the phase after
-    // needs this warp's next P, so never a phase late.
-    auto o_wait = [&](int x) {
-      return NT == 1 ? mbar_wait(&bars->o_done[x & 1], (x >> 1) & 1, abort, p.status)
-                     : mbar_wait(&bars->o_done[t], x & 1, abort, p.status);
-    };
+    // PV of this warpgroup's tile number x (of all it has had) is done.  Asked only
+    // about the latest one or the one before: S of the tile after x, seen by then,
+    // follows the PV before x, so the parity is never read a phase early; and the
+    // phase after needs this warp's next P, so never a phase late.
+    auto o_wait = [&](int x) { return mbar_wait(&bars->o_done[wg], x & 1, abort, p.status); };
+    float2* xch = reinterpret_cast<float2*>(smem + C::kOffXch);
 
     Cursor cur(p, bars);
     Seg s, s_next;
     bool ok = true;
     bool more = cur.next(s);
-    if (more) load_q(s);
-    int j = 0, round = 0;
-    while (ok && more) {
+    if (more && (NT == 2 || wg == 0)) load_q(s);
+    int j = 0, round = 0, seg = 0;
+    int n_mine = 0;  // tiles this warpgroup has had
+    for (; ok && more; ++seg) {
       const int node = (s.m * NT + t) * p.tb + row / p.G;
       const bool mine = row < p.RT && node < p.T;               // the row exists
       const bool warp_on = __any_sync(0xffffffffu, mine);
@@ -723,22 +718,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       const int mb = round & 1;
       const uint32_t* am = anc + mb * C::kMaxT * C::kWords + (mine ? node : 0) * C::kWords;
       const int off = draft_off(p, s.ctx);
-      bool more_next = false;
+      int mine_before = n_mine;
       float m_run = -INFINITY, l_run = 0.0f;
       for (int tile = s.t0; tile < s.t1; ++tile, ++j) {
-        const int sb = NT == 1 ? (j & 1) : t;
-        const int sph = NT == 1 ? (j >> 1) & 1 : j & 1;
-        const uint32_t s_col = NT == 1 ? static_cast<uint32_t>((j & 1) * 128) : t * 128u;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[sb], sph, abort, p.status))) {
+        if (NT == 1 && (j & 1) != wg) continue;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[wg], n_mine & 1, abort, p.status))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (tile == s.t1 - 1) {
-          more_next = cur.next(s_next);
-          if (more_next) load_q(s_next);
+        if (tile == s.t1 - 1) {  // every S of this segment is done: the next one's queries
+          s_next = s;
+          Cursor ahead = cur;
+          if (ahead.next(s_next)) load_q(s_next);
         }
-        if (tile == s.t0 && has_draft) {
+        if (has_draft && n_mine == mine_before) {
           if (!__all_sync(0xffffffffu, mbar_wait(&bars->mask_full[mb], (round >> 1) & 1, abort, p.status))) {
             ok = false;
             break;
@@ -774,7 +768,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             }
             uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
             for (int x = tid & 127; x < (tile_keys(p, tile, s.ctx) - lim) * CH; x += 128)
-              *reinterpret_cast<uint4*>(vt + tile_off(lim + x / CH, x % CH)) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(vt + swizzled_off(lim + x / CH, x % CH, PagedTile<D>::kHalf,
+                                                          PagedTile<D>::kGroup)) = make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
           }
         }
@@ -844,8 +839,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             weigh(masked ? 1.0f : p.scale_log2, m_run == -INFINITY ? 0.0f : -m_run);
           }
           l_run = l_run * alpha + rs;
-          if (tile > s.t0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-            if (!__all_sync(0xffffffffu, o_wait(j - 1))) {
+          if (n_mine > mine_before && __any_sync(0xffffffffu, alpha != 1.0f)) {
+            if (!__all_sync(0xffffffffu, o_wait(n_mine - 1))) {
               ok = false;
               break;
             }
@@ -864,20 +859,63 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[sb]);
+        if (lane == 0) mbar_arrive(&bars->p_full[wg]);
+        ++n_mine;
       }
       if (!ok) break;
 
       // ---------------------------------------------------------- epilogue
-      if (!__all_sync(0xffffffffu, o_wait(j - 1))) {
-        ok = false;
-        break;
+      // NT = 1: both warpgroups' states joined; warpgroup w writes half w of the
+      // output columns.  f0, f1: what accumulators 0 and 1 weigh.
+      float f0 = 1.0f, f1 = 1.0f;
+      if constexpr (NT == 1) {
+        // the other warpgroup has read the segment before's
+        if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->o_free, (seg - 1) & 1, abort, p.status))) {
+          ok = false;
+          break;
+        }
+        xch[wg * kBM + row] = make_float2(m_run, l_run);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->xch_full[wg]);
+        // (its own accumulator, and the other's: that warpgroup's last tile)
+        const int others = j - n_mine;
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(&bars->xch_full[wg ^ 1], seg & 1, abort, p.status) &&
+                            (n_mine == 0 || mbar_wait(&bars->o_done[wg], (n_mine - 1) & 1, abort, p.status)) &&
+                            (others == 0 || mbar_wait(&bars->o_done[wg ^ 1], (others - 1) & 1, abort, p.status)))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float2 a = xch[row], b = xch[kBM + row];
+        const float M = fmaxf(a.x, b.x);
+        // a state without tiles (or keys) has max -inf and sum 0: weight 0
+        f0 = a.x == -INFINITY && !(a.y != 0.0f) ? 0.0f : fast_exp2(a.x - M);
+        f1 = b.x == -INFINITY && !(b.y != 0.0f) ? 0.0f : fast_exp2(b.x - M);
+        m_run = M;
+        l_run = f0 * a.y + f1 * b.y;
+        if (s.t1 - s.t0 == 1) {  // one tile: the other accumulator holds an older segment's
+          if ((j & 1) == 0)
+            f0 = 0.0f;
+          else
+            f1 = 0.0f;
+        }
+      } else {
+        if (!__all_sync(0xffffffffu, o_wait(n_mine - 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
       }
-      tc_fence_after();
       const bool whole = s.t0 == 0 && s.t1 == s.tiles;
       // drafts this row sees whose V is not finite, and whether the row's own draft is absent
       bool absent = false;
       uint32_t fix_any = 0u;
+      if (has_draft && NT == 1 && n_mine == mine_before &&
+          !__all_sync(0xffffffffu, mbar_wait(&bars->mask_full[mb], (round >> 1) & 1, abort, p.status))) {
+        ok = false;  // this warpgroup had no tile of the segment, and has not seen the masks
+        break;
+      }
       if (has_draft && mine) {
         uint32_t own = 0u;
 #pragma unroll
@@ -895,10 +933,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       const int64_t obase = s.b * p.out_stride[0] + head * p.out_stride[1] + node * p.out_stride[2];
       if (warp_on) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        for (int cc = 0; cc < D / 32 / (NT == 1 ? 2 : 1); ++cc) {
+          const int c = NT == 1 ? wg * (D / 64) + cc : cc;
           uint32_t o[32];
-          tmem_ld32(tmem + lane_addr + o_col + c * 32, o);
+          tmem_ld32(tmem + lane_addr + (NT == 1 ? C::kColO : o_col) + c * 32, o);
           tmem_wait_ld(o);
+          if constexpr (NT == 1) {
+            uint32_t o1[32];
+            tmem_ld32(tmem + lane_addr + C::kColO + D + c * 32, o1);
+            tmem_wait_ld(o1);
+            // an accumulator of weight 0 may hold anything
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint((f0 != 0.0f ? f0 * __uint_as_float(o[i]) : 0.0f) +
+                                     (f1 != 0.0f ? f1 * __uint_as_float(o1[i]) : 0.0f));
+          }
           if (mine) {
             if (fix_any != 0u) {
               for (int a = max(0, s.t0 * kBN - off); a < min(p.T, s.t1 * kBN - off); ++a) {
@@ -945,14 +994,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           }
           __syncwarp();
         }
-        if (mine) {
+        if (mine && (NT == 2 || wg == 0)) {
           if (!whole)
             p.part_lse[prow] = absent ? __uint_as_float(kAbsent) : lse2;
           else if (p.lse != nullptr)
             p.lse[(static_cast<int64_t>(s.b) * p.Hq + head) * p.T + node] = lse2 * 0.6931471805599453f;
         }
       }
-      tc_fence_before();  // O is read: the next segment's PV may overwrite it after p_full
+      tc_fence_before();  // O is read: the next segment's PV may overwrite it
+      if constexpr (NT == 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->o_free);
+      }
       if (has_draft) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->mask_empty[mb]);
@@ -963,18 +1016,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         CutItem it;
         it.b = s.b, it.g = s.g, it.node0 = node0;
         it.rows = min(p.T - node0, NT * p.tb) * p.G;
-        it.pieces = run_of(bars->total, bars->n_cta, s.item0 + s.tiles - 1) - static_cast<int>(blockIdx.x) + 1;
+        it.pieces = bars->runs.of(s.item0 + s.tiles - 1) - static_cast<int>(blockIdx.x) + 1;
         it.first_is_head = s.item0 == bars->lo;
         p.cuts[blockIdx.x] = it;
       }
-      s = s_next;
-      more = more_next;
+      more = cur.next(s);
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 4) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -997,12 +1049,12 @@ cudaError_t launch(const TreeArgs& a, TreeParams& p, cudaStream_t stream) {
                              !make_rows_map(&mvn, a.v_new, a.cache.Hkv, p.new_box)))
     return cudaErrorInvalidValue;
   auto kern = paged_tree_tc_kernel<D, NT>;
-  if constexpr (NT == 2) {
+  {
     // the setmaxnreg split must fit in what the launch gives (a larger one waits forever)
     static const bool fits = [&] {
       cudaFuncAttributes fa;
       return cudaFuncGetAttributes(&fa, kern) == cudaSuccess &&
-             128 * C::kRegsCtl + 256 * C::kRegsSoft <= fa.numRegs * C::kThreads;
+             256 * C::kRegsCtl + 256 * C::kRegsSoft <= fa.numRegs * C::kThreads;
     }();
     if (!fits) return cudaErrorInvalidConfiguration;
   }

@@ -19,8 +19,8 @@
 // steps (as in tree_tc.cu), and an item cut between SMs leaves partial sums that
 // its last piece adds up in order: the result does not depend on the timing.
 //
-// Warps: 0 streams K pairs, 1 issues the MMAs, 2 streams query chunks, 3 their
-// LSEs, 4-7 and 8-11 own the two key tiles.
+// Warps: 0-3 stream K, 4 issues the MMAs, 5 streams query chunks, 6 their LSEs;
+// 8-11 and 12-15 own the two key tiles.
 #include <cuda.h>
 #include <math.h>
 
@@ -29,6 +29,8 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "paged_tile.cuh"
+#include "runs.cuh"
 
 namespace attn {
 namespace {
@@ -38,17 +40,17 @@ constexpr int kPair = 2 * kBM;
 constexpr int kBN = 128;       // query rows per chunk, at most
 constexpr int kBS = 16;
 constexpr int kBoxBytes = kBM * 128;
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kLseRing = 2;
 
 template <int D>
 struct Cfg {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = kBM * D * 2;
-  static constexpr int KS = 2;                // K pair stages
+  static constexpr int KS = D == 64 ? 8 : 4;  // K tile stages
   static constexpr int QS = D == 64 ? 4 : 3;  // query chunk stages
   static constexpr int kOffK = 0;
-  static constexpr int kOffQ = kOffK + KS * 2 * kTileBytes;
+  static constexpr int kOffQ = kOffK + KS * kTileBytes;
   static constexpr int kOffLse = kOffQ + QS * kTileBytes;  // [kLseRing][kBN] negated log2 LSEs, -inf: no weight
   static constexpr int kOffBar = kOffLse + kLseRing * kBN * 4;
   static constexpr int kSmemBytes = kOffBar + 512 + 1024;
@@ -56,13 +58,15 @@ struct Cfg {
 };
 
 struct Bars {
-  uint64_t k_full[2], k_empty[2];
+  uint64_t k_full[8], k_empty[8];
   uint64_t q_full[4], q_empty[4];
-  uint64_t s_full[2], s_free[2];  // [score buffer], both key tiles
+  uint64_t s_full[2][2], s_free[2][2];  // [key tile][score buffer]
   uint64_t l_full[kLseRing], l_empty[kLseRing];
   uint64_t piece_full, piece_go, drained;
-  int64_t lo, hi, total, bstart;
-  int b0, n_cta;
+  // this CTA's run, and where in it its first step lies
+  Runs runs;
+  int64_t lo, hi, item0;
+  int b0, g0, pair0, c0;
   uint32_t tmem_base;
   int abort, last;
   int odd[kLseRing];  // the chunk has columns without weight (padding, or rows that see nothing)
@@ -94,10 +98,8 @@ struct WeightParams {
 struct SeqWork {
   int start, n, keys, pairs, chunks, full, ct;
   int64_t steps;  // per KV head
-  __device__ int first(int p) const {
-    if (p < full) return 0;
-    return min((p * kPair - start) / ct, chunks - 1);
-  }
+  // At most chunks - 1: the pair's first key is one of the sequence's keys.
+  __device__ int first(int p) const { return p < full ? 0 : (p * kPair - start) / ct; }
 };
 
 __device__ __forceinline__ SeqWork seq_work(const WeightParams& p, int b, bool report_bad) {
@@ -117,7 +119,13 @@ __device__ __forceinline__ SeqWork seq_work(const WeightParams& p, int b, bool r
   w.chunks = (n + p.ct - 1) / p.ct;
   w.full = p.causal ? min(w.pairs, w.start / kPair + 1) : w.pairs;
   w.steps = static_cast<int64_t>(w.full) * w.chunks;
-  for (int x = w.full; x < w.pairs; ++x) w.steps += w.chunks - w.first(x);
+  if (kPair % p.ct == 0) {
+    // first(x) = k x - ceil(start / ct): an arithmetic series
+    const int64_t k = kPair / p.ct, m = w.pairs - w.full;
+    w.steps += m * (w.chunks + (w.start + p.ct - 1) / p.ct) - k * (m * (w.full + w.pairs - 1) / 2);
+  } else {
+    for (int x = w.full; x < w.pairs; ++x) w.steps += w.chunks - w.first(x);
+  }
   return w;
 }
 
@@ -135,23 +143,9 @@ struct Cursor {
   int b, g, pair, c;  // the next step: chunk c of this item
   SeqWork w;
   __device__ Cursor(const WeightParams& prm, const Bars* bars)
-      : p(prm), pos(bars->lo), hi(bars->hi), item0(0), b(bars->b0), g(0), pair(0), c(0) {
-    if (pos >= hi) return;
-    w = seq_work(p, b, false);
-    const int64_t local = pos - bars->bstart;
-    g = static_cast<int>(local / w.steps);
-    const int64_t rem = local - g * w.steps;  // step within the (sequence, KV head)
-    int64_t base;
-    if (rem < static_cast<int64_t>(w.full) * w.chunks) {
-      pair = static_cast<int>(rem / w.chunks);
-      base = static_cast<int64_t>(pair) * w.chunks;
-    } else {
-      pair = w.full;
-      base = static_cast<int64_t>(w.full) * w.chunks;
-      while (rem >= base + w.chunks - w.first(pair)) base += w.chunks - w.first(pair), ++pair;
-    }
-    c = w.first(pair) + static_cast<int>(rem - base);
-    item0 = pos - (rem - base);
+      : p(prm), pos(bars->lo), hi(bars->hi), item0(bars->item0), b(bars->b0), g(bars->g0), pair(bars->pair0),
+        c(bars->c0) {
+    if (pos < hi) w = seq_work(p, b, false);
   }
   __device__ bool next(Seg& s) {
     if (pos >= hi) return false;
@@ -183,11 +177,6 @@ struct Cursor {
   }
 };
 
-__device__ __forceinline__ int64_t run_lo(int64_t total, int n, int c) { return total * c / n; }
-__device__ __forceinline__ int run_of(int64_t total, int n, int64_t step) {
-  return static_cast<int>(((step + 1) * n - 1) / total);
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
@@ -202,10 +191,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 32) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars->k_full[s], 1);
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(&bars->s_full[t][s], 1);
+        mbar_init(&bars->s_free[t][s], 4);
+      }
+    }
+    for (int s = 0; s < 8; ++s) {
+      mbar_init(&bars->k_full[s], 2);  // two producer warps a tile
       mbar_init(&bars->k_empty[s], 1);
-      mbar_init(&bars->s_full[s], 1);
-      mbar_init(&bars->s_free[s], 8);
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&bars->q_full[s], 1);
@@ -222,17 +215,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 0) {
-    int64_t total = 0;
-    for (int b = lane; b < p.B; b += 32) total += seq_work(p, b, blockIdx.x == 0).steps * p.Hkv;
+    int64_t total = 0, mine0 = 0;
+    for (int base = 0; base < p.B; base += 32) {
+      const int64_t mine =
+          base + lane < p.B ? seq_work(p, base + lane, blockIdx.x == 0).steps * p.Hkv : 0;
+      if (base == 0) mine0 = mine;
+      total += mine;
+    }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
-    const int n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-    const int c = static_cast<int>(blockIdx.x);
-    const int64_t lo = c < n ? run_lo(total, n, c) : 0, hi = c < n ? run_lo(total, n, c + 1) : 0;
+    const Runs runs = Runs::make(total, gridDim.x);
+    const int cta = static_cast<int>(blockIdx.x);
+    const int64_t lo = cta < runs.n ? runs.lo(cta) : 0, hi = cta < runs.n ? runs.lo(cta + 1) : 0;
     int64_t run = 0;
     int b0 = 0;
     for (int base = 0; base < p.B && lo < hi; base += 32) {
-      const int64_t mine = base + lane < p.B ? seq_work(p, base + lane, false).steps * p.Hkv : 0;
+      const int64_t mine =
+          base == 0 ? mine0 : (base + lane < p.B ? seq_work(p, base + lane, false).steps * p.Hkv : 0);
       int64_t incl = mine;
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) {
@@ -249,13 +248,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       run += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) {
-      bars->lo = lo, bars->hi = hi, bars->total = total, bars->bstart = run;
-      bars->b0 = b0, bars->n_cta = n;
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_q);
+      bars->runs = runs;
+      bars->lo = lo, bars->hi = hi, bars->b0 = b0;
+      if (lo < hi) {
+        const SeqWork w = seq_work(p, b0, false);
+        const int g = static_cast<int>(div_pos(lo - run, w.steps));
+        int64_t rem = lo - run - g * w.steps;  // step within the (sequence, KV head)
+        int pair;
+        if (rem < static_cast<int64_t>(w.full) * w.chunks) {
+          pair = static_cast<int>(div_pos(rem, w.chunks));
+          rem -= static_cast<int64_t>(pair) * w.chunks;
+        } else {
+          pair = w.full;
+          rem -= static_cast<int64_t>(w.full) * w.chunks;
+          while (rem >= w.chunks - w.first(pair)) rem -= w.chunks - w.first(pair), ++pair;
+        }
+        bars->g0 = g, bars->pair0 = pair;
+        bars->c0 = w.first(pair) + static_cast<int>(rem);
+        bars->item0 = lo - rem;
+      }
     }
   }
-  if (warp == 1) {
+  if (warp == 4) {
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
   }
@@ -265,36 +281,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = bars->tmem_base;
   // scores of tile t, buffer j & 1, at column (2 t + (j & 1)) * 128
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ K pairs
-    // lane i < 16 owns block i of the pair
+  if (warp < 4) {
+    // ------------------------------------------------------------ K
+    // warp w, lane i < 4: block 4 w + i of the pair's sixteen, its id read a
+    // segment ahead; warps 0, 1 fill the first tile, 2, 3 the second
     Cursor cur(p, bars);
     Seg s;
-    int n = 0;
-    while (cur.next(s)) {
-      const int st = n % C::KS;
-      const int blocks = (cur.w.keys + kBS - 1) / kBS - s.pair * (kPair / kBS);
-      int id = lane < min(blocks, kPair / kBS)
-                   ? p.bt[static_cast<int64_t>(s.b) * p.bt_stride + s.pair * (kPair / kBS) + lane]
-                   : -1;
+    const int t = warp >> 1, place = warp * kWarpBlocks + lane;  // block of the pair
+    auto block_id = [&](const Seg& x, int keys) {
+      const int blk = x.pair * (kPair / kBS) + place;
+      return lane < kWarpBlocks && blk * kBS < keys ? p.bt[static_cast<int64_t>(x.b) * p.bt_stride + blk] : -1;
+    };
+    int n = t;
+    bool more = cur.next(s);
+    int id_next = more ? block_id(s, cur.w.keys) : -1;
+    while (more) {
+      int id = id_next;
+      const int g = s.g;
+      more = cur.next(s);
+      if (more) id_next = block_id(s, cur.w.keys);
       if (id != -1 && (id < 0 || id >= p.num_blocks)) {
         report(p.status, kStatusBounds);
         id = -1;
       }
-      const int bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * (kBS * D * 2);
+      const int st = n % C::KS;
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * (kBS * D * 2);
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->k_empty[st], ((n / C::KS) & 1) ^ 1, abort, p.status))) break;
       if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], bytes);
       __syncwarp();
-      if (id >= 0)
-#pragma unroll
-        for (int x = 0; x < C::kBoxes; ++x)
-          tma_load_4d(smem + C::kOffK + (st * 2 + (lane >> 3)) * C::kTileBytes + x * kBoxBytes + (lane & 7) * 2048,
-                      &tm_k, &bars->k_full[st], x * 64, 0, s.g, id);
-      ++n;
+      load_block<D>(smem + C::kOffK + st * C::kTileBytes, place % kTileBlocks, &tm_k, &bars->k_full[st], id, p.Hkv, g);
+      n += 2;
     }
-    if (lane == 0 && *abort)
-      for (int x = max(0, n - C::KS); x < n; ++x) drain_wait(&bars->k_full[x % C::KS], (x / C::KS) & 1);
-  } else if (warp == 1) {
+    if (lane == 0 && *abort)  // let the copies in flight land
+      for (int x = max(t, n - C::KS); x < n; x += 2) drain_wait(&bars->k_full[x % C::KS], (x / C::KS) & 1);
+  } else if (warp == 4) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, abort, p.status); };
@@ -303,36 +323,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n = 0, j = 0;
       bool ok = true;
       while (ok && cur.next(s)) {
-        const int st = n % C::KS;
-        ok = wait(&bars->k_full[st], n / C::KS);
         for (int c = s.c0; ok && c < s.c1; ++c, ++j) {
           const int qs = j % C::QS;
-          ok = wait(&bars->q_full[qs], j / C::QS) && wait(&bars->s_free[j & 1], (j >> 1) ^ 1);
+          ok = wait(&bars->q_full[qs], j / C::QS);
           if (!ok) break;
-          tc_fence_after();
           const int cols = min(p.ct, cur.w.n - c * p.ct) * p.G;
           const uint32_t idesc = idesc_bf16_f32(kBM, (cols + 15) / 16 * 16, false, false);
           const uint32_t qa = smem_u32(smem + C::kOffQ + qs * C::kTileBytes);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const uint32_t ka = smem_u32(smem + C::kOffK + (st * 2 + t) * C::kTileBytes);
+          for (int t = 0; ok && t < 2; ++t) {
+            // half a chunk apart, the two tiles' exponentials do not come at once
+            const int st = (n + t) % C::KS;
+            ok = (c > s.c0 || wait(&bars->k_full[st], (n + t) / C::KS)) &&
+                 wait(&bars->s_free[t][j & 1], (j >> 1) ^ 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t ka = smem_u32(smem + C::kOffK + st * C::kTileBytes);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
-              umma_bf16_ss(tmem + (2 * t + (j & 1)) * 128, sdesc_sw128(ka + off, 16, 1024),
-                           sdesc_sw128(qa + off, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+              // 16 dims = 32 bytes of a 128-byte row
+              umma_bf16_ss(tmem + (2 * t + (j & 1)) * 128,
+                           sdesc_sw128(ka + (kk >> 2) * PagedTile<D>::kHalf + (kk & 3) * 32, 16, PagedTile<D>::kGroup),
+                           sdesc_sw128(qa + (kk >> 2) * kBoxBytes + (kk & 3) * 32, 16, 1024), idesc,
+                           kk > 0 ? 1u : 0u);
             }
+            umma_commit(&bars->s_full[t][j & 1]);
+            if (c + 1 == s.c1) umma_commit(&bars->k_empty[st]);
           }
-          umma_commit(&bars->s_full[j & 1]);
           umma_commit(&bars->q_empty[qs]);
         }
-        if (ok) umma_commit(&bars->k_empty[st]);
-        ++n;
+        n += 2;
       }
       umma_commit(&bars->drained);
       drain_wait(&bars->drained, 0);
     }
-  } else if (warp == 2) {
+  } else if (warp == 5) {
     // ------------------------------------------------------------ query chunks
     if (lane == 0) {
       Cursor cur(p, bars);
@@ -355,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (*abort)
         for (int x = max(0, j - C::QS); x < j; ++x) drain_wait(&bars->q_full[x % C::QS], (x / C::QS) & 1);
     }
-  } else if (warp == 3) {
+  } else if (warp == 6) {
     // ------------------------------------------------------------ their LSEs
     // negated, in log2 units; -inf where a column has no weight (past the
     // chunk, or a row that saw nothing).  Loaded a chunk ahead of the store.
@@ -399,11 +424,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (ok && j > 0) publish(j - 1);
-  } else {
+  } else if (warp >= 8) {
     // ------------------------------------------------------------ sums
-    const int t = (warp >> 2) - 1;
+    const int t = (warp >> 2) & 1;  // key tile
     const int row = (warp & 3) * 32 + lane;
-    const int tid = threadIdx.x - 128;
+    const int tid = t * kBM + row;
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
     Cursor cur(p, bars);
     Seg s;
@@ -434,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = s.c0; c < s.c1; ++c, ++j) {
         const int buf = j & 1, sl = j % kLseRing;
         if (!__all_sync(0xffffffffu, mbar_wait(&bars->l_full[sl], (j / kLseRing) & 1, abort, p.status) &&
-                                         mbar_wait(&bars->s_full[buf], (j >> 1) & 1, abort, p.status))) {
+                                         mbar_wait(&bars->s_full[t][buf], (j >> 1) & 1, abort, p.status))) {
           ok = false;
           break;
         }
@@ -468,22 +493,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         if (!masked) {
-          // a whole chunk: the next 32 columns load while these are added (cr may
-          // be below 128 only with a column of padding, which is masked)
+          // a whole chunk (one with a column of padding is masked)
           uint32_t sa[32], sb[32];
           tmem_ld32(col, sa);
           tmem_wait_ld(sa);
-          tmem_ld32(col + 32, sb);
-          add32(sa, 0, std::false_type());
-          tmem_wait_ld(sb);
-          tmem_ld32(col + 64, sa);
-          add32(sb, 32, std::false_type());
-          tmem_wait_ld(sa);
-          tmem_ld32(col + 96, sb);
-          add32(sa, 64, std::false_type());
-          tmem_wait_ld(sb);
-          add32(sb, 96, std::false_type());
+#pragma unroll 1
+          for (int cc = 0; cc < kBN; cc += 64) {  // the next 32 columns load while these are added
+            tmem_ld32(col + cc + 32, sb);
+            add32(sa, cc, std::false_type());
+            tmem_wait_ld(sb);
+            if (cc + 64 < kBN) tmem_ld32(col + cc + 64, sa);
+            add32(sb, cc + 32, std::false_type());
+            if (cc + 64 < kBN) tmem_wait_ld(sa);
+          }
         } else {
+#pragma unroll 1
           for (int cc = 0; cc < cols; cc += 32) {
             uint32_t sr[32];
             tmem_ld32(col + cc, sr);
@@ -494,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&bars->s_free[buf]);
+          mbar_arrive(&bars->s_free[t][buf]);
           mbar_arrive(&bars->l_empty[sl]);
         }
       }
@@ -507,10 +531,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       // a cut item: leave the piece; the last one adds them in order
+      const Runs& runs = bars->runs;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (s.step0 == bars->lo ? 0 : 1);
       p.part[static_cast<int64_t>(slot) * kPair + tid] = got;
-      const int p0 = run_of(bars->total, bars->n_cta, s.item0);
-      const int np = run_of(bars->total, bars->n_cta, s.item1 - 1) - p0 + 1;
+      const int p0 = runs.of(s.item0);
+      const int np = runs.of(s.item1 - 1) - p0 + 1;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->piece_full);
       if (tid < 32 && !__all_sync(0xffffffffu, mbar_wait(&bars->piece_full, pieces & 1, abort, p.status))) {
@@ -543,8 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++pieces;
       if (bars->last) {
         __threadfence();
-        const bool head = run_lo(bars->total, bars->n_cta, p0) == s.item0;
+        const bool head = runs.lo(p0) == s.item0;
         float all = 0.f;
+#pragma unroll 4
         for (int x = 0; x < np; ++x) {
           const int sl = 2 * (p0 + x) + ((x == 0 && !head) ? 1 : 0);
           all += __ldcg(p.part + static_cast<int64_t>(sl) * kPair + tid);
@@ -556,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 4) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
