@@ -14,8 +14,9 @@
 // exponentials do.
 //
 // Every SM takes an equal run of the call's K/V tiles: an item (sequence, KV
-// head, row pair) is its draft tiles followed by its context tiles, the items
-// are laid end to end, and CTA c of n takes tiles [total c / n, total (c+1) / n).
+// head, group of row tiles) is its context tiles followed by its draft tiles (whose
+// masks are built meanwhile), the items are laid end to end, and each CTA takes an
+// equal run of tiles (runs.cuh).
 // An item inside one run is written at once; one that is cut leaves partials
 // (normalised rows and log2 LSE; at most two per CTA), which a second launch
 // merges in order, so results do not depend on the timing.  That launch spreads
@@ -55,7 +56,8 @@ constexpr int kBN = 128;
 constexpr int kBS = 16;
 constexpr int kBoxBytes = kBM * 128;
 constexpr float kRescaleMargin = 8.0f;
-constexpr int kBarBytes = 512;
+constexpr int kBarBytes = 1024;
+constexpr int kSegs = 4;  // segments the planner is ahead
 constexpr uint32_t kAbsent = 0x7fc0a5a5u;  // a partial's LSE for the row of an absent draft (a NaN of its own)
 
 template <int D, int NT>
@@ -83,6 +85,16 @@ struct Cfg {
   static constexpr int kRegsCtl = 72, kRegsSoft = 184;
 };
 
+// A run of one item's tiles [t0, t1): what every warp role works through.  One
+// warp plans them and hands them on in a small ring: with the arithmetic inlined
+// in each role the kernel was 136 KB of code, more than the instruction cache.
+struct Seg {
+  int b;  // -1: the end
+  int g, m, t0, t1, nct, ctx;  // nct: the item's context tiles; the drafts' follow
+  int slot;   // where its partial goes; -1: the item is whole
+  int there;  // the sequence is present (not idle, and fits its table)
+};
+
 struct Bars {
   uint64_t q_full[2];
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
@@ -92,9 +104,8 @@ struct Bars {
   uint64_t draft_in[4];  // a draft tile's K and V have landed in K stage ks (and the tile's V stage)
   uint64_t mask_full[2], mask_empty[2];
   uint64_t drained;
-  Runs runs;
-  int64_t lo, hi;        // this CTA's run of tiles, and the place of its first:
-  int b0, item0, tile0;  // sequence, item (KV head, row group) in it, tile in that
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  Seg segs[kSegs];
   uint32_t bad[2][8];  // drafts whose V holds a non-finite element
   uint32_t tmem_base;
   int abort;
@@ -127,9 +138,9 @@ struct TreeParams {
   int out_bf16;
   int64_t out_stride[3];
   float* lse;
-  float* part_o;    // [2 n][slot_rows][D]
-  float* part_lse;  // [2 n][slot_rows]
-  int slot_rows;
+  float* part_o;    // [2 n][D][pitch]: a column's rows side by side, as the TMEM lanes hold them
+  float* part_lse;  // [2 n][pitch]
+  int pitch;        // rows of a partial: 128 a row tile
   struct CutItem* cuts;  // [n] the item that starts in CTA c's run and goes on past it
   uint32_t* status;
 };
@@ -137,7 +148,7 @@ struct TreeParams {
 // pieces == 0: no item of the kind.  A CTA's first segment uses partial slot 2c, a
 // later one (only its last can be cut) slot 2c + 1.
 struct CutItem {
-  int b, g, node0, rows;
+  int b, g, node0;
   int pieces;         // in CTAs c, c + 1, ...
   int first_is_head;  // CTA c's run begins with it
 };
@@ -150,56 +161,16 @@ __device__ __forceinline__ int seq_ctx(const TreeParams& p, int b, bool& ok) {
 }
 __device__ __forceinline__ int seq_tiles(const TreeParams& p, int b, int& ctx, bool& ok) {
   ctx = seq_ctx(p, b, ok);
-  return p.ntd + (ctx + kBN - 1) / kBN;
+  return (ctx + kBN - 1) / kBN + p.ntd;
 }
 
 // The drafts' first key in their tiles: a block's start when they come from the cache.
 __device__ __forceinline__ int draft_off(const TreeParams& p, int ctx) { return p.k_new != nullptr ? 0 : ctx % kBS; }
 // Keys of a tile that its MMAs cover: a multiple of 16, at least 16.
-__device__ __forceinline__ int tile_keys(const TreeParams& p, int tile, int ctx) {
-  const int left = tile < p.ntd ? p.T + draft_off(p, ctx) - tile * kBN : ctx - (tile - p.ntd) * kBN;
+__device__ __forceinline__ int tile_keys(const TreeParams& p, int tile, int nct, int ctx) {
+  const int left = tile >= nct ? p.T + draft_off(p, ctx) - (tile - nct) * kBN : ctx - tile * kBN;
   return min(kBN, max(16, (left + 15) / 16 * 16));
 }
-
-// A run of one item's tiles [t0, t1) of `tiles`.
-struct Seg {
-  int b, g, m, t0, t1, tiles, ctx;
-  bool ok;        // the sequence is present
-  int64_t item0;  // the item's first tile in the call's order
-};
-
-struct Cursor {
-  const TreeParams& p;
-  int64_t pos, hi;
-  int b, item, t, tiles, ctx;
-  bool ok;
-  __device__ Cursor(const TreeParams& prm, const Bars* bars)
-      : p(prm), pos(bars->lo), hi(bars->hi), b(bars->b0), item(bars->item0), t(bars->tile0) {
-    if (pos < hi) tiles = seq_tiles(p, b, ctx, ok);
-  }
-  __device__ bool next(Seg& s) {
-    if (pos >= hi) return false;
-    if (t == tiles) {  // the item is done: the next one, or the next sequence
-      t = 0;
-      if (++item == p.Hkv * p.MP) {
-        item = 0;
-        tiles = seq_tiles(p, ++b, ctx, ok);
-      }
-    }
-    s.b = b;
-    s.g = item / p.MP;
-    s.m = item % p.MP;
-    s.t0 = t;
-    s.t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t + (hi - pos)));
-    s.tiles = tiles;
-    s.ctx = ctx;
-    s.ok = ok;
-    s.item0 = pos - t;
-    pos += s.t1 - t;
-    t = s.t1;
-    return true;
-  }
-};
 
 // Layout of tile `tile`: fresh drafts arrive as 64-column boxes of rows, cached
 // rows block by block.
@@ -207,8 +178,8 @@ struct Layout {
   uint32_t half, group;  // bytes to the next 64 columns, to the next 8 rows
 };
 template <int D>
-__device__ __forceinline__ Layout tile_layout(const TreeParams& p, int tile) {
-  if (tile < p.ntd && p.k_new != nullptr) return {static_cast<uint32_t>(kBoxBytes), 1024u};
+__device__ __forceinline__ Layout tile_layout(const TreeParams& p, bool draft) {
+  if (draft && p.k_new != nullptr) return {static_cast<uint32_t>(kBoxBytes), 1024u};
   return {PagedTile<D>::kHalf, PagedTile<D>::kGroup};
 }
 
@@ -239,60 +210,73 @@ __device__ __forceinline__ const uint16_t* draft_row(const TreeParams& p, bool i
 }
 
 // The merge: out = sum_c 2^(lse_c - M) out_c / sum_c 2^(lse_c - M) over a cut
-// item's pieces.  grid (CTAs of the main launch, groups of kMergeRows rows);
-// a warp per row (D = 128: four dims a lane) or per two rows (D = 64).  Waits for
-// the main launch to finish, then takes ~2 us.
-constexpr int kMergeThreads = 128, kMergeRows = 16;
+// item's pieces.  grid (CTAs of the main launch, groups of 32 rows), a warp per D /
+// 16 columns, a lane per row: partials are read as they were written, 128 bytes a
+// warp, and the rows leave through shared memory.
+constexpr int kMergeThreads = 512;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+  constexpr int CW = D / 16;
+  __shared__ float tile[32][D + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kLanes = D / 4;  // lanes per row
-  constexpr int kPer = kMergeThreads / kLanes;
   const int c0 = blockIdx.x;
   const CutItem it = p.cuts[c0];
-  const int lane = threadIdx.x % kLanes;
-  for (int r = blockIdx.y * kMergeRows + threadIdx.x / kLanes; r < min(it.rows, (static_cast<int>(blockIdx.y) + 1) * kMergeRows);
-       r += kPer) {
-    if (it.pieces == 0) return;
-    auto slot_row = [&](int c) {
-      const int slot = 2 * (c0 + c) + ((c == 0 && !it.first_is_head) ? 1 : 0);
-      return static_cast<int64_t>(slot) * p.slot_rows + r;
-    };
-    const float l0 = p.part_lse[slot_row(0)];
-    const bool absent = __float_as_uint(l0) == kAbsent;
-    float M = l0;
-    bool any = l0 != -INFINITY;  // a NaN counts: it has to reach the row
+  if (it.pieces == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sr = blockIdx.y * 32 + lane;  // row of the partials
+  // its draft and head
+  auto place = [&](int r, int& t, int& h) {
+    const int row = r % kBM;
+    t = it.node0 + r / kBM * p.tb + row / p.G;
+    h = it.g * p.G + row % p.G;
+    return row < p.RT && t < p.T;
+  };
+  int t, h;
+  const bool mine = place(sr, t, h);
+  auto slot = [&](int c) { return static_cast<int64_t>(2 * (c0 + c) + ((c == 0 && !it.first_is_head) ? 1 : 0)); };
+  float M = -INFINITY;
+  bool any = false, absent = false;  // a NaN counts as something: it has to reach the row
 #pragma unroll 8
-    for (int c = 1; c < it.pieces; ++c) {
-      const float l = p.part_lse[slot_row(c)];
-      M = fmaxf(M, l);
-      any |= l != -INFINITY;
-    }
-    float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f, ws = 0.f;
-    const bool empty = absent || !any;
-    if (!empty) {
-#pragma unroll 8
-      for (int c = 0; c < it.pieces; ++c) {
-        const float l = p.part_lse[slot_row(c)];
-        const float4 o = *reinterpret_cast<const float4*>(p.part_o + slot_row(c) * D + lane * 4);
-        const float w = l == -INFINITY ? 0.f : fast_exp2(l - M);
-        const bool use = l != -INFINITY;  // a piece that saw nothing holds zeros
-        ws += w;
-        a0 = fmaf(w, use ? o.x : 0.f, a0), a1 = fmaf(w, use ? o.y : 0.f, a1);
-        a2 = fmaf(w, use ? o.z : 0.f, a2), a3 = fmaf(w, use ? o.w : 0.f, a3);
-      }
-    }
-    const float inv = empty ? 0.f : 1.f / ws;
-    const int t = it.node0 + r / p.G, h = it.g * p.G + r % p.G;
-    const int64_t ob = it.b * p.out_stride[0] + h * p.out_stride[1] + t * p.out_stride[2] + lane * 4;
-    if (p.out_bf16)
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ob) =
-          make_uint2(pack_bf16x2(a0 * inv, a1 * inv), pack_bf16x2(a2 * inv, a3 * inv));
-    else
-      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + ob) = make_float4(a0 * inv, a1 * inv, a2 * inv, a3 * inv);
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[(static_cast<int64_t>(it.b) * p.Hq + h) * p.T + t] =
-          empty ? -INFINITY : (M + __log2f(ws)) * 0.6931471805599453f;
+  for (int c = 0; c < it.pieces; ++c) {
+    const float l = mine ? p.part_lse[slot(c) * p.pitch + sr] : -INFINITY;
+    absent |= __float_as_uint(l) == kAbsent;
+    any |= l != -INFINITY;
+    M = fmaxf(M, l);
+  }
+  float acc[CW], ws = 0.f;
+#pragma unroll
+  for (int i = 0; i < CW; ++i) acc[i] = 0.f;
+  const bool empty = absent || !any;
+#pragma unroll 2
+  for (int c = 0; c < it.pieces; ++c) {
+    const float l = mine ? p.part_lse[slot(c) * p.pitch + sr] : -INFINITY;
+    const float* o = p.part_o + (slot(c) * D + warp * CW) * p.pitch + sr;
+    const bool use = l != -INFINITY;  // a piece that saw nothing holds zeros
+    const float w = use ? fast_exp2(l - M) : 0.f;
+    ws += w;
+#pragma unroll
+    for (int i = 0; i < CW; ++i) acc[i] = fmaf(w, use ? o[static_cast<int64_t>(i) * p.pitch] : 0.f, acc[i]);
+  }
+  const float inv = empty ? 0.f : 1.f / ws;
+#pragma unroll
+  for (int i = 0; i < CW; ++i) tile[lane][warp * CW + i] = empty ? 0.f : acc[i] * inv;
+  if (warp == 0 && mine && p.lse != nullptr)
+    p.lse[(static_cast<int64_t>(it.b) * p.Hq + h) * p.T + t] =
+        empty ? -INFINITY : (M + __log2f(ws)) * 0.6931471805599453f;
+  __syncthreads();
+  const int r = threadIdx.x / 16, d = threadIdx.x % 16 * CW;
+  if (!place(blockIdx.y * 32 + r, t, h)) return;
+  const int64_t ob = it.b * p.out_stride[0] + h * p.out_stride[1] + t * p.out_stride[2] + d;
+  const float* x = &tile[r][d];
+  if (p.out_bf16) {
+#pragma unroll
+    for (int i = 0; i < CW; i += 4)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ob + i) =
+          make_uint2(pack_bf16x2(x[i], x[i + 1]), pack_bf16x2(x[i + 2], x[i + 3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < CW; i += 4)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + ob + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
   }
 }
 
@@ -308,7 +292,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   uint32_t* anc = reinterpret_cast<uint32_t*>(smem + C::kOffAnc);
   int32_t* par = reinterpret_cast<int32_t*>(smem + C::kOffPar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ntd = p.ntd;
   volatile int* abort = &bars->abort;
 
   if (threadIdx.x == 32) {
@@ -328,40 +311,45 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       mbar_init(&bars->v_empty[s], 1);
       mbar_init(&bars->draft_in[s], 4);
     }
+    for (int s = 0; s < kSegs; ++s) {
+      mbar_init(&bars->seg_full[s], 1);
+      mbar_init(&bars->seg_empty[s], 15);  // 4 producers, the issuer, 2 drafts' and 8 softmax warps
+    }
     mbar_init(&bars->o_free, 8);
     mbar_init(&bars->drained, 1);
     bars->abort = 0;
     fence_mbar_init();
   }
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (warp == 0) {
-    // the call's tiles, this CTA's run of them, and the sequence it starts in
+  // the planner's state: the call's runs, and the place of this CTA's first tile
+  Runs runs = {};
+  int64_t pos = 0, hi = 0, lo = 0;
+  int plan_b = 0, plan_item = 0, plan_t = 0;
+  if (warp == 5) {
     const int64_t items = static_cast<int64_t>(p.Hkv) * p.MP;
     int64_t total = 0, mine0 = 0;
+    auto seq_items = [&](int b, bool first) -> int64_t {
+      if (b >= p.B) return 0;
+      int ctx;
+      bool ok;
+      const int64_t n = seq_tiles(p, b, ctx, ok) * items;
+      if (first && blockIdx.x == 0 && !ok && p.ctx_lens[b] >= 0) report(p.status, kStatusBounds);
+      return n;
+    };
     for (int base = 0; base < p.B; base += 32) {
-      int64_t mine = 0;
-      if (base + lane < p.B) {
-        int ctx;
-        bool ok;
-        mine = seq_tiles(p, base + lane, ctx, ok) * items;
-        if (blockIdx.x == 0 && !ok && p.ctx_lens[base + lane] >= 0) report(p.status, kStatusBounds);
-      }
+      const int64_t mine = seq_items(base + lane, true);
       if (base == 0) mine0 = mine;
       total += mine;
     }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
-    const Runs runs = Runs::make(total, gridDim.x);
+    runs = Runs::make(total, gridDim.x);
     const int c = static_cast<int>(blockIdx.x);
-    const int64_t lo = c < runs.n ? runs.lo(c) : 0, hi = c < runs.n ? runs.lo(c + 1) : 0;
+    if (c < runs.n) lo = runs.lo(c), hi = runs.lo(c + 1);
+    pos = lo;
     int64_t run = 0;
     for (int base = 0; base < p.B && lo < hi; base += 32) {
-      int64_t mine = base == 0 ? mine0 : 0;
-      if (base > 0 && base + lane < p.B) {
-        int ctx;
-        bool ok;
-        mine = seq_tiles(p, base + lane, ctx, ok) * items;
-      }
+      const int64_t mine = base == 0 ? mine0 : seq_items(base + lane, false);
       int64_t incl = mine;
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) {
@@ -370,21 +358,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       }
       const uint32_t past = __ballot_sync(0xffffffffu, run + incl > lo);
       if (past != 0) {
-        if (lane == __ffs(past) - 1) {
-          const int64_t local = lo - run - (incl - mine), tiles = div_pos(mine, items);
-          bars->b0 = base + lane;
-          bars->item0 = static_cast<int>(div_pos(local, tiles));
-          bars->tile0 = static_cast<int>(local - bars->item0 * tiles);
-        }
+        const int l = __ffs(past) - 1;
+        const int64_t local = lo - run - __shfl_sync(0xffffffffu, incl - mine, l);
+        const int64_t tiles = div_pos(__shfl_sync(0xffffffffu, mine, l), items);
+        plan_b = base + l;
+        plan_item = static_cast<int>(div_pos(local, tiles));
+        plan_t = static_cast<int>(local - plan_item * tiles);
         break;
       }
       run += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) {
-      bars->runs = runs;
-      bars->lo = lo;
-      bars->hi = hi;
-      p.cuts[c].pieces = 0;  // unless the softmax below finds one
+      p.cuts[c].pieces = 0;  // unless an item starts here and goes on
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
@@ -405,6 +390,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
+  // segment i, for a whole warp; false at the end
+  auto seg_get = [&](int i, Seg& s) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars->seg_full[i % kSegs], (i / kSegs) & 1, abort, p.status))) return false;
+    s = bars->segs[i % kSegs];
+    return s.b >= 0;
+  };
+  auto seg_taken = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->seg_empty[i % kSegs]);
+  };
+
   if (warp < 8) regs_dec<C::kRegsCtl>();
   if (warp < 4) {
     // ------------------------------------------------------------ K/V tiles
@@ -419,22 +415,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     uint64_t* empty = is_v ? bars->v_empty : bars->k_empty;
     uint8_t* base = smem + (is_v ? C::kOffV : C::kOffK);
     const int place = (warp & 1) * kWarpBlocks + lane;
-    Cursor cur(p, bars);
     Seg s;
     int j = 0, issued = 0, st = 0, ks = 0;  // st, ks: tile j's stage, and its K stage
     uint32_t ph = 1u;                       // parity of the stage's last release
     bool ok = true;
-    while (ok && cur.next(s)) {
+    for (int i = 0; ok && seg_get(i, s); ++i) {
+      seg_taken(i);
       const int32_t* bt_row = p.bt + static_cast<int64_t>(s.b) * p.bt_stride;
       auto block_id = [&](int tile) {
         if (tile >= s.t1 || lane >= kWarpBlocks) return -1;
         int blk, end;  // the block, and where the tile's kind of blocks ends
-        if (tile < ntd) {
-          if (p.k_new != nullptr || !s.ok) return -1;
-          blk = s.ctx / kBS + tile * kTileBlocks + place;
+        if (tile >= s.nct) {
+          if (p.k_new != nullptr || !s.there) return -1;
+          blk = s.ctx / kBS + (tile - s.nct) * kTileBlocks + place;
           end = (s.ctx + p.T + kBS - 1) / kBS;
         } else {
-          blk = (tile - ntd) * kTileBlocks + place;
+          blk = tile * kTileBlocks + place;
           end = (s.ctx + kBS - 1) / kBS;
         }
         return blk < end ? bt_row[blk] : -1;
@@ -452,7 +448,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           ok = false;
           break;
         }
-        const bool draft = tile < ntd;
+        const bool draft = tile >= s.nct;
         // one box of k_new (v_new) per 64 columns, by the operand's first warp
         const bool fresh = draft && p.k_new != nullptr && (warp & 1) == 0;
         if (fresh) bytes = static_cast<uint32_t>(p.new_box) * D * 2;
@@ -461,7 +457,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
         __syncwarp();
         if (fresh) {
-          if (lane < C::kBoxes) tma_load_5d(dst + lane * kBoxBytes, map_new, bar, lane * 64, 0, tile * kBN, s.g, s.b);
+          if (lane < C::kBoxes) tma_load_5d(dst + lane * kBoxBytes, map_new, bar, lane * 64, 0,
+                                             (tile - s.nct) * kBN, s.g, s.b);
         } else {
           load_block<D>(dst, place, map, bar, id, p.Hkv, s.g);
         }
@@ -504,14 +501,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, abort, p.status); };
       auto wait_k = [&](int j) { return wait(&bars->k_full[j % C::KS], j / C::KS); };
       auto wait_v = [&](int j) { return wait(&bars->v_full[j % C::VS], j / C::VS); };
-      Cursor cur(p, bars);
-      Seg s;
-      int j = 0, seg = 0;
+      int j = 0;
       bool ok = true;
-      for (; ok && cur.next(s); ++seg) {
+      for (int seg = 0; ok; ++seg) {
+        ok = wait(&bars->seg_full[seg % kSegs], seg / kSegs);
+        if (!ok) break;
+        const Seg s = bars->segs[seg % kSegs];
+        if (s.b < 0) break;
+        mbar_arrive(&bars->seg_empty[seg % kSegs]);
         const int n = s.t1 - s.t0;
-        auto keys = [&](int x) { return tile_keys(p, s.t0 + x, s.ctx); };
-        auto lay = [&](int x) { return tile_layout<D>(p, s.t0 + x); };
+        auto keys = [&](int x) { return tile_keys(p, s.t0 + x, s.nct, s.ctx); };
+        auto lay = [&](int x) { return tile_layout<D>(p, s.t0 + x >= s.nct); };
         for (int t = 0; t < NT; ++t) ok = ok && wait(&bars->q_full[t], seg);
         if constexpr (NT == 1) {
           // tile j is warpgroup j & 1's; S runs two tiles ahead of PV
@@ -574,25 +574,72 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       umma_commit(&bars->drained);
       drain_wait(&bars->drained, 0);
     }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ planner
+    int ctx = 0, tiles = 0;
+    bool there = false;
+    if (pos < hi) tiles = seq_tiles(p, plan_b, ctx, there);
+    for (int i = 0;; ++i) {
+      Seg s = {};
+      s.b = -1;
+      if (pos < hi) {
+        if (plan_t == tiles) {  // the item is done: the next one, or the next sequence
+          plan_t = 0;
+          if (++plan_item == p.Hkv * p.MP) {
+            plan_item = 0;
+            tiles = seq_tiles(p, ++plan_b, ctx, there);
+          }
+        }
+        s.b = plan_b;
+        s.g = plan_item / p.MP;
+        s.m = plan_item % p.MP;
+        s.t0 = plan_t;
+        s.t1 = static_cast<int>(min(static_cast<int64_t>(tiles), plan_t + (hi - pos)));
+        s.nct = tiles - p.ntd;
+        s.ctx = ctx;
+        s.there = there;
+        const bool whole = s.t0 == 0 && s.t1 == tiles;
+        s.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (pos == lo ? 0 : 1);
+        if (!whole && s.t0 == 0 && lane == 0) {  // cut, and it starts here
+          CutItem it;
+          it.b = s.b, it.g = s.g, it.node0 = s.m * NT * p.tb;
+          it.pieces = runs.of(pos + tiles - 1) - static_cast<int>(blockIdx.x) + 1;
+          it.first_is_head = pos == lo;
+          p.cuts[blockIdx.x] = it;
+        }
+        pos += s.t1 - plan_t;
+        plan_t = s.t1;
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->seg_empty[i % kSegs], ((i / kSegs) & 1) ^ 1, abort, p.status)))
+        break;
+      if (lane == 0) {
+        bars->segs[i % kSegs] = s;
+        mbar_arrive(&bars->seg_full[i % kSegs]);
+      }
+      if (s.b < 0) break;
+    }
   } else if (warp == 6 || warp == 7) {
     // ------------------------------------------------------------ drafts
     constexpr int CH = D / 8;  // 16-byte chunks per row
     constexpr int NL = 64;
     const int lt = threadIdx.x - 192;
-    Cursor cur(p, bars);
     Seg s;
     int j0 = 0, round = 0;
     uint32_t in = 0u;  // bit ks: parity of the next draft tile in K stage ks
     bool ok = true;
-    while (ok && cur.next(s)) {
-      if (s.t0 < ntd) {
+    for (int i = 0; ok; ++i) {
+      ok = seg_get(i, s);
+      ok = !named_bar_or(1, NL, !ok);  // the two warps go the same way
+      if (!ok) break;
+      seg_taken(i);
+      if (s.t1 > s.nct) {
         const int mb = round & 1;
         uint32_t* am = anc + mb * C::kMaxT * C::kWords;
         // the masks of two segments before may still be in use
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->mask_empty[mb], ((round >> 1) & 1) ^ 1, abort, p.status));
         ok = !named_bar_or(1, NL, !ok);
         if (!ok) break;
-        for (int t = lt; t < p.T; t += NL) par[t] = s.ok ? p.parents[s.b * p.par_stride + t] : -2;
+        for (int t = lt; t < p.T; t += NL) par[t] = s.there ? p.parents[s.b * p.par_stride + t] : -2;
         if (lt < 8) bars->bad[mb][lt] = 0u;
         named_bar_sync(1, NL);
         // node t's ancestors, itself included: parents come before children, so
@@ -621,7 +668,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         named_bar_sync(1, NL);
         const int off = draft_off(p, s.ctx);
-        for (int tile = s.t0; ok && tile < min(s.t1, ntd); ++tile) {
+        for (int tile = max(s.t0, s.nct); ok && tile < s.t1; ++tile) {
           const int j = j0 + tile - s.t0;
           const int ks = j % C::KS, vs = j % C::VS;
           ok = __all_sync(0xffffffffu, mbar_wait(&bars->draft_in[ks], (in >> ks) & 1u, abort, p.status));
@@ -630,12 +677,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           if (!ok) break;
           const uint8_t* kt = smem + C::kOffK + ks * C::kTileBytes;
           uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
-          const int rows = tile_keys(p, tile, s.ctx);
-          const Layout lay = tile_layout<D>(p, tile);
+          const int rows = tile_keys(p, tile, s.nct, s.ctx);
+          const Layout lay = tile_layout<D>(p, true);
           const bool append = p.k_new != nullptr && s.m == 0;
 #pragma unroll 2
           for (int x = lt; x < rows * CH; x += NL) {
-            const int r = x / CH, ch = x % CH, node = tile * kBN + r - off;
+            const int r = x / CH, ch = x % CH, node = (tile - s.nct) * kBN + r - off;
             uint4* vp = reinterpret_cast<uint4*>(vt + swizzled_off(r, ch, lay.half, lay.group));
             // present: its own bit is set
             if (node < 0 || node >= p.T || !((am[node * C::kWords + (node >> 5)] >> (node & 31)) & 1u)) {
@@ -702,23 +749,23 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     auto o_wait = [&](int x) { return mbar_wait(&bars->o_done[wg], x & 1, abort, p.status); };
     float2* xch = reinterpret_cast<float2*>(smem + C::kOffXch);
 
-    Cursor cur(p, bars);
-    Seg s, s_next;
+    Seg s;
     bool ok = true;
-    bool more = cur.next(s);
-    if (more && (NT == 2 || wg == 0)) load_q(s);
-    int j = 0, round = 0, seg = 0;
+    int j = 0, round = 0;
     int n_mine = 0;  // tiles this warpgroup has had
-    for (; ok && more; ++seg) {
+    for (int seg = 0; ok && seg_get(seg, s); ++seg) {
+      seg_taken(seg);
+      if (seg == 0 && (NT == 2 || wg == 0)) load_q(s);
       const int node = (s.m * NT + t) * p.tb + row / p.G;
       const bool mine = row < p.RT && node < p.T;               // the row exists
       const bool warp_on = __any_sync(0xffffffffu, mine);
       const int head = s.g * p.G + row % p.G;
-      const bool has_draft = s.t0 < ntd;
+      const bool has_draft = s.t1 > s.nct;
       const int mb = round & 1;
       const uint32_t* am = anc + mb * C::kMaxT * C::kWords + (mine ? node : 0) * C::kWords;
       const int off = draft_off(p, s.ctx);
-      int mine_before = n_mine;
+      const int mine_before = n_mine;
+      bool masks = false;  // this warp has waited for the segment's masks
       float m_run = -INFINITY, l_run = 0.0f;
       for (int tile = s.t0; tile < s.t1; ++tile, ++j) {
         if (NT == 1 && (j & 1) != wg) continue;
@@ -728,11 +775,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         tc_fence_after();
         if (tile == s.t1 - 1) {  // every S of this segment is done: the next one's queries
-          s_next = s;
-          Cursor ahead = cur;
-          if (ahead.next(s_next)) load_q(s_next);
+          Seg ahead;
+          if (seg_get(seg + 1, ahead)) load_q(ahead);
         }
-        if (has_draft && n_mine == mine_before) {
+        if (tile >= s.nct && !masks) {
+          masks = true;
           if (!__all_sync(0xffffffffu, mbar_wait(&bars->mask_full[mb], (round >> 1) & 1, abort, p.status))) {
             ok = false;
             break;
@@ -741,18 +788,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         // keys this row may see, a bit each
         uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
         bool masked = !p.scale_positive;
-        if (tile < ntd) {
+        if (tile >= s.nct) {
           masked = true;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             // bits [32 x - off, +32) of the tile's drafts
-            const int w = tile * 4 + x - (off > 0 ? 1 : 0);
+            const int w = (tile - s.nct) * 4 + x - (off > 0 ? 1 : 0);
             const uint32_t lo = w >= 0 && w < C::kWords ? am[w] : 0u;
             const uint32_t hi = w + 1 >= 0 && w + 1 < C::kWords ? am[w + 1] : 0u;
             see[x] = mine ? (off > 0 ? __funnelshift_r(lo, hi, 32 - off) : lo) : 0u;
           }
         } else {
-          const int lim = s.ctx - (tile - ntd) * kBN;
+          const int lim = s.ctx - tile * kBN;
           if (lim < kBN) {
             masked = true;
 #pragma unroll
@@ -767,7 +814,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
               break;
             }
             uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
-            for (int x = tid & 127; x < (tile_keys(p, tile, s.ctx) - lim) * CH; x += 128)
+            for (int x = tid & 127; x < (tile_keys(p, tile, s.nct, s.ctx) - lim) * CH; x += 128)
               *reinterpret_cast<uint4*>(vt + swizzled_off(lim + x / CH, x % CH, PagedTile<D>::kHalf,
                                                           PagedTile<D>::kGroup)) = make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
@@ -779,9 +826,39 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_addr + s_col + c * 32, sr[c]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_wait_ld(sr[c]);
-          float alpha = 1.0f, rs = 0.0f;
-          // weights 2^(mul s + neg) of the row, P to TMEM and their sum
-          auto weigh = [&](float mul, float neg) {
+          float alpha = 1.0f, rs;
+          // First against the reference max at hand, without a max pass; if some
+          // row's sum says its scores outgrew it (2^64; or NaN), once more from the
+          // registers, with one.
+          bool fast = !masked && __all_sync(0xffffffffu, m_run != -INFINITY);
+          float mul = p.scale_log2;
+          if (masked) {
+            mul = 1.0f;
+#pragma unroll
+            for (int c = 0; c < kBN; ++c)
+              sr[c >> 5][c & 31] = ((see[c >> 5] >> (c & 31)) & 1u)
+                                       ? __float_as_uint(__uint_as_float(sr[c >> 5][c & 31]) * p.scale_log2)
+                                       : 0xff800000u;
+          }
+          for (;;) {
+            if (!fast) {
+              float mx[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+#pragma unroll
+              for (int c = 0; c < kBN; c += 2)
+                mx[(c >> 1) & 7] = fmax3(mx[(c >> 1) & 7], __uint_as_float(sr[c >> 5][c & 31]),
+                                         __uint_as_float(sr[c >> 5][(c & 31) + 1]));
+              // mul > 0: the largest score is the largest product
+              const float mt =
+                  fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * mul;
+              // the reference max moves only when the tile exceeds it by the margin
+              if (mt > m_run + kRescaleMargin || (m_run == -INFINITY && mt != -INFINITY)) {
+                alpha = fast_exp2(m_run - mt);
+                m_run = mt;
+              }
+            }
+            const float neg = m_run == -INFINITY ? 0.0f : -m_run;
             const uint64_t mul2 = f2_pack(mul, mul), neg2 = f2_pack(neg, neg);
             uint64_t sum[4];
 #pragma unroll
@@ -802,41 +879,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             float a0, a1;
             f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
             rs = a0 + a1;
-          };
-          // Against the reference max at hand, without a max pass; if some row's
-          // sum says its scores outgrew it (2^64; or NaN), from the registers again.
-          bool done = false;
-          if (!masked && __all_sync(0xffffffffu, m_run != -INFINITY)) {
-            weigh(p.scale_log2, -m_run);
-            done = __all_sync(0xffffffffu, rs <= 18446744073709551616.0f);
-            if (!done) tmem_wait_st();
-          }
-          if (!done) {
-            float mx[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
-            if (!masked) {
-#pragma unroll
-              for (int c = 0; c < kBN; c += 2)
-                mx[(c >> 1) & 7] = fmax3(mx[(c >> 1) & 7], __uint_as_float(sr[c >> 5][c & 31]),
-                                         __uint_as_float(sr[c >> 5][(c & 31) + 1]));
-            } else {
-#pragma unroll
-              for (int c = 0; c < kBN; ++c) {
-                const float x = ((see[c >> 5] >> (c & 31)) & 1u) ? __uint_as_float(sr[c >> 5][c & 31]) * p.scale_log2
-                                                                 : -INFINITY;
-                sr[c >> 5][c & 31] = __float_as_uint(x);
-                mx[c & 7] = fmaxf(mx[c & 7], x);
-              }
-            }
-            float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-            if (!masked) mt *= p.scale_log2;
-            // the reference max moves only when the tile exceeds it by the margin
-            if (mt > m_run + kRescaleMargin || (m_run == -INFINITY && mt != -INFINITY)) {
-              alpha = fast_exp2(m_run - mt);
-              m_run = mt;
-            }
-            weigh(masked ? 1.0f : p.scale_log2, m_run == -INFINITY ? 0.0f : -m_run);
+            if (!fast || __all_sync(0xffffffffu, rs <= 18446744073709551616.0f)) break;
+            tmem_wait_st();
+            fast = false;
           }
           l_run = l_run * alpha + rs;
           if (n_mine > mine_before && __any_sync(0xffffffffu, alpha != 1.0f)) {
@@ -907,13 +952,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         tc_fence_after();
       }
-      const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+      const bool whole = s.slot < 0;
       // drafts this row sees whose V is not finite, and whether the row's own draft is absent
       bool absent = false;
       uint32_t fix_any = 0u;
-      if (has_draft && NT == 1 && n_mine == mine_before &&
+      if (has_draft && !masks &&
           !__all_sync(0xffffffffu, mbar_wait(&bars->mask_full[mb], (round >> 1) & 1, abort, p.status))) {
-        ok = false;  // this warpgroup had no tile of the segment, and has not seen the masks
+        ok = false;  // this warpgroup had no draft tile, and has not seen the masks
         break;
       }
       if (has_draft && mine) {
@@ -928,11 +973,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       const bool empty = absent || l_run == 0.0f;
       const float inv = empty ? 0.0f : 1.0f / l_run;
       const float lse2 = empty ? -INFINITY : m_run + __log2f(l_run);
-      const int slot = 2 * static_cast<int>(blockIdx.x) + (s.item0 + s.t0 == bars->lo ? 0 : 1);
-      const int64_t prow = static_cast<int64_t>(slot) * p.slot_rows + t * p.RT + row;
+      const int64_t prow = static_cast<int64_t>(s.slot) * p.pitch + t * kBM + row;
       const int64_t obase = s.b * p.out_stride[0] + head * p.out_stride[1] + node * p.out_stride[2];
       if (warp_on) {
-#pragma unroll
+#pragma unroll 1
         for (int cc = 0; cc < D / 32 / (NT == 1 ? 2 : 1); ++cc) {
           const int c = NT == 1 ? wg * (D / 64) + cc : cc;
           uint32_t o[32];
@@ -950,7 +994,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           }
           if (mine) {
             if (fix_any != 0u) {
-              for (int a = max(0, s.t0 * kBN - off); a < min(p.T, s.t1 * kBN - off); ++a) {
+              for (int a = max(0, (s.t0 - s.nct) * kBN - off); a < min(p.T, (s.t1 - s.nct) * kBN - off); ++a) {
                 if (!((am[a >> 5] & bars->bad[mb][a >> 5]) >> (a & 31) & 1u)) continue;
                 const uint16_t* kr = draft_row<D>(p, false, s.b, s.g, a, s.ctx);
                 const uint16_t* vr = draft_row<D>(p, true, s.b, s.g, a, s.ctx);
@@ -971,11 +1015,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = empty ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
             if (!whole) {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
+              float* dst = p.part_o + (static_cast<int64_t>(s.slot) * D + c * 32) * p.pitch + t * kBM + row;
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                     __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+              for (int i = 0; i < 32; ++i) dst[static_cast<int64_t>(i) * p.pitch] = __uint_as_float(o[i]);
             } else if (p.out_bf16) {
               uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + obase + c * 32);
 #pragma unroll
@@ -1011,16 +1053,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         if (lane == 0) mbar_arrive(&bars->mask_empty[mb]);
         ++round;
       }
-      if (!whole && s.t0 == 0 && tid == 0) {  // cut, and it starts here
-        const int node0 = s.m * NT * p.tb;
-        CutItem it;
-        it.b = s.b, it.g = s.g, it.node0 = node0;
-        it.rows = min(p.T - node0, NT * p.tb) * p.G;
-        it.pieces = bars->runs.of(s.item0 + s.tiles - 1) - static_cast<int>(blockIdx.x) + 1;
-        it.first_is_head = s.item0 == bars->lo;
-        p.cuts[blockIdx.x] = it;
-      }
-      more = cur.next(s);
     }
   }
 
@@ -1065,7 +1097,8 @@ cudaError_t launch(const TreeArgs& a, TreeParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // in place on the SMs as the main launch's CTAs leave
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.n_cta), static_cast<unsigned>((p.slot_rows + kMergeRows - 1) / kMergeRows));
+  // groups of 32 rows up to the last that any row tile uses
+  cfg.gridDim = dim3(static_cast<unsigned>(a.n_cta), static_cast<unsigned>(((NT - 1) * kBM + p.RT + 31) / 32));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1081,8 +1114,7 @@ cudaError_t launch(const TreeArgs& a, TreeParams& p, cudaStream_t stream) {
 // Partials of two cut items per CTA (their rows), and a CutItem per CTA.
 size_t tree_partial_bytes(int64_t T, int64_t G, int D, int n_cta) {
   if (T == 0 || G == 0 || G > kBM) return 0;
-  const int64_t group = static_cast<int64_t>(tree_nt(T, G)) * tile_drafts(T, G);  // drafts per item
-  const size_t rows = static_cast<size_t>(2) * n_cta * group * G;
+  const size_t rows = static_cast<size_t>(2) * n_cta * tree_nt(T, G) * kBM;
   const size_t parts = (rows * (D + 1) * sizeof(float) + 255) & ~size_t(255);
   return parts + ((n_cta * sizeof(CutItem) + 255) & ~size_t(255));
 }
@@ -1123,8 +1155,8 @@ cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream) {
   p.out = a.out.data;
   p.out_bf16 = a.out.dtype == ATTN_BF16;
   p.lse = a.lse;
-  p.slot_rows = nt * p.RT;
-  const size_t rows = static_cast<size_t>(2) * a.n_cta * p.slot_rows;
+  p.pitch = nt * kBM;
+  const size_t rows = static_cast<size_t>(2) * a.n_cta * p.pitch;
   p.part_o = static_cast<float*>(a.partials);
   p.part_lse = p.part_o + rows * a.cache.D;
   const size_t parts = (rows * (a.cache.D + 1) * sizeof(float) + 255) & ~size_t(255);

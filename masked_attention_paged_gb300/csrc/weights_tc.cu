@@ -42,6 +42,8 @@ constexpr int kBS = 16;
 constexpr int kBoxBytes = kBM * 128;
 constexpr int kThreads = 512;
 constexpr int kLseRing = 2;
+constexpr int kSegs = 4;  // segments the planner is ahead
+constexpr int kBarBytes = 1024;
 
 template <int D>
 struct Cfg {
@@ -53,8 +55,18 @@ struct Cfg {
   static constexpr int kOffQ = kOffK + KS * kTileBytes;
   static constexpr int kOffLse = kOffQ + QS * kTileBytes;  // [kLseRing][kBN] negated log2 LSEs, -inf: no weight
   static constexpr int kOffBar = kOffLse + kLseRing * kBN * 4;
-  static constexpr int kSmemBytes = kOffBar + 512 + 1024;
+  static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+};
+
+// A run [c0, c1) of one item's chunks: what every warp role works through.  One
+// warp plans them and hands them on in a small ring (as in tree_tc.cu).
+struct Seg {
+  int b;  // -1: the end
+  int g, pair, c0, c1;
+  int n, start, keys;  // of the sequence
+  int slot;            // where its partial sums go; -1: the item is whole
+  int run0, pieces, head;  // a cut item: its first run, its runs, whether that run begins with it
 };
 
 struct Bars {
@@ -63,15 +75,13 @@ struct Bars {
   uint64_t s_full[2][2], s_free[2][2];  // [key tile][score buffer]
   uint64_t l_full[kLseRing], l_empty[kLseRing];
   uint64_t piece_full, piece_go, drained;
-  // this CTA's run, and where in it its first step lies
-  Runs runs;
-  int64_t lo, hi, item0;
-  int b0, g0, pair0, c0;
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  Seg segs[kSegs];
   uint32_t tmem_base;
   int abort, last;
   int odd[kLseRing];  // the chunk has columns without weight (padding, or rows that see nothing)
 };
-static_assert(sizeof(Bars) <= 512, "barrier block outgrew its shared-memory slot");
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block outgrew its shared-memory slot");
 
 struct WeightParams {
   int B, T, Hq, Hkv, G;
@@ -129,54 +139,6 @@ __device__ __forceinline__ SeqWork seq_work(const WeightParams& p, int b, bool r
   return w;
 }
 
-struct Seg {
-  int b, g, pair;
-  int c0, c1;        // chunks [c0, c1)
-  bool whole;
-  int64_t item0, item1;  // the item's steps in the call's order
-  int64_t step0;
-};
-
-struct Cursor {
-  const WeightParams& p;
-  int64_t pos, hi, item0;
-  int b, g, pair, c;  // the next step: chunk c of this item
-  SeqWork w;
-  __device__ Cursor(const WeightParams& prm, const Bars* bars)
-      : p(prm), pos(bars->lo), hi(bars->hi), item0(bars->item0), b(bars->b0), g(bars->g0), pair(bars->pair0),
-        c(bars->c0) {
-    if (pos < hi) w = seq_work(p, b, false);
-  }
-  __device__ bool next(Seg& s) {
-    if (pos >= hi) return false;
-    if (c == w.chunks) {  // the item is done: the next pair, KV head or sequence
-      item0 = pos;
-      if (++pair == w.pairs) {
-        pair = 0;
-        if (++g == p.Hkv) {
-          g = 0;
-          do w = seq_work(p, ++b, false);
-          while (w.steps == 0);
-        }
-      }
-      c = w.first(pair);
-    }
-    const int f = w.first(pair);
-    s.b = b;
-    s.g = g;
-    s.pair = pair;
-    s.c0 = c;
-    s.c1 = static_cast<int>(min(static_cast<int64_t>(w.chunks), c + (hi - pos)));
-    s.item0 = item0;
-    s.item1 = item0 + w.chunks - f;
-    s.step0 = pos;
-    s.whole = s.c0 == f && s.c1 == w.chunks;
-    pos += s.c1 - s.c0;
-    c = s.c1;
-    return true;
-  }
-};
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
@@ -208,13 +170,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->l_full[s], 1);
       mbar_init(&bars->l_empty[s], 8);
     }
+    for (int s = 0; s < kSegs; ++s) {
+      mbar_init(&bars->seg_full[s], 1);
+      mbar_init(&bars->seg_empty[s], 15);  // 4 producers, the issuer, Q's and the LSEs' warps, 8 that sum
+    }
     mbar_init(&bars->piece_full, 8);
     mbar_init(&bars->piece_go, 1);
     mbar_init(&bars->drained, 1);
     bars->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 0) {
+  // the planner's state: the call's runs, and the place of this CTA's first step
+  Runs runs = {};
+  int64_t pos = 0, lo = 0, hi = 0, item0 = 0;
+  int plan_b = 0, plan_g = 0, plan_pair = 0, plan_c = 0;
+  SeqWork work = {};
+  if (warp == 7) {
     int64_t total = 0, mine0 = 0;
     for (int base = 0; base < p.B; base += 32) {
       const int64_t mine =
@@ -224,11 +195,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
-    const Runs runs = Runs::make(total, gridDim.x);
+    runs = Runs::make(total, gridDim.x);
     const int cta = static_cast<int>(blockIdx.x);
-    const int64_t lo = cta < runs.n ? runs.lo(cta) : 0, hi = cta < runs.n ? runs.lo(cta + 1) : 0;
+    if (cta < runs.n) lo = runs.lo(cta), hi = runs.lo(cta + 1);
+    pos = lo;
     int64_t run = 0;
-    int b0 = 0;
     for (int base = 0; base < p.B && lo < hi; base += 32) {
       const int64_t mine =
           base == 0 ? mine0 : (base + lane < p.B ? seq_work(p, base + lane, false).steps * p.Hkv : 0);
@@ -241,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t past = __ballot_sync(0xffffffffu, run + incl > lo);
       if (past != 0) {
         const int l = __ffs(past) - 1;
-        b0 = base + l;
+        plan_b = base + l;
         run += __shfl_sync(0xffffffffu, incl - mine, l);
         break;
       }
@@ -250,25 +221,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_q);
-      bars->runs = runs;
-      bars->lo = lo, bars->hi = hi, bars->b0 = b0;
-      if (lo < hi) {
-        const SeqWork w = seq_work(p, b0, false);
-        const int g = static_cast<int>(div_pos(lo - run, w.steps));
-        int64_t rem = lo - run - g * w.steps;  // step within the (sequence, KV head)
-        int pair;
-        if (rem < static_cast<int64_t>(w.full) * w.chunks) {
-          pair = static_cast<int>(div_pos(rem, w.chunks));
-          rem -= static_cast<int64_t>(pair) * w.chunks;
-        } else {
-          pair = w.full;
-          rem -= static_cast<int64_t>(w.full) * w.chunks;
-          while (rem >= w.chunks - w.first(pair)) rem -= w.chunks - w.first(pair), ++pair;
-        }
-        bars->g0 = g, bars->pair0 = pair;
-        bars->c0 = w.first(pair) + static_cast<int>(rem);
-        bars->item0 = lo - rem;
+    }
+    if (lo < hi) {
+      work = seq_work(p, plan_b, false);
+      plan_g = static_cast<int>(div_pos(lo - run, work.steps));
+      int64_t rem = lo - run - plan_g * work.steps;  // step within the (sequence, KV head)
+      if (rem < static_cast<int64_t>(work.full) * work.chunks) {
+        plan_pair = static_cast<int>(div_pos(rem, work.chunks));
+        rem -= static_cast<int64_t>(plan_pair) * work.chunks;
+      } else {
+        plan_pair = work.full;
+        rem -= static_cast<int64_t>(work.full) * work.chunks;
+        while (rem >= work.chunks - work.first(plan_pair)) rem -= work.chunks - work.first(plan_pair), ++plan_pair;
       }
+      plan_c = work.first(plan_pair) + static_cast<int>(rem);
+      item0 = lo - rem;
     }
   }
   if (warp == 4) {
@@ -281,25 +248,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = bars->tmem_base;
   // scores of tile t, buffer j & 1, at column (2 t + (j & 1)) * 128
 
+  // segment i, for a whole warp; false at the end
+  auto seg_get = [&](int i, Seg& s) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars->seg_full[i % kSegs], (i / kSegs) & 1, abort, p.status))) return false;
+    s = bars->segs[i % kSegs];
+    return s.b >= 0;
+  };
+  auto seg_taken = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->seg_empty[i % kSegs]);
+  };
+
   if (warp < 4) {
     // ------------------------------------------------------------ K
     // warp w, lane i < 4: block 4 w + i of the pair's sixteen, its id read a
     // segment ahead; warps 0, 1 fill the first tile, 2, 3 the second
-    Cursor cur(p, bars);
     Seg s;
     const int t = warp >> 1, place = warp * kWarpBlocks + lane;  // block of the pair
-    auto block_id = [&](const Seg& x, int keys) {
+    auto block_id = [&](const Seg& x) {
       const int blk = x.pair * (kPair / kBS) + place;
-      return lane < kWarpBlocks && blk * kBS < keys ? p.bt[static_cast<int64_t>(x.b) * p.bt_stride + blk] : -1;
+      return lane < kWarpBlocks && blk * kBS < x.keys ? p.bt[static_cast<int64_t>(x.b) * p.bt_stride + blk] : -1;
     };
     int n = t;
-    bool more = cur.next(s);
-    int id_next = more ? block_id(s, cur.w.keys) : -1;
-    while (more) {
+    bool more = seg_get(0, s);
+    int id_next = more ? block_id(s) : -1;
+    for (int i = 0; more; ++i) {
       int id = id_next;
       const int g = s.g;
-      more = cur.next(s);
-      if (more) id_next = block_id(s, cur.w.keys);
+      seg_taken(i);
+      more = seg_get(i + 1, s);
+      if (more) id_next = block_id(s);
       if (id != -1 && (id < 0 || id >= p.num_blocks)) {
         report(p.status, kStatusBounds);
         id = -1;
@@ -318,16 +296,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, abort, p.status); };
-      Cursor cur(p, bars);
-      Seg s;
       int n = 0, j = 0;
       bool ok = true;
-      while (ok && cur.next(s)) {
+      for (int i = 0; ok; ++i) {
+        ok = wait(&bars->seg_full[i % kSegs], i / kSegs);
+        if (!ok) break;
+        const Seg s = bars->segs[i % kSegs];
+        if (s.b < 0) break;
+        mbar_arrive(&bars->seg_empty[i % kSegs]);
         for (int c = s.c0; ok && c < s.c1; ++c, ++j) {
           const int qs = j % C::QS;
           ok = wait(&bars->q_full[qs], j / C::QS);
           if (!ok) break;
-          const int cols = min(p.ct, cur.w.n - c * p.ct) * p.G;
+          const int cols = min(p.ct, s.n - c * p.ct) * p.G;
           const uint32_t idesc = idesc_bf16_f32(kBM, (cols + 15) / 16 * 16, false, false);
           const uint32_t qa = smem_u32(smem + C::kOffQ + qs * C::kTileBytes);
 #pragma unroll
@@ -360,12 +341,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 5) {
     // ------------------------------------------------------------ query chunks
     if (lane == 0) {
-      Cursor cur(p, bars);
-      Seg s;
       int j = 0;
       bool ok = true;
       const uint32_t bytes = static_cast<uint32_t>(p.cr) * D * 2;  // tokens past T arrive as zeros
-      while (ok && cur.next(s)) {
+      for (int i = 0; ok; ++i) {
+        ok = mbar_wait(&bars->seg_full[i % kSegs], (i / kSegs) & 1, abort, p.status);
+        if (!ok) break;
+        const Seg s = bars->segs[i % kSegs];
+        if (s.b < 0) break;
+        mbar_arrive(&bars->seg_empty[i % kSegs]);
         for (int c = s.c0; c < s.c1; ++c, ++j) {
           const int qs = j % C::QS;
           ok = mbar_wait(&bars->q_empty[qs], ((j / C::QS) & 1) ^ 1, abort, p.status);
@@ -384,7 +368,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ their LSEs
     // negated, in log2 units; -inf where a column has no weight (past the
     // chunk, or a row that saw nothing).  Loaded a chunk ahead of the store.
-    Cursor cur(p, bars);
     Seg s;
     int j = 0;
     bool ok = true;
@@ -409,14 +392,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&bars->l_full[sl]);
       return true;
     };
-    while (ok && cur.next(s)) {
+    for (int i = 0; ok && seg_get(i, s); ++i) {
+      seg_taken(i);
       const float* row = p.lse + (static_cast<int64_t>(s.b) * p.Hq + static_cast<int64_t>(s.g) * p.G) * p.T;
       for (int c = s.c0; ok && c < s.c1; ++c, ++j) {
         float next[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int t = c * p.ct + dt[x];
-          next[x] = dt[x] < p.ct && t < cur.w.n ? row[static_cast<int64_t>(dh[x]) * p.T + t] : -INFINITY;
+          next[x] = dt[x] < p.ct && t < s.n ? row[static_cast<int64_t>(dh[x]) * p.T + t] : -INFINITY;
         }
         if (j > 0) ok = publish(j - 1);
 #pragma unroll
@@ -424,19 +408,60 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (ok && j > 0) publish(j - 1);
+  } else if (warp == 7) {
+    // ------------------------------------------------------------ planner
+    for (int i = 0;; ++i) {
+      Seg s = {};
+      s.b = -1;
+      if (pos < hi) {
+        if (plan_c == work.chunks) {  // the item is done: the next pair, KV head or sequence
+          item0 = pos;
+          if (++plan_pair == work.pairs) {
+            plan_pair = 0;
+            if (++plan_g == p.Hkv) {
+              plan_g = 0;
+              do work = seq_work(p, ++plan_b, false);
+              while (work.steps == 0);
+            }
+          }
+          plan_c = work.first(plan_pair);
+        }
+        const int f = work.first(plan_pair);
+        s.b = plan_b, s.g = plan_g, s.pair = plan_pair;
+        s.c0 = plan_c;
+        s.c1 = static_cast<int>(min(static_cast<int64_t>(work.chunks), plan_c + (hi - pos)));
+        s.n = work.n, s.start = work.start, s.keys = work.keys;
+        s.slot = -1;
+        if (s.c0 != f || s.c1 != work.chunks) {
+          s.slot = 2 * static_cast<int>(blockIdx.x) + (pos == lo ? 0 : 1);
+          s.run0 = runs.of(item0);
+          s.pieces = runs.of(item0 + work.chunks - f - 1) - s.run0 + 1;
+          s.head = runs.lo(s.run0) == item0;
+        }
+        pos += s.c1 - plan_c;
+        plan_c = s.c1;
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->seg_empty[i % kSegs], ((i / kSegs) & 1) ^ 1, abort, p.status)))
+        break;
+      if (lane == 0) {
+        bars->segs[i % kSegs] = s;
+        mbar_arrive(&bars->seg_full[i % kSegs]);
+      }
+      if (s.b < 0) break;
+    }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ sums
     const int t = (warp >> 2) & 1;  // key tile
     const int row = (warp & 3) * 32 + lane;
     const int tid = t * kBM + row;
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    Cursor cur(p, bars);
     Seg s;
     int j = 0, pieces = 0;
     bool ok = true;
-    while (ok && cur.next(s)) {
+    for (int i = 0; ok && seg_get(i, s); ++i) {
+      seg_taken(i);
       const int key = s.pair * kPair + t * kBM + row;
-      const bool there = key < cur.w.keys;
+      const bool there = key < s.keys;
       const int blk = there ? p.bt[static_cast<int64_t>(s.b) * p.bt_stride + key / kBS] : -1;
       // The key's sum belongs to this thread alone, so an add without a return
       // value has no order to depend on, and no read to wait for.  A token of
@@ -444,13 +469,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto put = [&](float got) {
         if (blk < 0 || blk >= p.num_blocks) return;
         float* at = p.acc + (static_cast<int64_t>(blk) * p.Hkv + s.g) * kBS + key % kBS;
-        if (key < cur.w.start)
+        if (key < s.start)
           asm volatile("red.global.add.f32 [%0], %1;" ::"l"(at), "f"(got) : "memory");
         else
           *at = got;
       };
       // tokens that see the key: t >= tmin; the warp's last key is seen by the fewest
-      const int tmin = p.causal ? key - cur.w.start : 0;
+      const int tmin = p.causal ? key - s.start : 0;
       const int warp_tmin = __shfl_sync(0xffffffffu, tmin, 31);
       uint64_t sum[4];
 #pragma unroll
@@ -465,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const int t0 = c * p.ct;
-        const int cols = min(p.ct, cur.w.n - t0) * p.G;
+        const int cols = min(p.ct, s.n - t0) * p.G;
         const float* nl = lse_ring + sl * kBN;
         const bool masked = bars->odd[sl] != 0 || warp_tmin > t0;
         const int rel = max(0, min(tmin - t0, p.ct)) * p.G;  // columns >= rel see the key
@@ -526,16 +551,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       float a0, a1;
       f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
       const float got = a0 + a1;
-      if (s.whole) {
+      if (s.slot < 0) {
         put(got);
         continue;
       }
       // a cut item: leave the piece; the last one adds them in order
-      const Runs& runs = bars->runs;
-      const int slot = 2 * static_cast<int>(blockIdx.x) + (s.step0 == bars->lo ? 0 : 1);
-      p.part[static_cast<int64_t>(slot) * kPair + tid] = got;
-      const int p0 = runs.of(s.item0);
-      const int np = runs.of(s.item1 - 1) - p0 + 1;
+      p.part[static_cast<int64_t>(s.slot) * kPair + tid] = got;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->piece_full);
       if (tid < 32 && !__all_sync(0xffffffffu, mbar_wait(&bars->piece_full, pieces & 1, abort, p.status))) {
@@ -556,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (seen == before) break;
           before = seen;
         }
-        const bool last = (now & 0xffffffffull) == static_cast<unsigned long long>(np);
+        const bool last = (now & 0xffffffffull) == static_cast<unsigned long long>(s.pieces);
         if (last) *w = tag;
         bars->last = last;
         mbar_arrive(&bars->piece_go);
@@ -568,11 +589,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++pieces;
       if (bars->last) {
         __threadfence();
-        const bool head = runs.lo(p0) == s.item0;
         float all = 0.f;
 #pragma unroll 4
-        for (int x = 0; x < np; ++x) {
-          const int sl = 2 * (p0 + x) + ((x == 0 && !head) ? 1 : 0);
+        for (int x = 0; x < s.pieces; ++x) {
+          const int sl = 2 * (s.run0 + x) + ((x == 0 && !s.head) ? 1 : 0);
           all += __ldcg(p.part + static_cast<int64_t>(sl) * kPair + tid);
         }
         put(all);
