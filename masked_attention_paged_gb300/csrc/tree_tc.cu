@@ -57,7 +57,8 @@ constexpr int kBS = 16;
 constexpr int kBoxBytes = kBM * 128;
 constexpr float kRescaleMargin = 8.0f;
 constexpr int kBarBytes = 1024;
-constexpr int kSegs = 4;  // segments the planner is ahead
+constexpr int kSegs = 4;   // segments the planner is ahead
+constexpr int kSide = 48;  // draft keys that have a place of their own in shared memory (NT = 1)
 constexpr uint32_t kAbsent = 0x7fc0a5a5u;  // a partial's LSE for the row of an absent draft (a NaN of its own)
 
 template <int D, int NT>
@@ -76,8 +77,12 @@ struct Cfg {
   static constexpr int kOffV = kOffK + KS * kTileBytes;
   static constexpr int kOffAnc = kOffV + VS * kTileBytes;  // [2][kMaxT][kWords] ancestor bits
   static constexpr int kOffPar = kOffAnc + 2 * kMaxT * kWords * 4;  // [kMaxT] parents
-  static constexpr int kOffXch = kOffPar + kMaxT * 4;  // NT = 1: [2][kBM] running max and sum
-  static constexpr int kOffBar = kOffXch + (NT == 1 ? 2 * kBM * 8 : 0);
+  static constexpr int kOffRow = kOffPar + kMaxT * 4;      // [kMaxT] cache rows of the drafts
+  // NT = 1: [2][kBM] running max and sum; K and V of up to kSide draft keys
+  static constexpr int kOffXch = kOffRow + kMaxT * 8;
+  static constexpr int kSideBytes = kSide * D * 2;
+  static constexpr int kOffSide = (kOffXch + (NT == 1 ? 2 * kBM * 8 : 0) + 1023) / 1024 * 1024;
+  static constexpr int kOffBar = kOffSide + (NT == 1 ? 2 * kSideBytes : 0);
   static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   static constexpr uint32_t kColO = 256;  // O of warpgroup w at kColO + w * D; its scores at w * 128
@@ -103,6 +108,7 @@ struct Bars {
   uint64_t o_free;       // NT = 1: both warpgroups have read both accumulators
   uint64_t draft_in[4];  // a draft tile's K and V have landed in K stage ks (and the tile's V stage)
   uint64_t mask_full[2], mask_empty[2];
+  uint64_t side_in, side_ready, side_free;  // drafts in their own place: landed, clean, read
   uint64_t drained;
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   Seg segs[kSegs];
@@ -117,6 +123,7 @@ struct TreeParams {
   int tb, RT;  // drafts and rows (tb * G) of a row tile
   int MP;      // groups of NT row tiles per KV head
   int ntd;     // draft tiles
+  int side;    // the drafts (one tile, at most kSide keys) have a place of their own, not ring stages
   int new_box; // rows of a k_new / v_new box: T up to a multiple of 16, or 128
   float scale_log2;
   int scale_positive;
@@ -179,7 +186,7 @@ struct Layout {
 };
 template <int D>
 __device__ __forceinline__ Layout tile_layout(const TreeParams& p, bool draft) {
-  if (draft && p.k_new != nullptr) return {static_cast<uint32_t>(kBoxBytes), 1024u};
+  if (draft && p.k_new != nullptr) return {static_cast<uint32_t>(p.side ? kSide * 128 : kBoxBytes), 1024u};
   return {PagedTile<D>::kHalf, PagedTile<D>::kGroup};
 }
 
@@ -317,53 +324,58 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     }
     mbar_init(&bars->o_free, 8);
     mbar_init(&bars->drained, 1);
+    mbar_init(&bars->side_in, 1);
+    mbar_init(&bars->side_ready, 1);
+    mbar_init(&bars->side_free, 1);
     bars->abort = 0;
     fence_mbar_init();
   }
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // the planner's state: the call's runs, and the place of this CTA's first tile
   Runs runs = {};
-  int64_t pos = 0, hi = 0, lo = 0;
+  int pos = 0, hi = 0, lo = 0;
   int plan_b = 0, plan_item = 0, plan_t = 0;
   if (warp == 5) {
-    const int64_t items = static_cast<int64_t>(p.Hkv) * p.MP;
-    int64_t total = 0, mine0 = 0;
-    auto seq_items = [&](int b, bool first) -> int64_t {
+    // (all counts are below 2^31: the host has seen to it)
+    const int items = p.Hkv * p.MP;
+    int total = 0, mine0 = 0;
+    auto seq_items = [&](int b, bool first) {
       if (b >= p.B) return 0;
       int ctx;
       bool ok;
-      const int64_t n = seq_tiles(p, b, ctx, ok) * items;
+      const int n = seq_tiles(p, b, ctx, ok) * items;
       if (first && blockIdx.x == 0 && !ok && p.ctx_lens[b] >= 0) report(p.status, kStatusBounds);
       return n;
     };
+#pragma unroll 1
     for (int base = 0; base < p.B; base += 32) {
-      const int64_t mine = seq_items(base + lane, true);
+      const int mine = seq_items(base + lane, true);
       if (base == 0) mine0 = mine;
       total += mine;
     }
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
+    total = __reduce_add_sync(0xffffffffu, total);
     runs = Runs::make(total, gridDim.x);
     const int c = static_cast<int>(blockIdx.x);
     if (c < runs.n) lo = runs.lo(c), hi = runs.lo(c + 1);
     pos = lo;
-    int64_t run = 0;
+    int run = 0;
+#pragma unroll 1
     for (int base = 0; base < p.B && lo < hi; base += 32) {
-      const int64_t mine = base == 0 ? mine0 : seq_items(base + lane, false);
-      int64_t incl = mine;
+      const int mine = base == 0 ? mine0 : seq_items(base + lane, false);
+      int incl = mine;
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, incl, m);
+        const int up = __shfl_up_sync(0xffffffffu, incl, m);
         if (lane >= m) incl += up;
       }
       const uint32_t past = __ballot_sync(0xffffffffu, run + incl > lo);
       if (past != 0) {
         const int l = __ffs(past) - 1;
-        const int64_t local = lo - run - __shfl_sync(0xffffffffu, incl - mine, l);
-        const int64_t tiles = div_pos(__shfl_sync(0xffffffffu, mine, l), items);
+        const int local = lo - run - __shfl_sync(0xffffffffu, incl - mine, l);
+        const int tiles = __shfl_sync(0xffffffffu, mine, l) / items;
         plan_b = base + l;
-        plan_item = static_cast<int>(div_pos(local, tiles));
-        plan_t = static_cast<int>(local - plan_item * tiles);
+        plan_item = local / tiles;
+        plan_t = local - plan_item * tiles;
         break;
       }
       run += __shfl_sync(0xffffffffu, incl, 31);
@@ -380,6 +392,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     tmem_relinquish();
   }
   // query rows past a row tile's box: zeros, once
+#pragma unroll 1
   for (int x = threadIdx.x; x < NT * C::kBoxes * (kBM - p.RT) * 8; x += C::kThreads) {
     const int box = x / ((kBM - p.RT) * 8), y = x % ((kBM - p.RT) * 8);
     *reinterpret_cast<uint4*>(smem + C::kOffQ + box * kBoxBytes + p.RT * 128 + y * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -421,9 +434,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     bool ok = true;
     for (int i = 0; ok && seg_get(i, s); ++i) {
       seg_taken(i);
+      const int t_end = p.side ? min(s.t1, s.nct) : s.t1;  // drafts with their own place take no stage
       const int32_t* bt_row = p.bt + static_cast<int64_t>(s.b) * p.bt_stride;
       auto block_id = [&](int tile) {
-        if (tile >= s.t1 || lane >= kWarpBlocks) return -1;
+        if (tile >= t_end || lane >= kWarpBlocks) return -1;
         int blk, end;  // the block, and where the tile's kind of blocks ends
         if (tile >= s.nct) {
           if (p.k_new != nullptr || !s.there) return -1;
@@ -436,7 +450,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         return blk < end ? bt_row[blk] : -1;
       };
       int id_next = block_id(s.t0);
-      for (int tile = s.t0; tile < s.t1; ++tile, ++j) {
+      for (int tile = s.t0; tile < t_end; ++tile, ++j) {
         int id = id_next;
         id_next = block_id(tile + 1);
         if (id != -1 && (id < 0 || id >= p.num_blocks)) {
@@ -476,31 +490,30 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc_o = idesc_bf16_f32(kBM, D, false, true);
-      // w: the warpgroup whose scores and accumulator these are
-      auto issue_s = [&](int w, int j, int keys, Layout l) {  // S_w = Q K_j^T
+      // w: the warpgroup whose scores and accumulator these are; ka, va: the tile.
+      // A descriptor's start address counts 16 bytes in its low bits.
+      auto issue_s = [&](int w, uint32_t ka, int keys, Layout l) {  // S_w = Q K^T
         const uint32_t idesc_s = idesc_bf16_f32(kBM, keys, false, false);
-        const uint32_t qa = smem_u32(smem + C::kOffQ) + (NT == 2 ? w * C::kTileBytes : 0);
-        const uint32_t ka = smem_u32(smem + C::kOffK + (j % C::KS) * C::kTileBytes);
+        const uint64_t dq = sdesc_sw128(smem_u32(smem + C::kOffQ) + (NT == 2 ? w * C::kTileBytes : 0), 16, 1024);
+        const uint64_t dk = sdesc_sw128(ka, 16, l.group);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          // 16 dims = 32 bytes of a 128-byte row
-          umma_bf16_ss(tmem + w * 128, sdesc_sw128(qa + (kk >> 2) * kBoxBytes + (kk & 3) * 32, 16, 1024),
-                       sdesc_sw128(ka + (kk >> 2) * l.half + (kk & 3) * 32, 16, l.group), idesc_s, kk > 0 ? 1u : 0u);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)  // 16 dims = 32 bytes of a 128-byte row
+          umma_bf16_ss(tmem + w * 128, dq + (kk >> 2) * (kBoxBytes >> 4) + (kk & 3) * 2,
+                       dk + (kk >> 2) * (l.half >> 4) + (kk & 3) * 2, idesc_s, kk > 0 ? 1u : 0u);
         umma_commit(&bars->s_full[w]);
       };
-      auto issue_pv = [&](int w, int j, int keys, Layout l, bool first) {  // O_w (+)= P_w V_j
-        const uint32_t va = smem_u32(smem + C::kOffV + (j % C::VS) * C::kTileBytes);
-#pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk)
-          if (kk * 16 < keys)
-            umma_bf16_ts(tmem + C::kColO + w * D, tmem + w * 128 + kk * 8, sdesc_sw128(va + kk * 2 * l.group, l.half, l.group),
-                         idesc_o, (!first || kk > 0) ? 1u : 0u);
+      auto issue_pv = [&](int w, uint32_t va, int keys, Layout l, bool first) {  // O_w (+)= P_w V
+        const uint64_t dv = sdesc_sw128(va, l.half, l.group);
+#pragma unroll 1
+        for (int kk = 0; kk * 16 < keys; ++kk)
+          umma_bf16_ts(tmem + C::kColO + w * D, tmem + w * 128 + kk * 8, dv + kk * (l.group >> 3), idesc_o,
+                       (!first || kk > 0) ? 1u : 0u);
         umma_commit(&bars->o_done[w]);
       };
       auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, abort, p.status); };
-      auto wait_k = [&](int j) { return wait(&bars->k_full[j % C::KS], j / C::KS); };
-      auto wait_v = [&](int j) { return wait(&bars->v_full[j % C::VS], j / C::VS); };
+      auto k_at = [&](int r) { return smem_u32(smem + C::kOffK + (r % C::KS) * C::kTileBytes); };
+      auto v_at = [&](int r) { return smem_u32(smem + C::kOffV + (r % C::VS) * C::kTileBytes); };
+      int r = 0, round = 0;  // ring tiles, and drafts in their own place, so far
       int j = 0;
       bool ok = true;
       for (int seg = 0; ok; ++seg) {
@@ -514,59 +527,68 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         auto lay = [&](int x) { return tile_layout<D>(p, s.t0 + x >= s.nct); };
         for (int t = 0; t < NT; ++t) ok = ok && wait(&bars->q_full[t], seg);
         if constexpr (NT == 1) {
-          // tile j is warpgroup j & 1's; S runs two tiles ahead of PV
-          for (int x = 0; ok && x < min(2, n); ++x) {
-            ok = wait_k(j + x);
-            if (!ok) break;
+          // tile j is warpgroup j & 1's; S runs two tiles ahead of PV.  x: tile of the
+          // segment (r + x: its ring tile); the drafts, last, may lie aside.
+          auto aside = [&](int x) { return p.side && s.t0 + x >= s.nct; };
+          auto scores = [&](int x) {
+            if (aside(x)) {
+              if (!wait(&bars->side_ready, round)) return false;
+              tc_fence_after();
+              issue_s((j + x) & 1, smem_u32(smem + C::kOffSide), keys(x), lay(x));
+              return true;
+            }
+            if (!wait(&bars->k_full[(r + x) % C::KS], (r + x) / C::KS)) return false;
             tc_fence_after();
-            issue_s((j + x) & 1, j + x, keys(x), lay(x));
-            umma_commit(&bars->k_empty[(j + x) % C::KS]);
-          }
-          // the accumulators of the segment before have been read
-          if (seg > 0) ok = ok && wait(&bars->o_free, seg - 1);
-          for (int x = 0; ok && x < n; ++x, ++j) {
-            ok = wait(&bars->p_full[j & 1], j >> 1) && wait_v(j);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(j & 1, j, keys(x), lay(x), x < 2);
-            umma_commit(&bars->v_empty[j % C::VS]);
-            if (x + 2 < n) {
-              ok = wait_k(j + 2);
+            issue_s((j + x) & 1, k_at(r + x), keys(x), lay(x));
+            umma_commit(&bars->k_empty[(r + x) % C::KS]);
+            return true;
+          };
+#pragma unroll 1
+          for (int x = 0; ok && x < n + 2; ++x) {
+            if (x >= 2) {  // P_(x - 2) V, before S_x takes its scores' place
+              const int y = x - 2;
+              // the accumulators of the segment before have been read
+              if (y == 0 && seg > 0) ok = wait(&bars->o_free, seg - 1);
+              ok = ok && wait(&bars->p_full[(j + y) & 1], (j + y) >> 1) &&
+                   (aside(y) || wait(&bars->v_full[(r + y) % C::VS], (r + y) / C::VS));
               if (!ok) break;
               tc_fence_after();
-              issue_s(j & 1, j + 2, keys(x + 2), lay(x + 2));
-              umma_commit(&bars->k_empty[(j + 2) % C::KS]);
+              issue_pv((j + y) & 1, aside(y) ? smem_u32(smem + C::kOffSide + C::kSideBytes) : v_at(r + y), keys(y),
+                       lay(y), y < 2);
+              umma_commit(aside(y) ? &bars->side_free : &bars->v_empty[(r + y) % C::VS]);
             }
+            if (x < n) ok = scores(x);
           }
+          if (!ok) break;
+          j += n;
+          const bool had = p.side && s.t1 > s.nct;
+          r += had ? n - 1 : n;
+          round += had;
         } else {
+          auto wait_k = [&](int x) { return wait(&bars->k_full[x % C::KS], x / C::KS); };
+          auto wait_v = [&](int x) { return wait(&bars->v_full[x % C::VS], x / C::VS); };
           // PV_A, S_A', PV_B, S_B': each tile's softmax runs under the other's MMAs
-          ok = ok && wait_k(j);
-          if (ok) {
-            tc_fence_after();
-            issue_s(0, j, keys(0), lay(0));
-            issue_s(1, j, keys(0), lay(0));
-            umma_commit(&bars->k_empty[j % C::KS]);
-          }
-          for (int x = 0; ok && x < n; ++x, ++j) {
-            ok = wait(&bars->p_full[0], j) && wait_v(j);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(0, j, keys(x), lay(x), x == 0);
-            if (x + 1 < n) {
-              ok = wait_k(j + 1);
-              if (!ok) break;
-              tc_fence_after();
-              issue_s(0, j + 1, keys(x + 1), lay(x + 1));
+#pragma unroll 1
+          for (int x = -1; ok && x < n; ++x) {
+#pragma unroll 1
+            for (int w = 0; ok && w < 2; ++w) {
+              if (x >= 0) {
+                ok = wait(&bars->p_full[w], j) && (w > 0 || wait_v(j));
+                if (!ok) break;
+                tc_fence_after();
+                issue_pv(w, v_at(j), keys(x), lay(x), x == 0);
+                if (w == 1) umma_commit(&bars->v_empty[j % C::VS]);
+              }
+              if (x + 1 < n) {
+                const int jn = x < 0 ? j : j + 1;
+                ok = w > 0 || wait_k(jn);
+                if (!ok) break;
+                tc_fence_after();
+                issue_s(w, k_at(jn), keys(x + 1), lay(x + 1));
+                if (w == 1) umma_commit(&bars->k_empty[jn % C::KS]);
+              }
             }
-            ok = wait(&bars->p_full[1], j);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(1, j, keys(x), lay(x), x == 0);
-            umma_commit(&bars->v_empty[j % C::VS]);
-            if (x + 1 < n) {
-              issue_s(1, j + 1, keys(x + 1), lay(x + 1));
-              umma_commit(&bars->k_empty[(j + 1) % C::KS]);
-            }
+            if (x >= 0) ++j;
           }
         }
       }
@@ -594,7 +616,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         s.g = plan_item / p.MP;
         s.m = plan_item % p.MP;
         s.t0 = plan_t;
-        s.t1 = static_cast<int>(min(static_cast<int64_t>(tiles), plan_t + (hi - pos)));
+        s.t1 = min(tiles, plan_t + (hi - pos));
         s.nct = tiles - p.ntd;
         s.ctx = ctx;
         s.there = there;
@@ -624,6 +646,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     constexpr int NL = 64;
     const int lt = threadIdx.x - 192;
     Seg s;
+    int64_t* dst_row = reinterpret_cast<int64_t*>(smem + C::kOffRow);
     int j0 = 0, round = 0;
     uint32_t in = 0u;  // bit ks: parity of the next draft tile in K stage ks
     bool ok = true;
@@ -639,17 +662,54 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->mask_empty[mb], ((round >> 1) & 1) ^ 1, abort, p.status));
         ok = !named_bar_or(1, NL, !ok);
         if (!ok) break;
+        const int off = draft_off(p, s.ctx);
+        uint8_t* k_side = smem + C::kOffSide;
+        uint8_t* v_side = k_side + C::kSideBytes;
+        if (NT == 1 && p.side) {
+          // into their own place, once the drafts before have been read
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->side_free, (round & 1) ^ 1, abort, p.status));
+          ok = !named_bar_or(1, NL, !ok);
+          if (!ok) break;
+          if (warp == 6) {
+            int id = -1;  // lane i: block i of the cached drafts
+            const int blk = s.ctx / kBS + lane;
+            if (p.k_new == nullptr && s.there && lane < kSide / kBS && blk < (s.ctx + p.T + kBS - 1) / kBS) {
+              id = p.bt[static_cast<int64_t>(s.b) * p.bt_stride + blk];
+              if (id < 0 || id >= p.num_blocks) {
+                report(p.status, kStatusBounds);
+                id = -1;
+              }
+            }
+            const int blocks = __popc(__ballot_sync(0xffffffffu, id >= 0));
+            if (lane == 0)
+              mbar_arrive_expect_tx(&bars->side_in, 2u * (p.k_new != nullptr ? p.new_box : blocks * kBS) * D * 2);
+            __syncwarp();
+            if (p.k_new != nullptr) {
+              if (lane < 2 * C::kBoxes) {
+                const int x = lane % C::kBoxes;
+                tma_load_5d((lane < C::kBoxes ? k_side : v_side) + x * kSide * 128,
+                            lane < C::kBoxes ? &tm_kn : &tm_vn, &bars->side_in, x * 64, 0, 0, s.g, s.b);
+              }
+            } else {
+              load_block<D>(k_side, lane, &tm_k, &bars->side_in, id, p.Hkv, s.g);
+              load_block<D>(v_side, lane, &tm_v, &bars->side_in, id, p.Hkv, s.g);
+            }
+          }
+        }
+#pragma unroll 1
         for (int t = lt; t < p.T; t += NL) par[t] = s.there ? p.parents[s.b * p.par_stride + t] : -2;
         if (lt < 8) bars->bad[mb][lt] = 0u;
         named_bar_sync(1, NL);
         // node t's ancestors, itself included: parents come before children, so
         // a walk up ends within t steps; absent (no bits) unless it ends at -1
+#pragma unroll 1
         for (int t = lt; t < p.T; t += NL) {
           uint32_t w[C::kWords];
 #pragma unroll
           for (int x = 0; x < C::kWords; ++x) w[x] = 0u;
           int a = t;
           bool there = true;
+#pragma unroll 1
           for (;;) {
             const int up = par[a];
             if (up >= a) report(p.status, kStatusBounds);
@@ -665,38 +725,39 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           }
 #pragma unroll
           for (int x = 0; x < C::kWords; ++x) am[t * C::kWords + x] = there ? w[x] : 0u;
+          // present and to be cached: where
+          dst_row[t] = there && p.k_new != nullptr && s.m == 0 ? cache_row(p, s.b, s.g, s.ctx + t) : -1;
         }
         named_bar_sync(1, NL);
-        const int off = draft_off(p, s.ctx);
+#pragma unroll 1
         for (int tile = max(s.t0, s.nct); ok && tile < s.t1; ++tile) {
           const int j = j0 + tile - s.t0;
           const int ks = j % C::KS, vs = j % C::VS;
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->draft_in[ks], (in >> ks) & 1u, abort, p.status));
-          in ^= 1u << ks;
+          const bool side = NT == 1 && p.side;
+          ok = __all_sync(0xffffffffu, side ? mbar_wait(&bars->side_in, round & 1, abort, p.status)
+                                            : mbar_wait(&bars->draft_in[ks], (in >> ks) & 1u, abort, p.status));
+          if (!side) in ^= 1u << ks;
           ok = !named_bar_or(1, NL, !ok);
           if (!ok) break;
-          const uint8_t* kt = smem + C::kOffK + ks * C::kTileBytes;
-          uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
+          const uint8_t* kt = side ? k_side : smem + C::kOffK + ks * C::kTileBytes;
+          uint8_t* vt = side ? v_side : smem + C::kOffV + vs * C::kTileBytes;
           const int rows = tile_keys(p, tile, s.nct, s.ctx);
           const Layout lay = tile_layout<D>(p, true);
-          const bool append = p.k_new != nullptr && s.m == 0;
-#pragma unroll 2
+#pragma unroll 1
           for (int x = lt; x < rows * CH; x += NL) {
             const int r = x / CH, ch = x % CH, node = (tile - s.nct) * kBN + r - off;
-            uint4* vp = reinterpret_cast<uint4*>(vt + swizzled_off(r, ch, lay.half, lay.group));
+            const uint32_t at = swizzled_off(r, ch, lay.half, lay.group);
+            uint4* vp = reinterpret_cast<uint4*>(vt + at);
             // present: its own bit is set
             if (node < 0 || node >= p.T || !((am[node * C::kWords + (node >> 5)] >> (node & 31)) & 1u)) {
               *vp = make_uint4(0u, 0u, 0u, 0u);
               continue;
             }
             uint4 vw = *vp;
-            if (append) {
-              const int64_t row = cache_row(p, s.b, s.g, s.ctx + node);
-              if (row >= 0) {
-                *reinterpret_cast<uint4*>(p.kc + row * D + ch * 8) =
-                    *reinterpret_cast<const uint4*>(kt + swizzled_off(r, ch, lay.half, lay.group));
-                *reinterpret_cast<uint4*>(p.vc + row * D + ch * 8) = vw;
-              }
+            const int64_t row = dst_row[node];
+            if (row >= 0) {
+              *reinterpret_cast<uint4*>(p.kc + row * D + ch * 8) = *reinterpret_cast<const uint4*>(kt + at);
+              *reinterpret_cast<uint4*>(p.vc + row * D + ch * 8) = vw;
             }
             bool bad = false;
             vw.x = finite_pair(vw.x, bad), vw.y = finite_pair(vw.y, bad);
@@ -708,7 +769,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           }
           fence_proxy_async_smem();
           named_bar_sync(1, NL);
-          if (lt == 0) {
+          if (lt == 0 && side) mbar_arrive(&bars->side_ready);
+          if (lt == 0 && !side) {
             for (int x = 0; x < 2; ++x) {  // for both producers of each
               mbar_arrive(&bars->k_full[ks]);
               mbar_arrive(&bars->v_full[vs]);
@@ -751,8 +813,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 
     Seg s;
     bool ok = true;
-    int j = 0, round = 0;
-    int n_mine = 0;  // tiles this warpgroup has had
+    int j = 0, jr = 0, round = 0;  // tiles, ring tiles, segments with drafts so far
+    int n_mine = 0;                // tiles this warpgroup has had
     for (int seg = 0; ok && seg_get(seg, s); ++seg) {
       seg_taken(seg);
       if (seg == 0 && (NT == 2 || wg == 0)) load_q(s);
@@ -767,7 +829,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       const int mine_before = n_mine;
       bool masks = false;  // this warp has waited for the segment's masks
       float m_run = -INFINITY, l_run = 0.0f;
-      for (int tile = s.t0; tile < s.t1; ++tile, ++j) {
+      for (int tile = s.t0; tile < s.t1; ++tile, ++j, jr += !(p.side && tile > s.nct)) {
         if (NT == 1 && (j & 1) != wg) continue;
         if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[wg], n_mine & 1, abort, p.status))) {
           ok = false;
@@ -785,35 +847,34 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             break;
           }
         }
-        // keys this row may see, a bit each
-        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+        // which of the tile's keys [32 x, +32) this row may see, a bit each
+        const int lim = s.ctx - tile * kBN;  // of a context tile
         bool masked = !p.scale_positive;
+        auto see = [&](int x) -> uint32_t {
+          if (tile < s.nct) {
+            const int left = lim - x * 32;
+            return left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u);
+          }
+          if (!mine) return 0u;
+          // bits [32 x - off, +32) of the tile's drafts
+          const int w = (tile - s.nct) * 4 + x - (off > 0 ? 1 : 0);
+          const uint32_t lo = w >= 0 && w < C::kWords ? am[w] : 0u;
+          if (off == 0) return lo;
+          return __funnelshift_r(lo, w + 1 < C::kWords ? am[w + 1] : 0u, 32 - off);
+        };
         if (tile >= s.nct) {
           masked = true;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            // bits [32 x - off, +32) of the tile's drafts
-            const int w = (tile - s.nct) * 4 + x - (off > 0 ? 1 : 0);
-            const uint32_t lo = w >= 0 && w < C::kWords ? am[w] : 0u;
-            const uint32_t hi = w + 1 >= 0 && w + 1 < C::kWords ? am[w + 1] : 0u;
-            see[x] = mine ? (off > 0 ? __funnelshift_r(lo, hi, 32 - off) : lo) : 0u;
-          }
         } else {
-          const int lim = s.ctx - tile * kBN;
           if (lim < kBN) {
             masked = true;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int left = lim - x * 32;
-              see[x] = left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u);
-            }
             // V rows past the context: whatever the slots hold, or nothing loaded
-            const int vs = j % C::VS;
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs], (j / C::VS) & 1, abort, p.status))) {
+            const int vs = jr % C::VS;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs], (jr / C::VS) & 1, abort, p.status))) {
               ok = false;
               break;
             }
             uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
+#pragma unroll 1
             for (int x = tid & 127; x < (tile_keys(p, tile, s.nct, s.ctx) - lim) * CH; x += 128)
               *reinterpret_cast<uint4*>(vt + swizzled_off(lim + x / CH, x % CH, PagedTile<D>::kHalf,
                                                           PagedTile<D>::kGroup)) = make_uint4(0u, 0u, 0u, 0u);
@@ -821,68 +882,106 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           }
         }
         if (warp_on) {
-          uint32_t sr[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_addr + s_col + c * 32, sr[c]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_wait_ld(sr[c]);
           float alpha = 1.0f, rs;
-          // First against the reference max at hand, without a max pass; if some
-          // row's sum says its scores outgrew it (2^64; or NaN), once more from the
-          // registers, with one.
-          bool fast = !masked && __all_sync(0xffffffffu, m_run != -INFINITY);
-          float mul = p.scale_log2;
-          if (masked) {
-            mul = 1.0f;
-#pragma unroll
-            for (int c = 0; c < kBN; ++c)
-              sr[c >> 5][c & 31] = ((see[c >> 5] >> (c & 31)) & 1u)
-                                       ? __float_as_uint(__uint_as_float(sr[c >> 5][c & 31]) * p.scale_log2)
-                                       : 0xff800000u;
-          }
-          for (;;) {
-            if (!fast) {
-              float mx[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
-#pragma unroll
-              for (int c = 0; c < kBN; c += 2)
-                mx[(c >> 1) & 7] = fmax3(mx[(c >> 1) & 7], __uint_as_float(sr[c >> 5][c & 31]),
-                                         __uint_as_float(sr[c >> 5][(c & 31) + 1]));
-              // mul > 0: the largest score is the largest product
-              const float mt =
-                  fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * mul;
-              // the reference max moves only when the tile exceeds it by the margin
-              if (mt > m_run + kRescaleMargin || (m_run == -INFINITY && mt != -INFINITY)) {
-                alpha = fast_exp2(m_run - mt);
-                m_run = mt;
-              }
+          // the reference max moves only when the tile's exceeds it by the margin
+          auto raise = [&](float mt) {
+            if (mt > m_run + kRescaleMargin || (m_run == -INFINITY && mt != -INFINITY)) {
+              alpha = fast_exp2(m_run - mt);
+              m_run = mt;
             }
-            const float neg = m_run == -INFINITY ? 0.0f : -m_run;
+          };
+          // weights 2^(mul s + neg) of 32 scores: P to TMEM, and their sums
+          auto weigh32 = [&](const uint32_t (&x)[32], int c, float mul, float neg, uint64_t (&sum)[4]) {
             const uint64_t mul2 = f2_pack(mul, mul), neg2 = f2_pack(neg, neg);
-            uint64_t sum[4];
+            uint32_t pw[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t pw[16];
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                float x0, x1;
-                f2_unpack(ffma2(f2_pack(__uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1])), mul2, neg2), x0, x1);
-                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                pw[i >> 1] = pack_bf16x2(p0, p1);
-                sum[(i >> 1) & 3] = fadd2(sum[(i >> 1) & 3], f2_pack(p0, p1));
-              }
-              tmem_st16(tmem + lane_addr + s_col + c * 16, pw);
+            for (int i = 0; i < 32; i += 2) {
+              float x0, x1;
+              f2_unpack(ffma2(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), mul2, neg2), x0, x1);
+              const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+              pw[i >> 1] = pack_bf16x2(p0, p1);
+              sum[(i >> 1) & 3] = fadd2(sum[(i >> 1) & 3], f2_pack(p0, p1));
             }
-            float a0, a1;
-            f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
-            rs = a0 + a1;
-            if (!fast || __all_sync(0xffffffffu, rs <= 18446744073709551616.0f)) break;
-            tmem_wait_st();
-            fast = false;
+            tmem_st16(tmem + lane_addr + s_col + c * 16, pw);
+          };
+          // scores in log2 units, -inf where the row may not look
+          auto mask32 = [&](uint32_t (&x)[32], uint32_t w) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              x[i] = ((w >> i) & 1u) ? __float_as_uint(__uint_as_float(x[i]) * p.scale_log2) : 0xff800000u;
+          };
+          auto max32 = [&](const uint32_t (&x)[32], float (&mx)[4]) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+          };
+          uint64_t sum[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if constexpr (NT == 1) {
+            // Bound by HBM, with time to spare: two rolled passes over the scores in
+            // TMEM, 32 at a time.  (Code that runs once costs its fetch: unrolled
+            // over the 128 scores, a first tile took 2.3 us and this warp's code
+            // displaced the producers'.)  The second pass writes P over scores that
+            // it has read: chunk c's 16 columns end before chunk c + 1's begin.
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t x[32];
+              tmem_ld32(tmem + lane_addr + s_col + c * 32, x);
+              tmem_wait_ld(x);
+              if (masked) mask32(x, see(c));
+              max32(x, mx);
+            }
+            const float mul = masked ? 1.0f : p.scale_log2;  // > 0
+            raise(fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * mul);
+            const float neg = m_run == -INFINITY ? 0.0f : -m_run;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t x[32];
+              tmem_ld32(tmem + lane_addr + s_col + c * 32, x);
+              tmem_wait_ld(x);
+              if (masked) mask32(x, see(c));
+              weigh32(x, c, mul, neg, sum);
+            }
+          } else {
+            // Bound by the exponentials: all scores in registers at once, and first
+            // against the reference max at hand, without a max pass; if some row's
+            // sum says its scores outgrew it (2^64; or NaN), once more with one.
+            uint32_t sr[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_addr + s_col + c * 32, sr[c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_wait_ld(sr[c]);
+            bool fast = !masked && __all_sync(0xffffffffu, m_run != -INFINITY);
+            float mul = p.scale_log2;
+            if (masked) {
+              mul = 1.0f;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) mask32(sr[c], see(c));
+            }
+            for (;;) {
+              if (!fast) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) max32(sr[c], mx);
+                raise(fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * mul);
+              }
+              const float neg = m_run == -INFINITY ? 0.0f : -m_run;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) weigh32(sr[c], c, mul, neg, sum);
+              if (!fast) break;
+              float a0, a1;
+              f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
+              if (__all_sync(0xffffffffu, a0 + a1 <= 18446744073709551616.0f)) break;
+              tmem_wait_st();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
+              fast = false;
+            }
           }
+          float a0, a1;
+          f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
+          rs = a0 + a1;
           l_run = l_run * alpha + rs;
           if (n_mine > mine_before && __any_sync(0xffffffffu, alpha != 1.0f)) {
             if (!__all_sync(0xffffffffu, o_wait(n_mine - 1))) {
@@ -890,7 +989,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
               break;
             }
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
               tmem_ld32(tmem + lane_addr + o_col + c * 32, o);
@@ -976,24 +1075,23 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       const int64_t prow = static_cast<int64_t>(s.slot) * p.pitch + t * kBM + row;
       const int64_t obase = s.b * p.out_stride[0] + head * p.out_stride[1] + node * p.out_stride[2];
       if (warp_on) {
+        // 16 columns at a time, rolled (it runs once a segment: its code's fetch counts)
 #pragma unroll 1
-        for (int cc = 0; cc < D / 32 / (NT == 1 ? 2 : 1); ++cc) {
-          const int c = NT == 1 ? wg * (D / 64) + cc : cc;
-          uint32_t o[32];
-          tmem_ld32(tmem + lane_addr + (NT == 1 ? C::kColO : o_col) + c * 32, o);
-          tmem_wait_ld(o);
+        for (int c = NT == 1 ? wg * (D / 2) : 0; c < (NT == 1 ? (wg + 1) * (D / 2) : D); c += 16) {
+          uint32_t o[16];
+          tmem_ld16_now(tmem + lane_addr + (NT == 1 ? C::kColO : o_col) + c, o);
           if constexpr (NT == 1) {
-            uint32_t o1[32];
-            tmem_ld32(tmem + lane_addr + C::kColO + D + c * 32, o1);
-            tmem_wait_ld(o1);
+            uint32_t o1[16];
+            tmem_ld16_now(tmem + lane_addr + C::kColO + D + c, o1);
             // an accumulator of weight 0 may hold anything
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < 16; ++i)
               o[i] = __float_as_uint((f0 != 0.0f ? f0 * __uint_as_float(o[i]) : 0.0f) +
                                      (f1 != 0.0f ? f1 * __uint_as_float(o1[i]) : 0.0f));
           }
           if (mine) {
             if (fix_any != 0u) {
+#pragma unroll 1
               for (int a = max(0, (s.t0 - s.nct) * kBN - off); a < min(p.T, (s.t1 - s.nct) * kBN - off); ++a) {
                 if (!((am[a >> 5] & bars->bad[mb][a >> 5]) >> (a & 31) & 1u)) continue;
                 const uint16_t* kr = draft_row<D>(p, false, s.b, s.g, a, s.ctx);
@@ -1001,35 +1099,36 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 const uint16_t* qr = p.q + s.b * p.q_stride[0] + head * p.q_stride[1] + node * p.q_stride[2];
                 if (kr == nullptr || vr == nullptr) continue;
                 float dot = 0.f;
+#pragma unroll 1
                 for (int d = 0; d < D; ++d)
                   dot = fmaf(__uint_as_float(static_cast<uint32_t>(qr[d]) << 16),
                              __uint_as_float(static_cast<uint32_t>(kr[d]) << 16), dot);
                 const float w = fast_exp2(dot * p.scale_log2 - m_run);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float v = __uint_as_float(static_cast<uint32_t>(vr[c * 32 + i]) << 16);
+                for (int i = 0; i < 16; ++i) {
+                  const float v = __uint_as_float(static_cast<uint32_t>(vr[c + i]) << 16);
                   if (!isfinite(v)) o[i] = __float_as_uint(fmaf(w, v, __uint_as_float(o[i])));
                 }
               }
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = empty ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+            for (int i = 0; i < 16; ++i) o[i] = empty ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
             if (!whole) {
-              float* dst = p.part_o + (static_cast<int64_t>(s.slot) * D + c * 32) * p.pitch + t * kBM + row;
+              float* dst = p.part_o + (static_cast<int64_t>(s.slot) * D + c) * p.pitch + t * kBM + row;
 #pragma unroll
-              for (int i = 0; i < 32; ++i) dst[static_cast<int64_t>(i) * p.pitch] = __uint_as_float(o[i]);
+              for (int i = 0; i < 16; ++i) dst[i * (NT * kBM)] = __uint_as_float(o[i]);
             } else if (p.out_bf16) {
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + obase + c * 32);
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + obase + c);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < 2; ++i)
                 dst[i] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
                                     pack_bf16x2(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
                                     pack_bf16x2(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
                                     pack_bf16x2(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])));
             } else {
-              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + obase + c * 32);
+              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + obase + c);
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
+              for (int i = 0; i < 4; ++i)
                 dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                      __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
             }
@@ -1131,6 +1230,7 @@ cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream) {
   p.RT = p.tb * p.G;
   p.MP = (p.T + nt * p.tb - 1) / (nt * p.tb);
   p.new_box = std::min(kBN, (p.T + 15) / 16 * 16);
+  p.side = nt == 1 && p.T + (a.k_new.data != nullptr ? 0 : kBS - 1) <= kSide;
   p.ntd = a.k_new.data != nullptr ? (p.T + kBN - 1) / kBN : (p.T + kBS - 1 + kBN - 1) / kBN;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.scale_positive = p.scale_log2 > 0.0f;
@@ -1156,6 +1256,9 @@ cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream) {
   p.out_bf16 = a.out.dtype == ATTN_BF16;
   p.lse = a.lse;
   p.pitch = nt * kBM;
+  // the planner counts tiles in 31 bits
+  const int64_t most = static_cast<int64_t>(p.B) * p.Hkv * p.MP * ((static_cast<int64_t>(p.max_blocks) * kBS + kBN - 1) / kBN + p.ntd);
+  if (most > 0x7fffffff) return cudaErrorInvalidValue;
   const size_t rows = static_cast<size_t>(2) * a.n_cta * p.pitch;
   p.part_o = static_cast<float*>(a.partials);
   p.part_lse = p.part_o + rows * a.cache.D;

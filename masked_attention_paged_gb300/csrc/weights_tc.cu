@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   // the planner's state: the call's runs, and the place of this CTA's first step
-  Runs runs = {};
+  Runs64 runs = {};
   int64_t pos = 0, lo = 0, hi = 0, item0 = 0;
   int plan_b = 0, plan_g = 0, plan_pair = 0, plan_c = 0;
   SeqWork work = {};
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
-    runs = Runs::make(total, gridDim.x);
+    runs = Runs64::make(total, gridDim.x);
     const int cta = static_cast<int>(blockIdx.x);
     if (cta < runs.n) lo = runs.lo(cta), hi = runs.lo(cta + 1);
     pos = lo;
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       plan_g = static_cast<int>(div_pos(lo - run, work.steps));
       int64_t rem = lo - run - plan_g * work.steps;  // step within the (sequence, KV head)
       if (rem < static_cast<int64_t>(work.full) * work.chunks) {
-        plan_pair = static_cast<int>(div_pos(rem, work.chunks));
+        plan_pair = static_cast<int>(div_pos(rem, static_cast<int64_t>(work.chunks)));
         rem -= static_cast<int64_t>(plan_pair) * work.chunks;
       } else {
         plan_pair = work.full;
