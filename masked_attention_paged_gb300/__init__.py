@@ -113,6 +113,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = False):
     """Load libattn.so (built in-tree by ``__graft_entry__.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -239,7 +241,8 @@ def _ptr(t: Optional[torch.Tensor], name: str = "tensor"):
     """Device pointer of t (None passes through as NULL)."""
     if t is None:
         return None
-    _require(_on_device(t), f"{name} must be on a CUDA device")
+    if not _on_device(t):
+        raise ValueError(f"{name} must be on a CUDA device")
     return t.data_ptr()
 
 
@@ -748,11 +751,13 @@ def _check_devices(name: str, *tensors: Optional[torch.Tensor]):
     """The kernels run on the current device: a tensor of another one is refused."""
     current = -1
     for t in tensors:
-        if t is not None and t.is_cuda:
-            if current < 0:
-                current = torch.cuda.current_device()
-            if t.get_device() != current:
-                raise ValueError(f"{name} runs on the current device cuda:{current}, got a tensor on {t.device}")
+        if t is not None:
+            device = t.get_device()  # -1 on the CPU: refused where its pointer is taken
+            if device != current and device >= 0:
+                if current < 0:
+                    current = torch.cuda.current_device()
+                if device != current:
+                    raise ValueError(f"{name} runs on the current device cuda:{current}, got a tensor on {t.device}")
 
 
 def _check_rope(positions: torch.Tensor, freqs: torch.Tensor, B: int, T: int, D: int):
