@@ -12,6 +12,8 @@ fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 import struct
@@ -204,6 +206,28 @@ def _cache_bytes(k_cache: torch.Tensor, v_cache: torch.Tensor) -> bytes:
         raise ValueError("K and V caches must be on a CUDA device")
     nb, heads, bs, D = k_cache.shape
     return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), _dtype_code(k_cache), bs, nb, heads, D)
+
+
+_marshal = None      # the compiled packer (marshal.cpp), or None
+_marshal_tried = False
+
+
+def _pack(fmt: str, *args):
+    """A C entry point's arguments in one step, or None: the caller then takes
+    them one by one, with every check worded."""
+    global _marshal, _marshal_tried
+    if not _marshal_tried:
+        _marshal_tried = True
+        path = _build.marshal_path()
+        if os.path.exists(path):
+            loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
+            try:
+                _marshal = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+            except ImportError:  # built against another Python: the checks below serve
+                pass
+    if _marshal is None:
+        return None
+    return _marshal.pack(fmt, torch.cuda.current_device(), *args)
 
 
 def _stream(stream) -> int:
@@ -790,6 +814,12 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, in
         out = torch.empty_like(x)
     elif not (out.dtype == x.dtype and out.shape == x.shape):
         raise ValueError(f"out must be {x.dtype} {tuple(x.shape)}")
+    if x.is_cuda:
+        packed = _pack("yRf===Y=", x, positions, freqs, int(bool(interleaved)), int(bool(inverse)), float(magnitude),
+                       out, _stream(stream))
+        if packed is not None:
+            _check("rope_apply", lib.rope_apply(*packed))
+            return out
     full = out
     if x.dim() == 3:
         x, full = _one_token(x, out)
@@ -843,8 +873,17 @@ def rope_kv_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, po
     [B, T]), and write the rotated keys and v_new to cache slots start_pos[b] +
     i.  Without the T dimension (and positions [B]): one token a sequence.
     Returns the rotated q (q_out may be q)."""
-    return _rope_append("rope_kv_append", _cache_bytes(k_cache, v_cache), k_cache.device, q, k_new, v_new, positions, freqs,
-                        block_table, start_pos, interleaved, magnitude, q_out, workspace, stream)
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    if k_cache.is_cuda:
+        ws = workspace or _small_ws(k_cache.device)
+        packed = _pack("yyyRf==Ycbv===", q, k_new, v_new, positions, freqs, int(bool(interleaved)), float(magnitude),
+                       q_out, k_cache, v_cache, block_table, start_pos, ws.ptr, ws.nbytes, _stream(stream))
+        if packed is not None:
+            _check("rope_kv_append", load().rope_kv_append(*packed))
+            return q_out
+    return _rope_append("rope_kv_append", _cache_bytes(k_cache, v_cache), k_cache.device, q, k_new, v_new, positions,
+                        freqs, block_table, start_pos, interleaved, magnitude, q_out, workspace, stream)
 
 
 def rope_kv_append_q8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, positions: torch.Tensor,
@@ -890,15 +929,21 @@ def paged_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     B, Hq, T, D = q.shape
     if scale is None:
         scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device).transpose(1, 2)
+    if lse is None and return_lse:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+    if workspace is not None and q.is_cuda:
+        packed = _pack("xoocbvq=Xl===", q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parents, float(scale),
+                       out, lse, workspace.ptr, workspace.nbytes, _stream(stream))
+        if packed is not None:
+            _check("paged_tree_attn", lib.paged_tree_attn(*packed))
+            return (out, lse) if return_lse else out
     _check_block_table(block_table, B)
     _check_int32_vec(ctx_lens, B, "ctx_lens")
     _check_int32_rows(parents, B, "parents")
     if parents.shape[1] != T:
         raise ValueError(f"parents must be [{B}, {T}], got {tuple(parents.shape)}")
-    if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device).transpose(1, 2)
-    if lse is None and return_lse:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
     if lse is not None:
         _check_f32_buffer(lse, B * Hq * T, "lse")
     _check_devices("paged_tree_attn", q, k_cache, v_cache, block_table, ctx_lens, parents, k_new, v_new, out, lse)
@@ -925,6 +970,13 @@ def kv_tree_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: to
     ctx_lens[b] + i."""
     lib = load()
     B = ctx_lens.shape[0]
+    if k_cache.is_cuda:
+        ws = workspace or _small_ws(k_cache.device)
+        packed = _pack("cbVrv====", k_cache, v_cache, block_table, ctx_lens, path, n_accept, B, ws.ptr, ws.nbytes,
+                       _stream(stream))
+        if packed is not None:
+            _check("kv_tree_accept", lib.kv_tree_accept(*packed))
+            return
     _check_block_table(block_table, B)
     _check_int32_vec(ctx_lens, B, "ctx_lens")
     _check_int32_rows(path, B, "path")
@@ -961,6 +1013,13 @@ def paged_attn_weights(q: torch.Tensor, lse: torch.Tensor, k_cache: torch.Tensor
     lse float32 [B, Hq, T] as an attention call returned it; [B, Hq, D] and [B,
     Hq] for one token a sequence.  q_lens int32 [B]: queries of each sequence."""
     lib = load()
+    if workspace is not None and q.is_cuda:
+        packed = _pack("ylcbvn==A===", q, lse, k_cache, k_cache, block_table, start_pos, q_lens, int(bool(causal)),
+                       float(1.0 / math.sqrt(q.shape[-1]) if scale is None else scale), acc, workspace.ptr,
+                       workspace.nbytes, _stream(stream))
+        if packed is not None:
+            _check("paged_attn_weights", lib.paged_attn_weights(*packed))
+            return acc
     if q.dim() == 3:
         q, lse = q.unsqueeze(2), lse.unsqueeze(2)
     B, Hq, T, D = q.shape
@@ -997,6 +1056,18 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
     [B], kept int32 [B, Hkv, keep]: the source slots, -1 past them)."""
     lib = load()
     B, Hkv = ctx_lens.shape[0], k_cache.shape[1]
+    keep = int(keep)
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=k_cache.device)
+    if kept is None:
+        kept = torch.empty((B, Hkv, max(keep, 0)), dtype=torch.int32, device=k_cache.device)
+    if k_cache.is_cuda and kept.shape == (B, Hkv, keep):
+        ws = workspace or _small_ws(k_cache.device)
+        packed = _pack("cAbVb====vK===", k_cache, v_cache, acc, block_table, ctx_lens, dst_block_table, B, keep,
+                       int(sink), int(recent), new_lens, kept, ws.ptr, ws.nbytes, _stream(stream))
+        if packed is not None:
+            _check("kv_evict", lib.kv_evict(*packed))
+            return new_lens, kept
     _check_block_table(block_table, B)
     _check_int32_vec(ctx_lens, B, "ctx_lens")
     if not (isinstance(dst_block_table, torch.Tensor) and dst_block_table.dtype == torch.int32
@@ -1005,11 +1076,6 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
         raise ValueError(f"dst_block_table must be int32 [>= {B}, blocks] with contiguous rows")
     c = _cache_bytes(k_cache, v_cache)
     _check_acc(acc, k_cache)
-    keep = int(keep)
-    if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=k_cache.device)
-    if kept is None:
-        kept = torch.empty((B, Hkv, max(keep, 0)), dtype=torch.int32, device=k_cache.device)
     _check_int32_vec(new_lens, B, "new_lens")
     if not (kept.dtype == torch.int32 and kept.is_contiguous() and kept.shape == (B, Hkv, keep)):
         raise ValueError(f"kept must be contiguous int32 {(B, Hkv, keep)}, got {tuple(kept.shape)}")

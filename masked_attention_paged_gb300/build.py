@@ -2,7 +2,9 @@
 
 Each .cu under csrc/ is compiled in parallel to an object file, then linked
 into ``_build/libattn_<machine>.so``.  No CMake, no torch extension machinery:
-the library is a plain C-ABI shared object.
+the library is a plain C-ABI shared object.  marshal.cpp, which only reads the
+binding's arguments, is a Python module of its own beside it (g++, torch's
+headers); the binding works without it, at a higher cost per call.
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import platform
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -48,6 +51,23 @@ def _stale(obj: str, src: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def marshal_path() -> str:
+    """The argument packer's module, per machine and version of torch."""
+    import torch
+    return os.path.join(BUILD, f"_marshal_{platform.machine()}_{torch.__version__.replace('+', '_')}.so")
+
+
+def _marshal_command(out: str) -> list[str]:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [INCLUDE, os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+           os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    return ["g++", "-O1", "-std=c++17", "-fPIC", "-shared", *[x for p in inc for x in ("-I", p)],
+            os.path.join(CSRC, "marshal.cpp"), "-o", out, "-L", os.path.join(root, "lib"), "-ltorch_python",
+            "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{os.path.join(root, 'lib')}"]
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     exe = nvcc()
@@ -65,15 +85,28 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr, file=sys.stderr)
         return r
 
+    marshal = marshal_path()
+    if force or _stale(marshal, os.path.join(CSRC, "marshal.cpp")):
+        tmp = marshal + f".tmp{os.getpid()}"
+
+        def build_marshal(cmd=_marshal_command(tmp)):
+            try:
+                run(cmd)
+                os.replace(tmp, marshal)
+            except (RuntimeError, OSError) as e:
+                print(f"marshal.cpp was not built, calls take longer on the host: {e}", file=sys.stderr)
+
+        jobs.append(build_marshal)
+    cu_jobs = any(not callable(j) for j in jobs)
     if jobs:
         with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
-            list(ex.map(run, jobs))
-    if force or jobs or not os.path.exists(LIB_PATH):
+            list(ex.map(lambda j: j() if callable(j) else run(j), jobs))
+    if force or cu_jobs or not os.path.exists(LIB_PATH):
         tmp = LIB_PATH + f".tmp{os.getpid()}"
         run([exe, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB_PATH)
