@@ -86,12 +86,13 @@ __global__ void __launch_bounds__(kAcceptThreads) kv_tree_accept_kernel(const Ac
 // kv_evict, first launch: which tokens stay.  One cluster per (KV head,
 // sequence); its CTAs split the context into consecutive ranges.  A token's rank
 // is its accumulated weight as an unsigned key (order-preserving bits; NaN below
-// everything, protected tokens above).  The keep-th largest key is found by
-// bisection on its bits, two at a time: 16 rounds of counting the keys at or
-// above three thresholds, in registers (kKeys a thread; longer ranges are read
-// again from L2 each round), one reduction and one cluster barrier a round.
-// Ties at the threshold go to the lowest slots.  The cost is the rounds'
-// latency, not the bytes: 4160 tokens about 5 us.
+// everything, protected tokens above).  The keep-th largest key is found eight
+// bits at a time: a histogram of the keys that agree with the bits found so far
+// in every CTA, added up into every CTA of the cluster, and the digit at which
+// the count from above reaches `keep`.  Ties at the threshold go to the lowest
+// slots.  Keys lie in shared memory and the loops over them stay rolled (a range
+// longer than kKeys is read again from L2 in each pass): the cost is latency,
+// of four passes and of fetching the code once, not the bytes.
 // ---------------------------------------------------------------------------
 struct EvictParams {
   const uint4* kc;
@@ -112,10 +113,11 @@ struct EvictParams {
   int32_t* new_lens;
   int32_t* kept;  // [B, Hkv, keep]
   uint32_t* status;
+  bool vec_acc;  // acc begins on a 16-byte boundary
 };
 
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
-constexpr int kKeys = 16;  // keys a thread holds
+constexpr int kKeys = 8192;  // keys a CTA holds
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ uint32_t rank_key(float x) {
@@ -129,23 +131,24 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// store to the word at the same shared-memory place in CTA `rank` of the cluster
-__device__ __forceinline__ void peer_store(int* p, uint32_t rank, int v) {
+// Not the .aligned forms: lanes may come here from different sides of a branch.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// the word at the same shared-memory place in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t peer_word(const int* p, uint32_t rank) {
   uint32_t addr;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+  return addr;
 }
 
 // grid (cluster size, Hkv, B), clusters along x
-__global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const EvictParams p, const int nc) {
-  __shared__ int warp_cnt[kSelWarps][3];
-  // every CTA's counts, pushed by their owners, alternating between rounds (a
-  // cluster barrier separates a buffer's readers from its next writers)
-  __shared__ int cta_cnt[2][kMaxCluster][3];
-  __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps];
+__global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const EvictParams p, const int nc) {
+  __shared__ __align__(16) uint32_t keys[kKeys];
+  __shared__ int hist[256];
+  // the cluster's histogram, alternating between passes: a CTA clears one before
+  // the cluster barrier after which its peers add to it
+  __shared__ __align__(16) int total[2][256];
+  __shared__ int warp_cnt[2][kSelWarps], cta_cnt[kMaxCluster][2];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int g = blockIdx.y, b = blockIdx.z;
   const int rank = static_cast<int>(cluster_rank());
@@ -162,145 +165,158 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const E
     for (int i = rank * kSelThreads + threadIdx.x; i < p.keep; i += nc * kSelThreads) kept[i] = i < L ? i : -1;
     return;
   }
+  for (int i = threadIdx.x; i < 256; i += kSelThreads) hist[i] = total[0][i] = 0;
+  cluster_arrive();
   const int32_t* bt = p.bt + b * p.bt_stride;
-  auto key_of = [&](int i) -> uint32_t {
-    if (i < p.sink || i >= L - p.recent) return 0xffffffffu;
+  const auto block_sums = [&](int blk) { return p.acc + (static_cast<int64_t>(blk) * p.Hkv + g) * kBS; };
+  const auto known = [&](int blk) { return blk >= 0 && blk < p.num_blocks; };
+  const auto protect = [&](int i) { return i < p.sink || i >= L - p.recent; };
+  // this warp's tokens [w0, w1): a consecutive range of the cluster's warps
+  const int per = ((L + nc * kSelWarps - 1) / (nc * kSelWarps) + 31) / 32 * 32;
+  const int w0 = static_cast<int>(min(static_cast<int64_t>(L), static_cast<int64_t>(rank * kSelWarps + warp) * per));
+  const int w1 = min(L, w0 + per);
+  const bool held = per <= kKeys / kSelWarps;  // the same for the whole cluster
+  uint32_t* mine = keys + warp * (kKeys / kSelWarps);
+  if (held) {
+    // four tokens of a block a lane and step: all block ids, then all sums
+    constexpr int kSteps = kKeys / kSelWarps / 128;
+    int blk[kSteps];
+    float4 x[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int i = w0 + 128 * s + 4 * lane;
+      blk[s] = i < w1 ? bt[i / kBS] : -1;
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int i = w0 + 128 * s + 4 * lane;
+      x[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!known(blk[s])) continue;
+      const float* at = block_sums(blk[s]) + i % kBS;
+      if (p.vec_acc)
+        x[s] = *reinterpret_cast<const float4*>(at);
+      else
+        x[s] = make_float4(at[0], at[1], at[2], at[3]);
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int i = w0 + 128 * s + 4 * lane;
+      if (i >= w1) continue;
+      uint32_t k[4] = {rank_key(x[s].x), rank_key(x[s].y), rank_key(x[s].z), rank_key(x[s].w)};
+      if (!known(blk[s])) {
+        report(p.status, kStatusBounds);
+        k[0] = k[1] = k[2] = k[3] = 0u;
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (protect(i + c)) k[c] = 0xffffffffu;
+      *reinterpret_cast<uint4*>(mine + 128 * s + 4 * lane) = make_uint4(k[0], k[1], k[2], k[3]);
+    }
+  }
+  const auto key_at = [&](int i) -> uint32_t {  // i in [w0, w1)
+    if (held) return mine[i - w0];
+    if (protect(i)) return 0xffffffffu;
     const int blk = bt[i / kBS];
-    if (blk < 0 || blk >= p.num_blocks) {
+    if (!known(blk)) {
       report(p.status, kStatusBounds);
       return 0u;
     }
-    return rank_key(p.acc[(static_cast<int64_t>(blk) * p.Hkv + g) * kBS + i % kBS]);
+    return rank_key(block_sums(blk)[i % kBS]);
   };
-  // this warp's tokens [w0, w1): a consecutive range of the cluster's warps, 32
-  // aligned, element e of lane l at w0 + 32 e + l
-  const int per = ((L + nc * kSelWarps - 1) / (nc * kSelWarps) + 31) / 32 * 32;
-  const int w0 = min(L, (rank * kSelWarps + warp) * per), w1 = min(L, w0 + per);
-  const int ne = (w1 - w0 + 31) / 32;
-  const bool held = per <= 32 * kKeys;  // the same for the whole cluster
-  uint32_t key[kKeys];
-  if (held) {
-    // all block ids, then all sums: two round trips to memory
-#pragma unroll
-    for (int e = 0; e < kKeys; ++e) {
-      const int i = w0 + 32 * e + lane;
-      key[e] = i < w1 ? static_cast<uint32_t>(bt[i / kBS]) : 0u;
+  cluster_wait();  // every CTA's words are zero
+  __syncwarp();
+  uint32_t thr = 0u;  // the bits found so far
+  int above = 0;      // keys whose found bits are greater
+#pragma unroll 1
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    const int turn = (shift >> 3) & 1;
+    int* sum = total[turn ^ 1];
+#pragma unroll 2
+    for (int i = w0 + lane; i - lane < w1; i += 32) {
+      const uint32_t k = i < w1 ? key_at(i) : 0u;
+      const bool in = i < w1 && ((k ^ thr) >> shift >> 8) == 0u;
+      const uint32_t m = __ballot_sync(0xffffffffu, in);
+      if (m == 0u) continue;
+      // the first lane counts for all that share its digit: equal and nearly
+      // equal sums would queue at one word otherwise
+      const int first = __ffs(static_cast<int>(m)) - 1, digit = static_cast<int>((k >> shift) & 255u);
+      const int lead = __shfl_sync(0xffffffffu, digit, first);
+      const bool same = in && digit == lead;
+      const int n = __popc(__ballot_sync(0xffffffffu, same));
+      if (in && (!same || lane == first)) atomicAdd(&hist[digit], same ? n : 1);
     }
-#pragma unroll
-    for (int e = 0; e < kKeys; ++e) {
-      const int i = w0 + 32 * e + lane;
-      const bool there = i < w1 && key[e] < static_cast<uint64_t>(p.num_blocks);
-      if (i < w1 && !there) report(p.status, kStatusBounds);
-      const float x = there ? p.acc[(static_cast<int64_t>(key[e]) * p.Hkv + g) * kBS + i % kBS] : 0.f;
-      key[e] = there ? rank_key(x) : 0u;
-      if (i < w1 && (i < p.sink || i >= L - p.recent)) key[e] = 0xffffffffu;
-    }
-  }
-  // largest threshold that at least `keep` keys reach (a filler key 0 is only
-  // counted at threshold 0, which is never asked about)
-  uint32_t thr = 0u;
-  int above = 0;  // keys >= thr + (1 << shift) of the last round: after it, keys > thr
-  for (int round = 0; round < 16; ++round) {
-    const int shift = 30 - 2 * round;
-    const uint32_t t1 = thr + (1u << shift), t2 = thr + (2u << shift), t3 = thr + (3u << shift);
-    int c1 = 0, c2 = 0, c3 = 0;
-    if (held) {
-#pragma unroll
-      for (int e = 0; e < kKeys; ++e) {
-        if (e >= ne) break;
-        c1 += key[e] >= t1, c2 += key[e] >= t2, c3 += key[e] >= t3;
-      }
-    } else {
-      for (int e = 0; e < ne; ++e) {
-        const int i = w0 + 32 * e + lane;
-        const uint32_t k = i < w1 ? key_of(i) : 0u;
-        c1 += k >= t1, c2 += k >= t2, c3 += k >= t3;
-      }
-    }
-    c1 = __reduce_add_sync(0xffffffffu, c1);
-    c2 = __reduce_add_sync(0xffffffffu, c2);
-    c3 = __reduce_add_sync(0xffffffffu, c3);
-    if (lane == 0) warp_cnt[warp][0] = c1, warp_cnt[warp][1] = c2, warp_cnt[warp][2] = c3;
     __syncthreads();
-    if (threadIdx.x < 3 * nc) {
-      const int c = threadIdx.x % 3;
-      int s = 0;
+    if (threadIdx.x < 256) {
+      const int v = hist[threadIdx.x];
+      hist[threadIdx.x] = 0;
+      total[turn][threadIdx.x] = 0;
+      if (v != 0)
+        for (int r = 0; r < nc; ++r)
+          asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(
+                           peer_word(sum + threadIdx.x, static_cast<uint32_t>(r))),
+                       "r"(v)
+                       : "memory");
+    }
+    cluster_arrive();
+    cluster_wait();
+    // every warp alike: eight digits a lane, counted from the largest down
+    const int4 lo = reinterpret_cast<const int4*>(sum)[2 * lane], hi = reinterpret_cast<const int4*>(sum)[2 * lane + 1];
+    const int n[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const int own = ((n[0] + n[1]) + (n[2] + n[3])) + ((n[4] + n[5]) + (n[6] + n[7]));
+    int from = own;  // of this lane's digits and all greater ones
 #pragma unroll
-      for (int w = 0; w < kSelWarps; ++w) s += warp_cnt[w][c];
-      peer_store(&cta_cnt[round & 1][rank][c], threadIdx.x / 3, s);
+    for (int d = 1; d < 32; d *= 2) {
+      const int up = __shfl_down_sync(0xffffffffu, from, d);
+      if (lane + d < 32) from += up;
     }
-    cluster_sync();
-    c1 = c2 = c3 = 0;
-    for (int r = 0; r < nc; ++r) {
-      c1 += cta_cnt[round & 1][r][0];
-      c2 += cta_cnt[round & 1][r][1];
-      c3 += cta_cnt[round & 1][r][2];
-    }
-    if (c3 >= p.keep)
-      thr = t3;
-    else if (c2 >= p.keep)
-      thr = t2, above = c3;
-    else if (c1 >= p.keep)
-      thr = t1, above = c2;
-    else
-      above = c1;
+    const int need = p.keep - above;
+    // the lane that holds the digit: the largest that reaches `need`
+    const int at = 31 - __clz(static_cast<int>(__ballot_sync(0xffffffffu, from >= need)));
+    int past = from - own, digit = 7;
+#pragma unroll
+    for (int d = 7; d > 0; --d)
+      if (digit == d && past + n[d] < need) past += n[d], digit = d - 1;
+    thr |= static_cast<uint32_t>(8 * at + __shfl_sync(0xffffffffu, digit, at)) << shift;
+    above += __shfl_sync(0xffffffffu, past, at);
   }
   // `above` keys are greater than thr; the first keep - above of those equal to it stay too
   const int need = p.keep - above;
   int gt = 0, eq = 0;
-  auto key_at = [&](int e) -> uint32_t {
-    const int i = w0 + 32 * e + lane;
-    return i < w1 ? key_of(i) : 0u;
-  };
-  if (held) {
-#pragma unroll
-    for (int e = 0; e < kKeys; ++e) {
-      if (e >= ne) break;
-      const bool in = w0 + 32 * e + lane < w1;
-      gt += in && key[e] > thr, eq += in && key[e] == thr;
-    }
-  } else {
-    for (int e = 0; e < ne; ++e) {
-      const bool in = w0 + 32 * e + lane < w1;
-      const uint32_t k = key_at(e);
-      gt += in && k > thr, eq += in && k == thr;
-    }
+#pragma unroll 2
+  for (int i = w0 + lane; i < w1; i += 32) {
+    const uint32_t k = key_at(i);
+    gt += k > thr, eq += k == thr;
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
-  if (lane == 0) warp_gt[warp] = gt, warp_eq[warp] = eq;
+  if (lane == 0) warp_cnt[0][warp] = gt, warp_cnt[1][warp] = eq;
   __syncthreads();
   if (threadIdx.x < 2 * nc) {
     const int c = threadIdx.x & 1;
     int s = 0;
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) s += c ? warp_eq[w] : warp_gt[w];
-    peer_store(&cta_cnt[0][rank][c], threadIdx.x >> 1, s);  // round 15 used buffer 1
+    for (int w = 0; w < kSelWarps; ++w) s += warp_cnt[c][w];
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(
+                     peer_word(&cta_cnt[rank][c], static_cast<uint32_t>(threadIdx.x >> 1))),
+                 "r"(s)
+                 : "memory");
   }
-  cluster_sync();
+  cluster_arrive();
+  cluster_wait();
   int gt0 = 0, eq0 = 0;  // before this warp's range
-  if (lane < warp) gt0 = warp_gt[lane], eq0 = warp_eq[lane];
-  if (lane < rank) gt0 += cta_cnt[0][lane][0], eq0 += cta_cnt[0][lane][1];
+  if (lane < warp) gt0 = warp_cnt[0][lane], eq0 = warp_cnt[1][lane];
+  if (lane < rank) gt0 += cta_cnt[lane][0], eq0 += cta_cnt[lane][1];
   gt0 = __reduce_add_sync(0xffffffffu, gt0);
   eq0 = __reduce_add_sync(0xffffffffu, eq0);
   const uint32_t below = (1u << lane) - 1u;
-  auto place = [&](int e, uint32_t k) {
-    const int i = w0 + 32 * e + lane;
+#pragma unroll 1
+  for (int i = w0 + lane; i - lane < w1; i += 32) {
     const bool in = i < w1;
+    const uint32_t k = in ? key_at(i) : 0u;
     const uint32_t mg = __ballot_sync(0xffffffffu, in && k > thr), me = __ballot_sync(0xffffffffu, in && k == thr);
     const int e_rank = eq0 + __popc(me & below);
     if (in && (k > thr || (k == thr && e_rank < need))) kept[gt0 + __popc(mg & below) + min(e_rank, need)] = i;
     gt0 += __popc(mg);
     eq0 += __popc(me);
-  };
-  if (held) {
-#pragma unroll
-    for (int e = 0; e < kKeys; ++e) {
-      if (e >= ne) break;
-      place(e, key[e]);
-    }
-  } else {
-    for (int e = 0; e < ne; ++e) place(e, key_at(e));
   }
 }
 
@@ -389,10 +405,11 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t stream) {
   p.new_lens = a.new_lens;
   p.kept = a.kept;
   p.status = a.status;
-  // a CTA per kSelThreads * kKeys tokens of the longest possible context, up to a portable cluster
+  p.vec_acc = reinterpret_cast<uintptr_t>(a.acc) % 16 == 0;
+  // a CTA per kKeys tokens of the longest possible context, up to a portable cluster
   const int64_t slots = static_cast<int64_t>(a.max_blocks) * kBS;
   int nc = 1;
-  while (nc < kMaxCluster && static_cast<int64_t>(nc) * kSelThreads * kKeys < slots) nc *= 2;
+  while (nc < kMaxCluster && static_cast<int64_t>(nc) * kKeys < slots) nc *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(nc), static_cast<unsigned>(a.cache.Hkv), static_cast<unsigned>(a.B));
   cfg.blockDim = dim3(kSelThreads);
