@@ -58,6 +58,7 @@ constexpr int kBoxBytes = kBM * 128;
 constexpr float kRescaleMargin = 8.0f;
 constexpr int kBarBytes = 1024;
 constexpr int kSegs = 4;   // segments the planner is ahead
+constexpr int kItemCost = 3;  // what an item costs a CTA besides its tiles, in tiles
 constexpr int kSide = 48;  // draft keys that have a place of their own in shared memory (NT = 1)
 constexpr uint32_t kAbsent = 0x7fc0a5a5u;  // a partial's LSE for the row of an absent draft (a NaN of its own)
 
@@ -157,7 +158,7 @@ struct TreeParams {
 struct CutItem {
   int b, g, node0;
   int pieces;         // in CTAs c, c + 1, ...
-  int first_is_head;  // CTA c's run begins with it
+  int first_is_head;  // it is the first segment of CTA c's run
 };
 
 // A sequence that does not fit its table, or is idle, has no context and no drafts.
@@ -343,7 +344,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       if (b >= p.B) return 0;
       int ctx;
       bool ok;
-      const int n = seq_tiles(p, b, ctx, ok) * items;
+      const int n = (kItemCost + seq_tiles(p, b, ctx, ok)) * items;
       if (first && blockIdx.x == 0 && !ok && p.ctx_lens[b] >= 0) report(p.status, kStatusBounds);
       return n;
     };
@@ -372,10 +373,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       if (past != 0) {
         const int l = __ffs(past) - 1;
         const int local = lo - run - __shfl_sync(0xffffffffu, incl - mine, l);
-        const int tiles = __shfl_sync(0xffffffffu, mine, l) / items;
+        const int units = __shfl_sync(0xffffffffu, mine, l) / items;
         plan_b = base + l;
-        plan_item = local / tiles;
-        plan_t = local - plan_item * tiles;
+        plan_item = local / units;
+        plan_t = local - plan_item * units - kItemCost;
         break;
       }
       run += __shfl_sync(0xffffffffu, incl, 31);
@@ -604,14 +605,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     for (int i = 0;; ++i) {
       Seg s = {};
       s.b = -1;
-      if (pos < hi) {
-        if (plan_t == tiles) {  // the item is done: the next one, or the next sequence
-          plan_t = 0;
-          if (++plan_item == p.Hkv * p.MP) {
-            plan_item = 0;
-            tiles = seq_tiles(p, ++plan_b, ctx, there);
-          }
+      if (pos < hi && plan_t == tiles) {  // the item is done: the next one, or the next sequence
+        plan_t = -kItemCost;
+        if (++plan_item == p.Hkv * p.MP) {
+          plan_item = 0;
+          tiles = seq_tiles(p, ++plan_b, ctx, there);
         }
+      }
+      if (plan_t < 0) {  // the item's own cost, or as much of it as falls into this run
+        const int skip = min(-plan_t, hi - pos);
+        pos += skip;
+        plan_t += skip;
+      }
+      if (pos < hi) {
         s.b = plan_b;
         s.g = plan_item / p.MP;
         s.m = plan_item % p.MP;
@@ -621,12 +627,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         s.ctx = ctx;
         s.there = there;
         const bool whole = s.t0 == 0 && s.t1 == tiles;
-        s.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (pos == lo ? 0 : 1);
+        s.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (i == 0 ? 0 : 1);
         if (!whole && s.t0 == 0 && lane == 0) {  // cut, and it starts here
           CutItem it;
           it.b = s.b, it.g = s.g, it.node0 = s.m * NT * p.tb;
           it.pieces = runs.of(pos + tiles - 1) - static_cast<int>(blockIdx.x) + 1;
-          it.first_is_head = pos == lo;
+          it.first_is_head = i == 0;
           p.cuts[blockIdx.x] = it;
         }
         pos += s.t1 - plan_t;
@@ -1257,7 +1263,7 @@ cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream) {
   p.lse = a.lse;
   p.pitch = nt * kBM;
   // the planner counts tiles in 31 bits
-  const int64_t most = static_cast<int64_t>(p.B) * p.Hkv * p.MP * ((static_cast<int64_t>(p.max_blocks) * kBS + kBN - 1) / kBN + p.ntd);
+  const int64_t most = static_cast<int64_t>(p.B) * p.Hkv * p.MP * ((static_cast<int64_t>(p.max_blocks) * kBS + kBN - 1) / kBN + p.ntd + kItemCost);
   if (most > 0x7fffffff) return cudaErrorInvalidValue;
   const size_t rows = static_cast<size_t>(2) * a.n_cta * p.pitch;
   p.part_o = static_cast<float*>(a.partials);
