@@ -35,6 +35,7 @@ struct AcceptParams {
 // V at D = 128: one pass for the usual path).
 constexpr int kAcceptThreads = 256, kAcceptVecs = 8;
 __global__ void __launch_bounds__(kAcceptThreads) kv_tree_accept_kernel(const AcceptParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // in place before the launch before it ends
   const int g = blockIdx.x, b = blockIdx.y;
   const int ctx = p.ctx_lens[b], n = p.n_accept[b];
   if (ctx < 0 || n <= 0) return;  // idle, or nothing accepted
@@ -448,9 +449,16 @@ cudaError_t launch_tree_accept(const AcceptArgs& a, cudaStream_t stream) {
   p.max_path = a.max_path;
   p.n_accept = a.n_accept;
   p.status = a.status;
-  dim3 grid(static_cast<unsigned>(a.cache.Hkv), static_cast<unsigned>(a.B));
-  kv_tree_accept_kernel<<<grid, kAcceptThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.cache.Hkv), static_cast<unsigned>(a.B));
+  cfg.blockDim = dim3(kAcceptThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_tree_accept_kernel, p);
 }
 
 }  // namespace attn

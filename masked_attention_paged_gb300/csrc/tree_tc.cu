@@ -226,6 +226,7 @@ template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
   constexpr int CW = D / 16;
   __shared__ float tile[32][D + 1];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c0 = blockIdx.x;
   const CutItem it = p.cuts[c0];
@@ -664,6 +665,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       if (s.t1 > s.nct) {
         const int mb = round & 1;
         uint32_t* am = anc + mb * C::kMaxT * C::kWords;
+        // parents and block ids set out first, and are put down after the waits
+        int up_of[C::kMaxT / NL], blk_of[C::kMaxT / NL];
+        const bool append = s.there && p.k_new != nullptr && s.m == 0;
+#pragma unroll
+        for (int x = 0; x < C::kMaxT / NL; ++x) {
+          const int t = lt + x * NL;
+          up_of[x] = s.there && t < p.T ? p.parents[s.b * p.par_stride + t] : -2;
+          blk_of[x] = append && t < p.T ? p.bt[static_cast<int64_t>(s.b) * p.bt_stride + (s.ctx + t) / kBS] : -1;
+        }
         // the masks of two segments before may still be in use
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->mask_empty[mb], ((round >> 1) & 1) ^ 1, abort, p.status));
         ok = !named_bar_or(1, NL, !ok);
@@ -702,8 +712,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             }
           }
         }
-#pragma unroll 1
-        for (int t = lt; t < p.T; t += NL) par[t] = s.there ? p.parents[s.b * p.par_stride + t] : -2;
+#pragma unroll
+        for (int x = 0; x < C::kMaxT / NL; ++x)
+          if (lt + x * NL < p.T) par[lt + x * NL] = up_of[x], dst_row[lt + x * NL] = blk_of[x];
         if (lt < 8) bars->bad[mb][lt] = 0u;
         named_bar_sync(1, NL);
         // node t's ancestors, itself included: parents come before children, so
@@ -732,7 +743,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
           for (int x = 0; x < C::kWords; ++x) am[t * C::kWords + x] = there ? w[x] : 0u;
           // present and to be cached: where
-          dst_row[t] = there && p.k_new != nullptr && s.m == 0 ? cache_row(p, s.b, s.g, s.ctx + t) : -1;
+          const int64_t blk = dst_row[t];
+          int64_t at = -1;
+          if (there && append) {
+            if (blk >= 0 && blk < p.num_blocks)
+              at = (blk * p.Hkv + s.g) * kBS + (s.ctx + t) % kBS;
+            else
+              report(p.status, kStatusBounds);
+          }
+          dst_row[t] = at;
         }
         named_bar_sync(1, NL);
 #pragma unroll 1
