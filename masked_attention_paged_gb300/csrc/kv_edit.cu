@@ -37,13 +37,17 @@ constexpr int kAcceptThreads = 256, kAcceptVecs = 8;
 __global__ void __launch_bounds__(kAcceptThreads) kv_tree_accept_kernel(const AcceptParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // in place before the launch before it ends
   const int g = blockIdx.x, b = blockIdx.y;
-  const int ctx = p.ctx_lens[b], n = p.n_accept[b];
-  if (ctx < 0 || n <= 0) return;  // idle, or nothing accepted
   const int32_t* path = p.path + b * p.path_stride;
+  const int ctx = p.ctx_lens[b], n = p.n_accept[b];
+  // the path's start sets out with the lengths (and is in L1 from here on)
+  const int mine = threadIdx.x < p.max_path ? path[threadIdx.x] : 0;
+  const int before = threadIdx.x > 0 && threadIdx.x < p.max_path ? path[threadIdx.x - 1] : -1;
+  if (ctx < 0 || n <= 0) return;  // idle, or nothing accepted
   const int64_t slots = static_cast<int64_t>(p.max_blocks) * kBS;
   bool bad = n > p.max_path;
-  for (int i = threadIdx.x; !bad && i < n; i += kAcceptThreads)
-    bad = path[i] < 0 || static_cast<int64_t>(ctx) + path[i] >= slots || (i > 0 && path[i] <= path[i - 1]);
+  const auto wrong = [&](int at, int last) { return at <= last || static_cast<int64_t>(ctx) + at >= slots; };
+  if (!bad && static_cast<int>(threadIdx.x) < n) bad = wrong(mine, before);  // the first entry against -1
+  for (int i = threadIdx.x + kAcceptThreads; !bad && i < n; i += kAcceptThreads) bad = wrong(path[i], path[i - 1]);
   if (__syncthreads_or(bad)) {  // the sequence is left as it was
     if (threadIdx.x == 0 && g == 0) report(p.status, kStatusBounds);
     return;

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
 #pragma unroll
   for (int i = 0; i < CW; ++i) acc[i] = 0.f;
   const bool empty = absent || !any;
-#pragma unroll 2
+#pragma unroll 32 / CW
   for (int c = 0; c < it.pieces; ++c) {
     const float l = mine ? p.part_lse[slot(c) * p.pitch + sr] : -INFINITY;
     const float* o = p.part_o + (slot(c) * D + warp * CW) * p.pitch + sr;
