@@ -135,9 +135,10 @@ __device__ __forceinline__ void decode_merge_head(const SplitMerge& sm, int b, i
 // brings the count of (b, gkv) to ns (the splits that hold tokens), merge the
 // splits of the group's G heads (warp w takes heads w, w + NW, ...).  Every
 // CTA publishes its partial before its count (the fence), and the merging CTA
-// fences again before it reads the others'.  A word of another generation,
-// or one already at ns (the same generation replayed, as from a captured
-// graph), starts the count afresh.  Called by all NW * 32 threads.
+// fences again before it reads the others'.  It also sets the count back to
+// zero: the same generation may be replayed (from a captured graph), with
+// contexts that have more splits by then.  A word of another generation starts
+// the count afresh.  Called by all NW * 32 threads.
 template <int D, int G, int NW>
 __device__ __forceinline__ void decode_finish(const SplitMerge& sm, int gkv, int b, int ns) {
   __shared__ int s_last;
@@ -148,13 +149,13 @@ __device__ __forceinline__ void decode_finish(const SplitMerge& sm, int gkv, int
     const unsigned long long tag = static_cast<unsigned long long>(sm.gen) << 32;
     unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(c), now;
     for (;;) {
-      const bool fresh = (old >> 32) == sm.gen && (old & 0xffffffffull) < static_cast<unsigned long long>(ns);
-      now = fresh ? old + 1 : tag + 1;
+      now = (old >> 32) == sm.gen ? old + 1 : tag + 1;
       const unsigned long long seen = atomicCAS(c, old, now);
       if (seen == old) break;
       old = seen;
     }
     s_last = (now & 0xffffffffull) == static_cast<unsigned long long>(ns);
+    if (s_last) *reinterpret_cast<volatile unsigned long long*>(c) = tag;
   }
   __syncthreads();
   if (!s_last) return;

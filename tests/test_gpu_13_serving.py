@@ -176,6 +176,30 @@ def test_the_same_steps_as_one_graph():
     assert s.ws.status() == 0
 
 
+@pytest.mark.parametrize("D,Hkv", [(128, 2), (64, 1)])
+def test_a_captured_decode_step_whose_contexts_grow(D, Hkv):
+    """One graph over contexts that gain splits between replays, and lose some again: the eager call's bits."""
+    g = torch.Generator().manual_seed(4)
+    mb = 400
+    bt = torch.randperm(2 * mb, generator=g).to(torch.int32).view(2, mb).to(DEV)
+    kc, vc = (torch.randn(2 * mb, Hkv, 16, D, generator=g).bfloat16().to(DEV) for _ in range(2))
+    q = torch.randn(2, 4 * Hkv, D, generator=g).bfloat16().to(DEV)
+    lens, out = _int([1000, 900]), torch.empty_like(q)
+    ws = lib.Workspace(lib.paged_decode_workspace_size(2, 4 * Hkv, mb, 16, D))
+    lib.paged_decode_attn(q, kc, vc, bt, lens, out=out, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lib.paged_decode_attn(q, kc, vc, bt, lens, out=out, workspace=ws)
+    for now in ([1000, 900], [2500, 900], [4700, 1100], [6400, 6000], [1500, 6400], [3100, 17]):
+        lens.copy_(_int(now))
+        want = lib.paged_decode_attn(q, kc, vc, bt, lens)
+        for _ in range(3):
+            out.zero_()
+            graph.replay()
+            assert torch.equal(out, want), now
+    assert ws.status() == 0
+
+
 def test_the_packed_arguments_are_those_of_the_worded_checks(monkeypatch):
     """Each call takes its arguments in one compiled step where they are plainly as documented: the same tuple."""
     s = _Server(64, seed=1)
