@@ -521,7 +521,7 @@ attn_status rope_kv_append_q8(const attn_tensor *q, const attn_tensor *k_new, co
 
 /*
  * paged_tree_attn -- attention of a tree of drafted tokens over a paged cache:
- * the drafts' K/V are appended and every draft attends, in one launch.
+ * the drafts' K/V are appended and every draft attends.
  *
  * Sequence b holds ctx_lens[b] tokens and T drafts; parents[b][t] says which
  * token draft t follows:
@@ -554,7 +554,10 @@ attn_status rope_kv_append_q8(const attn_tensor *q, const attn_tensor *k_new, co
  *                 SMs.  It needs no clearing between calls (only the status
  *                 word must start at zero).  Calls that share a workspace must
  *                 not overlap on the GPU.
- * T <= 256.  Blocks that hold drafts must not be shared between sequences.
+ * T <= 256, and up to 2^31 key tiles of 128 in all (batch * Hkv * ceil(T * Hq / Hkv
+ * / 128) * (max_blocks / 8 + 7) below that is always taken), else
+ * ATTN_ERR_UNSUPPORTED.  Blocks that hold drafts must not be shared between
+ * sequences.
  * Products run on the tensor cores with fp32 accumulation; the softmax weights
  * are rounded to bf16 before P.V, as in attn_fwd.  Results do not depend on
  * timing.

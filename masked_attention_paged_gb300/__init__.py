@@ -930,7 +930,7 @@ def paged_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device).transpose(1, 2)
+        out = torch.empty_strided((B, Hq, T, D), (T * Hq * D, D, Hq * D, 1), dtype=q.dtype, device=q.device)
     if lse is None and return_lse:
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
     if workspace is not None and q.is_cuda:

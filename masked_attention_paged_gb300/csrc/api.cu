@@ -708,7 +708,8 @@ attn_status paged_tree_attn(const attn_tensor* q, const attn_tensor* k_new, cons
       if (k_new->shape[i] != want[i] || v_new->shape[i] != want[i]) return ATTN_ERR_INVALID_ARG;
   }
   if (T > kTreeMaxDrafts || B > 65535 || Hq > 65535 || Hq / cache->num_kv_heads > 128 ||
-      cache->num_blocks * cache->num_kv_heads > 0x7fffffff)
+      cache->num_blocks * cache->num_kv_heads > 0x7fffffff ||
+      !tree_units_fit(B, cache->num_kv_heads, T, Hq / cache->num_kv_heads, max_blocks))
     return ATTN_ERR_UNSUPPORTED;
   const size_t need = paged_tree_workspace_size(static_cast<int32_t>(B), static_cast<int32_t>(Hq),
                                                 cache->num_kv_heads, static_cast<int32_t>(T), max_blocks,

@@ -198,6 +198,8 @@ struct TreeArgs {
 };
 // workspace past the status block, G = Hq / Hkv
 size_t tree_partial_bytes(int64_t T, int64_t G, int D, int n_cta);
+// whether the call's key tiles (as wide as its table) can be counted in 31 bits
+bool tree_units_fit(int64_t B, int64_t Hkv, int64_t T, int64_t G, int64_t max_blocks);
 cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream);
 
 struct AcceptArgs {

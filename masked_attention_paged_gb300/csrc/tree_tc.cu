@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   int pos = 0, hi = 0, lo = 0;
   int plan_b = 0, plan_item = 0, plan_t = 0;
   if (warp == 5) {
-    // (all counts are below 2^31: the host has seen to it)
+    // (all counts are below 2^31: tree_units_fit)
     const int items = p.Hkv * p.MP;
     int total = 0, mine0 = 0;
     auto seq_items = [&](int b, bool first) {
@@ -1243,6 +1243,13 @@ size_t tree_partial_bytes(int64_t T, int64_t G, int D, int n_cta) {
   return parts + ((n_cta * sizeof(CutItem) + 255) & ~size_t(255));
 }
 
+bool tree_units_fit(int64_t B, int64_t Hkv, int64_t T, int64_t G, int64_t max_blocks) {
+  if (T == 0) return true;
+  const int64_t rows = tree_nt(T, G) * tile_drafts(T, G);
+  const int64_t units = (max_blocks * kBS + kBN - 1) / kBN + (T + kBS - 1 + kBN - 1) / kBN + kItemCost;
+  return B * Hkv * ((T + rows - 1) / rows) <= 0x7fffffff / units;
+}
+
 cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream) {
   TreeParams p = {};
   p.B = static_cast<int>(a.B);
@@ -1281,9 +1288,6 @@ cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream) {
   p.out_bf16 = a.out.dtype == ATTN_BF16;
   p.lse = a.lse;
   p.pitch = nt * kBM;
-  // the planner counts tiles in 31 bits
-  const int64_t most = static_cast<int64_t>(p.B) * p.Hkv * p.MP * ((static_cast<int64_t>(p.max_blocks) * kBS + kBN - 1) / kBN + p.ntd + kItemCost);
-  if (most > 0x7fffffff) return cudaErrorInvalidValue;
   const size_t rows = static_cast<size_t>(2) * a.n_cta * p.pitch;
   p.part_o = static_cast<float*>(a.partials);
   p.part_lse = p.part_o + rows * a.cache.D;

@@ -40,6 +40,10 @@ def test_paged_tree_rejects(L):
     assert call(q=_t([2, 12, 6, 64]), out=_t([2, 12, 6, 64])) == INVALID
     assert call(q=_t([2, 10, 6, 128]), out=_t([2, 10, 6, 128])) == INVALID  # 10 % 4
     assert call(q=_t([2, 12, 257, 128]), out=_t([2, 12, 257, 128]), ps=257) == UNSUPPORTED
+    # 128 x 4 (sequence, KV head)s of 2^21 tiles are counted in 31 bits, three row groups of each are not
+    wide = lambda t: _t([128, 12, t, 128])  # noqa: E731
+    assert call(q=wide(6), out=wide(6), bts=1 << 24, mb=1 << 24) != UNSUPPORTED
+    assert call(q=wide(256), out=wide(256), ps=256, bts=1 << 24, mb=1 << 24) == UNSUPPORTED
     assert call(out=_t([2, 12, 7, 128])) == INVALID
     assert call(q=_t([2, 12, 6, 128], data=FAKE + 8)) == INVALID
     assert call(out=_t([2, 12, 6, 128], data=FAKE + 8)) == INVALID
