@@ -294,50 +294,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = max(t, n - C::KS); x < n; x += 2) drain_wait(&bars->k_full[x % C::KS], (x / C::KS) & 1);
   } else if (warp == 4) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, abort, p.status); };
-      int n = 0, j = 0;
-      bool ok = true;
-      for (int i = 0; ok; ++i) {
-        ok = wait(&bars->seg_full[i % kSegs], i / kSegs);
+    // The whole warp goes through the loop, with values that are alike in all
+    // lanes (uniform registers, which the descriptors have to be in), and one lane
+    // issues: with one lane in the loop an MMA took ~120 cycles to issue.
+    auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    auto wait = [&](uint64_t* bar, int phase) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort, p.status)) != 0;
+    };
+    const uint32_t tm = uni(tmem);
+    const uint64_t k0 = sdesc_sw128(smem_u32(smem + C::kOffK), 16, PagedTile<D>::kGroup);
+    const uint64_t q0 = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
+    int n = 0, j = 0;
+    bool ok = true;
+    Seg s;
+    for (int i = 0; ok && seg_get(i, s); ++i) {
+      seg_taken(i);
+      const int c0 = uni(s.c0), c1 = uni(s.c1), rows = uni(s.n);
+      for (int c = c0; ok && c < c1; ++c, ++j) {
+        const int qs = j % C::QS;
+        ok = wait(&bars->q_full[qs], j / C::QS);
         if (!ok) break;
-        const Seg s = bars->segs[i % kSegs];
-        if (s.b < 0) break;
-        mbar_arrive(&bars->seg_empty[i % kSegs]);
-        for (int c = s.c0; ok && c < s.c1; ++c, ++j) {
-          const int qs = j % C::QS;
-          ok = wait(&bars->q_full[qs], j / C::QS);
+        const int cols = min(p.ct, rows - c * p.ct) * p.G;
+        const uint32_t idesc = idesc_bf16_f32(kBM, (cols + 15) / 16 * 16, false, false);
+        const uint64_t qd = q0 + qs * (C::kTileBytes >> 4);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          // half a chunk apart, the two tiles' exponentials do not come at once
+          const int st = (n + t) % C::KS;
+          ok = ok && (c > c0 || wait(&bars->k_full[st], (n + t) / C::KS)) &&
+               wait(&bars->s_free[t][j & 1], (j >> 1) ^ 1);
           if (!ok) break;
-          const int cols = min(p.ct, s.n - c * p.ct) * p.G;
-          const uint32_t idesc = idesc_bf16_f32(kBM, (cols + 15) / 16 * 16, false, false);
-          const uint32_t qa = smem_u32(smem + C::kOffQ + qs * C::kTileBytes);
+          tc_fence_after();
+          const uint64_t kd = k0 + st * (C::kTileBytes >> 4);
+          const uint32_t to = tm + (2 * t + (j & 1)) * 128;
+          if (elect_one()) {
 #pragma unroll
-          for (int t = 0; ok && t < 2; ++t) {
-            // half a chunk apart, the two tiles' exponentials do not come at once
-            const int st = (n + t) % C::KS;
-            ok = (c > s.c0 || wait(&bars->k_full[st], (n + t) / C::KS)) &&
-                 wait(&bars->s_free[t][j & 1], (j >> 1) ^ 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t ka = smem_u32(smem + C::kOffK + st * C::kTileBytes);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              // 16 dims = 32 bytes of a 128-byte row
-              umma_bf16_ss(tmem + (2 * t + (j & 1)) * 128,
-                           sdesc_sw128(ka + (kk >> 2) * PagedTile<D>::kHalf + (kk & 3) * 32, 16, PagedTile<D>::kGroup),
-                           sdesc_sw128(qa + (kk >> 2) * kBoxBytes + (kk & 3) * 32, 16, 1024), idesc,
-                           kk > 0 ? 1u : 0u);
-            }
+            for (int kk = 0; kk < D / 16; ++kk)  // 16 dims = 32 bytes of a 128-byte row
+              umma_bf16_ss(to, kd + (kk >> 2) * (PagedTile<D>::kHalf >> 4) + (kk & 3) * 2,
+                           qd + (kk >> 2) * (kBoxBytes >> 4) + (kk & 3) * 2, idesc, kk > 0 ? 1u : 0u);
             umma_commit(&bars->s_full[t][j & 1]);
-            if (c + 1 == s.c1) umma_commit(&bars->k_empty[st]);
+            if (c + 1 == c1) umma_commit(&bars->k_empty[st]);
+            if (t == 1) umma_commit(&bars->q_empty[qs]);
           }
-          umma_commit(&bars->q_empty[qs]);
+          __syncwarp();
         }
-        n += 2;
       }
+      n += 2;
+    }
+    if (elect_one()) {
       umma_commit(&bars->drained);
       drain_wait(&bars->drained, 0);
     }
+    __syncwarp();
   } else if (warp == 5) {
     // ------------------------------------------------------------ query chunks
     if (lane == 0) {
