@@ -490,114 +490,124 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     }
   } else if (warp == 4) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_o = idesc_bf16_f32(kBM, D, false, true);
-      // w: the warpgroup whose scores and accumulator these are; ka, va: the tile.
-      // A descriptor's start address counts 16 bytes in its low bits.
-      auto issue_s = [&](int w, uint32_t ka, int keys, Layout l) {  // S_w = Q K^T
-        const uint32_t idesc_s = idesc_bf16_f32(kBM, keys, false, false);
-        const uint64_t dq = sdesc_sw128(smem_u32(smem + C::kOffQ) + (NT == 2 ? w * C::kTileBytes : 0), 16, 1024);
-        const uint64_t dk = sdesc_sw128(ka, 16, l.group);
+    // The whole warp goes through the loop, with values that are alike in all
+    // lanes (uniform registers, which the descriptors have to be in), and one lane
+    // issues: a lane alone in the loop took over 100 cycles an MMA.
+    constexpr uint32_t idesc_o = idesc_bf16_f32(kBM, D, false, true);
+    auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const uint32_t tm = uni(tmem);
+    // w: the warpgroup whose scores and accumulator these are; ka, va: the tile; free:
+    // told (if not null) when the tile's stage has been read.  A descriptor's start
+    // address counts 16 bytes in its low bits.
+    auto issue_s = [&](int w, uint32_t ka, int keys, Layout l, uint64_t* free) {  // S_w = Q K^T
+      const uint32_t idesc_s = idesc_bf16_f32(kBM, keys, false, false);
+      const uint64_t dq = sdesc_sw128(smem_u32(smem + C::kOffQ) + (NT == 2 ? w * C::kTileBytes : 0), 16, 1024);
+      const uint64_t dk = sdesc_sw128(ka, 16, l.group);
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)  // 16 dims = 32 bytes of a 128-byte row
-          umma_bf16_ss(tmem + w * 128, dq + (kk >> 2) * (kBoxBytes >> 4) + (kk & 3) * 2,
+          umma_bf16_ss(tm + w * 128, dq + (kk >> 2) * (kBoxBytes >> 4) + (kk & 3) * 2,
                        dk + (kk >> 2) * (l.half >> 4) + (kk & 3) * 2, idesc_s, kk > 0 ? 1u : 0u);
         umma_commit(&bars->s_full[w]);
-      };
-      auto issue_pv = [&](int w, uint32_t va, int keys, Layout l, bool first) {  // O_w (+)= P_w V
-        const uint64_t dv = sdesc_sw128(va, l.half, l.group);
-#pragma unroll 1
-        for (int kk = 0; kk * 16 < keys; ++kk)
-          umma_bf16_ts(tmem + C::kColO + w * D, tmem + w * 128 + kk * 8, dv + kk * (l.group >> 3), idesc_o,
+        if (free != nullptr) umma_commit(free);
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int w, uint32_t va, int keys, Layout l, bool first, uint64_t* free) {  // O_w (+)= P_w V
+      const uint64_t dv = sdesc_sw128(va, l.half, l.group);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk) {
+          if (kk * 16 >= keys) break;
+          umma_bf16_ts(tm + C::kColO + w * D, tm + w * 128 + kk * 8, dv + kk * (l.group >> 3), idesc_o,
                        (!first || kk > 0) ? 1u : 0u);
+        }
         umma_commit(&bars->o_done[w]);
-      };
-      auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, abort, p.status); };
-      auto k_at = [&](int r) { return smem_u32(smem + C::kOffK + (r % C::KS) * C::kTileBytes); };
-      auto v_at = [&](int r) { return smem_u32(smem + C::kOffV + (r % C::VS) * C::kTileBytes); };
-      int r = 0, round = 0;  // ring tiles, and drafts in their own place, so far
-      int j = 0;
-      bool ok = true;
-      for (int seg = 0; ok; ++seg) {
-        ok = wait(&bars->seg_full[seg % kSegs], seg / kSegs);
-        if (!ok) break;
-        const Seg s = bars->segs[seg % kSegs];
-        if (s.b < 0) break;
-        mbar_arrive(&bars->seg_empty[seg % kSegs]);
-        const int n = s.t1 - s.t0;
-        auto keys = [&](int x) { return tile_keys(p, s.t0 + x, s.nct, s.ctx); };
-        auto lay = [&](int x) { return tile_layout<D>(p, s.t0 + x >= s.nct); };
-        for (int t = 0; t < NT; ++t) ok = ok && wait(&bars->q_full[t], seg);
-        if constexpr (NT == 1) {
-          // tile j is warpgroup j & 1's; S runs two tiles ahead of PV.  x: tile of the
-          // segment (r + x: its ring tile); the drafts, last, may lie aside.
-          auto aside = [&](int x) { return p.side && s.t0 + x >= s.nct; };
-          auto scores = [&](int x) {
-            if (aside(x)) {
-              if (!wait(&bars->side_ready, round)) return false;
-              tc_fence_after();
-              issue_s((j + x) & 1, smem_u32(smem + C::kOffSide), keys(x), lay(x));
-              return true;
-            }
-            if (!wait(&bars->k_full[(r + x) % C::KS], (r + x) / C::KS)) return false;
-            tc_fence_after();
-            issue_s((j + x) & 1, k_at(r + x), keys(x), lay(x));
-            umma_commit(&bars->k_empty[(r + x) % C::KS]);
-            return true;
-          };
+        if (free != nullptr) umma_commit(free);
+      }
+      __syncwarp();
+    };
+    auto wait = [&](uint64_t* bar, int phase) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort, p.status)) != 0;
+    };
+    auto k_at = [&](int r) { return smem_u32(smem + C::kOffK + (r % C::KS) * C::kTileBytes); };
+    auto v_at = [&](int r) { return smem_u32(smem + C::kOffV + (r % C::VS) * C::kTileBytes); };
+    int r = 0, round = 0;  // ring tiles, and drafts in their own place, so far
+    int j = 0;
+    bool ok = true;
+    Seg sg;
+    for (int seg = 0; ok && seg_get(seg, sg); ++seg) {
+      seg_taken(seg);
+      const int t0 = uni(sg.t0), t1 = uni(sg.t1), nct = uni(sg.nct), ctx = uni(sg.ctx);
+      const int n = t1 - t0;
+      auto keys = [&](int x) { return tile_keys(p, t0 + x, nct, ctx); };
+      auto lay = [&](int x) { return tile_layout<D>(p, t0 + x >= nct); };
+      for (int t = 0; t < NT; ++t) ok = ok && wait(&bars->q_full[t], seg);
+      if constexpr (NT == 1) {
+        // tile j is warpgroup j & 1's; S runs two tiles ahead of PV.  x: tile of the
+        // segment (r + x: its ring tile); the drafts, last, may lie aside.
+        auto aside = [&](int x) { return p.side && t0 + x >= nct; };
+        auto scores = [&](int x) {
+          const bool a = aside(x);
+          if (!(a ? wait(&bars->side_ready, round) : wait(&bars->k_full[(r + x) % C::KS], (r + x) / C::KS))) return false;
+          tc_fence_after();
+          issue_s((j + x) & 1, a ? smem_u32(smem + C::kOffSide) : k_at(r + x), keys(x), lay(x),
+                  a ? nullptr : &bars->k_empty[(r + x) % C::KS]);
+          return true;
+        };
 #pragma unroll 1
-          for (int x = 0; ok && x < n + 2; ++x) {
-            if (x >= 2) {  // P_(x - 2) V, before S_x takes its scores' place
-              const int y = x - 2;
-              // the accumulators of the segment before have been read
-              if (y == 0 && seg > 0) ok = wait(&bars->o_free, seg - 1);
-              ok = ok && wait(&bars->p_full[(j + y) & 1], (j + y) >> 1) &&
-                   (aside(y) || wait(&bars->v_full[(r + y) % C::VS], (r + y) / C::VS));
+        for (int x = 0; ok && x < n + 2; ++x) {
+          if (x >= 2) {  // P_(x - 2) V, before S_x takes its scores' place
+            const int y = x - 2;
+            const bool a = aside(y);
+            // the accumulators of the segment before have been read
+            if (y == 0 && seg > 0) ok = wait(&bars->o_free, seg - 1);
+            ok = ok && wait(&bars->p_full[(j + y) & 1], (j + y) >> 1) &&
+                 (a || wait(&bars->v_full[(r + y) % C::VS], (r + y) / C::VS));
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv((j + y) & 1, a ? smem_u32(smem + C::kOffSide + C::kSideBytes) : v_at(r + y), keys(y), lay(y), y < 2,
+                     a ? &bars->side_free : &bars->v_empty[(r + y) % C::VS]);
+          }
+          if (x < n) ok = scores(x);
+        }
+        if (!ok) break;
+        j += n;
+        const bool had = p.side && t1 > nct;
+        r += had ? n - 1 : n;
+        round += had;
+      } else {
+        auto wait_k = [&](int x) { return wait(&bars->k_full[x % C::KS], x / C::KS); };
+        auto wait_v = [&](int x) { return wait(&bars->v_full[x % C::VS], x / C::VS); };
+        // PV_A, S_A', PV_B, S_B': each tile's softmax runs under the other's MMAs
+#pragma unroll 1
+        for (int x = -1; ok && x < n; ++x) {
+#pragma unroll 1
+          for (int w = 0; ok && w < 2; ++w) {
+            if (x >= 0) {
+              ok = wait(&bars->p_full[w], j) && (w > 0 || wait_v(j));
               if (!ok) break;
               tc_fence_after();
-              issue_pv((j + y) & 1, aside(y) ? smem_u32(smem + C::kOffSide + C::kSideBytes) : v_at(r + y), keys(y),
-                       lay(y), y < 2);
-              umma_commit(aside(y) ? &bars->side_free : &bars->v_empty[(r + y) % C::VS]);
+              issue_pv(w, v_at(j), keys(x), lay(x), x == 0, w == 1 ? &bars->v_empty[j % C::VS] : nullptr);
             }
-            if (x < n) ok = scores(x);
-          }
-          if (!ok) break;
-          j += n;
-          const bool had = p.side && s.t1 > s.nct;
-          r += had ? n - 1 : n;
-          round += had;
-        } else {
-          auto wait_k = [&](int x) { return wait(&bars->k_full[x % C::KS], x / C::KS); };
-          auto wait_v = [&](int x) { return wait(&bars->v_full[x % C::VS], x / C::VS); };
-          // PV_A, S_A', PV_B, S_B': each tile's softmax runs under the other's MMAs
-#pragma unroll 1
-          for (int x = -1; ok && x < n; ++x) {
-#pragma unroll 1
-            for (int w = 0; ok && w < 2; ++w) {
-              if (x >= 0) {
-                ok = wait(&bars->p_full[w], j) && (w > 0 || wait_v(j));
-                if (!ok) break;
-                tc_fence_after();
-                issue_pv(w, v_at(j), keys(x), lay(x), x == 0);
-                if (w == 1) umma_commit(&bars->v_empty[j % C::VS]);
-              }
-              if (x + 1 < n) {
-                const int jn = x < 0 ? j : j + 1;
-                ok = w > 0 || wait_k(jn);
-                if (!ok) break;
-                tc_fence_after();
-                issue_s(w, k_at(jn), keys(x + 1), lay(x + 1));
-                if (w == 1) umma_commit(&bars->k_empty[jn % C::KS]);
-              }
+            if (x + 1 < n) {
+              const int jn = x < 0 ? j : j + 1;
+              ok = w > 0 || wait_k(jn);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(w, k_at(jn), keys(x + 1), lay(x + 1), w == 1 ? &bars->k_empty[jn % C::KS] : nullptr);
             }
-            if (x >= 0) ++j;
           }
+          if (x >= 0) ++j;
         }
       }
-      // no MMA may be in flight when the TMEM is freed
+    }
+    // no MMA may be in flight when the TMEM is freed
+    if (elect_one()) {
       umma_commit(&bars->drained);
       drain_wait(&bars->drained, 0);
     }
+    __syncwarp();
   } else if (warp == 5) {
     // ------------------------------------------------------------ planner
     int ctx = 0, tiles = 0;
