@@ -41,8 +41,9 @@ constexpr int kBN = 128;       // query rows per chunk, at most
 constexpr int kBS = 16;
 constexpr int kBoxBytes = kBM * 128;
 constexpr int kThreads = 512;
-constexpr int kLseRing = 2;
+constexpr int kLseRing = 2;  // as the score buffers
 constexpr int kSegs = 4;  // segments the planner is ahead
+constexpr int kItemCost = 3;  // what an item costs a CTA besides its steps, in steps
 constexpr int kBarBytes = 1024;
 
 template <int D>
@@ -66,14 +67,13 @@ struct Seg {
   int g, pair, c0, c1;
   int n, start, keys;  // of the sequence
   int slot;            // where its partial sums go; -1: the item is whole
-  int run0, pieces, head;  // a cut item: its first run, its runs, whether that run begins with it
+  int run0, pieces, head;  // a cut item: its first run, its runs, whether it is that run's first segment
 };
 
 struct Bars {
   uint64_t k_full[8], k_empty[8];
   uint64_t q_full[4], q_empty[4];
-  uint64_t s_full[2][2], s_free[2][2];  // [key tile][score buffer]
-  uint64_t l_full[kLseRing], l_empty[kLseRing];
+  uint64_t s_full[2][2], s_free[2][2];  // [key tile][step & 1]: scores and LSEs are there, have been read
   uint64_t piece_full, piece_go, drained;
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   Seg segs[kSegs];
@@ -107,7 +107,7 @@ struct WeightParams {
 // see; pair p >= full starts at chunk first(p).
 struct SeqWork {
   int start, n, keys, pairs, chunks, full, ct;
-  int64_t steps;  // per KV head
+  int64_t units;  // per KV head: its pairs' steps and kItemCost each
   // At most chunks - 1: the pair's first key is one of the sequence's keys.
   __device__ int first(int p) const { return p < full ? 0 : (p * kPair - start) / ct; }
 };
@@ -128,13 +128,13 @@ __device__ __forceinline__ SeqWork seq_work(const WeightParams& p, int b, bool r
   w.pairs = (w.keys + kPair - 1) / kPair;
   w.chunks = (n + p.ct - 1) / p.ct;
   w.full = p.causal ? min(w.pairs, w.start / kPair + 1) : w.pairs;
-  w.steps = static_cast<int64_t>(w.full) * w.chunks;
+  w.units = static_cast<int64_t>(w.full) * w.chunks + static_cast<int64_t>(w.pairs) * kItemCost;
   if (kPair % p.ct == 0) {
     // first(x) = k x - ceil(start / ct): an arithmetic series
     const int64_t k = kPair / p.ct, m = w.pairs - w.full;
-    w.steps += m * (w.chunks + (w.start + p.ct - 1) / p.ct) - k * (m * (w.full + w.pairs - 1) / 2);
+    w.units += m * (w.chunks + (w.start + p.ct - 1) / p.ct) - k * (m * (w.full + w.pairs - 1) / 2);
   } else {
-    for (int x = w.full; x < w.pairs; ++x) w.steps += w.chunks - w.first(x);
+    for (int x = w.full; x < w.pairs; ++x) w.units += w.chunks - w.first(x);
   }
   return w;
 }
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 32) {
     for (int s = 0; s < 2; ++s) {
       for (int t = 0; t < 2; ++t) {
-        mbar_init(&bars->s_full[t][s], 1);
+        mbar_init(&bars->s_full[t][s], 2);  // the MMAs and the LSEs' warp
         mbar_init(&bars->s_free[t][s], 4);
       }
     }
@@ -165,10 +165,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 4; ++s) {
       mbar_init(&bars->q_full[s], 1);
       mbar_init(&bars->q_empty[s], 1);
-    }
-    for (int s = 0; s < kLseRing; ++s) {
-      mbar_init(&bars->l_full[s], 1);
-      mbar_init(&bars->l_empty[s], 8);
     }
     for (int s = 0; s < kSegs; ++s) {
       mbar_init(&bars->seg_full[s], 1);
@@ -189,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t total = 0, mine0 = 0;
     for (int base = 0; base < p.B; base += 32) {
       const int64_t mine =
-          base + lane < p.B ? seq_work(p, base + lane, blockIdx.x == 0).steps * p.Hkv : 0;
+          base + lane < p.B ? seq_work(p, base + lane, blockIdx.x == 0).units * p.Hkv : 0;
       if (base == 0) mine0 = mine;
       total += mine;
     }
@@ -202,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t run = 0;
     for (int base = 0; base < p.B && lo < hi; base += 32) {
       const int64_t mine =
-          base == 0 ? mine0 : (base + lane < p.B ? seq_work(p, base + lane, false).steps * p.Hkv : 0);
+          base == 0 ? mine0 : (base + lane < p.B ? seq_work(p, base + lane, false).units * p.Hkv : 0);
       int64_t incl = mine;
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) {
@@ -224,17 +220,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lo < hi) {
       work = seq_work(p, plan_b, false);
-      plan_g = static_cast<int>(div_pos(lo - run, work.steps));
-      int64_t rem = lo - run - plan_g * work.steps;  // step within the (sequence, KV head)
-      if (rem < static_cast<int64_t>(work.full) * work.chunks) {
-        plan_pair = static_cast<int>(div_pos(rem, static_cast<int64_t>(work.chunks)));
-        rem -= static_cast<int64_t>(plan_pair) * work.chunks;
+      plan_g = static_cast<int>(div_pos(lo - run, work.units));
+      int64_t rem = lo - run - plan_g * work.units;  // unit within the (sequence, KV head)
+      const int64_t most = kItemCost + work.chunks;
+      if (rem < work.full * most) {
+        plan_pair = static_cast<int>(div_pos(rem, most));
+        rem -= plan_pair * most;
       } else {
         plan_pair = work.full;
-        rem -= static_cast<int64_t>(work.full) * work.chunks;
-        while (rem >= work.chunks - work.first(plan_pair)) rem -= work.chunks - work.first(plan_pair), ++plan_pair;
+        rem -= work.full * most;
+        while (rem >= most - work.first(plan_pair)) rem -= most - work.first(plan_pair), ++plan_pair;
       }
-      plan_c = work.first(plan_pair) + static_cast<int>(rem);
+      plan_c = work.first(plan_pair) + static_cast<int>(rem) - kItemCost;
       item0 = lo - rem;
     }
   }
@@ -385,8 +382,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int x = 0; x < 4; ++x) dt[x] = (lane + 32 * x) / p.G, dh[x] = (lane + 32 * x) % p.G;
     auto publish = [&](int jj) {
       const int sl = jj % kLseRing;
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars->l_empty[sl], ((jj / kLseRing) & 1) ^ 1, abort, p.status)))
-        return false;
+      for (int t = 0; t < 2; ++t)
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_free[t][sl], ((jj / kLseRing) & 1) ^ 1, abort, p.status)))
+          return false;
       bool odd = false;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -397,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       odd = __any_sync(0xffffffffu, odd);
       if (lane == 0) bars->odd[sl] = odd;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->l_full[sl]);
+      if (lane < 2) mbar_arrive(&bars->s_full[lane][sl]);
       return true;
     };
     for (int i = 0; ok && seg_get(i, s); ++i) {
@@ -421,30 +419,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0;; ++i) {
       Seg s = {};
       s.b = -1;
-      if (pos < hi) {
-        if (plan_c == work.chunks) {  // the item is done: the next pair, KV head or sequence
-          item0 = pos;
-          if (++plan_pair == work.pairs) {
-            plan_pair = 0;
-            if (++plan_g == p.Hkv) {
-              plan_g = 0;
-              do work = seq_work(p, ++plan_b, false);
-              while (work.steps == 0);
-            }
+      if (pos < hi && plan_c == work.chunks) {  // the item is done: the next pair, KV head or sequence
+        item0 = pos;
+        if (++plan_pair == work.pairs) {
+          plan_pair = 0;
+          if (++plan_g == p.Hkv) {
+            plan_g = 0;
+            do work = seq_work(p, ++plan_b, false);
+            while (work.units == 0);
           }
-          plan_c = work.first(plan_pair);
         }
-        const int f = work.first(plan_pair);
+        plan_c = work.first(plan_pair) - kItemCost;
+      }
+      const int f = pos < hi ? work.first(plan_pair) : 0;
+      if (plan_c < f) {  // the item's own cost, or as much of it as falls into this run
+        const int skip = static_cast<int>(min(static_cast<int64_t>(f - plan_c), hi - pos));
+        pos += skip;
+        plan_c += skip;
+      }
+      if (pos < hi) {
         s.b = plan_b, s.g = plan_g, s.pair = plan_pair;
         s.c0 = plan_c;
         s.c1 = static_cast<int>(min(static_cast<int64_t>(work.chunks), plan_c + (hi - pos)));
         s.n = work.n, s.start = work.start, s.keys = work.keys;
         s.slot = -1;
         if (s.c0 != f || s.c1 != work.chunks) {
-          s.slot = 2 * static_cast<int>(blockIdx.x) + (pos == lo ? 0 : 1);
-          s.run0 = runs.of(item0);
-          s.pieces = runs.of(item0 + work.chunks - f - 1) - s.run0 + 1;
-          s.head = runs.lo(s.run0) == item0;
+          const int64_t step0 = item0 + kItemCost;
+          s.slot = 2 * static_cast<int>(blockIdx.x) + (i == 0 ? 0 : 1);
+          s.run0 = runs.of(step0);
+          s.pieces = runs.of(step0 + work.chunks - f - 1) - s.run0 + 1;
+          s.head = runs.lo(s.run0) >= item0;  // nothing of the item before lies in that run
         }
         pos += s.c1 - plan_c;
         plan_c = s.c1;
@@ -490,9 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < 4; ++x) sum[x] = f2_pack(0.f, 0.f);
       const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
       for (int c = s.c0; c < s.c1; ++c, ++j) {
-        const int buf = j & 1, sl = j % kLseRing;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->l_full[sl], (j / kLseRing) & 1, abort, p.status) &&
-                                         mbar_wait(&bars->s_full[t][buf], (j >> 1) & 1, abort, p.status))) {
+        const int sl = j % kLseRing;  // the score buffer as well
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[t][sl], (j / kLseRing) & 1, abort, p.status))) {
           ok = false;
           break;
         }
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* nl = lse_ring + sl * kBN;
         const bool masked = bars->odd[sl] != 0 || warp_tmin > t0;
         const int rel = max(0, min(tmin - t0, p.ct)) * p.G;  // columns >= rel see the key
-        const uint32_t col = tmem + lane_addr + (2 * t + buf) * 128;
+        const uint32_t col = tmem + lane_addr + (2 * t + sl) * 128;
         auto add32 = [&](const uint32_t (&sr)[32], int cc, auto masked_c) {
           constexpr bool MASKED = decltype(masked_c)::value;
 #pragma unroll
@@ -530,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t sa[32], sb[32];
           tmem_ld32(col, sa);
           tmem_wait_ld(sa);
-#pragma unroll 1
+#pragma unroll
           for (int cc = 0; cc < kBN; cc += 64) {  // the next 32 columns load while these are added
             tmem_ld32(col + cc + 32, sb);
             add32(sa, cc, std::false_type());
@@ -550,10 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars->s_free[t][buf]);
-          mbar_arrive(&bars->l_empty[sl]);
-        }
+        if (lane == 0) mbar_arrive(&bars->s_free[t][sl]);
       }
       if (!ok) break;
       float a0, a1;
