@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const Evic
   for (int shift = 24; shift >= 0; shift -= 8) {
     const int turn = (shift >> 3) & 1;
     int* sum = total[turn ^ 1];
-#pragma unroll 2
+#pragma unroll 4
     for (int i = w0 + lane; i - lane < w1; i += 32) {
       const uint32_t k = i < w1 ? key_at(i) : 0u;
       const bool in = i < w1 && ((k ^ thr) >> shift >> 8) == 0u;
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const Evic
   // `above` keys are greater than thr; the first keep - above of those equal to it stay too
   const int need = p.keep - above;
   int gt = 0, eq = 0;
-#pragma unroll 2
+#pragma unroll 4
   for (int i = w0 + lane; i < w1; i += 32) {
     const uint32_t k = key_at(i);
     gt += k > thr, eq += k == thr;
