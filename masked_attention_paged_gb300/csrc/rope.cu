@@ -16,7 +16,9 @@
 // tokens and a range of their heads; its threads first compute the tokens'
 // sines and cosines into shared memory (one sincospif each: shared by all heads
 // of a token), then move rows, 16 elements (two 16-byte vectors of bf16) a
-// thread and step.
+// thread and step.  16 sequences x 1024 tokens (32 query and 8 KV heads, D =
+// 128): 68 us for 403 MB, 5.9 TB/s, 87 % of the measured copy rate; one token of
+// one sequence 3.2 us and of 64 sequences 3.4 us, a launch and its loads.
 #include <math.h>
 
 #include <algorithm>

@@ -5,18 +5,29 @@
 // whole context and, among the drafts, to itself and its ancestors:
 //   s_j = scale q.k_j,  out = sum_j softmax(s)_j v_j,  lse = log sum_j e^{s_j}.
 //
-// Few query rows read a long cache, so K and V are read once for all T drafts
-// and all G query heads of a KV head.  A row tile is the G heads of tb = min(T,
+// Few query rows read a long cache, so K and V are read once for all drafts and
+// query heads of a KV head that fit NT row tiles.  A row tile is the G heads of tb = min(T,
 // 128 / G) drafts (row r: draft r / G, head r % G), one 5-D TMA box of q whatever
 // its strides; NT row tiles share every K/V tile (NT = 1 if one holds all drafts,
 // else 2).  What bounds it is HBM (a 128-key tile of K and V at D = 128 is 64 KB,
 // 1.4 us of an SM's share), until rows pass 256 a KV head and the tensor cores and
-// exponentials do.
+// exponentials do.  Measured (merge and path acceptance included; Hkv = 8, D = 128):
+//   64 sequences x 25 drafts, G = 4, up to 8192 tokens   269 us, 1.66 GB, 91 % of
+//                                                        the measured copy rate
+//   16 x 27, G = 4, up to 4096 tokens                    57 us (28 us of bytes): 17
+//        tiles a CTA; the rest is each segment's start and end and the merge
+//   1 x 64, G = 8, 131063 tokens                         233 us (144 us of MMAs):
+//        the softmax between a tile's two products; 52 % tensor-pipe activity
+//   1 x 8, G = 2, D = 64, 700 tokens                     20 us, three launches'
+//        latency: a tile passes through in 8 us, the drafts' in 11
 //
 // Every SM takes an equal run of the call's K/V tiles: an item (sequence, KV
 // head, group of row tiles) is its context tiles followed by its draft tiles (whose
 // masks are built meanwhile), the items are laid end to end, and each CTA takes an
-// equal run of tiles (runs.cuh).
+// equal run (runs.cuh) of tiles and of kItemCost for each item: its start and end
+// cost about 4 us, so equal runs of tiles alone left the CTAs with three short
+// segments 11 us behind those with one (16 x 27: 62 us, with 3 counted 59.5, with 2
+// 60.3, with 4 60.1).
 // An item inside one run is written at once; one that is cut leaves partials
 // (normalised rows and log2 LSE; at most two per CTA), which a second launch
 // merges in order, so results do not depend on the timing.  That launch spreads
@@ -32,7 +43,7 @@
 // the K/V tiles in turn, each with a score buffer, an output accumulator and a
 // running max and sum of its own, joined by the LSE rule when an item ends: one
 // warpgroup alone took 2.1 us a tile, more than the tile's bytes.  P goes over its
-// S as bf16 (relative rounding 2^-9; row sums are taken in fp32 before it).
+// S as bf16 (relative rounding 2^-8; row sums are taken in fp32 before it).
 //
 // V rows past the context's end and rows of absent drafts are zeroed: P is 0
 // there, but 0 x NaN is not.  A draft's own V may hold infinities or NaN that
@@ -549,7 +560,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         auto aside = [&](int x) { return p.side && t0 + x >= nct; };
         auto scores = [&](int x) {
           const bool a = aside(x);
-          if (!(a ? wait(&bars->side_ready, round) : wait(&bars->k_full[(r + x) % C::KS], (r + x) / C::KS))) return false;
+          if (!wait(a ? &bars->side_ready : &bars->k_full[(r + x) % C::KS], a ? round : (r + x) / C::KS)) return false;
           tc_fence_after();
           issue_s((j + x) & 1, a ? smem_u32(smem + C::kOffSide) : k_at(r + x), keys(x), lay(x),
                   a ? nullptr : &bars->k_empty[(r + x) % C::KS]);
@@ -566,8 +577,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                  (a || wait(&bars->v_full[(r + y) % C::VS], (r + y) / C::VS));
             if (!ok) break;
             tc_fence_after();
-            issue_pv((j + y) & 1, a ? smem_u32(smem + C::kOffSide + C::kSideBytes) : v_at(r + y), keys(y), lay(y), y < 2,
-                     a ? &bars->side_free : &bars->v_empty[(r + y) % C::VS]);
+            issue_pv((j + y) & 1, a ? smem_u32(smem + C::kOffSide + C::kSideBytes) : v_at(r + y), keys(y), lay(y),
+                     y < 2, a ? &bars->side_free : &bars->v_empty[(r + y) % C::VS]);
           }
           if (x < n) ok = scores(x);
         }
@@ -1207,7 +1218,8 @@ template <int D, int NT>
 cudaError_t launch(const TreeArgs& a, TreeParams& p, cudaStream_t stream) {
   using C = Cfg<D, NT>;
   CUtensorMap mq, mk, mv, mkn, mvn;
-  if (!make_rows_map(&mq, a.q, a.cache.Hkv, p.tb) || !make_paged_map(&mk, a.cache.k, a.cache.num_blocks, a.cache.Hkv, D) ||
+  if (!make_rows_map(&mq, a.q, a.cache.Hkv, p.tb) ||
+      !make_paged_map(&mk, a.cache.k, a.cache.num_blocks, a.cache.Hkv, D) ||
       !make_paged_map(&mv, a.cache.v, a.cache.num_blocks, a.cache.Hkv, D))
     return cudaErrorInvalidValue;
   mkn = mk, mvn = mv;  // not read without k_new
