@@ -134,6 +134,7 @@ struct TreeParams {
   int B, T, Hq, Hkv, G;
   int tb, RT;  // drafts and rows (tb * G) of a row tile
   int MP;      // groups of NT row tiles per KV head
+  int shares;  // of the CTAs, one for each such group (or 1: a share takes all groups)
   int ntd;     // draft tiles
   int side;    // the drafts (one tile, at most kSide keys) have a place of their own, not ring stages
   int new_box; // rows of a k_new / v_new box: T up to a multiple of 16, or 128
@@ -346,11 +347,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // the planner's state: the call's runs, and the place of this CTA's first tile
   Runs runs = {};
-  int pos = 0, hi = 0, lo = 0;
+  int pos = 0, hi = 0, lo = 0, share = 0;
   int plan_b = 0, plan_item = 0, plan_t = 0;
   if (warp == 5) {
     // (all counts are below 2^31: tree_units_fit)
-    const int items = p.Hkv * p.MP;
+    const int items = p.shares > 1 ? p.Hkv : p.Hkv * p.MP;  // of a sequence, in this CTA's share
     int total = 0, mine0 = 0;
     auto seq_items = [&](int b, bool first) {
       if (b >= p.B) return 0;
@@ -367,9 +368,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       total += mine;
     }
     total = __reduce_add_sync(0xffffffffu, total);
-    runs = Runs::make(total, gridDim.x);
-    const int c = static_cast<int>(blockIdx.x);
-    if (c < runs.n) lo = runs.lo(c), hi = runs.lo(c + 1);
+    const int per = gridDim.x / p.shares, c = static_cast<int>(blockIdx.x) % per;
+    share = static_cast<int>(blockIdx.x) / per;
+    runs = Runs::make(total, per);
+    if (share < p.shares && c < runs.n) lo = runs.lo(c), hi = runs.lo(c + 1);
     pos = lo;
     int run = 0;
 #pragma unroll 1
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       run += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) {
-      p.cuts[c].pieces = 0;  // unless an item starts here and goes on
+      p.cuts[blockIdx.x].pieces = 0;  // unless an item starts here and goes on
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
@@ -629,7 +631,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       s.b = -1;
       if (pos < hi && plan_t == tiles) {  // the item is done: the next one, or the next sequence
         plan_t = -kItemCost;
-        if (++plan_item == p.Hkv * p.MP) {
+        if (++plan_item == (p.shares > 1 ? p.Hkv : p.Hkv * p.MP)) {
           plan_item = 0;
           tiles = seq_tiles(p, ++plan_b, ctx, there);
         }
@@ -641,8 +643,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       }
       if (pos < hi) {
         s.b = plan_b;
-        s.g = plan_item / p.MP;
-        s.m = plan_item % p.MP;
+        s.g = p.shares > 1 ? plan_item : plan_item / p.MP;
+        s.m = p.shares > 1 ? share : plan_item % p.MP;
         s.t0 = plan_t;
         s.t1 = min(tiles, plan_t + (hi - pos));
         s.nct = tiles - p.ntd;
@@ -653,7 +655,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         if (!whole && s.t0 == 0 && lane == 0) {  // cut, and it starts here
           CutItem it;
           it.b = s.b, it.g = s.g, it.node0 = s.m * NT * p.tb;
-          it.pieces = runs.of(pos + tiles - 1) - static_cast<int>(blockIdx.x) + 1;
+          it.pieces = runs.of(pos + tiles - 1) - static_cast<int>(blockIdx.x % (gridDim.x / p.shares)) + 1;
           it.first_is_head = i == 0;
           p.cuts[blockIdx.x] = it;
         }
@@ -1283,6 +1285,11 @@ cudaError_t launch_paged_tree(const TreeArgs& a, cudaStream_t stream) {
   p.tb = tile_drafts(p.T, p.G);
   p.RT = p.tb * p.G;
   p.MP = (p.T + nt * p.tb - 1) / (nt * p.tb);
+  // Each row group to a share of the CTAs of its own: they come to a K/V tile at the
+  // same time, and all but one of them find it in L2.  With one share for all, its
+  // groups came to it half a run apart (1 x 64 drafts, G = 8, 131063 tokens: 1.08 GB
+  // read for 0.54).  At most 8 shares leave 3 % of 152 CTAs idle.
+  p.shares = p.MP <= std::min(8, a.n_cta) ? p.MP : 1;
   p.new_box = std::min(kBN, (p.T + 15) / 16 * 16);
   p.side = nt == 1 && p.T + (a.k_new.data != nullptr ? 0 : kBS - 1) <= kSide;
   p.ntd = a.k_new.data != nullptr ? (p.T + kBN - 1) / kBN : (p.T + kBS - 1 + kBN - 1) / kBN;

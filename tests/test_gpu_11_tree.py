@@ -144,7 +144,7 @@ def _check(s, scale=None, out_dtype=torch.bfloat16, status=0):
 
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("T,Hq,Hkv", [(1, 2, 2), (1, 8, 1), (7, 6, 2), (32, 8, 2), (33, 8, 2), (20, 5, 1), (64, 8, 2),
-                                      (100, 4, 2), (128, 1, 1), (129, 2, 1), (200, 3, 1), (256, 2, 2)])
+                                      (100, 4, 2), (128, 1, 1), (129, 2, 1), (200, 3, 1), (256, 2, 2), (23, 100, 1)])
 def test_tree(T, Hq, Hkv, D):
     """No context, contexts around block and tile ends, one row tile, two, and several pairs of them."""
     _check(_make([0, 1, 15, 130, 256, 301], T, Hq, Hkv, D, seed=T * 7 + D))
