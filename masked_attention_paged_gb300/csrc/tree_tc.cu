@@ -993,38 +993,48 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
               weigh32(x, c, mul, neg, sum);
             }
           } else {
-            // Bound by the exponentials: all scores in registers at once, and first
-            // against the reference max at hand, without a max pass; if some row's
-            // sum says its scores outgrew it (2^64; or NaN), once more with one.
+            // Bound by this chain's latency: scores go to registers, the first 32 ahead of
+            // the others, and are weighed against the reference max at hand, without a
+            // max pass; if some row's sum says its scores outgrew it (2^64; or NaN), once
+            // more with one.
             uint32_t sr[4][32];
+            tmem_ld32(tmem + lane_addr + s_col, sr[0]);
+            const bool fast = !masked && __all_sync(0xffffffffu, m_run != -INFINITY);
+            tmem_wait_ld(sr[0]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_addr + s_col + c * 32, sr[c]);
+            for (int c = 1; c < 4; ++c) tmem_ld32(tmem + lane_addr + s_col + c * 32, sr[c]);
+            bool done = false;
+            if (fast) {
+              weigh32(sr[0], 0, p.scale_log2, -m_run, sum);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_wait_ld(sr[c]);
-            bool fast = !masked && __all_sync(0xffffffffu, m_run != -INFINITY);
-            float mul = p.scale_log2;
-            if (masked) {
-              mul = 1.0f;
+              for (int c = 1; c < 4; ++c) tmem_wait_ld(sr[c]);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) mask32(sr[c], see(c));
-            }
-            for (;;) {
-              if (!fast) {
+              for (int c = 1; c < 4; ++c) weigh32(sr[c], c, p.scale_log2, -m_run, sum);
+              float a0, a1;
+              f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
+              done = __all_sync(0xffffffffu, a0 + a1 <= 18446744073709551616.0f);
+              if (!done) {
+                tmem_wait_st();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) max32(sr[c], mx);
-                raise(fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * mul);
+                for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
               }
+            } else {
+#pragma unroll
+              for (int c = 1; c < 4; ++c) tmem_wait_ld(sr[c]);
+            }
+            if (!done) {
+              float mul = p.scale_log2;
+              if (masked) {
+                mul = 1.0f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) mask32(sr[c], see(c));
+              }
+#pragma unroll
+              for (int c = 0; c < 4; ++c) max32(sr[c], mx);
+              raise(fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * mul);
               const float neg = m_run == -INFINITY ? 0.0f : -m_run;
 #pragma unroll
               for (int c = 0; c < 4; ++c) weigh32(sr[c], c, mul, neg, sum);
-              if (!fast) break;
-              float a0, a1;
-              f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
-              if (__all_sync(0xffffffffu, a0 + a1 <= 18446744073709551616.0f)) break;
-              tmem_wait_st();
-#pragma unroll
-              for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
-              fast = false;
             }
           }
           float a0, a1;
