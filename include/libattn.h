@@ -539,10 +539,10 @@ attn_status rope_kv_append_q8(const attn_tensor *q, const attn_tensor *k_new, co
  * chunk.
  *
  *   q, out        [batch, Hq, T, head_dim]; q bf16, out bf16 or f32 (strided
- *                 views, 16-byte aligned rows); Hq a multiple of Hkv, at most 128
- *                 query heads per KV head
- *   k_new, v_new  [batch, Hkv, T, head_dim] bf16: draft t's rows, written to slot
- *                 ctx_lens[b] + t.  Both NULL: they are in the cache already.
+ *                 views, 16-byte aligned rows, no stride 0 in q); Hq a multiple of
+ *                 Hkv, at most 128 query heads per KV head
+ *   k_new, v_new  [batch, Hkv, T, head_dim] bf16 (as q): draft t's rows, written to
+ *                 slot ctx_lens[b] + t.  Both NULL: they are in the cache already.
  *   parents       int32, row b at parents + b * par_stride_b (0: one tree for all)
  *   ctx_lens      int32 [batch].  < 0: an idle sequence (nothing cached, out = 0,
  *                 lse = -inf).  ctx_lens[b] + T past the table sets
@@ -605,8 +605,8 @@ attn_status kv_tree_accept(const attn_kv_cache *cache, const int32_t *block_tabl
  * i sees tokens t <= start_pos[b] + i (causal = 1) or t < start_pos[b] + n (0).
  * A row whose lse is -inf (it saw nothing) adds nothing.
  *
- *   q        [batch, Hq, T, head_dim] bf16 (strided view, 16-byte aligned rows);
- *            Hq / Hkv <= 128
+ *   q        [batch, Hq, T, head_dim] bf16 (strided view, 16-byte aligned rows, no
+ *            stride 0); Hq / Hkv <= 128
  *   lse      float32 [batch, Hq, T] contiguous
  *   cache    K is read (V is not)
  *   acc      float32 [num_blocks, num_kv_heads, block_size], the sums of the

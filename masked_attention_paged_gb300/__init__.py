@@ -240,6 +240,18 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _fresh(make, stream, device):
+    """make(), its memory of the stream that the call runs on: what a call
+    allocates must neither wait for nor be reused on the current stream when
+    another one was passed."""
+    if stream is None or device.type != "cuda":
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return make()
+
+
 def _check(name: str, st: int):
     if st != 0:
         raise LibAttnError(name, st)
@@ -811,7 +823,7 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, in
     the transposed rotation, which is its gradient.  out may be x."""
     lib = load()
     if out is None:
-        out = torch.empty_like(x)
+        out = _fresh(lambda: torch.empty_like(x), stream, x.device)
     elif not (out.dtype == x.dtype and out.shape == x.shape):
         raise ValueError(f"out must be {x.dtype} {tuple(x.shape)}")
     if x.is_cuda:
@@ -840,7 +852,7 @@ def _rope_append(name, cache, device, q, k_new, v_new, positions, freqs, block_t
                  q_out, workspace, stream):
     lib = load()
     if q_out is None:
-        q_out = torch.empty_like(q)
+        q_out = _fresh(lambda: torch.empty_like(q), stream, q.device)
     elif not (q_out.dtype == q.dtype and q_out.shape == q.shape):
         raise ValueError(f"q_out must be {q.dtype} {tuple(q.shape)}")
     full = q_out
@@ -874,7 +886,7 @@ def rope_kv_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, po
     i.  Without the T dimension (and positions [B]): one token a sequence.
     Returns the rotated q (q_out may be q)."""
     if q_out is None:
-        q_out = torch.empty_like(q)
+        q_out = _fresh(lambda: torch.empty_like(q), stream, q.device)
     if k_cache.is_cuda:
         ws = workspace or _small_ws(k_cache.device)
         packed = _pack("yyyRf==Ycbv===", q, k_new, v_new, positions, freqs, int(bool(interleaved)), float(magnitude),
@@ -930,9 +942,10 @@ def paged_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty_strided((B, Hq, T, D), (T * Hq * D, D, Hq * D, 1), dtype=q.dtype, device=q.device)
+        out = _fresh(lambda: torch.empty_strided((B, Hq, T, D), (T * Hq * D, D, Hq * D, 1), dtype=q.dtype,
+                                                 device=q.device), stream, q.device)
     if lse is None and return_lse:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+        lse = _fresh(lambda: torch.empty((B, Hq, T), dtype=torch.float32, device=q.device), stream, q.device)
     if workspace is not None and q.is_cuda:
         packed = _pack("xoocbvq=Xl===", q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parents, float(scale),
                        out, lse, workspace.ptr, workspace.nbytes, _stream(stream))
@@ -951,8 +964,8 @@ def paged_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     max_blocks = block_table.shape[1]
     ws = workspace
     if ws is None:
-        ws = Workspace(paged_tree_workspace_size(B, Hq, k_cache.shape[1], T, max_blocks, k_cache.shape[2], D),
-                       device=q.device)
+        need = paged_tree_workspace_size(B, Hq, k_cache.shape[1], T, max_blocks, k_cache.shape[2], D)
+        ws = _fresh(lambda: Workspace(need, device=q.device), stream, q.device)
     dk = _tensor_bytes(k_new) if k_new is not None else None
     dv = _tensor_bytes(v_new) if v_new is not None else None
     st = lib.paged_tree_attn(_tensor_bytes(q), dk, dv, c, _ptr(block_table, "block_table"),
@@ -1036,8 +1049,8 @@ def paged_attn_weights(q: torch.Tensor, lse: torch.Tensor, k_cache: torch.Tensor
     max_blocks = block_table.shape[1]
     ws = workspace
     if ws is None:
-        ws = Workspace(paged_attn_weights_workspace_size(B, k_cache.shape[1], max_blocks, k_cache.shape[2]),
-                       device=q.device)
+        need = paged_attn_weights_workspace_size(B, k_cache.shape[1], max_blocks, k_cache.shape[2])
+        ws = _fresh(lambda: Workspace(need, device=q.device), stream, q.device)
     st = lib.paged_attn_weights(_tensor_bytes(q), _ptr(lse, "lse"), c, _ptr(block_table, "block_table"),
                                 block_table.stride(0), max_blocks, _ptr(start_pos, "start_pos"),
                                 _ptr(q_lens, "q_lens"), int(bool(causal)), float(scale), _ptr(acc, "acc"), ws.ptr,
@@ -1058,9 +1071,10 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
     B, Hkv = ctx_lens.shape[0], k_cache.shape[1]
     keep = int(keep)
     if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=k_cache.device)
+        new_lens = _fresh(lambda: torch.empty(B, dtype=torch.int32, device=k_cache.device), stream, k_cache.device)
     if kept is None:
-        kept = torch.empty((B, Hkv, max(keep, 0)), dtype=torch.int32, device=k_cache.device)
+        kept = _fresh(lambda: torch.empty((B, Hkv, max(keep, 0)), dtype=torch.int32, device=k_cache.device), stream,
+                      k_cache.device)
     if k_cache.is_cuda and kept.shape == (B, Hkv, keep):
         ws = workspace or _small_ws(k_cache.device)
         packed = _pack("cAbVb====vK===", k_cache, v_cache, acc, block_table, ctx_lens, dst_block_table, B, keep,

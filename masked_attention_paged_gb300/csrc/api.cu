@@ -46,6 +46,14 @@ bool vec16_ok(const attn_tensor* t) {
   return true;
 }
 
+// Rows that a TMA map can walk: vec16_ok, and no stride of zero over more than one
+// element.
+bool tma_rows_ok(const attn_tensor* t) {
+  for (int i = 0; i < t->ndim - 1; ++i)
+    if (t->stride[i] == 0 && t->shape[i] > 1) return false;
+  return vec16_ok(t);
+}
+
 View4 view(const attn_tensor* t) {
   View4 v;
   v.data = t->data;
@@ -718,8 +726,8 @@ attn_status paged_tree_attn(const attn_tensor* q, const attn_tensor* k_new, cons
   if (B == 0 || T == 0) return ATTN_OK;
   if (block_table == nullptr || ctx_lens == nullptr || parents == nullptr) return ATTN_ERR_INVALID_ARG;
   if (B > 1 && (bt_stride < max_blocks || (par_stride_b != 0 && par_stride_b < T))) return ATTN_ERR_INVALID_ARG;
-  if (!vec16_ok(q) || !vec16_ok(out)) return ATTN_ERR_INVALID_ARG;
-  if (k_new != nullptr && (!vec16_ok(k_new) || !vec16_ok(v_new))) return ATTN_ERR_INVALID_ARG;
+  if (!tma_rows_ok(q) || !vec16_ok(out)) return ATTN_ERR_INVALID_ARG;
+  if (k_new != nullptr && (!tma_rows_ok(k_new) || !tma_rows_ok(v_new))) return ATTN_ERR_INVALID_ARG;
   TreeArgs a;
   a.cache = paged(cache);
   a.q = view(q);
@@ -801,7 +809,7 @@ attn_status paged_attn_weights(const attn_tensor* q, const float* lse, const att
   if (block_table == nullptr || start_pos == nullptr || lse == nullptr || acc == nullptr) return ATTN_ERR_INVALID_ARG;
   if (!aligned(lse, 4) || !aligned(acc, 4)) return ATTN_ERR_INVALID_ARG;
   if (B > 1 && bt_stride < max_blocks) return ATTN_ERR_INVALID_ARG;
-  if (!vec16_ok(q)) return ATTN_ERR_INVALID_ARG;
+  if (!tma_rows_ok(q)) return ATTN_ERR_INVALID_ARG;
   WeightArgs a;
   a.cache = paged(cache);
   a.q = view(q);

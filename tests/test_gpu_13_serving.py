@@ -176,6 +176,42 @@ def test_the_same_steps_as_one_graph():
     assert s.ws.status() == 0
 
 
+def test_another_stream_than_the_current_one():
+    """What a call allocates belongs to the stream that it runs on: nothing still queued on the current stream may
+    write to it, and it may be called with a raw handle."""
+    s = _Server(64, seed=3)
+    lens, parents, path, n = _int([T0, 31, 5]), _int([PARENTS] * B), _int(PATHS), _int(ACCEPT)
+    s.kc.copy_(torch.randn(s.kc.shape, generator=s.gen))
+    s.vc.copy_(torch.randn(s.vc.shape, generator=s.gen))
+    q, k, v, pos = s.rand(HQ, T1), s.rand(HKV, T1), s.rand(HKV, T1), _int([DEPTH] * B)
+    start = s.kc.clone(), s.vc.clone(), s.acc.clone()
+    big = torch.randn(4096, 4096, device=DEV)
+
+    def chain(stream):
+        for x, y in zip((s.kc, s.vc, s.acc), start):
+            x.copy_(y)
+        torch.cuda.synchronize()
+        if stream is not None:
+            for _ in range(20):
+                big @ big  # the current stream stays busy, and fills what it then frees
+            for shape in ((B, HQ, T1, 64), (B, HQ, T1), (B, HKV, 40), (B,)):
+                torch.full(shape, 7, dtype=torch.int32, device=DEV)
+        kw = dict(stream=stream)
+        rq, rk = lib.rope_apply(q, pos, s.fr, **kw), lib.rope_apply(k, pos, s.fr, **kw)
+        out, lse = lib.paged_tree_attn(rq, s.kc, s.vc, s.bt, lens, parents, k_new=rk, v_new=v, return_lse=True, **kw)
+        lib.kv_tree_accept(s.kc, s.vc, s.bt, lens, path, n, **kw)
+        lib.paged_attn_weights(rq, lse, s.kc, s.bt, lens, s.acc, q_lens=n, **kw)
+        nl, kept = lib.kv_evict(s.kc, s.vc, s.acc, s.bt, lens, s.dt, 40, sink=1, recent=2, **kw)
+        torch.cuda.synchronize()
+        return [x.clone() for x in (rq, out, lse, s.kc, s.vc, s.acc, nl, kept)]
+
+    want = chain(None)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        for x, y in zip(chain(stream), want):
+            assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("D,Hkv", [(128, 2), (64, 1)])
 def test_a_captured_decode_step_whose_contexts_grow(D, Hkv):
     """One graph over contexts that gain splits between replays, and lose some again: the eager call's bits."""

@@ -47,6 +47,13 @@ def test_paged_tree_rejects(L):
     assert call(out=_t([2, 12, 7, 128])) == INVALID
     assert call(q=_t([2, 12, 6, 128], data=FAKE + 8)) == INVALID
     assert call(out=_t([2, 12, 6, 128], data=FAKE + 8)) == INVALID
+    flat = _t([2, 12, 6, 128])
+    flat.stride[1] = 0  # one row for all heads
+    assert call(q=flat) == INVALID
+    assert call(k=kn, v=kn) != INVALID
+    one = _t([2, 4, 6, 128])
+    one.stride[0] = 0
+    assert call(k=kn, v=one) == INVALID
     assert call(scale=float("nan")) == INVALID
     assert call(cl=None) == INVALID
     assert call(par=None) == INVALID
