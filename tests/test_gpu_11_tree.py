@@ -330,3 +330,44 @@ def test_accept(D, Hkv):
     lib.kv_tree_accept(k2, vc.clone(), bt[:1], args[1][:1], args[2][:1], torch.tensor(n[:1], dtype=torch.int32,
                                                                                      device=DEV), workspace=ws)
     assert ws.status() == 5 and torch.equal(k2, kc)
+
+
+@pytest.mark.parametrize("before", ["nothing", "memset", "copy", "join"])
+def test_accept_captured_after_anything(before):
+    """The call may begin a graph, follow work that is no kernel, or wait for two streams: it sees what they wrote."""
+    g = _gen(17)
+    kc, vc = (torch.randn(12, 2, 16, 64, generator=g).bfloat16().to(DEV) for _ in range(2))
+    bt = torch.randperm(12, generator=g).to(torch.int32).view(2, 6).to(DEV)
+    ctx, path = torch.tensor([10, 30], dtype=torch.int32), torch.tensor([[0, 2, 5], [1, 4, 0]], dtype=torch.int32)
+    n = torch.tensor([3, 2], dtype=torch.int32)
+    want = [c.clone() for c in (kc, vc)]
+    ws = lib.Workspace(256)
+    dev = [x.to(DEV) for x in (ctx, path, n)]
+    lib.kv_tree_accept(*want, bt, *dev, workspace=ws)
+    spare = dev[0].clone()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    k2, v2 = kc.clone(), vc.clone()
+    with torch.cuda.graph(graph):
+        if before == "memset":
+            dev[0].zero_()
+        elif before in ("copy", "join"):
+            dev[0].copy_(spare)
+        if before == "join":
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                k2.copy_(kc)
+            v2.copy_(vc)
+            torch.cuda.current_stream().wait_stream(side)
+        lib.kv_tree_accept(k2, v2, bt, *dev, workspace=ws)
+    if before == "memset":
+        ctx.zero_()
+        want = [c.clone() for c in (kc, vc)]
+        lib.kv_tree_accept(*want, bt, ctx.to(DEV), *dev[1:], workspace=ws)
+    for _ in range(3):
+        k2.copy_(kc)
+        v2.copy_(vc)
+        graph.replay()
+        assert torch.equal(k2, want[0]) and torch.equal(v2, want[1])
+        if before in ("copy", "join"):
+            dev[0].random_(0, 20)
+    assert ws.status() == 0
