@@ -208,13 +208,15 @@ def _cache_bytes(k_cache: torch.Tensor, v_cache: torch.Tensor) -> bytes:
     return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), _dtype_code(k_cache), bs, nb, heads, D)
 
 
-_marshal = None      # the compiled packer (marshal.cpp), or None
+_marshal = None      # the compiled caller (marshal.cpp), or None
 _marshal_tried = False
+_entries: dict = {}  # C entry points' addresses
 
 
-def _pack(fmt: str, *args):
-    """A C entry point's arguments in one step, or None: the caller then takes
-    them one by one, with every check worded."""
+def _call(name: str, fmt: str, *args) -> bool:
+    """The C entry point, its arguments checked and converted in one step; False
+    (and nothing called) where they are not plainly as documented: the caller
+    then takes them one by one, with every check worded."""
     global _marshal, _marshal_tried
     if not _marshal_tried:
         _marshal_tried = True
@@ -223,11 +225,19 @@ def _pack(fmt: str, *args):
             loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
             try:
                 _marshal = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
-            except ImportError:  # built against another Python: the checks below serve
+            except ImportError:  # built against another Python: the checks serve
                 pass
     if _marshal is None:
-        return None
-    return _marshal.pack(fmt, torch.cuda.current_device(), *args)
+        return False
+    entry = _entries.get(name)
+    if entry is None:
+        entry = _entries[name] = ctypes.cast(getattr(load(), name), ctypes.c_void_p).value
+    st = _marshal.call(entry, name, fmt, torch.cuda.current_device(), *args)
+    if st is None:
+        return False
+    if st != 0:
+        raise LibAttnError(name, st)
+    return True
 
 
 def _stream(stream) -> int:
@@ -827,10 +837,8 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, in
     elif not (out.dtype == x.dtype and out.shape == x.shape):
         raise ValueError(f"out must be {x.dtype} {tuple(x.shape)}")
     if x.is_cuda:
-        packed = _pack("yRf===Y=", x, positions, freqs, int(bool(interleaved)), int(bool(inverse)), float(magnitude),
-                       out, _stream(stream))
-        if packed is not None:
-            _check("rope_apply", lib.rope_apply(*packed))
+        if _call("rope_apply", "yRf===Y=", x, positions, freqs, int(bool(interleaved)), int(bool(inverse)),
+                 float(magnitude), out, _stream(stream)):
             return out
     full = out
     if x.dim() == 3:
@@ -889,10 +897,8 @@ def rope_kv_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, po
         q_out = _fresh(lambda: torch.empty_like(q), stream, q.device)
     if k_cache.is_cuda:
         ws = workspace or _small_ws(k_cache.device)
-        packed = _pack("yyyRf==Ycbv===", q, k_new, v_new, positions, freqs, int(bool(interleaved)), float(magnitude),
-                       q_out, k_cache, v_cache, block_table, start_pos, ws.ptr, ws.nbytes, _stream(stream))
-        if packed is not None:
-            _check("rope_kv_append", load().rope_kv_append(*packed))
+        if _call("rope_kv_append", "yyyRf==Ycbv===", q, k_new, v_new, positions, freqs, int(bool(interleaved)),
+                 float(magnitude), q_out, k_cache, v_cache, block_table, start_pos, ws.ptr, ws.nbytes, _stream(stream)):
             return q_out
     return _rope_append("rope_kv_append", _cache_bytes(k_cache, v_cache), k_cache.device, q, k_new, v_new, positions,
                         freqs, block_table, start_pos, interleaved, magnitude, q_out, workspace, stream)
@@ -947,10 +953,8 @@ def paged_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if lse is None and return_lse:
         lse = _fresh(lambda: torch.empty((B, Hq, T), dtype=torch.float32, device=q.device), stream, q.device)
     if workspace is not None and q.is_cuda:
-        packed = _pack("xoocbvq=Xl===", q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parents, float(scale),
-                       out, lse, workspace.ptr, workspace.nbytes, _stream(stream))
-        if packed is not None:
-            _check("paged_tree_attn", lib.paged_tree_attn(*packed))
+        if _call("paged_tree_attn", "xoocbvq=Xl===", q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parents,
+                 float(scale), out, lse, workspace.ptr, workspace.nbytes, _stream(stream)):
             return (out, lse) if return_lse else out
     _check_block_table(block_table, B)
     _check_int32_vec(ctx_lens, B, "ctx_lens")
@@ -985,10 +989,8 @@ def kv_tree_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: to
     B = ctx_lens.shape[0]
     if k_cache.is_cuda:
         ws = workspace or _small_ws(k_cache.device)
-        packed = _pack("cbVrv====", k_cache, v_cache, block_table, ctx_lens, path, n_accept, B, ws.ptr, ws.nbytes,
-                       _stream(stream))
-        if packed is not None:
-            _check("kv_tree_accept", lib.kv_tree_accept(*packed))
+        if _call("kv_tree_accept", "cbVrv====", k_cache, v_cache, block_table, ctx_lens, path, n_accept, B, ws.ptr,
+                 ws.nbytes, _stream(stream)):
             return
     _check_block_table(block_table, B)
     _check_int32_vec(ctx_lens, B, "ctx_lens")
@@ -1027,11 +1029,9 @@ def paged_attn_weights(q: torch.Tensor, lse: torch.Tensor, k_cache: torch.Tensor
     Hq] for one token a sequence.  q_lens int32 [B]: queries of each sequence."""
     lib = load()
     if workspace is not None and q.is_cuda:
-        packed = _pack("ylcbvn==A===", q, lse, k_cache, k_cache, block_table, start_pos, q_lens, int(bool(causal)),
-                       float(1.0 / math.sqrt(q.shape[-1]) if scale is None else scale), acc, workspace.ptr,
-                       workspace.nbytes, _stream(stream))
-        if packed is not None:
-            _check("paged_attn_weights", lib.paged_attn_weights(*packed))
+        if _call("paged_attn_weights", "ylcbvn==A===", q, lse, k_cache, k_cache, block_table, start_pos, q_lens,
+                 int(bool(causal)), float(1.0 / math.sqrt(q.shape[-1]) if scale is None else scale), acc, workspace.ptr,
+                 workspace.nbytes, _stream(stream)):
             return acc
     if q.dim() == 3:
         q, lse = q.unsqueeze(2), lse.unsqueeze(2)
@@ -1077,10 +1077,8 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
                       k_cache.device)
     if k_cache.is_cuda and kept.shape == (B, Hkv, keep):
         ws = workspace or _small_ws(k_cache.device)
-        packed = _pack("cAbVb====vK===", k_cache, v_cache, acc, block_table, ctx_lens, dst_block_table, B, keep,
-                       int(sink), int(recent), new_lens, kept, ws.ptr, ws.nbytes, _stream(stream))
-        if packed is not None:
-            _check("kv_evict", lib.kv_evict(*packed))
+        if _call("kv_evict", "cAbVb====vK===", k_cache, v_cache, acc, block_table, ctx_lens, dst_block_table, B, keep,
+                 int(sink), int(recent), new_lens, kept, ws.ptr, ws.nbytes, _stream(stream)):
             return new_lens, kept
     _check_block_table(block_table, B)
     _check_int32_vec(ctx_lens, B, "ctx_lens")

@@ -1,39 +1,69 @@
-// marshal.cpp -- the binding's arguments in one step.
+// marshal.cpp -- a call of the binding in one step.
 //
 // A call of a few microseconds on the GPU is bound by the host: in Python, reading
-// the pointer, type, shape and strides of a dozen tensors and checking them takes
-// longer than the launch.  pack(format, device, ...) does that for a whole call and
-// returns the C entry point's arguments as a tuple, or None when anything is not
-// plainly as the format says; the Python code then goes through its own checks,
-// which word the refusal (or take the rarer form).  Nothing is kept between calls.
+// the pointer, type, shape and strides of a dozen tensors, checking them and
+// converting them for the C entry takes longer than the launch.  call(address,
+// name, format, device, ...) does that for a whole call and returns the entry's
+// status, or None (and calls nothing) when anything is not plainly as the format
+// says; the Python code then goes through its own checks, which word the refusal
+// (or take the rarer form).  Nothing is kept between calls.
 //
 // Format letters (sizes B, H, T, D are those of the first x / y):
-//   x  tensor, bf16 or f32, 4-D          -> attn_tensor as bytes
+//   x  tensor, bf16 or f32, 4-D          -> attn_tensor
 //   y  the same, or 3-D [B, H, D] rows read as [B, H, 1, D]; all y's alike
 //   X, Y  as x, y, of the first's sizes (Y: and type)
-//   o  as x, or None                     -> bytes or None
-//   c  two tensors: a K and a V cache    -> attn_kv_cache as bytes
+//   o  as x, or None                     -> attn_tensor or null
+//   c  two tensors: a K and a V cache    -> attn_kv_cache
 //   b  block table, >= B rows            -> pointer, row stride, columns
 //   V  int32 vector that sets B          -> pointer
 //   v  int32 vector of B                 -> pointer
-//   n  int32 vector of B, or None        -> pointer or None
+//   n  int32 vector of B, or None        -> pointer or null
 //   R  int32 [B, T] rows (y's 3-D: [B])  -> pointer, row stride
 //   r  int32 [B, n] rows                 -> pointer, row stride, n
 //   q  int32 [B, T] rows                 -> pointer, row stride
 //   f  int64 frequencies, 1 .. D / 2     -> pointer, twice their number
-//   l  f32, contiguous, B H T elements, or None -> pointer or None
+//   l  f32, contiguous, B H T elements, or None -> pointer or null
 //   A  f32 [blocks, Hkv, 16] of the cache -> pointer
 //   K  int32, contiguous [B, Hkv, n]     -> pointer
-//   =  any object                        -> itself
+//   =  an int, a float, or None          -> itself
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
+#include <utility>
 
 #include "libattn.h"
 
 namespace {
+
+// One argument of a C entry: a pointer or an integer, or a float.
+struct Value {
+  int64_t i = 0;
+  double d = 0.0;
+};
+
+template <typename T>
+T as(const Value& v) {
+  if constexpr (std::is_pointer_v<T>)
+    return reinterpret_cast<T>(static_cast<intptr_t>(v.i));
+  else if constexpr (std::is_floating_point_v<T>)
+    return static_cast<T>(v.d);
+  else
+    return static_cast<T>(v.i);
+}
+
+template <typename... A, size_t... I>
+int invoke(attn_status (*fn)(A...), const Value* v, std::index_sequence<I...>) {
+  return static_cast<int>(fn(as<A>(v[I])...));
+}
+// fn: an entry of this declaration, at `address`; -1 if it takes another number of arguments
+template <typename... A>
+int invoke(attn_status (*)(A...), intptr_t address, const Value* v, size_t n) {
+  if (n != sizeof...(A)) return -1;
+  return invoke(reinterpret_cast<attn_status (*)(A...)>(address), v, std::index_sequence_for<A...>());
+}
 
 struct Sizes {
   int64_t B = -1, H = 0, T = 0, D = 0;
@@ -72,30 +102,32 @@ bool int32_rows(const at::Tensor& t, int64_t device) {
   return on(t, device) && t.scalar_type() == at::kInt && t.dim() == 2 && (t.size(1) <= 1 || t.stride(1) == 1);
 }
 
-PyObject* address(const at::Tensor& t) { return PyLong_FromVoidPtr(t.data_ptr()); }
-
-PyObject* pack(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  if (nargs < 2 || !PyUnicode_Check(args[0]) || !PyLong_Check(args[1])) {
-    PyErr_SetString(PyExc_TypeError, "pack(format, device, ...)");
+PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  if (nargs < 4 || !PyLong_Check(args[0]) || !PyUnicode_Check(args[1]) || !PyUnicode_Check(args[2]) ||
+      !PyLong_Check(args[3])) {
+    PyErr_SetString(PyExc_TypeError, "call(address, name, format, device, ...)");
     return nullptr;
   }
-  const char* f = PyUnicode_AsUTF8(args[0]);
-  const int64_t device = PyLong_AsLongLong(args[1]);
-  if (f == nullptr || (device == -1 && PyErr_Occurred())) return nullptr;
-  PyObject* out[64];
-  int n = 0;
-  Py_ssize_t a = 2;
+  const intptr_t entry = static_cast<intptr_t>(PyLong_AsLongLong(args[0]));
+  const char* name = PyUnicode_AsUTF8(args[1]);
+  const char* f = PyUnicode_AsUTF8(args[2]);
+  const int64_t device = PyLong_AsLongLong(args[3]);
+  if (name == nullptr || f == nullptr || PyErr_Occurred()) return nullptr;
+  constexpr int kMost = 32;
+  Value out[kMost];
+  attn_tensor tensors[8];
+  attn_kv_cache cache;
+  int n = 0, n_tensors = 0;
+  Py_ssize_t a = 4;
   Sizes s;
   bool ok = true, error = false;
-  auto put = [&](PyObject* o) {
-    if (o == nullptr || n == 64) {
-      error = true;
-      Py_XDECREF(o);
-    } else {
-      out[n++] = o;
-    }
+  auto put = [&](int64_t i) {
+    if (n == kMost)
+      ok = false;
+    else
+      out[n++].i = i;
   };
-  auto none = [&] { Py_INCREF(Py_None); put(Py_None); };
+  auto address = [](const void* p) { return static_cast<int64_t>(reinterpret_cast<intptr_t>(p)); };
   try {
     for (; ok && !error && *f != 0; ++f) {
       if (a >= nargs) {
@@ -103,13 +135,20 @@ PyObject* pack(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
         break;
       }
       PyObject* o = args[a++];
-      if (*f == '=') {
-        Py_INCREF(o);
-        put(o);
+      if (o == Py_None && (*f == '=' || *f == 'o' || *f == 'n' || *f == 'l')) {
+        put(0);
         continue;
       }
-      if (o == Py_None && (*f == 'o' || *f == 'n' || *f == 'l')) {
-        none();
+      if (*f == '=') {
+        if (PyFloat_Check(o) && n < kMost) {
+          out[n++].d = PyFloat_AS_DOUBLE(o);
+        } else if (PyLong_Check(o)) {
+          int past = 0;
+          put(PyLong_AsLongLongAndOverflow(o, &past));
+          ok = ok && past == 0;
+        } else {
+          ok = false;
+        }
         continue;
       }
       if (!THPVariable_Check(o)) {
@@ -123,7 +162,11 @@ PyObject* pack(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
         case 'X':
         case 'Y':
         case 'o': {
-          attn_tensor d;
+          if (n_tensors == 8) {
+            ok = false;
+            break;
+          }
+          attn_tensor& d = tensors[n_tensors];
           const bool first = s.B < 0;
           const bool insert = (*f == 'y' || *f == 'Y') && (first ? t.dim() == 3 : s.one_token);
           ok = describe(t, device, insert, &d);
@@ -136,7 +179,8 @@ PyObject* pack(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
             s.type = t.scalar_type();
             s.one_token = insert;
           }
-          put(PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&d), sizeof(d)));
+          ++n_tensors;
+          put(address(&d));
           break;
         }
         case 'c': {
@@ -149,7 +193,7 @@ PyObject* pack(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
                t.scalar_type() == v.scalar_type() && t.is_contiguous() && v.is_contiguous() &&
                (t.scalar_type() == at::kBFloat16 || t.scalar_type() == at::kFloat);
           if (!ok) break;
-          attn_kv_cache c;
+          attn_kv_cache& c = cache;
           std::memset(&c, 0, sizeof(c));
           c.k = t.data_ptr();
           c.v = v.data_ptr();
@@ -158,7 +202,7 @@ PyObject* pack(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
           c.num_kv_heads = static_cast<int32_t>(s.kv_heads = t.size(1));
           c.block_size = static_cast<int32_t>(s.slots = t.size(2));
           c.head_dim = static_cast<int32_t>(t.size(3));
-          put(PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&c), sizeof(c)));
+          put(address(&c));
           break;
         }
         case 'b':
@@ -166,9 +210,9 @@ PyObject* pack(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
                t.stride(0) >= t.size(1);
           if (!ok) break;
           s.table_rows = s.table_rows < 0 ? t.size(0) : std::min(s.table_rows, t.size(0));
-          put(address(t));
-          put(PyLong_FromLongLong(t.stride(0)));
-          put(PyLong_FromLongLong(t.size(1)));
+          put(address(t.data_ptr()));
+          put(t.stride(0));
+          put(t.size(1));
           break;
         case 'V':
         case 'v':
@@ -181,85 +225,89 @@ PyObject* pack(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
             ok = s.table_rows < 0 || s.table_rows >= s.B;
             if (!ok) break;
           }
-          put(address(t));
+          put(address(t.data_ptr()));
           break;
         case 'R':
           if (s.one_token) {  // [B]: a row of one
             ok = on(t, device) && t.scalar_type() == at::kInt && t.dim() == 1 && t.size(0) == s.B;
             if (!ok) break;
-            put(address(t));
-            put(PyLong_FromLongLong(t.stride(0)));
+            put(address(t.data_ptr()));
+            put(t.stride(0));
             break;
           }
           [[fallthrough]];
         case 'q':
           ok = int32_rows(t, device) && t.size(0) == s.B && t.size(1) == s.T;
           if (!ok) break;
-          put(address(t));
-          put(PyLong_FromLongLong(t.stride(0)));
+          put(address(t.data_ptr()));
+          put(t.stride(0));
           break;
         case 'r':
           ok = int32_rows(t, device) && t.size(0) == s.B;
           if (!ok) break;
-          put(address(t));
-          put(PyLong_FromLongLong(t.stride(0)));
-          put(PyLong_FromLongLong(t.size(1)));
+          put(address(t.data_ptr()));
+          put(t.stride(0));
+          put(t.size(1));
           break;
         case 'f':
           ok = on(t, device) && t.scalar_type() == at::kLong && t.dim() == 1 && t.is_contiguous() && t.size(0) >= 1 &&
                t.size(0) <= s.D / 2;
           if (!ok) break;
-          put(address(t));
-          put(PyLong_FromLongLong(2 * t.size(0)));
+          put(address(t.data_ptr()));
+          put(2 * t.size(0));
           break;
         case 'l':
           ok = on(t, device) && t.scalar_type() == at::kFloat && t.is_contiguous() && t.numel() == s.B * s.H * s.T;
           if (!ok) break;
-          put(address(t));
+          put(address(t.data_ptr()));
           break;
         case 'A':
           ok = on(t, device) && t.scalar_type() == at::kFloat && t.is_contiguous() && t.dim() == 3 &&
                t.size(0) == s.blocks && t.size(1) == s.kv_heads && t.size(2) == s.slots;
           if (!ok) break;
-          put(address(t));
+          put(address(t.data_ptr()));
           break;
         case 'K':
           ok = on(t, device) && t.scalar_type() == at::kInt && t.is_contiguous() && t.dim() == 3 && t.size(0) == s.B &&
                t.size(1) == s.kv_heads;
           if (!ok) break;
-          put(address(t));
+          put(address(t.data_ptr()));
           break;
         default:
-          PyErr_Format(PyExc_ValueError, "pack: no format letter %c", *f);
+          PyErr_Format(PyExc_ValueError, "call: no format letter %c", *f);
           error = true;
       }
     }
   } catch (...) {  // a tensor without storage and the like: not plainly what the format says
     ok = false;
   }
-  if (!error && ok && a != nargs) ok = false;
-  if (error || !ok) {
-    for (int i = 0; i < n; ++i) Py_DECREF(out[i]);
-    if (error) {
-      if (!PyErr_Occurred()) PyErr_NoMemory();
-      return nullptr;
-    }
-    Py_RETURN_NONE;
-  }
-  PyObject* tuple = PyTuple_New(n);
-  if (tuple == nullptr) {
-    for (int i = 0; i < n; ++i) Py_DECREF(out[i]);
-    return nullptr;
-  }
-  for (int i = 0; i < n; ++i) PyTuple_SET_ITEM(tuple, i, out[i]);
-  return tuple;
+  if (error) return nullptr;
+  if (!ok || a != nargs) Py_RETURN_NONE;
+  int st = -1;
+  const size_t count = static_cast<size_t>(n);
+  Py_BEGIN_ALLOW_THREADS;
+  if (std::strcmp(name, "rope_kv_append") == 0)
+    st = invoke(&rope_kv_append, entry, out, count);
+  else if (std::strcmp(name, "rope_apply") == 0)
+    st = invoke(&rope_apply, entry, out, count);
+  else if (std::strcmp(name, "paged_tree_attn") == 0)
+    st = invoke(&paged_tree_attn, entry, out, count);
+  else if (std::strcmp(name, "kv_tree_accept") == 0)
+    st = invoke(&kv_tree_accept, entry, out, count);
+  else if (std::strcmp(name, "paged_attn_weights") == 0)
+    st = invoke(&paged_attn_weights, entry, out, count);
+  else if (std::strcmp(name, "kv_evict") == 0)
+    st = invoke(&kv_evict, entry, out, count);
+  Py_END_ALLOW_THREADS;
+  if (st < 0) return PyErr_Format(PyExc_ValueError, "call: %s with %d arguments", name, n);
+  return PyLong_FromLong(st);
 }
 
 PyMethodDef kMethods[] = {
-    {"pack", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(pack)), METH_FASTCALL,
-     "pack(format, device, ...): a C entry point's arguments, or None"},
+    {"call", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(call)), METH_FASTCALL,
+     "call(address, name, format, device, ...): a C entry point's status, or None"},
     {nullptr, nullptr, 0, nullptr}};
-PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", "The binding's arguments in one step.", -1, kMethods,
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", "A call of the binding in one step.", -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

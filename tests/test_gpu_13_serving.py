@@ -4,6 +4,7 @@ the weights that each call's rows give to the cached tokens, the eviction, and
 on over the shorter cache.  Every step is held against its definition in 64
 bits, from the tensors that it was given, with the bounds of that operator's own
 tests; a chain of steps as one captured graph gives the eager chain's bits."""
+import ctypes
 import math
 import os
 import sys
@@ -153,7 +154,8 @@ def test_the_same_steps_as_one_graph():
                                        workspace=s.ws)
         lib.kv_tree_accept(s.kc, s.vc, s.bt, lens, path, n, workspace=s.ws)
         lib.paged_attn_weights(torch.gather(rq, 2, idx[..., None].expand(B, HQ, 4, 128)),
-                               torch.gather(lse, 2, idx).contiguous(), s.kc, s.bt, lens, s.acc, q_lens=n, workspace=s.ws)
+                               torch.gather(lse, 2, idx).contiguous(), s.kc, s.bt, lens, s.acc, q_lens=n,
+                               workspace=s.ws)
         lib.kv_evict(s.kc, s.vc, s.acc, s.bt, lens + n, s.dt, 40, sink=SINK, recent=RECENT, new_lens=new_lens,
                      kept=kept, workspace=s.ws)
         return rq, out, lse
@@ -236,19 +238,37 @@ def test_a_captured_decode_step_whose_contexts_grow(D, Hkv):
     assert ws.status() == 0
 
 
-def test_the_packed_arguments_are_those_of_the_worded_checks(monkeypatch):
-    """Each call takes its arguments in one compiled step where they are plainly as documented: the same tuple."""
+def test_a_compiled_call_passes_what_the_worded_checks_pass(monkeypatch):
+    """Each call takes its arguments in one compiled step where they are plainly as documented: the same ones."""
     s = _Server(64, seed=1)
-    got = []
+    got, keep = [], []
+    bytes_of = lambda p, n: ctypes.string_at(p, n)  # noqa: E731
+
+    def entry(name):
+        """A C function of the entry's type that notes its arguments, descriptors by their bytes."""
+        res, types = lib._signatures()[name]
+        tensors, cache = {"rope_apply": ((0, 8), -1), "rope_kv_append": ((0, 1, 2, 9), 10),
+                          "paged_tree_attn": ((0, 1, 2, 11), 3), "kv_tree_accept": ((), 0),
+                          "paged_attn_weights": ((0,), 2), "kv_evict": ((), 0)}[name]
+
+        def note(*args):
+            seen = list(args)
+            for i in (*tensors, cache):
+                if i >= 0 and seen[i] is not None:
+                    seen[i] = bytes_of(seen[i], ctypes.sizeof(lib.AttnKVCache if i == cache else lib.AttnTensor))
+            got.append((name, seen))
+            return 0
+        keep.append(ctypes.CFUNCTYPE(res, *types)(note))
+        return keep[-1]
+
+    names = ("rope_apply", "rope_kv_append", "paged_tree_attn", "kv_tree_accept", "paged_attn_weights", "kv_evict")
+    fake = {n: entry(n) for n in names}
 
     class Recorder:
         def __getattr__(self, name):
-            def call(*args):
-                got.append((name, args))
-                return 0
-            return call
+            return ctypes.CFUNCTYPE(ctypes.c_int, *lib._signatures()[name][1])(
+                ctypes.cast(fake[name], ctypes.c_void_p).value)
 
-    monkeypatch.setattr(lib, "load", lambda *a, **k: Recorder())
     lens, path, n = _int([5, 6, 7]), _int(PATHS), _int(ACCEPT)
     q, k, v, pos = s.rand(HQ, T1), s.rand(HKV, T1), s.rand(HKV, T1), _int([DEPTH] * B)
     out, lse = torch.empty_like(q), torch.empty(B, HQ, T1, device=DEV)
@@ -268,28 +288,35 @@ def test_the_packed_arguments_are_those_of_the_worded_checks(monkeypatch):
         lambda: lib.kv_evict(s.kc, s.vc, s.acc, s.bt, lens, s.dt, 40, sink=1, recent=2, new_lens=nl, kept=kept,
                              workspace=ws),
     ]
-    for call in calls:
-        call()
-    packed, got[:] = list(got), []
-    whole = lib._pack
+    lib.rope_apply(q, pos, s.fr)  # the module is loaded
     assert lib._marshal is not None, "marshal.cpp was not built"
-    monkeypatch.setattr(lib, "_pack", lambda *a: None)
+    monkeypatch.setattr(lib, "_entries", {n: ctypes.cast(f, ctypes.c_void_p).value for n, f in fake.items()})
     for call in calls:
         call()
-    plain = list(got)
-    value = lambda x: bytes(x) if isinstance(x, (bytes, bytearray)) else getattr(x, "value", x)  # noqa: E731
-    for (na, a), (nb, b) in zip(packed, plain):
-        assert na == nb and [value(x) for x in a] == [value(x) for x in b], na
-    # what is not plainly as documented goes the other way
-    dev = torch.cuda.current_device()
-    assert whole("yR", q, pos) is not None
+    compiled, got[:] = list(got), []
+    assert len(compiled) == len(calls)
+    monkeypatch.setattr(lib, "_call", lambda *a: False)
+    monkeypatch.setattr(lib, "load", lambda *a, **k: Recorder())
+    for call in calls:
+        call()
+    assert got == compiled
+    # what is not plainly as documented goes the other way, and calls nothing
+    dev, entry = torch.cuda.current_device(), ctypes.cast(fake["rope_apply"], ctypes.c_void_p).value
+    got[:] = []
+
+    def go(fmt, *args, device=dev, name="rope_apply"):
+        return lib._marshal.call(entry, name, fmt, device, *args)
+
     for fmt, args in (("x", [q.cpu()]), ("x", [q.half()]), ("x", [q[0]]), ("x", [None]), ("x", [1.0]), ("x", []),
                       ("x", [q, q]), ("yR", [q, pos.long()]), ("yR", [q, pos[:, :3]]), ("yR", [q, pos.t()]),
                       ("xv", [q, lens[:2]]), ("xb", [q, s.bt[:2]]), ("xb", [q, s.bt.t()]), ("xl", [q, lse[:, :, ::2]]),
                       ("xY", [q, q.float()]), ("xX", [q, k]), ("yf", [q, s.fr.int()]), ("yf", [q, s.fr.repeat(4)]),
                       ("c", [s.kc, s.vc[:-1]]), ("c", [s.kc, s.vc.float()]), ("cA", [s.kc, s.vc, s.acc[:-1]]),
-                      ("bV", [s.bt[:2], lens]), ("c", [s.kc])):
-        assert lib._marshal.pack(fmt, dev, *args) is None, fmt
-    assert lib._marshal.pack("x", dev + 1, q) is None
-    with pytest.raises(ValueError):
-        lib._marshal.pack("?", dev, q)
+                      ("bV", [s.bt[:2], lens]), ("c", [s.kc]), ("=", ["1"]), ("=", [1 << 70]), ("x" * 9, [q] * 9),
+                      ("=" * 40, [0] * 40)):
+        assert go(fmt, *args) is None, fmt
+    assert go("x", q, device=dev + 1) is None
+    for bad in (lambda: go("?", q), lambda: go("x", q), lambda: go("x", q, name="attn_fwd")):
+        with pytest.raises(ValueError):
+            bad()
+    assert got == []
