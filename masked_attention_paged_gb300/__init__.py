@@ -232,12 +232,17 @@ def _call(name: str, fmt: str, *args) -> bool:
     entry = _entries.get(name)
     if entry is None:
         entry = _entries[name] = ctypes.cast(getattr(load(), name), ctypes.c_void_p).value
-    st = _marshal.call(entry, name, fmt, torch.cuda.current_device(), *args)
+    st = _marshal.call(entry, name, fmt, *args)
     if st is None:
         return False
     if st != 0:
         raise LibAttnError(name, st)
     return True
+
+
+def _handle(stream):
+    """A stream argument as a raw handle; None stays None."""
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
 def _stream(stream) -> int:
@@ -837,8 +842,8 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, in
     elif not (out.dtype == x.dtype and out.shape == x.shape):
         raise ValueError(f"out must be {x.dtype} {tuple(x.shape)}")
     if x.is_cuda:
-        if _call("rope_apply", "yRf===Y=", x, positions, freqs, int(bool(interleaved)), int(bool(inverse)),
-                 float(magnitude), out, _stream(stream)):
+        if _call("rope_apply", "yRf===YS", x, positions, freqs, int(bool(interleaved)), int(bool(inverse)),
+                 float(magnitude), out, _handle(stream)):
             return out
     full = out
     if x.dim() == 3:
@@ -897,8 +902,8 @@ def rope_kv_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, po
         q_out = _fresh(lambda: torch.empty_like(q), stream, q.device)
     if k_cache.is_cuda:
         ws = workspace or _small_ws(k_cache.device)
-        if _call("rope_kv_append", "yyyRf==Ycbv===", q, k_new, v_new, positions, freqs, int(bool(interleaved)),
-                 float(magnitude), q_out, k_cache, v_cache, block_table, start_pos, ws.ptr, ws.nbytes, _stream(stream)):
+        if _call("rope_kv_append", "yyyRf==YcbvWS", q, k_new, v_new, positions, freqs, int(bool(interleaved)),
+                 float(magnitude), q_out, k_cache, v_cache, block_table, start_pos, ws.tensor, _handle(stream)):
             return q_out
     return _rope_append("rope_kv_append", _cache_bytes(k_cache, v_cache), k_cache.device, q, k_new, v_new, positions,
                         freqs, block_table, start_pos, interleaved, magnitude, q_out, workspace, stream)
@@ -953,8 +958,8 @@ def paged_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if lse is None and return_lse:
         lse = _fresh(lambda: torch.empty((B, Hq, T), dtype=torch.float32, device=q.device), stream, q.device)
     if workspace is not None and q.is_cuda:
-        if _call("paged_tree_attn", "xoocbvq=Xl===", q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parents,
-                 float(scale), out, lse, workspace.ptr, workspace.nbytes, _stream(stream)):
+        if _call("paged_tree_attn", "xoocbvq=XlWS", q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parents,
+                 float(scale), out, lse, workspace.tensor, _handle(stream)):
             return (out, lse) if return_lse else out
     _check_block_table(block_table, B)
     _check_int32_vec(ctx_lens, B, "ctx_lens")
@@ -989,8 +994,8 @@ def kv_tree_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: to
     B = ctx_lens.shape[0]
     if k_cache.is_cuda:
         ws = workspace or _small_ws(k_cache.device)
-        if _call("kv_tree_accept", "cbVrv====", k_cache, v_cache, block_table, ctx_lens, path, n_accept, B, ws.ptr,
-                 ws.nbytes, _stream(stream)):
+        if _call("kv_tree_accept", "cbVrv=WS", k_cache, v_cache, block_table, ctx_lens, path, n_accept, B, ws.tensor,
+                 _handle(stream)):
             return
     _check_block_table(block_table, B)
     _check_int32_vec(ctx_lens, B, "ctx_lens")
@@ -1029,9 +1034,9 @@ def paged_attn_weights(q: torch.Tensor, lse: torch.Tensor, k_cache: torch.Tensor
     Hq] for one token a sequence.  q_lens int32 [B]: queries of each sequence."""
     lib = load()
     if workspace is not None and q.is_cuda:
-        if _call("paged_attn_weights", "ylcbvn==A===", q, lse, k_cache, k_cache, block_table, start_pos, q_lens,
-                 int(bool(causal)), float(1.0 / math.sqrt(q.shape[-1]) if scale is None else scale), acc, workspace.ptr,
-                 workspace.nbytes, _stream(stream)):
+        if _call("paged_attn_weights", "ylcbvn==AWS", q, lse, k_cache, k_cache, block_table, start_pos, q_lens,
+                 int(bool(causal)), float(1.0 / math.sqrt(q.shape[-1]) if scale is None else scale), acc, workspace.tensor,
+                 _handle(stream)):
             return acc
     if q.dim() == 3:
         q, lse = q.unsqueeze(2), lse.unsqueeze(2)
@@ -1077,8 +1082,8 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
                       k_cache.device)
     if k_cache.is_cuda and kept.shape == (B, Hkv, keep):
         ws = workspace or _small_ws(k_cache.device)
-        if _call("kv_evict", "cAbVb====vK===", k_cache, v_cache, acc, block_table, ctx_lens, dst_block_table, B, keep,
-                 int(sink), int(recent), new_lens, kept, ws.ptr, ws.nbytes, _stream(stream)):
+        if _call("kv_evict", "cAbVb====vKWS", k_cache, v_cache, acc, block_table, ctx_lens, dst_block_table, B, keep,
+                 int(sink), int(recent), new_lens, kept, ws.tensor, _handle(stream)):
             return new_lens, kept
     _check_block_table(block_table, B)
     _check_int32_vec(ctx_lens, B, "ctx_lens")

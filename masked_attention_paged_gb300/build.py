@@ -2,8 +2,8 @@
 
 Each .cu under csrc/ is compiled in parallel to an object file, then linked
 into ``_build/libattn_<machine>.so``.  No CMake, no torch extension machinery:
-the library is a plain C-ABI shared object.  marshal.cpp, which only reads the
-binding's arguments, is a Python module of its own beside it (g++, torch's
+the library is a plain C-ABI shared object.  marshal.cpp, which makes the
+binding's calls in one step, is a Python module of its own beside it (g++, torch's
 headers); the binding works without it, at a higher cost per call.
 """
 from __future__ import annotations
@@ -52,7 +52,7 @@ def _stale(obj: str, src: str) -> bool:
 
 
 def marshal_path() -> str:
-    """The argument packer's module, per machine and version of torch."""
+    """The binding's compiled module, per machine and version of torch."""
     import torch
     return os.path.join(BUILD, f"_marshal_{platform.machine()}_{torch.__version__.replace('+', '_')}.so")
 
@@ -65,7 +65,7 @@ def _marshal_command(out: str) -> list[str]:
            sysconfig.get_paths()["include"]]
     return ["g++", "-O1", "-std=c++17", "-fPIC", "-shared", *[x for p in inc for x in ("-I", p)],
             os.path.join(CSRC, "marshal.cpp"), "-o", out, "-L", os.path.join(root, "lib"), "-ltorch_python",
-            "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{os.path.join(root, 'lib')}"]
+            "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{os.path.join(root, 'lib')}"]
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
@@ -99,6 +99,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
                 run(cmd)
                 os.replace(tmp, marshal)
             except (RuntimeError, OSError) as e:
+                if os.path.exists(marshal):  # of other declarations
+                    os.remove(marshal)
                 print(f"marshal.cpp was not built, calls take longer on the host: {e}", file=sys.stderr)
 
         jobs.append(build_marshal)

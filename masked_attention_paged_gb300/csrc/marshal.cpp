@@ -3,8 +3,8 @@
 // A call of a few microseconds on the GPU is bound by the host: in Python, reading
 // the pointer, type, shape and strides of a dozen tensors, checking them and
 // converting them for the C entry takes longer than the launch.  call(address,
-// name, format, device, ...) does that for a whole call and returns the entry's
-// status, or None (and calls nothing) when anything is not plainly as the format
+// name, format, ...) does that for a whole call on the current device and returns
+// the entry's status, or None (and calls nothing) when anything is not plainly as the format
 // says; the Python code then goes through its own checks, which word the refusal
 // (or take the rarer form).  Nothing is kept between calls.
 //
@@ -25,8 +25,12 @@
 //   l  f32, contiguous, B H T elements, or None -> pointer or null
 //   A  f32 [blocks, Hkv, 16] of the cache -> pointer
 //   K  int32, contiguous [B, Hkv, n]     -> pointer
-//   =  an int, a float, or None          -> itself
+//   W  a workspace's bytes               -> pointer, their number
+//   S  a stream handle, or None          -> itself, or the current stream
+//   =  an int or a float                 -> itself
 #include <Python.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -103,22 +107,20 @@ bool int32_rows(const at::Tensor& t, int64_t device) {
 }
 
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  if (nargs < 4 || !PyLong_Check(args[0]) || !PyUnicode_Check(args[1]) || !PyUnicode_Check(args[2]) ||
-      !PyLong_Check(args[3])) {
-    PyErr_SetString(PyExc_TypeError, "call(address, name, format, device, ...)");
+  if (nargs < 3 || !PyLong_Check(args[0]) || !PyUnicode_Check(args[1]) || !PyUnicode_Check(args[2])) {
+    PyErr_SetString(PyExc_TypeError, "call(address, name, format, ...)");
     return nullptr;
   }
   const intptr_t entry = static_cast<intptr_t>(PyLong_AsLongLong(args[0]));
   const char* name = PyUnicode_AsUTF8(args[1]);
   const char* f = PyUnicode_AsUTF8(args[2]);
-  const int64_t device = PyLong_AsLongLong(args[3]);
   if (name == nullptr || f == nullptr || PyErr_Occurred()) return nullptr;
   constexpr int kMost = 32;
   Value out[kMost];
   attn_tensor tensors[8];
   attn_kv_cache cache;
   int n = 0, n_tensors = 0;
-  Py_ssize_t a = 4;
+  Py_ssize_t a = 3;
   Sizes s;
   bool ok = true, error = false;
   auto put = [&](int64_t i) {
@@ -129,18 +131,23 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   };
   auto address = [](const void* p) { return static_cast<int64_t>(reinterpret_cast<intptr_t>(p)); };
   try {
+    const int64_t device = c10::cuda::current_device();
     for (; ok && !error && *f != 0; ++f) {
       if (a >= nargs) {
         ok = false;
         break;
       }
       PyObject* o = args[a++];
-      if (o == Py_None && (*f == '=' || *f == 'o' || *f == 'n' || *f == 'l')) {
+      if (o == Py_None && *f == 'S') {
+        put(address(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream()));
+        continue;
+      }
+      if (o == Py_None && (*f == 'o' || *f == 'n' || *f == 'l')) {
         put(0);
         continue;
       }
-      if (*f == '=') {
-        if (PyFloat_Check(o) && n < kMost) {
+      if (*f == '=' || *f == 'S') {
+        if (*f == '=' && PyFloat_Check(o) && n < kMost) {
           out[n++].d = PyFloat_AS_DOUBLE(o);
         } else if (PyLong_Check(o)) {
           int past = 0;
@@ -267,6 +274,12 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
           if (!ok) break;
           put(address(t.data_ptr()));
           break;
+        case 'W':
+          ok = on(t, device) && t.scalar_type() == at::kByte && t.dim() == 1 && t.is_contiguous();
+          if (!ok) break;
+          put(address(t.data_ptr()));
+          put(t.numel());
+          break;
         case 'K':
           ok = on(t, device) && t.scalar_type() == at::kInt && t.is_contiguous() && t.dim() == 3 && t.size(0) == s.B &&
                t.size(1) == s.kv_heads;
@@ -305,7 +318,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 
 PyMethodDef kMethods[] = {
     {"call", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(call)), METH_FASTCALL,
-     "call(address, name, format, device, ...): a C entry point's status, or None"},
+     "call(address, name, format, ...): a C entry point's status, or None"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", "A call of the binding in one step.", -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

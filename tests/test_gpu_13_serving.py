@@ -301,11 +301,11 @@ def test_a_compiled_call_passes_what_the_worded_checks_pass(monkeypatch):
         call()
     assert got == compiled
     # what is not plainly as documented goes the other way, and calls nothing
-    dev, entry = torch.cuda.current_device(), ctypes.cast(fake["rope_apply"], ctypes.c_void_p).value
+    entry = ctypes.cast(fake["rope_apply"], ctypes.c_void_p).value
     got[:] = []
 
-    def go(fmt, *args, device=dev, name="rope_apply"):
-        return lib._marshal.call(entry, name, fmt, device, *args)
+    def go(fmt, *args, name="rope_apply"):
+        return lib._marshal.call(entry, name, fmt, *args)
 
     for fmt, args in (("x", [q.cpu()]), ("x", [q.half()]), ("x", [q[0]]), ("x", [None]), ("x", [1.0]), ("x", []),
                       ("x", [q, q]), ("yR", [q, pos.long()]), ("yR", [q, pos[:, :3]]), ("yR", [q, pos.t()]),
@@ -313,9 +313,8 @@ def test_a_compiled_call_passes_what_the_worded_checks_pass(monkeypatch):
                       ("xY", [q, q.float()]), ("xX", [q, k]), ("yf", [q, s.fr.int()]), ("yf", [q, s.fr.repeat(4)]),
                       ("c", [s.kc, s.vc[:-1]]), ("c", [s.kc, s.vc.float()]), ("cA", [s.kc, s.vc, s.acc[:-1]]),
                       ("bV", [s.bt[:2], lens]), ("c", [s.kc]), ("=", ["1"]), ("=", [1 << 70]), ("x" * 9, [q] * 9),
-                      ("=" * 40, [0] * 40)):
+                      ("=" * 40, [0] * 40), ("=", [None]), ("W", [lens]), ("W", [ws.tensor[::2]]), ("S", [1.5])):
         assert go(fmt, *args) is None, fmt
-    assert go("x", q, device=dev + 1) is None
     for bad in (lambda: go("?", q), lambda: go("x", q), lambda: go("x", q, name="attn_fwd")):
         with pytest.raises(ValueError):
             bad()
