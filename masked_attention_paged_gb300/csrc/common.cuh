@@ -249,6 +249,35 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// A launch that may take its place on the SMs before the launch ahead of it in the
+// stream ends: when that one's CTAs have all let it in or left.  Its kernel touches
+// global memory only after wait_for_launch_ahead(), which returns once that launch
+// is complete, and with it everything before it in the stream.  Kernels let the
+// next launch in where it is their own second half (tree and merge, selection and
+// copy) or follows in the same step (merge, acceptance, weights); beside other work
+// its waiting CTAs cost more than they save (a rotation of 25 MB 10.4 us instead of
+// 8.5, the eviction of 2 x 65521 tokens 31.7 instead of 29.4).
+__device__ __forceinline__ void let_next_launch_in() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_launch_ahead() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                         A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...);
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;

@@ -35,7 +35,8 @@ struct AcceptParams {
 // V at D = 128: one pass for the usual path).
 constexpr int kAcceptThreads = 256, kAcceptVecs = 8;
 __global__ void __launch_bounds__(kAcceptThreads) kv_tree_accept_kernel(const AcceptParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // in place before the launch before it ends
+  let_next_launch_in();
+  wait_for_launch_ahead();
   const int g = blockIdx.x, b = blockIdx.y;
   const int32_t* path = p.path + b * p.path_stride;
   const int ctx = p.ctx_lens[b], n = p.n_accept[b];
@@ -155,7 +156,8 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const Evic
   // the cluster barrier after which its peers add to it
   __shared__ __align__(16) int total[2][256];
   __shared__ int warp_cnt[2][kSelWarps], cta_cnt[kMaxCluster][2];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_launch_in();
+  wait_for_launch_ahead();
   const int g = blockIdx.y, b = blockIdx.z;
   const int rank = static_cast<int>(cluster_rank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -336,7 +338,7 @@ constexpr int kCopyThreads = 256, kCopyVecs = 8, kCopyRows = 128;
 template <int CH>  // 16-byte chunks per row
 __global__ void __launch_bounds__(kCopyThreads) kv_evict_copy_kernel(const EvictParams p) {
   __shared__ int64_t from[kCopyRows], to[kCopyRows];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_launch_ahead();
   const int g = blockIdx.y, b = blockIdx.z;
   const int r0 = blockIdx.x * kCopyRows;
   const int32_t* kept = p.kept + (static_cast<int64_t>(b) * p.Hkv + g) * p.keep + r0;
@@ -422,22 +424,21 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t stream) {
   cfg.gridDim = dim3(static_cast<unsigned>(nc), static_cast<unsigned>(a.cache.Hkv), static_cast<unsigned>(a.B));
   cfg.blockDim = dim3(kSelThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(nc);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kv_evict_select_kernel, p, nc);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>((a.keep + kCopyRows - 1) / kCopyRows),
-                     static_cast<unsigned>(a.cache.Hkv), static_cast<unsigned>(a.B));
-  cfg.blockDim = dim3(kCopyThreads);
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  return p.ch == 16 ? cudaLaunchKernelEx(&cfg, kv_evict_copy_kernel<16>, p)
-                    : cudaLaunchKernelEx(&cfg, kv_evict_copy_kernel<8>, p);
+  const dim3 grid(static_cast<unsigned>((a.keep + kCopyRows - 1) / kCopyRows),
+                  static_cast<unsigned>(a.cache.Hkv), static_cast<unsigned>(a.B));
+  const auto copy = p.ch == 16 ? kv_evict_copy_kernel<16> : kv_evict_copy_kernel<8>;
+  return launch_early(copy, grid, kCopyThreads, 0, stream, p);
 }
 
 cudaError_t launch_tree_accept(const AcceptArgs& a, cudaStream_t stream) {
@@ -456,16 +457,8 @@ cudaError_t launch_tree_accept(const AcceptArgs& a, cudaStream_t stream) {
   p.max_path = a.max_path;
   p.n_accept = a.n_accept;
   p.status = a.status;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.cache.Hkv), static_cast<unsigned>(a.B));
-  cfg.blockDim = dim3(kAcceptThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_tree_accept_kernel, p);
+  const dim3 grid(static_cast<unsigned>(a.cache.Hkv), static_cast<unsigned>(a.B));
+  return launch_early(kv_tree_accept_kernel, grid, kAcceptThreads, 0, stream, p);
 }
 
 }  // namespace attn

@@ -199,6 +199,7 @@ template <bool BF16, bool INTER, bool VEC, bool Q8>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   extern __shared__ float2 cs[];  // [tokens][n]
   __shared__ int64_t row_base[kMaxTokens];  // cache row of (token, KV head 0), -1: not cached
+  wait_for_launch_ahead();
   const int64_t first = static_cast<int64_t>(blockIdx.x) * p.tokens;
   const int ntok = static_cast<int>(min(static_cast<int64_t>(p.tokens), static_cast<int64_t>(p.B) * p.T - first));
   const int h0 = blockIdx.y * p.heads;
@@ -347,8 +348,7 @@ Rows rows(const View4& t) { return {t.data, t.stride[0], t.stride[1], t.stride[2
 template <bool BF16, bool INTER, bool VEC, bool Q8>
 cudaError_t launch(const RopeParams& p, dim3 grid, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(p.tokens) * p.n * sizeof(float2);
-  rope_kernel<BF16, INTER, VEC, Q8><<<grid, kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(rope_kernel<BF16, INTER, VEC, Q8>, grid, kThreads, smem, stream, p);
 }
 
 template <bool BF16, bool Q8>

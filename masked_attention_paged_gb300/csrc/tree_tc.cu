@@ -238,8 +238,8 @@ template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
   constexpr int CW = D / 16;
   __shared__ float tile[32][D + 1];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_launch_in();
+  wait_for_launch_ahead();
   const int c0 = blockIdx.x;
   const CutItem it = p.cuts[c0];
   if (it.pieces == 0) return;
@@ -344,7 +344,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     bars->abort = 0;
     fence_mbar_init();
   }
-  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_launch_in();
+  if (warp == 4) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  // query rows past a row tile's box: zeros, once
+#pragma unroll 1
+  for (int x = threadIdx.x; x < NT * C::kBoxes * (kBM - p.RT) * 8; x += C::kThreads) {
+    const int box = x / ((kBM - p.RT) * 8), y = x % ((kBM - p.RT) * 8);
+    *reinterpret_cast<uint4*>(smem + C::kOffQ + box * kBoxBytes + p.RT * 128 + y * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  wait_for_launch_ahead();
   // the planner's state: the call's runs, and the place of this CTA's first tile
   Runs runs = {};
   int pos = 0, hi = 0, lo = 0, share = 0;
@@ -402,17 +414,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       tma_prefetch_desc(&tm_v);
     }
   }
-  if (warp == 4) {
-    tmem_alloc(&bars->tmem_base, 512);
-    tmem_relinquish();
-  }
-  // query rows past a row tile's box: zeros, once
-#pragma unroll 1
-  for (int x = threadIdx.x; x < NT * C::kBoxes * (kBM - p.RT) * 8; x += C::kThreads) {
-    const int box = x / ((kBM - p.RT) * 8), y = x % ((kBM - p.RT) * 8);
-    *reinterpret_cast<uint4*>(smem + C::kOffQ + box * kBoxBytes + p.RT * 128 + y * 16) = make_uint4(0u, 0u, 0u, 0u);
-  }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1250,21 +1251,12 @@ cudaError_t launch(const TreeArgs& a, TreeParams& p, cudaStream_t stream) {
   }
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(a.n_cta), C::kThreads, C::kSmemBytes, stream>>>(mq, mk, mv, mkn, mvn, p);
-  e = cudaGetLastError();
+  const dim3 ctas(static_cast<unsigned>(a.n_cta));
+  e = launch_early(kern, ctas, C::kThreads, C::kSmemBytes, stream, mq, mk, mv, mkn, mvn, p);
   if (e != cudaSuccess) return e;
-  // in place on the SMs as the main launch's CTAs leave
-  cudaLaunchConfig_t cfg = {};
   // groups of 32 rows up to the last that any row tile uses
-  cfg.gridDim = dim3(static_cast<unsigned>(a.n_cta), static_cast<unsigned>(((NT - 1) * kBM + p.RT + 31) / 32));
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, p);
+  const dim3 grid(static_cast<unsigned>(a.n_cta), static_cast<unsigned>(((NT - 1) * kBM + p.RT + 31) / 32));
+  return launch_early(tree_merge_kernel<D>, grid, kMergeThreads, 0, stream, p);
 }
 
 }  // namespace

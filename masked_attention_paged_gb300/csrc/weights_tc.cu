@@ -183,6 +183,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     bars->abort = 0;
     fence_mbar_init();
   }
+  if (warp == 4) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  wait_for_launch_ahead();
   // the planner's state: the call's runs, and the place of this CTA's first step
   Runs64 runs = {};
   int64_t pos = 0, lo = 0, hi = 0, item0 = 0;
@@ -241,10 +246,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       plan_c = work.first(plan_pair) + static_cast<int>(rem) - kItemCost;
       item0 = lo - rem;
     }
-  }
-  if (warp == 4) {
-    tmem_alloc(&bars->tmem_base, 512);
-    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
@@ -633,8 +634,7 @@ cudaError_t launch(const WeightArgs& a, const WeightParams& p, cudaStream_t stre
   auto kern = attn_weights_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(a.n_cta), kThreads, Cfg<D>::kSmemBytes, stream>>>(mk, mq, p);
-  return cudaGetLastError();
+  return launch_early(kern, dim3(static_cast<unsigned>(a.n_cta)), kThreads, Cfg<D>::kSmemBytes, stream, mk, mq, p);
 }
 
 size_t part_bytes(int n_cta) { return static_cast<size_t>(2) * n_cta * kPair * sizeof(float); }
