@@ -18,7 +18,7 @@
 // of a token), then move rows, 16 elements (two 16-byte vectors of bf16) a
 // thread and step.  16 sequences x 1024 tokens (32 query and 8 KV heads, D =
 // 128): 68 us for 403 MB, 5.9 TB/s, 87 % of the measured copy rate; one token of
-// one sequence 3.2 us and of 64 sequences 3.4 us, a launch and its loads.
+// one sequence 3.0 us and of 64 sequences 3.4 us, a launch and its loads.
 #include <math.h>
 
 #include <algorithm>
