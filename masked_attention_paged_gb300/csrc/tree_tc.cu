@@ -997,8 +997,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           } else {
             // Bound by this chain's latency: scores go to registers, the first 32 ahead of
             // the others, and are weighed against the reference max at hand, without a
-            // max pass; if some row's sum says its scores outgrew it (2^64; or NaN), once
-            // more with one.
+            // max pass; if some row's sum says its scores outgrew it (128 weights of 2^8,
+            // the margin of a max pass, so that P V keeps the same room; or NaN), once more
+            // with one.
             uint32_t sr[4][32];
             tmem_ld32(tmem + lane_addr + s_col, sr[0]);
             const bool fast = !masked && __all_sync(0xffffffffu, m_run != -INFINITY);
@@ -1014,7 +1015,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
               for (int c = 1; c < 4; ++c) weigh32(sr[c], c, p.scale_log2, -m_run, sum);
               float a0, a1;
               f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
-              done = __all_sync(0xffffffffu, a0 + a1 <= 18446744073709551616.0f);
+              done = __all_sync(0xffffffffu, a0 + a1 <= kBN * 256.0f);  // 2^kRescaleMargin
               if (!done) {
                 tmem_wait_st();
 #pragma unroll

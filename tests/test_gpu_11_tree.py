@@ -173,6 +173,25 @@ def test_f32_output_scales_and_peaked_scores():
     _check(_make([700, 400], 40, 8, 2, 64, seed=8, gain=8.0))
 
 
+@pytest.mark.parametrize("T,Hq", [(20, 4), (70, 4)])
+def test_scores_that_keep_rising_over_large_values(T, Hq):
+    """Each 128 keys outscore the ones before by up to e^20, and the values are 1e32: no weight may be large enough to
+    take a product past float32."""
+    s = _make([900, 400], T, Hq, 1, 128, seed=21)
+    g = _gen(22)
+    for b, n in enumerate((900, 400)):
+        at = torch.arange(n, device=DEV)
+        blk = s["bt"][b, at // 16].long()
+        up = 0.5 * (at // 128).to(torch.bfloat16) + torch.randn(n, generator=g).to(DEV).bfloat16() * 0.1
+        s["kc"][blk, 0, at % 16, 0] = up
+        s["vc"][blk, 0, at % 16] = (torch.randn(n, 128, generator=g) * 1e32).bfloat16().to(DEV)
+    s["q"][..., 0] = 40.0  # a step of 0.5 in the first dim is 20 in the score, at scale 1
+    s["v_new"] = s["v_new"] * 1e32
+    s["q"][..., 1:] *= 0.05
+    o, _ = _check(s, scale=1.0)
+    assert bool(torch.isfinite(o).all())
+
+
 def test_a_chain_is_a_causal_chunk():
     """Parents -1, 0, 1, ...: the same cache and, within both calls' rounding, the same rows as paged_prefill_attn."""
     s = _make([77, 512], 50, 8, 2, 128, seed=9, cut=False)
