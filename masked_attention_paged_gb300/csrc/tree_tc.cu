@@ -974,9 +974,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             // TMEM, 32 at a time.  (Code that runs once costs its fetch: unrolled
             // over the 128 scores, a first tile took 2.3 us and this warp's code
             // displaced the producers'.)  The second pass writes P over scores that
-            // it has read: chunk c's 16 columns end before chunk c + 1's begin.
+            // it has read: chunk c's 16 columns end before chunk c + 1's begin.  Chunks
+            // past the tile's keys have no scores, and no P that the MMAs read.
+            const int nc = masked ? (tile_keys(p, tile, s.nct, s.ctx) + 31) / 32 : 4;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < nc; ++c) {
               uint32_t x[32];
               tmem_ld32(tmem + lane_addr + s_col + c * 32, x);
               tmem_wait_ld(x);
@@ -987,7 +989,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             raise(fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * mul);
             const float neg = m_run == -INFINITY ? 0.0f : -m_run;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < nc; ++c) {
               uint32_t x[32];
               tmem_ld32(tmem + lane_addr + s_col + c * 32, x);
               tmem_wait_ld(x);
