@@ -1142,10 +1142,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll 1
         for (int c = NT == 1 ? wg * (D / 2) : 0; c < (NT == 1 ? (wg + 1) * (D / 2) : D); c += 16) {
           uint32_t o[16];
-          tmem_ld16_now(tmem + lane_addr + (NT == 1 ? C::kColO : o_col) + c, o);
-          if constexpr (NT == 1) {
+          if constexpr (NT == 2) {
+            tmem_ld16_now(tmem + lane_addr + o_col + c, o);
+          } else {
             uint32_t o1[16];
-            tmem_ld16_now(tmem + lane_addr + C::kColO + D + c, o1);
+            tmem_ld16x2_now(tmem + lane_addr + C::kColO + c, o, tmem + lane_addr + C::kColO + D + c, o1);
             // an accumulator of weight 0 may hold anything
 #pragma unroll
             for (int i = 0; i < 16; ++i)
