@@ -98,8 +98,10 @@ __global__ void __launch_bounds__(kAcceptThreads) kv_tree_accept_kernel(const Ac
 // the count from above reaches `keep`.  Ties at the threshold go to the lowest
 // slots.  Keys lie in shared memory and the loops over them stay rolled (a range
 // longer than kKeys is read again from L2 in each pass): the cost is latency,
-// of four passes and of fetching the code once, not the bytes.  2 x 8 contexts of
-// 65521 tokens: 22 us (45 us with sixteen rounds of counting two bits at a time).
+// of the passes and of fetching the code once, not the bytes.  It ends with the
+// pass after which every key of the digit stays: the third, for distinct sums.  2 x 8
+// contexts of 65521 tokens: 20 us (22 with all four passes, 45 with sixteen rounds of
+// counting two bits at a time).
 // ---------------------------------------------------------------------------
 struct EvictParams {
   const uint4* kc;
@@ -284,8 +286,19 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const Evic
 #pragma unroll
     for (int d = 7; d > 0; --d)
       if (digit == d && past + n[d] < need) past += n[d], digit = d - 1;
+    int count = n[7];  // keys of that digit
+#pragma unroll
+    for (int d = 0; d < 7; ++d)
+      if (digit == d) count = n[d];
     thr |= static_cast<uint32_t>(8 * at + __shfl_sync(0xffffffffu, digit, at)) << shift;
     above += __shfl_sync(0xffffffffu, past, at);
+    if (__shfl_sync(0xffffffffu, count, at) == p.keep - above) {
+      // All of them stay (with distinct sums, after three passes mostly): the greater
+      // keys are those from thr on.  thr > 0: as many as `keep` keys reach it, of more.
+      thr -= 1u;
+      above = p.keep;
+      break;  // the cluster's warps all alike
+    }
   }
   // `above` keys are greater than thr; the first keep - above of those equal to it stay too
   const int need = p.keep - above;
