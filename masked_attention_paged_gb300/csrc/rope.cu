@@ -17,8 +17,8 @@
 // sines and cosines into shared memory (one sincospif each: shared by all heads
 // of a token), then move rows, 16 elements (two 16-byte vectors of bf16) a
 // thread and step.  16 sequences x 1024 tokens (32 query and 8 KV heads, D =
-// 128): 68 us for 403 MB, 5.9 TB/s, 87 % of the measured copy rate; one token of
-// one sequence 3.0 us and of 64 sequences 3.4 us, a launch and its loads.
+// 128): 66 us for 403 MB, 6.1 TB/s, 90 % of the measured copy rate; one token of
+// one sequence 3.2 us and of 64 sequences 3.0 us, a launch and its loads.
 #include <math.h>
 
 #include <algorithm>
@@ -95,16 +95,18 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float x) {
     static_cast<float*>(p)[i] = x;
 }
 
+// 8 elements from 16-byte words
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float* x) {
+__device__ __forceinline__ void unpack8(const uint4* w, float* x) {
   if constexpr (BF16) {
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    x[0] = bf16lo_to_f32(w.x), x[1] = bf16hi_to_f32(w.x), x[2] = bf16lo_to_f32(w.y), x[3] = bf16hi_to_f32(w.y);
-    x[4] = bf16lo_to_f32(w.z), x[5] = bf16hi_to_f32(w.z), x[6] = bf16lo_to_f32(w.w), x[7] = bf16hi_to_f32(w.w);
+    x[0] = bf16lo_to_f32(w->x), x[1] = bf16hi_to_f32(w->x), x[2] = bf16lo_to_f32(w->y), x[3] = bf16hi_to_f32(w->y);
+    x[4] = bf16lo_to_f32(w->z), x[5] = bf16hi_to_f32(w->z), x[6] = bf16lo_to_f32(w->w), x[7] = bf16hi_to_f32(w->w);
   } else {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = f[0], b = f[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[4 * i] = __uint_as_float(w[i].x), x[4 * i + 1] = __uint_as_float(w[i].y);
+      x[4 * i + 2] = __uint_as_float(w[i].z), x[4 * i + 3] = __uint_as_float(w[i].w);
+    }
   }
 }
 
@@ -194,9 +196,13 @@ __device__ __forceinline__ void store_q8(float (&x)[16], int8_t* dst, float* sca
 
 // grid (token groups, head ranges).  VEC: 16-byte rows and whole slots; else
 // element by element (odd strides, or a half layout whose n is no multiple
-// of 8).
-template <bool BF16, bool INTER, bool VEC, bool Q8>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+// of 8).  ONE (and VEC): a thread has one row, whose loads need not wait for the
+// sines: 25 MB in 7.5 instead of 8.6 us; with more rows a thread the registers cost
+// more than that saves (16 x 1024 tokens 73.4 instead of 67.6 us).  There bf16 rows
+// take 32 registers, so that an SM holds 8 CTAs (65.8 us; with 34, 68.7).
+template <bool BF16, bool INTER, bool VEC, bool Q8, bool ONE>
+__global__ void __launch_bounds__(kThreads, BF16 && VEC && !ONE && !Q8 ? 8 : 4)
+    rope_kernel(const RopeParams p) {
   extern __shared__ float2 cs[];  // [tokens][n]
   __shared__ int64_t row_base[kMaxTokens];  // cache row of (token, KV head 0), -1: not cached
   wait_for_launch_ahead();
@@ -204,6 +210,34 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   const int ntok = static_cast<int>(min(static_cast<int64_t>(p.tokens), static_cast<int64_t>(p.B) * p.T - first));
   const int h0 = blockIdx.y * p.heads;
   const int nh = min(p.heads, p.Hq + 2 * p.Hkv - h0);
+
+  const int S = p.slots;
+  const int s = threadIdx.x % S;   // this thread's slot of every row it moves
+  const int step = kThreads / S;   // rows per pass; an S that does not divide the CTA leaves threads over
+  const SlotAt at = slot_at<INTER>(s, p.n);
+  const bool spare = threadIdx.x >= step * S;  // never with Q8: S is 4 or 8 there
+  const int rows_all = ntok * nh;
+  int tok = 0, h = threadIdx.x / S;  // this thread's row; VEC: its 16 elements in w
+  auto settle = [&] {
+    while (h >= nh && tok < ntok) h -= nh, ++tok;
+    return tok < ntok && !spare;
+  };
+  constexpr int EB = BF16 ? 2 : 4, kWords = EB;
+  uint4 w[kWords] = {};
+  auto fetch = [&] {
+    const int64_t token = first + tok;
+    const int b = static_cast<int>(token / p.T), t = static_cast<int>(token % p.T);
+    const int head = h0 + h, kv = head - p.Hq;
+    const Rows& src = kv < 0 ? p.in : (kv < p.Hkv ? p.k : p.v);
+    const uint8_t* row = static_cast<const uint8_t*>(src.data) +
+                         src.at(b, kv < 0 ? head : (kv < p.Hkv ? kv : kv - p.Hkv), t) * EB;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      w[i] = *reinterpret_cast<const uint4*>(row + (i < kWords / 2 ? at.e0 : at.e1) * EB + i % (kWords / 2) * 16);
+  };
+  if constexpr (ONE) {  // it sets out before the sines
+    if (settle()) fetch();
+  }
 
   for (int i = threadIdx.x; i < ntok * p.n; i += kThreads) {
     const int64_t tok = first + i / p.n;
@@ -231,16 +265,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   }
   __syncthreads();
 
-  const int S = p.slots;
-  const int s = threadIdx.x % S;   // this thread's slot of every row it moves
-  const int step = kThreads / S;   // rows per pass; an S that does not divide the CTA leaves threads over
-  const SlotAt at = slot_at<INTER>(s, p.n);
-  const bool spare = threadIdx.x >= step * S;  // never with Q8: S is 4 or 8 there
-  int tok = 0, h = threadIdx.x / S;
-  const int rows_all = ntok * nh;
   for (int r = 0; r < rows_all; r += step, h += step) {  // the same trips for every thread: Q8 shuffles
-    while (h >= nh && tok < ntok) h -= nh, ++tok;
-    const bool there = tok < ntok && !spare;
+    const bool there = settle();
+    if constexpr (VEC) {
+      if (!ONE && there) fetch();
+    }
     if (!Q8 && !there) continue;
     const int tk = there ? tok : 0, head = h0 + (there ? h : 0);
     const int64_t token = first + tk;
@@ -270,34 +299,28 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
     const int64_t o = src->at(b, hh, t);
     const float2* tcs = cs + tk * p.n;
     if constexpr (VEC) {
-      constexpr int EB = BF16 ? 2 : 4;
       if (Q8 && cached) {
         // Not reached by every row of a warp at once: the S lanes of a row do
         // so together, and the shuffles below stay within them.
         float x[16];
-        load8<BF16>(from, o + at.e0, x);
-        load8<BF16>(from, o + at.e1, x + 8);
+        unpack8<BF16>(w, x);
+        unpack8<BF16>(w + kWords / 2, x + 8);
         if (rot) rotate16<INTER>(x, at, tcs, p.n);
         store_q8(x, write ? static_cast<int8_t*>(to) + dst : nullptr, scale, at, S, s == 0);
       } else if (write) {
         const bool turned = rot && (INTER ? at.e0 < 2 * p.n : at.half_pairs);
         if (turned) {
           float x[16];
-          load8<BF16>(from, o + at.e0, x);
-          load8<BF16>(from, o + at.e1, x + 8);
+          unpack8<BF16>(w, x);
+          unpack8<BF16>(w + kWords / 2, x + 8);
           rotate16<INTER>(x, at, tcs, p.n);
           store8<BF16>(to, dst + at.e0, x);
           store8<BF16>(to, dst + at.e1, x + 8);
         } else {  // values and dims past rotary_dim: a bit copy
-          const uint8_t* f = static_cast<const uint8_t*>(from);
           uint8_t* g = static_cast<uint8_t*>(to);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int e = half ? at.e1 : at.e0;
-#pragma unroll
-            for (int x = 0; x < 8 * EB; x += 16)
-              *reinterpret_cast<uint4*>(g + (dst + e) * EB + x) = *reinterpret_cast<const uint4*>(f + (o + e) * EB + x);
-          }
+          for (int i = 0; i < kWords; ++i)
+            *reinterpret_cast<uint4*>(g + (dst + (i < kWords / 2 ? at.e0 : at.e1)) * EB + i % (kWords / 2) * 16) = w[i];
         }
       }
     } else if (write) {
@@ -345,21 +368,21 @@ bool rows_vec16(const View4& t) {
 
 Rows rows(const View4& t) { return {t.data, t.stride[0], t.stride[1], t.stride[2]}; }
 
-template <bool BF16, bool INTER, bool VEC, bool Q8>
+template <bool BF16, bool INTER, bool VEC, bool Q8, bool ONE>
 cudaError_t launch(const RopeParams& p, dim3 grid, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(p.tokens) * p.n * sizeof(float2);
-  return launch_early(rope_kernel<BF16, INTER, VEC, Q8>, grid, kThreads, smem, stream, p);
+  return launch_early(rope_kernel<BF16, INTER, VEC, Q8, ONE>, grid, kThreads, smem, stream, p);
 }
 
-template <bool BF16, bool Q8>
-cudaError_t pick(const RopeParams& p, bool inter, bool vec, dim3 grid, cudaStream_t stream) {
+template <bool BF16, bool INTER, bool Q8>
+cudaError_t pick(const RopeParams& p, bool vec, dim3 grid, cudaStream_t stream) {
   if (vec)
-    return inter ? launch<BF16, true, true, Q8>(p, grid, stream) : launch<BF16, false, true, Q8>(p, grid, stream);
+    return p.tokens * p.heads <= kThreads / p.slots ? launch<BF16, INTER, true, Q8, true>(p, grid, stream)
+                                                    : launch<BF16, INTER, true, Q8, false>(p, grid, stream);
   if constexpr (Q8)
     return cudaErrorNotSupported;
   else
-    return inter ? launch<BF16, true, false, false>(p, grid, stream)
-                 : launch<BF16, false, false, false>(p, grid, stream);
+    return launch<BF16, INTER, false, false, false>(p, grid, stream);
 }
 
 }  // namespace
@@ -418,9 +441,13 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
   const int64_t gx = (tokens + p.tokens - 1) / p.tokens;
   if (gx > 0x7fffffff) return cudaErrorInvalidValue;
   dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>((all_heads + p.heads - 1) / p.heads));
-  if (append && a.cache.k_scale != nullptr) return pick<true, true>(p, a.interleaved, vec, grid, stream);
-  if (a.x.dtype == ATTN_BF16) return pick<true, false>(p, a.interleaved, vec, grid, stream);
-  return pick<false, false>(p, a.interleaved, vec, grid, stream);
+  if (append && a.cache.k_scale != nullptr)
+    return a.interleaved ? pick<true, true, true>(p, vec, grid, stream) : pick<true, false, true>(p, vec, grid, stream);
+  if (a.x.dtype == ATTN_BF16)
+    return a.interleaved ? pick<true, true, false>(p, vec, grid, stream)
+                         : pick<true, false, false>(p, vec, grid, stream);
+  return a.interleaved ? pick<false, true, false>(p, vec, grid, stream)
+                       : pick<false, false, false>(p, vec, grid, stream);
 }
 
 }  // namespace attn

@@ -12,14 +12,14 @@
 // else 2).  What bounds it is HBM (a 128-key tile of K and V at D = 128 is 64 KB,
 // 1.4 us of an SM's share), until rows pass 256 a KV head and the tensor cores and
 // exponentials do.  Measured (merge and path acceptance included; Hkv = 8, D = 128):
-//   64 sequences x 25 drafts, G = 4, up to 8192 tokens   268 us, 1.66 GB, 91 % of
+//   64 sequences x 25 drafts, G = 4, up to 8192 tokens   269 us, 1.66 GB, 91 % of
 //                                                        the measured copy rate
-//   16 x 27, G = 4, up to 4096 tokens                    57 us (28 us of bytes): 17
+//   16 x 27, G = 4, up to 4096 tokens                    56 us (28 us of bytes): 17
 //        tiles a CTA; the rest is each segment's start and end and the merge
 //   1 x 64, G = 8, 131063 tokens                         225 us (144 us of MMAs):
 //        the chain of a row tile: scores arrive, 2300 cycles of softmax, 1650 for
 //        the products of both row tiles
-//   1 x 8, G = 2, D = 64, 700 tokens                     19 us, three launches'
+//   1 x 8, G = 2, D = 64, 700 tokens                     18 us, three launches'
 //        latency: a tile passes through in 8 us, the drafts' in 11
 //
 // Every SM takes an equal run of the call's K/V tiles: an item (sequence, KV
