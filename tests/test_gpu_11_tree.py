@@ -192,6 +192,23 @@ def test_scores_that_keep_rising_over_large_values(T, Hq):
     assert bool(torch.isfinite(o).all())
 
 
+@pytest.mark.parametrize("T", [128, 256])
+def test_deep_chains_whole_and_cut(T):
+    """Ancestors a hundred levels up; chains that break off at an absent draft, or at one that names itself, which take
+    everything below with them; two chains interleaved."""
+    s = _make([40, 7, 0, 300, 18], T, 1, 1, 64, seed=23)
+    chain = list(range(-1, T - 1))
+    par = [list(chain) for _ in range(5)]
+    par[1][100] = -2
+    par[2][60] = 60
+    par[3] = [-1, -1, *range(T - 2)]
+    par[4][T - 1], par[4][T // 2] = T - 3, -1
+    s["parents"] = torch.tensor(par, dtype=torch.int32, device=DEV)
+    _check(s, status=5)
+    s["parents"][2, 60] = -1
+    _check(s)
+
+
 def test_a_chain_is_a_causal_chunk():
     """Parents -1, 0, 1, ...: the same cache and, within both calls' rounding, the same rows as paged_prefill_attn."""
     s = _make([77, 512], 50, 8, 2, 128, seed=9, cut=False)
