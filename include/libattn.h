@@ -652,9 +652,10 @@ attn_status paged_attn_weights(const attn_tensor *q, const float *lse, const att
  *   ctx_lens   int32 [batch]; < 0 marks an idle sequence; more than the table
  *              holds sets ATTN_ERR_DEVICE_BOUNDS and is cut to it
  *   keep       >= 1; sink, recent >= 0, sink + recent <= keep
- *   new_lens   int32 [batch], written: min(L, keep) (idle: ctx_lens[b])
+ *   new_lens   int32 [batch], written: min(L, keep) (idle: ctx_lens[b]).  It may be
+ *              ctx_lens itself; else the two must not overlap.
  *   kept       int32 [batch, num_kv_heads, keep], written: the source slots in
- *              order, -1 past them
+ *              order, -1 past them; overlaps neither of the lengths
  *   workspace  >= kv_append_workspace_size() bytes (the status word)
  */
 attn_status kv_evict(const attn_kv_cache *cache, float *acc, const int32_t *block_table, int64_t bt_stride,

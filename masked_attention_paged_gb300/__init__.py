@@ -1071,7 +1071,8 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
     """Keep `keep` tokens of each sequence and KV head (the first `sink`, the
     last `recent`, and the largest acc of the others) and copy their K, V and
     acc, in order, to the blocks of dst_block_table.  Returns (new_lens int32
-    [B], kept int32 [B, Hkv, keep]: the source slots, -1 past them)."""
+    [B], kept int32 [B, Hkv, keep]: the source slots, -1 past them); new_lens may
+    be ctx_lens, which is then updated in place."""
     lib = load()
     B, Hkv = ctx_lens.shape[0], k_cache.shape[1]
     keep = int(keep)

@@ -54,6 +54,12 @@ bool tma_rows_ok(const attn_tensor* t) {
   return vec16_ok(t);
 }
 
+// Whether [a, a + a_bytes) and [b, b + b_bytes) share a byte.
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(b_bytes) && y < x + static_cast<uintptr_t>(a_bytes);
+}
+
 View4 view(const attn_tensor* t) {
   View4 v;
   v.data = t->data;
@@ -851,6 +857,11 @@ attn_status kv_evict(const attn_kv_cache* cache, float* acc, const int32_t* bloc
     return ATTN_ERR_INVALID_ARG;
   if (!aligned(acc, 4)) return ATTN_ERR_INVALID_ARG;
   if (batch > 1 && (bt_stride < max_blocks || dst_stride < dst_blocks)) return ATTN_ERR_INVALID_ARG;
+  const int64_t lens_bytes = 4 * static_cast<int64_t>(batch);
+  const int64_t kept_bytes = lens_bytes * cache->num_kv_heads * keep;
+  if (new_lens != ctx_lens && overlap(new_lens, lens_bytes, ctx_lens, lens_bytes)) return ATTN_ERR_INVALID_ARG;
+  if (overlap(kept, kept_bytes, ctx_lens, lens_bytes) || overlap(kept, kept_bytes, new_lens, lens_bytes))
+    return ATTN_ERR_INVALID_ARG;
   EvictArgs a;
   a.cache = paged(cache);
   a.acc = acc;

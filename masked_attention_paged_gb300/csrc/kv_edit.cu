@@ -167,10 +167,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const Evic
   const int len = p.ctx_lens[b];
   const int64_t slots = static_cast<int64_t>(p.max_blocks) * kBS;
   const int L = len < 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(len), slots));
-  if (rank == 0 && threadIdx.x == 0 && g == 0) {
-    if (len > slots) report(p.status, kStatusBounds);
-    p.new_lens[b] = len < 0 ? len : min(L, p.keep);
-  }
+  if (rank == 0 && threadIdx.x == 0 && g == 0 && len > slots) report(p.status, kStatusBounds);
   if (L <= p.keep) {  // everything stays (the whole cluster leaves here)
     for (int i = rank * kSelThreads + threadIdx.x; i < p.keep; i += nc * kSelThreads) kept[i] = i < L ? i : -1;
     return;
@@ -342,7 +339,8 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const Evic
 }
 
 // kv_evict, second launch: the kept rows and their weights to the other table's
-// blocks.  grid (row groups, Hkv, B).  The rows' places come first, one thread a
+// blocks, and the new lengths: new_lens may be ctx_lens itself, which every cluster of
+// the selection reads for itself and nothing here but the thread that writes.  grid (row groups, Hkv, B).  The rows' places come first, one thread a
 // row (kept slot -> block -> row: three dependent loads, once), then the rows
 // stream through registers, kCopyVecs 16-byte vectors a thread in flight.  64
 // sequences x 8 heads, 4096 rows of D = 128 kept: 310 us for 2.15 GB, the measured
@@ -355,6 +353,11 @@ __global__ void __launch_bounds__(kCopyThreads) kv_evict_copy_kernel(const Evict
   const int g = blockIdx.y, b = blockIdx.z;
   const int r0 = blockIdx.x * kCopyRows;
   const int32_t* kept = p.kept + (static_cast<int64_t>(b) * p.Hkv + g) * p.keep + r0;
+  if (r0 == 0 && g == 0 && threadIdx.x == 0) {
+    const int len = p.ctx_lens[b];
+    const int64_t most = min(static_cast<int64_t>(p.max_blocks) * kBS, static_cast<int64_t>(p.keep));
+    p.new_lens[b] = static_cast<int>(min(static_cast<int64_t>(len), most));  // an idle sequence's stays negative
+  }
   // the cache row of a slot, or -1
   auto place = [&](const int32_t* table, int blocks, int slot) -> int64_t {
     const int blk = slot / kBS < blocks ? table[slot / kBS] : -1;
