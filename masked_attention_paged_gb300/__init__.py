@@ -354,16 +354,34 @@ class Workspace:
 _default_ws: dict = {}
 
 
-def _small_ws(device) -> Workspace:
+def _default(key, nbytes: int, device, stream) -> Workspace:
+    """A workspace for the calls on a device that pass none, made at the first of
+    them and kept under `key`.  Its zeroes are in place before any call uses it,
+    on whichever stream.  A call that is captured into a graph before there is
+    one gets a workspace of its own, which is not kept: its clearing is part of
+    the graph, and each replay would wipe the status of every other call."""
+    device = torch.device(device)
+
+    def make():
+        ws = Workspace(nbytes, device=device)
+        if device.type == "cuda":
+            if torch.cuda.is_current_stream_capturing():
+                return ws
+            torch.cuda.current_stream(device).synchronize()
+        _default_ws[key] = ws
+        return ws
+
+    return _fresh(make, stream, device)
+
+
+def _small_ws(device, stream=None) -> Workspace:
+    """The default workspace of the calls that need the status word alone."""
     key = torch.device(device).index
     ws = _default_ws.get(key)
-    if ws is None:
-        ws = Workspace(256, device=device)
-        _default_ws[key] = ws
-    return ws
+    return _default(key, 256, device, stream) if ws is None else ws
 
 
-def _attn_ws(q: torch.Tensor, k: torch.Tensor) -> Workspace:
+def _attn_ws(q: torch.Tensor, k: torch.Tensor, stream=None) -> Workspace:
     """Default attn_fwd workspace: the status word plus room for the per-tile
     key bounds and the last-wave partials of this shape (kept per device,
     grown when a call needs more).  It is shared by every call on the device
@@ -373,8 +391,7 @@ def _attn_ws(q: torch.Tensor, k: torch.Tensor) -> Workspace:
     key = ("attn", torch.device(q.device).index)
     ws = _default_ws.get(key)
     if ws is None or ws.nbytes < need:
-        ws = Workspace(max(need, 256), device=q.device)
-        _default_ws[key] = ws
+        ws = _default(key, max(need, 256), q.device, stream)
     return ws
 
 
@@ -423,7 +440,7 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_pad_mask: Op
         _require(m.dim() == 2 and tuple(m.shape) == (q.shape[0], k.shape[2]) and m.stride(1) == 1,
                  f"key_pad_mask must be [{q.shape[0]}, {k.shape[2]}] with contiguous rows, got {tuple(m.shape)}")
         mptr, mstride = _ptr(m, "key_pad_mask"), m.stride(0)
-    ws = workspace or _attn_ws(q, k)
+    ws = workspace or _attn_ws(q, k, stream)
     dq, dk, dv, do = _desc(q), _desc(k), _desc(v), _desc(out)
     st = lib.attn_fwd(ctypes.byref(dq), ctypes.byref(dk), ctypes.byref(dv), mptr, mstride, float(scale),
                       ctypes.byref(do), _ptr(lse, "lse"), ws.ptr, ws.nbytes, _stream(stream))
@@ -447,7 +464,7 @@ def attn_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_lens:
         lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
     if lse is not None:
         _check_f32_buffer(lse, q.shape[0] * q.shape[1] * q.shape[2], "lse")
-    ws = workspace or _attn_ws(q, k)
+    ws = workspace or _attn_ws(q, k, stream)
     dq, dk, dv, do = _desc(q), _desc(k), _desc(v), _desc(out)
     st = lib.attn_fwd_varlen(ctypes.byref(dq), ctypes.byref(dk), ctypes.byref(dv), _ptr(key_lens, "key_lens"),
                              float(scale), ctypes.byref(do), _ptr(lse, "lse"), ws.ptr, ws.nbytes, _stream(stream))
@@ -509,7 +526,7 @@ def kv_append(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.T
     lib = load()
     _check_block_table(block_table, k_new.shape[0])
     _check_int32_vec(pos, k_new.shape[0], "pos")
-    ws = workspace or _small_ws(k_cache.device)
+    ws = workspace or _small_ws(k_cache.device, stream)
     c = _cache(k_cache, v_cache)
     dk, dv = _desc(k_new), _desc(v_new)
     st = lib.kv_append(ctypes.byref(c), _ptr(block_table, "block_table"), block_table.stride(0),
@@ -607,7 +624,7 @@ def paged_prefill_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
     if lse is not None:
         _check_f32_buffer(lse, B * Hq * T, "lse")
-    ws = workspace or _small_ws(q.device)
+    ws = workspace or _small_ws(q.device, stream)
     c = _cache(k_cache, v_cache)
     dq, do = _desc(q), _desc(out)
     dk = ctypes.byref(_desc(k_new)) if k_new is not None else None
@@ -644,7 +661,7 @@ def kv_append_q8(kq_cache: torch.Tensor, vq_cache: torch.Tensor, k_scale: torch.
     lib = load()
     _check_block_table(block_table, k_new.shape[0])
     _check_int32_vec(pos, k_new.shape[0], "pos")
-    ws = workspace or _small_ws(kq_cache.device)
+    ws = workspace or _small_ws(kq_cache.device, stream)
     c = _cache_q8(kq_cache, vq_cache, k_scale, v_scale)
     dk, dv = _desc(k_new), _desc(v_new)
     st = lib.kv_append_q8(ctypes.byref(c), _ptr(block_table, "block_table"), block_table.stride(0),
@@ -736,7 +753,7 @@ def paged_kv_gather(cache: torch.Tensor, block_table: torch.Tensor, lens: torch.
     _require(out.dtype == cache.dtype and tuple(out.shape) == (B, Hkv, max_len, D) and out.is_contiguous(),
              f"out must be contiguous {cache.dtype} [{B}, {Hkv}, {max_len}, {D}]")
     c = _cache(cache, cache)
-    ws = workspace or _small_ws(cache.device)
+    ws = workspace or _small_ws(cache.device, stream)
     st = lib.paged_kv_gather(ctypes.byref(c), 0, _ptr(block_table, "block_table"), block_table.stride(0),
                              block_table.shape[1], _ptr(lens, "lens"), B, max_len, _ptr(out, "out"), ws.ptr, ws.nbytes,
                              _stream(stream))
@@ -879,7 +896,7 @@ def _rope_append(name, cache, device, q, k_new, v_new, positions, freqs, block_t
     _check_block_table(block_table, B)
     _check_int32_vec(start_pos, B, "start_pos")
     _check_devices(name, q, k_new, v_new, positions, freqs, block_table, start_pos, q_out)
-    ws = workspace or _small_ws(device)
+    ws = workspace or _small_ws(device, stream)
     _require(k_new.dim() == 4 and v_new.dim() == 4, "k_new and v_new must have q's number of dimensions")
     st = getattr(lib, name)(_tensor_bytes(q), _tensor_bytes(k_new), _tensor_bytes(v_new), _ptr(positions, "positions"),
                             positions.stride(0), _ptr(freqs, "freqs"), 2 * freqs.shape[0], int(bool(interleaved)),
@@ -901,7 +918,7 @@ def rope_kv_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, po
     if q_out is None:
         q_out = _fresh(lambda: torch.empty_like(q), stream, q.device)
     if k_cache.is_cuda:
-        ws = workspace or _small_ws(k_cache.device)
+        ws = workspace or _small_ws(k_cache.device, stream)
         if _call("rope_kv_append", "yyyRf==YcbvWS", q, k_new, v_new, positions, freqs, int(bool(interleaved)),
                  float(magnitude), q_out, k_cache, v_cache, block_table, start_pos, ws.tensor, _handle(stream)):
             return q_out
@@ -993,7 +1010,7 @@ def kv_tree_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: to
     lib = load()
     B = ctx_lens.shape[0]
     if k_cache.is_cuda:
-        ws = workspace or _small_ws(k_cache.device)
+        ws = workspace or _small_ws(k_cache.device, stream)
         if _call("kv_tree_accept", "cbVrv=WS", k_cache, v_cache, block_table, ctx_lens, path, n_accept, B, ws.tensor,
                  _handle(stream)):
             return
@@ -1002,7 +1019,7 @@ def kv_tree_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: to
     _check_int32_rows(path, B, "path")
     _check_int32_vec(n_accept, B, "n_accept")
     _check_devices("kv_tree_accept", k_cache, v_cache, block_table, ctx_lens, path, n_accept)
-    ws = workspace or _small_ws(k_cache.device)
+    ws = workspace or _small_ws(k_cache.device, stream)
     c = _cache_bytes(k_cache, v_cache)
     st = lib.kv_tree_accept(c, _ptr(block_table, "block_table"), block_table.stride(0),
                             block_table.shape[1], _ptr(ctx_lens, "ctx_lens"), _ptr(path, "path"), path.stride(0),
@@ -1082,7 +1099,7 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
         kept = _fresh(lambda: torch.empty((B, Hkv, max(keep, 0)), dtype=torch.int32, device=k_cache.device), stream,
                       k_cache.device)
     if k_cache.is_cuda and kept.shape == (B, Hkv, keep):
-        ws = workspace or _small_ws(k_cache.device)
+        ws = workspace or _small_ws(k_cache.device, stream)
         if _call("kv_evict", "cAbVb====vKWS", k_cache, v_cache, acc, block_table, ctx_lens, dst_block_table, B, keep,
                  int(sink), int(recent), new_lens, kept, ws.tensor, _handle(stream)):
             return new_lens, kept
@@ -1098,7 +1115,7 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
     if not (kept.dtype == torch.int32 and kept.is_contiguous() and kept.shape == (B, Hkv, keep)):
         raise ValueError(f"kept must be contiguous int32 {(B, Hkv, keep)}, got {tuple(kept.shape)}")
     _check_devices("kv_evict", k_cache, v_cache, acc, block_table, ctx_lens, dst_block_table, new_lens, kept)
-    ws = workspace or _small_ws(k_cache.device)
+    ws = workspace or _small_ws(k_cache.device, stream)
     st = lib.kv_evict(c, _ptr(acc, "acc"), _ptr(block_table, "block_table"), block_table.stride(0),
                       block_table.shape[1], _ptr(ctx_lens, "ctx_lens"), _ptr(dst_block_table, "dst_block_table"),
                       dst_block_table.stride(0), dst_block_table.shape[1], B, keep, int(sink), int(recent),

@@ -40,3 +40,57 @@ def test_evict_updates_the_lengths_in_place(B, Hkv, longest):
         for x, y in zip(call(True), want):
             assert torch.equal(x, y)
     assert ws.status() == 0
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_default_workspace_is_zeroed_before_another_stream_uses_it(monkeypatch, raw):
+    monkeypatch.setattr(lib, "_default_ws", {})
+    kc, vc, acc, bt, lens, dt = _evict_inputs([100, 60], 2, 64, 32, seed=30)
+    bad = dt.clone()
+    bad[0, 0] = -9  # noted in the workspace's status
+    side = torch.cuda.Stream()
+    lib.kv_evict(kc, vc, acc, bt, lens, dt, 32, workspace=lib.Workspace(256))  # the code is loaded
+    torch.cuda._sleep(1000)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # the current stream has a tenth of a second to go
+    lib.kv_evict(kc, vc, acc, bt, lens, bad, 32, stream=side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
+    assert lib._small_ws(kc.device).status() == 5
+
+
+def test_a_default_attention_workspace_is_zeroed_before_another_stream_uses_it(monkeypatch):
+    """The word that a call leaves stays: a timed-out wait of the self-test stands for any."""
+    monkeypatch.setattr(lib, "_default_ws", {})
+    q = torch.zeros(1, 1, 64, 64, dtype=torch.bfloat16, device=DEV)
+    out, lse, side = torch.empty_like(q), torch.empty(1, 1, 64, device=DEV), torch.cuda.Stream()
+    first = lib.Workspace(lib.attn_fwd_workspace_size_for(1, 1, 64, 64))  # the code is loaded
+    lib.attn_fwd(q, q, q, out=out, lse=lse, workspace=first)
+    lib._check("selftest", lib.load().attn_selftest_wait_timeout(first.ptr, first.nbytes, 100, side.cuda_stream))
+    torch.cuda._sleep(1000)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    lib.attn_fwd(q, q, q, out=out, lse=lse, stream=side)
+    ws = lib._attn_ws(q, q)
+    lib._check("selftest", lib.load().attn_selftest_wait_timeout(ws.ptr, ws.nbytes, 100, side.cuda_stream))
+    torch.cuda.synchronize()
+    assert ws.status() == 4
+
+
+def test_a_replayed_graph_leaves_the_status_of_other_calls(monkeypatch):
+    """The first call on a device captured without a workspace: its clearing is no part of a word that others share."""
+    monkeypatch.setattr(lib, "_default_ws", {})
+    kc, vc, acc, bt, lens, dt = _evict_inputs([100, 60], 2, 64, 32, seed=31)
+    nl, kept = torch.empty_like(lens), torch.empty(2, 2, 32, dtype=torch.int32, device=DEV)
+    want = lib.kv_evict(kc.clone(), vc.clone(), acc.clone(), bt, lens, dt, 32, sink=1, recent=4,
+                        workspace=lib.Workspace(256))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lib.kv_evict(kc, vc, acc, bt, lens, dt, 32, sink=1, recent=4, new_lens=nl, kept=kept)
+    bad = dt.clone()
+    bad[0, 0] = -9  # noted in the workspace's status
+    lib.kv_evict(kc.clone(), vc.clone(), acc.clone(), bt, lens, bad, 32)
+    assert lib._small_ws(kc.device).status() == 5
+    for _ in range(2):
+        graph.replay()
+        assert torch.equal(nl, want[0]) and torch.equal(kept, want[1])
+        assert lib._small_ws(kc.device).status() == 5
