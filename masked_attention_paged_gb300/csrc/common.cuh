@@ -278,6 +278,32 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sm
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...);
 }
 
+// A count in a workspace, of the CTAs that have left their piece of a result: the
+// one that brings it to `all` joins the pieces.  The workspace is not cleared between
+// calls, so the 64-bit word says whose count it is: 16 bits of kCountMark, 28 of the
+// call's generation, 20 of the count; any other word counts as zero.  The mark makes
+// the upper half a signalling NaN, which no arithmetic yields, and above every index
+// or length: what the calls leave in a workspace (float partials, small integers) is
+// never taken for a count, and generations tell the counts of calls apart.  (A
+// generation alone is a small number: a word of two small integers could pass.)  The
+// last one sets the count back to zero: the same generation may be replayed, from a
+// captured graph.
+constexpr unsigned long long kCountMark = 0x7fa5ull << 48;
+constexpr int kCountBits = 20;
+__device__ __forceinline__ bool count_last(unsigned long long* word, uint32_t gen, int all) {
+  const unsigned long long zero = kCountMark | static_cast<unsigned long long>(gen & 0xfffffffu) << kCountBits;
+  unsigned long long before = *reinterpret_cast<volatile unsigned long long*>(word), now;
+  for (;;) {
+    now = (before ^ zero) >> kCountBits == 0 ? before + 1 : zero + 1;
+    const unsigned long long seen = atomicCAS(word, before, now);
+    if (seen == before) break;
+    before = seen;
+  }
+  const bool last = now - zero == static_cast<unsigned long long>(all);
+  if (last) *reinterpret_cast<volatile unsigned long long*>(word) = zero;
+  return last;
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;

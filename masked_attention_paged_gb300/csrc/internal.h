@@ -121,7 +121,7 @@ struct DecodeArgs {
   float scale;
   void* partials;  // workspace after the status block
   int n_split;     // split slots per (sequence, head) in the partial buffer
-  uint32_t gen;    // this call's generation, tags its split counts (never 0)
+  uint32_t gen;    // this call's generation, tags its split counts
   uint32_t* status;
 };
 // tokens per split-K work unit of the paged decode
@@ -233,7 +233,7 @@ struct WeightArgs {
   float* acc;      // [num_blocks, Hkv, 16]
   void* partials;  // workspace after the status block
   int n_cta;       // CTAs of the launch (one per SM)
-  uint32_t gen;    // this call's generation (never 0)
+  uint32_t gen;    // this call's generation, tags its counts
   uint32_t* status;
 };
 size_t weights_partial_bytes(int64_t B, int64_t Hkv, int max_blocks, int n_cta);

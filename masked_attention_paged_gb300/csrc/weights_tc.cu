@@ -104,7 +104,7 @@ struct WeightParams {
   const int32_t* q_lens;  // or null: T each
   float* acc;             // [num_blocks, Hkv, 16]
   float* part;            // [2 n][kPair]
-  unsigned long long* count;  // [B, Hkv, pairs] (generation << 32) | pieces done
+  unsigned long long* count;  // [B, Hkv, pairs] pieces done (count_last)
   int pairs_max;
   uint32_t gen;
   uint32_t* status;
@@ -581,21 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (tid == 0) {
         __threadfence();
-        // the count returns to zero with the last piece; a word of another
-        // generation (another call, or anything else) reads as zero
-        unsigned long long* w =
-            p.count + (static_cast<int64_t>(s.b) * p.Hkv + s.g) * p.pairs_max + s.pair;
-        const unsigned long long tag = static_cast<unsigned long long>(p.gen) << 32;
-        unsigned long long before = *reinterpret_cast<volatile unsigned long long*>(w), now;
-        for (;;) {
-          now = (before >> 32) == p.gen ? before + 1 : tag + 1;
-          const unsigned long long seen = atomicCAS(w, before, now);
-          if (seen == before) break;
-          before = seen;
-        }
-        const bool last = (now & 0xffffffffull) == static_cast<unsigned long long>(s.pieces);
-        if (last) *w = tag;
-        bars->last = last;
+        bars->last = count_last(p.count + (static_cast<int64_t>(s.b) * p.Hkv + s.g) * p.pairs_max + s.pair, p.gen,
+                                s.pieces);
         mbar_arrive(&bars->piece_go);
       }
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->piece_go, pieces & 1, abort, p.status))) {

@@ -94,3 +94,50 @@ def test_a_replayed_graph_leaves_the_status_of_other_calls(monkeypatch):
         graph.replay()
         assert torch.equal(nl, want[0]) and torch.equal(kept, want[1])
         assert lib._small_ws(kc.device).status() == 5
+
+
+_STALE_COUNTS = """
+import math, torch
+import masked_attention_paged_gb300 as lib
+DEV = "cuda"
+g = torch.Generator().manual_seed(1)
+mb, Hkv, D = 700, 2, 64
+bt = torch.randperm(mb, generator=g).to(torch.int32).view(1, mb).to(DEV)
+kc, vc = (torch.randn(mb, Hkv, 16, D, generator=g).bfloat16().to(DEV) for _ in range(2))
+q = torch.randn(1, 8, D, generator=g).bfloat16().to(DEV)
+lens = torch.tensor([mb * 16], dtype=torch.int32, device=DEV)
+lse = torch.full((1, 8), 9.0, device=DEV)
+size = max(lib.paged_decode_workspace_size(1, 8, mb, 16, D), lib.paged_attn_weights_workspace_size(1, Hkv, mb))
+ws = lib.Workspace(size)
+
+def decode():
+    out = torch.zeros_like(q)
+    lib.paged_decode_attn(q, kc, vc, bt, lens, out=out, workspace=ws)
+    return out
+
+def weights():
+    acc = torch.zeros(mb, Hkv, 16, device=DEV)
+    lib.paged_attn_weights(q, lse, kc, bt, lens - 1, acc, workspace=ws)
+    return acc
+
+want = {f: f() for f in (decode, weights)}
+number = 2  # calls so far that count
+for _ in range(4):
+    for f, ref in want.items():
+        number += 1
+        words = ws.tensor[256:].view(torch.int32).view(-1, 2)
+        words[:, 0], words[:, 1] = 1000, number
+        got = f()
+        assert torch.equal(got, ref), (f.__name__, number, float((got - ref).abs().max()))
+assert ws.status() == 0
+print("counted")
+"""
+
+
+def test_small_integers_in_a_workspace_are_no_counts():
+    """What a call finds where its counts go are other calls' tables of small integers; the calls of a fresh process are
+    numbered from one, so that some of these words hold the very number of the call."""
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _STALE_COUNTS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "counted" in r.stdout, r.stderr[-2000:]
