@@ -225,7 +225,7 @@ def _call(name: str, fmt: str, *args) -> bool:
             loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
             try:
                 _marshal = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
-            except ImportError:  # built against another Python: the checks serve
+            except ImportError:  # a library that it was linked to is not there: the checks serve
                 pass
     if _marshal is None:
         return False

@@ -52,9 +52,12 @@ def _stale(obj: str, src: str) -> bool:
 
 
 def marshal_path() -> str:
-    """The binding's compiled module, per machine and version of torch."""
+    """The binding's compiled module, per machine, version of torch and ABI of the
+    interpreter: it is compiled against Python's object layouts, which nothing
+    checks when it is loaded."""
     import torch
-    return os.path.join(BUILD, f"_marshal_{platform.machine()}_{torch.__version__.replace('+', '_')}.so")
+    abi = sysconfig.get_config_var("SOABI") or sys.implementation.cache_tag
+    return os.path.join(BUILD, f"_marshal_{platform.machine()}_{torch.__version__.replace('+', '_')}_{abi}.so")
 
 
 def _marshal_command(out: str) -> list[str]:

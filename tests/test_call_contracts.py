@@ -1,7 +1,9 @@
 """What the rotary, tree, weight and eviction calls promise about their arguments
 beside shapes and types, without a GPU: which outputs may be which inputs."""
 import ctypes
+import sysconfig
 
+from masked_attention_paged_gb300 import build
 from test_boundary import FAKE, INVALID, L, _cache  # noqa: F401
 
 
@@ -19,3 +21,13 @@ def test_evict_refuses_lengths_that_overlap_in_part(L):  # noqa: F811
         assert call(FAKE, FAKE + 16, at) == INVALID
         assert call(FAKE + 16, FAKE, at) == INVALID
         assert call(FAKE, FAKE, at) == INVALID
+
+
+def test_the_compiled_caller_is_told_apart_by_interpreter(monkeypatch):
+    """Compiled against one Python's object layouts, it is not what another one loads from the same tree."""
+    here, var = build.marshal_path(), sysconfig.get_config_var
+    assert sysconfig.get_config_var("SOABI") in here
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda n: "cpython-399-other" if n == "SOABI" else var(n))
+    assert build.marshal_path() != here
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda n: None if n == "SOABI" else var(n))
+    assert build.marshal_path().endswith(".so") and "None" not in build.marshal_path()
