@@ -799,13 +799,16 @@ _ROPE_SCALING = {"plain": 0, "linear": 1, "base": 2, "banded": 3, "ramp": 4}
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
-                     original_len: int = 0, low: float = 1.0, high: float = 4.0, device=None):
+                     original_len: int = 0, low: float = 1.0, high: Optional[float] = None, device=None):
     """Frequencies for the rope calls: (freqs, magnitude) with freqs int64
     [rotary_dim / 2] on the device, each pair's turns a token as a 64-bit
     fraction.  scaling: "plain", "linear" (positions / factor), "base" (a larger
     base), "banded" or "ramp" (slow pairs interpolated, fast ones kept; low and
-    high in turns over original_len tokens)."""
+    high in turns over original_len tokens; high is 4 for "banded" and 32 for
+    "ramp" unless given, the values that models of either kind are trained with)."""
     _require(scaling in _ROPE_SCALING, f"scaling must be one of {sorted(_ROPE_SCALING)}, got {scaling!r}")
+    if high is None:
+        high = 32.0 if scaling == "ramp" else 4.0
     turns = torch.empty(max(0, int(rotary_dim) // 2), dtype=torch.int64)
     magnitude = ctypes.c_float(1.0)
     st = load().attn_rope_frequencies(int(rotary_dim), float(base), _ROPE_SCALING[scaling], float(factor),

@@ -3,6 +3,10 @@ beside shapes and types, without a GPU: which outputs may be which inputs."""
 import ctypes
 import sysconfig
 
+import pytest
+import torch
+
+import masked_attention_paged_gb300 as lib
 from masked_attention_paged_gb300 import build
 from test_boundary import FAKE, INVALID, L, _cache  # noqa: F401
 
@@ -31,3 +35,13 @@ def test_the_compiled_caller_is_told_apart_by_interpreter(monkeypatch):
     assert build.marshal_path() != here
     monkeypatch.setattr(sysconfig, "get_config_var", lambda n: None if n == "SOABI" else var(n))
     assert build.marshal_path().endswith(".so") and "None" not in build.marshal_path()
+
+
+@pytest.mark.parametrize("scaling,high", [("banded", 4.0), ("ramp", 32.0)])
+def test_rope_frequencies_blend_as_models_of_each_kind_do_unless_told(scaling, high):
+    kw = dict(scaling=scaling, factor=8.0, original_len=8192, device="cpu")
+    got, m = lib.rope_frequencies(128, **kw)
+    want, n = lib.rope_frequencies(128, high=high, **kw)
+    assert torch.equal(got, want) and m == n
+    other, _ = lib.rope_frequencies(128, high=36.0 - high, **kw)
+    assert not torch.equal(got, other)
