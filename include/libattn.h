@@ -473,7 +473,7 @@ attn_status attn_rope_frequencies(int32_t rotary_dim, double base, int32_t scali
  *   x, out     [B, H, T, D] bf16 or f32, the same dtype (strided views of any
  *              alignment; 16-byte aligned rows are faster); out may be x itself
  *              (same data pointer and strides), else they must not overlap.
- *              D <= 512.
+ *              No stride 0 in out (rows of its own each).  D <= 512.
  *   positions  int32, token t of row b at positions[b * pos_stride_b + t]
  *              (pos_stride_b = 0: one row for all); any value, negative too
  *   freqs      [rotary_dim / 2] on the device; rotary_dim even, 2 .. D
@@ -539,7 +539,7 @@ attn_status rope_kv_append_q8(const attn_tensor *q, const attn_tensor *k_new, co
  * chunk.
  *
  *   q, out        [batch, Hq, T, head_dim]; q bf16, out bf16 or f32 (strided
- *                 views, 16-byte aligned rows, no stride 0 in q); Hq a multiple of
+ *                 views, 16-byte aligned rows, no stride 0); Hq a multiple of
  *                 Hkv, at most 128 query heads per KV head
  *   k_new, v_new  [batch, Hkv, T, head_dim] bf16 (as q): draft t's rows, written to
  *                 slot ctx_lens[b] + t.  Both NULL: they are in the cache already.

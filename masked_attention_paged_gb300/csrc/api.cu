@@ -46,13 +46,16 @@ bool vec16_ok(const attn_tensor* t) {
   return true;
 }
 
-// Rows that a TMA map can walk: vec16_ok, and no stride of zero over more than one
-// element.
-bool tma_rows_ok(const attn_tensor* t) {
+// No stride of zero over more than one element: rows of an output would be written by
+// several threads (and rotated several times, in place).
+bool rows_apart(const attn_tensor* t) {
   for (int i = 0; i < t->ndim - 1; ++i)
     if (t->stride[i] == 0 && t->shape[i] > 1) return false;
-  return vec16_ok(t);
+  return true;
 }
+
+// Rows that a TMA map can walk.
+bool tma_rows_ok(const attn_tensor* t) { return rows_apart(t) && vec16_ok(t); }
 
 // Whether [a, a + a_bytes) and [b, b + b_bytes) share a byte.
 bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
@@ -596,6 +599,10 @@ static attn_status rope_args(RopeArgs& a, const attn_tensor* x, const int32_t* p
   if (pos_stride_b < 0) return ATTN_ERR_INVALID_ARG;
   const int eb = elem_bytes(x->dtype);
   if (!aligned(x->data, eb) || !aligned(out->data, eb)) return ATTN_ERR_INVALID_ARG;
+  if (!rows_apart(out)) return ATTN_ERR_INVALID_ARG;
+  if (x->data == out->data)  // in place: the same rows
+    for (int i = 0; i < 3; ++i)
+      if (x->shape[i] > 1 && x->stride[i] != out->stride[i]) return ATTN_ERR_INVALID_ARG;
   a.x = view(x);
   a.out = view(out);
   a.positions = positions;
@@ -726,7 +733,7 @@ attn_status paged_tree_attn(const attn_tensor* q, const attn_tensor* k_new, cons
   if (B == 0 || T == 0) return ATTN_OK;
   if (block_table == nullptr || ctx_lens == nullptr || parents == nullptr) return ATTN_ERR_INVALID_ARG;
   if (B > 1 && (bt_stride < max_blocks || (par_stride_b != 0 && par_stride_b < T))) return ATTN_ERR_INVALID_ARG;
-  if (!tma_rows_ok(q) || !vec16_ok(out)) return ATTN_ERR_INVALID_ARG;
+  if (!tma_rows_ok(q) || !tma_rows_ok(out)) return ATTN_ERR_INVALID_ARG;
   if (k_new != nullptr && (!tma_rows_ok(k_new) || !tma_rows_ok(v_new))) return ATTN_ERR_INVALID_ARG;
   TreeArgs a;
   a.cache = paged(cache);

@@ -8,7 +8,7 @@ import torch
 
 import masked_attention_paged_gb300 as lib
 from masked_attention_paged_gb300 import build
-from test_boundary import FAKE, INVALID, L, _cache  # noqa: F401
+from test_boundary import FAKE, INVALID, L, _cache, _t  # noqa: F401
 
 
 def test_evict_refuses_lengths_that_overlap_in_part(L):  # noqa: F811
@@ -45,3 +45,30 @@ def test_rope_frequencies_blend_as_models_of_each_kind_do_unless_told(scaling, h
     assert torch.equal(got, want) and m == n
     other, _ = lib.rope_frequencies(128, high=36.0 - high, **kw)
     assert not torch.equal(got, other)
+
+
+FAR = FAKE + (1 << 30)  # another buffer
+
+
+def _rope(L, x, out):  # noqa: F811
+    return L.rope_apply(ctypes.byref(x), FAKE, 5, FAKE, 64, 0, 0, 1.0, ctypes.byref(out), None)
+
+
+def test_rows_of_an_output_must_be_apart(L):  # noqa: F811
+    """A broadcast output has rows that several threads write; in place they would be rotated several times."""
+    shape, row = (2, 4, 5, 128), (2560, 640, 128, 1)
+    for i in range(3):
+        flat = _t(shape, stride=[0 if j == i else v for j, v in enumerate(row)], data=FAR)
+        assert _rope(L, _t(shape), flat) == INVALID, i
+        assert _rope(L, flat, flat) == INVALID, i
+        c = _cache(H=4)
+        assert L.rope_kv_append(*(ctypes.byref(_t(shape)) for _ in range(3)), FAKE, 5, FAKE,
+                                64, 0, 1.0, ctypes.byref(flat), ctypes.byref(c), FAKE, 10, 10, FAKE, FAKE, 256,
+                                None) == INVALID, i
+        assert L.paged_tree_attn(ctypes.byref(_t(shape)), None, None, ctypes.byref(c), FAKE, 10, 10, FAKE,
+                                 FAKE, 5, 0.1, ctypes.byref(flat), None, FAKE, 1 << 30, None) == INVALID, i
+
+
+def test_a_rotation_in_place_has_the_same_rows(L):  # noqa: F811
+    shape = (2, 4, 5, 128)
+    assert _rope(L, _t(shape), _t(shape, stride=(2560, 128, 512, 1))) == INVALID
