@@ -734,7 +734,6 @@ attn_status paged_tree_attn(const attn_tensor* q, const attn_tensor* k_new, cons
   if (block_table == nullptr || ctx_lens == nullptr || parents == nullptr) return ATTN_ERR_INVALID_ARG;
   if (B > 1 && (bt_stride < max_blocks || (par_stride_b != 0 && par_stride_b < T))) return ATTN_ERR_INVALID_ARG;
   if (!tma_rows_ok(q) || !tma_rows_ok(out)) return ATTN_ERR_INVALID_ARG;
-  if (out->data == q->data) return ATTN_ERR_INVALID_ARG;  // q is read again beside values that are not finite
   if (k_new != nullptr && (!tma_rows_ok(k_new) || !tma_rows_ok(v_new))) return ATTN_ERR_INVALID_ARG;
   TreeArgs a;
   a.cache = paged(cache);

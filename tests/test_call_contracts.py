@@ -72,10 +72,3 @@ def test_rows_of_an_output_must_be_apart(L):  # noqa: F811
 def test_a_rotation_in_place_has_the_same_rows(L):  # noqa: F811
     shape = (2, 4, 5, 128)
     assert _rope(L, _t(shape), _t(shape, stride=(2560, 128, 512, 1))) == INVALID
-
-
-def test_a_tree_is_not_attended_in_place(L):  # noqa: F811
-    """A row whose values are not finite reads its query again after its first columns are written."""
-    c, q = _cache(H=4), _t((2, 4, 5, 128))
-    assert L.paged_tree_attn(ctypes.byref(q), None, None, ctypes.byref(c), FAKE, 10, 10, FAKE, FAKE, 5, 0.1,
-                             ctypes.byref(q), None, FAKE, 1 << 30, None) == INVALID
