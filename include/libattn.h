@@ -539,8 +539,10 @@ attn_status rope_kv_append_q8(const attn_tensor *q, const attn_tensor *k_new, co
  * chunk.
  *
  *   q, out        [batch, Hq, T, head_dim]; q bf16, out bf16 or f32 (strided
- *                 views, 16-byte aligned rows, no stride 0); Hq a multiple of
- *                 Hkv, at most 128 query heads per KV head
+ *                 views, 16-byte aligned rows, no stride 0; out must not
+ *                 overlap q, k_new or v_new, which are read again where a
+ *                 value is not finite); Hq a multiple of Hkv, at most 128
+ *                 query heads per KV head
  *   k_new, v_new  [batch, Hkv, T, head_dim] bf16 (as q): draft t's rows, written to
  *                 slot ctx_lens[b] + t.  Both NULL: they are in the cache already.
  *   parents       int32, row b at parents + b * par_stride_b (0: one tree for all)
