@@ -395,6 +395,14 @@ def _attn_ws(q: torch.Tensor, k: torch.Tensor, stream=None) -> Workspace:
     return ws
 
 
+def _ws_ptr(ws: Workspace):
+    return _ptr(ws.tensor, "workspace")
+
+
+def _ws_tensor(workspace: Optional[Workspace]):
+    return workspace.tensor if workspace is not None else None
+
+
 def check_device_status(ws: Workspace, stream=None) -> int:
     raw = ctypes.c_uint32(0)
     st = load().attn_check_device_status(ws.ptr, ctypes.byref(raw), _stream(stream))
@@ -443,7 +451,7 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_pad_mask: Op
     ws = workspace or _attn_ws(q, k, stream)
     dq, dk, dv, do = _desc(q), _desc(k), _desc(v), _desc(out)
     st = lib.attn_fwd(ctypes.byref(dq), ctypes.byref(dk), ctypes.byref(dv), mptr, mstride, float(scale),
-                      ctypes.byref(do), _ptr(lse, "lse"), ws.ptr, ws.nbytes, _stream(stream))
+                      ctypes.byref(do), _ptr(lse, "lse"), _ws_ptr(ws), ws.nbytes, _stream(stream))
     _check("attn_fwd", st)
     return (out, lse) if return_lse else out
 
@@ -467,7 +475,7 @@ def attn_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_lens:
     ws = workspace or _attn_ws(q, k, stream)
     dq, dk, dv, do = _desc(q), _desc(k), _desc(v), _desc(out)
     st = lib.attn_fwd_varlen(ctypes.byref(dq), ctypes.byref(dk), ctypes.byref(dv), _ptr(key_lens, "key_lens"),
-                             float(scale), ctypes.byref(do), _ptr(lse, "lse"), ws.ptr, ws.nbytes, _stream(stream))
+                             float(scale), ctypes.byref(do), _ptr(lse, "lse"), _ws_ptr(ws), ws.nbytes, _stream(stream))
     _check("attn_fwd_varlen", st)
     return (out, lse) if return_lse else out
 
@@ -530,7 +538,7 @@ def kv_append(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.T
     c = _cache(k_cache, v_cache)
     dk, dv = _desc(k_new), _desc(v_new)
     st = lib.kv_append(ctypes.byref(c), _ptr(block_table, "block_table"), block_table.stride(0),
-                       block_table.shape[1], _ptr(pos, "pos"), ctypes.byref(dk), ctypes.byref(dv), ws.ptr,
+                       block_table.shape[1], _ptr(pos, "pos"), ctypes.byref(dk), ctypes.byref(dv), _ws_ptr(ws),
                        ws.nbytes, _stream(stream))
     _check("kv_append", st)
 
@@ -563,7 +571,7 @@ def paged_decode_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     st = lib.paged_decode_attn(ctypes.byref(dq), ctypes.byref(c), _ptr(block_table, "block_table"),
                                block_table.stride(0), max_blocks, _ptr(ctx_lens, "ctx_lens"), float(scale),
                                ctypes.byref(do), _ptr(lse, "lse"),
-                               ws.ptr, ws.nbytes, _stream(stream))
+                               _ws_ptr(ws), ws.nbytes, _stream(stream))
     _check("paged_decode_attn", st)
     return (out, lse) if return_lse else out
 
@@ -596,7 +604,7 @@ def paged_decode_attn_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.
     dq, dk, dv, do = _desc(q), _desc(k_new), _desc(v_new), _desc(out)
     st = lib.paged_decode_attn_append(ctypes.byref(dq), ctypes.byref(dk), ctypes.byref(dv), ctypes.byref(c),
                                       _ptr(block_table, "block_table"), block_table.stride(0), max_blocks,
-                                      _ptr(pos, "pos"), float(scale), ctypes.byref(do), _ptr(lse, "lse"), ws.ptr,
+                                      _ptr(pos, "pos"), float(scale), ctypes.byref(do), _ptr(lse, "lse"), _ws_ptr(ws),
                                       ws.nbytes,
                                       _stream(stream))
     _check("paged_decode_attn_append", st)
@@ -631,7 +639,7 @@ def paged_prefill_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     dv = ctypes.byref(_desc(v_new)) if v_new is not None else None
     st = lib.paged_prefill_attn(ctypes.byref(dq), dk, dv, ctypes.byref(c), _ptr(block_table, "block_table"),
                                 block_table.stride(0), block_table.shape[1], _ptr(start_pos, "start_pos"),
-                                int(bool(causal)), float(scale), ctypes.byref(do), _ptr(lse, "lse"), ws.ptr,
+                                int(bool(causal)), float(scale), ctypes.byref(do), _ptr(lse, "lse"), _ws_ptr(ws),
                                 ws.nbytes, _stream(stream))
     _check("paged_prefill_attn", st)
     return (out, lse) if return_lse else out
@@ -665,7 +673,7 @@ def kv_append_q8(kq_cache: torch.Tensor, vq_cache: torch.Tensor, k_scale: torch.
     c = _cache_q8(kq_cache, vq_cache, k_scale, v_scale)
     dk, dv = _desc(k_new), _desc(v_new)
     st = lib.kv_append_q8(ctypes.byref(c), _ptr(block_table, "block_table"), block_table.stride(0),
-                          block_table.shape[1], _ptr(pos, "pos"), ctypes.byref(dk), ctypes.byref(dv), ws.ptr,
+                          block_table.shape[1], _ptr(pos, "pos"), ctypes.byref(dk), ctypes.byref(dv), _ws_ptr(ws),
                           ws.nbytes, _stream(stream))
     _check("kv_append_q8", st)
 
@@ -699,7 +707,7 @@ def paged_decode_attn_q8(q: torch.Tensor, kq_cache: torch.Tensor, vq_cache: torc
     st = lib.paged_decode_attn_q8(ctypes.byref(dq), ctypes.byref(c), _ptr(block_table, "block_table"),
                                   block_table.stride(0), max_blocks, _ptr(ctx_lens, "ctx_lens"), float(scale),
                                   ctypes.byref(do), _ptr(lse, "lse"),
-                                  ws.ptr, ws.nbytes, _stream(stream))
+                                  _ws_ptr(ws), ws.nbytes, _stream(stream))
     _check("paged_decode_attn_q8", st)
     return (out, lse) if return_lse else out
 
@@ -733,7 +741,7 @@ def paged_decode_attn_append_q8(q: torch.Tensor, k_new: torch.Tensor, v_new: tor
     st = lib.paged_decode_attn_append_q8(ctypes.byref(dq), ctypes.byref(dk), ctypes.byref(dv), ctypes.byref(c),
                                          _ptr(block_table, "block_table"), block_table.stride(0), max_blocks,
                                          _ptr(pos, "pos"), float(scale), ctypes.byref(do), _ptr(lse, "lse"),
-                                         ws.ptr, ws.nbytes, _stream(stream))
+                                         _ws_ptr(ws), ws.nbytes, _stream(stream))
     _check("paged_decode_attn_append_q8", st)
     return (out, lse) if return_lse else out
 
@@ -755,8 +763,8 @@ def paged_kv_gather(cache: torch.Tensor, block_table: torch.Tensor, lens: torch.
     c = _cache(cache, cache)
     ws = workspace or _small_ws(cache.device, stream)
     st = lib.paged_kv_gather(ctypes.byref(c), 0, _ptr(block_table, "block_table"), block_table.stride(0),
-                             block_table.shape[1], _ptr(lens, "lens"), B, max_len, _ptr(out, "out"), ws.ptr, ws.nbytes,
-                             _stream(stream))
+                             block_table.shape[1], _ptr(lens, "lens"), B, max_len, _ptr(out, "out"), _ws_ptr(ws),
+                             ws.nbytes, _stream(stream))
     _check("paged_kv_gather", st)
     return out
 
@@ -881,7 +889,7 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, in
     return out
 
 
-def _rope_append(name, cache, device, q, k_new, v_new, positions, freqs, block_table, start_pos, interleaved, magnitude,
+def _rope_append(name, cache, caches, q, k_new, v_new, positions, freqs, block_table, start_pos, interleaved, magnitude,
                  q_out, workspace, stream):
     lib = load()
     if q_out is None:
@@ -898,13 +906,14 @@ def _rope_append(name, cache, device, q, k_new, v_new, positions, freqs, block_t
     _check_rope(positions, freqs, B, T, D)
     _check_block_table(block_table, B)
     _check_int32_vec(start_pos, B, "start_pos")
-    _check_devices(name, q, k_new, v_new, positions, freqs, block_table, start_pos, q_out)
-    ws = workspace or _small_ws(device, stream)
+    _check_devices(name, q, k_new, v_new, positions, freqs, block_table, start_pos, q_out, *caches,
+                   _ws_tensor(workspace))
+    ws = workspace or _small_ws(caches[0].device, stream)
     _require(k_new.dim() == 4 and v_new.dim() == 4, "k_new and v_new must have q's number of dimensions")
     st = getattr(lib, name)(_tensor_bytes(q), _tensor_bytes(k_new), _tensor_bytes(v_new), _ptr(positions, "positions"),
                             positions.stride(0), _ptr(freqs, "freqs"), 2 * freqs.shape[0], int(bool(interleaved)),
                             float(magnitude), _tensor_bytes(full), cache, _ptr(block_table, "block_table"),
-                            block_table.stride(0), block_table.shape[1], _ptr(start_pos, "start_pos"), ws.ptr,
+                            block_table.stride(0), block_table.shape[1], _ptr(start_pos, "start_pos"), _ws_ptr(ws),
                             ws.nbytes, _stream(stream))
     _check(name, st)
     return q_out
@@ -925,8 +934,8 @@ def rope_kv_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, po
         if _call("rope_kv_append", "yyyRf==YcbvWS", q, k_new, v_new, positions, freqs, int(bool(interleaved)),
                  float(magnitude), q_out, k_cache, v_cache, block_table, start_pos, ws.tensor, _handle(stream)):
             return q_out
-    return _rope_append("rope_kv_append", _cache_bytes(k_cache, v_cache), k_cache.device, q, k_new, v_new, positions,
-                        freqs, block_table, start_pos, interleaved, magnitude, q_out, workspace, stream)
+    return _rope_append("rope_kv_append", _cache_bytes(k_cache, v_cache), (k_cache, v_cache), q, k_new, v_new,
+                        positions, freqs, block_table, start_pos, interleaved, magnitude, q_out, workspace, stream)
 
 
 def rope_kv_append_q8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, positions: torch.Tensor,
@@ -936,9 +945,9 @@ def rope_kv_append_q8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
                       workspace: Optional[Workspace] = None, stream=None):
     """rope_kv_append into an INT8 cache (codes int8 [N, Hkv, 16, D], scales
     float32 [N, Hkv, 16])."""
-    return _rope_append("rope_kv_append_q8", bytes(_cache_q8(kq_cache, vq_cache, k_scale, v_scale)), kq_cache.device, q,
-                        k_new, v_new, positions, freqs, block_table, start_pos, interleaved, magnitude, q_out,
-                        workspace, stream)
+    return _rope_append("rope_kv_append_q8", bytes(_cache_q8(kq_cache, vq_cache, k_scale, v_scale)),
+                        (kq_cache, vq_cache, k_scale, v_scale), q, k_new, v_new, positions, freqs, block_table,
+                        start_pos, interleaved, magnitude, q_out, workspace, stream)
 
 
 # --------------------------------------------------------------------------
@@ -988,7 +997,8 @@ def paged_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         raise ValueError(f"parents must be [{B}, {T}], got {tuple(parents.shape)}")
     if lse is not None:
         _check_f32_buffer(lse, B * Hq * T, "lse")
-    _check_devices("paged_tree_attn", q, k_cache, v_cache, block_table, ctx_lens, parents, k_new, v_new, out, lse)
+    _check_devices("paged_tree_attn", q, k_cache, v_cache, block_table, ctx_lens, parents, k_new, v_new, out, lse,
+                   _ws_tensor(workspace))
     c = _cache_bytes(k_cache, v_cache)
     max_blocks = block_table.shape[1]
     ws = workspace
@@ -999,8 +1009,8 @@ def paged_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     dv = _tensor_bytes(v_new) if v_new is not None else None
     st = lib.paged_tree_attn(_tensor_bytes(q), dk, dv, c, _ptr(block_table, "block_table"),
                              block_table.stride(0), max_blocks, _ptr(ctx_lens, "ctx_lens"), _ptr(parents, "parents"),
-                             parents.stride(0), float(scale), _tensor_bytes(out), _ptr(lse, "lse"), ws.ptr, ws.nbytes,
-                             _stream(stream))
+                             parents.stride(0), float(scale), _tensor_bytes(out), _ptr(lse, "lse"), _ws_ptr(ws),
+                             ws.nbytes, _stream(stream))
     _check("paged_tree_attn", st)
     return (out, lse) if return_lse else out
 
@@ -1021,12 +1031,12 @@ def kv_tree_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: to
     _check_int32_vec(ctx_lens, B, "ctx_lens")
     _check_int32_rows(path, B, "path")
     _check_int32_vec(n_accept, B, "n_accept")
-    _check_devices("kv_tree_accept", k_cache, v_cache, block_table, ctx_lens, path, n_accept)
+    _check_devices("kv_tree_accept", k_cache, v_cache, block_table, ctx_lens, path, n_accept, _ws_tensor(workspace))
     ws = workspace or _small_ws(k_cache.device, stream)
     c = _cache_bytes(k_cache, v_cache)
     st = lib.kv_tree_accept(c, _ptr(block_table, "block_table"), block_table.stride(0),
                             block_table.shape[1], _ptr(ctx_lens, "ctx_lens"), _ptr(path, "path"), path.stride(0),
-                            path.shape[1], _ptr(n_accept, "n_accept"), B, ws.ptr, ws.nbytes, _stream(stream))
+                            path.shape[1], _ptr(n_accept, "n_accept"), B, _ws_ptr(ws), ws.nbytes, _stream(stream))
     _check("kv_tree_accept", st)
 
 
@@ -1070,7 +1080,7 @@ def paged_attn_weights(q: torch.Tensor, lse: torch.Tensor, k_cache: torch.Tensor
         _check_int32_vec(q_lens, B, "q_lens")
     c = _cache_bytes(k_cache, k_cache)
     _check_acc(acc, k_cache)
-    _check_devices("paged_attn_weights", q, lse, k_cache, block_table, start_pos, acc, q_lens)
+    _check_devices("paged_attn_weights", q, lse, k_cache, block_table, start_pos, acc, q_lens, _ws_tensor(workspace))
     max_blocks = block_table.shape[1]
     ws = workspace
     if ws is None:
@@ -1078,7 +1088,7 @@ def paged_attn_weights(q: torch.Tensor, lse: torch.Tensor, k_cache: torch.Tensor
         ws = _fresh(lambda: Workspace(need, device=q.device), stream, q.device)
     st = lib.paged_attn_weights(_tensor_bytes(q), _ptr(lse, "lse"), c, _ptr(block_table, "block_table"),
                                 block_table.stride(0), max_blocks, _ptr(start_pos, "start_pos"),
-                                _ptr(q_lens, "q_lens"), int(bool(causal)), float(scale), _ptr(acc, "acc"), ws.ptr,
+                                _ptr(q_lens, "q_lens"), int(bool(causal)), float(scale), _ptr(acc, "acc"), _ws_ptr(ws),
                                 ws.nbytes, _stream(stream))
     _check("paged_attn_weights", st)
     return acc
@@ -1117,11 +1127,12 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
     _check_int32_vec(new_lens, B, "new_lens")
     if not (kept.dtype == torch.int32 and kept.is_contiguous() and kept.shape == (B, Hkv, keep)):
         raise ValueError(f"kept must be contiguous int32 {(B, Hkv, keep)}, got {tuple(kept.shape)}")
-    _check_devices("kv_evict", k_cache, v_cache, acc, block_table, ctx_lens, dst_block_table, new_lens, kept)
+    _check_devices("kv_evict", k_cache, v_cache, acc, block_table, ctx_lens, dst_block_table, new_lens, kept,
+                   _ws_tensor(workspace))
     ws = workspace or _small_ws(k_cache.device, stream)
     st = lib.kv_evict(c, _ptr(acc, "acc"), _ptr(block_table, "block_table"), block_table.stride(0),
                       block_table.shape[1], _ptr(ctx_lens, "ctx_lens"), _ptr(dst_block_table, "dst_block_table"),
                       dst_block_table.stride(0), dst_block_table.shape[1], B, keep, int(sink), int(recent),
-                      _ptr(new_lens, "new_lens"), _ptr(kept, "kept"), ws.ptr, ws.nbytes, _stream(stream))
+                      _ptr(new_lens, "new_lens"), _ptr(kept, "kept"), _ws_ptr(ws), ws.nbytes, _stream(stream))
     _check("kv_evict", st)
     return new_lens, kept

@@ -8,6 +8,7 @@ import torch
 
 import masked_attention_paged_gb300 as lib
 from masked_attention_paged_gb300 import build
+from test_binding_marshalling import rec  # noqa: F401  (fixture)
 from test_boundary import FAKE, INVALID, L, _cache, _t  # noqa: F401
 
 
@@ -72,3 +73,43 @@ def test_rows_of_an_output_must_be_apart(L):  # noqa: F811
 def test_a_rotation_in_place_has_the_same_rows(L):  # noqa: F811
     shape = (2, 4, 5, 128)
     assert _rope(L, _t(shape), _t(shape, stride=(2560, 128, 512, 1))) == INVALID
+
+
+def _calls(ws):
+    """Each call that checks devices, with its caches: (name, the call, tensors that its kernels touch)."""
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.ones(*s, dtype=torch.int32)  # noqa: E731
+    q, kn, k, v, acc = bf(2, 8, 3, 128), bf(2, 2, 3, 128), bf(9, 2, 16, 128), bf(9, 2, 16, 128), torch.zeros(9, 2, 16)
+    kq, vq, ks, vs = k.to(torch.int8), v.to(torch.int8), torch.zeros(9, 2, 16), torch.zeros(9, 2, 16)
+    bt, dt, n, pos, fr = i32(2, 4), i32(2, 4), i32(2), i32(2, 3), torch.ones(64, dtype=torch.int64)
+    lse = torch.zeros(2, 8, 3)
+    kw = dict(workspace=ws, stream=0)
+    return [
+        ("rope_kv_append", lambda: lib.rope_kv_append(q, kn, kn, pos, fr, k, v, bt, n, **kw), (k, v, bt, pos, fr)),
+        ("rope_kv_append_q8", lambda: lib.rope_kv_append_q8(q, kn, kn, pos, fr, kq, vq, ks, vs, bt, n, **kw),
+         (kq, vq, ks, vs, bt)),
+        ("paged_tree_attn", lambda: lib.paged_tree_attn(q, k, v, bt, n, pos, k_new=kn, v_new=kn, **kw), (k, v, pos)),
+        ("kv_tree_accept", lambda: lib.kv_tree_accept(k, v, bt, n, pos, n, **kw), (k, v, bt, pos)),
+        ("paged_attn_weights", lambda: lib.paged_attn_weights(q, lse, k, bt, n, acc, **kw), (k, lse, acc)),
+        ("kv_evict", lambda: lib.kv_evict(k, v, acc, bt, n, dt, 5, **kw), (k, v, acc, bt, dt)),
+    ]
+
+
+def test_caches_and_workspaces_are_held_to_the_current_device(rec, monkeypatch):  # noqa: F811
+    """A kernel of one device that reads a cache or writes a workspace of another faults."""
+    seen = {}
+    monkeypatch.setattr(lib, "_check_devices", lambda name, *t: seen.setdefault(name, []).extend(t))
+    ws = lib.Workspace(1 << 20, device="cpu")
+    for name, call, tensors in _calls(ws):
+        call()
+        for t in (*tensors, ws.tensor):
+            assert any(t is x for x in seen[name]), (name, tuple(t.shape))
+
+
+def test_a_workspace_off_the_gpu_is_refused(rec, monkeypatch):  # noqa: F811
+    ws = lib.Workspace(1 << 20, device="cpu")
+    monkeypatch.setattr(lib, "_on_device", lambda t: t is not ws.tensor)
+    for name, call, _ in _calls(ws):
+        with pytest.raises(ValueError, match="workspace must be on a CUDA device"):
+            call()
+    assert not set(rec.calls) - {"paged_tree_workspace_size", "paged_attn_weights_workspace_size"}
