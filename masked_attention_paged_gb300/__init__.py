@@ -1105,7 +1105,10 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
     be ctx_lens, which is then updated in place."""
     lib = load()
     B, Hkv = ctx_lens.shape[0], k_cache.shape[1]
-    keep = int(keep)
+    keep, sink, recent = int(keep), int(sink), int(recent)
+    for name, n in (("keep", keep), ("sink", sink), ("recent", recent)):
+        if not -1 << 31 <= n < 1 << 31:  # the C call would see its low 32 bits
+            raise ValueError(f"{name} must be a 32-bit integer, got {n}")
     if new_lens is None:
         new_lens = _fresh(lambda: torch.empty(B, dtype=torch.int32, device=k_cache.device), stream, k_cache.device)
     if kept is None:
@@ -1114,7 +1117,7 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
     if k_cache.is_cuda and kept.shape == (B, Hkv, keep):
         ws = workspace or _small_ws(k_cache.device, stream)
         if _call("kv_evict", "cAbVb====vKWS", k_cache, v_cache, acc, block_table, ctx_lens, dst_block_table, B, keep,
-                 int(sink), int(recent), new_lens, kept, ws.tensor, _handle(stream)):
+                 sink, recent, new_lens, kept, ws.tensor, _handle(stream)):
             return new_lens, kept
     _check_block_table(block_table, B)
     _check_int32_vec(ctx_lens, B, "ctx_lens")
@@ -1132,7 +1135,7 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
     ws = workspace or _small_ws(k_cache.device, stream)
     st = lib.kv_evict(c, _ptr(acc, "acc"), _ptr(block_table, "block_table"), block_table.stride(0),
                       block_table.shape[1], _ptr(ctx_lens, "ctx_lens"), _ptr(dst_block_table, "dst_block_table"),
-                      dst_block_table.stride(0), dst_block_table.shape[1], B, keep, int(sink), int(recent),
+                      dst_block_table.stride(0), dst_block_table.shape[1], B, keep, sink, recent,
                       _ptr(new_lens, "new_lens"), _ptr(kept, "kept"), _ws_ptr(ws), ws.nbytes, _stream(stream))
     _check("kv_evict", st)
     return new_lens, kept

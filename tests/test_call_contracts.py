@@ -113,3 +113,14 @@ def test_a_workspace_off_the_gpu_is_refused(rec, monkeypatch):  # noqa: F811
         with pytest.raises(ValueError, match="workspace must be on a CUDA device"):
             call()
     assert not set(rec.calls) - {"paged_tree_workspace_size", "paged_attn_weights_workspace_size"}
+
+
+@pytest.mark.parametrize("kw", [dict(sink=1 << 32), dict(recent=(1 << 32) + 2), dict(sink=-(1 << 40)),
+                                dict(keep=1 << 31)])
+def test_evict_counts_past_32_bits_are_refused(rec, kw):  # noqa: F811
+    """Their low 32 bits are counts like any other: no sinks, two recent tokens."""
+    k, acc = torch.zeros(9, 2, 16, 128, dtype=torch.bfloat16), torch.zeros(9, 2, 16)
+    bt, n = torch.ones(2, 4, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="must be a 32-bit integer"):
+        lib.kv_evict(k, k, acc, bt, n, bt, **{"keep": 5, **kw}, stream=0)
+    assert not rec.calls
