@@ -529,7 +529,8 @@ attn_status rope_kv_append_q8(const attn_tensor *q, const attn_tensor *k_new, co
  *     0 .. t - 1   that draft
  *     below -1     none: an absent draft (a shorter tree in the batch).  It and
  *                  the drafts that follow it are not cached, nobody attends to
- *                  them, and their rows are out = 0, lse = -inf.
+ *                  them, and their rows are out = 0, lse = -inf.  A block that
+ *                  would hold only such drafts may have any id in the table.
  * A parent at or past its own index sets ATTN_ERR_DEVICE_BOUNDS and counts as
  * absent.  Draft t attends to the ctx_lens[b] cached tokens, to itself and to
  * its ancestors: with s_j = scale * <q[b,h,t,:], K[j]> over those,

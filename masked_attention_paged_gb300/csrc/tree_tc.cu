@@ -453,7 +453,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       seg_taken(i);
       const int t_end = p.side ? min(s.t1, s.nct) : s.t1;  // drafts with their own place take no stage
       const int32_t* bt_row = p.bt + static_cast<int64_t>(s.b) * p.bt_stride;
-      auto block_id = [&](int tile) {
+      auto block_id = [&](int tile, bool& want) {
+        want = false;
         if (tile >= t_end || lane >= kWarpBlocks) return -1;
         int blk, end;  // the block, and where the tile's kind of blocks ends
         if (tile >= s.nct) {
@@ -464,14 +465,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           blk = tile * kTileBlocks + place;
           end = (s.ctx + kBS - 1) / kBS;
         }
-        return blk < end ? bt_row[blk] : -1;
+        want = blk < end;
+        return want ? bt_row[blk] : -1;
       };
-      int id_next = block_id(s.t0);
+      bool want_next;
+      int id_next = block_id(s.t0, want_next);
       for (int tile = s.t0; tile < t_end; ++tile, ++j) {
         int id = id_next;
-        id_next = block_id(tile + 1);
-        if (id != -1 && (id < 0 || id >= p.num_blocks)) {
-          report(p.status, kStatusBounds);
+        const bool want = want_next;
+        id_next = block_id(tile + 1, want_next);
+        if (id < 0 || id >= p.num_blocks) {
+          // a table may hold any id here, -1 too; a draft's is the drafts' warps' to
+          // report, who know whether the draft is there
+          if (want && tile < s.nct) report(p.status, kStatusBounds);
           id = -1;
         }
         uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * (kBS * D * 2);
@@ -693,11 +699,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         // parents and block ids set out first, and are put down after the waits
         int up_of[C::kMaxT / NL], blk_of[C::kMaxT / NL];
         const bool append = s.there && p.k_new != nullptr && s.m == 0;
+        const bool placed = append || p.k_new == nullptr;  // the drafts' blocks are written, or read
 #pragma unroll
         for (int x = 0; x < C::kMaxT / NL; ++x) {
           const int t = lt + x * NL;
           up_of[x] = s.there && t < p.T ? p.parents[s.b * p.par_stride + t] : -2;
-          blk_of[x] = append && t < p.T ? p.bt[static_cast<int64_t>(s.b) * p.bt_stride + (s.ctx + t) / kBS] : -1;
+          blk_of[x] =
+              placed && s.there && t < p.T ? p.bt[static_cast<int64_t>(s.b) * p.bt_stride + (s.ctx + t) / kBS] : -1;
         }
         // the masks of two segments before may still be in use
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->mask_empty[mb], ((round >> 1) & 1) ^ 1, abort, p.status));
@@ -716,10 +724,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             const int blk = s.ctx / kBS + lane;
             if (p.k_new == nullptr && s.there && lane < kSide / kBS && blk < (s.ctx + p.T + kBS - 1) / kBS) {
               id = p.bt[static_cast<int64_t>(s.b) * p.bt_stride + blk];
-              if (id < 0 || id >= p.num_blocks) {
-                report(p.status, kStatusBounds);
-                id = -1;
-              }
+              if (id < 0 || id >= p.num_blocks) id = -1;  // reported below, if a draft of it is there
             }
             const int blocks = __popc(__ballot_sync(0xffffffffu, id >= 0));
             if (lane == 0)
@@ -776,14 +781,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
             for (int w = 0; w < C::kWords; ++w) set[t * C::kWords + w] = 0u;
           }
-          // present and to be cached: where
+          // present: where it is to be cached
           const int64_t blk = dst_row[t];
           int64_t at = -1;
-          if (up == -1 && append) {
-            if (blk >= 0 && blk < p.num_blocks)
-              at = (blk * p.Hkv + s.g) * kBS + (s.ctx + t) % kBS;
-            else
+          if (up == -1 && placed) {
+            if (blk < 0 || blk >= p.num_blocks)
               report(p.status, kStatusBounds);
+            else if (append)
+              at = (blk * p.Hkv + s.g) * kBS + (s.ctx + t) % kBS;
           }
           dst_row[t] = at;
         }

@@ -9,6 +9,7 @@ import torch
 import masked_attention_paged_gb300 as lib
 
 sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+from test_gpu_11_tree import _make as _tree_inputs, _run as _tree_run  # noqa: E402
 from test_gpu_12_evict import _evict_inputs  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -141,3 +142,50 @@ def test_small_integers_in_a_workspace_are_no_counts():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", _STALE_COUNTS], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "counted" in r.stdout, r.stderr[-2000:]
+
+
+BAD = (-1, -7, "past")  # ids that name no block; -1 is what tables are often filled with
+
+
+def _with(s, b, i, bad):
+    """The inputs with entry i of sequence b's table set to an id that names no block."""
+    bt = s["bt"].clone()
+    bt[b, i] = s["kc"].shape[0] if bad == "past" else bad
+    return dict(s, bt=bt)
+
+
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("T", [6, 40, 70])  # drafts aside, in ring stages, two row tiles
+def test_tree_reports_every_id_that_names_no_block(T, bad):
+    s = _tree_inputs([300, 300, 20], T, 4, 2, 64, seed=40 + T)
+    good = _tree_run(s)
+    # a block in the middle of the context, its last, and one of the drafts alone
+    for i in (3, 18, (300 + T - 1) // 16):
+        o, l, _, _, st = _tree_run(_with(s, 0, i, bad))
+        assert st == 5, (i, st)
+        assert torch.equal(o[1:], good[0][1:]) and torch.equal(l[1:], good[1][1:])
+    assert good[4] == 0
+
+
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("T", [20, 40, 70])
+def test_blocks_of_absent_drafts_alone_need_not_be_there(T, bad):
+    """Shorter trees of a batch: what the table holds past their drafts is no matter, also when the drafts are cached
+    already; the block of a draft that is there is."""
+    s = _tree_inputs([300, 305, 20], T, 4, 2, 64, seed=50 + T)
+    n = int((s["parents"][1] >= -1).sum())
+    assert n == T // 2
+    fresh = _tree_run(s)
+    cached = dict(s, kc=fresh[2], vc=fresh[3])
+    none = dict(k_new=None, v_new=None)
+    want = _tree_run(cached, **none)
+    assert fresh[4] == want[4] == 0
+    last, first_free = (305 + n - 1) // 16, (305 + n + 15) // 16
+    assert first_free <= (305 + T - 1) // 16
+    for inputs, ref, kw in ((s, fresh, {}), (cached, want, none)):
+        o, l, _, _, st = _tree_run(_with(inputs, 1, first_free, bad), **kw)
+        assert st == 0 and torch.equal(o, ref[0]) and torch.equal(l, ref[1])
+        o, l, _, _, st = _tree_run(_with(inputs, 1, last, bad), **kw)
+        assert st == 5
+        for b in (0, 2):
+            assert torch.equal(o[b], ref[0][b]) and torch.equal(l[b], ref[1][b])
