@@ -270,21 +270,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     // segment ahead; warps 0, 1 fill the first tile, 2, 3 the second
     Seg s;
     const int t = warp >> 1, place = warp * kWarpBlocks + lane;  // block of the pair
+    bool want_next = false;  // a key of the sequence is in it
     auto block_id = [&](const Seg& x) {
       const int blk = x.pair * (kPair / kBS) + place;
-      return lane < kWarpBlocks && blk * kBS < x.keys ? p.bt[static_cast<int64_t>(x.b) * p.bt_stride + blk] : -1;
+      want_next = lane < kWarpBlocks && blk * kBS < x.keys;
+      return want_next ? p.bt[static_cast<int64_t>(x.b) * p.bt_stride + blk] : -1;
     };
     int n = t;
     bool more = seg_get(0, s);
     int id_next = more ? block_id(s) : -1;
     for (int i = 0; more; ++i) {
       int id = id_next;
+      const bool want = want_next;
       const int g = s.g;
       seg_taken(i);
       more = seg_get(i + 1, s);
       if (more) id_next = block_id(s);
-      if (id != -1 && (id < 0 || id >= p.num_blocks)) {
-        report(p.status, kStatusBounds);
+      if (id < 0 || id >= p.num_blocks) {  // a table may hold any id, -1 too
+        if (want) report(p.status, kStatusBounds);
         id = -1;
       }
       const int st = n % C::KS;

@@ -10,7 +10,7 @@ import masked_attention_paged_gb300 as lib
 
 sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 from test_gpu_11_tree import _make as _tree_inputs, _run as _tree_run  # noqa: E402
-from test_gpu_12_evict import _evict_inputs  # noqa: E402
+from test_gpu_12_evict import _evict_inputs, _make as _weight_inputs, _run as _weight_run  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -189,3 +189,17 @@ def test_blocks_of_absent_drafts_alone_need_not_be_there(T, bad):
         assert st == 5
         for b in (0, 2):
             assert torch.equal(o[b], ref[0][b]) and torch.equal(l[b], ref[1][b])
+
+
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("T", [1, 50])
+def test_weights_report_every_id_that_names_no_block(T, bad):
+    s = _weight_inputs([400, 20], T, 4, 2, 64, seed=60 + T)
+    good, st = _weight_run(s)
+    assert st == 0
+    for i in (4, (400 + T - 1) // 16):
+        lost = int(s["bt"][0, i])
+        out, st = _weight_run(_with(s, 0, i, bad))
+        keep = torch.arange(good.shape[0], device=DEV) != lost
+        assert st == 5 and torch.equal(out[keep].view(torch.int32), good[keep].view(torch.int32))
+        assert torch.equal(out[lost].view(torch.int32), s["acc"][lost].view(torch.int32))
