@@ -316,21 +316,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kBlk = kBN / 16;
       constexpr int kBlockBytes = 16 * D * 2;
       const int32_t* bt_row = prm.bt + static_cast<int64_t>(b) * prm.bt_stride + kv0 * kBlk;
+      bool want_next = false;  // a key of the CTA's is in it
       auto block_id = [&](int j) {
         const int nb = min(kBlk, (n_keys - (kv0 + j) * kBN + 15) / 16);
-        return (j < nkv && lane < nb) ? bt_row[j * kBlk + lane] : -1;
+        want_next = j < nkv && lane < nb;
+        return want_next ? bt_row[j * kBlk + lane] : -1;
       };
       int id_next = block_id(0);
       for (int j = 0; j < nkv; ++j) {
         const int s = j % C::kStages;
         const uint32_t ph = (j / C::kStages) & 1;
         int id = id_next;
+        const bool want = want_next;
         id_next = block_id(j + 1);
-        if (lane < kBlk && id != -1 && (id < 0 || id >= prm.num_blocks)) {
-          report(prm.status, kStatusBounds);
+        if (id < 0 || id >= prm.num_blocks) {  // a table may hold any id, -1 too
+          if (want) report(prm.status, kStatusBounds);
           id = -1;
         }
-        if (id >= 0 && lane >= kBlk) id = -1;
         const int n_ok = __popc(__ballot_sync(0xffffffffu, id >= 0));
         if (!__all_sync(0xffffffffu, mbar_wait(&bars->k_empty[s], ph ^ 1, abort, prm.status))) break;
         if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[s], n_ok * kBlockBytes);

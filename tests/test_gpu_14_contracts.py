@@ -203,3 +203,29 @@ def test_weights_report_every_id_that_names_no_block(T, bad):
         keep = torch.arange(good.shape[0], device=DEV) != lost
         assert st == 5 and torch.equal(out[keep].view(torch.int32), good[keep].view(torch.int32))
         assert torch.equal(out[lost].view(torch.int32), s["acc"][lost].view(torch.int32))
+
+
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_reports_every_id_that_names_no_block(D, causal, bad):
+    g = torch.Generator().manual_seed(70)
+    nb, mb, T = 60, 25, 40
+    kc, vc = (torch.randn(nb, 2, 16, D, generator=g).bfloat16().to(DEV) for _ in range(2))
+    s = dict(kc=kc, bt=torch.randperm(nb, generator=g)[:2 * mb].to(torch.int32).view(2, mb).to(DEV))
+    q = torch.randn(2, 4, T, D, generator=g).bfloat16().to(DEV)
+    start = torch.tensor([330, 31], dtype=torch.int32, device=DEV)
+    ws = lib.Workspace(256)
+
+    def run(x):
+        ws.reset()
+        out, lse = lib.paged_prefill_attn(q, kc, vc, x["bt"], start, causal=causal, return_lse=True, workspace=ws)
+        return out, lse, ws.status()
+
+    good = run(s)
+    assert good[2] == 0
+    for i in (3, 20, (330 + T - 1) // 16):  # in the context, at its end, in the chunk
+        out, lse, st = run(_with(s, 0, i, bad))
+        assert st == 5, i
+        assert torch.equal(out[1], good[0][1]) and torch.equal(lse[1], good[1][1])
+    assert run(_with(s, 0, 24, bad))[2] == 0  # past the chunk
