@@ -229,3 +229,93 @@ def test_prefill_reports_every_id_that_names_no_block(D, causal, bad):
         assert st == 5, i
         assert torch.equal(out[1], good[0][1]) and torch.equal(lse[1], good[1][1])
     assert run(_with(s, 0, 24, bad))[2] == 0  # past the chunk
+
+
+def _step(q, k, v, kc, vc, acc, bt, dt, lens, parents, path, n, freqs, ws):
+    """One step of a server over its cache: every call of the three groups."""
+    pos = lens[:, None] + torch.arange(q.shape[2], device=DEV, dtype=torch.int32)
+    rq = lib.rope_kv_append(q, k, v, pos, freqs, kc, vc, bt, lens, workspace=ws)
+    cached, _ = lib.paged_tree_attn(rq, kc, vc, bt, lens, parents, return_lse=True, workspace=ws)
+    out, lse = lib.paged_tree_attn(rq, kc, vc, bt, lens, parents, k_new=k, v_new=v, return_lse=True, workspace=ws)
+    lib.kv_tree_accept(kc, vc, bt, lens, path, n, workspace=ws)
+    few = path.shape[1]
+    lib.paged_attn_weights(rq[:, :, :few], lse[:, :, :few].contiguous(), kc, bt, lens, acc, q_lens=n, workspace=ws)
+    new_lens, kept = lib.kv_evict(kc, vc, acc, bt, lens + n, dt, 100, sink=4, recent=20, workspace=ws)
+    return rq, cached, out, lse, new_lens, kept
+
+
+def _step_inputs(seed, blocks, B, Hq, Hkv, T, D, longest):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV).bfloat16()  # noqa: E731
+    mb = (longest + T + 15) // 16
+    perm = torch.randperm(blocks, generator=g, device=DEV).to(torch.int32)
+    lens = torch.randint(1, longest, (B,), generator=g, device=DEV).to(torch.int32)
+    lens[0] = longest
+    size = max(lib.paged_tree_workspace_size(B, Hq, Hkv, T, mb, 16, D),
+               lib.paged_attn_weights_workspace_size(B, Hkv, mb))
+    return dict(q=r(B, Hq, T, D), k=r(B, Hkv, T, D), v=r(B, Hkv, T, D), kc=r(blocks, Hkv, 16, D),
+                vc=r(blocks, Hkv, 16, D), acc=torch.rand(blocks, Hkv, 16, generator=g, device=DEV),
+                bt=perm[:B * mb].view(B, mb), dt=perm[B * mb:B * mb + 7 * B].view(B, 7), lens=lens,
+                parents=torch.tensor([[max(-1, t - 1 - t % 2) for t in range(T)]] * B, dtype=torch.int32, device=DEV),
+                path=torch.tensor([[0, 2, 5, 8]] * B, dtype=torch.int32, device=DEV),
+                n=torch.arange(B, device=DEV, dtype=torch.int32) % 5, freqs=lib.rope_frequencies(D)[0],
+                ws=lib.Workspace(size))
+
+
+def _same(x, y):
+    return torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+
+
+def test_two_steps_at_once():
+    """Two threads, two streams, workspaces and caches of their own: the results of each alone."""
+    import threading
+    inputs = [_step_inputs(seed, 500, 4, 8, 4, T, 64, 900) for seed, T in ((1, 9), (2, 40))]
+    streams = [torch.cuda.Stream() for _ in inputs]
+    want, wrong = [None, None], []
+
+    def go(i, times):
+        try:
+            s = inputs[i]
+            with torch.cuda.stream(streams[i]):
+                for _ in range(times):
+                    x = {k: v.clone() if k in ("kc", "vc", "acc") else v for k, v in s.items()}
+                    got = [t.clone() for t in (*_step(**x), x["kc"], x["vc"], x["acc"])]
+                    if want[i] is None:
+                        want[i] = got
+                    assert all(_same(a, b) for a, b in zip(got, want[i]))
+                assert s["ws"].status() == 0
+        except BaseException as e:
+            wrong.append(e)
+
+    torch.cuda.synchronize()
+    go(0, 1), go(1, 1)
+    threads = [threading.Thread(target=go, args=(i, 40)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+
+
+def test_offsets_past_32_bits():
+    """A cache of 2.3e9 elements, the step in its first blocks and in its last: the same bits."""
+    s = _step_inputs(3, 200, 3, 32, 8, 11, 128, 600)
+    n, few = 140000, 200
+    ends = []
+    big = {c: torch.zeros(n, *s[c].shape[1:], dtype=s[c].dtype, device=DEV) for c in ("kc", "vc", "acc")}
+    assert big["kc"].numel() > 1 << 31
+    for flip in (False, True):
+        for c in big:
+            (big[c][n - few:] if flip else big[c][:few]).copy_(s[c].flip(0) if flip else s[c])
+        at = lambda t: (n - 1 - t).to(torch.int32) if flip else t  # noqa: E731
+        x = dict(s, **big, bt=at(s["bt"]).contiguous(), dt=at(s["dt"]).contiguous())
+        got = [t.clone() for t in _step(**x)]
+        ends.append(got + [(big[c][n - few:].flip(0) if flip else big[c][:few]).clone() for c in big])
+    assert s["ws"].status() == 0
+    assert all(_same(a, b) for a, b in zip(*ends))
+    # a rotation of rows 2^29 elements apart, in place
+    far = torch.zeros(9, (1 << 29) + 64, dtype=torch.bfloat16, device=DEV)[:, -64:][None, None]
+    far.copy_(torch.randn(9, 64, device=DEV))
+    pos, (freqs, _) = torch.arange(9, dtype=torch.int32, device=DEV)[None], lib.rope_frequencies(64)
+    want = lib.rope_apply(far.contiguous(), pos, freqs)
+    assert torch.equal(lib.rope_apply(far, pos, freqs, out=far), want)
