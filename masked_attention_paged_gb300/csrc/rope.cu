@@ -18,7 +18,8 @@
 // of a token), then move rows, 16 elements (two 16-byte vectors of bf16) a
 // thread and step.  16 sequences x 1024 tokens (32 query and 8 KV heads, D =
 // 128): 66 us for 403 MB, 6.1 TB/s, 90 % of the measured copy rate; one token of
-// one sequence 3.2 us and of 64 sequences 3.0 us, a launch and its loads.
+// one sequence 3.2 us and of 64 sequences 3.0 us, a launch and its loads.  Into the
+// INT8 cache 96 us and 4.5: a division an element and a reduction over a row's lanes.
 #include <math.h>
 
 #include <algorithm>
