@@ -262,7 +262,9 @@ def _fresh(make, stream, device):
     if stream is None or device.type != "cuda":
         return make()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        # (of the handle 0, the default stream, an ExternalStream would be a new one)
+        stream = int(stream)
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         return make()
 

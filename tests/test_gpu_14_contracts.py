@@ -319,3 +319,20 @@ def test_offsets_past_32_bits():
     pos, (freqs, _) = torch.arange(9, dtype=torch.int32, device=DEV)[None], lib.rope_frequencies(64)
     want = lib.rope_apply(far.contiguous(), pos, freqs)
     assert torch.equal(lib.rope_apply(far, pos, freqs, out=far), want)
+
+
+def test_the_handle_of_the_default_stream_is_the_default_stream():
+    """What a call allocates and zeroes is ordered before its kernels also when the stream comes as its handle, 0."""
+    here = torch.device(DEV, torch.cuda.current_device())
+    side = torch.cuda.Stream()
+    for stream in (0, torch.cuda.default_stream(), side, side.cuda_stream):
+        handle = getattr(stream, "cuda_stream", stream)
+        with torch.cuda.stream(torch.cuda.Stream()):  # whichever is current
+            assert lib._fresh(lambda: torch.cuda.current_stream().cuda_stream, stream, here) == handle
+    # the zeroes of a workspace would reach it from a stream that nothing orders before the call's
+    s = _weight_inputs([700, 90, 400], 60, 8, 2, 128, seed=80)
+    want, _ = _weight_run(s)
+    for _ in range(50):
+        acc = s["acc"].clone()
+        lib.paged_attn_weights(s["q"], s["lse"], s["kc"], s["bt"], s["start"], acc, scale=s["scale"], stream=0)
+        assert torch.equal(acc.view(torch.int32), want.view(torch.int32))
