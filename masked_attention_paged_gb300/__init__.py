@@ -438,9 +438,9 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_pad_mask: Op
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _fresh(lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device), stream, q.device)
     if lse is None and return_lse:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        lse = _fresh(lambda: torch.empty(q.shape[:3], dtype=torch.float32, device=q.device), stream, q.device)
     if lse is not None:
         _check_f32_buffer(lse, q.shape[0] * q.shape[1] * q.shape[2], "lse")
     mptr, mstride = None, 0
@@ -469,9 +469,9 @@ def attn_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_lens:
         scale = 1.0 / math.sqrt(q.shape[-1])
     _check_int32_vec(key_lens, q.shape[0], "key_lens")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _fresh(lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device), stream, q.device)
     if lse is None and return_lse:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        lse = _fresh(lambda: torch.empty(q.shape[:3], dtype=torch.float32, device=q.device), stream, q.device)
     if lse is not None:
         _check_f32_buffer(lse, q.shape[0] * q.shape[1] * q.shape[2], "lse")
     ws = workspace or _attn_ws(q, k, stream)
@@ -494,7 +494,7 @@ def key_padding_to_additive(key_padding_mask: torch.Tensor, out: Optional[torch.
     _require(kpm.dtype == torch.uint8, f"key_padding_mask must be bool or uint8, got {kpm.dtype}")
     B, Pk = kpm.shape
     if out is None:
-        out = torch.empty(B, Pk, dtype=torch.float32, device=kpm.device)
+        out = _fresh(lambda: torch.empty(B, Pk, dtype=torch.float32, device=kpm.device), stream, kpm.device)
     _require(out.dtype == torch.float32 and out.dim() == 2 and tuple(out.shape) == (B, Pk) and out.stride(1) == 1,
              f"out must be float32 [{B}, {Pk}] with contiguous rows")
     st = lib.attn_key_padding_to_additive(_ptr(kpm, "key_padding_mask"), kpm.stride(0), B, Pk, _ptr(out, "out"),
@@ -510,10 +510,12 @@ def attn_lse_merge(outs: Sequence[torch.Tensor], lses: Sequence[torch.Tensor], o
     n = len(outs)
     _require(n >= 1 and len(lses) == n, f"attn_lse_merge takes n >= 1 outputs and as many LSEs ({n}, {len(lses)})")
     if out is None:
-        out = torch.empty(outs[0].shape, dtype=outs[0].dtype, device=outs[0].device)
+        out = _fresh(lambda: torch.empty(outs[0].shape, dtype=outs[0].dtype, device=outs[0].device),
+                     stream, outs[0].device)
     rows = outs[0].shape[0] * outs[0].shape[1] * outs[0].shape[2]  # B * H * P
     if lse is None:
-        lse = torch.empty(lses[0].shape, dtype=torch.float32, device=outs[0].device)
+        lse = _fresh(lambda: torch.empty(lses[0].shape, dtype=torch.float32, device=outs[0].device),
+                     stream, outs[0].device)
     _check_f32_buffer(lse, rows, "lse")
     for i, l in enumerate(lses):
         _check_f32_buffer(l, rows, f"lses[{i}]")
@@ -558,16 +560,16 @@ def paged_decode_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     _check_block_table(block_table, B)
     _check_int32_vec(ctx_lens, B, "ctx_lens")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _fresh(lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device), stream, q.device)
     if lse is None and return_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = _fresh(lambda: torch.empty((B, Hq), dtype=torch.float32, device=q.device), stream, q.device)
     if lse is not None:
         _check_f32_buffer(lse, B * Hq, "lse")
     max_blocks = block_table.shape[1]
     need = paged_decode_workspace_size(B, Hq, max_blocks, k_cache.shape[2], D)
     ws = workspace
     if ws is None or ws.nbytes < need:
-        ws = Workspace(need, device=q.device)
+        ws = _fresh(lambda: Workspace(need, device=q.device), stream, q.device)
     c = _cache(k_cache, v_cache)
     dq, do = _desc(q), _desc(out)
     st = lib.paged_decode_attn(ctypes.byref(dq), ctypes.byref(c), _ptr(block_table, "block_table"),
@@ -592,16 +594,16 @@ def paged_decode_attn_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.
     _check_block_table(block_table, B)
     _check_int32_vec(pos, B, "pos")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _fresh(lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device), stream, q.device)
     if lse is None and return_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = _fresh(lambda: torch.empty((B, Hq), dtype=torch.float32, device=q.device), stream, q.device)
     if lse is not None:
         _check_f32_buffer(lse, B * Hq, "lse")
     max_blocks = block_table.shape[1]
     need = paged_decode_workspace_size(B, Hq, max_blocks, k_cache.shape[2], D)
     ws = workspace
     if ws is None or ws.nbytes < need:
-        ws = Workspace(need, device=q.device)
+        ws = _fresh(lambda: Workspace(need, device=q.device), stream, q.device)
     c = _cache(k_cache, v_cache)
     dq, dk, dv, do = _desc(q), _desc(k_new), _desc(v_new), _desc(out)
     st = lib.paged_decode_attn_append(ctypes.byref(dq), ctypes.byref(dk), ctypes.byref(dv), ctypes.byref(c),
@@ -629,9 +631,9 @@ def paged_prefill_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     _check_block_table(block_table, B)
     _check_int32_vec(start_pos, B, "start_pos")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _fresh(lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device), stream, q.device)
     if lse is None and return_lse:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+        lse = _fresh(lambda: torch.empty((B, Hq, T), dtype=torch.float32, device=q.device), stream, q.device)
     if lse is not None:
         _check_f32_buffer(lse, B * Hq * T, "lse")
     ws = workspace or _small_ws(q.device, stream)
@@ -694,16 +696,16 @@ def paged_decode_attn_q8(q: torch.Tensor, kq_cache: torch.Tensor, vq_cache: torc
     _check_block_table(block_table, B)
     _check_int32_vec(ctx_lens, B, "ctx_lens")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _fresh(lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device), stream, q.device)
     if lse is None and return_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = _fresh(lambda: torch.empty((B, Hq), dtype=torch.float32, device=q.device), stream, q.device)
     if lse is not None:
         _check_f32_buffer(lse, B * Hq, "lse")
     max_blocks = block_table.shape[1]
     need = paged_decode_workspace_size(B, Hq, max_blocks, kq_cache.shape[2], D)
     ws = workspace
     if ws is None or ws.nbytes < need:
-        ws = Workspace(need, device=q.device)
+        ws = _fresh(lambda: Workspace(need, device=q.device), stream, q.device)
     c = _cache_q8(kq_cache, vq_cache, k_scale, v_scale)
     dq, do = _desc(q), _desc(out)
     st = lib.paged_decode_attn_q8(ctypes.byref(dq), ctypes.byref(c), _ptr(block_table, "block_table"),
@@ -728,16 +730,16 @@ def paged_decode_attn_append_q8(q: torch.Tensor, k_new: torch.Tensor, v_new: tor
     _check_block_table(block_table, B)
     _check_int32_vec(pos, B, "pos")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _fresh(lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device), stream, q.device)
     if lse is None and return_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = _fresh(lambda: torch.empty((B, Hq), dtype=torch.float32, device=q.device), stream, q.device)
     if lse is not None:
         _check_f32_buffer(lse, B * Hq, "lse")
     max_blocks = block_table.shape[1]
     need = paged_decode_workspace_size(B, Hq, max_blocks, kq_cache.shape[2], D)
     ws = workspace
     if ws is None or ws.nbytes < need:
-        ws = Workspace(need, device=q.device)
+        ws = _fresh(lambda: Workspace(need, device=q.device), stream, q.device)
     c = _cache_q8(kq_cache, vq_cache, k_scale, v_scale)
     dq, dk, dv, do = _desc(q), _desc(k_new), _desc(v_new), _desc(out)
     st = lib.paged_decode_attn_append_q8(ctypes.byref(dq), ctypes.byref(dk), ctypes.byref(dv), ctypes.byref(c),
@@ -759,7 +761,8 @@ def paged_kv_gather(cache: torch.Tensor, block_table: torch.Tensor, lens: torch.
     _check_int32_vec(lens, B, "lens")
     _check_block_table(block_table, B)
     if out is None:
-        out = torch.zeros((B, Hkv, max_len, D), dtype=cache.dtype, device=cache.device)
+        out = _fresh(lambda: torch.zeros((B, Hkv, max_len, D), dtype=cache.dtype, device=cache.device),
+                     stream, cache.device)
     _require(out.dtype == cache.dtype and tuple(out.shape) == (B, Hkv, max_len, D) and out.is_contiguous(),
              f"out must be contiguous {cache.dtype} [{B}, {Hkv}, {max_len}, {D}]")
     c = _cache(cache, cache)

@@ -336,3 +336,36 @@ def test_the_handle_of_the_default_stream_is_the_default_stream():
         acc = s["acc"].clone()
         lib.paged_attn_weights(s["q"], s["lse"], s["kc"], s["bt"], s["start"], acc, scale=s["scale"], stream=0)
         assert torch.equal(acc.view(torch.int32), want.view(torch.int32))
+
+
+def test_what_the_older_calls_allocate_belongs_to_their_stream():
+    """The zeroes of a workspace or of the gather's rows, queued on a busy current stream, would land on the results."""
+    g = torch.Generator().manual_seed(90)
+    kc, vc = (torch.randn(200, 2, 16, 128, generator=g).bfloat16().to(DEV) for _ in range(2))
+    bt = torch.randperm(200, generator=g)[:180].to(torch.int32).view(2, 90).to(DEV)
+    lens = torch.tensor([1400, 700], dtype=torch.int32, device=DEV)
+    q = torch.randn(2, 8, 128, generator=g).bfloat16().to(DEV)
+    qp = torch.randn(2, 8, 33, 128, generator=g).bfloat16().to(DEV)
+    kq, sc = torch.randint(-127, 128, kc.shape, generator=g, dtype=torch.int8).to(DEV), torch.rand(200, 2, 16).to(DEV)
+    side = torch.cuda.Stream()
+
+    def chain(stream):
+        kw = dict(stream=stream)
+        out, lse = lib.attn_fwd(qp, qp, qp, **kw)
+        return [out, lse, lib.attn_fwd_varlen(qp, qp, qp, short, **kw)[0],
+                *lib.attn_lse_merge([out, out], [lse, lse], **kw),
+                lib.paged_decode_attn(q, kc, vc, bt, lens, **kw),
+                lib.paged_decode_attn_append(q, q[:, :2], q[:, 2:4], kc, vc, bt, lens, **kw),
+                lib.paged_prefill_attn(qp, kc, vc, bt, lens, **kw),
+                lib.paged_decode_attn_q8(q, kq, kq, sc, sc, bt, lens, **kw),
+                lib.paged_kv_gather(kc, bt, lens, 1400, **kw)]
+
+    short = lens.clamp(max=20)
+    want = [x.clone() for x in chain(None)]
+    chain(side)  # the default workspaces are there
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        torch.cuda._sleep(100_000_000)
+        got = chain(stream)
+        torch.cuda.synchronize()
+        assert all(_same(a, b) for a, b in zip(got, want))
