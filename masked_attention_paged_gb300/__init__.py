@@ -370,8 +370,11 @@ def _default(key, nbytes: int, device, stream) -> Workspace:
             if torch.cuda.is_current_stream_capturing():
                 return ws
             torch.cuda.current_stream(device).synchronize()
-        _default_ws[key] = ws
-        return ws
+        with _lock:  # of two threads that come here at once, one's is kept and both use it
+            kept = _default_ws.get(key)
+            if kept is None or kept.nbytes < nbytes:
+                kept = _default_ws[key] = ws
+        return kept
 
     return _fresh(make, stream, device)
 

@@ -124,3 +124,26 @@ def test_evict_counts_past_32_bits_are_refused(rec, kw):  # noqa: F811
     with pytest.raises(ValueError, match="must be a 32-bit integer"):
         lib.kv_evict(k, k, acc, bt, n, bt, **{"keep": 5, **kw}, stream=0)
     assert not rec.calls
+
+
+def test_two_first_calls_at_once_share_one_default_workspace(rec, monkeypatch):  # noqa: F811
+    """What either notes in the status word is noted for all: neither's workspace is lost."""
+    import threading
+    made, both = lib.Workspace, threading.Barrier(2)
+
+    def slowly(*a, **k):
+        both.wait(20)  # neither is kept before both are made
+        return made(*a, **k)
+
+    monkeypatch.setattr(lib, "Workspace", slowly)
+    got = [None, None]
+
+    def go(i):
+        got[i] = lib._small_ws("cpu")
+
+    threads = [threading.Thread(target=go, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert got[0] is got[1] is lib._small_ws("cpu")
