@@ -1114,9 +1114,8 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
     lib = load()
     B, Hkv = ctx_lens.shape[0], k_cache.shape[1]
     keep, sink, recent = int(keep), int(sink), int(recent)
-    for name, n in (("keep", keep), ("sink", sink), ("recent", recent)):
-        if not -1 << 31 <= n < 1 << 31:  # the C call would see its low 32 bits
-            raise ValueError(f"{name} must be a 32-bit integer, got {n}")
+    if max(keep, sink, recent) >= 1 << 31 or min(keep, sink, recent) < -1 << 31:  # C would see their low 32 bits
+        raise ValueError(f"keep, sink and recent must be 32-bit integers, got {keep}, {sink} and {recent}")
     if new_lens is None:
         new_lens = _fresh(lambda: torch.empty(B, dtype=torch.int32, device=k_cache.device), stream, k_cache.device)
     if kept is None:

@@ -121,7 +121,7 @@ def test_evict_counts_past_32_bits_are_refused(rec, kw):  # noqa: F811
     """Their low 32 bits are counts like any other: no sinks, two recent tokens."""
     k, acc = torch.zeros(9, 2, 16, 128, dtype=torch.bfloat16), torch.zeros(9, 2, 16)
     bt, n = torch.ones(2, 4, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
-    with pytest.raises(ValueError, match="must be a 32-bit integer"):
+    with pytest.raises(ValueError, match="must be 32-bit integers"):
         lib.kv_evict(k, k, acc, bt, n, bt, **{"keep": 5, **kw}, stream=0)
     assert not rec.calls
 
