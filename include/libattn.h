@@ -667,6 +667,201 @@ attn_status kv_evict(const attn_kv_cache *cache, float *acc, const int32_t *bloc
                      int32_t *new_lens, int32_t *kept,
                      void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * draft_verify -- which drafts of a tree the target model keeps, and the token
+ * after them, from given random numbers: the path for kv_tree_accept and the next
+ * step's first token.
+ *
+ * Sequence b's nodes are those of paged_tree_attn: node 0 (parent -1) is the token
+ * chosen last, the others follow a node before them (a parent below -1: absent;
+ * other nodes with parent -1 are never reached).  target_probs[b][t] is the
+ * target's distribution p after node t, draft_probs[b][t] the distribution q that
+ * t's children were drawn from.  From node 0 on, the children of the node where the
+ * sequence stands are tested in index order, child x with its number u:
+ *     r = p, S = 1, Q = 1 at first;
+ *     taken (the sequence stands there from now on) if  u q[x] S < r[x] Q,  else
+ *     r <- max(r - (S / Q) q, 0) for every token,  S <- sum r,
+ *     and without replacement  Q <- Q - q[x].
+ * r = max(p - C q, 0) throughout, with C the sum of the factors S / Q.  Without
+ * replacement (siblings are different tokens) a token that was refused at the node is
+ * not tested again, and none is once Q <= 0.  Without draft_probs the drafts are
+ * taken for certain (q is 1 at x): taken if u S < r[x], else S <- S - r[x] and
+ * r[x] <- 0; a refused token is not tested again.
+ * The next token is drawn from r of the last node: the lowest v with sum_{w <= v}
+ * r[w] > u_0 sum r (the last v with r[v] > 0 if rounding leaves none); if sum r = 0,
+ * p takes r's place.  So the emitted tokens are distributed as the target's
+ * own, whatever the drafts were, when siblings are drawn as `replacement` says.
+ *
+ *   target_probs  [batch, T, V] f32 or bf16 (strided view, rows contiguous)
+ *   draft_probs   the same, or NULL.  Numbers of [0, 1]; a NaN counts as 0.
+ *   tokens        int32, row b at tokens + b * tok_stride_b; node 0's is not read
+ *   parents       int32, row b at parents + b * par_stride_b (0: one tree for all)
+ *   uniforms      float32 of [0, 1), row b at uniforms + b * uni_stride_b: entry t for
+ *                 node t's test, entry 0 for the next token
+ *   path          int32 [batch, T], written: the taken nodes, node 0 first, then -1
+ *   n_accept      int32 [batch], written: their number (node 0 counts)
+ *   next_token    int32 [batch], written
+ * A sequence whose node 0 has a parent below -1 is idle: n_accept 0, next_token -1.
+ * A parent at or past its own index, or the token of a present draft outside [0, V),
+ * sets ATTN_ERR_DEVICE_BOUNDS and counts as absent; so does a row without a positive
+ * entry to draw from (next_token -1).
+ *   workspace     >= draft_verify_workspace_size(...) bytes (the status word)
+ * 1 <= T <= 256, 1 <= V <= 2^30; outputs do not overlap each other or the inputs.  Tests and
+ * sums carry 46 bits or more, so that a result hangs on rounding only where a number
+ * lies within 1e-13 of a border; it does not depend on timing.
+ */
+size_t draft_verify_workspace_size(int32_t batch, int32_t num_drafts, int64_t vocab);
+attn_status draft_verify(const attn_tensor *target_probs, const attn_tensor *draft_probs,
+                         const int32_t *tokens, int64_t tok_stride_b, const int32_t *parents, int64_t par_stride_b,
+                         const float *uniforms, int64_t uni_stride_b, int32_t replacement,
+                         int32_t *path, int32_t *n_accept, int32_t *next_token,
+                         void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Pages with owners.  refs[num_blocks] (int32, device) counts how many table rows
+ * name each block; a block with count 0 is free.  Unused table entries are -1.  The
+ * calls below keep counts, tables and lengths in step, on the device, so that a
+ * captured decode loop can allocate.  New blocks are the lowest free ones, given out
+ * in row order and, in a row, in column order: results do not depend on timing.
+ * Calls on the same pool must be ordered.
+ *   workspace  >= kv_pool_workspace_size(num_blocks, rows) bytes, rows the most rows
+ *              of a call's tables (children for kv_fork); no clearing between calls
+ * num_blocks <= 2^20 (else ATTN_ERR_UNSUPPORTED).
+ */
+size_t kv_pool_workspace_size(int64_t num_blocks, int32_t rows);
+
+/* One tensor of a paged cache (K, V, codes, scales, weights, of any layer): block i
+ * is the block_bytes bytes at data + i * block_bytes. */
+typedef struct attn_pool_tensor {
+    void *data;
+    int64_t block_bytes;
+} attn_pool_tensor;
+
+/* kv_free -- sequences give their blocks back: every entry >= 0 of row b is counted
+ * off refs and set to -1, and ctx_lens[b] becomes -1 (idle).
+ *   done  int32 [batch]: the rows with a non-zero entry; NULL: all rows
+ * An entry >= num_blocks, or a count that is not positive, sets
+ * ATTN_ERR_DEVICE_BOUNDS; the count is left alone.
+ *   workspace >= kv_append_workspace_size() bytes */
+attn_status kv_free(int32_t *refs, int64_t num_blocks, int32_t *block_table, int64_t bt_stride, int32_t max_blocks,
+                    int32_t *ctx_lens, const int32_t *done, int32_t batch,
+                    void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* kv_reserve -- blocks for the next tokens: of row b's entries for the slots
+ * ctx_lens[b] .. ctx_lens[b] + n_new[b] - 1, those that are negative get a new block
+ * (refs 1).  ctx_lens[b] < 0 (idle) or n_new[b] <= 0 leaves the row alone; slots past
+ * the table set ATTN_ERR_DEVICE_BOUNDS and leave it alone too.  When the free blocks
+ * run out the remaining entries stay -1, and the same flag is set. */
+attn_status kv_reserve(int32_t *refs, int64_t num_blocks, int32_t *block_table, int64_t bt_stride,
+                       int32_t max_blocks, const int32_t *ctx_lens, const int32_t *n_new, int32_t batch,
+                       void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* kv_fork -- child j goes on from sequence src[j], L = ctx_lens[src[j]] tokens: its
+ * row names the same L / 16 full blocks (one more owner each), and if L % 16 tokens
+ * are left, a new block (refs 1) with a copy of all of the source's partial block,
+ * in every tensor.  The rest of its row is -1, child_lens[j] = L.  src[j] < 0, or an
+ * idle source: an idle child (length -1, row -1).  A src[j] >= batch, a context past
+ * either table, a block id outside the pool, or no free block left: the same, with
+ * ATTN_ERR_DEVICE_BOUNDS.  The children's rows are overwritten without being given
+ * back (kv_free them first).
+ *   tensors      n_tensors <= 256 of them (host array)
+ *   child_table  int32 [children, child_blocks] (row stride child_stride); overlaps
+ *                neither block_table nor the other arguments */
+attn_status kv_fork(int32_t n_tensors, const attn_pool_tensor *tensors, int32_t *refs, int64_t num_blocks,
+                    const int32_t *block_table, int64_t bt_stride, int32_t max_blocks, const int32_t *ctx_lens,
+                    int32_t batch, const int32_t *src, int32_t *child_table, int64_t child_stride,
+                    int32_t child_blocks, int32_t *child_lens, int32_t children,
+                    void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* kv_compact -- the blocks in use move to the front of the pool: of U blocks with
+ * refs != 0, those at or past U move, in order, to the free places below U; counts
+ * and table entries follow.  used[0] = U is written; blocks U .. num_blocks - 1 are
+ * free afterwards (their bytes stay).  The table names every block in use as often
+ * as refs says; an entry that names a free block at or past U, or one outside the
+ * pool, sets ATTN_ERR_DEVICE_BOUNDS and stays. */
+attn_status kv_compact(int32_t n_tensors, const attn_pool_tensor *tensors, int32_t *refs, int64_t num_blocks,
+                       int32_t *block_table, int64_t bt_stride, int32_t max_blocks, int32_t batch, int32_t *used,
+                       void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * An 8-bit floating-point paged KV cache.  K and V codes [num_blocks, num_kv_heads,
+ * block_size, head_dim] e4m3 (4 exponent bits, 3 of fraction, no infinities, largest
+ * 448; contiguous, 16-byte aligned), and one float32 scale per (block, KV head) of K
+ * and of V, [num_blocks, num_kv_heads] (contiguous): a row's value is code * scale.
+ * Scales are powers of two (or 0 for a block of zeros), so that a value is exact in
+ * bf16, and a scale that grows leaves the codes' fractions as they are.
+ */
+typedef struct attn_kv_cache_f8 {
+    void *k;
+    void *v;
+    float *k_scale;
+    float *v_scale;
+    int64_t num_blocks;
+    int32_t block_size;   /* 16 */
+    int32_t num_kv_heads;
+    int32_t head_dim;     /* 64 or 128 */
+    int32_t reserved;     /* 0 */
+} attn_kv_cache_f8;
+
+/*
+ * kv_append_f8 -- write T new tokens of K and V per sequence, token i to slot
+ * start_pos[b] + i.  For every block that gets some, and K and V on their own: with
+ * a the largest finite |x| of the new rows in the block (of a KV head),
+ *     scale = the smallest 2^e >= a / 448 (e >= -126; 0 if a = 0), and not below the
+ *             block's present scale if the block holds older tokens (slots before
+ *             start_pos[b]; a block whose first slot is written begins anew)
+ *     code  = x / scale rounded to nearest, ties to even, +-448 at most (NaN: NaN)
+ * and, if the scale grew, the older codes c become c * (old / new), rounded alike
+ * (exact unless it falls below 2^-6).  Slots past the new tokens are left as they
+ * are.
+ *   k_new, v_new [batch, num_kv_heads, T, head_dim] bf16 (strided views, 16-byte
+ *                aligned rows)
+ *   start_pos    int32 [batch]; < 0: an idle sequence
+ *   lens         int32 [batch]: new tokens of each sequence (clamped to [0, T]), or
+ *                NULL (T)
+ * start_pos[b] + lens[b] past the table sets ATTN_ERR_DEVICE_BOUNDS and writes
+ * nothing for the sequence; a bad block id sets it and leaves that block's rows out.
+ * Blocks that are written must not be shared between sequences.
+ *   workspace >= kv_append_workspace_size() bytes (the status word)
+ */
+attn_status kv_append_f8(const attn_kv_cache_f8 *cache, const int32_t *block_table, int64_t bt_stride,
+                         int32_t max_blocks, const int32_t *start_pos, const int32_t *lens,
+                         const attn_tensor *k_new, const attn_tensor *v_new,
+                         void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * paged_attn_f8 -- attention of T query tokens per sequence over an e4m3 cache, from
+ * one (a decode step) to a long chunk (a prompt), whose keys are in the cache.
+ *
+ * Sequence b has n = lens[b] queries (clamped to [0, T]; T without lens), query i at
+ * position start_pos[b] + i.  With g = h / (Hq / Hkv):
+ *     s_t = scale * <q[b,h,i,:], K[t]>,  t <= start_pos[b] + i      (causal = 1)
+ *                                        t <  start_pos[b] + n      (causal = 0)
+ *     out[b,h,i,:] = sum_t softmax(s)_t V[t],  lse[b,h,i] = log sum_t exp(s_t).
+ * Rows i >= n, and those of an idle sequence (start_pos[b] < 0), are out = 0, lse =
+ * -inf.  What slots past the last key hold (NaN codes too) does not reach a result.
+ * start_pos[b] + n past the table sets ATTN_ERR_DEVICE_BOUNDS and counts as idle; a
+ * bad block id sets it and is left out: the sequence's result must be discarded.
+ *
+ *   q, out     [batch, Hq, T, head_dim]; q bf16, out bf16 or f32 (strided views,
+ *              16-byte aligned rows, no stride 0; out must not overlap q)
+ *   lse        float32 [batch, Hq, T] contiguous, or NULL
+ *   workspace  >= paged_attn_f8_workspace_size(...) bytes on the current device:
+ *              partial rows of what is split between SMs, and counts; no clearing
+ *              between calls.  Calls that share a workspace must not overlap on the
+ *              GPU.
+ * Hq / Hkv <= 128.  Products on the tensor cores with fp32 accumulation: codes enter
+ * exactly, q to 2^-19 of its row's largest element or better, the softmax weights
+ * rounded to fp16 (bf16 for more than 16 query rows per KV head).  Results do not
+ * depend on timing.
+ */
+size_t paged_attn_f8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t num_queries,
+                                    int32_t max_blocks, int32_t block_size, int32_t head_dim);
+attn_status paged_attn_f8(const attn_tensor *q, const attn_kv_cache_f8 *cache, const int32_t *block_table,
+                          int64_t bt_stride, int32_t max_blocks, const int32_t *start_pos, const int32_t *lens,
+                          int32_t causal, float scale, const attn_tensor *out, float *lse,
+                          void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Test/debug export: gather the paged cache of every (sequence, KV head) into
  * contiguous dst [batch, num_kv_heads, max_len, head_dim] (bf16), tokens
  * t < lens[b]; rows t >= lens[b] are left untouched.  Bit-exact.

@@ -31,6 +31,9 @@ __all__ = [
     "rope_frequencies", "rope_apply", "rope_kv_append", "rope_kv_append_q8",
     "paged_tree_workspace_size", "paged_tree_attn", "kv_tree_accept",
     "paged_attn_weights_workspace_size", "paged_attn_weights", "kv_evict",
+    "draft_verify_workspace_size", "draft_verify",
+    "kv_pool_workspace_size", "kv_free", "kv_reserve", "kv_fork", "kv_compact",
+    "kv_append_f8", "paged_attn_f8_workspace_size", "paged_attn_f8",
 ]
 
 ATTN_F32, ATTN_BF16 = 0, 1
@@ -59,6 +62,14 @@ class AttnKVCacheQ8(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int64), ("block_size", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AttnPoolTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("block_bytes", ctypes.c_int64)]
+
+
+class AttnKVCacheF8(ctypes.Structure):
+    _fields_ = AttnKVCacheQ8._fields_
 
 
 def _signatures() -> dict:
@@ -98,6 +109,16 @@ def _signatures() -> dict:
         "paged_attn_weights_workspace_size": (SZ, [I32, I32, I32, I32]),
         "paged_attn_weights": (I32, [P, P, P, P, I64, I32, P, P, I32, F, P, P, SZ, P]),
         "kv_evict": (I32, [P, P, P, I64, I32, P, P, I64, I32, I32, I32, I32, I32, P, P, P, SZ, P]),
+        "draft_verify_workspace_size": (SZ, [I32, I32, I64]),
+        "draft_verify": (I32, [P, P, P, I64, P, I64, P, I64, I32, P, P, P, P, SZ, P]),
+        "kv_pool_workspace_size": (SZ, [I64, I32]),
+        "kv_free": (I32, [P, I64, P, I64, I32, P, P, I32, P, SZ, P]),
+        "kv_reserve": (I32, [P, I64, P, I64, I32, P, P, I32, P, SZ, P]),
+        "kv_fork": (I32, [I32, P, P, I64, P, I64, I32, P, I32, P, P, I64, I32, P, I32, P, SZ, P]),
+        "kv_compact": (I32, [I32, P, P, I64, P, I64, I32, I32, P, P, SZ, P]),
+        "kv_append_f8": (I32, [P, P, I64, I32, P, P, P, P, P, SZ, P]),
+        "paged_attn_f8_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32, I32]),
+        "paged_attn_f8": (I32, [P, P, P, I64, I32, P, P, I32, F, P, P, P, SZ, P]),
         "attn_check_device_status": (I32, [P, ctypes.POINTER(ctypes.c_uint32), P]),
         "attn_reset_device_status": (I32, [P, P]),
         "attn_selftest_wait_timeout": (I32, [P, SZ, ctypes.c_uint32, P]),
@@ -145,7 +166,9 @@ def exported_symbols() -> list[str]:
             "attn_fwd_workspace_size_for", "kv_append_q8", "paged_decode_attn_q8", "paged_decode_attn_append_q8",
             "attn_rope_frequencies", "rope_apply", "rope_kv_append", "rope_kv_append_q8",
             "paged_tree_workspace_size", "paged_tree_attn", "kv_tree_accept",
-            "paged_attn_weights_workspace_size", "paged_attn_weights", "kv_evict"]
+            "paged_attn_weights_workspace_size", "paged_attn_weights", "kv_evict",
+            "draft_verify_workspace_size", "draft_verify", "kv_pool_workspace_size", "kv_free", "kv_reserve",
+            "kv_fork", "kv_compact", "kv_append_f8", "paged_attn_f8_workspace_size", "paged_attn_f8"]
 
 
 # --------------------------------------------------------------------------
@@ -1146,3 +1169,285 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, bl
                       _ptr(new_lens, "new_lens"), _ptr(kept, "kept"), _ws_ptr(ws), ws.nbytes, _stream(stream))
     _check("kv_evict", st)
     return new_lens, kept
+
+
+# --------------------------------------------------------------------------
+# which drafts the target keeps
+# --------------------------------------------------------------------------
+def draft_verify_workspace_size(batch: int, num_drafts: int, vocab: int) -> int:
+    return int(load().draft_verify_workspace_size(batch, num_drafts, vocab))
+
+
+def _check_probs(t: torch.Tensor, name: str):
+    if not (isinstance(t, torch.Tensor) and t.dtype in _DTYPE_CODES and t.dim() == 3):
+        raise ValueError(f"{name} must be float32 or bfloat16 [B, T, V]")
+
+
+def draft_verify(target_probs: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor, uniforms: torch.Tensor,
+                 draft_probs: Optional[torch.Tensor] = None, replacement: bool = False,
+                 path: Optional[torch.Tensor] = None, n_accept: Optional[torch.Tensor] = None,
+                 next_token: Optional[torch.Tensor] = None, workspace: Optional[Workspace] = None, stream=None):
+    """Go down a tree of drafted tokens (int32 [B, T] tokens and parents, node 0
+    the token chosen last) as far as the target's probabilities (float32 or bf16
+    [B, T, V], row t after node t) and the given random numbers (float32 [B, T]
+    of [0, 1): entry t tests node t, entry 0 draws the next token) take it.
+    draft_probs: the distributions that the children of each node were drawn
+    from, with `replacement` or (siblings all different) without; None: the
+    drafts are certain.  Returns (path int32 [B, T]: the nodes kept, -1 past them;
+    n_accept int32 [B], node 0 included; next_token int32 [B]): path and n_accept
+    as kv_tree_accept takes them."""
+    lib = load()
+    _check_probs(target_probs, "target_probs")
+    B, T, V = target_probs.shape
+    dev = target_probs.device
+    if path is None:
+        path = _fresh(lambda: torch.empty((B, T), dtype=torch.int32, device=dev), stream, dev)
+    if n_accept is None:
+        n_accept = _fresh(lambda: torch.empty(B, dtype=torch.int32, device=dev), stream, dev)
+    if next_token is None:
+        next_token = _fresh(lambda: torch.empty(B, dtype=torch.int32, device=dev), stream, dev)
+    if draft_probs is not None:
+        _check_probs(draft_probs, "draft_probs")
+    for t, name in ((tokens, "tokens"), (parents, "parents")):
+        _check_int32_rows(t, B, name)
+        if t.shape[1] != T:
+            raise ValueError(f"{name} must be [{B}, {T}], got {tuple(t.shape)}")
+    if not (isinstance(uniforms, torch.Tensor) and uniforms.dtype == torch.float32 and uniforms.shape == (B, T)
+            and (T <= 1 or uniforms.stride(1) == 1)):
+        raise ValueError(f"uniforms must be float32 [{B}, {T}] with contiguous rows")
+    if not (path.dtype == torch.int32 and path.shape == (B, T) and path.is_contiguous()):
+        raise ValueError(f"path must be contiguous int32 [{B}, {T}]")
+    _check_int32_vec(n_accept, B, "n_accept")
+    _check_int32_vec(next_token, B, "next_token")
+    _check_devices("draft_verify", target_probs, draft_probs, tokens, parents, uniforms, path, n_accept, next_token,
+                   _ws_tensor(workspace))
+    ws = workspace or _small_ws(dev, stream)
+    st = lib.draft_verify(_tensor_bytes(target_probs), None if draft_probs is None else _tensor_bytes(draft_probs),
+                          _ptr(tokens, "tokens"), tokens.stride(0), _ptr(parents, "parents"), parents.stride(0),
+                          _ptr(uniforms, "uniforms"), uniforms.stride(0), int(bool(replacement)), _ptr(path, "path"),
+                          _ptr(n_accept, "n_accept"), _ptr(next_token, "next_token"), _ws_ptr(ws), ws.nbytes,
+                          _stream(stream))
+    _check("draft_verify", st)
+    return path, n_accept, next_token
+
+
+# --------------------------------------------------------------------------
+# blocks with owner counts
+# --------------------------------------------------------------------------
+def kv_pool_workspace_size(num_blocks: int, rows: int) -> int:
+    return int(load().kv_pool_workspace_size(num_blocks, rows))
+
+
+def _check_refs(refs: torch.Tensor):
+    if not (isinstance(refs, torch.Tensor) and refs.dtype == torch.int32 and refs.dim() == 1 and refs.is_contiguous()):
+        raise ValueError("refs must be contiguous int32 [num_blocks]")
+
+
+def _check_pool_table(t: torch.Tensor, name: str):
+    """int32 [rows, blocks], rows contiguous and apart: the pool calls write it."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.dim() == 2 and t.stride(1) == 1
+            and t.stride(0) >= t.shape[1]):
+        raise ValueError(f"{name} must be int32 [rows, blocks] with contiguous rows")
+
+
+def _pool_tensors(caches: Sequence[torch.Tensor], num_blocks: int):
+    """The cache tensors whose blocks move, as (array, number)."""
+    arr = (AttnPoolTensor * max(1, len(caches)))()
+    for i, c in enumerate(caches):
+        if not (isinstance(c, torch.Tensor) and c.dim() >= 1 and c.shape[0] == num_blocks and c.is_contiguous()):
+            raise ValueError(f"caches[{i}] must be contiguous with {num_blocks} blocks in its first dimension")
+        arr[i].data = _ptr(c, f"caches[{i}]")
+        arr[i].block_bytes = c.numel() // num_blocks * c.element_size() if num_blocks else 0
+    return ctypes.addressof(arr), len(caches), arr
+
+
+def _pool_ws(workspace, num_blocks, rows, device, stream) -> Workspace:
+    if workspace is not None:
+        return workspace
+    need = kv_pool_workspace_size(num_blocks, rows)
+    return _fresh(lambda: Workspace(need, device=device), stream, device)
+
+
+def kv_free(refs: torch.Tensor, block_table: torch.Tensor, ctx_lens: torch.Tensor,
+            done: Optional[torch.Tensor] = None, workspace: Optional[Workspace] = None, stream=None):
+    """Give back the blocks of the rows with done[b] != 0 (int32 [B]; None: all):
+    each entry is counted off refs (int32 [num_blocks]) and becomes -1, and the
+    row's ctx_lens entry becomes -1 (idle)."""
+    lib = load()
+    _check_refs(refs)
+    _check_pool_table(block_table, "block_table")
+    B = block_table.shape[0]
+    _check_int32_vec(ctx_lens, B, "ctx_lens")
+    if done is not None:
+        _check_int32_vec(done, B, "done")
+    _check_devices("kv_free", refs, block_table, ctx_lens, done, _ws_tensor(workspace))
+    ws = workspace or _small_ws(refs.device, stream)
+    st = lib.kv_free(_ptr(refs, "refs"), refs.shape[0], _ptr(block_table, "block_table"), block_table.stride(0),
+                     block_table.shape[1], _ptr(ctx_lens, "ctx_lens"), _ptr(done, "done"), B, _ws_ptr(ws), ws.nbytes,
+                     _stream(stream))
+    _check("kv_free", st)
+
+
+def kv_reserve(refs: torch.Tensor, block_table: torch.Tensor, ctx_lens: torch.Tensor, n_new: torch.Tensor,
+               workspace: Optional[Workspace] = None, stream=None):
+    """Give every row the blocks that its next n_new[b] tokens (int32 [B]) need
+    and it does not have: the lowest free ones, in row order."""
+    lib = load()
+    _check_refs(refs)
+    _check_pool_table(block_table, "block_table")
+    B = block_table.shape[0]
+    _check_int32_vec(ctx_lens, B, "ctx_lens")
+    _check_int32_vec(n_new, B, "n_new")
+    _check_devices("kv_reserve", refs, block_table, ctx_lens, n_new, _ws_tensor(workspace))
+    ws = _pool_ws(workspace, refs.shape[0], B, refs.device, stream)
+    st = lib.kv_reserve(_ptr(refs, "refs"), refs.shape[0], _ptr(block_table, "block_table"), block_table.stride(0),
+                        block_table.shape[1], _ptr(ctx_lens, "ctx_lens"), _ptr(n_new, "n_new"), B, _ws_ptr(ws),
+                        ws.nbytes, _stream(stream))
+    _check("kv_reserve", st)
+
+
+def kv_fork(caches: Sequence[torch.Tensor], refs: torch.Tensor, block_table: torch.Tensor, ctx_lens: torch.Tensor,
+            src: torch.Tensor, child_table: torch.Tensor, child_lens: torch.Tensor,
+            workspace: Optional[Workspace] = None, stream=None):
+    """Child j (a row of child_table, written in full, and child_lens[j]) goes on
+    from sequence src[j] (int32 [children], < 0: idle): it shares the source's full
+    blocks and gets a copy of its partial one, in every tensor of caches (any types,
+    each contiguous [num_blocks, ...], K and V of all layers at once)."""
+    lib = load()
+    _check_refs(refs)
+    _check_block_table(block_table, 0)
+    _check_pool_table(child_table, "child_table")
+    B, C = block_table.shape[0], child_table.shape[0]
+    _check_int32_vec(ctx_lens, B, "ctx_lens")
+    _check_int32_vec(src, C, "src")
+    _check_int32_vec(child_lens, C, "child_lens")
+    at, n, keep = _pool_tensors(caches, refs.shape[0])
+    _check_devices("kv_fork", *caches, refs, block_table, ctx_lens, src, child_table, child_lens,
+                   _ws_tensor(workspace))
+    ws = _pool_ws(workspace, refs.shape[0], C, refs.device, stream)
+    st = lib.kv_fork(n, at, _ptr(refs, "refs"), refs.shape[0], _ptr(block_table, "block_table"),
+                     block_table.stride(0), block_table.shape[1], _ptr(ctx_lens, "ctx_lens"), B, _ptr(src, "src"),
+                     _ptr(child_table, "child_table"), child_table.stride(0), child_table.shape[1],
+                     _ptr(child_lens, "child_lens"), C, _ws_ptr(ws), ws.nbytes, _stream(stream))
+    _check("kv_fork", st)
+
+
+def kv_compact(caches: Sequence[torch.Tensor], refs: torch.Tensor, block_table: torch.Tensor,
+               used: Optional[torch.Tensor] = None, workspace: Optional[Workspace] = None, stream=None):
+    """Move the blocks in use to the front of the pool, in every tensor of caches
+    (as kv_fork), with their counts and the table's entries.  Returns used (int32
+    [1]): how many there are; all later blocks are free."""
+    lib = load()
+    _check_refs(refs)
+    _check_pool_table(block_table, "block_table")
+    if used is None:
+        used = _fresh(lambda: torch.empty(1, dtype=torch.int32, device=refs.device), stream, refs.device)
+    _check_int32_vec(used, 1, "used")
+    at, n, keep = _pool_tensors(caches, refs.shape[0])
+    _check_devices("kv_compact", *caches, refs, block_table, used, _ws_tensor(workspace))
+    ws = _pool_ws(workspace, refs.shape[0], 0, refs.device, stream)
+    st = lib.kv_compact(n, at, _ptr(refs, "refs"), refs.shape[0], _ptr(block_table, "block_table"),
+                        block_table.stride(0), block_table.shape[1], block_table.shape[0], _ptr(used, "used"),
+                        _ws_ptr(ws), ws.nbytes, _stream(stream))
+    _check("kv_compact", st)
+    return used
+
+
+# --------------------------------------------------------------------------
+# a cache in e4m3, one scale per block and head
+# --------------------------------------------------------------------------
+def _cache_f8(kq: torch.Tensor, vq: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor) -> bytes:
+    """The AttnKVCacheF8 of four tensors, as bytes."""
+    if not (kq.dtype == torch.float8_e4m3fn and vq.dtype == torch.float8_e4m3fn):
+        raise ValueError("e4m3 caches must be float8_e4m3fn")
+    if not (kq.dim() == 4 and kq.shape == vq.shape):
+        raise ValueError("e4m3 caches must be [num_blocks, Hkv, block_size, D], K and V alike")
+    if not (k_scale.dtype == torch.float32 and v_scale.dtype == torch.float32 and k_scale.shape == kq.shape[:2]
+            and v_scale.shape == kq.shape[:2]):
+        raise ValueError(f"block scales must be float32 {tuple(kq.shape[:2])}")
+    for t in (kq, vq, k_scale, v_scale):
+        if not (t.is_contiguous() and _on_device(t)):
+            raise ValueError("e4m3 caches and scales must be contiguous CUDA tensors")
+    c = AttnKVCacheF8()
+    c.k, c.v, c.k_scale, c.v_scale = kq.data_ptr(), vq.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()
+    c.num_blocks, c.num_kv_heads, c.block_size, c.head_dim = kq.shape
+    return bytes(c)
+
+
+def kv_append_f8(kq_cache: torch.Tensor, vq_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                 block_table: torch.Tensor, start_pos: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                 lens: Optional[torch.Tensor] = None, workspace: Optional[Workspace] = None, stream=None):
+    """Write T new tokens a sequence (k_new, v_new bf16 [B, Hkv, T, D], or [B, Hkv,
+    D] for one) at slots start_pos[b] + i of an e4m3 cache (codes float8_e4m3fn [N,
+    Hkv, 16, D], scales float32 [N, Hkv], powers of two): a block whose new rows need
+    a larger scale gets it, and its older codes are rounded again.  lens int32 [B]:
+    new tokens of each sequence."""
+    lib = load()
+    c = _cache_f8(kq_cache, vq_cache, k_scale, v_scale)
+    if k_new.dim() == 3:
+        k_new, v_new = _one_token(k_new, v_new)
+    if not (k_new.dim() == 4 and v_new.dim() == 4):
+        raise ValueError(f"k_new and v_new must be [B, Hkv, T, D] or [B, Hkv, D], got {tuple(k_new.shape)}")
+    B = k_new.shape[0]
+    _check_block_table(block_table, B)
+    _check_int32_vec(start_pos, B, "start_pos")
+    if lens is not None:
+        _check_int32_vec(lens, B, "lens")
+    _check_devices("kv_append_f8", kq_cache, vq_cache, k_scale, v_scale, block_table, start_pos, k_new, v_new, lens,
+                   _ws_tensor(workspace))
+    ws = workspace or _small_ws(kq_cache.device, stream)
+    st = lib.kv_append_f8(c, _ptr(block_table, "block_table"), block_table.stride(0), block_table.shape[1],
+                          _ptr(start_pos, "start_pos"), _ptr(lens, "lens"), _tensor_bytes(k_new), _tensor_bytes(v_new),
+                          _ws_ptr(ws), ws.nbytes, _stream(stream))
+    _check("kv_append_f8", st)
+
+
+def paged_attn_f8_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, num_queries: int, max_blocks: int,
+                                 block_size: int = 16, head_dim: int = 128) -> int:
+    return int(load().paged_attn_f8_workspace_size(batch, num_q_heads, num_kv_heads, num_queries, max_blocks,
+                                                   block_size, head_dim))
+
+
+def paged_attn_f8(q: torch.Tensor, kq_cache: torch.Tensor, vq_cache: torch.Tensor, k_scale: torch.Tensor,
+                  v_scale: torch.Tensor, block_table: torch.Tensor, start_pos: torch.Tensor,
+                  lens: Optional[torch.Tensor] = None, causal: bool = True, scale: Optional[float] = None,
+                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, return_lse: bool = False,
+                  workspace: Optional[Workspace] = None, stream=None):
+    """Attention over an e4m3 cache (as kv_append_f8): q [B, Hq, T, D] at positions
+    start_pos[b] + i, whose keys are in the cache (causal: up to its own); [B, Hq,
+    D] for one token a sequence.  lens int32 [B]: queries of each sequence (the
+    others' rows are 0, their LSE -inf)."""
+    lib = load()
+    full = q.dim() == 4
+    if not full and q.dim() != 3:
+        raise ValueError(f"q must be [B, Hq, T, D] or [B, Hq, D], got {tuple(q.shape)}")
+    B, Hq, D = q.shape[0], q.shape[1], q.shape[-1]
+    T = q.shape[2] if full else 1
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = _fresh(lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device), stream, q.device)
+    elif out.shape != q.shape:
+        raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
+    if lse is None and return_lse:
+        lse = _fresh(lambda: torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device), stream, q.device)
+    if lse is not None:
+        _check_f32_buffer(lse, B * Hq * T, "lse")
+    c = _cache_f8(kq_cache, vq_cache, k_scale, v_scale)
+    _check_block_table(block_table, B)
+    _check_int32_vec(start_pos, B, "start_pos")
+    if lens is not None:
+        _check_int32_vec(lens, B, "lens")
+    _check_devices("paged_attn_f8", q, kq_cache, vq_cache, k_scale, v_scale, block_table, start_pos, lens, out, lse,
+                   _ws_tensor(workspace))
+    max_blocks = block_table.shape[1]
+    ws = workspace
+    if ws is None:
+        need = paged_attn_f8_workspace_size(B, Hq, kq_cache.shape[1], T, max_blocks, kq_cache.shape[2], D)
+        ws = _fresh(lambda: Workspace(need, device=q.device), stream, q.device)
+    q4, o4 = (q, out) if full else _one_token(q, out)
+    st = lib.paged_attn_f8(_tensor_bytes(q4), c, _ptr(block_table, "block_table"), block_table.stride(0), max_blocks,
+                           _ptr(start_pos, "start_pos"), _ptr(lens, "lens"), int(bool(causal)), float(scale),
+                           _tensor_bytes(o4), _ptr(lse, "lse"), _ws_ptr(ws), ws.nbytes, _stream(stream))
+    _check("paged_attn_f8", st)
+    return (out, lse) if return_lse else out

@@ -883,6 +883,300 @@ attn_status kv_evict(const attn_kv_cache* cache, float* acc, const int32_t* bloc
   return from_cuda(launch_kv_evict(a, stream));
 }
 
+// ---------------------------------------------------------------------------
+// draft verification
+// ---------------------------------------------------------------------------
+size_t draft_verify_workspace_size(int32_t batch, int32_t num_drafts, int64_t vocab) {
+  return batch < 0 || num_drafts < 0 || vocab < 0 ? 0 : kStatusBytes;
+}
+
+attn_status draft_verify(const attn_tensor* target_probs, const attn_tensor* draft_probs, const int32_t* tokens,
+                         int64_t tok_stride_b, const int32_t* parents, int64_t par_stride_b, const float* uniforms,
+                         int64_t uni_stride_b, int32_t replacement, int32_t* path, int32_t* n_accept,
+                         int32_t* next_token, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  attn_status st;
+  if ((st = check_tensor(target_probs, 3)) != ATTN_OK) return st;
+  const int64_t B = target_probs->shape[0], T = target_probs->shape[1], V = target_probs->shape[2];
+  if (draft_probs != nullptr) {
+    if ((st = check_tensor(draft_probs, 3)) != ATTN_OK) return st;
+    for (int i = 0; i < 3; ++i)
+      if (draft_probs->shape[i] != target_probs->shape[i]) return ATTN_ERR_INVALID_ARG;
+    if (draft_probs->dtype != target_probs->dtype) return ATTN_ERR_INVALID_ARG;
+  }
+  if (T < 1 || V < 1) return ATTN_ERR_INVALID_ARG;
+  if (T > kVerifyMaxDrafts || V > (1 << 30) || B > 65535) return ATTN_ERR_UNSUPPORTED;
+  if ((st = check_workspace(workspace, workspace_bytes, kStatusBytes)) != ATTN_OK) return st;
+  if (B == 0) return ATTN_OK;
+  if (tokens == nullptr || parents == nullptr || uniforms == nullptr || path == nullptr || n_accept == nullptr ||
+      next_token == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  if (B > 1 && (tok_stride_b < T || (par_stride_b != 0 && par_stride_b < T) || uni_stride_b < T))
+    return ATTN_ERR_INVALID_ARG;
+  const int eb = elem_bytes(target_probs->dtype);
+  if (!aligned(target_probs->data, eb) || (draft_probs != nullptr && !aligned(draft_probs->data, eb)))
+    return ATTN_ERR_INVALID_ARG;
+  const struct {
+    const void* at;
+    int64_t bytes;
+  } outs[3] = {{path, 4 * B * T}, {n_accept, 4 * B}, {next_token, 4 * B}},
+    ins[3] = {{tokens, 4 * ((B - 1) * tok_stride_b + T)},
+              {parents, 4 * ((B - 1) * par_stride_b + T)},
+              {uniforms, 4 * ((B - 1) * uni_stride_b + T)}};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i].at, outs[i].bytes, outs[j].at, outs[j].bytes)) return ATTN_ERR_INVALID_ARG;
+    for (int j = 0; j < 3; ++j)
+      if (overlap(outs[i].at, outs[i].bytes, ins[j].at, ins[j].bytes)) return ATTN_ERR_INVALID_ARG;
+  }
+  VerifyArgs a;
+  a.p = view(target_probs);
+  a.q = draft_probs != nullptr ? view(draft_probs) : View4{};
+  a.tokens = tokens;
+  a.tok_stride = tok_stride_b;
+  a.parents = parents;
+  a.par_stride = par_stride_b;
+  a.uniforms = uniforms;
+  a.uni_stride = uni_stride_b;
+  a.replacement = replacement != 0;
+  a.B = B;
+  a.T = T;
+  a.V = V;
+  a.path = path;
+  a.n_accept = n_accept;
+  a.next = next_token;
+  a.status = static_cast<uint32_t*>(workspace);
+  if (device_sm_count() <= 0) return ATTN_ERR_CUDA;
+  return from_cuda(launch_draft_verify(a, stream));
+}
+
+// ---------------------------------------------------------------------------
+// pools of blocks with owner counts
+// ---------------------------------------------------------------------------
+size_t kv_pool_workspace_size(int64_t num_blocks, int32_t rows) {
+  if (num_blocks < 0 || num_blocks > kPoolMaxBlocks || rows < 0) return 0;
+  return kStatusBytes + pool_workspace_bytes(num_blocks, rows);
+}
+
+// What every pool call checks; `need` bytes of workspace.
+static attn_status check_pool(PoolArgs& a, int32_t n_tensors, const attn_pool_tensor* tensors, int32_t* refs,
+                              int64_t num_blocks, int32_t* table, int64_t stride, int32_t max_blocks, int32_t* lens,
+                              int32_t batch, void* workspace, size_t workspace_bytes, size_t need) {
+  if (num_blocks <= 0 || batch < 0 || max_blocks <= 0 || max_blocks > (1 << 24) || n_tensors < 0 ||
+      (n_tensors > 0 && tensors == nullptr))
+    return ATTN_ERR_INVALID_ARG;
+  if (num_blocks > kPoolMaxBlocks || batch > 65535 || n_tensors > kPoolMaxTensors) return ATTN_ERR_UNSUPPORTED;
+  for (int i = 0; i < n_tensors; ++i) {
+    if (tensors[i].data == nullptr || tensors[i].block_bytes <= 0) return ATTN_ERR_INVALID_ARG;
+    if (tensors[i].block_bytes > (int64_t(1) << 36)) return ATTN_ERR_UNSUPPORTED;
+  }
+  const attn_status st = check_workspace(workspace, workspace_bytes, need);
+  if (st != ATTN_OK) return st;
+  if (refs == nullptr || (batch > 0 && table == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (batch > 1 && stride < max_blocks) return ATTN_ERR_INVALID_ARG;
+  a.n_tensors = n_tensors;
+  a.tensors = tensors;
+  a.refs = refs;
+  a.num_blocks = num_blocks;
+  a.block_table = table;
+  a.bt_stride = stride;
+  a.max_blocks = max_blocks;
+  a.ctx_lens = lens;
+  a.batch = batch;
+  a.scratch = static_cast<uint8_t*>(workspace) + kStatusBytes;
+  a.status = static_cast<uint32_t*>(workspace);
+  return ATTN_OK;
+}
+
+attn_status kv_free(int32_t* refs, int64_t num_blocks, int32_t* block_table, int64_t bt_stride, int32_t max_blocks,
+                    int32_t* ctx_lens, const int32_t* done, int32_t batch, void* workspace, size_t workspace_bytes,
+                    cudaStream_t stream) {
+  PoolArgs a;
+  const attn_status st = check_pool(a, 0, nullptr, refs, num_blocks, block_table, bt_stride, max_blocks, ctx_lens,
+                                    batch, workspace, workspace_bytes, kStatusBytes);
+  if (st != ATTN_OK || batch == 0) return st;
+  if (ctx_lens == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (done != nullptr && overlap(done, 4 * static_cast<int64_t>(batch), ctx_lens, 4 * static_cast<int64_t>(batch)))
+    return ATTN_ERR_INVALID_ARG;
+  return from_cuda(launch_kv_free(a, done, stream));
+}
+
+attn_status kv_reserve(int32_t* refs, int64_t num_blocks, int32_t* block_table, int64_t bt_stride, int32_t max_blocks,
+                       const int32_t* ctx_lens, const int32_t* n_new, int32_t batch, void* workspace,
+                       size_t workspace_bytes, cudaStream_t stream) {
+  PoolArgs a;
+  const attn_status st =
+      check_pool(a, 0, nullptr, refs, num_blocks, block_table, bt_stride, max_blocks, const_cast<int32_t*>(ctx_lens),
+                 batch, workspace, workspace_bytes, kv_pool_workspace_size(num_blocks, batch));
+  if (st != ATTN_OK || batch == 0) return st;
+  if (ctx_lens == nullptr || n_new == nullptr) return ATTN_ERR_INVALID_ARG;
+  return from_cuda(launch_kv_reserve(a, n_new, stream));
+}
+
+attn_status kv_fork(int32_t n_tensors, const attn_pool_tensor* tensors, int32_t* refs, int64_t num_blocks,
+                    const int32_t* block_table, int64_t bt_stride, int32_t max_blocks, const int32_t* ctx_lens,
+                    int32_t batch, const int32_t* src, int32_t* child_table, int64_t child_stride,
+                    int32_t child_blocks, int32_t* child_lens, int32_t children, void* workspace,
+                    size_t workspace_bytes, cudaStream_t stream) {
+  if (children < 0 || child_blocks <= 0 || child_blocks > (1 << 24)) return ATTN_ERR_INVALID_ARG;
+  if (children > 65535) return ATTN_ERR_UNSUPPORTED;
+  PoolArgs a;
+  const attn_status st =
+      check_pool(a, n_tensors, tensors, refs, num_blocks, const_cast<int32_t*>(block_table), bt_stride, max_blocks,
+                 const_cast<int32_t*>(ctx_lens), batch, workspace, workspace_bytes,
+                 kv_pool_workspace_size(num_blocks, children));
+  if (st != ATTN_OK || children == 0) return st;
+  if (src == nullptr || child_table == nullptr || child_lens == nullptr || (batch > 0 && ctx_lens == nullptr))
+    return ATTN_ERR_INVALID_ARG;
+  if (children > 1 && child_stride < child_blocks) return ATTN_ERR_INVALID_ARG;
+  const int64_t table_bytes = 4 * (static_cast<int64_t>(batch > 0 ? batch - 1 : 0) * bt_stride + max_blocks);
+  const int64_t child_bytes = 4 * (static_cast<int64_t>(children - 1) * child_stride + child_blocks);
+  const int64_t lens_bytes = 4 * static_cast<int64_t>(children);
+  if (overlap(child_table, child_bytes, child_lens, lens_bytes) ||
+      overlap(child_table, child_bytes, src, lens_bytes) || overlap(child_lens, lens_bytes, src, lens_bytes))
+    return ATTN_ERR_INVALID_ARG;
+  if (batch > 0 && (overlap(child_table, child_bytes, block_table, table_bytes) ||
+                    overlap(child_lens, lens_bytes, block_table, table_bytes) ||
+                    overlap(child_table, child_bytes, ctx_lens, 4 * static_cast<int64_t>(batch)) ||
+                    overlap(child_lens, lens_bytes, ctx_lens, 4 * static_cast<int64_t>(batch))))
+    return ATTN_ERR_INVALID_ARG;
+  if (device_sm_count() <= 0) return ATTN_ERR_CUDA;
+  return from_cuda(launch_kv_fork(a, src, child_table, child_stride, child_blocks, child_lens, children, stream));
+}
+
+attn_status kv_compact(int32_t n_tensors, const attn_pool_tensor* tensors, int32_t* refs, int64_t num_blocks,
+                       int32_t* block_table, int64_t bt_stride, int32_t max_blocks, int32_t batch, int32_t* used,
+                       void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  PoolArgs a;
+  const attn_status st = check_pool(a, n_tensors, tensors, refs, num_blocks, block_table, bt_stride, max_blocks,
+                                    nullptr, batch, workspace, workspace_bytes, kv_pool_workspace_size(num_blocks, 0));
+  if (st != ATTN_OK) return st;
+  if (used == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (device_sm_count() <= 0) return ATTN_ERR_CUDA;
+  return from_cuda(launch_kv_compact(a, used, stream));
+}
+
+// ---------------------------------------------------------------------------
+// e4m3 cache
+// ---------------------------------------------------------------------------
+static attn_status check_cache_f8(const attn_kv_cache_f8* c) {
+  if (c == nullptr || c->k == nullptr || c->v == nullptr || c->k_scale == nullptr || c->v_scale == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  if (c->num_blocks <= 0 || c->num_kv_heads <= 0 || c->block_size <= 0 || c->head_dim <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (c->block_size != 16) return ATTN_ERR_UNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 128) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+    return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+static F8Cache paged_f8(const attn_kv_cache_f8* c) {
+  F8Cache p;
+  p.k = static_cast<uint8_t*>(c->k);
+  p.v = static_cast<uint8_t*>(c->v);
+  p.k_scale = c->k_scale;
+  p.v_scale = c->v_scale;
+  p.num_blocks = c->num_blocks;
+  p.Hkv = c->num_kv_heads;
+  p.D = c->head_dim;
+  return p;
+}
+
+attn_status kv_append_f8(const attn_kv_cache_f8* cache, const int32_t* block_table, int64_t bt_stride,
+                         int32_t max_blocks, const int32_t* start_pos, const int32_t* lens, const attn_tensor* k_new,
+                         const attn_tensor* v_new, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  attn_status st;
+  if ((st = check_cache_f8(cache)) != ATTN_OK) return st;
+  if ((st = check_tensor(k_new, 4)) != ATTN_OK) return st;
+  if ((st = check_tensor(v_new, 4)) != ATTN_OK) return st;
+  const int64_t B = k_new->shape[0], T = k_new->shape[2];
+  if (k_new->dtype != ATTN_BF16 || v_new->dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
+  const int64_t want[4] = {B, cache->num_kv_heads, T, cache->head_dim};
+  for (int i = 0; i < 4; ++i)
+    if (k_new->shape[i] != want[i] || v_new->shape[i] != want[i]) return ATTN_ERR_INVALID_ARG;
+  if (max_blocks <= 0 || max_blocks > (1 << 24)) return ATTN_ERR_INVALID_ARG;
+  if (B > 65535 || T > (1 << 28) || cache->num_kv_heads > 65535) return ATTN_ERR_UNSUPPORTED;
+  if ((st = check_workspace(workspace, workspace_bytes, kStatusBytes)) != ATTN_OK) return st;
+  if (B == 0 || T == 0) return ATTN_OK;
+  if (block_table == nullptr || start_pos == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (B > 1 && bt_stride < max_blocks) return ATTN_ERR_INVALID_ARG;
+  if (!vec16_ok(k_new) || !vec16_ok(v_new)) return ATTN_ERR_INVALID_ARG;
+  F8AppendArgs a;
+  a.cache = paged_f8(cache);
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.max_blocks = max_blocks;
+  a.start_pos = start_pos;
+  a.lens = lens;
+  a.k_new = view(k_new);
+  a.v_new = view(v_new);
+  a.B = B;
+  a.T = T;
+  a.status = static_cast<uint32_t*>(workspace);
+  return from_cuda(launch_kv_append_f8(a, stream));
+}
+
+size_t paged_attn_f8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t num_queries,
+                                    int32_t max_blocks, int32_t block_size, int32_t head_dim) {
+  if (batch < 0 || num_q_heads < 0 || num_kv_heads <= 0 || num_queries < 0 || max_blocks < 0 || block_size != 16 ||
+      (head_dim != 64 && head_dim != 128) || num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > 128)
+    return 0;
+  if (batch == 0 || num_queries == 0 || num_q_heads == 0) return kStatusBytes;
+  return kStatusBytes + f8_attn_partial_bytes(batch, num_q_heads, num_kv_heads, num_queries, max_blocks, head_dim,
+                                              device_sm_count());
+}
+
+attn_status paged_attn_f8(const attn_tensor* q, const attn_kv_cache_f8* cache, const int32_t* block_table,
+                          int64_t bt_stride, int32_t max_blocks, const int32_t* start_pos, const int32_t* lens,
+                          int32_t causal, float scale, const attn_tensor* out, float* lse, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream) {
+  attn_status st;
+  if ((st = check_cache_f8(cache)) != ATTN_OK) return st;
+  if ((st = check_tensor(q, 4)) != ATTN_OK) return st;
+  if ((st = check_tensor(out, 4)) != ATTN_OK) return st;
+  const int64_t B = q->shape[0], Hq = q->shape[1], T = q->shape[2], D = q->shape[3];
+  for (int i = 0; i < 4; ++i)
+    if (out->shape[i] != q->shape[i]) return ATTN_ERR_INVALID_ARG;
+  if (q->dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
+  if (D != cache->head_dim) return ATTN_ERR_INVALID_ARG;
+  if (Hq <= 0 || Hq % cache->num_kv_heads != 0) return ATTN_ERR_INVALID_ARG;
+  if (!isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (max_blocks <= 0 || max_blocks > (1 << 24)) return ATTN_ERR_INVALID_ARG;
+  if (B > 65535 || Hq > 65535 || T > (1 << 24) || Hq / cache->num_kv_heads > 128 ||
+      cache->num_blocks * cache->num_kv_heads > 0x7fffffff ||
+      !f8_attn_fits(B, Hq, cache->num_kv_heads, T, max_blocks))
+    return ATTN_ERR_UNSUPPORTED;
+  const size_t need = paged_attn_f8_workspace_size(static_cast<int32_t>(B), static_cast<int32_t>(Hq),
+                                                   cache->num_kv_heads, static_cast<int32_t>(T), max_blocks,
+                                                   cache->block_size, cache->head_dim);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != ATTN_OK) return st;
+  if (B == 0 || T == 0) return ATTN_OK;
+  if (block_table == nullptr || start_pos == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (B > 1 && bt_stride < max_blocks) return ATTN_ERR_INVALID_ARG;
+  if (!tma_rows_ok(q) || !tma_rows_ok(out)) return ATTN_ERR_INVALID_ARG;
+  F8AttnArgs a;
+  a.cache = paged_f8(cache);
+  a.q = view(q);
+  a.out = view(out);
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.max_blocks = max_blocks;
+  a.start_pos = start_pos;
+  a.lens = lens;
+  a.causal = causal != 0;
+  a.B = B;
+  a.Hq = Hq;
+  a.T = T;
+  a.scale = scale;
+  a.lse = lse;
+  a.partials = static_cast<uint8_t*>(workspace) + kStatusBytes;
+  a.n_cta = device_sm_count();
+  a.gen = next_count_gen();
+  a.status = static_cast<uint32_t*>(workspace);
+  if (a.n_cta <= 0) return ATTN_ERR_CUDA;
+  return from_cuda(launch_paged_attn_f8(a, stream));
+}
+
 attn_status attn_selftest_wait_timeout(void* workspace, size_t workspace_bytes, uint32_t timeout_us,
                                        cudaStream_t stream) {
   attn_status st;

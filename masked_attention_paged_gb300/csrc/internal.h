@@ -278,6 +278,93 @@ struct RopeArgs {
 bool rope_rows_in_vectors(const RopeArgs& a);
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
 
+constexpr int kVerifyMaxDrafts = 256;  // nodes of a tree
+struct VerifyArgs {
+  View4 p, q;  // [B, T, V]; q.data null without draft probabilities
+  const int32_t* tokens;  // row b at tokens + b * tok_stride
+  int64_t tok_stride;
+  const int32_t* parents;
+  int64_t par_stride;
+  const float* uniforms;
+  int64_t uni_stride;
+  int replacement;
+  int64_t B, T, V;
+  int32_t* path;      // [B, T]
+  int32_t* n_accept;  // [B]
+  int32_t* next;      // [B]
+  uint32_t* status;
+};
+cudaError_t launch_draft_verify(const VerifyArgs& a, cudaStream_t stream);
+
+// A pool of blocks with owner counts, and the tensors whose blocks they are.
+constexpr int kPoolMaxTensors = 256;
+constexpr int64_t kPoolMaxBlocks = 1 << 20;
+struct PoolArgs {
+  int n_tensors = 0;
+  const attn_pool_tensor* tensors = nullptr;
+  int32_t* refs;
+  int64_t num_blocks;
+  int32_t* block_table;  // (kv_fork only reads it)
+  int64_t bt_stride;
+  int max_blocks;
+  int32_t* ctx_lens;  // (kv_free alone writes it)
+  int batch;
+  void* scratch;  // workspace after the status block
+  uint32_t* status;
+};
+size_t pool_workspace_bytes(int64_t num_blocks, int64_t rows);  // past the status block
+cudaError_t launch_kv_free(const PoolArgs& a, const int32_t* done, cudaStream_t stream);
+cudaError_t launch_kv_reserve(const PoolArgs& a, const int32_t* n_new, cudaStream_t stream);
+cudaError_t launch_kv_fork(const PoolArgs& a, const int32_t* src, int32_t* child_table, int64_t child_stride,
+                           int child_blocks, int32_t* child_lens, int children, cudaStream_t stream);
+cudaError_t launch_kv_compact(const PoolArgs& a, int32_t* used, cudaStream_t stream);
+
+// An e4m3 cache: codes, and a scale per (block, KV head).
+struct F8Cache {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;  // [num_blocks, Hkv]
+  float* v_scale;
+  int64_t num_blocks;
+  int Hkv;
+  int D;
+};
+struct F8AppendArgs {
+  F8Cache cache;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int max_blocks;
+  const int32_t* start_pos;  // [B]
+  const int32_t* lens;       // [B] new tokens, or null (T)
+  View4 k_new, v_new;        // [B, Hkv, T, D]
+  int64_t B, T;
+  uint32_t* status;
+};
+cudaError_t launch_kv_append_f8(const F8AppendArgs& a, cudaStream_t stream);
+
+struct F8AttnArgs {
+  F8Cache cache;
+  View4 q, out;  // [B, Hq, T, D]
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int max_blocks;
+  const int32_t* start_pos;  // [B] position of the first query
+  const int32_t* lens;       // [B] queries, or null (T)
+  int causal;
+  int64_t B, Hq, T;
+  float scale;
+  float* lse;      // [B, Hq, T] or null
+  void* partials;  // workspace after the status block
+  int n_cta;       // SMs of the device
+  uint32_t gen;    // this call's generation, tags its counts
+  uint32_t* status;
+};
+// workspace past the status block
+size_t f8_attn_partial_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t T, int64_t max_blocks, int D, int n_cta);
+// whether the call's work can be counted in 31 bits
+bool f8_attn_fits(int64_t B, int64_t Hq, int64_t Hkv, int64_t T, int64_t max_blocks);
+cudaError_t launch_paged_attn_f8(const F8AttnArgs& a, cudaStream_t stream);
+
 // boolean key-padding mask (non-zero = padded) -> additive 0 / -inf
 cudaError_t launch_padding_mask_to_additive(const uint8_t* kpm, int64_t kpm_stride, int64_t B, int64_t Pk,
                                             float* out, int64_t out_stride, cudaStream_t stream);
