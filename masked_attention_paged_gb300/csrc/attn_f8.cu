@@ -1,5 +1,5 @@
-// attn_f8.cu -- attention of few query rows over an e4m3 paged cache on the tensor
-// cores (paged_attn_f8).
+// attn_f8.cu -- attention of few query rows (at most 16 per KV head: decode steps and
+// short drafts) over an e4m3 paged cache (paged_attn_f8).
 //
 // A warp takes a block (16 tokens of one KV head) at a time, with no conversion of K:
 //  * q is split into two e4m3 numbers, q = (hi + lo) 2^e, with 2^e the power of two that
@@ -38,7 +38,6 @@ struct F8MmaParams {
   const float* vs;
   int64_t num_blocks;
   int Hkv, Hq, G, T;
-  int groups;  // of 8 NR query rows per KV head
   const uint16_t* q;
   int64_t q_stride[3];
   const int32_t* bt;
@@ -53,9 +52,9 @@ struct F8MmaParams {
   int out_bf16;
   int64_t out_stride[3];
   float* lse;
-  float* part_o;    // [(b, KV head, group, split)][8 NR][D]
+  float* part_o;    // [(b, KV head, split)][8 NR][D]
   float* part_lse;  // [the same][8 NR], log2 units
-  unsigned long long* count;  // [b, KV head, group]
+  unsigned long long* count;  // [b, KV head]
   uint32_t gen;
   uint32_t* status;
 };
@@ -111,7 +110,7 @@ __device__ __forceinline__ void write_row(const F8MmaParams& p, int b, int h, in
     *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at) = make_float2(x, y);
 }
 
-// grid (splits, KV heads x row groups, sequences)
+// grid (splits, KV heads, sequences)
 template <int D, int NR>
 __global__ void __launch_bounds__(kWarps * 32, NR == 1 ? 4 : 3)
     paged_attn_f8_mma_kernel(const __grid_constant__ F8MmaParams p) {
@@ -145,8 +144,8 @@ __global__ void __launch_bounds__(kWarps * 32, NR == 1 ? 4 : 3)
   __syncthreads();
   wait_for_launch_ahead();
 
-  const int split = blockIdx.x, gkv = blockIdx.y / p.groups, rg = blockIdx.y % p.groups, b = blockIdx.z;
-  const int R = p.T * p.G;  // rows of the KV head
+  const int split = blockIdx.x, gkv = blockIdx.y, b = blockIdx.z;
+  const int R = p.T * p.G;  // rows of the KV head: query r / G, head r % G
   int start;
   bool past;
   const int n = queries(p, b, start, past);
@@ -156,10 +155,8 @@ __global__ void __launch_bounds__(kWarps * 32, NR == 1 ? 4 : 3)
     const int i = r / p.G;
     return r >= R || i >= n ? 0 : (p.causal ? start + i + 1 : start + n);
   };
-  const int r0 = rg * kRows;
-  const int last_row = min(r0 + kRows, n * p.G) - 1;  // the last that sees anything
-  const int kend = last_row < r0 ? 0 : limit(last_row);
-  const int kfirst = kend == 0 ? 0 : limit(r0);       // the least of those that do
+  const int kend = n == 0 ? 0 : limit(n * p.G - 1);  // keys of the last row that sees any
+  const int kfirst = limit(0);                        // and of the first
   auto write_empty = [&](int r) {
     const int h = gkv * p.G + r % p.G, i = r / p.G;
     for (int d = 2 * lane; d < D; d += 64) write_row<D>(p, b, h, i, d, 0.f, 0.f);
@@ -167,8 +164,8 @@ __global__ void __launch_bounds__(kWarps * 32, NR == 1 ? 4 : 3)
   };
   const int t_begin = split * p.split_tokens;
   if (t_begin >= kend) {
-    if (split == 0)  // no row of the group sees anything
-      for (int r = r0 + warp; r < min(r0 + kRows, R); r += kWarps) write_empty(r);
+    if (split == 0)  // no row sees anything
+      for (int r = warp; r < R; r += kWarps) write_empty(r);
     return;
   }
   const int t_end = min(kend, t_begin + p.split_tokens);
@@ -219,7 +216,7 @@ __global__ void __launch_bounds__(kWarps * 32, NR == 1 ? 4 : 3)
   int lim[NR];
 #pragma unroll
   for (int nr = 0; nr < NR; ++nr) {
-    const int r = r0 + 8 * nr + g;
+    const int r = 8 * nr + g;
     lim[nr] = limit(r);
     float x[kSteps * 8], a = 0.f;
     const bool there = lim[nr] > 0;
@@ -464,16 +461,14 @@ __global__ void __launch_bounds__(kWarps * 32, NR == 1 ? 4 : 3)
   }
   __syncthreads();
   const int ns = (kend + p.split_tokens - 1) / p.split_tokens;  // splits with keys
-  const int64_t unit = (static_cast<int64_t>(b) * p.Hkv + gkv) * p.groups + rg;
-  for (int rr = warp; rr < kRows; rr += kWarps) {
-    const int r = r0 + rr;
-    if (r >= R) break;
+  const int64_t unit = static_cast<int64_t>(b) * p.Hkv + gkv;
+  for (int r = warp; r < R; r += kWarps) {
     float M = -INFINITY, wgt[kWarps], l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, comb[(w * kRows + rr) * kRec + D]);
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, comb[(w * kRows + r) * kRec + D]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float* rec = comb + (w * kRows + rr) * kRec + D;
+      const float* rec = comb + (w * kRows + r) * kRec + D;
       // a warp that saw nothing has max -inf and sum 0; a NaN sum is something
       wgt[w] = rec[0] == -INFINITY ? (rec[1] == 0.f ? 0.f : 1.f) : fast_exp2(rec[0] - M);
       l = fmaf(wgt[w], rec[1], l);
@@ -482,13 +477,13 @@ __global__ void __launch_bounds__(kWarps * 32, NR == 1 ? 4 : 3)
     const float inv = empty ? 0.f : 1.f / l;
     const float lse2 = empty ? -INFINITY : M + __log2f(l);
     const int h = gkv * p.G + r % p.G, i = r / p.G;
-    const int64_t slot = (unit * p.n_split + split) * kRows + rr;
+    const int64_t slot = (unit * p.n_split + split) * kRows + r;
     for (int d = 2 * lane; d < D; d += 64) {
       float x = 0.f, y = 0.f;
       if (!empty) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float* rec = comb + (w * kRows + rr) * kRec + d;
+          const float* rec = comb + (w * kRows + r) * kRec + d;
           if (wgt[w] == 0.f) continue;
           x = fmaf(wgt[w], rec[0], x);
           y = fmaf(wgt[w], rec[1], y);
@@ -517,10 +512,8 @@ __global__ void __launch_bounds__(kWarps * 32, NR == 1 ? 4 : 3)
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  for (int rr = warp; rr < kRows; rr += kWarps) {
-    const int r = r0 + rr;
-    if (r >= R) break;
-    const int64_t first = unit * p.n_split * kRows + rr;
+  for (int r = warp; r < R; r += kWarps) {
+    const int64_t first = unit * p.n_split * kRows + r;
     float M = -INFINITY;
     bool any = false;
     for (int k = lane; k < ns; k += 32) {
@@ -561,9 +554,9 @@ __global__ void __launch_bounds__(kWarps * 32, NR == 1 ? 4 : 3)
   }
 }
 
-// Rows of a KV head a CTA takes, and the tokens of a split.
-int rows_of(int64_t T, int64_t G) { return T * G <= 8 ? 8 : 16; }
-int64_t groups_of(int64_t T, int64_t G) { return (T * G + rows_of(T, G) - 1) / rows_of(T, G); }
+constexpr int64_t kMostRows = 16;  // of a KV head; more go to chunk_f8_tc.cu
+int rows_of(int64_t rows) { return rows <= 8 ? 8 : 16; }
+// tokens of a split
 int split_tokens(int64_t units, int64_t max_blocks, int n_cta) {
   // half a split as long as the GPU has room for the CTAs, down to a block a warp
   int tokens = 1024;
@@ -572,17 +565,16 @@ int split_tokens(int64_t units, int64_t max_blocks, int n_cta) {
 }
 
 struct Layout {
-  int64_t groups, units, n_split;
+  int64_t units, n_split;
   int tokens;
   size_t o, lse, count, bytes;  // offsets and size of the workspace
 };
 Layout layout(int64_t B, int64_t Hq, int64_t Hkv, int64_t T, int64_t max_blocks, int D, int n_cta) {
   Layout l;
-  l.groups = groups_of(T, Hq / Hkv);
-  l.units = B * Hkv * l.groups;
+  l.units = B * Hkv;
   l.tokens = split_tokens(l.units, max_blocks, n_cta);
   l.n_split = std::max<int64_t>(1, (max_blocks * kBS + l.tokens - 1) / l.tokens);
-  const size_t rows = static_cast<size_t>(l.units) * l.n_split * rows_of(T, Hq / Hkv);
+  const size_t rows = static_cast<size_t>(l.units) * l.n_split * rows_of(T * (Hq / Hkv));
   l.o = 0;
   l.lse = rows * D * 4;
   l.count = (l.lse + rows * 4 + 255) & ~size_t(255);
@@ -599,7 +591,7 @@ cudaError_t launch_mma(const F8AttnArgs& a, F8MmaParams& p, const Layout& l, cud
   constexpr int smem = 1024 + kWarps * kStages * (2 * kBS * D + 8);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(l.n_split), static_cast<unsigned>(a.cache.Hkv * l.groups),
+  const dim3 grid(static_cast<unsigned>(l.n_split), static_cast<unsigned>(a.cache.Hkv),
                   static_cast<unsigned>(a.B));
   return launch_early(kern, grid, kWarps * 32, smem, stream, p);
 }
@@ -607,16 +599,19 @@ cudaError_t launch_mma(const F8AttnArgs& a, F8MmaParams& p, const Layout& l, cud
 }  // namespace
 
 size_t f8_attn_partial_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t T, int64_t max_blocks, int D, int n_cta) {
-  return layout(B, Hq, Hkv, T, max_blocks, D, n_cta).bytes;
+  const int64_t G = Hq / Hkv;
+  return T * G > kMostRows ? f8_chunk_partial_bytes(T, G, D, n_cta) : layout(B, Hq, Hkv, T, max_blocks, D, n_cta).bytes;
 }
 
 bool f8_attn_fits(int64_t B, int64_t Hq, int64_t Hkv, int64_t T, int64_t max_blocks) {
-  return T * (Hq / Hkv) <= (1 << 28) && Hkv * groups_of(std::max<int64_t>(T, 1), Hq / Hkv) <= 65535;
+  const int64_t G = Hq / Hkv;
+  return T * G <= kMostRows || f8_chunk_fits(B, Hkv, T, G, max_blocks);
 }
 
 cudaError_t launch_paged_attn_f8(const F8AttnArgs& a, cudaStream_t stream) {
-  F8MmaParams p = {};
   const int G = static_cast<int>(a.Hq / a.cache.Hkv);
+  if (a.T * G > kMostRows) return launch_chunk_f8(a, stream);
+  F8MmaParams p = {};
   const Layout l = layout(a.B, a.Hq, a.cache.Hkv, a.T, a.max_blocks, a.cache.D, a.n_cta);
   p.kq = a.cache.k;
   p.vq = a.cache.v;
@@ -627,7 +622,6 @@ cudaError_t launch_paged_attn_f8(const F8AttnArgs& a, cudaStream_t stream) {
   p.Hq = static_cast<int>(a.Hq);
   p.G = G;
   p.T = static_cast<int>(a.T);
-  p.groups = static_cast<int>(l.groups);
   p.q = static_cast<const uint16_t*>(a.q.data);
   for (int i = 0; i < 3; ++i) p.q_stride[i] = a.q.stride[i], p.out_stride[i] = a.out.stride[i];
   p.bt = a.block_table;
@@ -649,8 +643,8 @@ cudaError_t launch_paged_attn_f8(const F8AttnArgs& a, cudaStream_t stream) {
   p.gen = a.gen;
   p.status = a.status;
   if (a.cache.D == 64)
-    return rows_of(a.T, G) == 8 ? launch_mma<64, 1>(a, p, l, stream) : launch_mma<64, 2>(a, p, l, stream);
-  return rows_of(a.T, G) == 8 ? launch_mma<128, 1>(a, p, l, stream) : launch_mma<128, 2>(a, p, l, stream);
+    return rows_of(a.T * G) == 8 ? launch_mma<64, 1>(a, p, l, stream) : launch_mma<64, 2>(a, p, l, stream);
+  return rows_of(a.T * G) == 8 ? launch_mma<128, 1>(a, p, l, stream) : launch_mma<128, 2>(a, p, l, stream);
 }
 
 }  // namespace attn

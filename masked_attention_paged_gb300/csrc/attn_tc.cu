@@ -1140,17 +1140,22 @@ bool make_rows_map(CUtensorMap* map, const View4& t, int64_t Hkv, int tokens) {
   return r == CUDA_SUCCESS;
 }
 
-bool make_code_cache_map(CUtensorMap* map, void* base, int64_t num_blocks, int Hkv) {
+bool make_code_map(CUtensorMap* map, void* base, int64_t num_blocks, int Hkv, int D) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return false;
-  const cuuint64_t dims[4] = {128, 16, static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(num_blocks)};
-  const cuuint64_t strides[3] = {128, 16 * 128, static_cast<cuuint64_t>(Hkv) * 16 * 128};
-  const cuuint32_t box[4] = {128, 16, 1, 1};
+  const cuuint64_t row = static_cast<cuuint64_t>(D);  // bytes
+  const cuuint64_t dims[4] = {row, 16, static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(num_blocks)};
+  const cuuint64_t strides[3] = {row, 16 * row, static_cast<cuuint64_t>(Hkv) * 16 * row};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(D), 16, 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool make_code_cache_map(CUtensorMap* map, void* base, int64_t num_blocks, int Hkv) {
+  return make_code_map(map, base, num_blocks, Hkv, 128);
 }
 
 namespace {

@@ -364,6 +364,14 @@ size_t f8_attn_partial_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t T, int6
 // whether the call's work can be counted in 31 bits
 bool f8_attn_fits(int64_t B, int64_t Hq, int64_t Hkv, int64_t T, int64_t max_blocks);
 cudaError_t launch_paged_attn_f8(const F8AttnArgs& a, cudaStream_t stream);
+// more than 16 query rows per KV head (chunk_f8_tc.cu), G = Hq / Hkv; workspace and
+// limits as the two above
+size_t f8_chunk_partial_bytes(int64_t T, int64_t G, int D, int n_cta);
+bool f8_chunk_fits(int64_t B, int64_t Hkv, int64_t T, int64_t G, int64_t max_blocks);
+cudaError_t launch_chunk_f8(const F8AttnArgs& a, cudaStream_t stream);
+// 4-D u8 tensor map over codes [num_blocks, Hkv, 16, D] (contiguous, D 64 or 128): box =
+// the codes of one (block, head), swizzled by a row's bytes
+bool make_code_map(CUtensorMap* map, void* base, int64_t num_blocks, int Hkv, int D);
 
 // boolean key-padding mask (non-zero = padded) -> additive 0 / -inf
 cudaError_t launch_padding_mask_to_additive(const uint8_t* kpm, int64_t kpm_stride, int64_t B, int64_t Pk,

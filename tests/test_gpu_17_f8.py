@@ -154,7 +154,7 @@ def _compare(got, lse, ref, ref_lse, mag, all_v, qn, codes, scales, scale, rows,
     ds = abs(scale) * top * kmax * D * (2.0 ** -19 + 4 * 2.0 ** -24)
     ds = np.minimum(ds, 1.0) + 2.0 ** -22 * np.abs(np.where(np.isfinite(ref_lse), ref_lse, 0.0))
     w = 2 * np.expm1(2 * ds) + (2.0 ** -11 if rows <= 16 else 2.0 ** -8) + 2.0 ** -18
-    tol = w[..., None] * mag + np.abs(ref) * (torch.finfo(dtype).eps / 2) + 2.0 ** -25 * all_v + 1e-30
+    tol = w[..., None] * mag + np.abs(ref) * (torch.finfo(dtype).eps / 2) + (rows <= 16) * 2.0 ** -25 * all_v + 1e-30
     got, lse = got.double().cpu().numpy(), lse.double().cpu().numpy()
     assert np.array_equal(np.isnan(got), np.isnan(ref))
     assert (np.abs(got - ref)[~np.isnan(ref)] <= tol[~np.isnan(ref)]).all(), np.nanmax(np.abs(got - ref) - tol)

@@ -161,7 +161,7 @@ def test_paged_attn_f8_rejects(L):  # noqa: F811
     assert call(q=flat) == INVALID and call(out=flat) == INVALID
     assert call(scale=float("inf")) == INVALID
     assert call(bt=None) == INVALID and call(pos=None) == INVALID and call(st=9) == INVALID and call(mb=0) == INVALID
-    assert call(ws=None) == WORKSPACE and call(n=256) == WORKSPACE
+    assert call(ws=None) == WORKSPACE and call(n=255) == WORKSPACE
     assert call(q=_t([2, 12, 0, 128])) == OK and call(q=_t([0, 12, 6, 128])) == OK
 
 
