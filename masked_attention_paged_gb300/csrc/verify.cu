@@ -13,9 +13,8 @@
 //
 // Tests and sums decide between whole numbers, so they carry twice a float's digits:
 // p - C q as an unevaluated sum of two floats (the products' and differences' errors
-// are exact by FMA), summed the same way, and in double above a lane.  Doubles
-// throughout would bound the kernel: the SM does two a cycle, and a row of 131072
-// needs five for each entry.
+// are exact by FMA), and sums of such pairs.  Doubles would bound the kernel (the SM
+// does two a cycle): only warp 0's scalars are.
 #include <math.h>
 
 #include "common.cuh"
@@ -71,11 +70,66 @@ __device__ __forceinline__ const void* row_at(const void* base, int64_t off) {
   return static_cast<const uint8_t*>(base) + off * (BF16 ? 2 : 4);
 }
 
-// hi + lo += x + y, |y| far below |x| (the error of hi + x is exact)
-__device__ __forceinline__ void add_pair(float& hi, float& lo, float x, float y) {
-  const float s = hi + x, b = s - hi;
-  lo += ((hi - (s - b)) + (x - b)) + y;
-  hi = s;
+// A number as an unevaluated sum of two floats, |y| far below |x|.
+using Pair = float2;
+// acc += x + y (the error of the first sum is exact)
+__device__ __forceinline__ void add_to(Pair& acc, float x, float y) {
+  const float s = acc.x + x, b = s - acc.x;
+  acc.y += ((acc.x - (s - b)) + (x - b)) + y;
+  acc.x = s;
+}
+__device__ __forceinline__ Pair tidy(Pair a) {
+  const float s = a.x + a.y;
+  return make_float2(s, a.y - (s - a.x));
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  add_to(a, b.x, b.y);
+  return tidy(a);
+}
+__device__ __forceinline__ Pair shfl_xor(Pair a, int m) {
+  return make_float2(__shfl_xor_sync(0xffffffffu, a.x, m), __shfl_xor_sync(0xffffffffu, a.y, m));
+}
+__device__ __forceinline__ Pair shfl_up(Pair a, int d) {
+  return make_float2(__shfl_up_sync(0xffffffffu, a.x, d), __shfl_up_sync(0xffffffffu, a.y, d));
+}
+__device__ __forceinline__ Pair shfl(Pair a, int l) {
+  return make_float2(__shfl_sync(0xffffffffu, a.x, l), __shfl_sync(0xffffffffu, a.y, l));
+}
+__device__ __forceinline__ bool greater(Pair a, Pair b) { return (a.x - b.x) + (a.y - b.y) > 0.f; }
+__device__ __forceinline__ double value(Pair a) { return static_cast<double>(a.x) + static_cast<double>(a.y); }
+__device__ __forceinline__ Pair pair_of(double x) {
+  const float h = static_cast<float>(x);
+  return make_float2(h, static_cast<float>(x - static_cast<double>(h)));
+}
+// sums over the lanes up to this one
+__device__ __forceinline__ Pair scan(Pair a, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const Pair up = shfl_up(a, d);
+    if (lane >= d) a = add(a, up);
+  }
+  return a;
+}
+// The lane in whose part of [before, ...) `goal` falls, `mine` being each lane's part: the first
+// whose end is past it, else (by rounding) the last with a part at all.  before: that
+// lane's start.
+__device__ __forceinline__ int pick(Pair mine, Pair goal, Pair& before, int lane) {
+  const Pair upto = add(before, scan(mine, lane));
+  const uint32_t past = __ballot_sync(0xffffffffu, greater(upto, goal));
+  const uint32_t on = __ballot_sync(0xffffffffu, mine.x > 0.f);
+  const uint32_t among = past & on;
+  const int l = among != 0u ? __ffs(static_cast<int>(among)) - 1 : (on != 0u ? 31 - __clz(static_cast<int>(on)) : 0);
+  const Pair ahead = shfl_up(upto, 1);
+  const Pair start = lane == 0 ? before : ahead;
+  before = shfl(start, l);
+  return l;
+}
+// p - c q > 0 as a pair (0 if not), c = ch + cl
+__device__ __forceinline__ Pair residual(float x, float y, float ch, float cl) {
+  const float t = __fmul_rn(ch, y), d = x - t;
+  // errors of the product and, where d > 0, of the difference
+  const float e = ((x - d) - t) - fmaf(cl, y, fmaf(ch, y, -t));
+  return d + e > 0.f ? make_float2(d, e) : make_float2(0.f, 0.f);
 }
 
 // What the walk asks of the whole cluster.
@@ -91,8 +145,9 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
   __shared__ float px[kMaxDrafts], qx[kMaxDrafts], uni[kMaxDrafts];
   __shared__ int par[kMaxDrafts], tok[kMaxDrafts];
   __shared__ uint8_t refused[kMaxDrafts];  // of the node where the sequence stands
-  __shared__ double warp_sum[kWarps], cta_sum[2][kMaxCtas];
+  __shared__ Pair warp_sum[kWarps], cta_sum[2][kMaxCtas], found_start, found_goal;
   __shared__ Ask ask;
+  __shared__ int found;  // the warp whose part the next token is in; -1: not this CTA's
   let_next_launch_in();
   wait_for_launch_ahead();
   const int b = blockIdx.y, rank = static_cast<int>(cluster_rank());
@@ -135,22 +190,22 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
   const int w0 = static_cast<int>(min(static_cast<int64_t>(V), static_cast<int64_t>(rank * kWarps + warp) * per));
   const int w1 = static_cast<int>(min(static_cast<int64_t>(V), static_cast<int64_t>(w0) + per));
   int turn = 0;
-  // the sum that `ask` asks for, alike in every thread of the cluster; warp_sum and
+  // the sum that `ask` asks for, in warp 0 of every CTA alike; warp_sum and
   // cta_sum[turn] hold its parts afterwards
   auto row_sum = [&](int node, double c, bool without) -> double {
     const void* pr = row_at<BF16>(p.p, b * p.ps0 + node * p.ps1);
-    float hi = 0.f, lo = 0.f;
+    Pair acc = make_float2(0.f, 0.f);
     if (c == 0.0) {
       for (int v0 = w0 + lane; v0 < w1; v0 += 32 * kUnroll) {
         float x[kUnroll];
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) x[k] = v0 + 32 * k < w1 ? load<BF16>(pr, v0 + 32 * k) : 0.f;
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) add_pair(hi, lo, x[k] > 0.f ? x[k] : 0.f, 0.f);
+        for (int k = 0; k < kUnroll; ++k) add_to(acc, fmaxf(x[k], 0.f), 0.f);
       }
     } else {
       const void* qr = row_at<BF16>(p.q, b * p.qs0 + node * p.qs1);
-      const float ch = static_cast<float>(c), cl = static_cast<float>(c - ch);
+      const Pair cp = pair_of(c);
       for (int v0 = w0 + lane; v0 < w1; v0 += 32 * kUnroll) {
         float x[kUnroll], y[kUnroll];
 #pragma unroll
@@ -161,42 +216,46 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
         }
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) {
-          const float t = __fmul_rn(ch, y[k]), d = x[k] - t;
-            // errors of the product and, where d > 0, of the difference
-          const float e = ((x[k] - d) - t) - fmaf(cl, y[k], fmaf(ch, y[k], -t));
-          const bool on = d + e > 0.f;
-          add_pair(hi, lo, on ? d : 0.f, on ? e : 0.f);
+          const Pair r = residual(x[k], y[k], cp.x, cp.y);
+          add_to(acc, r.x, r.y);
         }
       }
     }
-    double s = static_cast<double>(hi) + static_cast<double>(lo);
     if (without) {  // the refused tokens of this warp's part (each once)
       for (int t = node + 1 + lane; t < T; t += 32)
-        if (refused[t] && tok[t] >= w0 && tok[t] < w1 && px[t] > 0.f) s -= px[t];
+        if (refused[t] && tok[t] >= w0 && tok[t] < w1) add_to(acc, -px[t], 0.f);
     }
+    acc = tidy(acc);
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-    if (lane == 0) warp_sum[warp] = fmax(s, 0.0);
+    for (int m = 16; m >= 1; m >>= 1) acc = add(acc, shfl_xor(acc, m));
+    if (lane == 0) warp_sum[warp] = acc.x > 0.f ? acc : make_float2(0.f, 0.f);
     __syncthreads();
     turn ^= 1;
-    if (threadIdx.x < nc) {
-      double all = 0.0;
-      for (int w = 0; w < kWarps; ++w) all += warp_sum[w];
-      uint32_t at;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                   : "=r"(at)
-                   : "r"(smem_u32(&cta_sum[turn][rank])), "r"(threadIdx.x));
-      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(all) : "memory");
+    const auto all_lanes = [&](Pair s) {  // of the first 16 lanes, the others hold 0
+#pragma unroll
+      for (int m = 8; m >= 1; m >>= 1) s = add(s, shfl_xor(s, m));
+      return s;
+    };
+    const Pair none = make_float2(0.f, 0.f);
+    if (warp == 0) {
+      const Pair s = all_lanes(warp_sum[lane % kWarps]);
+      if (lane < nc) {
+        uint32_t at;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(at)
+                     : "r"(smem_u32(&cta_sum[turn][rank])), "r"(lane));
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(s.x), "f"(s.y) : "memory");
+      }
     }
     cluster_sync();
-    double all = 0.0;
-    for (int r = 0; r < nc; ++r) all += cta_sum[turn][r];
-    return all;
+    if (warp != 0) return 0.0;
+    return value(shfl(all_lanes(lane % 16 < nc ? cta_sum[turn][lane % 16] : none), 0));
   };
+  static_assert(kWarps == 16 && kMaxCtas == 16, "a lane per part");
 
   // ---- the walk, in warp 0 of every CTA alike
   int node = 0, n = 1, t = 0;
-  double c = 0.0, mass = 1.0, left = 1.0;
+  double c = 0.0, mass = 1.0, left = 1.0, total = 0.0;
   bool known = true;   // mass is this row's at c
   bool summed = false; // the parts of the last sum are this node's at c
   for (;;) {
@@ -268,26 +327,24 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
     __syncthreads();
     const Ask a = ask;
     if (a.sum) {
-      const double s = row_sum(a.node, a.c, certain);
-      if (!certain) mass = s;
+      total = row_sum(a.node, a.c, certain);
+      if (!certain) mass = total;
       known = summed = true;
     }
     if (a.done) break;
     __syncthreads();  // ask has been read
   }
-  // (only warp 0 kept n; every warp has the last ask)
   const int last = ask.node;
-  double cc = ask.c;
-  bool without = certain;
-  double total = 0.0;
-  for (int r = 0; r < nc; ++r) total += cta_sum[turn][r];
-  if (!(total > 0.0) && (cc != 0.0 || without)) {  // nothing is left: from p itself
-    cc = 0.0;
-    without = false;
+  // nothing is left of a row that something was taken from: the token comes from p itself
+  bool whole = ask.c == 0.0 && !certain;
+  if (warp == 0 && lane == 0) found = total > 0.0;
+  __syncthreads();
+  if (!found && !whole) {  // (the cluster's CTAs alike)
+    whole = true;
     total = row_sum(last, 0.0, false);
   }
-  if (rank == 0) {
-    if (warp == 0) {
+  if (warp == 0) {
+    if (rank == 0) {
       if (lane == 0) {
         path[0] = 0;
         p.n_accept[b] = n;
@@ -298,67 +355,67 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
       }
       for (int i = n + lane; i < T; i += 32) path[i] = -1;
     }
+    // ---- the next token: which CTA, which warp's part
+    int who = -1;
+    if (total > 0.0) {
+      const Pair goal = pair_of(static_cast<double>(uni[0]) * total), none = make_float2(0.f, 0.f);
+      Pair before = none;
+      if (pick(lane < nc ? cta_sum[turn][lane] : none, goal, before, lane) == rank)
+        who = pick(lane < kWarps ? warp_sum[lane] : none, goal, before, lane);
+      found_start = before;
+      found_goal = goal;
+    }
+    if (lane == 0) found = who;
   }
-  if (!(total > 0.0)) return;
-
-  // ---- the next token: which CTA, which warp, which lane
-  const double goal = static_cast<double>(uni[0]) * total;
-  double before = 0.0;
-  int owner = -1, last_on = 0;
-  double at_owner = 0.0, at_last = 0.0;
-  for (int r = 0; r < nc; ++r) {
-    const double s = cta_sum[turn][r];
-    if (s > 0.0) last_on = r, at_last = before;
-    if (owner < 0 && before + s > goal) owner = r, at_owner = before;
-    before += s;
-  }
-  if (owner < 0) owner = last_on, at_owner = at_last;
-  if (owner != rank) return;
-  before = at_owner;
-  int who = -1, last_warp = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    const double s = warp_sum[w];
-    if (s > 0.0) last_warp = w, at_last = before;
-    if (who < 0 && before + s > goal) who = w, at_owner = before;
-    before += s;
-  }
-  if (who < 0) who = last_warp, at_owner = at_last;
-  if (who != warp) return;
-  before = at_owner;
+  __syncthreads();
+  if (found < 0) return;
+  // ---- in it: all warps take a piece of that part, then one warp the piece's entries
   const void* pr = row_at<BF16>(p.p, b * p.ps0 + last * p.ps1);
-  const void* qr = cc != 0.0 ? row_at<BF16>(p.q, b * p.qs0 + last * p.qs1) : nullptr;
-  auto weight = [&](int v) -> double {
-    double w = load<BF16>(pr, v);
-    if (qr != nullptr) w -= cc * static_cast<double>(fmaxf(load<BF16>(qr, v), 0.f));
-    if (without)
+  const void* qr = row_at<BF16>(p.q, b * p.qs0 + last * p.qs1);
+  const Pair cp = whole ? make_float2(0.f, 0.f) : pair_of(ask.c);
+  auto weight = [&](int v) -> Pair {
+    const float x = load<BF16>(pr, v);
+    if (!whole && certain) {
       for (int i = last + 1; i < T; ++i)
-        if (refused[i] && tok[i] == v) w = 0.0;
-    return w > 0.0 ? w : 0.0;
+        if (refused[i] && tok[i] == v) return make_float2(0.f, 0.f);
+    }
+    if (cp.x == 0.f) return make_float2(fmaxf(x, 0.f), 0.f);
+    return tidy(residual(x, fmaxf(load<BF16>(qr, v), 0.f), cp.x, cp.y));
   };
-  const int each = (w1 - w0 + 31) / 32;
-  const int v0 = min(w1, w0 + lane * each), v1 = min(w1, v0 + each);
-  double mine = 0.0;
-  for (int v = v0; v < v1; ++v) mine += weight(v);
-  double incl = mine;
+  const int part0 = static_cast<int>(min(static_cast<int64_t>(V), static_cast<int64_t>(rank * kWarps + found) * per));
+  const int part1 = static_cast<int>(min(static_cast<int64_t>(V), static_cast<int64_t>(part0) + per));
+  const int piece = ((part1 - part0 + kWarps - 1) / kWarps + 31) / 32 * 32;
+  const int v0 = min(part1, part0 + warp * piece), v1 = min(part1, v0 + piece);
+  Pair acc = make_float2(0.f, 0.f);
+  for (int v = v0 + lane; v < v1; v += 32) {
+    const Pair w = weight(v);
+    add_to(acc, w.x, w.y);
+  }
+  acc = tidy(acc);
 #pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const double up = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += up;
-  }
-  const uint32_t past = __ballot_sync(0xffffffffu, before + incl > goal);
-  const uint32_t on = __ballot_sync(0xffffffffu, mine > 0.0);
-  if (on == 0u) return;  // (a warp with a positive sum has a positive weight)
-  const int pick = past != 0u ? __ffs(static_cast<int>(past)) - 1 : 31 - __clz(static_cast<int>(on));
-  if (lane != pick) return;
-  double sum = before + (incl - mine);
+  for (int m = 16; m >= 1; m >>= 1) acc = add(acc, shfl_xor(acc, m));
+  __syncthreads();  // the parts' sums have been read
+  if (lane == 0) warp_sum[warp] = acc;
+  __syncthreads();
+  if (warp != 0) return;
+  const Pair goal = found_goal;
+  Pair before = found_start;
+  const int w = pick(lane < kWarps ? warp_sum[lane] : make_float2(0.f, 0.f), goal, before, lane);
+  const int e0 = min(part1, part0 + w * piece), e1 = min(part1, e0 + piece);
   int token = -1;
-  for (int v = v0; v < v1; ++v) {
-    const double w = weight(v);
-    if (w > 0.0) token = v;
-    sum += w;
-    if (sum > goal) break;
+  for (int v = e0; v < e1; v += 32) {  // 32 entries at a time
+    const Pair mine = v + lane < e1 ? weight(v + lane) : make_float2(0.f, 0.f);
+    const Pair upto = add(before, scan(mine, lane));
+    const uint32_t past = __ballot_sync(0xffffffffu, mine.x > 0.f && greater(upto, goal));
+    const uint32_t on = __ballot_sync(0xffffffffu, mine.x > 0.f);
+    if (past != 0u) {
+      token = v + __ffs(static_cast<int>(past)) - 1;
+      break;
+    }
+    if (on != 0u) token = v + 31 - __clz(static_cast<int>(on));
+    before = shfl(upto, 31);
   }
-  p.next[b] = token;
+  if (lane == 0) p.next[b] = token;
 }
 
 template <bool BF16>
