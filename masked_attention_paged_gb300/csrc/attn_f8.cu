@@ -90,9 +90,6 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b) {
 // Token of position n (0..15) of a block in the order the fragments use: with the
 // 128-byte swizzle, fragment loads of K and of V then meet no bank twice.
 __device__ __forceinline__ int tok_of(int n) { return n ^ ((n & 1) << 2); }
-// bytes that are NaN codes, as 0x80 each
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-
 // A sequence's queries: n of them (0: idle, or past its table), from position `start` on.
 __device__ __forceinline__ int queries(const F8MmaParams& p, int b, int& start, bool& past) {
   start = p.start[b];
@@ -242,8 +239,9 @@ __global__ void __launch_bounds__(kWarps * 32, NR == 1 ? 4 : 3)
     }
     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-    const float up = pow2(a > 0.f ? f8_scale_exponent(a) : 0), inv = 1.0f / up;
-    mul[nr] = p.scale_log2 * up;
+    const int e2 = a > 0.f ? f8_scale_exponent(a) : 0;
+    const float inv = pow2(-e2);
+    mul[nr] = p.scale_log2 * pow2(e2);
 #pragma unroll
     for (int c = 0; c < kSteps; ++c)
 #pragma unroll

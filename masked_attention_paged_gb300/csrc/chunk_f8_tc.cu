@@ -17,8 +17,7 @@
 // leaves partials (normalised rows and log2 LSE), which a second launch joins in
 // order, so results do not depend on timing.
 //
-// Warps: 0 streams K codes, 1 V codes (lane i < 8 the block i of a tile), 2 issues the
-// MMAs, 3 plans the segments, 4-7 convert V, 8-11 and 12-15 softmax (thread r owns row
+// Warps: 0 streams the codes, 1 issues the MMAs, 3 plans the segments, 4-7 convert V, 8-11 and 12-15 softmax (thread r owns row
 // r: TMEM lane r; it also splits its row of q).  With NT = 2 each warpgroup has a row
 // tile.  With NT = 1 both have the same rows and take the key tiles in turn, each with a
 // score buffer, an accumulator and a running max and sum of its own, joined by the LSE
@@ -46,7 +45,7 @@ constexpr int kBM = 128;
 constexpr int kBN = 128;
 constexpr int kBS = 16;
 constexpr float kRescaleMargin = 8.0f;
-constexpr int kBarBytes = 3072;
+constexpr int kBarBytes = 4096;
 constexpr int kSegs = 4;      // segments the planner is ahead
 constexpr int kItemCost = 3;  // what an item costs a CTA besides its tiles, in tiles
 constexpr int kScales = 8;    // tiles whose key scales are held: more than K's stages and the scores ahead of P
@@ -73,8 +72,9 @@ struct Cfg {
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   static_assert(KS + 2 < kScales, "the ring of scales outlasts the stages");
   static constexpr uint32_t kColO = 256;  // O of warpgroup w at kColO + w * D; its scores at w * 128
-  // 512 threads launched with 128 registers; 256 x 72 + 256 x 184 = 65536
-  static constexpr int kRegsCtl = 72, kRegsSoft = 184;
+  // 512 threads launched with 128 registers; 256 x 56 + 256 x 200 = 65536 (184: the
+  // softmax of NT = 2 spills)
+  static constexpr int kRegsCtl = 56, kRegsSoft = 200;
   // codes of a row: 128 bytes, 128-byte swizzle (D = 128), or 64 and 64
   static constexpr uint32_t kGroup = 8 * D;  // next 8 rows
   static __device__ __forceinline__ uint32_t code_off(int r, int c) {  // 16-byte chunk c of row r
@@ -90,7 +90,7 @@ struct Cfg {
 struct Seg {
   int b;  // -1: the end
   int g, i0, t0, t1;
-  int start, n;  // the sequence's first position and queries; n <= i0: nothing is seen
+  int start, n;  // the sequence's first position and queries
   int kend;      // keys that the item's last row sees
   int slot;      // where its partial goes; -1: the item is whole
 };
@@ -98,7 +98,7 @@ struct Seg {
 struct Bars {
   uint64_t k_full[4], k_empty[4], c_full[4], c_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2], p_full[2], o_done[2];  // [warpgroup]
-  uint64_t q_full[2];
+  uint64_t q_raw[2], q_full[2];
   uint64_t sc_full[kScales];
   uint64_t xch_full[2];  // NT = 1: a warpgroup's running max and sum are in smem
   uint64_t o_free;       // NT = 1: both warpgroups have read both accumulators
@@ -106,10 +106,11 @@ struct Bars {
   uint64_t drained;
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   Seg segs[kSegs];
-  float ks[kScales][8];
+  alignas(16) float ks[kScales][8];  // read four at a time
   uint32_t there[kScales];  // blocks of the tile whose id is good
   float vs[4][8];           // by V code stage; -1: no such block
   uint32_t bad[kNotes][4][kSpread / 32];  // tokens start + i0 + .. whose V holds a NaN, by converting warp
+  float qmul[2][kBM];  // rows' factors
   uint32_t tmem_base;
   int abort;
 };
@@ -145,6 +146,7 @@ struct ChunkParams {
   float* part_o;    // [2 n][D][pitch]: a column's rows side by side, as the TMEM lanes hold them
   float* part_lse;  // [2 n][pitch]
   int pitch;        // rows of a partial: 128 a row tile
+  int ctas;         // n: CTAs of the main launch
   CutItem* cuts;    // [n] the item that starts in CTA c's run and goes on past it
   uint32_t* status;
 };
@@ -156,11 +158,12 @@ __device__ __forceinline__ int seq_queries(const ChunkParams& p, int b, int& sta
   past = start >= 0 && static_cast<int64_t>(start) + n > static_cast<int64_t>(p.max_blocks) * kBS;
   return start < 0 || past ? 0 : n;
 }
-// Keys of the row group that begins at query i0, and its tiles (one for a group that sees nothing).
+// Keys of the row group that begins at query i0, and its tiles (a group that sees nothing has
+// none, and is no item: the second launch writes it).
 __device__ __forceinline__ int group_keys(const ChunkParams& p, int start, int n, int i0, int rows) {
   return i0 >= n ? 0 : start + (p.causal ? min(i0 + rows, n) : n);
 }
-__device__ __forceinline__ int key_tiles(int kend) { return max(1, (kend + kBN - 1) / kBN); }
+__device__ __forceinline__ int key_tiles(int kend) { return (kend + kBN - 1) / kBN; }
 // Keys of a tile that its MMAs cover: a multiple of 16, at least 16.
 __device__ __forceinline__ int tile_keys(int kend, int tile) {
   return min(kBN, max(16, (kend - tile * kBN + 15) / 16 * 16));
@@ -189,7 +192,8 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
 // Joins the pieces of the cut items: out = sum_c 2^(lse_c - M) out_c / sum_c 2^(lse_c - M).
 // grid (CTAs of the main launch, groups of 32 rows), a warp per D / 16 columns, a lane
 // per row: partials are read as they were written, 128 bytes a warp, and the rows
-// leave through shared memory.
+// leave through shared memory.  CTAs past the main launch's write the rows of groups
+// that see nothing.
 constexpr int kMergeThreads = 512;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
@@ -198,9 +202,31 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
   let_next_launch_in();
   wait_for_launch_ahead();
   const int c0 = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (c0 >= p.ctas) {
+    const int span = p.pitch / kBM * p.tb;
+    const int64_t all = static_cast<int64_t>(p.B) * p.MP * p.Hq;
+    for (int64_t x = (c0 - p.ctas) * gridDim.y + blockIdx.y; x < all; x += (gridDim.x - p.ctas) * gridDim.y) {
+      const int h = static_cast<int>(x % p.Hq), j = static_cast<int>(x / p.Hq), b = j / p.MP;
+      const int i0 = (j - b * p.MP) * span;
+      int start;
+      bool past;
+      if (i0 < seq_queries(p, b, start, past)) continue;
+      for (int i = i0 + warp; i < min(i0 + span, p.T); i += kMergeThreads / 32) {
+        const int64_t ob = b * p.out_stride[0] + h * p.out_stride[1] + i * p.out_stride[2];
+        for (int d = 2 * lane; d < D; d += 64) {
+          if (p.out_bf16)
+            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + ob + d) = 0u;
+          else
+            *reinterpret_cast<float2*>(static_cast<float*>(p.out) + ob + d) = make_float2(0.f, 0.f);
+        }
+        if (lane == 0 && p.lse != nullptr) p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.T + i] = -INFINITY;
+      }
+    }
+    return;
+  }
   const CutItem it = p.cuts[c0];
   if (it.pieces == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sr = blockIdx.y * 32 + lane;  // row of the partials
   auto place = [&](int r, int& i, int& h) {  // its query and head
     const int row = r % kBM;
@@ -269,10 +295,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 
   if (threadIdx.x == 32) {
     for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->q_raw[t], NT == 1 ? 8 : 4);
       mbar_init(&bars->q_full[t], NT == 1 ? 8 : 4);
+      mbar_init(&bars->o_done[t], 1);
       mbar_init(&bars->s_full[t], 1);
       mbar_init(&bars->p_full[t], 4);
-      mbar_init(&bars->o_done[t], 1);
       mbar_init(&bars->xch_full[t], 4);
     }
     for (int s = 0; s < 4; ++s) {
@@ -286,7 +313,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     for (int s = 0; s < kScales; ++s) mbar_init(&bars->sc_full[s], 1);
     for (int s = 0; s < kSegs; ++s) {
       mbar_init(&bars->seg_full[s], 1);
-      mbar_init(&bars->seg_empty[s], 15);  // 2 producers, the issuer, 4 converting and 8 softmax warps
+      mbar_init(&bars->seg_empty[s], 14);  // the producer, the issuer, 4 converting and 8 softmax warps
     }
     for (int s = 0; s < kNotes; ++s) mbar_init(&bars->conv[s], 4);
     mbar_init(&bars->o_free, 8);
@@ -295,7 +322,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     fence_mbar_init();
   }
   let_next_launch_in();
-  if (warp == 2) {
+  if (warp == 1) {
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
   }
@@ -321,7 +348,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       bool past;
       const int t = pair(j, start, n, i0, past);
       if (first && blockIdx.x == 0 && i0 == 0 && past) report(p.status, kStatusBounds);
-      return (kItemCost + t) * p.Hkv;
+      return t > 0 ? (kItemCost + t) * p.Hkv : 0;
     };
 #pragma unroll 1
     for (int base = 0; base < pairs; base += 32) {
@@ -382,19 +409,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   };
 
   if (warp < 8) regs_dec<C::kRegsCtl>();
-  if (warp < 2) {
+  if (warp == 0) {
     // ------------------------------------------------------------ K and V codes
-    // lane i < 8 owns block i of a tile: its id is read a tile ahead, its scale with it
-    const bool is_v = warp == 1;
-    const int S = is_v ? C::VC : C::KS;
+    // lane i < 8 owns K's block i of a tile, lane 8 + i V's: its id is read a tile
+    // ahead, its scale with it
+    const bool is_v = lane >= kTileBlocks;
+    const int own = lane % kTileBlocks;
+    const bool works = lane < 2 * kTileBlocks;
     const void* map = is_v ? static_cast<const void*>(&tm_v) : &tm_k;
     const float* scales = is_v ? p.vs : p.ks;
-    uint64_t* full = is_v ? bars->c_full : bars->k_full;
-    uint64_t* empty = is_v ? bars->c_empty : bars->k_empty;
-    uint8_t* base = smem + (is_v ? C::kOffC : C::kOffK);
     Seg s;
-    int j = 0, issued = 0, st = 0;
-    uint32_t ph = 1u;  // parity of the stage's last release
+    int j = 0, k_issued = 0, c_issued = 0;
     bool ok = true;
     for (int i = 0; ok && seg_get(i, s); ++i) {
       seg_taken(i);
@@ -402,10 +427,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       const int blocks = (s.kend + kBS - 1) / kBS;
       float sc_next;
       auto block_id = [&](int tile) {
-        const int blk = tile * kTileBlocks + lane;
+        const int blk = tile * kTileBlocks + own;
         int id = -1;
         sc_next = -1.0f;
-        if (tile < s.t1 && lane < kTileBlocks && blk < blocks) {
+        if (tile < s.t1 && works && blk < blocks) {
           id = bt_row[blk];
           if (id < 0 || id >= p.num_blocks) {
             report(p.status, kStatusBounds);
@@ -421,32 +446,43 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         const int id = id_next;
         const float sc = sc_next;
         id_next = block_id(tile + 1);
-        const uint32_t there = __ballot_sync(0xffffffffu, id >= 0);
-        if (!wait_all(&empty[st], ph)) {
+        const uint32_t there = __ballot_sync(0xffffffffu, id >= 0) & 0xffu;  // (V's blocks are K's)
+        const uint32_t bytes = __popc(there) * (kBS * D);
+        const int ks = j % C::KS, cs = j % C::VC;
+        if (!wait_all(&bars->k_empty[ks], (j / C::KS) ^ 1)) {
           ok = false;
           break;
         }
-        if (is_v) {
-          if (lane < kTileBlocks) bars->vs[st][lane] = sc;
-        } else {
-          // (the tile that had this slot is kScales back: its weights are written)
-          if (lane < kTileBlocks) bars->ks[j % kScales][lane] = sc;
-          if (lane == 0) bars->there[j % kScales] = there;
-        }
+        // (the tile that had this slot is kScales back: its weights are written)
+        if (lane < kTileBlocks) bars->ks[j % kScales][lane] = sc;
+        if (lane == 0) bars->there[j % kScales] = there;
         __syncwarp();
         if (lane == 0) {
-          if (!is_v) mbar_arrive(&bars->sc_full[j % kScales]);
-          mbar_arrive_expect_tx(&full[st], __popc(there) * (kBS * D));
+          mbar_arrive(&bars->sc_full[j % kScales]);
+          mbar_arrive_expect_tx(&bars->k_full[ks], bytes);
         }
         __syncwarp();
-        if (id >= 0) tma_load_4d(base + st * C::kCodeBytes + lane * (kBS * D), map, &full[st], 0, 0, s.g, id);
-        issued = j + 1;
-        if (++st == S) st = 0, ph ^= 1u;
+        if (!is_v && id >= 0)
+          tma_load_4d(smem + C::kOffK + ks * C::kCodeBytes + own * (kBS * D), map, &bars->k_full[ks], 0, 0, s.g, id);
+        k_issued = j + 1;
+        if (!wait_all(&bars->c_empty[cs], (j / C::VC) ^ 1)) {
+          ok = false;
+          break;
+        }
+        if (is_v && works) bars->vs[cs][own] = sc;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&bars->c_full[cs], bytes);
+        __syncwarp();
+        if (is_v && id >= 0)
+          tma_load_4d(smem + C::kOffC + cs * C::kCodeBytes + own * (kBS * D), map, &bars->c_full[cs], 0, 0, s.g, id);
+        c_issued = j + 1;
       }
     }
-    if (lane == 0 && *abort)  // let every copy in flight land before the CTA exits
-      for (int x = max(0, issued - S); x < issued; ++x) drain_wait(&full[x % S], (x / S) & 1);
-  } else if (warp == 2) {
+    if (lane == 0 && *abort) {  // let every copy in flight land before the CTA exits
+      for (int x = max(0, k_issued - C::KS); x < k_issued; ++x) drain_wait(&bars->k_full[x % C::KS], (x / C::KS) & 1);
+      for (int x = max(0, c_issued - C::VC); x < c_issued; ++x) drain_wait(&bars->c_full[x % C::VC], (x / C::VC) & 1);
+    }
+  } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp goes through the loop, with values that are alike in all lanes
     // (uniform registers, which the descriptors have to be in), and one lane issues.
@@ -503,40 +539,38 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             const int y = x - 2;
             // the accumulators of the segment before have been read
             if (y == 0 && seg > 0) ok = wait_all(&bars->o_free, seg - 1);
-            ok = ok && wait_all(&bars->p_full[(j + y) & 1], (j + y) >> 1) && wait_v(j + y);
+            ok = ok && wait_v(j + y) && (x >= n || wait_k(j + x)) && wait_all(&bars->p_full[(j + y) & 1], (j + y) >> 1);
             if (!ok) break;
             tc_fence_after();
             issue_pv((j + y) & 1, j + y, keys(y), y < 2, true);
-          }
-          if (x < n) {
+          } else if (x < n) {
             ok = wait_k(j + x);
             if (!ok) break;
             tc_fence_after();
-            issue_s((j + x) & 1, j + x, keys(x), true);
           }
+          if (x < n) issue_s((j + x) & 1, j + x, keys(x), true);
         }
         j += n;
       } else {
-        // PV_A, S_A', PV_B, S_B': each tile's softmax runs under the other's MMAs
+        // PV_A, S_A', PV_B, S_B': each tile's softmax runs under the other's MMAs.  What both
+        // need but the softmax is waited for ahead.
+        ok = ok && wait_k(j);
+        if (!ok) break;
+        tc_fence_after();
+        issue_s(0, j, keys(0), false);
+        issue_s(1, j, keys(0), true);
 #pragma unroll 1
-        for (int x = -1; ok && x < n; ++x) {
+        for (int x = 0; ok && x < n; ++x, ++j) {
+          const bool more = x + 1 < n;
+          ok = wait_v(j) && (!more || wait_k(j + 1));
 #pragma unroll 1
           for (int w = 0; ok && w < 2; ++w) {
-            if (x >= 0) {
-              ok = wait_all(&bars->p_full[w], j) && (w > 0 || wait_v(j));
-              if (!ok) break;
-              tc_fence_after();
-              issue_pv(w, j, keys(x), x == 0, w == 1);
-            }
-            if (x + 1 < n) {
-              const int jn = x < 0 ? j : j + 1;
-              ok = w > 0 || wait_k(jn);
-              if (!ok) break;
-              tc_fence_after();
-              issue_s(w, jn, keys(x + 1), w == 1);
-            }
+            ok = wait_all(&bars->p_full[w], j);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(w, j, keys(x), x == 0, w == 1);
+            if (more) issue_s(w, j + 1, keys(x + 1), w == 1);
           }
-          if (x >= 0) ++j;
         }
       }
     }
@@ -558,7 +592,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         plan_t = -kItemCost;
         if (++plan_g == p.Hkv) {
           plan_g = 0;
-          if (++plan_j < p.B * p.MP) tiles = pair(plan_j, start, n, i0, past);
+          // (there is more to do, so an item follows)
+          do tiles = pair(++plan_j, start, n, i0, past);
+          while (tiles == 0 && plan_j + 1 < p.B * p.MP);
         }
       }
       if (plan_t < 0) {  // the item's own cost, or as much of it as falls into this run
@@ -594,7 +630,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       }
       if (s.b < 0) break;
     }
-  } else if (warp < 8) {
+  } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ V to bf16
     // A lane takes a row's 16 codes at a time.  A quarter warp is four neighbouring
     // chunks of rows r and r ^ 5: loads and stores then meet no bank twice.
@@ -626,41 +662,44 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         for (int x = 0; x < 4; ++x) {
           const int r = cw * 32 + x * 8 + r8;
           if (cw * 32 + x * 8 >= keys) break;
-          const float sc = bars->vs[cs][r / kBS];
-          const bool on = sc >= 0.0f || !(sc == sc);  // -1: no such block (a NaN scale is the cache's own)
-          const uint64_t sc2 = f2_pack(sc, sc);
+          const float sc = bars->vs[cs][r / kBS];  // -1: no such block
+          const bool on = sc != -1.0f;
+          const uint64_t sc2 = f2_pack(on ? sc : 0.0f, on ? sc : 0.0f);
+          uint32_t u[CH / 4][4];
 #pragma unroll
           for (int y = 0; y < CH / 4; ++y) {
-            const int c = c0 + 4 * y;
             uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (on && r < left) w = *reinterpret_cast<const uint4*>(src + C::code_off(r, c));
-            uint32_t u[4] = {w.x, w.y, w.z, w.w}, o[8];
-            if (watch) {
-              uint32_t any = 0u;
+            if (on && r < left) w = *reinterpret_cast<const uint4*>(src + C::code_off(r, c0 + 4 * y));
+            u[y][0] = w.x, u[y][1] = w.y, u[y][2] = w.z, u[y][3] = w.w;
+          }
+          const int token = tile * kBN + r;
+          if (watch && token >= first - 1) {  // not all rows see it: NaNs go in as zeros
+            uint32_t any = 0u;
+#pragma unroll
+            for (int y = 0; y < CH / 4; ++y)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const uint32_t bad = ((u[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                const uint32_t bad = nan_codes(u[y][k]);
                 any |= bad;
-                u[k] &= ~((bad >> 7) * 255u);
+                u[y][k] &= ~((bad >> 7) * 255u);
               }
-              const int token = tile * kBN + r;
-              if (any != 0u && token >= first - 1) {
-                const int at = token - (first - 1);
-                if (at < kSpread) atomicOr(&notes[at >> 5], 1u << (at & 31));
-              } else if (any != 0u) {  // all rows see it
-                u[0] = w.x, u[1] = w.y, u[2] = w.z, u[3] = w.w;
-              }
-            }
+            const int at = token - (first - 1);
+            if (any != 0u && at < kSpread) atomicOr(&notes[at >> 5], 1u << (at & 31));
+          }
+#pragma unroll
+          for (int y = 0; y < CH / 4; ++y) {
+            uint32_t o[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               float lo, hi;
-              half2_f32(f8_half2(k & 1 ? u[k >> 1] >> 16 : u[k >> 1]), lo, hi);
+              half2_f32(f8_half2(k & 1 ? u[y][k >> 1] >> 16 : u[y][k >> 1]), lo, hi);
               f2_unpack(fmul2(f2_pack(lo, hi), sc2), lo, hi);
-              o[k] = on ? pack_bf16x2(lo, hi) : 0u;
+              o[k] = pack_bf16x2(lo, hi);
             }
-            *reinterpret_cast<uint4*>(dst + swizzled_off(r, 2 * c, PagedTile<D>::kHalf, PagedTile<D>::kGroup)) =
+            const int c = 2 * (c0 + 4 * y);
+            *reinterpret_cast<uint4*>(dst + swizzled_off(r, c, PagedTile<D>::kHalf, PagedTile<D>::kGroup)) =
                 make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst + swizzled_off(r, 2 * c + 1, PagedTile<D>::kHalf, PagedTile<D>::kGroup)) =
+            *reinterpret_cast<uint4*>(dst + swizzled_off(r, c + 1, PagedTile<D>::kHalf, PagedTile<D>::kGroup)) =
                 make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
@@ -674,7 +713,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&bars->conv[i % kNotes]);
     }
-  } else {
+  } else if (warp >= 8) {
     // ------------------------------------------------------------ softmax
     regs_inc<C::kRegsSoft>();
     const int wg = (warp >> 2) - 2;
@@ -688,78 +727,118 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     // about the latest one or the one before: the parity is never read a phase off.
     auto o_wait = [&](int x) { return mbar_wait(&bars->o_done[wg], x & 1, abort, p.status); };
 
+    // The rows of q that this warp loads and splits: its 32, or (NT = 1) half of them, the
+    // other warpgroup's warp the rest.  Called when every S of the segment before is
+    // done; the copies land while that one ends.  A row's first half lies where its hi
+    // will, the second where its lo will.
+    constexpr int kQRows = NT == 2 ? 32 : 16;
+    const int q_row0 = NT == 2 ? 0 : wg * kQRows;
+    int q_loads = 0;
+    auto load_q = [&](const Seg& n) {
+      const int qi = n.i0 + t * p.tb + row / p.G, head = n.g * p.G + row % p.G;
+      const bool part = lane >= q_row0 && lane < q_row0 + kQRows;
+      const bool there = part && row < p.RT && qi < n.n;
+      uint8_t* dst = smem + C::kOffQ + t * 2 * C::kQBytes + row * D;
+      if (part && !there) {
+#pragma unroll
+        for (int c = 0; c < D; c += 16)
+          *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<uint4*>(dst + C::kQBytes + c) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();  // what was read there before the copies
+      const uint32_t m = __ballot_sync(0xffffffffu, there);
+      if (lane == 0) mbar_arrive_expect_tx(&bars->q_raw[t], __popc(m) * 2u * D);
+      __syncwarp();
+      if (there) {
+        const uint16_t* src = p.q + n.b * p.q_stride[0] + head * p.q_stride[1] + qi * p.q_stride[2];
+        bulk_load(dst, src, D, &bars->q_raw[t]);
+        bulk_load(dst + C::kQBytes, src + D / 2, D, &bars->q_raw[t]);
+      }
+      ++q_loads;
+    };
+
     Seg s;
     bool ok = true;
     int j = 0, n_mine = 0;  // tiles so far, and those that this warpgroup has had
     for (int seg = 0; ok && seg_get(seg, s); ++seg) {
       seg_taken(seg);
+      if (seg == 0) load_q(s);
       const int qi = s.i0 + t * p.tb + row / p.G;     // the row's query
       const bool mine = row < p.RT && qi < p.T;       // the row exists
       const bool sees = row < p.RT && qi < s.n;       // and has keys
       const bool warp_on = __any_sync(0xffffffffu, mine);
       const int head = s.g * p.G + row % p.G;
-      // (lanes without a row of their own: no limit that would hold up the warp)
-      const int row_lim = !mine ? 0x7fffffff : (sees ? (p.causal ? s.start + qi + 1 : s.kend) : 0);
+      // (a row that sees nothing has zeros for q, and no limit that would hold up its warp:
+      // its results are not used)
+      const int row_lim = !sees ? 0x7fffffff : (p.causal ? s.start + qi + 1 : s.kend);
 
-      // ---- this row of q, as hi and lo.  Every S of the segment before is done: this
-      // warpgroup has seen its last (NT = 1: and heard of the other's).  NT = 1:
-      // warpgroup 0 writes hi and 1 lo.
-      float mul = 0.0f;  // log2 units of a score of q's codes with unscaled K codes
+      // ---- q, from where load_q left it, as hi and lo: what a row's lanes (16 bytes each)
+      // write is what they have read.  Rolled, four steps at a time: it runs once a segment,
+      // and code that does costs its fetch.
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->q_raw[t], seg & 1, abort, p.status))) {
+        ok = false;
+        break;
+      }
       if (warp_on) {
-        const uint16_t* src = p.q + s.b * p.q_stride[0] + head * p.q_stride[1] + qi * p.q_stride[2];
-        float a = 0.0f;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 w = sees ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x = fabsf(bf16lo_to_f32(u[k])), y = fabsf(bf16hi_to_f32(u[k]));
-            a = fmaxf(a, fmaxf(x < INFINITY ? x : 0.0f, y < INFINITY ? y : 0.0f));
-          }
-        }
-        const float up = pow2(a > 0.0f ? f8_scale_exponent(a) : 0), inv = 1.0f / up;
-        mul = p.scale_log2 * up;
+        constexpr int LPR = D / 8, RPI = 32 / LPR, NI = kQRows / RPI;  // lanes a row, rows a step, steps
         uint8_t* qs = smem + C::kOffQ + t * 2 * C::kQBytes;
-#pragma unroll 2
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t hi4[4], lo4[4];
+        const int row0 = quarter * 32 + q_row0 + lane / LPR, c = lane % LPR;
+#pragma unroll 1
+        for (int it0 = 0; it0 < NI; it0 += 4) {
+          uint32_t h[4][4], l[4][4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint4 w = sees ? reinterpret_cast<const uint4*>(src)[2 * c + k] : make_uint4(0u, 0u, 0u, 0u);
+          for (int y = 0; y < 4; ++y) {
+            const int r = row0 + (it0 + y) * RPI;
+            const uint4 w = *reinterpret_cast<const uint4*>(qs + c / (LPR / 2) * C::kQBytes + r * D + c % (LPR / 2) * 16);
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            float x[8], a = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-              uint32_t h2[2], l2[2];
-#pragma unroll
-              for (int f = 0; f < 2; ++f) {
-                float x = bf16lo_to_f32(u[e + f]), y = bf16hi_to_f32(u[e + f]);
-                // infinite scores make no distribution either
-                x = fabsf(x) < INFINITY ? x * inv : NAN;
-                y = fabsf(y) < INFINITY ? y * inv : NAN;
-                h2[f] = f8_codes(x, y);
-                float hx, hy;
-                half2_f32(f8_half2(h2[f]), hx, hy);
-                l2[f] = f8_codes(x - hx, y - hy);
-              }
-              hi4[2 * k + e / 2] = h2[0] | h2[1] << 16;
-              lo4[2 * k + e / 2] = l2[0] | l2[1] << 16;
+            for (int k = 0; k < 4; ++k) {
+              x[2 * k] = bf16lo_to_f32(u[k]);
+              x[2 * k + 1] = bf16hi_to_f32(u[k]);
             }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const bool finite = fabsf(x[k]) < INFINITY;
+              a = fmaxf(a, finite ? fabsf(x[k]) : 0.0f);
+              x[k] = finite ? x[k] : NAN;  // infinite scores make no distribution either
+            }
+#pragma unroll
+            for (int m = 1; m < LPR; m *= 2) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, m));
+            const int e = a > 0.0f ? f8_scale_exponent(a) : 0;
+            const float inv = pow2(-e);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float x0 = x[2 * k] * inv, x1 = x[2 * k + 1] * inv;
+              h[y][k] = f8_codes(x0, x1);
+              float y0, y1;
+              half2_f32(f8_half2(h[y][k]), y0, y1);
+              l[y][k] = f8_codes(x0 - y0, x1 - y1);
+            }
+            if (c == 0) bars->qmul[t][r] = p.scale_log2 * pow2(e);
           }
-          const uint32_t at = C::code_off(row, c);
-          if (NT == 2 || wg == 0) *reinterpret_cast<uint4*>(qs + at) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
-          if (NT == 2 || wg == 1)
-            *reinterpret_cast<uint4*>(qs + C::kQBytes + at) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+          __syncwarp();
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t at = C::code_off(row0 + (it0 + y) * RPI, c / 2) + c % 2 * 8;
+            *reinterpret_cast<uint2*>(qs + at) = make_uint2(h[y][0] | h[y][1] << 16, h[y][2] | h[y][3] << 16);
+            *reinterpret_cast<uint2*>(qs + C::kQBytes + at) = make_uint2(l[y][0] | l[y][1] << 16, l[y][2] | l[y][3] << 16);
+          }
         }
         fence_proxy_async_smem();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->q_full[t]);
+      if (NT == 1 && !__all_sync(0xffffffffu, mbar_wait(&bars->q_full[0], seg & 1, abort, p.status))) {
+        ok = false;
+        break;
+      }
+      const float mul = bars->qmul[t][row];  // log2 units of a score of q's codes with unscaled K codes
 
       const int mine_before = n_mine;
       float m_run = -INFINITY, l_run = 0.0f;
-      for (int tile = s.t0; tile < s.t1; ++tile, ++j) {
+      for (int tile = s.t0; ok && tile < s.t1; ++tile, ++j) {
         if (NT == 1 && (j & 1) != wg) continue;
+        const int keys = tile_keys(s.kend, tile);
         if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[wg], n_mine & 1, abort, p.status) &&
                                          mbar_wait(&bars->sc_full[j % kScales], (j / kScales) & 1, abort, p.status))) {
           ok = false;
@@ -767,14 +846,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         tc_fence_after();
         if (warp_on) {
-          const int keys = tile_keys(s.kend, tile);
           const uint32_t there = bars->there[j % kScales];
           const int lim = row_lim - tile * kBN;
           const bool masked = __any_sync(0xffffffffu, lim < kBN) || there != 0xffu;
           const float* ks = bars->ks[j % kScales];
-          float alpha = 1.0f, rs;
-          // the reference max moves only when the tile's exceeds it by the margin
+          float alpha = 1.0f;
+          bool raised = false;  // the reference max may have moved (alike in the warp)
+          // it moves only when the step's exceeds it by the margin
           auto raise = [&](float mt) {
+            raised = true;
             if (mt > m_run + kRescaleMargin || (m_run == -INFINITY && mt != -INFINITY)) {
               alpha = fast_exp2(m_run - mt);
               m_run = mt;
@@ -788,7 +868,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             for (int i = 0; i < 32; i += 2) {
               const float f = i < 16 ? f0 : f1;
               float x0, x1;
-              f2_unpack(ffma2(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f2_pack(f, f), neg2), x0, x1);
+              f2_unpack(ffma2(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f2_pack(f, f), neg2), x0,
+                        x1);
               const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
               pw[i >> 1] = pack_bf16x2(p0, p1);
               sum[(i >> 1) & 3] = fadd2(sum[(i >> 1) & 3], f2_pack(p0, p1));
@@ -797,10 +878,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           };
           // scores in log2 units, -inf where the row may not look
           auto scale32 = [&](uint32_t (&x)[32], int c, float f0, float f1) {
-            const int lim0 = (there >> (2 * c)) & 1u ? lim - c * 32 : 0, lim1 = (there >> (2 * c + 1)) & 1u ? lim - c * 32 : 0;
+            const int lim0 = (there >> (2 * c)) & 1u ? lim - c * 32 : 0;
+            const int lim1 = (there >> (2 * c + 1)) & 1u ? lim - c * 32 : 0;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              x[i] = i < (i < 16 ? lim0 : lim1) ? __float_as_uint(__uint_as_float(x[i]) * (i < 16 ? f0 : f1)) : 0xff800000u;
+              x[i] = i < (i < 16 ? lim0 : lim1) ? __float_as_uint(__uint_as_float(x[i]) * (i < 16 ? f0 : f1))
+                                                : 0xff800000u;
           };
           auto max32 = [&](const uint32_t (&x)[32], float (&mx)[4]) {
 #pragma unroll
@@ -841,25 +924,27 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
               }
             }
           } else {
-            // Bound by this chain's latency: scores go to registers, the first 32 ahead of
-            // the others, and are weighed against the reference max at hand, without a
-            // max pass; if some row's sum says its scores outgrew it, once more with one.
+            // Bound by this chain's latency: scores go to registers, half of them ahead of the
+            // others, and are weighed against the reference max at hand, without a max
+            // pass; if some row's sum says its scores outgrew it, once more with one.
             uint32_t sr[4][32];
             tmem_ld32(tmem + lane_addr + s_col, sr[0]);
-            const float4 ka = *reinterpret_cast<const float4*>(ks), kb = *reinterpret_cast<const float4*>(ks + 4);
-            const float f[8] = {mul * ka.x, mul * ka.y, mul * ka.z, mul * ka.w,
-                                mul * kb.x, mul * kb.y, mul * kb.z, mul * kb.w};
+            tmem_ld32(tmem + lane_addr + s_col + 32, sr[1]);
             const bool fast = !masked && __all_sync(0xffffffffu, m_run != -INFINITY);
             tmem_wait_ld(sr[0]);
-#pragma unroll
-            for (int c = 1; c < 4; ++c) tmem_ld32(tmem + lane_addr + s_col + c * 32, sr[c]);
+            tmem_wait_ld(sr[1]);
+            tmem_ld32(tmem + lane_addr + s_col + 64, sr[2]);
+            tmem_ld32(tmem + lane_addr + s_col + 96, sr[3]);
             bool done = false;
             if (fast) {
-              weigh32(sr[0], 0, f[0], f[1], -m_run, sum);
 #pragma unroll
-              for (int c = 1; c < 4; ++c) tmem_wait_ld(sr[c]);
-#pragma unroll
-              for (int c = 1; c < 4; ++c) weigh32(sr[c], c, f[2 * c], f[2 * c + 1], -m_run, sum);
+              for (int c = 0; c < 4; ++c) {
+                if (c == 2) {
+                  tmem_wait_ld(sr[2]);
+                  tmem_wait_ld(sr[3]);
+                }
+                weigh32(sr[c], c, mul * ks[2 * c], mul * ks[2 * c + 1], -m_run, sum);
+              }
               float a0, a1;
               f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
               done = __all_sync(0xffffffffu, a0 + a1 <= 18446744073709551616.0f);  // 2^64; false for a NaN
@@ -869,13 +954,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
               }
             } else {
-#pragma unroll
-              for (int c = 1; c < 4; ++c) tmem_wait_ld(sr[c]);
+              tmem_wait_ld(sr[2]);
+              tmem_wait_ld(sr[3]);
             }
             if (!done) {
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                scale32(sr[c], c, f[2 * c], f[2 * c + 1]);
+                scale32(sr[c], c, mul * ks[2 * c], mul * ks[2 * c + 1]);
                 max32(sr[c], mx);
               }
               raise(fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])));
@@ -884,11 +969,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
               for (int c = 0; c < 4; ++c) weigh32(sr[c], c, 1.0f, 1.0f, neg, sum);
             }
           }
-          float a0, a1;
-          f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
-          rs = a0 + a1;
-          l_run = l_run * alpha + rs;
-          if (n_mine > mine_before && __any_sync(0xffffffffu, alpha != 1.0f)) {
+          if (raised && n_mine > mine_before && __any_sync(0xffffffffu, alpha != 1.0f)) {
             if (!__all_sync(0xffffffffu, o_wait(n_mine - 1))) {
               ok = false;
               break;
@@ -905,6 +986,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             }
           }
           tmem_wait_st();
+          float a0, a1;
+          f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
+          l_run = l_run * alpha + (a0 + a1);
         }
         tc_fence_before();
         __syncwarp();
@@ -955,8 +1039,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         tc_fence_after();
       }
+      {
+        Seg ahead;
+        if (seg_get(seg + 1, ahead)) load_q(ahead);
+      }
       // tokens from i0 on that this row sees and whose V holds a NaN (none of an earlier part's)
-      const bool straddles = p.causal && s.t1 * kBN > s.start + s.i0 + 1 && s.kend > 0;
+      const bool straddles = p.causal && s.t1 * kBN > s.start + s.i0 + 1;
       bool fix = false;
       if (straddles) {
         if (!__all_sync(0xffffffffu, mbar_wait(&bars->conv[seg % kNotes], (seg / kNotes) & 1, abort, p.status))) {
@@ -968,24 +1056,28 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         for (int x = 0; x < 4 * kSpread / 32; ++x) any |= bars->bad[seg % kNotes][0][x];
         fix = any != 0u;  // alike in the whole warp
       }
-      const bool empty = l_run == 0.0f;
+      const bool empty = !sees || l_run == 0.0f;
       const bool whole = s.slot < 0;
       const float inv = empty ? 0.0f : 1.0f / l_run;
       const float lse2 = empty ? -INFINITY : m_run + __log2f(l_run);
       const int64_t obase = s.b * p.out_stride[0] + head * p.out_stride[1] + qi * p.out_stride[2];
       if (warp_on) {
-        // 16 columns at a time, rolled (it runs once a segment: its code's fetch counts)
+        // 32 columns at a time, rolled (it runs once a segment: its code's fetch counts)
 #pragma unroll 1
-        for (int c = NT == 1 ? wg * (D / 2) : 0; c < (NT == 1 ? (wg + 1) * (D / 2) : D); c += 16) {
-          uint32_t o[16];
+        for (int c = NT == 1 ? wg * (D / 2) : 0; c < (NT == 1 ? (wg + 1) * (D / 2) : D); c += 32) {
+          uint32_t o[32];
           if constexpr (NT == 2) {
-            tmem_ld16_now(tmem + lane_addr + o_col + c, o);
+            tmem_ld32(tmem + lane_addr + o_col + c, o);
+            tmem_wait_ld(o);
           } else {
-            uint32_t o1[16];
-            tmem_ld16x2_now(tmem + lane_addr + C::kColO + c, o, tmem + lane_addr + C::kColO + D + c, o1);
+            uint32_t o1[32];
+            tmem_ld32(tmem + lane_addr + C::kColO + c, o);
+            tmem_ld32(tmem + lane_addr + C::kColO + D + c, o1);
+            tmem_wait_ld(o);
+            tmem_wait_ld(o1);
             // an accumulator of weight 0 may hold anything
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < 32; ++i)
               o[i] = __float_as_uint((f0 != 0.0f ? f0 * __uint_as_float(o[i]) : 0.0f) +
                                      (f1 != 0.0f ? f1 * __uint_as_float(o1[i]) : 0.0f));
           }
@@ -996,26 +1088,26 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 const int token = s.start + s.i0 + x;
                 uint32_t word = 0u;
                 for (int w = 0; w < 4; ++w) word |= bars->bad[seg % kNotes][w][x >> 5];
-                if (!((word >> (x & 31)) & 1u) || token >= row_lim) continue;
+                if (!((word >> (x & 31)) & 1u) || token >= row_lim || !sees) continue;
                 const int id = p.bt[static_cast<int64_t>(s.b) * p.bt_stride + token / kBS];
                 if (id < 0 || id >= p.num_blocks) continue;
                 const uint8_t* v =
                     p.vq + ((static_cast<int64_t>(id) * p.Hkv + s.g) * kBS + token % kBS) * static_cast<int64_t>(D) + c;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < 32; ++i)
                   if ((v[i] & 0x7f) == 0x7f) o[i] = 0x7fc00000u;
               }
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = empty ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+            for (int i = 0; i < 32; ++i) o[i] = empty ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
             if (!whole) {
               float* dst = p.part_o + (static_cast<int64_t>(s.slot) * D + c) * p.pitch + t * kBM + row;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) dst[i * (NT * kBM)] = __uint_as_float(o[i]);
+              for (int i = 0; i < 32; ++i) dst[i * (NT * kBM)] = __uint_as_float(o[i]);
             } else if (p.out_bf16) {
               uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + obase + c);
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
+              for (int i = 0; i < 4; ++i)
                 dst[i] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
                                     pack_bf16x2(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
                                     pack_bf16x2(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
@@ -1023,7 +1115,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             } else {
               float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + obase + c);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < 8; ++i)
                 dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                      __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
             }
@@ -1043,11 +1135,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         if (lane == 0) mbar_arrive(&bars->o_free);
       }
     }
+    if (lane == 0 && *abort && q_loads > 0) drain_wait(&bars->q_raw[t], (q_loads - 1) & 1);
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 2) {
+  if (warp == 1) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -1083,7 +1176,10 @@ cudaError_t launch(const F8AttnArgs& a, const ChunkParams& p, cudaStream_t strea
   e = launch_early(kern, dim3(static_cast<unsigned>(a.n_cta)), C::kThreads, C::kSmemBytes, stream, mk, mv, p);
   if (e != cudaSuccess) return e;
   // groups of 32 rows up to the last that any row tile uses
-  const dim3 grid(static_cast<unsigned>(a.n_cta), static_cast<unsigned>(((NT - 1) * kBM + p.RT + 31) / 32));
+  // (and, for groups that see nothing, a few CTAs more)
+  const int64_t heads = static_cast<int64_t>(p.B) * p.MP * p.Hq;
+  const dim3 grid(static_cast<unsigned>(a.n_cta + std::min<int64_t>(a.n_cta, (heads + 31) / 32)),
+                  static_cast<unsigned>(((NT - 1) * kBM + p.RT + 31) / 32));
   return launch_early(chunk_merge_kernel<D>, grid, kMergeThreads, 0, stream, p);
 }
 
@@ -1127,6 +1223,7 @@ cudaError_t launch_chunk_f8(const F8AttnArgs& a, cudaStream_t stream) {
   p.out_bf16 = a.out.dtype == ATTN_BF16;
   p.lse = a.lse;
   p.pitch = nt * kBM;
+  p.ctas = a.n_cta;
   p.part_o = static_cast<float*>(a.partials);
   p.part_lse = p.part_o + part_rows(p.T, p.G, a.n_cta) * a.cache.D;
   p.cuts = reinterpret_cast<CutItem*>(static_cast<uint8_t*>(a.partials) + part_bytes(p.T, p.G, a.cache.D, a.n_cta));

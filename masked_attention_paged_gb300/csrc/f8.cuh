@@ -32,4 +32,7 @@ __device__ __forceinline__ void half2_f32(uint32_t x, float& lo, float& hi) {
       : "r"(x));
 }
 
+// bytes that are NaN codes, as 0x80 each
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
 }  // namespace attn
