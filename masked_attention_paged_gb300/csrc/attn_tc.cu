@@ -1120,7 +1120,9 @@ bool make_paged_map(CUtensorMap* map, void* base, int64_t num_blocks, int Hkv, i
   return r == CUDA_SUCCESS;
 }
 
-bool make_rows_map(CUtensorMap* map, const View4& t, int64_t Hkv, int tokens) {
+namespace {
+// 5-D map over a [B, H, T, D] view as make_rows_map, boxes of `inner` columns
+bool make_grouped_rows_map(CUtensorMap* map, const View4& t, int64_t Hkv, int tokens, int inner) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return false;
   const int64_t G = t.shape[1] / Hkv;
@@ -1132,12 +1134,23 @@ bool make_rows_map(CUtensorMap* map, const View4& t, int64_t Hkv, int tokens) {
     dims[i + 1] = static_cast<cuuint64_t>(size[i]);
     strides[i] = size[i] > 1 ? static_cast<cuuint64_t>(stride[i]) * 2 : cuuint64_t(1) << 30;  // extent 1: any
   }
-  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tokens), 1, 1};
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(inner), static_cast<cuuint32_t>(G),
+                             static_cast<cuuint32_t>(tokens), 1, 1};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, t.data, dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   inner == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+}  // namespace
+
+bool make_rows_map(CUtensorMap* map, const View4& t, int64_t Hkv, int tokens) {
+  return make_grouped_rows_map(map, t, Hkv, tokens, 64);
+}
+
+bool make_half_rows_map(CUtensorMap* map, const View4& t, int64_t Hkv, int tokens, int D) {
+  return make_grouped_rows_map(map, t, Hkv, tokens, D / 2);
 }
 
 bool make_code_map(CUtensorMap* map, void* base, int64_t num_blocks, int Hkv, int D) {

@@ -17,7 +17,7 @@
 // leaves partials (normalised rows and log2 LSE), which a second launch joins in
 // order, so results do not depend on timing.
 //
-// Warps: 0 streams the codes, 1 issues the MMAs, 3 plans the segments, 4-7 convert V, 8-11 and 12-15 softmax (thread r owns row
+// Warps: 0 streams the codes, 1 issues the MMAs, 2 waits for it, 3 plans the segments, 4-7 convert V, 8-11 and 12-15 softmax (thread r owns row
 // r: TMEM lane r; it also splits its row of q).  With NT = 2 each warpgroup has a row
 // tile.  With NT = 1 both have the same rows and take the key tiles in turn, each with a
 // score buffer, an accumulator and a running max and sum of its own, joined by the LSE
@@ -283,8 +283,8 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
-    paged_chunk_f8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                          const __grid_constant__ ChunkParams p) {
+    paged_chunk_f8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ChunkParams p) {
   using C = Cfg<D, NT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -295,11 +295,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 
   if (threadIdx.x == 32) {
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bars->q_raw[t], NT == 1 ? 8 : 4);
+      mbar_init(&bars->q_raw[t], 1);
       mbar_init(&bars->q_full[t], NT == 1 ? 8 : 4);
       mbar_init(&bars->o_done[t], 1);
       mbar_init(&bars->s_full[t], 1);
-      mbar_init(&bars->p_full[t], 4);
+      mbar_init(&bars->p_full[t], 5);  // four softmax warps, and warp 2
       mbar_init(&bars->xch_full[t], 4);
     }
     for (int s = 0; s < 4; ++s) {
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     for (int s = 0; s < kScales; ++s) mbar_init(&bars->sc_full[s], 1);
     for (int s = 0; s < kSegs; ++s) {
       mbar_init(&bars->seg_full[s], 1);
-      mbar_init(&bars->seg_empty[s], 14);  // the producer, the issuer, 4 converting and 8 softmax warps
+      mbar_init(&bars->seg_empty[s], 15);  // the producer, the issuer, warp 2, 4 converting and 8 softmax warps
     }
     for (int s = 0; s < kNotes; ++s) mbar_init(&bars->conv[s], 4);
     mbar_init(&bars->o_free, 8);
@@ -385,6 +385,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     }
     if (lane == 0) {
       p.cuts[blockIdx.x].pieces = 0;  // unless an item starts here and goes on
+      tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
@@ -522,7 +523,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       __syncwarp();
     };
     auto wait_k = [&](int x) { return wait_all(&bars->k_full[x % C::KS], x / C::KS); };
-    auto wait_v = [&](int x) { return wait_all(&bars->v_full[x % C::VS], x / C::VS); };
     int j = 0;
     bool ok = true;
     Seg sg;
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             const int y = x - 2;
             // the accumulators of the segment before have been read
             if (y == 0 && seg > 0) ok = wait_all(&bars->o_free, seg - 1);
-            ok = ok && wait_v(j + y) && (x >= n || wait_k(j + x)) && wait_all(&bars->p_full[(j + y) & 1], (j + y) >> 1);
+            ok = ok && wait_all(&bars->p_full[(j + y) & 1], (j + y) >> 1);
             if (!ok) break;
             tc_fence_after();
             issue_pv((j + y) & 1, j + y, keys(y), y < 2, true);
@@ -552,8 +552,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         j += n;
       } else {
-        // PV_A, S_A', PV_B, S_B': each tile's softmax runs under the other's MMAs.  What both
-        // need but the softmax is waited for ahead.
+        // PV_A, S_A', PV_B, S_B': each tile's softmax runs under the other's MMAs
         ok = ok && wait_k(j);
         if (!ok) break;
         tc_fence_after();
@@ -562,7 +561,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll 1
         for (int x = 0; ok && x < n; ++x, ++j) {
           const bool more = x + 1 < n;
-          ok = wait_v(j) && (!more || wait_k(j + 1));
 #pragma unroll 1
           for (int w = 0; ok && w < 2; ++w) {
             ok = wait_all(&bars->p_full[w], j);
@@ -580,6 +578,31 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       drain_wait(&bars->drained, 0);
     }
     __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ the issuer's waits
+    // For each tile, that its V is there and the K of the scores that the issuer goes on
+    // with: one arrival more on p_full, so that the issuer has one wait (each takes it
+    // over 200 cycles, ready or not) instead of three.
+    Seg s;
+    int j = 0;
+    bool ok = true;
+    for (int i = 0; ok && seg_get(i, s); ++i) {
+      seg_taken(i);
+      const int n = s.t1 - s.t0;
+      for (int x = 0; ok && x < n; ++x, ++j) {
+        constexpr int kAhead = NT == 1 ? 2 : 1;  // tiles that the scores are ahead
+        const int k = j + kAhead;
+        ok = wait_all(&bars->v_full[j % C::VS], j / C::VS) &&
+             (x + kAhead >= n || wait_all(&bars->k_full[k % C::KS], k / C::KS));
+        for (int w = 0; w < 2; ++w) {
+          if (NT == 1 && w != (j & 1)) continue;
+          const int phase = NT == 1 ? j >> 1 : j;  // the one before is over: this arrival is not its
+          ok = ok && (phase == 0 || wait_all(&bars->p_full[w], phase - 1));
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(&bars->p_full[w]);
+        }
+      }
+    }
   } else if (warp == 3) {
     // ------------------------------------------------------------ planner
     int start = 0, n = 0, i0 = 0, tiles = 0;
@@ -727,32 +750,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     // about the latest one or the one before: the parity is never read a phase off.
     auto o_wait = [&](int x) { return mbar_wait(&bars->o_done[wg], x & 1, abort, p.status); };
 
-    // The rows of q that this warp loads and splits: its 32, or (NT = 1) half of them, the
-    // other warpgroup's warp the rest.  Called when every S of the segment before is
-    // done; the copies land while that one ends.  A row's first half lies where its hi
-    // will, the second where its lo will.
+    // The rows of q that this warp splits: its 32, or (NT = 1) half of them, the other
+    // warpgroup's warp the rest.
     constexpr int kQRows = NT == 2 ? 32 : 16;
     const int q_row0 = NT == 2 ? 0 : wg * kQRows;
+    // A row tile's queries, two boxes: rows' first halves to where hi will be, second
+    // halves to lo's place.  Called when every S of the segment before is done; they land
+    // while that one ends.
+    const bool loads_q = quarter == 0 && lane == 0 && (NT == 2 || wg == 0);
     int q_loads = 0;
     auto load_q = [&](const Seg& n) {
-      const int qi = n.i0 + t * p.tb + row / p.G, head = n.g * p.G + row % p.G;
-      const bool part = lane >= q_row0 && lane < q_row0 + kQRows;
-      const bool there = part && row < p.RT && qi < n.n;
-      uint8_t* dst = smem + C::kOffQ + t * 2 * C::kQBytes + row * D;
-      if (part && !there) {
+      if (!loads_q) return;
+      mbar_arrive_expect_tx(&bars->q_raw[t], static_cast<uint32_t>(p.RT) * 2u * D);
 #pragma unroll
-        for (int c = 0; c < D; c += 16)
-          *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<uint4*>(dst + C::kQBytes + c) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_proxy_async_smem();  // what was read there before the copies
-      const uint32_t m = __ballot_sync(0xffffffffu, there);
-      if (lane == 0) mbar_arrive_expect_tx(&bars->q_raw[t], __popc(m) * 2u * D);
-      __syncwarp();
-      if (there) {
-        const uint16_t* src = p.q + n.b * p.q_stride[0] + head * p.q_stride[1] + qi * p.q_stride[2];
-        bulk_load(dst, src, D, &bars->q_raw[t]);
-        bulk_load(dst + C::kQBytes, src + D / 2, D, &bars->q_raw[t]);
-      }
+      for (int x = 0; x < 2; ++x)
+        tma_load_5d(smem + C::kOffQ + (2 * t + x) * C::kQBytes, &tm_q, &bars->q_raw[t], x * (D / 2), 0,
+                    n.i0 + t * p.tb, n.g, n.b);
       ++q_loads;
     };
 
@@ -782,35 +795,31 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         constexpr int LPR = D / 8, RPI = 32 / LPR, NI = kQRows / RPI;  // lanes a row, rows a step, steps
         uint8_t* qs = smem + C::kOffQ + t * 2 * C::kQBytes;
         const int row0 = quarter * 32 + q_row0 + lane / LPR, c = lane % LPR;
+        const uint32_t seen = __ballot_sync(0xffffffffu, sees);
 #pragma unroll 1
         for (int it0 = 0; it0 < NI; it0 += 4) {
           uint32_t h[4][4], l[4][4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int r = row0 + (it0 + y) * RPI;
-            const uint4 w = *reinterpret_cast<const uint4*>(qs + c / (LPR / 2) * C::kQBytes + r * D + c % (LPR / 2) * 16);
+            uint4 w = *reinterpret_cast<const uint4*>(qs + c / (LPR / 2) * C::kQBytes + C::code_off(r, c % (LPR / 2)));
+            // rows that see nothing may hold anything
+            if (!((seen >> (r & 31)) & 1u)) w = make_uint4(0u, 0u, 0u, 0u);
+            uint32_t top = bf16x2_max_abs(bf16x2_max_abs(w.x & 0x7fff7fffu, w.y), w.z);  // (a NaN is not the largest)
+            top = bf16x2_max_abs(top, w.w);
+#pragma unroll
+            for (int m = 1; m < LPR; m *= 2) top = bf16x2_max_abs(top, __shfl_xor_sync(0xffffffffu, top, m));
+            const float a = fmaxf(bf16lo_to_f32(top), bf16hi_to_f32(top));
+            const int e = a > 0.0f && a < INFINITY ? f8_scale_exponent(a) : 0;
+            // infinite scores make no distribution either
+            const float inv = a < INFINITY ? pow2(-e) : NAN;
+            const uint64_t inv2 = f2_pack(inv, inv);
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-            float x[8], a = 0.0f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              x[2 * k] = bf16lo_to_f32(u[k]);
-              x[2 * k + 1] = bf16hi_to_f32(u[k]);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const bool finite = fabsf(x[k]) < INFINITY;
-              a = fmaxf(a, finite ? fabsf(x[k]) : 0.0f);
-              x[k] = finite ? x[k] : NAN;  // infinite scores make no distribution either
-            }
-#pragma unroll
-            for (int m = 1; m < LPR; m *= 2) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, m));
-            const int e = a > 0.0f ? f8_scale_exponent(a) : 0;
-            const float inv = pow2(-e);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float x0 = x[2 * k] * inv, x1 = x[2 * k + 1] * inv;
+              float x0, x1, y0, y1;
+              f2_unpack(fmul2(f2_pack(bf16lo_to_f32(u[k]), bf16hi_to_f32(u[k])), inv2), x0, x1);
               h[y][k] = f8_codes(x0, x1);
-              float y0, y1;
               half2_f32(f8_half2(h[y][k]), y0, y1);
               l[y][k] = f8_codes(x0 - y0, x1 - y1);
             }
@@ -839,8 +848,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       for (int tile = s.t0; ok && tile < s.t1; ++tile, ++j) {
         if (NT == 1 && (j & 1) != wg) continue;
         const int keys = tile_keys(s.kend, tile);
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[wg], n_mine & 1, abort, p.status) &&
-                                         mbar_wait(&bars->sc_full[j % kScales], (j / kScales) & 1, abort, p.status))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->sc_full[j % kScales], (j / kScales) & 1, abort, p.status) &&
+                                         mbar_wait(&bars->s_full[wg], n_mine & 1, abort, p.status))) {
           ok = false;
           break;
         }
@@ -1135,7 +1144,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         if (lane == 0) mbar_arrive(&bars->o_free);
       }
     }
-    if (lane == 0 && *abort && q_loads > 0) drain_wait(&bars->q_raw[t], (q_loads - 1) & 1);
+    if (q_loads > 0 && *abort) drain_wait(&bars->q_raw[t], (q_loads - 1) & 1);
   }
 
   tc_fence_before();
@@ -1157,8 +1166,8 @@ size_t part_bytes(int64_t T, int64_t G, int D, int n_cta) {
 template <int D, int NT>
 cudaError_t launch(const F8AttnArgs& a, const ChunkParams& p, cudaStream_t stream) {
   using C = Cfg<D, NT>;
-  CUtensorMap mk, mv;
-  if (!make_code_map(&mk, a.cache.k, a.cache.num_blocks, a.cache.Hkv, D) ||
+  CUtensorMap mq, mk, mv;
+  if (!make_half_rows_map(&mq, a.q, a.cache.Hkv, p.tb, D) || !make_code_map(&mk, a.cache.k, a.cache.num_blocks, a.cache.Hkv, D) ||
       !make_code_map(&mv, a.cache.v, a.cache.num_blocks, a.cache.Hkv, D))
     return cudaErrorInvalidValue;
   auto kern = paged_chunk_f8_kernel<D, NT>;
@@ -1173,7 +1182,7 @@ cudaError_t launch(const F8AttnArgs& a, const ChunkParams& p, cudaStream_t strea
   }
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = launch_early(kern, dim3(static_cast<unsigned>(a.n_cta)), C::kThreads, C::kSmemBytes, stream, mk, mv, p);
+  e = launch_early(kern, dim3(static_cast<unsigned>(a.n_cta)), C::kThreads, C::kSmemBytes, stream, mq, mk, mv, p);
   if (e != cudaSuccess) return e;
   // groups of 32 rows up to the last that any row tile uses
   // (and, for groups that see nothing, a few CTAs more)

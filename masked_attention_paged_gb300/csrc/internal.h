@@ -177,6 +177,8 @@ bool make_paged_map(CUtensorMap* map, void* base, int64_t num_blocks, int Hkv, i
 // KV head, batch): box 64 columns x the G = H / Hkv heads of `tokens` tokens, 128-byte
 // swizzle, so row r of a box is token r / G, head r % G; zero fill past T
 bool make_rows_map(CUtensorMap* map, const View4& t, int64_t Hkv, int tokens);
+// the same with boxes of half a row, swizzled by its D bytes (D 64 or 128)
+bool make_half_rows_map(CUtensorMap* map, const View4& t, int64_t Hkv, int tokens, int D);
 
 constexpr int kTreeMaxDrafts = 256;  // drafts per sequence of the tree attention
 struct TreeArgs {
