@@ -707,8 +707,8 @@ attn_status kv_evict(const attn_kv_cache *cache, float *acc, const int32_t *bloc
  * entry to draw from (next_token -1).
  *   workspace     >= draft_verify_workspace_size(...) bytes (the status word)
  * 1 <= T <= 256, 1 <= V <= 2^30; outputs do not overlap each other or the inputs.  Tests and
- * sums carry 46 bits or more, so that a result hangs on rounding only where a number
- * lies within 1e-13 of a border; it does not depend on timing.
+ * sums carry 44 bits or more, so that a result hangs on rounding only where a number
+ * lies within 1e-12 of a border; it does not depend on timing.
  */
 size_t draft_verify_workspace_size(int32_t batch, int32_t num_drafts, int64_t vocab);
 attn_status draft_verify(const attn_tensor *target_probs, const attn_tensor *draft_probs,

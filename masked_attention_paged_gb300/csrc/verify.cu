@@ -13,8 +13,9 @@
 //
 // Tests and sums decide between whole numbers, so they carry twice a float's digits:
 // p - C q as an unevaluated sum of two floats (the products' and differences' errors
-// are exact by FMA), and sums of such pairs.  Doubles would bound the kernel (the SM
-// does two a cycle): only warp 0's scalars are.
+// are exact by FMA), and sums and products of such pairs.  Doubles would bound the
+// kernel: the SM does two a cycle, and a chain of them (a test, a quotient) took the
+// walk 2 us at each refusal.
 #include <math.h>
 
 #include "common.cuh"
@@ -23,11 +24,11 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 16;    // of a cluster
 constexpr int kMaxDrafts = kVerifyMaxDrafts;
-constexpr int kUnroll = 8;
+constexpr int kUnroll = 8;  // entries of a row that a lane has in flight
 
 struct VerifyParams {
   const void* p;
@@ -96,10 +97,20 @@ __device__ __forceinline__ Pair shfl(Pair a, int l) {
   return make_float2(__shfl_sync(0xffffffffu, a.x, l), __shfl_sync(0xffffffffu, a.y, l));
 }
 __device__ __forceinline__ bool greater(Pair a, Pair b) { return (a.x - b.x) + (a.y - b.y) > 0.f; }
-__device__ __forceinline__ double value(Pair a) { return static_cast<double>(a.x) + static_cast<double>(a.y); }
-__device__ __forceinline__ Pair pair_of(double x) {
-  const float h = static_cast<float>(x);
-  return make_float2(h, static_cast<float>(x - static_cast<double>(h)));
+__device__ __forceinline__ Pair of(float x) { return make_float2(x, 0.f); }
+__device__ __forceinline__ Pair negative(Pair a) { return make_float2(-a.x, -a.y); }
+__device__ __forceinline__ Pair times(Pair a, Pair b) {
+  const float h = __fmul_rn(a.x, b.x);
+  return tidy(make_float2(h, fmaf(a.x, b.x, -h) + fmaf(a.x, b.y, a.y * b.x)));
+}
+__device__ __forceinline__ Pair over(Pair a, Pair b) {  // the quotient, and that of what it leaves
+  const float h = __fdividef(a.x, b.x);
+  const Pair rest = add(a, negative(times(b, of(h))));
+  const float l = __fdividef(rest.x, b.x);
+  const Pair rest2 = add(rest, negative(times(b, of(l))));
+  Pair q = tidy(make_float2(h, l));
+  q.y += __fdividef(rest2.x, b.x);
+  return tidy(q);
 }
 // sums over the lanes up to this one
 __device__ __forceinline__ Pair scan(Pair a, int lane) {
@@ -135,16 +146,18 @@ __device__ __forceinline__ Pair residual(float x, float y, float ch, float cl) {
 // What the walk asks of the whole cluster.
 struct Ask {
   int node;
-  double c;    // sum of max(p - c q, 0) over node's row, without its refused tokens if the drafts are certain
+  Pair c;      // sum of max(p - c q, 0) over node's row, without its refused tokens if the drafts are certain
   int sum;     // a sum is needed (else: the last one serves)
   int done;    // the walk is over
 };
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyParams p, const int nc) {
+// Four CTAs an SM: 64 sequences are 512.
+__global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyParams p, const int nc) {
   __shared__ float px[kMaxDrafts], qx[kMaxDrafts], uni[kMaxDrafts];
   __shared__ int par[kMaxDrafts], tok[kMaxDrafts];
   __shared__ uint8_t refused[kMaxDrafts];  // of the node where the sequence stands
+  __shared__ uint8_t first[kMaxDrafts];    // taken, if it is the first to be tested at its node: u q < p
   __shared__ Pair warp_sum[kWarps], cta_sum[2][kMaxCtas], found_start, found_goal;
   __shared__ Ask ask;
   __shared__ int found;  // the warp whose part the next token is in; -1: not this CTA's
@@ -170,6 +183,7 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
     if (up >= 0) {
       px[t] = fmaxf(load<BF16>(p.p, b * p.ps0 + up * p.ps1 + x), 0.f);  // 0 for a NaN
       qx[t] = certain ? 1.0f : fmaxf(load<BF16>(p.q, b * p.qs0 + up * p.qs1 + x), 0.f);
+      first[t] = fmaf(-uni[t], qx[t], px[t]) > 0.f;  // the sign is exact: one rounding
     }
   }
   __syncthreads();
@@ -192,10 +206,10 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
   int turn = 0;
   // the sum that `ask` asks for, in warp 0 of every CTA alike; warp_sum and
   // cta_sum[turn] hold its parts afterwards
-  auto row_sum = [&](int node, double c, bool without) -> double {
+  auto row_sum = [&](int node, Pair c, bool without) -> Pair {
     const void* pr = row_at<BF16>(p.p, b * p.ps0 + node * p.ps1);
     Pair acc = make_float2(0.f, 0.f);
-    if (c == 0.0) {
+    if (c.x == 0.f) {
       for (int v0 = w0 + lane; v0 < w1; v0 += 32 * kUnroll) {
         float x[kUnroll];
 #pragma unroll
@@ -205,7 +219,6 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
       }
     } else {
       const void* qr = row_at<BF16>(p.q, b * p.qs0 + node * p.qs1);
-      const Pair cp = pair_of(c);
       for (int v0 = w0 + lane; v0 < w1; v0 += 32 * kUnroll) {
         float x[kUnroll], y[kUnroll];
 #pragma unroll
@@ -216,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
         }
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) {
-          const Pair r = residual(x[k], y[k], cp.x, cp.y);
+          const Pair r = residual(x[k], y[k], c.x, c.y);
           add_to(acc, r.x, r.y);
         }
       }
@@ -238,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
     };
     const Pair none = make_float2(0.f, 0.f);
     if (warp == 0) {
-      const Pair s = all_lanes(warp_sum[lane % kWarps]);
+      const Pair s = all_lanes(lane % 16 < kWarps ? warp_sum[lane % kWarps] : none);
       if (lane < nc) {
         uint32_t at;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
@@ -248,15 +261,19 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
       }
     }
     cluster_sync();
-    if (warp != 0) return 0.0;
-    return value(shfl(all_lanes(lane % 16 < nc ? cta_sum[turn][lane % 16] : none), 0));
+    if (warp != 0) return none;
+    return shfl(all_lanes(lane % 16 < nc ? cta_sum[turn][lane % 16] : none), 0);
   };
-  static_assert(kWarps == 16 && kMaxCtas == 16, "a lane per part");
+  static_assert(kWarps <= 16 && kMaxCtas == 16, "a lane per part");
 
   // ---- the walk, in warp 0 of every CTA alike
   int node = 0, n = 1, t = 0;
-  double c = 0.0, mass = 1.0, left = 1.0, total = 0.0;
+  // (p and q enter the tests times 2^60: products of small numbers stay normal)
+  constexpr float kUp = 1152921504606846976.f;
+  const Pair zero = of(0.f), one = of(1.f);
+  Pair c = zero, mass = one, left = one, total = zero;
   bool known = true;   // mass is this row's at c
+  bool fresh = true;   // nothing has been refused at the node
   bool summed = false; // the parts of the last sum are this node's at c
   for (;;) {
     if (warp == 0) {
@@ -274,10 +291,10 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
         }
         if (found < 0) break;
         const int x = tok[found];
-        if (certain || !p.replacement) {  // a token that was refused here is not tested again
+        if (!fresh && (certain || !p.replacement)) {  // a token that was refused here is not tested again
           bool seen = false;
           for (int i = node + 1 + lane; i < found; i += 32) seen |= refused[i] && tok[i] == x;
-          if (__any_sync(0xffffffffu, seen) || left <= 0.0) {
+          if (__any_sync(0xffffffffu, seen) || !(left.x > 0.f)) {
             t = found;
             continue;
           }
@@ -286,32 +303,37 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
           need = true;
           break;
         }
-        const double u = uni[found], pv = px[found], qv = qx[found];
         bool yes;
-        if (certain) {
-          yes = u * mass < pv;
+        if (fresh) {
+          yes = first[found];
+        } else if (certain) {
+          yes = greater(of(px[found]), times(of(uni[found]), mass));
         } else {
-          const double r = pv - c * qv;
-          yes = u * qv * mass < (r > 0.0 ? r : 0.0) * left;
+          const float qv = qx[found] * kUp;
+          const Pair r = tidy(residual(px[found] * kUp, qv, c.x, c.y));
+          yes = greater(times(r, left), times(times(of(uni[found]), of(qv)), mass));
         }
         t = found;
         if (yes) {
-          // (refused drafts of the node that is left are none of the new one's)
-          for (int i = node + 1 + lane; i < T; i += 32) refused[i] = 0;
-          __syncwarp();
+          if (!fresh) {  // (refused drafts of the node that is left are none of the new one's)
+            for (int i = node + 1 + lane; i < T; i += 32) refused[i] = 0;
+            __syncwarp();
+          }
           node = found;
           if (rank == 0 && lane == 0) path[n] = node;
           ++n;
-          c = 0.0, mass = 1.0, left = 1.0;
-          known = true, summed = false;
+          c = zero, mass = left = one;
+          known = fresh = true;
+          summed = false;
         } else {
           if (certain) {
-            mass -= pv;
+            mass = add(mass, of(-px[found]));
           } else {
-            c += mass / left;
-            if (!p.replacement) left -= qv;
+            c = fresh ? one : add(c, p.replacement ? mass : over(mass, left));
+            if (!p.replacement) left = add(left, of(-qx[found]));
             known = false;
           }
+          fresh = false;
           if (lane == 0) refused[found] = 1;
           __syncwarp();
           summed = false;
@@ -336,19 +358,19 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
   }
   const int last = ask.node;
   // nothing is left of a row that something was taken from: the token comes from p itself
-  bool whole = ask.c == 0.0 && !certain;
-  if (warp == 0 && lane == 0) found = total > 0.0;
+  bool whole = ask.c.x == 0.f && !certain;
+  if (warp == 0 && lane == 0) found = total.x > 0.f;
   __syncthreads();
   if (!found && !whole) {  // (the cluster's CTAs alike)
     whole = true;
-    total = row_sum(last, 0.0, false);
+    total = row_sum(last, zero, false);
   }
   if (warp == 0) {
     if (rank == 0) {
       if (lane == 0) {
         path[0] = 0;
         p.n_accept[b] = n;
-        if (!(total > 0.0)) {
+        if (!(total.x > 0.f)) {
           p.next[b] = -1;
           report(p.status, kStatusBounds);
         }
@@ -357,8 +379,8 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
     }
     // ---- the next token: which CTA, which warp's part
     int who = -1;
-    if (total > 0.0) {
-      const Pair goal = pair_of(static_cast<double>(uni[0]) * total), none = make_float2(0.f, 0.f);
+    if (total.x > 0.f) {
+      const Pair goal = times(of(uni[0]), total), none = make_float2(0.f, 0.f);
       Pair before = none;
       if (pick(lane < nc ? cta_sum[turn][lane] : none, goal, before, lane) == rank)
         who = pick(lane < kWarps ? warp_sum[lane] : none, goal, before, lane);
@@ -372,7 +394,7 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
   // ---- in it: all warps take a piece of that part, then one warp the piece's entries
   const void* pr = row_at<BF16>(p.p, b * p.ps0 + last * p.ps1);
   const void* qr = row_at<BF16>(p.q, b * p.qs0 + last * p.qs1);
-  const Pair cp = whole ? make_float2(0.f, 0.f) : pair_of(ask.c);
+  const Pair cp = whole ? zero : ask.c;
   auto weight = [&](int v) -> Pair {
     const float x = load<BF16>(pr, v);
     if (!whole && certain) {
