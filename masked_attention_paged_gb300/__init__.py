@@ -1197,7 +1197,8 @@ def draft_verify(target_probs: torch.Tensor, tokens: torch.Tensor, parents: torc
     n_accept int32 [B], node 0 included; next_token int32 [B]): path and n_accept
     as kv_tree_accept takes them."""
     lib = load()
-    _check_probs(target_probs, "target_probs")
+    if not (isinstance(target_probs, torch.Tensor) and target_probs.dim() == 3):
+        raise ValueError("target_probs must be float32 or bfloat16 [B, T, V]")
     B, T, V = target_probs.shape
     dev = target_probs.device
     if path is None:
@@ -1206,6 +1207,12 @@ def draft_verify(target_probs: torch.Tensor, tokens: torch.Tensor, parents: torc
         n_accept = _fresh(lambda: torch.empty(B, dtype=torch.int32, device=dev), stream, dev)
     if next_token is None:
         next_token = _fresh(lambda: torch.empty(B, dtype=torch.int32, device=dev), stream, dev)
+    if dev.type == "cuda":
+        ws = workspace or _small_ws(dev, stream)
+        if _call("draft_verify", "pPqqu=kvvWS", target_probs, draft_probs, tokens, parents, uniforms,
+                 int(bool(replacement)), path, n_accept, next_token, ws.tensor, _handle(stream)):
+            return path, n_accept, next_token
+    _check_probs(target_probs, "target_probs")
     if draft_probs is not None:
         _check_probs(draft_probs, "draft_probs")
     for t, name in ((tokens, "tokens"), (parents, "parents")):
@@ -1274,6 +1281,11 @@ def kv_free(refs: torch.Tensor, block_table: torch.Tensor, ctx_lens: torch.Tenso
     each entry is counted off refs (int32 [num_blocks]) and becomes -1, and the
     row's ctx_lens entry becomes -1 (idle)."""
     lib = load()
+    if refs.is_cuda:
+        ws = workspace or _small_ws(refs.device, stream)
+        if _call("kv_free", "Ztvn=WS", refs, block_table, ctx_lens, done, block_table.shape[0], ws.tensor,
+                 _handle(stream)):
+            return
     _check_refs(refs)
     _check_pool_table(block_table, "block_table")
     B = block_table.shape[0]
@@ -1293,6 +1305,10 @@ def kv_reserve(refs: torch.Tensor, block_table: torch.Tensor, ctx_lens: torch.Te
     """Give every row the blocks that its next n_new[b] tokens (int32 [B]) need
     and it does not have: the lowest free ones, in row order."""
     lib = load()
+    if workspace is not None and refs.is_cuda:
+        if _call("kv_reserve", "Ztvv=WS", refs, block_table, ctx_lens, n_new, block_table.shape[0], workspace.tensor,
+                 _handle(stream)):
+            return
     _check_refs(refs)
     _check_pool_table(block_table, "block_table")
     B = block_table.shape[0]
@@ -1314,6 +1330,10 @@ def kv_fork(caches: Sequence[torch.Tensor], refs: torch.Tensor, block_table: tor
     blocks and gets a copy of its partial one, in every tensor of caches (any types,
     each contiguous [num_blocks, ...], K and V of all layers at once)."""
     lib = load()
+    if workspace is not None and refs.is_cuda:
+        if _call("kv_fork", "LZtv=Vtv=WS", caches, refs, block_table, ctx_lens, block_table.shape[0], src, child_table,
+                 child_lens, child_table.shape[0], workspace.tensor, _handle(stream)):
+            return
     _check_refs(refs)
     _check_block_table(block_table, 0)
     _check_pool_table(child_table, "child_table")
@@ -1338,10 +1358,16 @@ def kv_compact(caches: Sequence[torch.Tensor], refs: torch.Tensor, block_table: 
     (as kv_fork), with their counts and the table's entries.  Returns used (int32
     [1]): how many there are; all later blocks are free."""
     lib = load()
-    _check_refs(refs)
-    _check_pool_table(block_table, "block_table")
+    if not isinstance(refs, torch.Tensor):
+        raise ValueError("refs must be contiguous int32 [num_blocks]")
     if used is None:
         used = _fresh(lambda: torch.empty(1, dtype=torch.int32, device=refs.device), stream, refs.device)
+    if workspace is not None and refs.is_cuda:
+        if _call("kv_compact", "LZt=UWS", caches, refs, block_table, block_table.shape[0], used, workspace.tensor,
+                 _handle(stream)):
+            return used
+    _check_refs(refs)
+    _check_pool_table(block_table, "block_table")
     _check_int32_vec(used, 1, "used")
     at, n, keep = _pool_tensors(caches, refs.shape[0])
     _check_devices("kv_compact", *caches, refs, block_table, used, _ws_tensor(workspace))
@@ -1383,6 +1409,11 @@ def kv_append_f8(kq_cache: torch.Tensor, vq_cache: torch.Tensor, k_scale: torch.
     a larger scale gets it, and its older codes are rounded again.  lens int32 [B]:
     new tokens of each sequence."""
     lib = load()
+    if kq_cache.is_cuda:
+        ws = workspace or _small_ws(kq_cache.device, stream)
+        if _call("kv_append_f8", "ebVnyyWS", kq_cache, vq_cache, k_scale, v_scale, block_table, start_pos, lens, k_new,
+                 v_new, ws.tensor, _handle(stream)):
+            return
     c = _cache_f8(kq_cache, vq_cache, k_scale, v_scale)
     if k_new.dim() == 3:
         k_new, v_new = _one_token(k_new, v_new)
@@ -1431,6 +1462,10 @@ def paged_attn_f8(q: torch.Tensor, kq_cache: torch.Tensor, vq_cache: torch.Tenso
         raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
     if lse is None and return_lse:
         lse = _fresh(lambda: torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device), stream, q.device)
+    if workspace is not None and q.is_cuda:
+        if _call("paged_attn_f8", "yebvn==OlWS", q, kq_cache, vq_cache, k_scale, v_scale, block_table, start_pos, lens,
+                 int(bool(causal)), float(scale), out, lse, workspace.tensor, _handle(stream)):
+            return (out, lse) if return_lse else out
     if lse is not None:
         _check_f32_buffer(lse, B * Hq * T, "lse")
     c = _cache_f8(kq_cache, vq_cache, k_scale, v_scale)

@@ -25,6 +25,16 @@
 //   l  f32, contiguous, B H T elements, or None -> pointer or null
 //   A  f32 [blocks, Hkv, 16] of the cache -> pointer
 //   K  int32, contiguous [B, Hkv, n]     -> pointer
+//   O  as Y, of any type                -> attn_tensor
+//   p  tensor, bf16 or f32, 3-D          -> attn_tensor; B, T and D are its sizes
+//   P  as p, of its sizes and type, or None -> attn_tensor or null
+//   u  f32 [B, T] rows                   -> pointer, row stride
+//   k  int32, contiguous [B, T]          -> pointer
+//   e  four tensors: an e4m3 cache and its scales -> attn_kv_cache_f8
+//   L  a list of tensors with as many blocks as Z says -> their number, attn_pool_tensor[]
+//   Z  int32 vector of a pool's blocks   -> pointer, their number
+//   t  table, rows apart, that sets B or has B rows -> pointer, row stride, columns
+//   U  int32, one element                -> pointer
 //   W  a workspace's bytes               -> pointer, their number
 //   S  a stream handle, or None          -> itself, or the current stream
 //   =  an int or a float                 -> itself
@@ -36,6 +46,7 @@
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
+#include <vector>
 #include <utility>
 
 #include "libattn.h"
@@ -73,23 +84,25 @@ struct Sizes {
   int64_t B = -1, H = 0, T = 0, D = 0;
   int64_t blocks = 0, kv_heads = 0, slots = 0;  // of the cache
   int64_t table_rows = -1;  // least of the block tables seen
+  int64_t pool = -1;        // blocks of the pool
   at::ScalarType type = at::kBFloat16;
   bool one_token = false;
 };
 
 bool on(const at::Tensor& t, int64_t device) { return t.is_cuda() && t.get_device() == device; }
 
-bool describe(const at::Tensor& t, int64_t device, bool insert, attn_tensor* d) {
+// a 4-D tensor, or (insert) 3-D rows with a dimension of one before the last; or (three) 3-D as it is
+bool describe(const at::Tensor& t, int64_t device, bool insert, attn_tensor* d, bool three = false) {
   if (!on(t, device)) return false;
   const auto type = t.scalar_type();
   if (type != at::kBFloat16 && type != at::kFloat) return false;
   const int64_t n = t.dim();
-  if (n != (insert ? 3 : 4)) return false;
+  if (n != (insert || three ? 3 : 4)) return false;
   std::memset(d, 0, sizeof(*d));
   d->data = t.data_ptr();
   d->dtype = type == at::kBFloat16 ? ATTN_BF16 : ATTN_F32;
-  d->ndim = 4;
-  for (int i = 0, k = 0; i < 4; ++i) {
+  d->ndim = three ? 3 : 4;
+  for (int i = 0, k = 0; i < d->ndim; ++i) {
     if (insert && i == 2) {
       d->shape[2] = 1;
       d->stride[2] = t.size(2) * t.stride(2);
@@ -119,6 +132,8 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   Value out[kMost];
   attn_tensor tensors[8];
   attn_kv_cache cache;
+  attn_kv_cache_f8 cache_f8;
+  std::vector<attn_pool_tensor> pool;
   int n = 0, n_tensors = 0;
   Py_ssize_t a = 3;
   Sizes s;
@@ -142,7 +157,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
         put(address(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream()));
         continue;
       }
-      if (o == Py_None && (*f == 'o' || *f == 'n' || *f == 'l')) {
+      if (o == Py_None && (*f == 'o' || *f == 'n' || *f == 'l' || *f == 'P')) {
         put(0);
         continue;
       }
@@ -158,6 +173,27 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
         }
         continue;
       }
+      if (*f == 'L') {
+        const bool list = PyList_Check(o);
+        const Py_ssize_t count = list ? PyList_GET_SIZE(o) : (PyTuple_Check(o) ? PyTuple_GET_SIZE(o) : -1);
+        ok = count >= 0 && count <= 4096;
+        pool.resize(ok ? static_cast<size_t>(count) : 0);
+        for (Py_ssize_t i = 0; ok && i < count; ++i) {
+          PyObject* x = list ? PyList_GET_ITEM(o, i) : PyTuple_GET_ITEM(o, i);
+          ok = THPVariable_Check(x);
+          if (!ok) break;
+          const at::Tensor& c = THPVariable_Unpack(x);
+          ok = on(c, device) && c.dim() >= 1 && c.size(0) > 0 && c.is_contiguous() &&
+               (s.pool < 0 || s.pool == c.size(0));
+          if (!ok) break;
+          s.pool = c.size(0);
+          pool[i].data = c.data_ptr();
+          pool[i].block_bytes = c.numel() / c.size(0) * static_cast<int64_t>(c.element_size());
+        }
+        put(count);
+        put(address(pool.data()));
+        continue;
+      }
       if (!THPVariable_Check(o)) {
         ok = false;
         break;
@@ -168,26 +204,107 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
         case 'y':
         case 'X':
         case 'Y':
+        case 'O':
         case 'o': {
           if (n_tensors == 8) {
             ok = false;
             break;
           }
           attn_tensor& d = tensors[n_tensors];
-          const bool first = s.B < 0;
-          const bool insert = (*f == 'y' || *f == 'Y') && (first ? t.dim() == 3 : s.one_token);
+          const bool first = n_tensors == 0;
+          const bool insert = (*f == 'y' || *f == 'Y' || *f == 'O') && (first ? t.dim() == 3 : s.one_token);
           ok = describe(t, device, insert, &d);
-          if (*f == 'X' || *f == 'Y')
+          if (*f == 'X' || *f == 'Y' || *f == 'O')
             ok = ok && d.shape[0] == s.B && d.shape[1] == s.H && d.shape[2] == s.T && d.shape[3] == s.D &&
-                 (*f == 'X' || t.scalar_type() == s.type);
+                 (*f != 'Y' || t.scalar_type() == s.type);
           if (!ok) break;
           if (first) {
+            ok = s.B < 0 || s.B == d.shape[0];  // (a vector before it may have said)
+            if (!ok) break;
             s.B = d.shape[0], s.H = d.shape[1], s.T = d.shape[2], s.D = d.shape[3];
             s.type = t.scalar_type();
             s.one_token = insert;
           }
           ++n_tensors;
           put(address(&d));
+          break;
+        }
+        case 'p':
+        case 'P': {
+          if (n_tensors == 8) {
+            ok = false;
+            break;
+          }
+          attn_tensor& d = tensors[n_tensors];
+          ok = describe(t, device, false, &d, true);
+          if (!ok) break;
+          if (*f == 'p') {
+            s.B = d.shape[0], s.T = d.shape[1], s.D = d.shape[2];
+            s.type = t.scalar_type();
+          }
+          ok = d.shape[0] == s.B && d.shape[1] == s.T && d.shape[2] == s.D && t.scalar_type() == s.type;
+          ++n_tensors;
+          put(address(&d));
+          break;
+        }
+        case 'u':
+          ok = on(t, device) && t.scalar_type() == at::kFloat && t.dim() == 2 && t.size(0) == s.B && t.size(1) == s.T &&
+               (s.T <= 1 || t.stride(1) == 1);
+          if (!ok) break;
+          put(address(t.data_ptr()));
+          put(t.stride(0));
+          break;
+        case 'k':
+          ok = on(t, device) && t.scalar_type() == at::kInt && t.is_contiguous() && t.dim() == 2 && t.size(0) == s.B &&
+               t.size(1) == s.T;
+          if (!ok) break;
+          put(address(t.data_ptr()));
+          break;
+        case 'Z':
+          ok = on(t, device) && t.scalar_type() == at::kInt && t.dim() == 1 && t.is_contiguous() &&
+               (s.pool < 0 || s.pool == t.size(0));
+          if (!ok) break;
+          put(address(t.data_ptr()));
+          put(t.size(0));
+          break;
+        case 't':
+          ok = on(t, device) && t.scalar_type() == at::kInt && t.dim() == 2 && t.stride(1) == 1 &&
+               t.stride(0) >= t.size(1) && (s.B < 0 || s.B == t.size(0));
+          if (!ok) break;
+          s.B = t.size(0);
+          put(address(t.data_ptr()));
+          put(t.stride(0));
+          put(t.size(1));
+          break;
+        case 'U':
+          ok = on(t, device) && t.scalar_type() == at::kInt && t.dim() == 1 && t.size(0) == 1;
+          if (!ok) break;
+          put(address(t.data_ptr()));
+          break;
+        case 'e': {
+          const at::Tensor* c[4] = {&t, nullptr, nullptr, nullptr};
+          for (int i = 1; ok && i < 4; ++i) {
+            ok = a < nargs && THPVariable_Check(args[a]);
+            if (ok) c[i] = &THPVariable_Unpack(args[a++]);
+          }
+          if (!ok) break;
+          for (int i = 0; i < 4; ++i) ok = ok && on(*c[i], device) && c[i]->is_contiguous();
+          ok = ok && t.dim() == 4 && t.sizes() == c[1]->sizes() && t.scalar_type() == at::kFloat8_e4m3fn &&
+               c[1]->scalar_type() == at::kFloat8_e4m3fn;
+          for (int i = 2; i < 4; ++i)
+            ok = ok && c[i]->scalar_type() == at::kFloat && c[i]->dim() == 2 && c[i]->size(0) == t.size(0) &&
+                 c[i]->size(1) == t.size(1);
+          if (!ok) break;
+          std::memset(&cache_f8, 0, sizeof(cache_f8));
+          cache_f8.k = t.data_ptr();
+          cache_f8.v = c[1]->data_ptr();
+          cache_f8.k_scale = static_cast<float*>(c[2]->data_ptr());
+          cache_f8.v_scale = static_cast<float*>(c[3]->data_ptr());
+          cache_f8.num_blocks = t.size(0);
+          cache_f8.num_kv_heads = static_cast<int32_t>(t.size(1));
+          cache_f8.block_size = static_cast<int32_t>(t.size(2));
+          cache_f8.head_dim = static_cast<int32_t>(t.size(3));
+          put(address(&cache_f8));
           break;
         }
         case 'c': {
@@ -311,6 +428,20 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     st = invoke(&paged_attn_weights, entry, out, count);
   else if (std::strcmp(name, "kv_evict") == 0)
     st = invoke(&kv_evict, entry, out, count);
+  else if (std::strcmp(name, "draft_verify") == 0)
+    st = invoke(&draft_verify, entry, out, count);
+  else if (std::strcmp(name, "kv_free") == 0)
+    st = invoke(&kv_free, entry, out, count);
+  else if (std::strcmp(name, "kv_reserve") == 0)
+    st = invoke(&kv_reserve, entry, out, count);
+  else if (std::strcmp(name, "kv_fork") == 0)
+    st = invoke(&kv_fork, entry, out, count);
+  else if (std::strcmp(name, "kv_compact") == 0)
+    st = invoke(&kv_compact, entry, out, count);
+  else if (std::strcmp(name, "kv_append_f8") == 0)
+    st = invoke(&kv_append_f8, entry, out, count);
+  else if (std::strcmp(name, "paged_attn_f8") == 0)
+    st = invoke(&paged_attn_f8, entry, out, count);
   Py_END_ALLOW_THREADS;
   if (st < 0) return PyErr_Format(PyExc_ValueError, "call: %s with %d arguments", name, n);
   return PyLong_FromLong(st);

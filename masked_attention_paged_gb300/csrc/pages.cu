@@ -82,12 +82,15 @@ __device__ __forceinline__ void each(const Pass& s, int rank, Put put) {
   }
 }
 
-// list[0 .. min(want, free)): the lowest free blocks; returns how many.
-__device__ int lowest_free(const int32_t* refs, int n, int want, int32_t* list, int* warp_sum) {
+// list[0 .. min(want, free)): the lowest free blocks; returns how many.  s, mine: the
+// first pass, looked at by look_free before it was known how many are wanted.
+__device__ __forceinline__ int look_free(const int32_t* refs, int n, int base, Pass& s) {
+  return look(refs, n, base, s, [](int, int32_t r) { return r == 0; });
+}
+__device__ int lowest_free(const int32_t* refs, int n, int want, int32_t* list, int* warp_sum, Pass& s, int mine) {
   int found = 0;
   for (int base = 0; base < n && found < want; base += kPass) {
-    Pass s;
-    const int mine = look(refs, n, base, s, [](int, int32_t r) { return r == 0; });
+    if (base > 0) mine = look_free(refs, n, base, s);
     int total;
     const int before = sum_before((threadIdx.x & 31) == 0 ? mine : 0, warp_sum, total);
     each(s, found + __shfl_sync(0xffffffffu, before, 0), [&](int rank, int id) {
@@ -155,6 +158,8 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(const ReserveParam
   let_next_launch_in();
   wait_for_launch_ahead();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Pass ahead;
+  const int mine = look_free(p.refs, p.num_blocks, 0, ahead);
   // the columns of row b that the new tokens' slots are in
   auto columns = [&](int b, int& end) {
     const int64_t ctx = p.ctx_lens[b], n = p.n_new[b];
@@ -185,7 +190,7 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(const ReserveParam
     if (b < p.rows) p.count[b] = min(want + before, p.num_blocks);
     want = min(want + total, p.num_blocks);
   }
-  const int got = lowest_free(p.refs, p.num_blocks, want, p.list, warp_sum);
+  const int got = lowest_free(p.refs, p.num_blocks, want, p.list, warp_sum, ahead, mine);
   __syncthreads();
   for (int b = warp; b < p.rows; b += kWarps) {
     int end, rank = p.count[b];
@@ -210,42 +215,75 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(const ReserveParam
 // ---------------------------------------------------------------------------
 // moves of whole blocks, in every tensor of the pool
 // ---------------------------------------------------------------------------
+template <int CAP>  // room for so many: the arguments of a launch are copied each time
 struct PoolTensors {
   int n;
-  uint8_t* data[kPoolMaxTensors];
-  int64_t bytes[kPoolMaxTensors];
-  int first[kPoolMaxTensors + 1];  // pieces of a block in the tensors before
-  uint8_t unit[kPoolMaxTensors];   // 16, 4 or 1 bytes at a time: what base and block size allow
+  uint8_t* data[CAP];
+  int64_t bytes[CAP];
+  int first[CAP + 1];  // pieces of a block in the tensors before
+  uint8_t unit[CAP];   // 16, 4 or 1 bytes at a time: what base and block size allow
 };
 
+// A piece of a block to move: at most kPiece bytes.
+struct Move {
+  const uint8_t* src;
+  uint8_t* dst;
+  int len, unit;  // len 0: none
+};
 // piece r of block `from` to block `to`
-__device__ __forceinline__ void move_piece(const PoolTensors& pt, int r, int64_t from, int64_t to) {
+template <int CAP>
+__device__ __forceinline__ Move piece_of(const PoolTensors<CAP>& pt, int r, int64_t from, int64_t to) {
   int t = 0;
-  for (int step = 128; step > 0; step /= 2)  // the last tensor that begins at or before r
+#pragma unroll
+  for (int step = CAP / 2; step > 0; step /= 2)  // the last tensor that begins at or before r
     if (t + step < pt.n && pt.first[t + step] <= r) t += step;
   const int64_t bytes = pt.bytes[t], off = static_cast<int64_t>(r - pt.first[t]) * kPiece;
-  const int len = static_cast<int>(min(static_cast<int64_t>(kPiece), bytes - off));
-  const uint8_t* src = pt.data[t] + from * bytes + off;
-  uint8_t* dst = pt.data[t] + to * bytes + off;
-  if (pt.unit[t] == 16) {
-    uint4 w[kMoveVecs];
-    const int n = len / 16;
+  Move m;
+  m.src = pt.data[t] + from * bytes + off;
+  m.dst = pt.data[t] + to * bytes + off;
+  m.len = static_cast<int>(min(static_cast<int64_t>(kPiece), bytes - off));
+  m.unit = pt.unit[t];
+  return m;
+}
+
+// Moves get(w) for w = first, first + step, ... below n, the next one's place looked up
+// (a chain of loads) while the bytes of this one are on their way.
+template <typename Get>
+__device__ __forceinline__ void move_all(int64_t first, int64_t n, int64_t step, Get get) {
+  if (first >= n) return;
+  Move m = get(first);
+  for (int64_t w = first; w < n; w += step) {
+    Move next;
+    next.len = 0;
+    if (m.len > 0 && m.unit == 16) {
+      uint4 x[kMoveVecs];
+      const int vecs = m.len / 16;
 #pragma unroll
-    for (int u = 0; u < kMoveVecs; ++u) {
-      const int i = u * kMoveThreads + threadIdx.x;
-      if (i < n) w[u] = reinterpret_cast<const uint4*>(src)[i];
-    }
+      for (int u = 0; u < kMoveVecs; ++u) {
+        const int i = u * kMoveThreads + threadIdx.x;
+        if (i < vecs) x[u] = __ldcs(reinterpret_cast<const uint4*>(m.src) + i);
+      }
+      if (w + step < n) next = get(w + step);
 #pragma unroll
-    for (int u = 0; u < kMoveVecs; ++u) {
-      const int i = u * kMoveThreads + threadIdx.x;
-      if (i < n) reinterpret_cast<uint4*>(dst)[i] = w[u];
+      for (int u = 0; u < kMoveVecs; ++u) {
+        const int i = u * kMoveThreads + threadIdx.x;
+        if (i < vecs) reinterpret_cast<uint4*>(m.dst)[i] = x[u];
+      }
+    } else {
+      if (m.unit == 4) {
+        for (int i = threadIdx.x; i < m.len / 4; i += kMoveThreads)
+          reinterpret_cast<uint32_t*>(m.dst)[i] = reinterpret_cast<const uint32_t*>(m.src)[i];
+      } else {
+        for (int i = threadIdx.x; i < m.len; i += kMoveThreads) m.dst[i] = m.src[i];
+      }
+      if (w + step < n) next = get(w + step);
     }
-  } else if (pt.unit[t] == 4) {
-    for (int i = threadIdx.x; i < len / 4; i += kMoveThreads)
-      reinterpret_cast<uint32_t*>(dst)[i] = reinterpret_cast<const uint32_t*>(src)[i];
-  } else {
-    for (int i = threadIdx.x; i < len; i += kMoveThreads) dst[i] = src[i];
+    m = next;
   }
+}
+// w = q * d + r, both below 2^31 mostly
+__device__ __forceinline__ int quotient(int64_t w, int d) {
+  return w >> 31 == 0 ? static_cast<int>(static_cast<uint32_t>(w) / static_cast<uint32_t>(d)) : static_cast<int>(w / d);
 }
 
 // ---------------------------------------------------------------------------
@@ -265,65 +303,73 @@ struct ForkParams {
   int child_blocks;
   int32_t* child_lens;
   int children;
-  int32_t* fresh;  // [children] workspace: the new block; -1: none needed; -2: an idle child
-  int32_t* list;   // [num_blocks] workspace
+  int2* copies;   // [children] workspace: from a block to a new one; .y -1: none needed, -2: an idle child
+  int32_t* list;  // [num_blocks] workspace
   uint32_t* status;
 };
 __global__ void __launch_bounds__(kThreads) kv_fork_plan_kernel(const ForkParams p) {
   __shared__ int warp_sum[kWarps];
   let_next_launch_in();
   wait_for_launch_ahead();
-  // what child j needs: 1 a new block, 0 none, -1 nothing (idle)
-  auto needs = [&](int j, bool tell) {
+  Pass ahead;
+  const int mine = look_free(p.refs, p.num_blocks, 0, ahead);
+  // what child j needs: 1 a new block (and which one it copies), 0 none, -1 nothing (idle)
+  auto needs = [&](int j, int& from, int& L) {
     const int s = p.src[j];
+    from = L = -1;
     if (s < 0) return -1;
-    const int L = s < p.batch ? p.ctx_lens[s] : 0;
+    if (s < p.batch) L = p.ctx_lens[s];
     if (s < p.batch && L < 0) return -1;
     const int last = (L - 1) / kBS;  // the block of the last token
     bool bad = s >= p.batch || (L > 0 && (last >= p.max_blocks || last >= p.child_blocks));
     if (!bad && L % kBS != 0) {
-      const int id = p.bt[s * p.bt_stride + last];
-      bad = id < 0 || id >= p.num_blocks;
+      from = p.bt[s * p.bt_stride + last];
+      bad = from < 0 || from >= p.num_blocks;
     }
-    if (bad && tell) report(p.status, kStatusBounds);
+    if (bad) report(p.status, kStatusBounds);
     return bad ? -1 : (L % kBS != 0 ? 1 : 0);
   };
   int want = 0;
   for (int base = 0; base < p.children; base += kThreads) {
     const int j = base + threadIdx.x;
-    const int n = j < p.children ? needs(j, true) : -1;
+    int from = -1, L = -1;
+    const int n = j < p.children ? needs(j, from, L) : -1;
     int total;
     const int before = sum_before(n > 0 ? 1 : 0, warp_sum, total);
-    if (j < p.children) p.fresh[j] = n > 0 ? want + before : (n == 0 ? -1 : -2);
+    if (j < p.children) {
+      p.copies[j] = make_int2(from, n > 0 ? want + before : (n == 0 ? -1 : -2));
+      p.child_lens[j] = n < 0 ? -1 : L;
+    }
     want += total;
   }
-  const int got = lowest_free(p.refs, p.num_blocks, want, p.list, warp_sum);
+  const int got = lowest_free(p.refs, p.num_blocks, want, p.list, warp_sum, ahead, mine);
   __syncthreads();
   for (int j = threadIdx.x; j < p.children; j += kThreads) {
-    int f = p.fresh[j];
-    if (f >= 0) {
-      if (f < got) {
-        f = p.list[f];
-        p.refs[f] = 1;
-      } else {
-        f = -2;
-        report(p.status, kStatusBounds);
-      }
-      p.fresh[j] = f;
+    const int rank = p.copies[j].y;
+    if (rank < 0) continue;
+    if (rank < got) {
+      const int block = p.list[rank];
+      p.refs[block] = 1;
+      p.copies[j].y = block;
+    } else {  // no block left
+      p.copies[j].y = -2;
+      p.child_lens[j] = -1;
+      report(p.status, kStatusBounds);
     }
-    p.child_lens[j] = f == -2 ? -1 : p.ctx_lens[p.src[j]];
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads)
-    kv_fork_apply_kernel(const __grid_constant__ ForkParams p, const __grid_constant__ PoolTensors pt, const int rows) {
+template <int CAP>
+__global__ void __launch_bounds__(kMoveThreads, 8)
+    kv_fork_apply_kernel(const __grid_constant__ ForkParams p, const __grid_constant__ PoolTensors<CAP> pt,
+                         const int rows) {
   let_next_launch_in();
   wait_for_launch_ahead();
   const int pieces = pt.first[pt.n];
   // `rows` CTAs write the children's rows, the others copy partial blocks
   if (blockIdx.x < rows) {
     for (int j = blockIdx.x; j < p.children; j += rows) {
-      const int f = p.fresh[j];
+      const int f = p.copies[j].y;
       const int full = f == -2 ? 0 : p.child_lens[j] / kBS;
       const int32_t* from = p.bt + (f == -2 ? 0 : p.src[j]) * p.bt_stride;
       for (int i = threadIdx.x; i < p.child_blocks; i += kMoveThreads) {
@@ -344,14 +390,14 @@ __global__ void __launch_bounds__(kMoveThreads)
     }
     return;
   }
-  const int64_t items = static_cast<int64_t>(p.children) * pieces;
-  for (int64_t w = blockIdx.x - rows; w < items; w += gridDim.x - rows) {
-    const int j = static_cast<int>(w / pieces);
-    const int f = p.fresh[j];
-    if (f < 0) continue;
-    move_piece(pt, static_cast<int>(w - static_cast<int64_t>(j) * pieces),
-               p.bt[p.src[j] * p.bt_stride + p.child_lens[j] / kBS], f);
-  }
+  move_all(blockIdx.x - rows, static_cast<int64_t>(p.children) * pieces, gridDim.x - rows, [&](int64_t w) {
+    const int j = quotient(w, pieces);
+    const int2 c = p.copies[j];
+    Move m;
+    m.len = 0;
+    if (c.y >= 0) m = piece_of(pt, static_cast<int>(w - static_cast<int64_t>(j) * pieces), c.x, c.y);
+    return m;
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -379,8 +425,8 @@ __global__ void __launch_bounds__(kThreads) kv_compact_plan_kernel(const Compact
   const int n = p.num_blocks;
   const bool lead = (threadIdx.x & 31) == 0;
   int used = 0;
+  Pass s;  // (a pool of one pass is looked at once)
   for (int base = 0; base < n; base += kPass) {
-    Pass s;
     const int mine = look(p.refs, n, base, s, [](int, int32_t r) { return r != 0; });
     int total;
     sum_before(lead ? mine : 0, warp_sum, total);
@@ -388,19 +434,28 @@ __global__ void __launch_bounds__(kThreads) kv_compact_plan_kernel(const Compact
   }
   int holes = 0, moves = 0;
   for (int base = 0; base < n; base += kPass) {
-    Pass s;
-    int total;
-    int mine = look(p.refs, n, base, s, [&](int id, int32_t r) { return r == 0 && id < used; });
-    int before = sum_before(lead ? mine : 0, warp_sum, total);
-    each(s, holes + __shfl_sync(0xffffffffu, before, 0), [&](int r, int id) { p.to[r] = id; });
-    holes += total;
-    mine = look(p.refs, n, base, s, [&](int id, int32_t r) { return r != 0 && id >= used; });
-    before = sum_before(lead ? mine : 0, warp_sum, total);
-    each(s, moves + __shfl_sync(0xffffffffu, before, 0), [&](int r, int id) {
+    if (n > kPass) look(p.refs, n, base, s, [](int, int32_t r) { return r != 0; });
+    Pass hole = s, move = s;  // free below `used`, in use from there on
+    int count[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+      const int below = min(max(used - (s.first + 32 * k), 0), 32);  // ids of the mask that are
+      const uint32_t m = below == 32 ? ~0u : (1u << below) - 1u;
+      hole.mask[k] = ~s.mask[k] & m;
+      move.mask[k] = s.mask[k] & ~m;
+      count[0] += __popc(hole.mask[k]);
+      count[1] += __popc(move.mask[k]);
+    }
+    int total;  // both counts in one sum: at most 2^14 each
+    const int before = sum_before(lead ? count[0] | count[1] << 16 : 0, warp_sum, total);
+    const int mine = __shfl_sync(0xffffffffu, before, 0);
+    each(hole, holes + (mine & 0xffff), [&](int r, int id) { p.to[r] = id; });
+    each(move, moves + (mine >> 16), [&](int r, int id) {
       p.from[r] = id;
       p.rank[id] = r;
     });
-    moves += total;
+    holes += total & 0xffff;
+    moves += total >> 16;
   }
   __syncthreads();
   for (int r = threadIdx.x; r < moves; r += kThreads) {
@@ -414,8 +469,9 @@ __global__ void __launch_bounds__(kThreads) kv_compact_plan_kernel(const Compact
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads)
-    kv_compact_apply_kernel(const __grid_constant__ CompactParams p, const __grid_constant__ PoolTensors pt,
+template <int CAP>
+__global__ void __launch_bounds__(kMoveThreads, 8)
+    kv_compact_apply_kernel(const __grid_constant__ CompactParams p, const __grid_constant__ PoolTensors<CAP> pt,
                             const int rows) {
   let_next_launch_in();
   wait_for_launch_ahead();
@@ -438,15 +494,15 @@ __global__ void __launch_bounds__(kMoveThreads)
     }
     return;
   }
-  const int64_t items = static_cast<int64_t>(moves) * pieces;
-  for (int64_t w = blockIdx.x - rows; w < items; w += gridDim.x - rows) {
-    const int r = static_cast<int>(w / pieces);
-    move_piece(pt, static_cast<int>(w - static_cast<int64_t>(r) * pieces), p.from[r], p.to[r]);
-  }
+  move_all(blockIdx.x - rows, static_cast<int64_t>(moves) * pieces, gridDim.x - rows, [&](int64_t w) {
+    const int r = quotient(w, pieces);
+    return piece_of(pt, static_cast<int>(w - static_cast<int64_t>(r) * pieces), p.from[r], p.to[r]);
+  });
 }
 
 // the tensors' pieces; false if a block has more than 31 bits of them
-bool lay_out(const PoolArgs& a, PoolTensors& pt) {
+template <int CAP>
+bool lay_out(const PoolArgs& a, PoolTensors<CAP>& pt) {
   pt.n = a.n_tensors;
   int64_t at = 0;
   for (int t = 0; t < a.n_tensors; ++t) {
@@ -467,11 +523,35 @@ int move_ctas(int64_t items) {
   return static_cast<int>(std::min<int64_t>(std::max<int64_t>(items, 1), 8 * device_sm_count()));
 }
 
+template <int CAP>
+cudaError_t fork(const PoolArgs& a, const ForkParams& p, cudaStream_t stream) {
+  PoolTensors<CAP> pt;
+  if (!lay_out(a, pt)) return cudaErrorInvalidValue;
+  const cudaError_t e = launch_early(kv_fork_plan_kernel, dim3(1), kThreads, 0, stream, p);
+  if (e != cudaSuccess) return e;
+  const int rows = std::min(p.children, device_sm_count());
+  const int ctas = rows + move_ctas(static_cast<int64_t>(p.children) * pt.first[pt.n]);
+  return launch_early(kv_fork_apply_kernel<CAP>, dim3(static_cast<unsigned>(ctas)), kMoveThreads, 0, stream, p, pt,
+                      rows);
+}
+
+template <int CAP>
+cudaError_t compact(const PoolArgs& a, const CompactParams& p, cudaStream_t stream) {
+  PoolTensors<CAP> pt;
+  if (!lay_out(a, pt)) return cudaErrorInvalidValue;
+  const cudaError_t e = launch_early(kv_compact_plan_kernel, dim3(1), kThreads, 0, stream, p);
+  if (e != cudaSuccess) return e;
+  const int rows = std::max(1, std::min(a.batch, device_sm_count()));
+  const int ctas = rows + move_ctas(a.num_blocks / 2 * pt.first[pt.n]);  // at most half of the blocks move
+  return launch_early(kv_compact_apply_kernel<CAP>, dim3(static_cast<unsigned>(ctas)), kMoveThreads, 0, stream, p, pt,
+                      rows);
+}
+
 }  // namespace
 
-// kv_fork and kv_reserve: a number a row and a list of blocks; kv_compact: three lists of blocks
+// kv_reserve: a number a row and a list of blocks; kv_fork: two numbers; kv_compact: three lists
 size_t pool_workspace_bytes(int64_t num_blocks, int64_t rows) {
-  return ((3 * static_cast<size_t>(num_blocks) + rows + 64) * 4 + 255) & ~size_t(255);
+  return ((3 * static_cast<size_t>(num_blocks) + 2 * rows + 64) * 4 + 255) & ~size_t(255);
 }
 
 cudaError_t launch_kv_free(const PoolArgs& a, const int32_t* done, cudaStream_t stream) {
@@ -521,16 +601,11 @@ cudaError_t launch_kv_fork(const PoolArgs& a, const int32_t* src, int32_t* child
   p.child_blocks = child_blocks;
   p.child_lens = child_lens;
   p.children = children;
-  p.list = static_cast<int32_t*>(a.scratch);
-  p.fresh = p.list + a.num_blocks;
+  p.copies = static_cast<int2*>(a.scratch);
+  p.list = reinterpret_cast<int32_t*>(p.copies + children);
   p.status = a.status;
-  PoolTensors pt;
-  if (!lay_out(a, pt)) return cudaErrorInvalidValue;
-  cudaError_t e = launch_early(kv_fork_plan_kernel, dim3(1), kThreads, 0, stream, p);
-  if (e != cudaSuccess) return e;
-  const int rows = std::min(children, device_sm_count());
-  const int ctas = rows + move_ctas(static_cast<int64_t>(children) * pt.first[pt.n]);
-  return launch_early(kv_fork_apply_kernel, dim3(static_cast<unsigned>(ctas)), kMoveThreads, 0, stream, p, pt, rows);
+  if (a.n_tensors <= 8) return fork<8>(a, p, stream);
+  return a.n_tensors <= 64 ? fork<64>(a, p, stream) : fork<kPoolMaxTensors>(a, p, stream);
 }
 
 cudaError_t launch_kv_compact(const PoolArgs& a, int32_t* used, cudaStream_t stream) {
@@ -547,14 +622,8 @@ cudaError_t launch_kv_compact(const PoolArgs& a, int32_t* used, cudaStream_t str
   p.to = p.from + a.num_blocks;
   p.rank = p.to + a.num_blocks;
   p.status = a.status;
-  PoolTensors pt;
-  if (!lay_out(a, pt)) return cudaErrorInvalidValue;
-  cudaError_t e = launch_early(kv_compact_plan_kernel, dim3(1), kThreads, 0, stream, p);
-  if (e != cudaSuccess) return e;
-  const int rows = std::max(1, std::min(a.batch, device_sm_count()));
-  const int ctas = rows + move_ctas(a.num_blocks / 2 * pt.first[pt.n]);  // at most half of the blocks move
-  return launch_early(kv_compact_apply_kernel, dim3(static_cast<unsigned>(ctas)), kMoveThreads, 0, stream, p, pt,
-                      rows);
+  if (a.n_tensors <= 8) return compact<8>(a, p, stream);
+  return a.n_tensors <= 64 ? compact<64>(a, p, stream) : compact<kPoolMaxTensors>(a, p, stream);
 }
 
 }  // namespace attn
