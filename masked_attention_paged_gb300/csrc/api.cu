@@ -1171,7 +1171,6 @@ attn_status paged_attn_f8(const attn_tensor* q, const attn_kv_cache_f8* cache, c
   a.lse = lse;
   a.partials = static_cast<uint8_t*>(workspace) + kStatusBytes;
   a.n_cta = device_sm_count();
-  a.gen = next_count_gen();
   a.status = static_cast<uint32_t*>(workspace);
   if (a.n_cta <= 0) return ATTN_ERR_CUDA;
   return from_cuda(launch_paged_attn_f8(a, stream));

@@ -7,12 +7,21 @@
 //    bits and e4m3 four, so hi + lo is q exactly, down to 2^-19 of the largest
 //    element.  hi and lo of eight rows are the 16 rows of one m16n8k32 product with
 //    the codes as they lie in the cache; adding a lane's two accumulators is the score,
-//    and the block's scale multiplies it.
-//  * the values go in transposed, O^T = V^T W^T (m16n8k16, fp16): a head's weights
+//    and the block's scale multiplies it.  (fp16 throughout, K converted like V, took 151
+//    us where this took 140.)
+//  * the values go in transposed, O^T = V^T W^T (m16n8k16, fp16): a row's weights
 //    are, register for register, their score fragment, and codes become fp16 exactly,
 //    two an instruction.  The block's value scale multiplies the products.
-// A warp's blocks arrive in its own ring of kStages; softmax is online with a lazy
-// running max (log2 units, it moves when a block exceeds it by kLazy).
+// Softmax is online with a lazy running max (log2 units, it moves when a block exceeds
+// it by kLazy).
+//
+// What bounds it is HBM, so nothing may stop the stream of blocks.  All blocks of the
+// call, item (sequence, KV head) after item, are laid end to end, and every warp takes an
+// equal run of them, kStages ahead in a ring of its own, across the items' borders.  No
+// warp waits for another: an item inside a run is written at once, one that is cut
+// leaves partials (normalised rows and log2 LSE; at most two a warp), which a second
+// launch joins in order, so results do not depend on timing.  (CTAs of 1024 tokens of an
+// item, joined by the last to come, spent 4 us each on their start and end.)
 #include <cuda.h>
 #include <math.h>
 
@@ -21,13 +30,13 @@
 #include "common.cuh"
 #include "f8.cuh"
 #include "internal.h"
+#include "runs.cuh"
 
 namespace attn {
 namespace {
 
 constexpr int kBS = 16;
 constexpr int kWarps = 4;
-constexpr int kStages = 3;
 constexpr float kLazy = 8.0f;
 
 struct F8MmaParams {
@@ -40,6 +49,7 @@ struct F8MmaParams {
   int Hkv, Hq, G, T;
   const uint16_t* q;
   int64_t q_stride[3];
+  int B;
   const int32_t* bt;
   int64_t bt_stride;
   int max_blocks;
@@ -47,15 +57,14 @@ struct F8MmaParams {
   const int32_t* lens;
   int causal;
   float scale_log2;
-  int split_tokens, n_split;
   void* out;
   int out_bf16;
   int64_t out_stride[3];
   float* lse;
-  float* part_o;    // [(b, KV head, split)][8 NR][D]
-  float* part_lse;  // [the same][8 NR], log2 units
-  unsigned long long* count;  // [b, KV head]
-  uint32_t gen;
+  int warps;        // of the launch
+  int side;         // heads side by side: warps that take the same run, a head each
+  float* part_o;    // [2 warps][8 NR][D]: a warp's first segment, and a later one
+  float* part_lse;  // [2 warps][8 NR], log2 units
   uint32_t* status;
 };
 
@@ -98,507 +107,661 @@ __device__ __forceinline__ int queries(const F8MmaParams& p, int b, int& start, 
   return start < 0 || past ? 0 : n;
 }
 
-template <int D>
-__device__ __forceinline__ void write_row(const F8MmaParams& p, int b, int h, int i, int d, float x, float y) {
-  const int64_t at = b * p.out_stride[0] + h * p.out_stride[1] + i * p.out_stride[2] + d;
-  if (p.out_bf16)
-    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at) = pack_bf16x2(x, y);
-  else
-    *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at) = make_float2(x, y);
+// An item's blocks: those with a key that some row sees.
+__device__ __forceinline__ int seq_blocks(const F8MmaParams& p, int b, int& start, int& n, bool& past) {
+  n = queries(p, b, start, past);
+  return n == 0 ? 0 : (start + n - 1) / kBS + 1;
+}
+// The sum of f(b) over the sequences, for a whole warp (64 bits: tables may be wide).
+template <typename F>
+__device__ __forceinline__ int64_t sum_over(int lane, int B, F f) {
+  int64_t s = 0;
+  for (int b = lane; b < B; b += 32) s += f(b);
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+  return s;
+}
+// The first sequence after b that has blocks (B: none), for a whole warp.
+__device__ __forceinline__ int next_seq(const F8MmaParams& p, int lane, int b, int& n_blocks) {
+  for (int base = b + 1; base < p.B; base += 32) {
+    int start, n, k = 0;
+    bool past;
+    if (base + lane < p.B) k = seq_blocks(p, base + lane, start, n, past);
+    const uint32_t some = __ballot_sync(0xffffffffu, k > 0);
+    if (some != 0u) {
+      const int l = __ffs(static_cast<int>(some)) - 1;
+      n_blocks = __shfl_sync(0xffffffffu, k, l);
+      return base + l;
+    }
+  }
+  n_blocks = 0;
+  return p.B;
+}
+// Runs of at least kLeast blocks: a shorter one is all start and end (8: 14.0 us for one
+// sequence of 700 tokens and D = 64 where 2 take 10.1).
+constexpr int kLeast = 2;
+// Heads side by side: their rows of a block lie together in memory, and are read at about the
+// same time (64 sequences of 8192: 137.5 us; 138.2 with 4 heads, 139.1 with each on its own).
+constexpr int kSide = 8;
+__device__ __forceinline__ Runs64 runs_of(int64_t total, int warps) {
+  return Runs64::make(total, static_cast<int>(min(static_cast<int64_t>(warps), (total + kLeast - 1) / kLeast)));
 }
 
-// grid (splits, KV heads, sequences)
+// Eight (D = 64) or sixteen dims of a row, scaled.
+template <int E>
+__device__ __forceinline__ void write_dims(void* out, int out_bf16, int64_t at, const float (&x)[E]) {
+  if (out_bf16) {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i)
+      dst[i] = make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]), pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
+                          pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+  } else {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+  }
+}
+
 template <int D, int NR>
-__global__ void __launch_bounds__(kWarps * 32, NR == 1 ? 4 : 3)
+struct MmaCfg {
+  // CTAs an SM, by registers: 64 sequences of 8192 tokens with 4 rows take 137 us on three, 150
+  // on four (128 registers) and 149 on two; with 16 rows 232 on two and 286 on three, which
+  // spill.  64 of 4096 with 16 rows and D = 64: 96 on two, 84 on three.
+  static constexpr int kCtas = D == 128 && NR == 2 ? 2 : 3;
+  // More blocks in flight make the stream slower: the same 137 us with three are 143 with four
+  // and 195 with five (138 with two); 237 with six for 16 rows, 231 with four.
+  static constexpr int kStages = NR == 1 ? 3 : 4;
+  static constexpr int kCodeBytes = kBS * D;  // one (block, head) of K or V
+  static constexpr int kSmem = 1024 + kWarps * kStages * (2 * kCodeBytes + 16);
+};
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kWarps * 32, MmaCfg<D, NR>::kCtas)
     paged_attn_f8_mma_kernel(const __grid_constant__ F8MmaParams p) {
-  constexpr int kCodeBytes = kBS * D;  // one (block, head) of K or V
+  using C = MmaCfg<D, NR>;
+  constexpr int kStages = C::kStages, kCodeBytes = C::kCodeBytes;
   constexpr int kRows = 8 * NR;
-  constexpr int kSteps = D / 32;       // of the score product
-  constexpr int kTiles = D / 16;       // of the output's dims
-  constexpr int kRec = D + 2;
+  constexpr int kSteps = D / 32;  // of the score product
+  constexpr int kTiles = D / 16;  // of the output's dims
   extern __shared__ uint8_t smem_raw[];
   uint8_t* codes = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // [warp][stage][K, V]
   uint64_t* bars = reinterpret_cast<uint64_t*>(codes + kWarps * kStages * 2 * kCodeBytes);
-  float* comb = reinterpret_cast<float*>(codes);  // [warp][row][D + 2] at the end
-  static_assert(kWarps * kRows * kRec * 4 <= kWarps * kStages * 2 * kCodeBytes, "records fit");
-  __shared__ int abort_flag, s_last;
+  float2* scales = reinterpret_cast<float2*>(bars + kWarps * kStages);  // [warp][stage] K's and V's; x = -inf: no block
+  __shared__ int abort_flag[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* wcodes = codes + warp * kStages * 2 * kCodeBytes;
   uint64_t* wbar = bars + warp * kStages;
+  float2* wscale = scales + warp * kStages;
+  int* abort = &abort_flag[warp];
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&wbar[s], 1);
-    if (warp == 0) {
-      abort_flag = 0;
-      if constexpr (D == 128) {
-        tma_prefetch_desc(&p.kmap);
-        tma_prefetch_desc(&p.vmap);
-      }
+    *abort = 0;
+    if constexpr (D == 128) {
+      tma_prefetch_desc(&p.kmap);
+      tma_prefetch_desc(&p.vmap);
     }
   }
   fence_mbar_init();
   let_next_launch_in();
-  __syncthreads();
+  __syncwarp();
   wait_for_launch_ahead();
 
-  const int split = blockIdx.x, gkv = blockIdx.y, b = blockIdx.z;
-  const int R = p.T * p.G;  // rows of the KV head: query r / G, head r % G
-  int start;
-  bool past;
-  const int n = queries(p, b, start, past);
-  if (past && threadIdx.x == 0 && split == 0) report(p.status, kStatusBounds);
-  // the keys that row r sees: [0, limit)
-  auto limit = [&](int r) {
-    const int i = r / p.G;
-    return r >= R || i >= n ? 0 : (p.causal ? start + i + 1 : start + n);
+  // ---- this warp's run, and where it begins
+  const int me = blockIdx.x * kWarps + warp;
+  auto blocks_of = [&](int b) {
+    int start, n;
+    bool past;
+    return seq_blocks(p, b, start, n, past);
   };
-  const int kend = n == 0 ? 0 : limit(n * p.G - 1);  // keys of the last row that sees any
-  const int kfirst = limit(0);                        // and of the first
-  auto write_empty = [&](int r) {
-    const int h = gkv * p.G + r % p.G, i = r / p.G;
-    for (int d = 2 * lane; d < D; d += 64) write_row<D>(p, b, h, i, d, 0.f, 0.f);
-    if (lane == 0 && p.lse != nullptr) p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.T + i] = -INFINITY;
-  };
-  const int t_begin = split * p.split_tokens;
-  if (t_begin >= kend) {
-    if (split == 0)  // no row sees anything
-      for (int r = warp; r < R; r += kWarps) write_empty(r);
-    return;
+  const int run_of_warp = me / p.side, off = me - run_of_warp * p.side;
+  const int Hgr = p.Hkv / p.side;  // groups of heads
+  const int64_t total = Hgr * sum_over(lane, p.B, [&](int b) {
+    int start, n;
+    bool past;
+    const int k = seq_blocks(p, b, start, n, past);
+    if (past && me == 0) report(p.status, kStatusBounds);
+    return k;
+  });
+  const Runs64 runs = runs_of(total, p.warps / p.side);
+  if (run_of_warp >= runs.n) return;
+  const int64_t lo = runs.lo(run_of_warp);
+  int left = static_cast<int>(runs.lo(run_of_warp + 1) - lo);  // blocks to take (a run of 2^31 would be 2^35 tokens)
+  int b = 0, grp = 0, blk = 0;                        // the next one
+  {
+    int64_t run = 0;
+    for (int base = 0;; base += 32) {
+      const int64_t mine = base + lane < p.B ? static_cast<int64_t>(blocks_of(base + lane)) * Hgr : 0;
+      int64_t incl = mine;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, incl, m);
+        if (lane >= m) incl += up;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, run + incl > lo);
+      if (past != 0u) {
+        const int l = __ffs(static_cast<int>(past)) - 1;
+        const int64_t local = lo - run - __shfl_sync(0xffffffffu, incl - mine, l);
+        const int each = static_cast<int>(__shfl_sync(0xffffffffu, mine, l) / Hgr);
+        b = base + l;
+        grp = static_cast<int>(div_pos(local, static_cast<int64_t>(each)));
+        blk = static_cast<int>(local - static_cast<int64_t>(grp) * each);
+        break;
+      }
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
   }
-  const int t_end = min(kend, t_begin + p.split_tokens);
-  const int nblk = (t_end - t_begin + kBS - 1) / kBS;
-  const int lb0 = t_begin / kBS;
 
-  const int my_n = nblk > warp ? (nblk - warp + kWarps - 1) / kWarps : 0;  // at most 32
-  int my_blk = -1;
+  // ---- the stream: blocks are asked for kStages ahead, lane i looking up number i of a
+  // window of 32 in an item
+  int ib = b, ig = grp, iblk = blk, inum = blocks_of(b), ileft = left;  // the next to be asked for
+  int win = 0, wlen = 0, wat = 0;  // the window's first block, its length, and the place in it
+  int my_id = -1;
   float my_ks = 0.f, my_vs = 0.f;
-  if (lane < my_n) {
-    my_blk = p.bt[b * p.bt_stride + lb0 + warp + kWarps * lane];
-    if (my_blk < 0 || my_blk >= p.num_blocks) {
-      report(p.status, kStatusBounds);
-      my_blk = -1;
-    } else {
-      my_ks = p.ks[static_cast<int64_t>(my_blk) * p.Hkv + gkv];
-      my_vs = p.vs[static_cast<int64_t>(my_blk) * p.Hkv + gkv];
-    }
-  }
-  auto issue = [&](int s, int blk) {
-    if (blk < 0) {  // bad id: the phase completes without data; the block is left out
-      mbar_arrive(&wbar[s]);
-      return;
-    }
-    uint8_t* dst = wcodes + s * 2 * kCodeBytes;
-    fence_proxy_async_smem();
-    mbar_arrive_expect_tx(&wbar[s], 2 * kCodeBytes);
-    if constexpr (D == 128) {
-      tma_load_4d(dst, &p.kmap, &wbar[s], 0, 0, gkv, blk);
-      tma_load_4d(dst + kCodeBytes, &p.vmap, &wbar[s], 0, 0, gkv, blk);
-    } else {
-      const int64_t at = (static_cast<int64_t>(blk) * p.Hkv + gkv) * kCodeBytes;
-      bulk_load(dst, p.kq + at, kCodeBytes, &wbar[s]);
-      bulk_load(dst + kCodeBytes, p.vq + at, kCodeBytes, &wbar[s]);
-    }
-  };
-  int issued = 0;
-  for (; issued < kStages && issued < my_n; ++issued) {
-    const int blk = __shfl_sync(0xffffffffu, my_blk, issued);
-    if (lane == 0) issue(issued, blk);
-  }
-
-  // ---- q as e4m3 A fragments, hi in rows 0..7, lo in rows 8..15.  The lane's dims are
-  // 16 t .. 16 t + 15 (and, D = 128, 64 more on): the word w of a token's 16 codes there
-  // meets q's word w, whatever order the product gives them.
-  uint32_t qa[NR][kSteps][4];
-  float mul[NR];  // scores in log2 units from products of q's codes with unscaled K codes
-  int lim[NR];
-#pragma unroll
-  for (int nr = 0; nr < NR; ++nr) {
-    const int r = 8 * nr + g;
-    lim[nr] = limit(r);
-    float x[kSteps * 8], a = 0.f;
-    const bool there = lim[nr] > 0;
-    const uint16_t* row =
-        p.q + b * p.q_stride[0] + (gkv * p.G + r % p.G) * p.q_stride[1] + static_cast<int64_t>(r / p.G) * p.q_stride[2];
-#pragma unroll
-    for (int c = 0; c < kSteps; ++c) {
-      const uint4 w = there ? *reinterpret_cast<const uint4*>(row + 16 * t + 64 * (c / 2) + 8 * (c % 2))
-                            : make_uint4(0u, 0u, 0u, 0u);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[8 * c + 2 * k] = bf16lo_to_f32(u[k]);
-        x[8 * c + 2 * k + 1] = bf16hi_to_f32(u[k]);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kSteps * 8; ++k) {
-      if (fabsf(x[k]) < INFINITY)
-        a = fmaxf(a, fabsf(x[k]));
-      else
-        x[k] = NAN;  // infinite scores make no distribution either
-    }
-    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-    const int e2 = a > 0.f ? f8_scale_exponent(a) : 0;
-    const float inv = pow2(-e2);
-    mul[nr] = p.scale_log2 * pow2(e2);
-#pragma unroll
-    for (int c = 0; c < kSteps; ++c)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {  // the word's four dims
-        uint32_t hi = 0u, lo = 0u;
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const float x0 = x[8 * c + 4 * k + e] * inv, x1 = x[8 * c + 4 * k + e + 1] * inv;
-          const uint32_t h2 = f8_codes(x0, x1);
-          float y0, y1;
-          half2_f32(f8_half2(h2), y0, y1);
-          hi |= h2 << (8 * e);
-          lo |= f8_codes(x0 - y0, x1 - y1) << (8 * e);
+  int stage_in = 0;
+  auto issue = [&]() {  // for the whole warp
+    if (ileft == 0) return;
+    if (wat == wlen) {
+      if (iblk == inum) {  // the next item
+        iblk = 0;
+        if (++ig == Hgr) {
+          ig = 0;
+          ib = next_seq(p, lane, ib, inum);  // (there is more to take, so one follows)
         }
-        qa[nr][c][2 * k] = hi;
-        qa[nr][c][2 * k + 1] = lo;
       }
-  }
-
-  const int T[4] = {tok_of(2 * t), tok_of(2 * t + 1), 8 + tok_of(2 * t), 8 + tok_of(2 * t + 1)};
-  const int krow = tok_of(g);
-  // O^T: tile j holds dims (D / 8) g + 2 j (rows g) and the next one (rows g + 8) of every
-  // row; columns 2t, 2t + 1 are this lane's rows
-  float o[NR][kTiles][4];
-  float m_run[NR], l_part[NR];  // of row g: running max (log2), this lane's sum
-#pragma unroll
-  for (int nr = 0; nr < NR; ++nr) {
-    m_run[nr] = -INFINITY, l_part[nr] = 0.f;
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[nr][j][e] = 0.f;
-  }
-
-  bool ok = true;
-  int s = 0;
-  uint32_t ph = 0;
-  for (int i = 0; i < my_n; ++i) {
-    const int blk = __shfl_sync(0xffffffffu, my_blk, i);
-    const float ks = __shfl_sync(0xffffffffu, my_ks, i), vs = __shfl_sync(0xffffffffu, my_vs, i);
-    if (!__all_sync(0xffffffffu, mbar_wait(&wbar[s], ph, &abort_flag, p.status))) {
-      ok = false;
-      break;
-    }
-    if (blk >= 0) {
-      const uint8_t* kb = wcodes + s * 2 * kCodeBytes;
-      const uint8_t* vb = kb + kCodeBytes;
-      const int tok0 = (lb0 + warp + kWarps * i) * kBS;
-      // ---- scores: n-tile j holds tokens 8 j + tok_of(n)
-      uint32_t pb[NR][2];
-      float sc[NR][4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint8_t* rowp = kb + (8 * j + krow) * D;
-        uint32_t w[kSteps][2];
-        if constexpr (D == 128) {
-          const uint4 k0 = *reinterpret_cast<const uint4*>(rowp + ((t ^ krow) << 4));
-          const uint4 k1 = *reinterpret_cast<const uint4*>(rowp + (((t + 4) ^ krow) << 4));
-          w[0][0] = k0.x, w[0][1] = k0.y, w[1][0] = k0.z, w[1][1] = k0.w;
-          w[2][0] = k1.x, w[2][1] = k1.y, w[3][0] = k1.z, w[3][1] = k1.w;
+      win = iblk;
+      wlen = min(32, min(inum - iblk, ileft));
+      wat = 0;
+      my_id = -1;
+      if (lane < wlen) {
+        my_id = p.bt[ib * p.bt_stride + win + lane];
+        if (my_id < 0 || my_id >= p.num_blocks) {
+          report(p.status, kStatusBounds);
+          my_id = -1;
         } else {
-          const uint4 k0 = *reinterpret_cast<const uint4*>(rowp + (t << 4));
-          w[0][0] = k0.x, w[0][1] = k0.y, w[1][0] = k0.z, w[1][1] = k0.w;
-        }
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < kSteps; ++c)
-            mma_e4m3(acc, qa[nr][c][0], qa[nr][c][1], qa[nr][c][2], qa[nr][c][3], w[c][0], w[c][1]);
-          sc[nr][2 * j] = acc[0] + acc[2];
-          sc[nr][2 * j + 1] = acc[1] + acc[3];
+          my_ks = p.ks[static_cast<int64_t>(my_id) * p.Hkv + ig * p.side + off];
+          my_vs = p.vs[static_cast<int64_t>(my_id) * p.Hkv + ig * p.side + off];
         }
       }
-      // ---- softmax
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr) {
-        const float f = mul[nr] * ks;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sc[nr][k] = tok0 + T[k] < lim[nr] ? sc[nr][k] * f : -INFINITY;
-        float bm = fmaxf(fmaxf(sc[nr][0], sc[nr][1]), fmaxf(sc[nr][2], sc[nr][3]));
-        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
-        // the reference max moves only by more than the margin
-        const bool moves = bm > m_run[nr] + kLazy;
-        if (__any_sync(0xffffffffu, moves)) {
-          const float alpha = moves ? fast_exp2(m_run[nr] - bm) : 1.f;  // 0 when m_run was -inf
-          if (moves) m_run[nr] = bm;
-          l_part[nr] *= alpha;
-          const float f0 = __shfl_sync(0xffffffffu, alpha, 8 * t), f1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
-#pragma unroll
-          for (int j = 0; j < kTiles; ++j) {
-            o[nr][j][0] *= f0;
-            o[nr][j][1] *= f1;
-            o[nr][j][2] *= f0;
-            o[nr][j][3] *= f1;
-          }
-        }
-        const float ref = m_run[nr] == -INFINITY ? 0.f : m_run[nr];
-        float w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = fast_exp2(sc[nr][k] - ref);
-        l_part[nr] += (w[0] + w[1]) + (w[2] + w[3]);
-        pb[nr][0] = pack_half2(w[0], w[1]);
-        pb[nr][1] = pack_half2(w[2], w[3]);
-      }
-      // ---- values: the lane's D / 8 dims of its four tokens
-      constexpr int kWords = D / 32;
-      uint32_t vw[4][kWords];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
+    }
+    if (lane == wat) {
+      uint64_t* bar = &wbar[stage_in];
+      uint8_t* dst = wcodes + stage_in * 2 * kCodeBytes;
+      if (my_id < 0) {  // bad id: the phase completes without data; the block is left out
+        wscale[stage_in] = make_float2(-INFINITY, 0.f);
+        mbar_arrive(bar);
+      } else {
+        wscale[stage_in] = make_float2(my_ks, my_vs);
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(bar, 2 * kCodeBytes);
         if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(vb + T[k] * D + ((g ^ (T[k] & 7)) << 4));
-          vw[k][0] = x.x, vw[k][1] = x.y, vw[k][2] = x.z, vw[k][3] = x.w;
+          tma_load_4d(dst, &p.kmap, bar, 0, 0, ig * p.side + off, my_id);
+          tma_load_4d(dst + kCodeBytes, &p.vmap, bar, 0, 0, ig * p.side + off, my_id);
         } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(vb + T[k] * D + g * 8);
-          vw[k][0] = x.x, vw[k][1] = x.y;
-        }
-      }
-      // Slots past the last key may hold NaN codes, and 0 x NaN is NaN.  So do tokens that
-      // some rows see and others do not: their NaN codes go in as zeros and are
-      // handed to the rows that see them.
-      if (tok0 + kBS > kfirst) {
-        uint32_t bad[4][kWords], any = 0u;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int c = 0; c < kWords; ++c) {
-            if (tok0 + T[k] >= kend) vw[k][c] = 0u;
-            bad[k][c] = nan_codes(vw[k][c]);
-            any |= bad[k][c];
-          }
-        if (__any_sync(0xffffffffu, any != 0u)) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int c = 0; c < kWords; ++c) vw[k][c] &= ~((bad[k][c] >> 7) * 255u);
-          // which of the dims have a NaN that the row sees: a product of ones
-#pragma unroll
-          for (int nr = 0; nr < NR; ++nr) {
-            uint32_t see[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              see[k] = (tok0 + T[2 * k] < lim[nr] ? 0x3c00u : 0u) | (tok0 + T[2 * k + 1] < lim[nr] ? 0x3c000000u : 0u);
-#pragma unroll
-            for (int j = 0; j < kTiles; ++j) {
-              uint32_t a[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {  // rows g + 8 (e & 1): dim 2 j + (e & 1); tokens 2 (e >> 1), + 1
-                const int byte = 2 * j + (e & 1), k = 2 * (e >> 1);
-                a[e] = ((bad[k][byte / 4] >> (8 * (byte % 4) + 7)) & 1u ? 0x3c00u : 0u) |
-                       ((bad[k + 1][byte / 4] >> (8 * (byte % 4) + 7)) & 1u ? 0x3c000000u : 0u);
-              }
-              float hit[4];
-              mma_f16_zero(hit, a, see[0], see[1]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (hit[e] > 0.f) o[nr][j][e] = NAN;
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < kWords; ++c) {
-        const uint32_t ab0 = prmt<0x5140u>(vw[0][c], vw[1][c]), ab1 = prmt<0x7362u>(vw[0][c], vw[1][c]);
-        const uint32_t cd0 = prmt<0x5140u>(vw[2][c], vw[3][c]), cd1 = prmt<0x7362u>(vw[2][c], vw[3][c]);
-        const uint32_t a0[4] = {f8_half2(ab0), f8_half2(ab0 >> 16), f8_half2(cd0), f8_half2(cd0 >> 16)};
-        const uint32_t a1[4] = {f8_half2(ab1), f8_half2(ab1 >> 16), f8_half2(cd1), f8_half2(cd1 >> 16)};
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-          float x[4];
-          mma_f16_zero(x, a0, pb[nr][0], pb[nr][1]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[nr][2 * c][e] = fmaf(x[e], vs, o[nr][2 * c][e]);
-          mma_f16_zero(x, a1, pb[nr][0], pb[nr][1]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[nr][2 * c + 1][e] = fmaf(x[e], vs, o[nr][2 * c + 1][e]);
+          const int64_t at = (static_cast<int64_t>(my_id) * p.Hkv + ig * p.side + off) * kCodeBytes;
+          bulk_load(dst, p.kq + at, kCodeBytes, bar);
+          bulk_load(dst + kCodeBytes, p.vq + at, kCodeBytes, bar);
         }
       }
     }
     __syncwarp();
-    if (issued < my_n) {
-      const int nb = __shfl_sync(0xffffffffu, my_blk, issued);
-      if (lane == 0) issue(s, nb);
-      ++issued;
-    }
-    if (++s == kStages) s = 0, ph ^= 1u;
-  }
-  if (!ok)  // let the copies in flight land
-    for (int i = max(0, issued - kStages); i < issued; ++i) drain_wait(&wbar[i % kStages], (i / kStages) & 1);
+    ++wat, ++iblk, --ileft;
+    if (++stage_in == kStages) stage_in = 0;
+  };
+  for (int s = 0; s < kStages; ++s) issue();
 
-  // ---- the warps' states, joined in shared memory
+  const int T[4] = {tok_of(2 * t), tok_of(2 * t + 1), 8 + tok_of(2 * t), 8 + tok_of(2 * t + 1)};
+  const int krow = tok_of(g);
+  const int R = p.T * p.G;  // rows of the KV head: query r / G, head r % G
+  bool ok = true;
+  int s = 0;
+  uint32_t ph = 0;
+  for (int seg = 0; ok && left > 0; ++seg) {
+    const int gkv = grp * p.side + off;
+    int start, n;
+    bool past;
+    const int nblk = seq_blocks(p, b, start, n, past);
+    const int blk0 = blk, count = min(left, nblk - blk);
+    // the keys that row r sees: [0, limit)
+    auto limit = [&](int r) {
+      const int i = r / p.G;
+      return r >= R || i >= n ? 0 : (p.causal ? start + i + 1 : start + n);
+    };
+    const int kend = limit(n * p.G - 1);  // keys of the last row that sees any
+    const int kfirst = limit(0);          // and of the first
+
+    // ---- q as e4m3 A fragments, hi in rows 0..7, lo in rows 8..15.  The lane's dims are
+    // 16 t .. 16 t + 15 (and, D = 128, 64 more on): the word w of a token's 16 codes there
+    // meets q's word w, whatever order the product gives them.
+    uint32_t qa[NR][kSteps][4];
+    float mul[NR];  // scores in log2 units from products of q's codes with unscaled K codes
+    int lim[NR];
 #pragma unroll
-  for (int nr = 0; nr < NR; ++nr) {
-    l_part[nr] += __shfl_xor_sync(0xffffffffu, l_part[nr], 1);
-    l_part[nr] += __shfl_xor_sync(0xffffffffu, l_part[nr], 2);
-  }
-  __syncthreads();  // every warp's codes have been read
+    for (int nr = 0; nr < NR; ++nr) {
+      const int r = 8 * nr + g;
+      lim[nr] = limit(r);
+      float x[kSteps * 8], a = 0.f;
+      const bool there = lim[nr] > 0;
+      const uint16_t* row =
+          p.q + b * p.q_stride[0] + (gkv * p.G + r % p.G) * p.q_stride[1] + r / p.G * p.q_stride[2];
 #pragma unroll
-  for (int nr = 0; nr < NR; ++nr) {
-    if (t == 0) {
-      float* rec = comb + (warp * kRows + 8 * nr + g) * kRec + D;
-      rec[0] = m_run[nr];
-      rec[1] = l_part[nr];
-    }
+      for (int c = 0; c < kSteps; ++c) {
+        const uint4 w = there ? *reinterpret_cast<const uint4*>(row + 16 * t + 64 * (c / 2) + 8 * (c % 2))
+                              : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int hc = 0; hc < 2; ++hc) {
-      float* rec = comb + (warp * kRows + 8 * nr + 2 * t + hc) * kRec + (D / 8) * g;
-#pragma unroll
-      for (int j = 0; j < kTiles; ++j) {
-        rec[2 * j] = o[nr][j][hc];
-        rec[2 * j + 1] = o[nr][j][2 + hc];
-      }
-    }
-  }
-  __syncthreads();
-  const int ns = (kend + p.split_tokens - 1) / p.split_tokens;  // splits with keys
-  const int64_t unit = static_cast<int64_t>(b) * p.Hkv + gkv;
-  for (int r = warp; r < R; r += kWarps) {
-    float M = -INFINITY, wgt[kWarps], l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, comb[(w * kRows + r) * kRec + D]);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float* rec = comb + (w * kRows + r) * kRec + D;
-      // a warp that saw nothing has max -inf and sum 0; a NaN sum is something
-      wgt[w] = rec[0] == -INFINITY ? (rec[1] == 0.f ? 0.f : 1.f) : fast_exp2(rec[0] - M);
-      l = fmaf(wgt[w], rec[1], l);
-    }
-    const bool empty = l == 0.f;
-    const float inv = empty ? 0.f : 1.f / l;
-    const float lse2 = empty ? -INFINITY : M + __log2f(l);
-    const int h = gkv * p.G + r % p.G, i = r / p.G;
-    const int64_t slot = (unit * p.n_split + split) * kRows + r;
-    for (int d = 2 * lane; d < D; d += 64) {
-      float x = 0.f, y = 0.f;
-      if (!empty) {
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float* rec = comb + (w * kRows + r) * kRec + d;
-          if (wgt[w] == 0.f) continue;
-          x = fmaf(wgt[w], rec[0], x);
-          y = fmaf(wgt[w], rec[1], y);
+        for (int k = 0; k < 4; ++k) {
+          x[8 * c + 2 * k] = bf16lo_to_f32(u[k]);
+          x[8 * c + 2 * k + 1] = bf16hi_to_f32(u[k]);
         }
       }
-      if (ns == 1)
-        write_row<D>(p, b, h, i, d, x * inv, y * inv);
-      else
-        *reinterpret_cast<float2*>(p.part_o + slot * D + d) = make_float2(x * inv, y * inv);
+#pragma unroll
+      for (int k = 0; k < kSteps * 8; ++k) {
+        if (fabsf(x[k]) < INFINITY)
+          a = fmaxf(a, fabsf(x[k]));
+        else
+          x[k] = NAN;  // infinite scores make no distribution either
+      }
+      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+      const int e2 = a > 0.f ? f8_scale_exponent(a) : 0;
+      const float inv = pow2(-e2);
+      mul[nr] = p.scale_log2 * pow2(e2);
+#pragma unroll
+      for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // the word's four dims
+          uint32_t hi = 0u, lo = 0u;
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const float x0 = x[8 * c + 4 * k + e] * inv, x1 = x[8 * c + 4 * k + e + 1] * inv;
+            const uint32_t h2 = f8_codes(x0, x1);
+            float y0, y1;
+            half2_f32(f8_half2(h2), y0, y1);
+            hi |= h2 << (8 * e);
+            lo |= f8_codes(x0 - y0, x1 - y1) << (8 * e);
+          }
+          qa[nr][c][2 * k] = hi;
+          qa[nr][c][2 * k + 1] = lo;
+        }
     }
-    if (lane == 0) {
-      if (ns > 1)
-        p.part_lse[slot] = lse2;
-      else if (p.lse != nullptr)
-        p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.T + i] = lse2 * 0.6931471805599453f;
-    }
-  }
-  if (ns == 1) return;
 
-  // ---- the last split of the unit to come here joins them all, in order
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    s_last = count_last(p.count + unit, p.gen, ns);
+    // O^T: tile j holds dims (D / 8) g + 2 j (rows g) and the next one (rows g + 8) of every
+    // row; columns 2t, 2t + 1 are this lane's rows
+    float o[NR][kTiles][4];
+    float m_run[NR], l_part[NR];  // of row g: running max (log2), this lane's sum
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+      m_run[nr] = -INFINITY, l_part[nr] = 0.f;
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nr][j][e] = 0.f;
+    }
+
+    for (; blk < blk0 + count; ++blk, --left) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&wbar[s], ph, abort, p.status))) {
+        ok = false;
+        break;
+      }
+      const float2 two = wscale[s];
+      const float ks = two.x, vs = two.y;
+      if (ks != -INFINITY) {
+        const uint8_t* kb = wcodes + s * 2 * kCodeBytes;
+        const uint8_t* vb = kb + kCodeBytes;
+        const int tok0 = blk * kBS;
+        // ---- scores: n-tile j holds tokens 8 j + tok_of(n)
+        uint32_t pb[NR][2];
+        float sc[NR][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint8_t* rowp = kb + (8 * j + krow) * D;
+          uint32_t w[kSteps][2];
+          if constexpr (D == 128) {
+            const uint4 k0 = *reinterpret_cast<const uint4*>(rowp + ((t ^ krow) << 4));
+            const uint4 k1 = *reinterpret_cast<const uint4*>(rowp + (((t + 4) ^ krow) << 4));
+            w[0][0] = k0.x, w[0][1] = k0.y, w[1][0] = k0.z, w[1][1] = k0.w;
+            w[2][0] = k1.x, w[2][1] = k1.y, w[3][0] = k1.z, w[3][1] = k1.w;
+          } else {
+            const uint4 k0 = *reinterpret_cast<const uint4*>(rowp + (t << 4));
+            w[0][0] = k0.x, w[0][1] = k0.y, w[1][0] = k0.z, w[1][1] = k0.w;
+          }
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < kSteps; ++c)
+              mma_e4m3(acc, qa[nr][c][0], qa[nr][c][1], qa[nr][c][2], qa[nr][c][3], w[c][0], w[c][1]);
+            sc[nr][2 * j] = acc[0] + acc[2];
+            sc[nr][2 * j + 1] = acc[1] + acc[3];
+          }
+        }
+        // ---- softmax
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          const float f = mul[nr] * ks;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sc[nr][k] = tok0 + T[k] < lim[nr] ? sc[nr][k] * f : -INFINITY;
+          float bm = fmaxf(fmaxf(sc[nr][0], sc[nr][1]), fmaxf(sc[nr][2], sc[nr][3]));
+          bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
+          bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
+          // the reference max moves only by more than the margin
+          const bool moves = bm > m_run[nr] + kLazy;
+          if (__any_sync(0xffffffffu, moves)) {
+            const float alpha = moves ? fast_exp2(m_run[nr] - bm) : 1.f;  // 0 when m_run was -inf
+            if (moves) m_run[nr] = bm;
+            l_part[nr] *= alpha;
+            const float f0 = __shfl_sync(0xffffffffu, alpha, 8 * t), f1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) {
+              o[nr][j][0] *= f0;
+              o[nr][j][1] *= f1;
+              o[nr][j][2] *= f0;
+              o[nr][j][3] *= f1;
+            }
+          }
+          const float ref = m_run[nr] == -INFINITY ? 0.f : m_run[nr];
+          float w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = fast_exp2(sc[nr][k] - ref);
+          l_part[nr] += (w[0] + w[1]) + (w[2] + w[3]);
+          pb[nr][0] = pack_half2(w[0], w[1]);
+          pb[nr][1] = pack_half2(w[2], w[3]);
+        }
+        // ---- values: the lane's D / 8 dims of its four tokens
+        constexpr int kWords = D / 32;
+        uint32_t vw[4][kWords];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(vb + T[k] * D + ((g ^ (T[k] & 7)) << 4));
+            vw[k][0] = x.x, vw[k][1] = x.y, vw[k][2] = x.z, vw[k][3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(vb + T[k] * D + g * 8);
+            vw[k][0] = x.x, vw[k][1] = x.y;
+          }
+        }
+        // Slots past the last key may hold NaN codes, and 0 x NaN is NaN.  So do tokens that
+        // some rows see and others do not: their NaN codes go in as zeros and are
+        // handed to the rows that see them.
+        if (tok0 + kBS > kfirst) {
+          uint32_t bad[4][kWords], any = 0u;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int c = 0; c < kWords; ++c) {
+              if (tok0 + T[k] >= kend) vw[k][c] = 0u;
+              bad[k][c] = nan_codes(vw[k][c]);
+              any |= bad[k][c];
+            }
+          if (__any_sync(0xffffffffu, any != 0u)) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int c = 0; c < kWords; ++c) vw[k][c] &= ~((bad[k][c] >> 7) * 255u);
+            // which of the dims have a NaN that the row sees: a product of ones
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+              uint32_t see[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                see[k] = (tok0 + T[2 * k] < lim[nr] ? 0x3c00u : 0u) |
+                         (tok0 + T[2 * k + 1] < lim[nr] ? 0x3c000000u : 0u);
+#pragma unroll
+              for (int j = 0; j < kTiles; ++j) {
+                uint32_t a[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {  // rows g + 8 (e & 1): dim 2 j + (e & 1); tokens 2 (e >> 1), + 1
+                  const int byte = 2 * j + (e & 1), k = 2 * (e >> 1);
+                  a[e] = ((bad[k][byte / 4] >> (8 * (byte % 4) + 7)) & 1u ? 0x3c00u : 0u) |
+                         ((bad[k + 1][byte / 4] >> (8 * (byte % 4) + 7)) & 1u ? 0x3c000000u : 0u);
+                }
+                float hit[4];
+                mma_f16_zero(hit, a, see[0], see[1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (hit[e] > 0.f) o[nr][j][e] = NAN;
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < kWords; ++c) {
+          const uint32_t ab0 = prmt<0x5140u>(vw[0][c], vw[1][c]), ab1 = prmt<0x7362u>(vw[0][c], vw[1][c]);
+          const uint32_t cd0 = prmt<0x5140u>(vw[2][c], vw[3][c]), cd1 = prmt<0x7362u>(vw[2][c], vw[3][c]);
+          const uint32_t a0[4] = {f8_half2(ab0), f8_half2(ab0 >> 16), f8_half2(cd0), f8_half2(cd0 >> 16)};
+          const uint32_t a1[4] = {f8_half2(ab1), f8_half2(ab1 >> 16), f8_half2(cd1), f8_half2(cd1 >> 16)};
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) {
+            float x[4];
+            mma_f16_zero(x, a0, pb[nr][0], pb[nr][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nr][2 * c][e] = fmaf(x[e], vs, o[nr][2 * c][e]);
+            mma_f16_zero(x, a1, pb[nr][0], pb[nr][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nr][2 * c + 1][e] = fmaf(x[e], vs, o[nr][2 * c + 1][e]);
+          }
+        }
+      }
+      __syncwarp();
+      if (++s == kStages) s = 0, ph ^= 1u;
+      issue();  // into the stage that was just read
+    }
+    if (!ok) break;
+
+    // ---- the segment's end: rows 2t and 2t + 1 of each group are this lane's, their states
+    // rows g's
+    const bool whole = blk0 == 0 && count == nblk;
+    const int64_t slot = 2 * static_cast<int64_t>(me) + (seg > 0 ? 1 : 0);
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+      float l = l_part[nr];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float lse2 = l == 0.f ? -INFINITY : m_run[nr] + __log2f(l);
+      const int r = 8 * nr + g;
+      if (t == 0 && r < R) {
+        if (!whole)
+          p.part_lse[slot * kRows + r] = lse2;
+        else if (p.lse != nullptr)
+          p.lse[(static_cast<int64_t>(b) * p.Hq + gkv * p.G + r % p.G) * p.T + r / p.G] = lse2 * 0.6931471805599453f;
+      }
+#pragma unroll
+      for (int hc = 0; hc < 2; ++hc) {
+        const float f = __shfl_sync(0xffffffffu, inv, 8 * t + 4 * hc);
+        const int rr = 8 * nr + 2 * t + hc;
+        float x[2 * kTiles];
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+          // (a row that sees nothing has weights of zero, but may have met a NaN)
+          x[2 * j] = f == 0.f ? 0.f : o[nr][j][hc] * f;
+          x[2 * j + 1] = f == 0.f ? 0.f : o[nr][j][2 + hc] * f;
+        }
+        if (rr >= R) continue;
+        if (whole)
+          write_dims(p.out, p.out_bf16,
+                     b * p.out_stride[0] + (gkv * p.G + rr % p.G) * p.out_stride[1] + rr / p.G * p.out_stride[2] +
+                         (D / 8) * g,
+                     x);
+        else
+          write_dims(p.part_o, 0, (slot * kRows + rr) * D + (D / 8) * g, x);
+      }
+    }
+    if (blk == nblk) {  // the next item
+      blk = 0;
+      if (++grp == Hgr) {
+        grp = 0;
+        int n_blocks;
+        if (left > 0) b = next_seq(p, lane, b, n_blocks);
+      }
+    }
   }
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  for (int r = warp; r < R; r += kWarps) {
-    const int64_t first = unit * p.n_split * kRows + r;
-    float M = -INFINITY;
-    bool any = false;
-    for (int k = lane; k < ns; k += 32) {
-      const float l = __ldcg(p.part_lse + first + static_cast<int64_t>(k) * kRows);
+  // after a wait that gave up: let the copies in flight land
+  for (; left > ileft; --left) {
+    drain_wait(&wbar[s], ph);
+    if (++s == kStages) s = 0, ph ^= 1u;
+  }
+}
+
+// Joins the pieces of the items that are cut between warps, and writes those that have no
+// blocks.  An item's rows go to as many CTAs as fill the GPU, a CTA's warps share them.
+constexpr int kMergeWarps = 16;
+template <int D, int NR>
+__global__ void __launch_bounds__(kMergeWarps * 32) f8_mma_merge_kernel(const __grid_constant__ F8MmaParams p) {
+  constexpr int kRows = 8 * NR, E = D / 32;
+  __shared__ float acc_of[kMergeWarps][D], sum_of[kMergeWarps];
+  let_next_launch_in();
+  wait_for_launch_ahead();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.x / p.Hkv, gkv = blockIdx.x - b * p.Hkv;
+  const int R = p.T * p.G;
+  const int rows = (R + gridDim.y - 1) / gridDim.y;  // of this CTA, `per` warps each
+  const int per = kMergeWarps / rows;
+  auto blocks_of = [&](int x) {
+    int start, n;
+    bool past;
+    return seq_blocks(p, x, start, n, past);
+  };
+  const int nblk = blocks_of(b);
+  int w0 = 0, w1 = 0, head = 0;  // the pieces' runs; whether the first is its run's first segment
+  if (nblk > 0) {
+    int64_t before = 0, all = 0;
+    for (int x = lane; x < p.B; x += 32) {
+      const int k = blocks_of(x);
+      all += k;
+      if (x < b) before += k;
+    }
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) {
+      before += __shfl_xor_sync(0xffffffffu, before, m);
+      all += __shfl_xor_sync(0xffffffffu, all, m);
+    }
+    const int Hgr = p.Hkv / p.side;
+    const Runs64 runs = runs_of(all * Hgr, p.warps / p.side);
+    const int64_t u0 = before * Hgr + static_cast<int64_t>(gkv / p.side) * nblk;
+    w0 = runs.of(u0);
+    w1 = runs.of(u0 + nblk - 1);
+    head = runs.lo(w0) == u0;
+    if (w0 == w1) return;  // written where it was computed
+  }
+  const int part = warp / per, sub = warp - part * per, row = blockIdx.y * rows + part;
+  const bool on = part < rows && row < R;
+  auto piece = [&](int c) {
+    return 2 * (static_cast<int64_t>(c) * p.side + gkv % p.side) + (c == w0 && !head ? 1 : 0);
+  };
+  float M = -INFINITY, ws = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  bool any = false;
+  if (on && nblk > 0) {
+    for (int c = w0 + lane; c <= w1; c += 32) {
+      const float l = p.part_lse[piece(c) * kRows + row];
+      any |= l != -INFINITY;  // a NaN counts as something: it has to reach the row
       M = fmaxf(M, l);
-      any |= l != -INFINITY;
     }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
     any = __any_sync(0xffffffffu, any);
-    const int h = gkv * p.G + r % p.G, i = r / p.G;
-    if (!any) {
-      write_empty(r);
-      continue;
-    }
-    float2 acc[D / 64];
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) acc[c] = make_float2(0.f, 0.f);
-    float ws = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < ns; ++k) {
-      const int64_t at = first + static_cast<int64_t>(k) * kRows;
-      const float l = __ldcg(p.part_lse + at);
+#pragma unroll 8
+    for (int c = w0 + sub; c <= w1; c += per) {
+      const int64_t at = piece(c) * kRows + row;
+      const float l = p.part_lse[at];
       const float w = l == -INFINITY ? 0.f : fast_exp2(l - M);
       ws += w;
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(p.part_o + at * D + 2 * lane + 64 * c));
-        acc[c].x = fmaf(w, x.x, acc[c].x);
-        acc[c].y = fmaf(w, x.y, acc[c].y);
+      const float* o = p.part_o + at * D + lane * E;
+      float x[E];
+      if constexpr (E == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(o);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(o);
+        x[0] = v.x, x[1] = v.y;
       }
-    }
-    const float inv = 1.f / ws;
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) write_row<D>(p, b, h, i, 2 * lane + 64 * c, acc[c].x * inv, acc[c].y * inv);
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.T + i] = (M + __log2f(ws)) * 0.6931471805599453f;
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[e], acc[e]);
+    }
   }
+  if (per > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc_of[warp][lane * E + e] = acc[e];
+    if (lane == 0) sum_of[warp] = ws;
+    __syncthreads();
+    if (sub != 0) return;
+    for (int k = 1; k < per && on; ++k) {
+      ws += sum_of[warp + k];
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += acc_of[warp + k][lane * E + e];
+    }
+  }
+  if (!on) return;
+  const int h = gkv * p.G + row % p.G, i = row / p.G;
+  const float inv = any ? 1.f / ws : 0.f;
+  const int64_t at = b * p.out_stride[0] + h * p.out_stride[1] + i * p.out_stride[2] + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const float x = any ? acc[e] * inv : 0.f, y = any ? acc[e + 1] * inv : 0.f;
+    if (p.out_bf16)
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at + e) = pack_bf16x2(x, y);
+    else
+      *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at + e) = make_float2(x, y);
+  }
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.T + i] =
+        any ? (M + __log2f(ws)) * 0.6931471805599453f : -INFINITY;
 }
 
-constexpr int64_t kMostRows = 16;  // of a KV head; more go to chunk_f8_tc.cu
+// Rows of a KV head; more go to chunk_f8_tc.cu, whose tile has 128.  Both sides with 16 rows
+// (D = 128, 8 KV heads): 64 sequences of 8192 tokens 232 us here and 382 there, 64 of
+// 4096 130 and 205, one of 20000 29 and 39, one of 500 15 and 21.
+constexpr int64_t kMostRows = 16;
 int rows_of(int64_t rows) { return rows <= 8 ? 8 : 16; }
-// tokens of a split
-int split_tokens(int64_t units, int64_t max_blocks, int n_cta) {
-  // half a split as long as the GPU has room for the CTAs, down to a block a warp
-  int tokens = 1024;
-  while (tokens > kWarps * kBS && units * ((max_blocks * kBS + tokens - 1) / tokens) < 4 * n_cta) tokens /= 2;
-  return tokens;
+int warps_of(int64_t rows, int D, int n_cta) {  // three CTAs an SM where registers allow, else two
+  const int ctas = rows > 8 ? (D == 64 ? MmaCfg<64, 2>::kCtas : MmaCfg<128, 2>::kCtas) : MmaCfg<128, 1>::kCtas;
+  static_assert(MmaCfg<64, 1>::kCtas == MmaCfg<128, 1>::kCtas, "");
+  return n_cta * kWarps * ctas;
 }
-
+// offsets and size of the workspace
 struct Layout {
-  int64_t units, n_split;
-  int tokens;
-  size_t o, lse, count, bytes;  // offsets and size of the workspace
+  size_t lse, bytes;
 };
-Layout layout(int64_t B, int64_t Hq, int64_t Hkv, int64_t T, int64_t max_blocks, int D, int n_cta) {
+Layout layout(int64_t rows, int D, int n_cta) {
+  const size_t n = static_cast<size_t>(2) * warps_of(rows, D, n_cta) * rows_of(rows);
   Layout l;
-  l.units = B * Hkv;
-  l.tokens = split_tokens(l.units, max_blocks, n_cta);
-  l.n_split = std::max<int64_t>(1, (max_blocks * kBS + l.tokens - 1) / l.tokens);
-  const size_t rows = static_cast<size_t>(l.units) * l.n_split * rows_of(T * (Hq / Hkv));
-  l.o = 0;
-  l.lse = rows * D * 4;
-  l.count = (l.lse + rows * 4 + 255) & ~size_t(255);
-  l.bytes = (l.count + l.units * 8 + 255) & ~size_t(255);
+  l.lse = n * D * 4;
+  l.bytes = (l.lse + n * 4 + 255) & ~size_t(255);
   return l;
 }
 
 template <int D, int NR>
-cudaError_t launch_mma(const F8AttnArgs& a, F8MmaParams& p, const Layout& l, cudaStream_t stream) {
+cudaError_t launch_mma(const F8AttnArgs& a, F8MmaParams& p, cudaStream_t stream) {
   if (D == 128 && (!make_code_cache_map(&p.kmap, a.cache.k, a.cache.num_blocks, a.cache.Hkv) ||
                    !make_code_cache_map(&p.vmap, a.cache.v, a.cache.num_blocks, a.cache.Hkv)))
     return cudaErrorInvalidValue;
   auto kern = paged_attn_f8_mma_kernel<D, NR>;
-  constexpr int smem = 1024 + kWarps * kStages * (2 * kBS * D + 8);
+  constexpr int smem = MmaCfg<D, NR>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(l.n_split), static_cast<unsigned>(a.cache.Hkv),
-                  static_cast<unsigned>(a.B));
-  return launch_early(kern, grid, kWarps * 32, smem, stream, p);
+  // no more CTAs than the call could have runs for
+  const int64_t runs = (a.B * (a.cache.Hkv / p.side) * static_cast<int64_t>(a.max_blocks) + kLeast - 1) / kLeast;
+  const int64_t most = (runs * p.side + kWarps - 1) / kWarps;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(p.warps / kWarps, most)));
+  e = launch_early(kern, grid, kWarps * 32, smem, stream, p);
+  if (e != cudaSuccess) return e;
+  const int64_t items = a.B * a.cache.Hkv;
+  // (one sequence of 20000 tokens and 16 rows: 29 us, 50 with a CTA an item; rows on more CTAs
+  // than that cost 64 sequences 4 us)
+  const int64_t shares = std::min<int64_t>(a.T * p.G, std::max<int64_t>(1, 2 * a.n_cta / items));
+  const dim3 join(static_cast<unsigned>(items), static_cast<unsigned>(shares));
+  return launch_early(f8_mma_merge_kernel<D, NR>, join, kMergeWarps * 32, 0, stream, p);
 }
 
 }  // namespace
 
 size_t f8_attn_partial_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t T, int64_t max_blocks, int D, int n_cta) {
   const int64_t G = Hq / Hkv;
-  return T * G > kMostRows ? f8_chunk_partial_bytes(T, G, D, n_cta) : layout(B, Hq, Hkv, T, max_blocks, D, n_cta).bytes;
+  return T * G > kMostRows ? f8_chunk_partial_bytes(T, G, D, n_cta) : layout(T * G, D, n_cta).bytes;
 }
 
 bool f8_attn_fits(int64_t B, int64_t Hq, int64_t Hkv, int64_t T, int64_t max_blocks) {
@@ -610,7 +773,7 @@ cudaError_t launch_paged_attn_f8(const F8AttnArgs& a, cudaStream_t stream) {
   const int G = static_cast<int>(a.Hq / a.cache.Hkv);
   if (a.T * G > kMostRows) return launch_chunk_f8(a, stream);
   F8MmaParams p = {};
-  const Layout l = layout(a.B, a.Hq, a.cache.Hkv, a.T, a.max_blocks, a.cache.D, a.n_cta);
+  const Layout l = layout(a.T * G, a.cache.D, a.n_cta);
   p.kq = a.cache.k;
   p.vq = a.cache.v;
   p.ks = a.cache.k_scale;
@@ -629,20 +792,20 @@ cudaError_t launch_paged_attn_f8(const F8AttnArgs& a, cudaStream_t stream) {
   p.lens = a.lens;
   p.causal = a.causal;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
-  p.split_tokens = l.tokens;
-  p.n_split = static_cast<int>(l.n_split);
+  p.B = static_cast<int>(a.B);
+  p.warps = warps_of(a.T * G, a.cache.D, a.n_cta);
+  p.side = 1;
+  while (p.side < kSide && p.Hkv % (2 * p.side) == 0) p.side *= 2;
   p.out = a.out.data;
   p.out_bf16 = a.out.dtype == ATTN_BF16;
   p.lse = a.lse;
   uint8_t* ws = static_cast<uint8_t*>(a.partials);
-  p.part_o = reinterpret_cast<float*>(ws + l.o);
+  p.part_o = reinterpret_cast<float*>(ws);
   p.part_lse = reinterpret_cast<float*>(ws + l.lse);
-  p.count = reinterpret_cast<unsigned long long*>(ws + l.count);
-  p.gen = a.gen;
   p.status = a.status;
   if (a.cache.D == 64)
-    return rows_of(a.T * G) == 8 ? launch_mma<64, 1>(a, p, l, stream) : launch_mma<64, 2>(a, p, l, stream);
-  return rows_of(a.T * G) == 8 ? launch_mma<128, 1>(a, p, l, stream) : launch_mma<128, 2>(a, p, l, stream);
+    return rows_of(a.T * G) == 8 ? launch_mma<64, 1>(a, p, stream) : launch_mma<64, 2>(a, p, stream);
+  return rows_of(a.T * G) == 8 ? launch_mma<128, 1>(a, p, stream) : launch_mma<128, 2>(a, p, stream);
 }
 
 }  // namespace attn

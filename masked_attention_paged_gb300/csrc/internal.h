@@ -358,7 +358,6 @@ struct F8AttnArgs {
   float* lse;      // [B, Hq, T] or null
   void* partials;  // workspace after the status block
   int n_cta;       // SMs of the device
-  uint32_t gen;    // this call's generation, tags its counts
   uint32_t* status;
 };
 // workspace past the status block
