@@ -47,7 +47,10 @@ constexpr int kBS = 16;
 constexpr float kRescaleMargin = 8.0f;
 constexpr int kBarBytes = 4096;
 constexpr int kSegs = 4;      // segments the planner is ahead
-constexpr int kItemCost = 3;  // what an item costs a CTA besides its tiles, in tiles
+// What an item costs a CTA besides its tiles, in tiles: the split of q, the products of the first
+// tile, the epilogue.  Two chunks of 1024 behind 8192 tokens: 199 us with 5, 6, 8 and 10, 203 with
+// 3, 205 with none; two of 64: 39, 45, 50; one of 2048 behind 10 tokens: 75, 81, 90 (2).
+constexpr int kItemCost = 6;
 constexpr int kScales = 8;    // tiles whose key scales are held: more than K's stages and the scores ahead of P
 constexpr int kNotes = 8;     // segments whose notes of NaNs are held: more than the planner is ahead
 constexpr int kSpread = 256;  // most queries of a row group: tokens that not all of its rows see
