@@ -28,6 +28,7 @@
 // NaN, too: such codes go in as zeros, and the epilogue gives them to the rows that
 // see them.
 #include <cuda.h>
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -415,13 +416,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   if (warp < 8) regs_dec<C::kRegsCtl>();
   if (warp == 0) {
     // ------------------------------------------------------------ K and V codes
-    // lane i < 8 owns K's block i of a tile, lane 8 + i V's: its id is read a tile
-    // ahead, its scale with it
-    const bool is_v = lane >= kTileBlocks;
-    const int own = lane % kTileBlocks;
-    const bool works = lane < 2 * kTileBlocks;
-    const void* map = is_v ? static_cast<const void*>(&tm_v) : &tm_k;
-    const float* scales = is_v ? p.vs : p.ks;
+    // Four tiles' blocks are looked up at a time, a lane each: ids a window ahead, scales
+    // three tiles ahead, so that no tile waits for either.
+    constexpr int kWindow = 32 / kTileBlocks;
+    const int own = lane % kTileBlocks, wt = lane / kTileBlocks;  // the block of a tile, the tile of a window
     Seg s;
     int j = 0, k_issued = 0, c_issued = 0;
     bool ok = true;
@@ -429,28 +427,36 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       seg_taken(i);
       const int32_t* bt_row = p.bt + static_cast<int64_t>(s.b) * p.bt_stride;
       const int blocks = (s.kend + kBS - 1) / kBS;
-      float sc_next;
-      auto block_id = [&](int tile) {
-        const int blk = tile * kTileBlocks + own;
-        int id = -1;
-        sc_next = -1.0f;
-        if (tile < s.t1 && works && blk < blocks) {
-          id = bt_row[blk];
-          if (id < 0 || id >= p.num_blocks) {
-            report(p.status, kStatusBounds);
-            id = -1;
-          } else {
-            sc_next = scales[static_cast<int64_t>(id) * p.Hkv + s.g];
-          }
+      auto block_id = [&](int tile0) {  // of the window that starts there; -1 past the segment
+        const int tile = tile0 + wt, blk = tile * kTileBlocks + own;
+        return tile < s.t1 && blk < blocks ? bt_row[blk] : INT_MIN;
+      };
+      float sck = -1.0f, scv = -1.0f;
+      auto look = [&](int& id) {  // the id, checked, and its scales
+        sck = scv = -1.0f;
+        if (id >= 0 && id < p.num_blocks) {
+          const int64_t at = static_cast<int64_t>(id) * p.Hkv + s.g;
+          sck = p.ks[at];
+          scv = p.vs[at];
+        } else {
+          if (id != INT_MIN) report(p.status, kStatusBounds);
+          id = -1;
         }
-        return id;
       };
       int id_next = block_id(s.t0);
+      look(id_next);
+      int id = -1;
+      float ks_id = -1.0f, vs_id = -1.0f;
       for (int tile = s.t0; tile < s.t1; ++tile, ++j) {
-        const int id = id_next;
-        const float sc = sc_next;
-        id_next = block_id(tile + 1);
-        const uint32_t there = __ballot_sync(0xffffffffu, id >= 0) & 0xffu;  // (V's blocks are K's)
+        const int w = (tile - s.t0) % kWindow;
+        if (w == 0) {
+          id = id_next, ks_id = sck, vs_id = scv;
+          id_next = block_id(tile + kWindow);
+        } else if (w == 1) {
+          look(id_next);
+        }
+        const bool owns = wt == w;
+        const uint32_t there = (__ballot_sync(0xffffffffu, id >= 0) >> (w * kTileBlocks)) & 0xffu;
         const uint32_t bytes = __popc(there) * (kBS * D);
         const int ks = j % C::KS, cs = j % C::VC;
         if (!wait_all(&bars->k_empty[ks], (j / C::KS) ^ 1)) {
@@ -458,7 +464,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           break;
         }
         // (the tile that had this slot is kScales back: its weights are written)
-        if (lane < kTileBlocks) bars->ks[j % kScales][lane] = sc;
+        if (owns) bars->ks[j % kScales][own] = ks_id;
         if (lane == 0) bars->there[j % kScales] = there;
         __syncwarp();
         if (lane == 0) {
@@ -466,19 +472,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           mbar_arrive_expect_tx(&bars->k_full[ks], bytes);
         }
         __syncwarp();
-        if (!is_v && id >= 0)
-          tma_load_4d(smem + C::kOffK + ks * C::kCodeBytes + own * (kBS * D), map, &bars->k_full[ks], 0, 0, s.g, id);
+        if (owns && id >= 0)
+          tma_load_4d(smem + C::kOffK + ks * C::kCodeBytes + own * (kBS * D), &tm_k, &bars->k_full[ks], 0, 0, s.g, id);
         k_issued = j + 1;
         if (!wait_all(&bars->c_empty[cs], (j / C::VC) ^ 1)) {
           ok = false;
           break;
         }
-        if (is_v && works) bars->vs[cs][own] = sc;
+        if (owns) bars->vs[cs][own] = vs_id;
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&bars->c_full[cs], bytes);
         __syncwarp();
-        if (is_v && id >= 0)
-          tma_load_4d(smem + C::kOffC + cs * C::kCodeBytes + own * (kBS * D), map, &bars->c_full[cs], 0, 0, s.g, id);
+        if (owns && id >= 0)
+          tma_load_4d(smem + C::kOffC + cs * C::kCodeBytes + own * (kBS * D), &tm_v, &bars->c_full[cs], 0, 0, s.g, id);
         c_issued = j + 1;
       }
     }
