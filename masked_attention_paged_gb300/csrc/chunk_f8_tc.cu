@@ -23,6 +23,16 @@
 // score buffer, an accumulator and a running max and sum of its own, joined by the LSE
 // rule when an item ends.
 //
+// What bounds it: 2 x 1024 tokens behind 8192 (32 heads over 8, D = 128) take 199 us where the
+// products alone would take 118.  A tile takes 3100 cycles a CTA: 2 x 1040 of products, which
+// also read shared memory at 128 bytes a cycle, all that it gives (8 KB a step of 65 cycles), so
+// that the TMA's and the converters' bytes come on top; and two waits of the issuer, 230
+// each.  An item's start and end cost some 12000 cycles.  With one row tile the converters
+// set the pace, 3000 cycles a tile (16 x 16 tokens behind 8192: 98 us; 76 with weights in one pass and
+// no conversion at all).
+// Two issuers, one a row tile, took 261 us (both products end late), in strict turns 224;
+// 64-key tiles 292; the converting loop unrolled twice 214, and rolled to one vector a step 231.
+//
 // Slots past the last key may hold NaN codes: their V rows go in as zeros (P is 0
 // there, but 0 x NaN is not).  A token that some rows see and others do not may be
 // NaN, too: such codes go in as zeros, and the epilogue gives them to the rows that
@@ -1166,6 +1176,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 }
 
 int tile_queries(int64_t T, int64_t G) { return static_cast<int>(std::min(T, kBM / G)); }
+// One row tile where it holds all rows (16 x 16 tokens of 4 heads behind 8192: 98 us, with two tiles
+// 102; 16 x 32 behind 4000: 61, 70), else two (2 x 1024 behind 8192 199 us, 360 with one at a
+// time; 2 x 40 36.5, 39.6).
 int chunk_nt(int64_t T, int64_t G) { return T <= kBM / G ? 1 : 2; }
 size_t part_rows(int64_t T, int64_t G, int n_cta) { return static_cast<size_t>(2) * n_cta * chunk_nt(T, G) * kBM; }
 size_t part_bytes(int64_t T, int64_t G, int D, int n_cta) {

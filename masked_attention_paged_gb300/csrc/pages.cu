@@ -5,6 +5,12 @@
 // prefix sum over the rows, and one over the free blocks); the bytes are then moved by
 // as many CTAs as fill the GPU.  Deciding is latency: a pool of 16384 blocks is one
 // pass of 16 loads a thread.
+//
+// Measured: 4100 blocks (4.3 GB read and written) moved to the front of a pool of 16384 in 680
+// us, 93 % of what a copy does.  A step of a search, 64 rows given back, forked anew from 16
+// prompts in eight layers and reserved for, takes 20 us, of which the bytes (8.4 MB read,
+// 33.6 written) are 6: four launches and their decisions, each a chain of loads by one CTA.
+// One prompt and four rows take 11 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -18,7 +24,9 @@ constexpr int kThreads = 1024;  // of the deciding CTA
 constexpr int kWarps = kThreads / 32;
 constexpr int kPerLane = 16;    // counts a lane looks at in a pass
 constexpr int kPass = kThreads * kPerLane;
-constexpr int kPiece = 16384;   // bytes a CTA moves in a step
+// Bytes a CTA moves in a step: 4100 blocks of 16 x 32 KB take 680 us (8 KB: 707, 32 KB: 902), the
+// step of 64 rows above 20.1 (21.3, 28.2).
+constexpr int kPiece = 16384;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveVecs = kPiece / 16 / kMoveThreads;
 
@@ -604,7 +612,7 @@ cudaError_t launch_kv_fork(const PoolArgs& a, const int32_t* src, int32_t* child
   p.copies = static_cast<int2*>(a.scratch);
   p.list = reinterpret_cast<int32_t*>(p.copies + children);
   p.status = a.status;
-  if (a.n_tensors <= 8) return fork<8>(a, p, stream);
+  // (a launch copies its arguments: room for 256 tensors is 0.3 us more of a small step's 11)
   return a.n_tensors <= 64 ? fork<64>(a, p, stream) : fork<kPoolMaxTensors>(a, p, stream);
 }
 
@@ -622,7 +630,6 @@ cudaError_t launch_kv_compact(const PoolArgs& a, int32_t* used, cudaStream_t str
   p.to = p.from + a.num_blocks;
   p.rank = p.to + a.num_blocks;
   p.status = a.status;
-  if (a.n_tensors <= 8) return compact<8>(a, p, stream);
   return a.n_tensors <= 64 ? compact<64>(a, p, stream) : compact<kPoolMaxTensors>(a, p, stream);
 }
 
