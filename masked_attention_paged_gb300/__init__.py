@@ -236,10 +236,11 @@ _marshal_tried = False
 _entries: dict = {}  # C entry points' addresses
 
 
-def _call(name: str, fmt: str, *args) -> bool:
+def _call(name: str, fmt: str, *args):
     """The C entry point, its arguments checked and converted in one step; False
     (and nothing called) where they are not plainly as documented: the caller
-    then takes them one by one, with every check worded."""
+    then takes them one by one, with every check worded.  Otherwise True, or
+    the results that were asked for by None (or True) in their places."""
     global _marshal, _marshal_tried
     if not _marshal_tried:
         _marshal_tried = True
@@ -258,9 +259,19 @@ def _call(name: str, fmt: str, *args) -> bool:
     st = _marshal.call(entry, name, fmt, *args)
     if st is None:
         return False
+    if type(st) is tuple:  # with the results that the step made
+        return st[1:]
     if st != 0:
         raise LibAttnError(name, st)
     return True
+
+
+def _results(made, *given):
+    """The given tensors, those that are None out of what _call made, in order."""
+    if made is True:
+        return given
+    made = iter(made)
+    return tuple(next(made) if x is None else x for x in given)
 
 
 def _handle(stream):
@@ -1199,6 +1210,11 @@ def draft_verify(target_probs: torch.Tensor, tokens: torch.Tensor, parents: torc
     lib = load()
     if not (isinstance(target_probs, torch.Tensor) and target_probs.dim() == 3):
         raise ValueError("target_probs must be float32 or bfloat16 [B, T, V]")
+    if stream is None and workspace is not None and target_probs.is_cuda:
+        got = _call("draft_verify", "pPqqu=kiiWS", target_probs, draft_probs, tokens, parents, uniforms,
+                    int(bool(replacement)), path, n_accept, next_token, workspace.tensor, None)
+        if got:
+            return _results(got, path, n_accept, next_token)
     B, T, V = target_probs.shape
     dev = target_probs.device
     if path is None:
@@ -1209,7 +1225,7 @@ def draft_verify(target_probs: torch.Tensor, tokens: torch.Tensor, parents: torc
         next_token = _fresh(lambda: torch.empty(B, dtype=torch.int32, device=dev), stream, dev)
     if dev.type == "cuda":
         ws = workspace or _small_ws(dev, stream)
-        if _call("draft_verify", "pPqqu=kvvWS", target_probs, draft_probs, tokens, parents, uniforms,
+        if _call("draft_verify", "pPqqu=kiiWS", target_probs, draft_probs, tokens, parents, uniforms,
                  int(bool(replacement)), path, n_accept, next_token, ws.tensor, _handle(stream)):
             return path, n_accept, next_token
     _check_probs(target_probs, "target_probs")
@@ -1360,6 +1376,11 @@ def kv_compact(caches: Sequence[torch.Tensor], refs: torch.Tensor, block_table: 
     lib = load()
     if not isinstance(refs, torch.Tensor):
         raise ValueError("refs must be contiguous int32 [num_blocks]")
+    if stream is None and workspace is not None and refs.is_cuda:
+        got = _call("kv_compact", "LZt=UWS", caches, refs, block_table, block_table.shape[0], used, workspace.tensor,
+                    None)
+        if got:
+            return _results(got, used)[0]
     if used is None:
         used = _fresh(lambda: torch.empty(1, dtype=torch.int32, device=refs.device), stream, refs.device)
     if workspace is not None and refs.is_cuda:
@@ -1456,6 +1477,15 @@ def paged_attn_f8(q: torch.Tensor, kq_cache: torch.Tensor, vq_cache: torch.Tenso
     T = q.shape[2] if full else 1
     if scale is None:
         scale = 1.0 / math.sqrt(D)
+    if stream is None and workspace is not None and q.is_cuda:
+        makes_lse = lse is None and return_lse
+        got = _call("paged_attn_f8", "yebvn==OlWS", q, kq_cache, vq_cache, k_scale, v_scale, block_table, start_pos,
+                    lens, int(bool(causal)), float(scale), out, True if makes_lse else lse, workspace.tensor, None)
+        if got:
+            if not makes_lse:
+                out, = _results(got, out)
+                return (out, lse) if return_lse else out
+            return _results(got, out, None)
     if out is None:
         out = _fresh(lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device), stream, q.device)
     elif out.shape != q.shape:

@@ -6,7 +6,9 @@
 // name, format, ...) does that for a whole call on the current device and returns
 // the entry's status, or None (and calls nothing) when anything is not plainly as the format
 // says; the Python code then goes through its own checks, which word the refusal
-// (or take the rarer form).  Nothing is kept between calls.
+// (or take the rarer form).  Results that the caller has no tensor for are made here, of the
+// current stream's memory, and returned behind the status, (status, result, ...).  Nothing is
+// kept between calls.
 //
 // Format letters (sizes B, H, T, D are those of the first x / y):
 //   x  tensor, bf16 or f32, 4-D          -> attn_tensor
@@ -22,23 +24,25 @@
 //   r  int32 [B, n] rows                 -> pointer, row stride, n
 //   q  int32 [B, T] rows                 -> pointer, row stride
 //   f  int64 frequencies, 1 .. D / 2     -> pointer, twice their number
-//   l  f32, contiguous, B H T elements, or None -> pointer or null
+//   l  f32, contiguous, B H T elements, or None -> pointer or null; True: a result of y's rows
 //   A  f32 [blocks, Hkv, 16] of the cache -> pointer
 //   K  int32, contiguous [B, Hkv, n]     -> pointer
-//   O  as Y, of any type                -> attn_tensor
+//   O  as Y, of any type, or None: a result like y, contiguous -> attn_tensor
 //   p  tensor, bf16 or f32, 3-D          -> attn_tensor; B, T and D are its sizes
 //   P  as p, of its sizes and type, or None -> attn_tensor or null
 //   u  f32 [B, T] rows                   -> pointer, row stride
-//   k  int32, contiguous [B, T]          -> pointer
+//   k  int32, contiguous [B, T], or None: a result -> pointer
+//   i  int32 vector of B, or None: a result -> pointer
 //   e  four tensors: an e4m3 cache and its scales -> attn_kv_cache_f8
 //   L  a list of tensors with as many blocks as Z says -> their number, attn_pool_tensor[]
 //   Z  int32 vector of a pool's blocks   -> pointer, their number
 //   t  table, rows apart, that sets B or has B rows -> pointer, row stride, columns
-//   U  int32, one element                -> pointer
+//   U  int32, one element, or None: a result -> pointer
 //   W  a workspace's bytes               -> pointer, their number
 //   S  a stream handle, or None          -> itself, or the current stream
 //   =  an int or a float                 -> itself
 #include <Python.h>
+#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -137,6 +141,9 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   int n = 0, n_tensors = 0;
   Py_ssize_t a = 3;
   Sizes s;
+  constexpr int kMostMade = 4;
+  at::Tensor made[kMostMade];
+  int n_made = 0;
   bool ok = true, error = false;
   auto put = [&](int64_t i) {
     if (n == kMost)
@@ -159,6 +166,28 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
       }
       if (o == Py_None && (*f == 'o' || *f == 'n' || *f == 'l' || *f == 'P')) {
         put(0);
+        continue;
+      }
+      const bool makes = (o == Py_None && (*f == 'k' || *f == 'i' || *f == 'U' || *f == 'O')) ||
+                         (o == Py_True && *f == 'l');
+      if (makes) {
+        if (n_made == kMostMade || n_tensors == 8 || (*f != 'U' && s.B < 0)) {
+          ok = false;
+          break;
+        }
+        const int64_t sizes[4] = {s.B, *f == 'k' ? s.T : s.H, s.one_token ? s.D : s.T, s.D};
+        const int64_t one = 1;
+        const int dims = *f == 'k' ? 2 : (*f == 'i' || *f == 'U' ? 1 : (*f == 'l' ? 3 : 4) - (s.one_token ? 1 : 0));
+        const at::ScalarType type = *f == 'O' ? s.type : (*f == 'l' ? at::kFloat : at::kInt);
+        at::Tensor& x = made[n_made++];
+        x = at::empty(*f == 'U' ? at::IntArrayRef(&one, 1) : at::IntArrayRef(sizes, dims),
+                      at::TensorOptions().dtype(type).device(at::kCUDA, static_cast<c10::DeviceIndex>(device)));
+        if (*f == 'O') {
+          ok = describe(x, device, s.one_token, &tensors[n_tensors]);
+          put(address(&tensors[n_tensors++]));
+        } else {
+          put(address(x.data_ptr()));
+        }
         continue;
       }
       if (*f == '=' || *f == 'S') {
@@ -340,6 +369,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
           break;
         case 'V':
         case 'v':
+        case 'i':
         case 'n':
           ok = on(t, device) && t.scalar_type() == at::kInt && t.dim() == 1 && t.is_contiguous() &&
                (*f == 'V' || t.size(0) == s.B);
@@ -444,7 +474,12 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     st = invoke(&paged_attn_f8, entry, out, count);
   Py_END_ALLOW_THREADS;
   if (st < 0) return PyErr_Format(PyExc_ValueError, "call: %s with %d arguments", name, n);
-  return PyLong_FromLong(st);
+  if (n_made == 0 || st != 0) return PyLong_FromLong(st);
+  PyObject* all = PyTuple_New(1 + n_made);
+  if (all == nullptr) return nullptr;
+  PyTuple_SET_ITEM(all, 0, PyLong_FromLong(st));
+  for (int i = 0; i < n_made; ++i) PyTuple_SET_ITEM(all, 1 + i, THPVariable_Wrap(made[i]));
+  return all;
 }
 
 PyMethodDef kMethods[] = {
