@@ -404,3 +404,25 @@ def test_it_equals_the_bf16_call_on_the_values(T):
     # both round weights (bf16 there) and outputs: |v| <= 8
     assert (got.float() - want.float()).abs().max() <= 8 * 2.0 ** -8 + 2 * want.float().abs().max() * 2.0 ** -8
     assert (lse - want_lse).abs().max() <= 1e-4
+
+
+@pytest.mark.parametrize("T,Hkv,G,D", [(1, 1, 2, 64), (1, 3, 1, 128), (2, 4, 2, 64), (1, 6, 2, 128), (1, 12, 1, 64),
+                                       (1, 16, 1, 64), (3, 8, 4, 64), (20, 2, 1, 64), (70, 1, 2, 128)])
+def test_many_sequences_most_of_them_idle(T, Hkv, G, D):
+    """More of them than a warp looks at in one step, with long gaps: before, between and behind."""
+    rng = np.random.default_rng(T * Hkv)
+    B, width, N = 175, 8, 90
+    codes, scales = _cache(N, Hkv, D, rng)
+    table = rng.integers(0, N, (B, width)).astype(np.int32)
+    start = rng.integers(0, width * BS - T, B).astype(np.int32)
+    lens = rng.integers(0, T + 1, B).astype(np.int32)
+    start[rng.random(B) < 0.4] = -1
+    start[:35] = -1
+    start[80:150] = -1
+    lens[85:120] = 0
+    lens[-3:] = 0
+    _check(_bf((B, Hkv * G, T, D), rng), codes, scales, table, start, lens=lens)
+    # one sequence at the end of them all
+    start[:-4] = -1
+    start[-4], lens[-4] = 100 - T, T
+    _check(_bf((B, Hkv * G, T, D), rng), codes, scales, table, start, lens=lens)

@@ -234,3 +234,66 @@ def test_two_pools_on_two_streams():
         for x, y in zip(got, want):
             assert torch.equal(x, y)
         assert torch.equal(s.table, alone.table) and torch.equal(s.refs, alone.refs) and s.ws.status() == 0
+
+
+@pytest.mark.parametrize("shape", [(3, 4, 64), (3, 4, 1, 64), (3, 4, 9, 64), (3, 4, 40, 128)])
+def test_results_made_or_given(shape):
+    """The same numbers in tensors of the caller, in those that the call makes, on a stream that is passed, and
+    without a workspace."""
+    rng = np.random.default_rng(len(shape))
+    Bq, Hq, D = shape[0], shape[1], shape[-1]
+    n = shape[2] if len(shape) == 4 else 1
+    s = F8Server(30, Bq, 6, 2, Hq // 2, D)
+    s.lens.copy_(_ints([0, 0, 0]))
+    k, v = (_bf((Bq, 2, 50, D), rng) for _ in range(2))
+    lib.kv_reserve(s.refs, s.table, s.lens, _ints([50] * 3), workspace=s.ws)
+    lib.kv_append_f8(*s.caches(), s.table, s.lens, k, v, workspace=s.ws)
+    start = _ints([50 - n, 3, -1])
+    q = _bf(shape, rng)
+    ws = lib.Workspace(lib.paged_attn_f8_workspace_size(Bq, Hq, 2, n, 6, BS, D))
+    args = (q, *s.caches(), s.table, start)
+    out, lse = torch.empty_like(q), torch.empty(shape[:-1], device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [(lib.paged_attn_f8(*args, out=out, lse=lse, workspace=ws), lse)]
+    got.append(lib.paged_attn_f8(*args, return_lse=True, workspace=ws))
+    got.append((lib.paged_attn_f8(*args, lse=torch.empty_like(lse), workspace=ws), lse))
+    got.append(lib.paged_attn_f8(*args, out=torch.empty_like(q), return_lse=True, workspace=ws))
+    got.append(lib.paged_attn_f8(*args, return_lse=True))
+    got.append((lib.paged_attn_f8(*args, workspace=ws), lse))
+    torch.cuda.synchronize()
+    got.append(lib.paged_attn_f8(*args, return_lse=True, workspace=ws, stream=side))
+    torch.cuda.synchronize()
+    assert got[0][0] is out
+    for o, l in got:
+        assert o.shape == shape and o.dtype == q.dtype and o.is_contiguous() and torch.equal(o, out)
+        assert l.shape == shape[:-1] and l.dtype == torch.float32 and torch.equal(l, lse)
+    f32 = lib.paged_attn_f8(*args, out=torch.empty(shape, device=DEV), workspace=ws)
+    assert f32.dtype == torch.float32 and torch.equal(f32.to(torch.bfloat16), out)
+    for bad in (dict(out=torch.empty(shape[1:], device=DEV)), dict(lse=torch.empty(7, device=DEV)),
+                dict(lens=_ints([1, 1]))):
+        with pytest.raises(ValueError):
+            lib.paged_attn_f8(*args, workspace=ws, **bad)
+
+
+def test_verified_paths_and_used_blocks_made_or_given():
+    d = Drafting()
+    d.draw(np.random.default_rng(1))
+    d.probs.copy_(d.draft)
+    args = (d.probs, d.tokens, d.parents, d.uniforms, d.draft)
+    want = lib.draft_verify(*args, path=d.path, n_accept=d.n, next_token=d.next, workspace=d.ws)
+    assert want[0] is d.path and want[1] is d.n and want[2] is d.next
+    for kw in (dict(workspace=d.ws), dict(), dict(workspace=d.ws, n_accept=_ints([9] * B)),
+               dict(workspace=d.ws, path=_ints(np.zeros((B, T))), next_token=_ints([9] * B)),
+               dict(workspace=d.ws, stream=torch.cuda.current_stream())):
+        got = lib.draft_verify(*args, **kw)
+        for x, y in zip(got, want):
+            assert x.dtype == torch.int32 and x.shape == y.shape and x.is_contiguous() and torch.equal(x, y)
+        for name, x in zip(("path", "n_accept", "next_token"), got):
+            assert kw.get(name, x) is x
+    for bad in (dict(path=_ints(np.zeros((B, T + 1)))), dict(n_accept=_ints([0])), dict(next_token=d.uniforms[:, 0])):
+        with pytest.raises(ValueError):
+            lib.draft_verify(*args, workspace=d.ws, **bad)
+    used = [lib.kv_compact([d.k, d.v], d.refs, d.table, workspace=w, used=u)
+            for w in (d.ws, None) for u in (None, _ints([77]))]
+    assert len({u.item() for u in used}) == 1 and all(u.shape == (1,) and u.dtype == torch.int32 for u in used)
