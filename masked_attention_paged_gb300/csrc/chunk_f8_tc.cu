@@ -23,8 +23,8 @@
 // score buffer, an accumulator and a running max and sum of its own, joined by the LSE
 // rule when an item ends.
 //
-// What bounds it: 2 x 1024 tokens behind 8192 (32 heads over 8, D = 128) take 199 us where the
-// products alone would take 118.  A tile takes 3100 cycles a CTA: 2 x 1040 of products, which
+// What bounds it: 2 x 1024 tokens behind 8192 (32 heads over 8, D = 128) take 200 us where the
+// products alone would take 123.  A tile takes 3100 cycles a CTA: 2 x 1040 of products, which
 // also read shared memory at 128 bytes a cycle, all that it gives (8 KB a step of 65 cycles), so
 // that the TMA's and the converters' bytes come on top; and two waits of the issuer, 230
 // each.  An item's start and end cost some 12000 cycles.  With one row tile the converters
