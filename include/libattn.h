@@ -761,8 +761,9 @@ attn_status kv_reserve(int32_t *refs, int64_t num_blocks, int32_t *block_table, 
  * are left, a new block (refs 1) with a copy of all of the source's partial block,
  * in every tensor.  The rest of its row is -1, child_lens[j] = L.  src[j] < 0, or an
  * idle source: an idle child (length -1, row -1).  A src[j] >= batch, a context past
- * either table, a block id outside the pool, or no free block left: the same, with
- * ATTN_ERR_DEVICE_BOUNDS.  The children's rows are overwritten without being given
+ * either table, a partial block's id outside the pool, or no free block left: the same,
+ * with ATTN_ERR_DEVICE_BOUNDS; a full block's id outside the pool sets it too, and
+ * becomes -1 in the child's row.  The children's rows are overwritten without being given
  * back (kv_free them first).
  *   tensors      n_tensors <= 256 of them (host array)
  *   child_table  int32 [children, child_blocks] (row stride child_stride); overlaps
@@ -847,7 +848,7 @@ attn_status kv_append_f8(const attn_kv_cache_f8 *cache, const int32_t *block_tab
  *              16-byte aligned rows, no stride 0; out must not overlap q)
  *   lse        float32 [batch, Hq, T] contiguous, or NULL
  *   workspace  >= paged_attn_f8_workspace_size(...) bytes on the current device:
- *              partial rows of what is split between SMs, and counts; no clearing
+ *              partial rows of what is cut between SMs; no clearing
  *              between calls.  Calls that share a workspace must not overlap on the
  *              GPU.
  * Hq / Hkv <= 128.  Products on the tensor cores with fp32 accumulation: codes enter

@@ -1475,11 +1475,13 @@ def paged_attn_f8(q: torch.Tensor, kq_cache: torch.Tensor, vq_cache: torch.Tenso
         raise ValueError(f"q must be [B, Hq, T, D] or [B, Hq, D], got {tuple(q.shape)}")
     B, Hq, D = q.shape[0], q.shape[1], q.shape[-1]
     T = q.shape[2] if full else 1
+    if lse is True:  # (which the compiled step takes for a result to make)
+        raise ValueError("lse must be a float32 tensor or None")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if stream is None and workspace is not None and q.is_cuda:
         makes_lse = lse is None and return_lse
-        got = _call("paged_attn_f8", "yebvn==OlWS", q, kq_cache, vq_cache, k_scale, v_scale, block_table, start_pos,
+        got = _call("paged_attn_f8", "yebvn==OEWS", q, kq_cache, vq_cache, k_scale, v_scale, block_table, start_pos,
                     lens, int(bool(causal)), float(scale), out, True if makes_lse else lse, workspace.tensor, None)
         if got:
             if not makes_lse:
@@ -1493,7 +1495,7 @@ def paged_attn_f8(q: torch.Tensor, kq_cache: torch.Tensor, vq_cache: torch.Tenso
     if lse is None and return_lse:
         lse = _fresh(lambda: torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device), stream, q.device)
     if workspace is not None and q.is_cuda:
-        if _call("paged_attn_f8", "yebvn==OlWS", q, kq_cache, vq_cache, k_scale, v_scale, block_table, start_pos, lens,
+        if _call("paged_attn_f8", "yebvn==OEWS", q, kq_cache, vq_cache, k_scale, v_scale, block_table, start_pos, lens,
                  int(bool(causal)), float(scale), out, lse, workspace.tensor, _handle(stream)):
             return (out, lse) if return_lse else out
     if lse is not None:

@@ -766,7 +766,7 @@ size_t f8_attn_partial_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t T, int6
 
 bool f8_attn_fits(int64_t B, int64_t Hq, int64_t Hkv, int64_t T, int64_t max_blocks) {
   const int64_t G = Hq / Hkv;
-  return T * G <= kMostRows || f8_chunk_fits(B, Hkv, T, G, max_blocks);
+  return T * G <= kMostRows ? B * Hkv <= 0x7fffffff : f8_chunk_fits(B, Hkv, T, G, max_blocks);  // (a CTA an item)
 }
 
 cudaError_t launch_paged_attn_f8(const F8AttnArgs& a, cudaStream_t stream) {

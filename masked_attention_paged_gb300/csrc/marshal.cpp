@@ -24,7 +24,8 @@
 //   r  int32 [B, n] rows                 -> pointer, row stride, n
 //   q  int32 [B, T] rows                 -> pointer, row stride
 //   f  int64 frequencies, 1 .. D / 2     -> pointer, twice their number
-//   l  f32, contiguous, B H T elements, or None -> pointer or null; True: a result of y's rows
+//   l  f32, contiguous, B H T elements, or None -> pointer or null
+//   E  as l, or True: a result of y's rows -> pointer or null
 //   A  f32 [blocks, Hkv, 16] of the cache -> pointer
 //   K  int32, contiguous [B, Hkv, n]     -> pointer
 //   O  as Y, of any type, or None: a result like y, contiguous -> attn_tensor
@@ -164,12 +165,12 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
         put(address(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream()));
         continue;
       }
-      if (o == Py_None && (*f == 'o' || *f == 'n' || *f == 'l' || *f == 'P')) {
+      if (o == Py_None && (*f == 'o' || *f == 'n' || *f == 'l' || *f == 'E' || *f == 'P')) {
         put(0);
         continue;
       }
       const bool makes = (o == Py_None && (*f == 'k' || *f == 'i' || *f == 'U' || *f == 'O')) ||
-                         (o == Py_True && *f == 'l');
+                         (o == Py_True && *f == 'E');
       if (makes) {
         if (n_made == kMostMade || n_tensors == 8 || (*f != 'U' && s.B < 0)) {
           ok = false;
@@ -177,8 +178,8 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
         }
         const int64_t sizes[4] = {s.B, *f == 'k' ? s.T : s.H, s.one_token ? s.D : s.T, s.D};
         const int64_t one = 1;
-        const int dims = *f == 'k' ? 2 : (*f == 'i' || *f == 'U' ? 1 : (*f == 'l' ? 3 : 4) - (s.one_token ? 1 : 0));
-        const at::ScalarType type = *f == 'O' ? s.type : (*f == 'l' ? at::kFloat : at::kInt);
+        const int dims = *f == 'k' ? 2 : (*f == 'i' || *f == 'U' ? 1 : (*f == 'E' ? 3 : 4) - (s.one_token ? 1 : 0));
+        const at::ScalarType type = *f == 'O' ? s.type : (*f == 'E' ? at::kFloat : at::kInt);
         at::Tensor& x = made[n_made++];
         x = at::empty(*f == 'U' ? at::IntArrayRef(&one, 1) : at::IntArrayRef(sizes, dims),
                       at::TensorOptions().dtype(type).device(at::kCUDA, static_cast<c10::DeviceIndex>(device)));
@@ -411,6 +412,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
           put(2 * t.size(0));
           break;
         case 'l':
+        case 'E':
           ok = on(t, device) && t.scalar_type() == at::kFloat && t.is_contiguous() && t.numel() == s.B * s.H * s.T;
           if (!ok) break;
           put(address(t.data_ptr()));

@@ -271,7 +271,7 @@ def test_results_made_or_given(shape):
     f32 = lib.paged_attn_f8(*args, out=torch.empty(shape, device=DEV), workspace=ws)
     assert f32.dtype == torch.float32 and torch.equal(f32.to(torch.bfloat16), out)
     for bad in (dict(out=torch.empty(shape[1:], device=DEV)), dict(lse=torch.empty(7, device=DEV)),
-                dict(lens=_ints([1, 1]))):
+                dict(lens=_ints([1, 1])), dict(lse=True), dict(lse=True, return_lse=True, stream=side)):
         with pytest.raises(ValueError):
             lib.paged_attn_f8(*args, workspace=ws, **bad)
 
@@ -294,6 +294,11 @@ def test_verified_paths_and_used_blocks_made_or_given():
     for bad in (dict(path=_ints(np.zeros((B, T + 1)))), dict(n_accept=_ints([0])), dict(next_token=d.uniforms[:, 0])):
         with pytest.raises(ValueError):
             lib.draft_verify(*args, workspace=d.ws, **bad)
+    q = torch.zeros(B, H * G, T, D, device=DEV, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):  # a result that no call makes
+        lib.paged_tree_attn(q, d.k, d.v, d.table, d.lens, d.parents, lse=True, workspace=d.ws)
+    with pytest.raises(ValueError):
+        lib.draft_verify(*args[:4], True, workspace=d.ws)
     used = [lib.kv_compact([d.k, d.v], d.refs, d.table, workspace=w, used=u)
             for w in (d.ws, None) for u in (None, _ints([77]))]
     assert len({u.item() for u in used}) == 1 and all(u.shape == (1,) and u.dtype == torch.int32 for u in used)

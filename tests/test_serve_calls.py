@@ -154,6 +154,7 @@ def test_paged_attn_f8_rejects(L):  # noqa: F811
     assert call(out=_t([2, 12, 7, 128])) == INVALID
     assert call(q=_t([1, 129, 2, 128]), c=_f8(H=1)) == UNSUPPORTED
     assert call(c=_f8(N=1 << 30)) == UNSUPPORTED
+    assert call(q=_t([65535, 65535, 1, 128]), c=_f8(H=65535)) == UNSUPPORTED  # more items than a grid has CTAs
     assert call(q=_t([2, 12, 6, 128], data=FAKE + 8)) == INVALID
     assert call(out=_t([2, 12, 6, 128], data=FAKE + 8)) == INVALID
     flat = _t([2, 12, 6, 128])
