@@ -23,8 +23,8 @@
 // score buffer, an accumulator and a running max and sum of its own, joined by the LSE
 // rule when an item ends.
 //
-// What bounds it: 2 x 1024 tokens behind 8192 (32 heads over 8, D = 128) take 200 us where the
-// products alone would take 123.  A tile takes 3100 cycles a CTA: 2 x 1040 of products, which
+// What bounds it: 2 x 1024 tokens behind 8192 (32 heads over 8, D = 128) take 195 us where the
+// products alone would take 123.  A tile takes 3000 cycles a CTA: 2 x 1040 of products, which
 // also read shared memory at 128 bytes a cycle, all that it gives (8 KB a step of 65 cycles), so
 // that the TMA's and the converters' bytes come on top; and two waits of the issuer, 230
 // each.  An item's start and end cost some 12000 cycles.  With one row tile the converters
@@ -889,10 +889,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
               m_run = mt;
             }
           };
-          // weights 2^(f s + neg) of 32 scores, f by block: P to TMEM, and their sums
-          auto weigh32 = [&](const uint32_t (&x)[32], int c, float f0, float f1, float neg, uint64_t (&sum)[4]) {
+          // weights 2^(f s + neg) of 32 scores, f by block, and their sums
+          auto weigh32 = [&](const uint32_t (&x)[32], uint32_t (&pw)[16], float f0, float f1, float neg,
+                             uint64_t (&sum)[4]) {
             const uint64_t neg2 = f2_pack(neg, neg);
-            uint32_t pw[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const float f = i < 16 ? f0 : f1;
@@ -903,7 +903,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
               pw[i >> 1] = pack_bf16x2(p0, p1);
               sum[(i >> 1) & 3] = fadd2(sum[(i >> 1) & 3], f2_pack(p0, p1));
             }
-            tmem_st16(tmem + lane_addr + s_col + c * 16, pw);
           };
           // scores in log2 units, -inf where the row may not look
           auto scale32 = [&](uint32_t (&x)[32], int c, float f0, float f1) {
@@ -923,10 +922,42 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          if constexpr (NT == 1) {
-            // Bound by HBM, with time to spare: two rolled passes over the scores in
-            // TMEM, 32 at a time (code that runs once costs its fetch).  The second
-            // writes P over scores that it has read.
+          bool done = false;
+          if constexpr (NT == 2) {
+            // Bound by this chain's latency: scores go to registers, half of them ahead of the
+            // others, and are weighed against the reference max at hand, without a max
+            // pass, unless some row's sum says its scores outgrew it.
+            if (!masked && __all_sync(0xffffffffu, m_run != -INFINITY)) {
+              uint32_t sr[4][32], pw[4][16];
+              tmem_ld32(tmem + lane_addr + s_col, sr[0]);
+              tmem_ld32(tmem + lane_addr + s_col + 32, sr[1]);
+              tmem_wait_ld(sr[0]);
+              tmem_wait_ld(sr[1]);
+              tmem_ld32(tmem + lane_addr + s_col + 64, sr[2]);
+              tmem_ld32(tmem + lane_addr + s_col + 96, sr[3]);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                if (c == 2) {
+                  tmem_wait_ld(sr[2]);
+                  tmem_wait_ld(sr[3]);
+                }
+                weigh32(sr[c], pw[c], mul * ks[2 * c], mul * ks[2 * c + 1], -m_run, sum);
+              }
+              float a0, a1;
+              f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
+              done = __all_sync(0xffffffffu, a0 + a1 <= 18446744073709551616.0f);  // 2^64; false for a NaN
+              if (done) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_st16(tmem + lane_addr + s_col + c * 16, pw[c]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
+              }
+            }
+          }
+          if (!done) {
+            // Two rolled passes over the scores in TMEM, 32 at a time (code that runs once costs
+            // its fetch).  The second writes P over scores that it has read.
             const int nc = (keys + 31) / 32;
 #pragma unroll 1
             for (int c = 0; c < nc; ++c) {
@@ -942,60 +973,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < nc; ++c) {
               const float f0 = mul * ks[2 * c], f1 = mul * ks[2 * c + 1];
-              uint32_t x[32];
+              uint32_t x[32], pw[16];
               tmem_ld32(tmem + lane_addr + s_col + c * 32, x);
               tmem_wait_ld(x);
               if (masked) {
                 scale32(x, c, f0, f1);
-                weigh32(x, c, 1.0f, 1.0f, neg, sum);
+                weigh32(x, pw, 1.0f, 1.0f, neg, sum);
               } else {
-                weigh32(x, c, f0, f1, neg, sum);
+                weigh32(x, pw, f0, f1, neg, sum);
               }
-            }
-          } else {
-            // Bound by this chain's latency: scores go to registers, half of them ahead of the
-            // others, and are weighed against the reference max at hand, without a max
-            // pass; if some row's sum says its scores outgrew it, once more with one.
-            uint32_t sr[4][32];
-            tmem_ld32(tmem + lane_addr + s_col, sr[0]);
-            tmem_ld32(tmem + lane_addr + s_col + 32, sr[1]);
-            const bool fast = !masked && __all_sync(0xffffffffu, m_run != -INFINITY);
-            tmem_wait_ld(sr[0]);
-            tmem_wait_ld(sr[1]);
-            tmem_ld32(tmem + lane_addr + s_col + 64, sr[2]);
-            tmem_ld32(tmem + lane_addr + s_col + 96, sr[3]);
-            bool done = false;
-            if (fast) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                if (c == 2) {
-                  tmem_wait_ld(sr[2]);
-                  tmem_wait_ld(sr[3]);
-                }
-                weigh32(sr[c], c, mul * ks[2 * c], mul * ks[2 * c + 1], -m_run, sum);
-              }
-              float a0, a1;
-              f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
-              done = __all_sync(0xffffffffu, a0 + a1 <= 18446744073709551616.0f);  // 2^64; false for a NaN
-              if (!done) {
-                tmem_wait_st();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
-              }
-            } else {
-              tmem_wait_ld(sr[2]);
-              tmem_wait_ld(sr[3]);
-            }
-            if (!done) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                scale32(sr[c], c, mul * ks[2 * c], mul * ks[2 * c + 1]);
-                max32(sr[c], mx);
-              }
-              raise(fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])));
-              const float neg = m_run == -INFINITY ? 0.0f : -m_run;
-#pragma unroll
-              for (int c = 0; c < 4; ++c) weigh32(sr[c], c, 1.0f, 1.0f, neg, sum);
+              tmem_st16(tmem + lane_addr + s_col + c * 16, pw);
             }
           }
           if (raised && n_mine > mine_before && __any_sync(0xffffffffu, alpha != 1.0f)) {
