@@ -28,7 +28,7 @@
 // also read shared memory at 128 bytes a cycle, all that it gives (8 KB a step of 65 cycles), so
 // that the TMA's and the converters' bytes come on top; and two waits of the issuer, 230
 // each.  An item's start and end cost some 12000 cycles.  With one row tile the converters
-// set the pace, 3000 cycles a tile (16 x 16 tokens behind 8192: 98 us; 76 with weights in one pass and
+// set the pace, 3000 cycles a tile (16 x 16 tokens behind 8192: 90 us; 76 with
 // no conversion at all).
 // Two issuers, one a row tile, took 261 us (both products end late), in strict turns 224;
 // two threads a row, 64 keys each, 229; 64-key tiles 292; waits polled instead of parked 203; the
@@ -923,36 +923,34 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           bool done = false;
-          if constexpr (NT == 2) {
-            // Bound by this chain's latency: scores go to registers, half of them ahead of the
-            // others, and are weighed against the reference max at hand, without a max
-            // pass, unless some row's sum says its scores outgrew it.
-            if (!masked && __all_sync(0xffffffffu, m_run != -INFINITY)) {
-              uint32_t sr[4][32], pw[4][16];
-              tmem_ld32(tmem + lane_addr + s_col, sr[0]);
-              tmem_ld32(tmem + lane_addr + s_col + 32, sr[1]);
-              tmem_wait_ld(sr[0]);
-              tmem_wait_ld(sr[1]);
-              tmem_ld32(tmem + lane_addr + s_col + 64, sr[2]);
-              tmem_ld32(tmem + lane_addr + s_col + 96, sr[3]);
+          // Bound by this chain's latency: scores go to registers, half of them ahead of the
+          // others, and are weighed against the reference max at hand, without a max
+          // pass, unless some row's sum says its scores outgrew it.
+          if (!masked && __all_sync(0xffffffffu, m_run != -INFINITY)) {
+            uint32_t sr[4][32], pw[4][16];
+            tmem_ld32(tmem + lane_addr + s_col, sr[0]);
+            tmem_ld32(tmem + lane_addr + s_col + 32, sr[1]);
+            tmem_wait_ld(sr[0]);
+            tmem_wait_ld(sr[1]);
+            tmem_ld32(tmem + lane_addr + s_col + 64, sr[2]);
+            tmem_ld32(tmem + lane_addr + s_col + 96, sr[3]);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                if (c == 2) {
-                  tmem_wait_ld(sr[2]);
-                  tmem_wait_ld(sr[3]);
-                }
-                weigh32(sr[c], pw[c], mul * ks[2 * c], mul * ks[2 * c + 1], -m_run, sum);
+            for (int c = 0; c < 4; ++c) {
+              if (c == 2) {
+                tmem_wait_ld(sr[2]);
+                tmem_wait_ld(sr[3]);
               }
-              float a0, a1;
-              f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
-              done = __all_sync(0xffffffffu, a0 + a1 <= 18446744073709551616.0f);  // 2^64; false for a NaN
-              if (done) {
+              weigh32(sr[c], pw[c], mul * ks[2 * c], mul * ks[2 * c + 1], -m_run, sum);
+            }
+            float a0, a1;
+            f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
+            done = __all_sync(0xffffffffu, a0 + a1 <= 18446744073709551616.0f);  // 2^64; false for a NaN
+            if (done) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_st16(tmem + lane_addr + s_col + c * 16, pw[c]);
-              } else {
+              for (int c = 0; c < 4; ++c) tmem_st16(tmem + lane_addr + s_col + c * 16, pw[c]);
+            } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
-              }
+              for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
             }
           }
           if (!done) {
@@ -1164,8 +1162,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 }
 
 int tile_queries(int64_t T, int64_t G) { return static_cast<int>(std::min(T, kBM / G)); }
-// One row tile where it holds all rows (16 x 16 tokens of 4 heads behind 8192: 98 us, with two tiles
-// 102; 16 x 32 behind 4000: 61, 70), else two (2 x 1024 behind 8192 199 us, 360 with one at a
+// One row tile where it holds all rows (16 x 16 tokens of 4 heads behind 8192: 90 us, with two tiles
+// 99; 16 x 32 behind 4000: 60, 67), else two (2 x 1024 behind 8192 195 us, 360 with one at a
 // time; 2 x 40 36.5, 39.6).
 int chunk_nt(int64_t T, int64_t G) { return T <= kBM / G ? 1 : 2; }
 size_t part_rows(int64_t T, int64_t G, int n_cta) { return static_cast<size_t>(2) * n_cta * chunk_nt(T, G) * kBM; }
