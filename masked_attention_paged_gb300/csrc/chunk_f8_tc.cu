@@ -27,12 +27,13 @@
 // products alone would take 123.  A tile takes 3000 cycles a CTA: 2 x 1040 of products, which
 // also read shared memory at 128 bytes a cycle, all that it gives (8 KB a step of 65 cycles), so
 // that the TMA's and the converters' bytes come on top; and two waits of the issuer, 230
-// each.  An item's start and end cost some 12000 cycles.  With one row tile the converters
-// set the pace, 3000 cycles a tile (16 x 16 tokens behind 8192: 90 us; 76 with
-// no conversion at all).
-// Two issuers, one a row tile, took 261 us (both products end late), in strict turns 224;
-// two threads a row, 64 keys each, 229; 64-key tiles 292; waits polled instead of parked 203; the
-// converting loop unrolled twice 214, and rolled to one vector a step 231.
+// each.  An item's start and end cost some 12000 cycles.  With one row tile the conversion
+// sets the pace, 2700 cycles a tile (16 x 16 tokens behind 8192: 90 us; 76 with none at all).
+// Not kept, next to the 200 us of then: two issuers, one a row tile, 261 (both products end
+// late), in strict turns 224; two threads a row, 64 keys each, 229; 64-key tiles 292; waits
+// polled instead of parked 203; the converting loop unrolled twice 214, and rolled to one
+// vector a step 231.  Next to 195: q split ahead of the epilogue before it 199; values and weights
+// in fp16, half the converters' instructions, 197.
 //
 // Slots past the last key may hold NaN codes: their V rows go in as zeros (P is 0
 // there, but 0 x NaN is not).  A token that some rows see and others do not may be
