@@ -22,6 +22,8 @@
 // leaves partials (normalised rows and log2 LSE; at most two a warp), which a second
 // launch joins in order, so results do not depend on timing.  (CTAs of 1024 tokens of an
 // item, joined by the last to come, spent 4 us each on their start and end.)
+// 64 sequences of up to 8192 tokens (32 heads over 8, D = 128) take 133 us, 0.81 GB at 90 % of
+// what a copy does; one of 700 (D = 64) 10 us, two launches of dependent loads.
 #include <cuda.h>
 #include <math.h>
 
@@ -36,7 +38,8 @@ namespace attn {
 namespace {
 
 constexpr int kBS = 16;
-constexpr int kWarps = 4;
+constexpr int kMostWarps = 12;  // of an SM
+constexpr int kFewWarps = 4;    // of a CTA of a small call
 constexpr float kLazy = 8.0f;
 
 struct F8MmaParams {
@@ -141,8 +144,8 @@ __device__ __forceinline__ int next_seq(const F8MmaParams& p, int lane, int b, i
 // sequence of 700 tokens and D = 64 where 2 take 10.1).
 constexpr int kLeast = 2;
 // Heads side by side: their rows of a block lie together in memory, and are read at about the
-// same time (64 sequences of 8192: 137.5 us; 138.2 with 4 heads, 139.1 with each on its own).
-constexpr int kSide = 8;
+// same time (64 sequences of 8192: 133 us; 135 with 8 heads or 2).
+constexpr int kSide = 4;
 __device__ __forceinline__ Runs64 runs_of(int64_t total, int warps) {
   return Runs64::make(total, static_cast<int>(min(static_cast<int64_t>(warps), (total + kLeast - 1) / kLeast)));
 }
@@ -165,19 +168,26 @@ __device__ __forceinline__ void write_dims(void* out, int out_bf16, int64_t at, 
 
 template <int D, int NR>
 struct MmaCfg {
-  // CTAs an SM, by registers: 64 sequences of 8192 tokens with 4 rows take 137 us on three, 150
-  // on four (128 registers) and 149 on two; with 16 rows 232 on two and 286 on three, which
-  // spill.  64 of 4096 with 16 rows and D = 64: 96 on two, 84 on three.
-  static constexpr int kCtas = D == 128 && NR == 2 ? 2 : 3;
-  // More blocks in flight make the stream slower: the same 137 us with three are 143 with four
-  // and 195 with five (138 with two); 237 with six for 16 rows, 231 with four.
+  // Warps of an SM, by registers: 64 sequences of 8192 tokens with 4 rows take 133 us on twelve
+  // (168 registers), 150 on sixteen and 149 on eight; with 16 rows 231 on eight and 286 on twelve,
+  // which spill (with q's fragments in shared memory instead 221, but 4 of 2000 27 instead of 23);
+  // 64 of 4096 with 16 rows and D = 64 96 on eight, 84 on twelve.
+  static constexpr int kSmWarps = D == 128 && NR == 2 ? 8 : 12;
+  // Twelve are one CTA where the call can fill the GPU, so that it is placed on an SM as a whole.
+  // (Of three CTAs of four, one or two were placed while a launch ahead of them still held shared
+  // memory, and the third after they were done: 188 us.)  Eight are two CTAs, whose warps do not
+  // run in step (257 us as one).  Calls with less for each SM spread it in CTAs of four (one
+  // sequence of 500 tokens and 16 rows 15 us, 20 in large ones).
+  static constexpr int kWarps = kSmWarps == 8 ? 4 : 12;
+  // More blocks in flight make the stream slower: the 133 us with three are 136 with four (134 with
+  // two; with each head on its own 195 with five); with 16 rows 236 with six, 234 with four.
   static constexpr int kStages = NR == 1 ? 3 : 4;
   static constexpr int kCodeBytes = kBS * D;  // one (block, head) of K or V
-  static constexpr int kSmem = 1024 + kWarps * kStages * (2 * kCodeBytes + 16);
+  static constexpr int smem(int warps) { return 1024 + warps * kStages * (2 * kCodeBytes + 16); }
 };
 
 template <int D, int NR>
-__global__ void __launch_bounds__(kWarps * 32, MmaCfg<D, NR>::kCtas)
+__global__ void __launch_bounds__(MmaCfg<D, NR>::kWarps * 32, MmaCfg<D, NR>::kSmWarps / MmaCfg<D, NR>::kWarps)
     paged_attn_f8_mma_kernel(const __grid_constant__ F8MmaParams p) {
   using C = MmaCfg<D, NR>;
   constexpr int kStages = C::kStages, kCodeBytes = C::kCodeBytes;
@@ -186,9 +196,10 @@ __global__ void __launch_bounds__(kWarps * 32, MmaCfg<D, NR>::kCtas)
   constexpr int kTiles = D / 16;  // of the output's dims
   extern __shared__ uint8_t smem_raw[];
   uint8_t* codes = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // [warp][stage][K, V]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(codes + kWarps * kStages * 2 * kCodeBytes);
-  float2* scales = reinterpret_cast<float2*>(bars + kWarps * kStages);  // [warp][stage] K's and V's; x = -inf: no block
-  __shared__ int abort_flag[kWarps];
+  const int warps = blockDim.x >> 5;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(codes + warps * kStages * 2 * kCodeBytes);
+  float2* scales = reinterpret_cast<float2*>(bars + warps * kStages);  // [warp][stage] K's and V's; x = -inf: no block
+  __shared__ int abort_flag[C::kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* wcodes = codes + warp * kStages * 2 * kCodeBytes;
@@ -209,7 +220,7 @@ __global__ void __launch_bounds__(kWarps * 32, MmaCfg<D, NR>::kCtas)
   wait_for_launch_ahead();
 
   // ---- this warp's run, and where it begins
-  const int me = blockIdx.x * kWarps + warp;
+  const int me = blockIdx.x * warps + warp;
   auto blocks_of = [&](int b) {
     int start, n;
     bool past;
@@ -607,32 +618,35 @@ __global__ void __launch_bounds__(kWarps * 32, MmaCfg<D, NR>::kCtas)
 
 // Joins the pieces of the items that are cut between warps, and writes those that have no
 // blocks.  An item's rows go to as many CTAs as fill the GPU, a CTA's warps share them.
-constexpr int kMergeWarps = 16;
+constexpr int kMergeWarps = 16;  // at most
 template <int D, int NR>
 __global__ void __launch_bounds__(kMergeWarps * 32) f8_mma_merge_kernel(const __grid_constant__ F8MmaParams p) {
   constexpr int kRows = 8 * NR, E = D / 32;
-  __shared__ float acc_of[kMergeWarps][D], sum_of[kMergeWarps];
+  __shared__ float acc_of[kMergeWarps][D];
+  __shared__ float2 sum_of[kMergeWarps];
   let_next_launch_in();
   wait_for_launch_ahead();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.x / p.Hkv, gkv = blockIdx.x - b * p.Hkv;
   const int R = p.T * p.G;
   const int rows = (R + gridDim.y - 1) / gridDim.y;  // of this CTA, `per` warps each
-  const int per = kMergeWarps / rows;
+  const int per = static_cast<int>(blockDim.x >> 5) / rows;
   auto blocks_of = [&](int x) {
     int start, n;
     bool past;
     return seq_blocks(p, x, start, n, past);
   };
-  const int nblk = blocks_of(b);
-  int w0 = 0, w1 = 0, head = 0;  // the pieces' runs; whether the first is its run's first segment
+  int64_t before = 0, all = 0;
+  int nblk = 0;
+  for (int x = lane; x < p.B; x += 32) {
+    const int k = blocks_of(x);
+    all += k;
+    if (x < b) before += k;
+    if (x == b) nblk = k;
+  }
+  nblk = __reduce_add_sync(0xffffffffu, nblk);
+  int w0 = 0, n = 0, head = 0;  // the pieces' runs: the first, their number; whether that is its run's first segment
   if (nblk > 0) {
-    int64_t before = 0, all = 0;
-    for (int x = lane; x < p.B; x += 32) {
-      const int k = blocks_of(x);
-      all += k;
-      if (x < b) before += k;
-    }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) {
       before += __shfl_xor_sync(0xffffffffu, before, m);
@@ -642,60 +656,82 @@ __global__ void __launch_bounds__(kMergeWarps * 32) f8_mma_merge_kernel(const __
     const Runs64 runs = runs_of(all * Hgr, p.warps / p.side);
     const int64_t u0 = before * Hgr + static_cast<int64_t>(gkv / p.side) * nblk;
     w0 = runs.of(u0);
-    w1 = runs.of(u0 + nblk - 1);
+    n = runs.of(u0 + nblk - 1) - w0 + 1;
     head = runs.lo(w0) == u0;
-    if (w0 == w1) return;  // written where it was computed
+    if (n == 1) return;  // written where it was computed
   }
   const int part = warp / per, sub = warp - part * per, row = blockIdx.y * rows + part;
   const bool on = part < rows && row < R;
-  auto piece = [&](int c) {
-    return 2 * (static_cast<int64_t>(c) * p.side + gkv % p.side) + (c == w0 && !head ? 1 : 0);
+  auto at_piece = [&](int i) {
+    return (2 * (static_cast<int64_t>(w0 + i) * p.side + gkv % p.side) + (i == 0 && !head ? 1 : 0)) * kRows + row;
   };
+  // this warp's pieces are sub, sub + per, ...: a lane per piece for their weights, then four
+  // pieces' rows at a time
   float M = -INFINITY, ws = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  bool any = false;
-  if (on && nblk > 0) {
-    for (int c = w0 + lane; c <= w1; c += 32) {
-      const float l = p.part_lse[piece(c) * kRows + row];
-      any |= l != -INFINITY;  // a NaN counts as something: it has to reach the row
-      M = fmaxf(M, l);
-    }
+  const int mine = on && n > sub ? (n - sub + per - 1) / per : 0;
+  for (int q0 = 0; q0 < mine; q0 += 32) {
+    const int here = min(32, mine - q0);
+    const float l = lane < here ? p.part_lse[at_piece(sub + (q0 + lane) * per)] : -INFINITY;
+    float top = fmaxf(l, M);  // (a NaN is not the largest: it gets to the row by its weight)
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
-    any = __any_sync(0xffffffffu, any);
-#pragma unroll 8
-    for (int c = w0 + sub; c <= w1; c += per) {
-      const int64_t at = piece(c) * kRows + row;
-      const float l = p.part_lse[at];
-      const float w = l == -INFINITY ? 0.f : fast_exp2(l - M);
-      ws += w;
-      const float* o = p.part_o + at * D + lane * E;
-      float x[E];
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(o);
-        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(o);
-        x[0] = v.x, x[1] = v.y;
+    for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+    const float alpha = M == -INFINITY ? 1.f : fast_exp2(M - top);
+    M = top;
+    const float w = l == -INFINITY ? 0.f : fast_exp2(l - M);
+    ws = ws * alpha + w;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= alpha;
+#pragma unroll 1
+    for (int k = 0; k < here; k += 4) {
+      float x[4][E], f[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        f[u] = __shfl_sync(0xffffffffu, w, (k + u) & 31);  // (0 past the last)
+        const float* o = p.part_o + at_piece(sub + (q0 + min(k + u, here - 1)) * per) * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(o);
+          x[u][0] = v.x, x[u][1] = v.y, x[u][2] = v.z, x[u][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(o);
+          x[u][0] = v.x, x[u][1] = v.y;
+        }
       }
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[e], acc[e]);
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (k + u < here) acc[e] = fmaf(f[u], x[u][e], acc[e]);
     }
   }
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, m);
   if (per > 1) {
 #pragma unroll
     for (int e = 0; e < E; ++e) acc_of[warp][lane * E + e] = acc[e];
-    if (lane == 0) sum_of[warp] = ws;
+    if (lane == 0) sum_of[warp] = make_float2(M, ws);
     __syncthreads();
-    if (sub != 0) return;
-    for (int k = 1; k < per && on; ++k) {
-      ws += sum_of[warp + k];
+    if (sub != 0 || !on) return;
+    float top = M;
+    for (int k = 1; k < per; ++k) top = fmaxf(top, sum_of[warp + k].x);
+    // (a warp without a max has weights of 0, or a NaN)
+    auto factor = [&](float m) { return m == -INFINITY ? 1.f : fast_exp2(m - top); };
+    const float own = factor(M);
+    ws *= own;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += acc_of[warp + k][lane * E + e];
+    for (int e = 0; e < E; ++e) acc[e] *= own;
+    for (int k = 1; k < per; ++k) {
+      const float2 s = sum_of[warp + k];
+      const float f = factor(s.x);
+      ws = fmaf(f, s.y, ws);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(f, acc_of[warp + k][lane * E + e], acc[e]);
     }
+    M = top;
   }
   if (!on) return;
+  const bool any = !(ws == 0.f);  // a NaN is something
   const int h = gkv * p.G + row % p.G, i = row / p.G;
   const float inv = any ? 1.f / ws : 0.f;
   const int64_t at = b * p.out_stride[0] + h * p.out_stride[1] + i * p.out_stride[2] + lane * E;
@@ -713,21 +749,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32) f8_mma_merge_kernel(const __
 }
 
 // Rows of a KV head; more go to chunk_f8_tc.cu, whose tile has 128.  Both sides with 16 rows
-// (D = 128, 8 KV heads): 64 sequences of 8192 tokens 232 us here and 382 there, 64 of
-// 4096 130 and 205, one of 20000 29 and 39, one of 500 15 and 21.
+// (D = 128, 8 KV heads): 64 sequences of 8192 tokens 234 us here and 382 there, 64 of
+// 4096 129 and 205, one of 20000 26 and 39, one of 500 14 and 21.
 constexpr int64_t kMostRows = 16;
 int rows_of(int64_t rows) { return rows <= 8 ? 8 : 16; }
-int warps_of(int64_t rows, int D, int n_cta) {  // three CTAs an SM where registers allow, else two
-  const int ctas = rows > 8 ? (D == 64 ? MmaCfg<64, 2>::kCtas : MmaCfg<128, 2>::kCtas) : MmaCfg<128, 1>::kCtas;
-  static_assert(MmaCfg<64, 1>::kCtas == MmaCfg<128, 1>::kCtas, "");
-  return n_cta * kWarps * ctas;
-}
 // offsets and size of the workspace
 struct Layout {
   size_t lse, bytes;
 };
 Layout layout(int64_t rows, int D, int n_cta) {
-  const size_t n = static_cast<size_t>(2) * warps_of(rows, D, n_cta) * rows_of(rows);
+  const size_t n = static_cast<size_t>(2) * n_cta * kMostWarps * rows_of(rows);
   Layout l;
   l.lse = n * D * 4;
   l.bytes = (l.lse + n * 4 + 255) & ~size_t(255);
@@ -740,21 +771,33 @@ cudaError_t launch_mma(const F8AttnArgs& a, F8MmaParams& p, cudaStream_t stream)
                    !make_code_cache_map(&p.vmap, a.cache.v, a.cache.num_blocks, a.cache.Hkv)))
     return cudaErrorInvalidValue;
   auto kern = paged_attn_f8_mma_kernel<D, NR>;
-  constexpr int smem = MmaCfg<D, NR>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto join = f8_mma_merge_kernel<D, NR>;
+  using C = MmaCfg<D, NR>;
+  // (an SM shares its memory out anew only when it is empty: both launches want the same)
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(C::kWarps));
+  for (const void* k : {reinterpret_cast<const void*>(kern), reinterpret_cast<const void*>(join)})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
-  // no more CTAs than the call could have runs for
+  p.warps = a.n_cta * C::kSmWarps;
+  // no more warps than the call could have runs for
   const int64_t runs = (a.B * (a.cache.Hkv / p.side) * static_cast<int64_t>(a.max_blocks) + kLeast - 1) / kLeast;
-  const int64_t most = (runs * p.side + kWarps - 1) / kWarps;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(p.warps / kWarps, most)));
-  e = launch_early(kern, grid, kWarps * 32, smem, stream, p);
+  const int64_t most = std::min<int64_t>(p.warps, runs * p.side);
+  const int warps = most > kFewWarps * a.n_cta ? C::kWarps : kFewWarps;
+  const dim3 grid(static_cast<unsigned>((most + warps - 1) / warps));
+  e = launch_early(kern, grid, warps * 32, C::smem(warps), stream, p);
   if (e != cudaSuccess) return e;
-  const int64_t items = a.B * a.cache.Hkv;
-  // (one sequence of 20000 tokens and 16 rows: 29 us, 50 with a CTA an item; rows on more CTAs
-  // than that cost 64 sequences 4 us)
-  const int64_t shares = std::min<int64_t>(a.T * p.G, std::max<int64_t>(1, 2 * a.n_cta / items));
-  const dim3 join(static_cast<unsigned>(items), static_cast<unsigned>(shares));
-  return launch_early(f8_mma_merge_kernel<D, NR>, join, kMergeWarps * 32, 0, stream, p);
+  // The second launch: with few rows in all, sixteen warps for each (one sequence of 20000 tokens
+  // and 16 rows: 25 us, 36 with eight); else CTAs of eight warps for an item, or half its rows,
+  // that fit in one wave (64 sequences of 8192 tokens: 136 us, 140 with sixteen).
+  const int64_t items = a.B * a.cache.Hkv, rows = a.T * p.G;
+  const bool few = items * rows <= 2 * a.n_cta;
+  const int join_warps = few ? 16 : 8;
+  const int64_t shares = few ? rows
+                             : std::min<int64_t>(rows, std::max<int64_t>((rows + join_warps - 1) / join_warps,
+                                                                         4 * a.n_cta / items));
+  const dim3 join_grid(static_cast<unsigned>(items), static_cast<unsigned>(shares));
+  return launch_early(join, join_grid, join_warps * 32, 0, stream, p);
 }
 
 }  // namespace
@@ -793,7 +836,6 @@ cudaError_t launch_paged_attn_f8(const F8AttnArgs& a, cudaStream_t stream) {
   p.causal = a.causal;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.B = static_cast<int>(a.B);
-  p.warps = warps_of(a.T * G, a.cache.D, a.n_cta);
   p.side = 1;
   while (p.side < kSide && p.Hkv % (2 * p.side) == 0) p.side *= 2;
   p.out = a.out.data;
