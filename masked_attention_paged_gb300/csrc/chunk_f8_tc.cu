@@ -253,27 +253,32 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
   int i, h;
   const bool mine = place(sr, i, h);
   auto slot = [&](int c) { return static_cast<int64_t>(2 * (c0 + c) + ((c == 0 && !it.first_is_head) ? 1 : 0)); };
-  float M = -INFINITY;
-  bool any = false;  // a NaN counts as something: it has to reach the row
-#pragma unroll 8
-  for (int c = 0; c < it.pieces; ++c) {
-    const float l = mine ? p.part_lse[slot(c) * p.pitch + sr] : -INFINITY;
-    any |= l != -INFINITY;
-    M = fmaxf(M, l);
-  }
-  float acc[CW], ws = 0.f;
+  // two pieces at a time, rows and LSEs on their way together; in order, with a running max
+  float M = -INFINITY, acc[CW], ws = 0.f;
 #pragma unroll
   for (int x = 0; x < CW; ++x) acc[x] = 0.f;
-#pragma unroll 32 / CW
-  for (int c = 0; c < it.pieces; ++c) {
-    const float l = mine ? p.part_lse[slot(c) * p.pitch + sr] : -INFINITY;
-    const float* o = p.part_o + (slot(c) * D + warp * CW) * p.pitch + sr;
-    const bool use = l != -INFINITY;  // a piece that saw nothing holds zeros
-    const float w = use ? fast_exp2(l - M) : 0.f;
-    ws += w;
+#pragma unroll 1
+  for (int c = 0; c < it.pieces; c += 2) {
+    float l[2], o[2][CW];
 #pragma unroll
-    for (int x = 0; x < CW; ++x) acc[x] = fmaf(w, use ? o[static_cast<int64_t>(x) * p.pitch] : 0.f, acc[x]);
+    for (int k = 0; k < 2; ++k) {
+      const bool there = mine && c + k < it.pieces;
+      const int64_t at = slot(min(c + k, it.pieces - 1));
+      l[k] = there ? p.part_lse[at * p.pitch + sr] : -INFINITY;
+      const float* src = p.part_o + (at * D + warp * CW) * p.pitch + sr;
+#pragma unroll
+      for (int x = 0; x < CW; ++x) o[k][x] = there ? src[static_cast<int64_t>(x) * p.pitch] : 0.f;
+    }
+    const float top = fmaxf(M, fmaxf(l[0], l[1]));  // (a NaN gets to the row by its weight)
+    const float alpha = M == -INFINITY ? 1.f : fast_exp2(M - top);
+    M = top;
+    const float w0 = l[0] == -INFINITY ? 0.f : fast_exp2(l[0] - M);  // a piece that saw nothing holds zeros
+    const float w1 = l[1] == -INFINITY ? 0.f : fast_exp2(l[1] - M);
+    ws = fmaf(ws, alpha, w0 + w1);
+#pragma unroll
+    for (int x = 0; x < CW; ++x) acc[x] = fmaf(w1, o[1][x], fmaf(w0, o[0][x], acc[x] * alpha));
   }
+  const bool any = !(ws == 0.f);  // a NaN is something
   const float inv = any ? 1.f / ws : 0.f;
 #pragma unroll
   for (int x = 0; x < CW; ++x) tile[lane][warp * CW + x] = any ? acc[x] * inv : 0.f;
