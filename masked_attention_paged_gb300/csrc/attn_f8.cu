@@ -749,8 +749,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) f8_mma_merge_kernel(const __
 }
 
 // Rows of a KV head; more go to chunk_f8_tc.cu, whose tile has 128.  Both sides with 16 rows
-// (D = 128, 8 KV heads): 64 sequences of 8192 tokens 234 us here and 382 there, 64 of
-// 4096 129 and 205, one of 20000 26 and 39, one of 500 14 and 21.
+// (D = 128, 8 KV heads): 64 sequences of 8192 tokens 234 us here and 289 there, 64 of
+// 4096 129 and 181, one of 20000 26 and 34, one of 500 14 and 21.
 constexpr int64_t kMostRows = 16;
 int rows_of(int64_t rows) { return rows <= 8 ? 8 : 16; }
 // offsets and size of the workspace

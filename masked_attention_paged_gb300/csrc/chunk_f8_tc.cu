@@ -23,17 +23,18 @@
 // score buffer, an accumulator and a running max and sum of its own, joined by the LSE
 // rule when an item ends.
 //
-// What bounds it: 2 x 1024 tokens behind 8192 (32 heads over 8, D = 128) take 195 us where the
+// What bounds it: 2 x 1024 tokens behind 8192 (32 heads over 8, D = 128) take 194 us where the
 // products alone would take 123.  A tile takes 3000 cycles a CTA: 2 x 1040 of products, which
 // also read shared memory at 128 bytes a cycle, all that it gives (8 KB a step of 65 cycles), so
 // that the TMA's and the converters' bytes come on top; and two waits of the issuer, 230
 // each.  An item's start and end cost some 12000 cycles.  With one row tile the conversion
-// sets the pace, 2700 cycles a tile (16 x 16 tokens behind 8192: 90 us; 76 with none at all).
+// sets the pace, 2700 cycles a tile (16 x 16 tokens behind 8192: 85 us; some 70 with none at all).
 // Not kept, next to the 200 us of then: two issuers, one a row tile, 261 (both products end
 // late), in strict turns 224; two threads a row, 64 keys each, 229; 64-key tiles 292; waits
 // polled instead of parked 203; the converting loop unrolled twice 214, and rolled to one
 // vector a step 231.  Next to 195: q split ahead of the epilogue before it 199; values and weights
-// in fp16, half the converters' instructions, 197.
+// in fp16, half the converters' instructions, 197; items joined in place by the last of up to four
+// CTAs 192, but 98 for the 16 x 16.
 //
 // Slots past the last key may hold NaN codes: their V rows go in as zeros (P is 0
 // there, but 0 x NaN is not).  A token that some rows see and others do not may be
@@ -61,8 +62,9 @@ constexpr float kRescaleMargin = 8.0f;
 constexpr int kBarBytes = 4096;
 constexpr int kSegs = 4;      // segments the planner is ahead
 // What an item costs a CTA besides its tiles, in tiles: the split of q, the products of the first
-// tile, the epilogue.  Two chunks of 1024 behind 8192 tokens: 199 us with 5, 6, 8 and 10, 203 with
-// 3, 205 with none; two of 64: 39, 45, 50; one of 2048 behind 10 tokens: 75, 81, 90 (2).
+// tile, the epilogue.  Two chunks of 1024 behind 8192 tokens: 194 us with 6, 193 with 8, 197 with
+// 3, 199 with none; two of 64: 35, 36, 40, 45; one of 2048 behind 10 tokens: 70, 70, 77, 155; 4 of
+// 300 behind 1000: 49.5, 50, 52, 60.
 constexpr int kItemCost = 6;
 constexpr int kScales = 8;    // tiles whose key scales are held: more than K's stages and the scores ahead of P
 constexpr int kNotes = 8;     // segments whose notes of NaNs are held: more than the planner is ahead
@@ -1168,9 +1170,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 }
 
 int tile_queries(int64_t T, int64_t G) { return static_cast<int>(std::min(T, kBM / G)); }
-// One row tile where it holds all rows (16 x 16 tokens of 4 heads behind 8192: 90 us, with two tiles
-// 99; 16 x 32 behind 4000: 60, 67), else two (2 x 1024 behind 8192 195 us, 360 with one at a
-// time; 2 x 40 36.5, 39.6).
+// One row tile where it holds all rows (16 x 16 tokens of 4 heads behind 8192: 85 us, with two tiles
+// 98; 16 x 32 behind 4000: 58, 66), else two (2 x 1024 behind 8192 194 us, 282 with one at a
+// time; 16 x 40 behind 2000 52, 69).
 int chunk_nt(int64_t T, int64_t G) { return T <= kBM / G ? 1 : 2; }
 size_t part_rows(int64_t T, int64_t G, int n_cta) { return static_cast<size_t>(2) * n_cta * chunk_nt(T, G) * kBM; }
 size_t part_bytes(int64_t T, int64_t G, int D, int n_cta) {
