@@ -773,11 +773,13 @@ cudaError_t launch_mma(const F8AttnArgs& a, F8MmaParams& p, cudaStream_t stream)
   auto kern = paged_attn_f8_mma_kernel<D, NR>;
   auto join = f8_mma_merge_kernel<D, NR>;
   using C = MmaCfg<D, NR>;
-  // (an SM shares its memory out anew only when it is empty: both launches want the same)
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(C::kWarps));
-  for (const void* k : {reinterpret_cast<const void*>(kern), reinterpret_cast<const void*>(join)})
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  // an SM shares its memory out anew only when it is empty: where it has more than one CTA of this
+  // launch, the second one asks for the same
+  if constexpr (C::kSmWarps > C::kWarps)
+    for (const void* k : {reinterpret_cast<const void*>(kern), reinterpret_cast<const void*>(join)})
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
   p.warps = a.n_cta * C::kSmWarps;
   // no more warps than the call could have runs for

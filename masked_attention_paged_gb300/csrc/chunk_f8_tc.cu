@@ -17,9 +17,9 @@
 // leaves partials (normalised rows and log2 LSE), which a second launch joins in
 // order, so results do not depend on timing.
 //
-// Warps: 0 streams the codes, 1 issues the MMAs, 2 waits for it, 3 plans the segments, 4-7 convert V, 8-11 and 12-15 softmax (thread r owns row
-// r: TMEM lane r; it also splits its row of q).  With NT = 2 each warpgroup has a row
-// tile.  With NT = 1 both have the same rows and take the key tiles in turn, each with a
+// Warps: 0 streams the codes, 1 issues the MMAs, 2 waits for it, 3 plans the segments, 4-7
+// convert V, 8-11 and 12-15 softmax (thread r owns row r: TMEM lane r; it also splits
+// its row of q).  With NT = 2 each warpgroup has a row tile.  With NT = 1 both have the same rows and take the key tiles in turn, each with a
 // score buffer, an accumulator and a running max and sum of its own, joined by the LSE
 // rule when an item ends.
 //
