@@ -23,7 +23,7 @@
 // score buffer, an accumulator and a running max and sum of its own, joined by the LSE
 // rule when an item ends.
 //
-// What bounds it: 2 x 1024 tokens behind 8192 (32 heads over 8, D = 128) take 194 us where the
+// What bounds it: 2 x 1024 tokens behind 8192 (32 heads over 8, D = 128) take 191 us where the
 // products alone would take 123.  A tile takes 3000 cycles a CTA: 2 x 1040 of products, which
 // also read shared memory at 128 bytes a cycle, all that it gives (8 KB a step of 65 cycles), so
 // that the TMA's and the converters' bytes come on top; and two waits of the issuer, 230
@@ -63,7 +63,7 @@ constexpr int kBarBytes = 4096;
 constexpr int kSegs = 4;      // segments the planner is ahead
 // What an item costs a CTA besides its tiles, in tiles: the split of q, the products of the first
 // tile, the epilogue.  Two chunks of 1024 behind 8192 tokens: 194 us with 6, 193 with 8, 197 with
-// 3, 199 with none; two of 64: 35, 36, 40, 45; one of 2048 behind 10 tokens: 70, 70, 77, 155; 4 of
+// 3, 199 with none (191 with 6 since the second launch is faster); two of 64: 35, 36, 40, 45; one of 2048 behind 10 tokens: 70, 70, 77, 155; 4 of
 // 300 behind 1000: 49.5, 50, 52, 60.
 constexpr int kItemCost = 6;
 constexpr int kScales = 8;    // tiles whose key scales are held: more than K's stages and the scores ahead of P
@@ -208,15 +208,18 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
 }
 
 // Joins the pieces of the cut items: out = sum_c 2^(lse_c - M) out_c / sum_c 2^(lse_c - M).
-// grid (CTAs of the main launch, groups of 32 rows), a warp per D / 16 columns, a lane
-// per row: partials are read as they were written, 128 bytes a warp, and the rows
-// leave through shared memory.  CTAs past the main launch's write the rows of groups
-// that see nothing.
-constexpr int kMergeThreads = 512;
+// grid (CTAs of the main launch, groups of 32 rows), a warp per D / 8 columns, a lane per row.
+// Two pieces at a time go to shared memory by asynchronous copies, 128 bytes of a column each
+// as they were written, so that an SM has most of its share on its way at once (in registers
+// four waves of CTAs: 18 us for 37 MB, 13 so); the rows leave through shared memory, too.  CTAs past
+// the main launch's write the rows of groups that see nothing.
+constexpr int kMergeThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
-  constexpr int CW = D / 16;
-  __shared__ float tile[32][D + 1];
+  constexpr int CW = D / 8;
+  __shared__ __align__(16) float buf[2][D][32];
+  float(*tile)[D + 1] = reinterpret_cast<float(*)[D + 1]>(&buf[0][0][0]);  // [32], when the pieces have been read
+  static_assert(32 * (D + 1) <= 2 * D * 32, "");
   let_next_launch_in();
   wait_for_launch_ahead();
   const int c0 = blockIdx.x;
@@ -255,31 +258,42 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
   int i, h;
   const bool mine = place(sr, i, h);
   auto slot = [&](int c) { return static_cast<int64_t>(2 * (c0 + c) + ((c == 0 && !it.first_is_head) ? 1 : 0)); };
-  // two pieces at a time, rows and LSEs on their way together; in order, with a running max
+  // in order, with a running max
   float M = -INFINITY, acc[CW], ws = 0.f;
 #pragma unroll
   for (int x = 0; x < CW; ++x) acc[x] = 0.f;
 #pragma unroll 1
   for (int c = 0; c < it.pieces; c += 2) {
-    float l[2], o[2][CW];
+    const int n = min(2, it.pieces - c);
+    if (c > 0) __syncthreads();  // the pieces before have been read
+    float l[2] = {-INFINITY, -INFINITY};
+    for (int k = 0; k < n; ++k) {
+      const float* src = p.part_o + slot(c + k) * D * p.pitch + blockIdx.y * 32;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const bool there = mine && c + k < it.pieces;
-      const int64_t at = slot(min(c + k, it.pieces - 1));
-      l[k] = there ? p.part_lse[at * p.pitch + sr] : -INFINITY;
-      const float* src = p.part_o + (at * D + warp * CW) * p.pitch + sr;
-#pragma unroll
-      for (int x = 0; x < CW; ++x) o[k][x] = there ? src[static_cast<int64_t>(x) * p.pitch] : 0.f;
+      for (int u = threadIdx.x; u < D * 8; u += kMergeThreads)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&buf[k][u / 8][u % 8 * 4])),
+                     "l"(src + static_cast<int64_t>(u / 8) * p.pitch + u % 8 * 4)
+                     : "memory");
+      if (mine) l[k] = p.part_lse[slot(c + k) * p.pitch + sr];
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
     const float top = fmaxf(M, fmaxf(l[0], l[1]));  // (a NaN gets to the row by its weight)
     const float alpha = M == -INFINITY ? 1.f : fast_exp2(M - top);
     M = top;
-    const float w0 = l[0] == -INFINITY ? 0.f : fast_exp2(l[0] - M);  // a piece that saw nothing holds zeros
-    const float w1 = l[1] == -INFINITY ? 0.f : fast_exp2(l[1] - M);
-    ws = fmaf(ws, alpha, w0 + w1);
+    ws *= alpha;
 #pragma unroll
-    for (int x = 0; x < CW; ++x) acc[x] = fmaf(w1, o[1][x], fmaf(w0, o[0][x], acc[x] * alpha));
+    for (int x = 0; x < CW; ++x) acc[x] *= alpha;
+    for (int k = 0; k < n; ++k) {
+      const float w = l[k] == -INFINITY ? 0.f : fast_exp2(l[k] - M);
+      ws += w;
+      if (w != 0.f) {  // (rows that are not there hold anything)
+#pragma unroll
+        for (int x = 0; x < CW; ++x) acc[x] = fmaf(w, buf[k][warp * CW + x][lane], acc[x]);
+      }
+    }
   }
+  __syncthreads();  // (the tile takes the pieces' place)
   const bool any = !(ws == 0.f);  // a NaN is something
   const float inv = any ? 1.f / ws : 0.f;
 #pragma unroll
@@ -288,7 +302,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
     p.lse[(static_cast<int64_t>(it.b) * p.Hq + h) * p.T + i] =
         any ? (M + __log2f(ws)) * 0.6931471805599453f : -INFINITY;
   __syncthreads();
-  const int r = threadIdx.x / 16, d = threadIdx.x % 16 * CW;
+  const int r = threadIdx.x / 8, d = threadIdx.x % 8 * CW;
   if (!place(blockIdx.y * 32 + r, i, h)) return;
   const int64_t ob = it.b * p.out_stride[0] + h * p.out_stride[1] + i * p.out_stride[2] + d;
   const float* x = &tile[r][d];
