@@ -68,6 +68,8 @@ struct F8MmaParams {
   int side;         // heads side by side: warps that take the same run, a head each
   float* part_o;    // [2 warps][8 NR][D]: a warp's first segment, and a later one
   float* part_lse;  // [2 warps][8 NR], log2 units
+  Runs64* runs;     // for the second launch: the runs, and where an item's blocks begin in them (times
+  int64_t* first;   // two, plus one if that is a warp's first segment), [B][Hkv / side]
   uint32_t* status;
 };
 
@@ -238,7 +240,9 @@ __global__ void __launch_bounds__(MmaCfg<D, NR>::kWarps * 32, MmaCfg<D, NR>::kSm
   const Runs64 runs = runs_of(total, p.warps / p.side);
   if (run_of_warp >= runs.n) return;
   const int64_t lo = runs.lo(run_of_warp);
-  int left = static_cast<int>(runs.lo(run_of_warp + 1) - lo);  // blocks to take (a run of 2^31 would be 2^35 tokens)
+  const int64_t hi = runs.lo(run_of_warp + 1);
+  if (me == 0 && lane == 0) *p.runs = runs;
+  int left = static_cast<int>(hi - lo);  // blocks to take (a run of 2^31 would be 2^35 tokens)
   int b = 0, grp = 0, blk = 0;                        // the next one
   {
     int64_t run = 0;
@@ -334,6 +338,7 @@ __global__ void __launch_bounds__(MmaCfg<D, NR>::kWarps * 32, MmaCfg<D, NR>::kSm
     bool past;
     const int nblk = seq_blocks(p, b, start, n, past);
     const int blk0 = blk, count = min(left, nblk - blk);
+    if (blk0 == 0 && off == 0 && lane == 0) p.first[static_cast<int64_t>(b) * Hgr + grp] = 2 * (hi - left) + (seg == 0);
     // the keys that row r sees: [0, limit)
     auto limit = [&](int r) {
       const int i = r / p.G;
@@ -617,7 +622,8 @@ __global__ void __launch_bounds__(MmaCfg<D, NR>::kWarps * 32, MmaCfg<D, NR>::kSm
 }
 
 // Joins the pieces of the items that are cut between warps, and writes those that have no
-// blocks.  An item's rows go to as many CTAs as fill the GPU, a CTA's warps share them.
+// blocks.  Where an item's pieces are, the first launch has left (found again from all the
+// sequences' lengths it took 1200 us of 8192 short sequences, 233 now in all).  An item's rows go to as many CTAs as fill the GPU, a CTA's warps share them.
 constexpr int kMergeWarps = 16;  // at most
 template <int D, int NR>
 __global__ void __launch_bounds__(kMergeWarps * 32) f8_mma_merge_kernel(const __grid_constant__ F8MmaParams p) {
@@ -631,33 +637,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) f8_mma_merge_kernel(const __
   const int R = p.T * p.G;
   const int rows = (R + gridDim.y - 1) / gridDim.y;  // of this CTA, `per` warps each
   const int per = static_cast<int>(blockDim.x >> 5) / rows;
-  auto blocks_of = [&](int x) {
-    int start, n;
-    bool past;
-    return seq_blocks(p, x, start, n, past);
-  };
-  int64_t before = 0, all = 0;
-  int nblk = 0;
-  for (int x = lane; x < p.B; x += 32) {
-    const int k = blocks_of(x);
-    all += k;
-    if (x < b) before += k;
-    if (x == b) nblk = k;
-  }
-  nblk = __reduce_add_sync(0xffffffffu, nblk);
+  int start, queries;
+  bool past;
+  const int nblk = seq_blocks(p, b, start, queries, past);
   int w0 = 0, n = 0, head = 0;  // the pieces' runs: the first, their number; whether that is its run's first segment
   if (nblk > 0) {
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) {
-      before += __shfl_xor_sync(0xffffffffu, before, m);
-      all += __shfl_xor_sync(0xffffffffu, all, m);
-    }
-    const int Hgr = p.Hkv / p.side;
-    const Runs64 runs = runs_of(all * Hgr, p.warps / p.side);
-    const int64_t u0 = before * Hgr + static_cast<int64_t>(gkv / p.side) * nblk;
+    const Runs64 runs = *p.runs;
+    const int64_t first = p.first[static_cast<int64_t>(b) * (p.Hkv / p.side) + gkv / p.side], u0 = first >> 1;
+    if (u0 < 0 || u0 + nblk > runs.lo(runs.n)) return;  // (not written: a wait of the first launch gave up)
     w0 = runs.of(u0);
     n = runs.of(u0 + nblk - 1) - w0 + 1;
-    head = runs.lo(w0) == u0;
+    head = static_cast<int>(first & 1);
     if (n == 1) return;  // written where it was computed
   }
   const int part = warp / per, sub = warp - part * per, row = blockIdx.y * rows + part;
@@ -755,13 +745,16 @@ constexpr int64_t kMostRows = 16;
 int rows_of(int64_t rows) { return rows <= 8 ? 8 : 16; }
 // offsets and size of the workspace
 struct Layout {
-  size_t lse, bytes;
+  size_t lse, runs, first, bytes;
 };
-Layout layout(int64_t rows, int D, int n_cta) {
+static_assert(sizeof(Runs64) == 16, "its place in the workspace");
+Layout layout(int64_t items, int64_t rows, int D, int n_cta) {
   const size_t n = static_cast<size_t>(2) * n_cta * kMostWarps * rows_of(rows);
   Layout l;
   l.lse = n * D * 4;
-  l.bytes = (l.lse + n * 4 + 255) & ~size_t(255);
+  l.runs = l.lse + n * 4;
+  l.first = l.runs + 16;
+  l.bytes = (l.first + items * 8 + 255) & ~size_t(255);
   return l;
 }
 
@@ -806,7 +799,7 @@ cudaError_t launch_mma(const F8AttnArgs& a, F8MmaParams& p, cudaStream_t stream)
 
 size_t f8_attn_partial_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t T, int64_t max_blocks, int D, int n_cta) {
   const int64_t G = Hq / Hkv;
-  return T * G > kMostRows ? f8_chunk_partial_bytes(T, G, D, n_cta) : layout(T * G, D, n_cta).bytes;
+  return T * G > kMostRows ? f8_chunk_partial_bytes(T, G, D, n_cta) : layout(B * Hkv, T * G, D, n_cta).bytes;
 }
 
 bool f8_attn_fits(int64_t B, int64_t Hq, int64_t Hkv, int64_t T, int64_t max_blocks) {
@@ -818,7 +811,7 @@ cudaError_t launch_paged_attn_f8(const F8AttnArgs& a, cudaStream_t stream) {
   const int G = static_cast<int>(a.Hq / a.cache.Hkv);
   if (a.T * G > kMostRows) return launch_chunk_f8(a, stream);
   F8MmaParams p = {};
-  const Layout l = layout(a.T * G, a.cache.D, a.n_cta);
+  const Layout l = layout(a.B * a.cache.Hkv, a.T * G, a.cache.D, a.n_cta);
   p.kq = a.cache.k;
   p.vq = a.cache.v;
   p.ks = a.cache.k_scale;
@@ -846,6 +839,8 @@ cudaError_t launch_paged_attn_f8(const F8AttnArgs& a, cudaStream_t stream) {
   uint8_t* ws = static_cast<uint8_t*>(a.partials);
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_lse = reinterpret_cast<float*>(ws + l.lse);
+  p.runs = reinterpret_cast<Runs64*>(ws + l.runs);
+  p.first = reinterpret_cast<int64_t*>(ws + l.first);
   p.status = a.status;
   if (a.cache.D == 64)
     return rows_of(a.T * G) == 8 ? launch_mma<64, 1>(a, p, stream) : launch_mma<64, 2>(a, p, stream);
