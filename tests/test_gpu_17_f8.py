@@ -426,3 +426,13 @@ def test_many_sequences_most_of_them_idle(T, Hkv, G, D):
     start[:-4] = -1
     start[-4], lens[-4] = 100 - T, T
     _check(_bf((B, Hkv * G, T, D), rng), codes, scales, table, start, lens=lens)
+
+
+@pytest.mark.parametrize("T,Hkv,G,D", [(1, 2, 1, 64), (2, 1, 6, 128), (5, 1, 4, 64)])
+def test_a_large_batch_of_short_sequences(T, Hkv, G, D):
+    """More items than warps: most runs hold several whole ones."""
+    rng = np.random.default_rng(T)
+    B, width, N = 2100, 3, 50
+    codes, scales = _cache(N, Hkv, D, rng)
+    start = rng.integers(-1, width * BS - T + 1, B).astype(np.int32)
+    _check(_bf((B, Hkv * G, T, D), rng), codes, scales, rng.integers(0, N, (B, width)).astype(np.int32), start)
