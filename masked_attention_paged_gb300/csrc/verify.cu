@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyP
   __shared__ uint8_t first[kMaxDrafts];    // taken, if it is the first to be tested at its node: u q < p
   __shared__ Pair warp_sum[kWarps], cta_sum[2][kMaxCtas], found_start, found_goal;
   __shared__ Ask ask;
-  __shared__ int found;  // the warp whose part the next token is in; -1: not this CTA's
+  __shared__ int found;     // the warp whose part the next token is in; -1: not this CTA's
+  __shared__ bool remains;  // the last row's sum is positive (not in `found`, which warp 0 sets while others read this)
   let_next_launch_in();
   wait_for_launch_ahead();
   const int b = blockIdx.y, rank = static_cast<int>(cluster_rank());
@@ -365,9 +366,9 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyP
   const int last = ask.node;
   // nothing is left of a row that something was taken from: the token comes from p itself
   bool whole = ask.c.x == 0.f && !certain;
-  if (warp == 0 && lane == 0) found = total.x > 0.f;
+  if (warp == 0 && lane == 0) remains = total.x > 0.f;
   __syncthreads();
-  if (!found && !whole) {  // (the cluster's CTAs alike)
+  if (!remains && !whole) {  // (the cluster's CTAs alike)
     whole = true;
     total = row_sum(last, zero, false);
   }
