@@ -60,10 +60,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 // every thread of every CTA of the cluster
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 template <bool BF16>
 __device__ __forceinline__ float load(const void* row, int64_t i) {
@@ -205,6 +203,10 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyP
     }
     return;
   }
+  // The first sum stores into the other CTAs' shared memory, which they must have begun to
+  // run for: the barrier's other half is there, behind the walk and the loads.
+  cluster_arrive();
+  bool started = false;  // alike in the whole cluster
 
   // this warp's part of a row: [w0, w1)
   const int per = (((V + nc * kWarps - 1) / (nc * kWarps)) + 31) / 32 * 32;
@@ -249,6 +251,8 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyP
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) acc = add(acc, shfl_xor(acc, m));
     if (lane == 0) warp_sum[warp] = acc.x > 0.f ? acc : make_float2(0.f, 0.f);
+    if (!started) cluster_wait();  // every CTA has begun
+    started = true;
     __syncthreads();
     turn ^= 1;
     const auto all_lanes = [&](Pair s) {  // of the first 16 lanes, the others hold 0
@@ -267,7 +271,8 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyP
         asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(s.x), "f"(s.y) : "memory");
       }
     }
-    cluster_sync();
+    cluster_arrive();
+    cluster_wait();
     if (warp != 0) return none;
     return shfl(all_lanes(lane % 16 < nc ? cta_sum[turn][lane % 16] : none), 0);
   };

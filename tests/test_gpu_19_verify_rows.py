@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import masked_attention_paged_gb300 as lib
 from _serve_ref import verify
 from test_gpu_15_verify import _equal, _inputs, _run
 
@@ -49,3 +50,29 @@ def test_a_token_after_a_refusal_in_every_part(B, V, mode):
         got, status = _run(p, q, tok, par, u)
         _equal(got, verify(p, q, tok, par, u, False))
         assert (got[1] == 1).all() and status == 0
+
+
+@pytest.mark.parametrize("mode", ["replacement", "distinct", "certain"])
+@pytest.mark.parametrize("B,T,V,wide", [(1, 6, WIDE, 3), (3, 9, 40001, 4), (30, 4, 2 * 16384, 2), (70, 5, 4097, 3)])
+def test_two_byte_probabilities_over_a_cluster(B, T, V, wide, mode):
+    p, q, tok, par, u = _inputs(B, T, V, seed=B + V, wide=wide, mode=mode, dtype=torch.bfloat16)
+    q = None if mode == "certain" else q
+    got, status = _run(p, q, tok, par, u, mode == "replacement", dtype=torch.bfloat16)
+    _equal(got, verify(p, q, tok, par, u, mode == "replacement"))
+    assert status == 0
+
+
+@pytest.mark.parametrize("B", [1, 9, 38])
+def test_calls_right_behind_one_another(B):
+    """Clusters of 16 that are placed while those of the call ahead still run, over trees with and without idle
+    sequences between them."""
+    p, q, tok, par, u = _inputs(B, 5, WIDE, seed=B, wide=3)
+    idle = par.copy()
+    idle[::2, 0] = -2
+    to = lambda x: torch.from_numpy(x).cuda()  # noqa: E731
+    P, Q, K, U, trees, ws = to(p), to(q), to(tok), to(u), [to(par), to(idle)], lib.Workspace(256)
+    got = [lib.draft_verify(P, K, trees[i % 2], U, draft_probs=Q, workspace=ws) for i in range(60)]
+    want = [verify(p, q, tok, x, u, False) for x in (par, idle)]
+    for i, x in enumerate(got):
+        _equal([y.cpu().numpy() for y in x], want[i % 2])
+    assert ws.status() == 0
