@@ -13,7 +13,10 @@
 //    are, register for register, their score fragment, and codes become fp16 exactly,
 //    two an instruction.  The block's value scale multiplies the products.
 // Softmax is online with a lazy running max (log2 units, it moves when a block exceeds
-// it by kLazy).
+// it by kLazy).  Weights are taken times 2^kLift, so that fp16 has room above for what kLazy lets
+// through (2^15 at most) and loses a weight only below 2^-32 of the largest: the sum keeps
+// those in 32 bits, and a long tail beside a few large weights would otherwise count there
+// and be missing from the values.
 //
 // What bounds it is HBM, so nothing may stop the stream of blocks.  All blocks of the
 // call, item (sequence, KV head) after item, are laid end to end, and every warp takes an
@@ -41,6 +44,9 @@ constexpr int kBS = 16;
 constexpr int kMostWarps = 12;  // of an SM
 constexpr int kFewWarps = 4;    // of a CTA of a small call
 constexpr float kLazy = 8.0f;
+constexpr float kLift = 7.0f;  // kLift + kLazy < 16, fp16's range
+constexpr float kUnlift = 1.0f / 128.0f;
+static_assert(kLift + kLazy <= 15.0f && kUnlift * (1 << static_cast<int>(kLift)) == 1.0f, "");
 
 struct F8MmaParams {
   CUtensorMap kmap, vmap;  // D = 128: codes [num_blocks, Hkv, 16, 128], box = one (block, head)
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(MmaCfg<D, NR>::kWarps * 32, MmaCfg<D, NR>::kSm
         wscale[stage_in] = make_float2(-INFINITY, 0.f);
         mbar_arrive(bar);
       } else {
-        wscale[stage_in] = make_float2(my_ks, my_vs);
+        wscale[stage_in] = make_float2(my_ks, my_vs * kUnlift);  // (exact, down to the subnormal numbers too)
         fence_proxy_async_smem();
         mbar_arrive_expect_tx(bar, 2 * kCodeBytes);
         if constexpr (D == 128) {
@@ -406,7 +412,7 @@ __global__ void __launch_bounds__(MmaCfg<D, NR>::kWarps * 32, MmaCfg<D, NR>::kSm
     // O^T: tile j holds dims (D / 8) g + 2 j (rows g) and the next one (rows g + 8) of every
     // row; columns 2t, 2t + 1 are this lane's rows
     float o[NR][kTiles][4];
-    float m_run[NR], l_part[NR];  // of row g: running max (log2), this lane's sum
+    float m_run[NR], l_part[NR];  // of row g: running max (log2) less kLift, this lane's sum
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
       m_run[nr] = -INFINITY, l_part[nr] = 0.f;
@@ -463,10 +469,10 @@ __global__ void __launch_bounds__(MmaCfg<D, NR>::kWarps * 32, MmaCfg<D, NR>::kSm
           bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
           bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
           // the reference max moves only by more than the margin
-          const bool moves = bm > m_run[nr] + kLazy;
+          const bool moves = bm > m_run[nr] + (kLift + kLazy);
           if (__any_sync(0xffffffffu, moves)) {
-            const float alpha = moves ? fast_exp2(m_run[nr] - bm) : 1.f;  // 0 when m_run was -inf
-            if (moves) m_run[nr] = bm;
+            const float alpha = moves ? fast_exp2(m_run[nr] - (bm - kLift)) : 1.f;  // 0 when m_run was -inf
+            if (moves) m_run[nr] = bm - kLift;
             l_part[nr] *= alpha;
             const float f0 = __shfl_sync(0xffffffffu, alpha, 8 * t), f1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
 #pragma unroll
@@ -586,7 +592,7 @@ __global__ void __launch_bounds__(MmaCfg<D, NR>::kWarps * 32, MmaCfg<D, NR>::kSm
       }
 #pragma unroll
       for (int hc = 0; hc < 2; ++hc) {
-        const float f = __shfl_sync(0xffffffffu, inv, 8 * t + 4 * hc);
+        const float f = __shfl_sync(0xffffffffu, inv, 8 * t + 4 * hc) * (1.0f / kUnlift);
         const int rr = 8 * nr + 2 * t + hc;
         float x[2 * kTiles];
 #pragma unroll

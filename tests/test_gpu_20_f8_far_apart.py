@@ -1,0 +1,53 @@
+"""The e4m3 cache where numbers are far apart, against the 64-bit reference."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import masked_attention_paged_gb300 as lib
+from _serve_ref import BS, attn_f8
+from test_gpu_17_f8 import _codes, _ints
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _attn(q, codes, scales, table, start, scale):
+    g = [_codes(c) for c in codes] + [torch.from_numpy(s).to(DEV) for s in scales]
+    B, Hq, T, D = q.shape
+    ws = lib.Workspace(lib.paged_attn_f8_workspace_size(B, Hq, codes[0].shape[1], T, table.shape[1], BS, D))
+    out = torch.empty(q.shape, device=DEV)
+    got, lse = lib.paged_attn_f8(q, *g, _ints(table), _ints(start), scale=scale, out=out, return_lse=True, workspace=ws)
+    assert ws.status() == 0
+    return got.double().cpu().numpy(), lse.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,G", [(1, 1), (2, 8), (30, 1), (60, 4)])
+@pytest.mark.parametrize("log2w", [-20, -25.5, -27, -30])
+def test_a_long_tail_of_small_weights(log2w, T, G, D):
+    """A key of each block has all the weight and a value of zero, the others 2^log2w of it: the output is theirs alone.
+
+    A weight is off by its rounding, 2^-11 (bf16 2^-8, with more than 16 rows) relative or, fp16 below its normal
+    numbers, 2^-32 of the largest; the sum that divides is that of all weights relative to the largest.  The rest as in
+    _compare of the e4m3 tests: q's split and the additions of a score, the exponential."""
+    rng = np.random.default_rng(D)
+    N = 64
+    codes = [np.zeros((N, 1, BS, D), np.uint8) for _ in range(2)]
+    scales = [np.ones((N, 1), np.float32) for _ in range(2)]
+    codes[0][:, 0, 0, 0] = 0x58  # 16
+    codes[1][:, 0, 1:] = rng.integers(0x30, 0x40, (N, BS - 1, D))
+    q = torch.zeros((1, G, T, D))
+    q[..., 0] = -log2w * math.log(2.0) / 16
+    q = q.to(DEV, torch.bfloat16)
+    table, start = rng.permutation(N).astype(np.int32)[None], [N * BS - T]
+    got, lse = _attn(q, codes, scales, table, start, 1.0)
+    qn = q.double().cpu().numpy()
+    ref, ref_lse, mag, all_v = attn_f8(qn, codes[0], scales[0], codes[1], scales[1], table, start, 1.0, True)
+    ds = qn[..., 0] * 16 * (2.0 ** -19 + 4 * D * 2.0 ** -24) + 2.0 ** -22 * ref_lse
+    w = 2 * np.expm1(2 * ds) + (2.0 ** -11 if T * G <= 16 else 2.0 ** -8) + 2.0 ** -18
+    small = 2.0 ** -32 * np.exp(qn[..., 0] * 16 - ref_lse)[..., None] * all_v if T * G <= 16 else 0.0
+    tol = w[..., None] * mag + np.abs(ref) * 2.0 ** -24 + small
+    assert (np.abs(got - ref) <= tol).all(), (np.abs(got - ref) / np.abs(ref)).max()
+    assert (np.abs(lse - ref_lse) <= 2 * ds + 2.0 ** -18).all()
