@@ -854,7 +854,8 @@ attn_status kv_append_f8(const attn_kv_cache_f8 *cache, const int32_t *block_tab
  * Hq / Hkv <= 128.  Products on the tensor cores with fp32 accumulation: codes enter
  * exactly, q to 2^-19 of its row's largest element or better, the softmax weights
  * rounded to fp16 (those below 2^-21 of the largest to a multiple of 2^-31 of it), or for
- * more than 16 query rows per KV head to bf16.  Results do not depend on timing.
+ * more than 16 query rows per KV head to bf16.  Values below 2^92 in size do not overflow
+ * on the way, in whatever order large scores come.  Results do not depend on timing.
  */
 size_t paged_attn_f8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t num_queries,
                                     int32_t max_blocks, int32_t block_size, int32_t head_dim);

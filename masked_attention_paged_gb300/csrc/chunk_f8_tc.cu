@@ -966,7 +966,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             }
             float a0, a1;
             f2_unpack(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), a0, a1);
-            done = __all_sync(0xffffffffu, a0 + a1 <= 18446744073709551616.0f);  // 2^64; false for a NaN
+            // What the margin lets through (above it some weight is past the margin, so that the passes
+            // below do move the max): the accumulators hold values up to 2^92.  False for a NaN.
+            static_assert(kRescaleMargin == 8.0f, "2^kRescaleMargin below");
+            done = __all_sync(0xffffffffu, a0 + a1 <= kBN * 256.0f);
             if (done) {
 #pragma unroll
               for (int c = 0; c < 4; ++c) tmem_st16(tmem + lane_addr + s_col + c * 16, pw[c]);

@@ -51,3 +51,33 @@ def test_a_long_tail_of_small_weights(log2w, T, G, D):
     tol = w[..., None] * mag + np.abs(ref) * 2.0 ** -24 + small
     assert (np.abs(got - ref) <= tol).all(), (np.abs(got - ref) / np.abs(ref)).max()
     assert (np.abs(lse - ref_lse) <= 2 * ds + 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,G", [(1, 1), (1, 12), (20, 1), (60, 4)])
+@pytest.mark.parametrize("nats", [12.0, 30.0, 36.0])
+def test_scores_that_outgrow_the_first_keys_before_large_values(nats, T, G, D):
+    """Values near 2^100, and keys from 300 on that score `nats` above all others: the weights that the first keys set
+    the measure for must not carry the sums past float32's range."""
+    rng = np.random.default_rng(T)
+    B, Hkv, width = 48, 2, 40
+    N = 60
+    codes = [np.zeros((N, Hkv, BS, D), np.uint8) for _ in range(2)]
+    scales = [np.ones((N, Hkv), np.float32), np.full((N, Hkv), 2.0 ** 92, np.float32)]
+    codes[0][N // 2:, :, :, 0] = 0x58  # 16
+    codes[1][...] = rng.integers(0x70, 0x7f, codes[1].shape) | (rng.integers(0, 2, codes[1].shape) * 128).astype(np.uint8)
+    table = rng.integers(0, N // 2, (B, width)).astype(np.int32)
+    table[:, 19:] += N // 2
+    q = torch.zeros((B, Hkv * G, T, D))
+    q[..., 0] = nats / 16
+    q = q.to(DEV, torch.bfloat16)
+    start = [width * BS - T - b for b in range(B)]
+    got, lse = _attn(q, codes, scales, table, start, 1.0)
+    assert np.isfinite(got).all()
+    got, lse, qn = got[::6], lse[::6], q[::6].double().cpu().numpy()
+    ref, ref_lse, mag, _ = attn_f8(qn, codes[0], scales[0], codes[1], scales[1], table[::6], start[::6], 1.0, True)
+    ds = qn[..., 0] * 16 * (2.0 ** -19 + 4 * D * 2.0 ** -24) + 2.0 ** -22 * np.abs(ref_lse)
+    w = 2 * np.expm1(2 * ds) + (2.0 ** -11 if T * G <= 16 else 2.0 ** -8) + 2.0 ** -18
+    # (a weight below fp16's normal numbers is off by 2^-32 of the largest, of sums of 64 keys and more)
+    assert (np.abs(got - ref) <= w[..., None] * mag + np.abs(ref) * 2.0 ** -24 + 2.0 ** -32 * 640 * 448 * 2.0 ** 92).all()
+    assert (np.abs(lse - ref_lse) <= 2 * ds + 2.0 ** -18).all()
