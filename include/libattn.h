@@ -808,7 +808,8 @@ typedef struct attn_kv_cache_f8 {
  * kv_append_f8 -- write T new tokens of K and V per sequence, token i to slot
  * start_pos[b] + i.  For every block that gets some, and K and V on their own: with
  * a the largest finite |x| of the new rows in the block (of a KV head),
- *     scale = the smallest 2^e >= a / 448 (e >= -126; 0 if a = 0), and not below the
+ *     scale = the smallest 2^e >= a / 448 (e >= -126; 0 if a = 0: infinities then
+ *             stand for 0), and not below the
  *             block's present scale if the block holds older tokens (slots before
  *             start_pos[b]; a block whose first slot is written begins anew)
  *     code  = x / scale rounded to nearest, ties to even, +-448 at most (NaN: NaN)

@@ -105,9 +105,9 @@ __global__ void __launch_bounds__(kWarps * 32, 7) kv_append_f8_kernel(const F8Ap
 #pragma unroll
       for (int k = 0; k < 4; ++k) c[k] = f8_codes(bf16lo_to_f32(u[k]) * inv, bf16hi_to_f32(u[k]) * inv);
       *out = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-    } else if (slot < s0 && grows && old != 0.f) {
+    } else if (slot < s0 && grows) {
       const uint2 was = *out;
-      const float r = old * inv;
+      const float r = old * inv;  // (0 if the older rows are zeros, or infinities whose codes stood for 0)
       const uint32_t u[4] = {was.x & 0xffffu, was.x >> 16, was.y & 0xffffu, was.y >> 16};
       uint32_t c[4];
 #pragma unroll

@@ -81,3 +81,26 @@ def test_scores_that_outgrow_the_first_keys_before_large_values(nats, T, G, D):
     # (a weight below fp16's normal numbers is off by 2^-32 of the largest, of sums of 64 keys and more)
     assert (np.abs(got - ref) <= w[..., None] * mag + np.abs(ref) * 2.0 ** -24 + 2.0 ** -32 * 640 * 448 * 2.0 ** 92).all()
     assert (np.abs(lse - ref_lse) <= 2 * ds + 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_block_that_begins_with_infinities_alone(D):
+    """Scale 0, so their codes stand for 0; when later rows set a scale, code times old scale over new is 0 again (and
+    a NaN stays one)."""
+    N, H = 2, 2
+    codes = [torch.zeros((N, H, BS, D), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.full((N, H), 3.0, device=DEV) for _ in range(2)]
+    table = _ints([[1, 0]])
+    new = torch.zeros((1, H, 3, D), device=DEV, dtype=torch.bfloat16)
+    new[0, :, 0, ::2], new[0, :, 1, 1], new[0, :, 1, 2] = math.inf, -math.inf, math.nan
+    lib.kv_append_f8(*codes, *scales, table, _ints([0]), new, -new)
+    assert (scales[0][1] == 0).all() and (scales[1][1] == 0).all()
+    rows = torch.full((1, H, 1, D), 3.0, device=DEV, dtype=torch.bfloat16)
+    lib.kv_append_f8(*codes, *scales, table, _ints([3]), rows, rows)
+    for c, s in zip(codes, scales):
+        x = c[1].float() * s[1][:, None, None]
+        want = torch.zeros((H, BS, D), device=DEV)
+        want[:, 3] = 3.0
+        want[:, 1, 2] = math.nan
+        assert torch.equal(s[1], torch.full((H,), 2.0 ** -7, device=DEV))
+        assert torch.equal(x.isnan(), want.isnan()) and torch.equal(x.nan_to_num(), want.nan_to_num())
