@@ -17,11 +17,13 @@
 // kernel: the SM does two a cycle, and a chain of them (a test, a quotient) took the
 // walk 2 us at each refusal.
 //
-// What bounds it is the chain of the sequence with the most refusals: 64 x 25 drafts over
+// What bounds it is latency, in the sequence with the most refusals: 64 x 25 drafts over
 // 131072 tokens take 43 us, four row sums one after the other and the draw in the longest,
 // where the bytes of all 100 sums are 15 us of HBM (116 us with doubles and CTAs of 512
-// threads); 16 x 27 over 100003 tokens 21 us; 1 x 5 over 32000 6.4: a launch, two loads that
-// depend on each other, and the draw.
+// threads).  A lane asks for single entries, eight at a time, so once the other sequences are
+// done an SM has 16 KB on its way (8 KB of two-byte entries), and HBM is 15 % busy.  16 x 27
+// over 100003 tokens 21.5 us; 1 x 5 over 32000 6.6: a launch, two loads that depend on each
+// other, and the draw.
 #include <math.h>
 
 #include "common.cuh"
@@ -167,6 +169,10 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyP
   __shared__ int found;     // the warp whose part the next token is in; -1: not this CTA's
   __shared__ bool remains;  // the last row's sum is positive (not in `found`, which warp 0 sets while others read this)
   let_next_launch_in();
+  // The first sum stores into the other CTAs' shared memory, which they must have begun to
+  // run for: the barrier's other half is there, behind the loads and the walk (1 x 5: 6.6 us; 7.0
+  // with this half behind the loads).
+  cluster_arrive();
   wait_for_launch_ahead();
   const int b = blockIdx.y, rank = static_cast<int>(cluster_rank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -201,11 +207,9 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyP
         p.next[b] = -1;
       }
     }
+    cluster_wait();
     return;
   }
-  // The first sum stores into the other CTAs' shared memory, which they must have begun to
-  // run for: the barrier's other half is there, behind the walk and the loads.
-  cluster_arrive();
   bool started = false;  // alike in the whole cluster
 
   // this warp's part of a row: [w0, w1)
@@ -456,8 +460,8 @@ template <bool BF16>
 cudaError_t launch(const VerifyArgs& a, const VerifyParams& p, cudaStream_t stream) {
   auto kern = draft_verify_kernel<BF16>;
   // CTAs a sequence: as many as the GPU holds at four an SM, and no fewer than 1024 entries each.
-  // 64 x 25 drafts over 131072 tokens: 43 us on eight; 42 on 16, 64 on four, 102 on two; 1 x 5 over
-  // 32000 6.4 us, 6.9 with no fewer than 2048 entries.
+  // 64 x 25 drafts over 131072 tokens: 43.3 us on eight; 43.2 on 16, 65 on four, 102 on two; 1 x 5
+  // over 32000 6.6 us, 7.0 with no fewer than 2048 entries.
   int nc = 1;
   while (nc < kMaxCtas && 2 * nc * a.B <= 4 * device_sm_count() && static_cast<int64_t>(nc) * 2048 <= a.V) nc *= 2;
   if (nc > 8) {
