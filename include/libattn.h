@@ -815,7 +815,9 @@ typedef struct attn_kv_cache_f8 {
  *     code  = x / scale rounded to nearest, ties to even, +-448 at most (NaN: NaN)
  * and, if the scale grew, the older codes c become c * (old / new), rounded alike
  * (exact unless it falls below 2^-6).  Slots past the new tokens are left as they
- * are.
+ * are.  Drafts that are refused later leave their mark: a scale that they raised stays
+ * as long as the block holds older tokens, and what the older codes lost when they were
+ * rounded again does not come back.
  *   k_new, v_new [batch, num_kv_heads, T, head_dim] bf16 (strided views, 16-byte
  *                aligned rows)
  *   start_pos    int32 [batch]; < 0: an idle sequence

@@ -1427,8 +1427,9 @@ def kv_append_f8(kq_cache: torch.Tensor, vq_cache: torch.Tensor, k_scale: torch.
     """Write T new tokens a sequence (k_new, v_new bf16 [B, Hkv, T, D], or [B, Hkv,
     D] for one) at slots start_pos[b] + i of an e4m3 cache (codes float8_e4m3fn [N,
     Hkv, 16, D], scales float32 [N, Hkv], powers of two): a block whose new rows need
-    a larger scale gets it, and its older codes are rounded again.  lens int32 [B]:
-    new tokens of each sequence."""
+    a larger scale gets it, and its older codes are rounded again (drafts that are
+    refused afterwards leave that behind).  lens int32 [B]: new tokens of each
+    sequence."""
     lib = load()
     if kq_cache.is_cuda:
         ws = workspace or _small_ws(kq_cache.device, stream)

@@ -9,11 +9,13 @@
 // element vectors, all in registers, so the rows are read once, their largest element
 // is a reduction over the warp's lanes, and codes leave eight bytes a lane.
 //
-// HBM bounds it: 16 sequences of 1024 new tokens (8 KV heads, D = 128) move 88 MB in 15.2 us,
-// 86 % of what a copy does.  A warp's work is one chain of loads and stores, so what counts is how
-// many are on an SM: seven CTAs by 72 registers (without the bound 161 registers, 18.2 us;
-// eight CTAs spill, 15.5).  One token each of 64 sequences is the launch and that
-// chain, 3.3 us.
+// Latency bounds it: 16 sequences of 1024 new tokens (8 KV heads, D = 128) move 88 MB in 17.6 us,
+// 74 % of what a copy does, with HBM 42 % and the issue slots 46 % busy (caches flushed).  A warp's
+// work is one chain, from the position to the block's id, the rows, their largest element and
+// the stores, and nothing of another block is on its way meanwhile.  So what counts is how many
+// warps are on an SM: seven CTAs by 72 registers.  (Over the same 88 MB again and again, of which
+// L2 keeps the stores: 15.2 us; without the bound, 161 registers, 18.2; eight CTAs spill, 15.5.)  One
+// token each of 64 sequences is the launch and that chain, 3.4 us.
 #include "common.cuh"
 #include "f8.cuh"
 #include "internal.h"

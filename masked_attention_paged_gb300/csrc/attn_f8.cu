@@ -25,8 +25,11 @@
 // leaves partials (normalised rows and log2 LSE; at most two a warp), which a second
 // launch joins in order, so results do not depend on timing.  (CTAs of 1024 tokens of an
 // item, joined by the last to come, spent 4 us each on their start and end.)
-// 64 sequences of up to 8192 tokens (32 heads over 8, D = 128) take 133 us, 0.81 GB at 90 % of
-// what a copy does; one of 700 (D = 64) 10 us, two launches of dependent loads.
+// 64 sequences of up to 8192 tokens (32 heads over 8, D = 128) take 132 us, 0.81 GB at 91 % of
+// what a copy does; one of 700 (D = 64) 10 us (13 to 14 as eager calls on other inputs each
+// time), two launches of dependent loads.  With 9 to 16 rows a KV head the registers of two row
+// groups leave eight warps an SM, too few to hide latency: 233 us for the 64 sequences with 16 rows,
+// where the bytes are 137.
 #include <cuda.h>
 #include <math.h>
 
@@ -629,7 +632,8 @@ __global__ void __launch_bounds__(MmaCfg<D, NR>::kWarps * 32, MmaCfg<D, NR>::kSm
 
 // Joins the pieces of the items that are cut between warps, and writes those that have no
 // blocks.  Where an item's pieces are, the first launch has left (found again from all the
-// sequences' lengths it took 1200 us of 8192 short sequences, 233 now in all).  An item's rows go to as many CTAs as fill the GPU, a CTA's warps share them.
+// sequences' lengths it took 1200 us of 8192 short sequences, 233 now in all).  An item's rows go
+// to as many CTAs as fill the GPU, a CTA's warps share them.
 constexpr int kMergeWarps = 16;  // at most
 template <int D, int NR>
 __global__ void __launch_bounds__(kMergeWarps * 32) f8_mma_merge_kernel(const __grid_constant__ F8MmaParams p) {

@@ -19,16 +19,18 @@
 //
 // Warps: 0 streams the codes, 1 issues the MMAs, 2 waits for it, 3 plans the segments, 4-7
 // convert V, 8-11 and 12-15 softmax (thread r owns row r: TMEM lane r; it also splits
-// its row of q).  With NT = 2 each warpgroup has a row tile.  With NT = 1 both have the same rows and take the key tiles in turn, each with a
-// score buffer, an accumulator and a running max and sum of its own, joined by the LSE
-// rule when an item ends.
+// its row of q).  With NT = 2 each warpgroup has a row tile.  With NT = 1 both have the same rows
+// and take the key tiles in turn, each with a score buffer, an accumulator and a running max
+// and sum of its own, joined by the LSE rule when an item ends.
 //
-// What bounds it: 2 x 1024 tokens behind 8192 (32 heads over 8, D = 128) take 191 us where the
-// products alone would take 123.  A tile takes 3000 cycles a CTA: 2 x 1040 of products, which
+// What bounds it: 2 x 1024 tokens behind 8192 (32 heads over 8, D = 128) take 190 us where the
+// products alone would take 123.  A tile takes 3000 cycles a CTA: 2 x 1030 of products, which
 // also read shared memory at 128 bytes a cycle, all that it gives (8 KB a step of 65 cycles), so
 // that the TMA's and the converters' bytes come on top; and two waits of the issuer, 230
-// each.  An item's start and end cost some 12000 cycles.  With one row tile the conversion
-// sets the pace, 2700 cycles a tile (16 x 16 tokens behind 8192: 85 us; some 70 with none at all).
+// each.  A row tile's value product waits for all of its softmax, some 1310 cycles, so the two
+// tiles' chains have nothing to spare.  An item's start and end cost some 12000 cycles.  With one
+// row tile the conversion sets the pace, 2700 cycles a tile (16 x 16 tokens behind 8192: 87 us; some
+// 72 with none at all).
 // Not kept, next to the 200 us of then: two issuers, one a row tile, 261 (both products end
 // late), in strict turns 224; two threads a row, 64 keys each, 229; 64-key tiles 292; waits
 // polled instead of parked 203; the converting loop unrolled twice 214, and rolled to one
@@ -62,9 +64,9 @@ constexpr float kRescaleMargin = 8.0f;
 constexpr int kBarBytes = 4096;
 constexpr int kSegs = 4;      // segments the planner is ahead
 // What an item costs a CTA besides its tiles, in tiles: the split of q, the products of the first
-// tile, the epilogue.  Two chunks of 1024 behind 8192 tokens: 194 us with 6, 193 with 8, 197 with
-// 3, 199 with none (191 with 6 since the second launch is faster); two of 64: 35, 36, 40, 45; one of 2048 behind 10 tokens: 70, 70, 77, 155; 4 of
-// 300 behind 1000: 49.5, 50, 52, 60.
+// tile, the epilogue.  Two chunks of 1024 behind 8192 tokens: 189 us with 6 and with 8, 192 with
+// 3, 194 with none; two of 64: 34, 35, 39, 44; one of 2048 behind 10 tokens: 67, 67, 74, 152; 4 of
+// 300 behind 1000: 47, 48, 49, 57.
 constexpr int kItemCost = 6;
 constexpr int kScales = 8;    // tiles whose key scales are held: more than K's stages and the scores ahead of P
 constexpr int kNotes = 8;     // segments whose notes of NaNs are held: more than the planner is ahead
@@ -872,7 +874,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           for (int y = 0; y < 4; ++y) {
             const uint32_t at = C::code_off(row0 + (it0 + y) * RPI, c / 2) + c % 2 * 8;
             *reinterpret_cast<uint2*>(qs + at) = make_uint2(h[y][0] | h[y][1] << 16, h[y][2] | h[y][3] << 16);
-            *reinterpret_cast<uint2*>(qs + C::kQBytes + at) = make_uint2(l[y][0] | l[y][1] << 16, l[y][2] | l[y][3] << 16);
+            *reinterpret_cast<uint2*>(qs + C::kQBytes + at) =
+                make_uint2(l[y][0] | l[y][1] << 16, l[y][2] | l[y][3] << 16);
           }
         }
         fence_proxy_async_smem();
@@ -1187,9 +1190,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 }
 
 int tile_queries(int64_t T, int64_t G) { return static_cast<int>(std::min(T, kBM / G)); }
-// One row tile where it holds all rows (16 x 16 tokens of 4 heads behind 8192: 85 us, with two tiles
-// 98; 16 x 32 behind 4000: 58, 66), else two (2 x 1024 behind 8192 194 us, 282 with one at a
-// time; 16 x 40 behind 2000 52, 69).
+// One row tile where it holds all rows (16 x 16 tokens of 4 heads behind 8192: 87 us, with two tiles
+// 96; 16 x 32 behind 4000: 56, 64), else two (2 x 1024 behind 8192 189 us, 279 with one at a
+// time; 16 x 40 behind 2000 50, 66).
 int chunk_nt(int64_t T, int64_t G) { return T <= kBM / G ? 1 : 2; }
 size_t part_rows(int64_t T, int64_t G, int n_cta) { return static_cast<size_t>(2) * n_cta * chunk_nt(T, G) * kBM; }
 size_t part_bytes(int64_t T, int64_t G, int D, int n_cta) {
@@ -1200,7 +1203,8 @@ template <int D, int NT>
 cudaError_t launch(const F8AttnArgs& a, const ChunkParams& p, cudaStream_t stream) {
   using C = Cfg<D, NT>;
   CUtensorMap mq, mk, mv;
-  if (!make_half_rows_map(&mq, a.q, a.cache.Hkv, p.tb, D) || !make_code_map(&mk, a.cache.k, a.cache.num_blocks, a.cache.Hkv, D) ||
+  if (!make_half_rows_map(&mq, a.q, a.cache.Hkv, p.tb, D) ||
+      !make_code_map(&mk, a.cache.k, a.cache.num_blocks, a.cache.Hkv, D) ||
       !make_code_map(&mv, a.cache.v, a.cache.num_blocks, a.cache.Hkv, D))
     return cudaErrorInvalidValue;
   auto kern = paged_chunk_f8_kernel<D, NT>;

@@ -7,10 +7,10 @@
 // pass of 16 loads a thread.
 //
 // Measured: 4100 blocks (4.3 GB read and written) moved to the front of a pool of 16384 in 680
-// us, 93 % of what a copy does.  A step of a search, 64 rows given back, forked anew from 16
-// prompts in eight layers and reserved for, takes 20 us, of which the bytes (8.4 MB read,
-// 33.6 written) are 6: four launches and their decisions, each a chain of loads by one CTA.
-// One prompt and four rows take 11 us.
+// to 695 us, 91 to 93 % of what a copy does.  A step of a search, 64 rows given back, forked anew
+// from 16 prompts in eight layers and reserved for, takes 20 us (24 of other contents each time),
+// of which the bytes (8.4 MB read, 33.6 written) are 6: four launches and their decisions, each
+// a chain of loads by one CTA.  One prompt and four rows take 11 us (13).
 #include <algorithm>
 
 #include "common.cuh"
